@@ -22,13 +22,14 @@ ATTN_DTYPE_BF16, ATTN_DTYPE_F32 = 0, 1
 ATTN_FWD_TILE_Q, ATTN_FWD_TILE_K = 256, 128
 ATTN_MERGE_MAX_PARTS = 16
 
-# every entry point declared in include/attn_slice.h
+# every entry point declared in include/attn_slice.h and include/attn_paged.h
 EXPORTS = ["attn_tiles_workspace_bytes", "attn_build_tiles", "attn_build_tiles_noalloc",
            "attn_tiles_totals",
            "attn_slices_from_block_grid", "attn_fwd", "attn_merge", "attn_bwd_workspace_bytes",
            "attn_bwd", "attn_last_device_error",
            "attn_set_wait_limit_ns", "attn_set_exp2_poly", "attn_selftest_wait_timeout",
-           "attn_strerror"]
+           "attn_strerror",
+           "attn_paged_workspace_bytes", "attn_paged_fwd", "attn_prefix_fwd", "attn_slices_from_windows"]
 
 
 class AttnSlice(ctypes.Structure):
@@ -86,6 +87,8 @@ def load(path: Optional[str] = None):
     lib.attn_selftest_wait_timeout.argtypes = [vp]
     lib.attn_strerror.argtypes = [i32]
     lib.attn_strerror.restype = ctypes.c_char_p
+    from . import paging
+    paging._declare(lib)
     for name in EXPORTS:
         if name != "attn_strerror":
             getattr(lib, name).restype = ctypes.c_int

@@ -362,9 +362,9 @@ int attn_merge(const void *const *h_o_parts, const float *const *h_lse_parts, in
 int attn_last_device_error(attn_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  unsigned int st[3] = {0, 0, 0};
+  unsigned int st[4] = {0, 0, 0, 0};
   if (attn::build_status_take(&st[0]) != ATTN_OK || attn::fwd_status_take(&st[1]) != ATTN_OK ||
-      attn::bwd_status_take(&st[2]) != ATTN_OK)
+      attn::bwd_status_take(&st[2]) != ATTN_OK || attn::paged_status_take(&st[3]) != ATTN_OK)
     return ATTN_ERR_CUDA;
   for (unsigned int x : st)
     if (x) return static_cast<int>(x);

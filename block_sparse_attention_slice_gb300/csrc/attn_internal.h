@@ -72,4 +72,13 @@ int merge_launch(const void *const *o_parts, const float *const *lse_parts, int 
                  int part_dtype, int s_len, int h, int d, void *out, int out_dtype, float *lse,
                  cudaStream_t s);
 
+// Attention over a paged cache (paged_api.cu, paged_rows.cu).
+struct PagedParams;
+size_t paged_rows_workspace(int d);
+int paged_rows_launch(PagedParams p, int d, cudaStream_t s);
+// Reads and clears the first failure status of the paged and cache kernels on
+// the current device; its device address for their launches (null on failure).
+int paged_status_take(unsigned int *status);
+unsigned int *paged_status();
+
 }  // namespace attn

@@ -1,0 +1,247 @@
+// C ABI of the attention over a paged cache: argument checks on the host and
+// the choice of kernel; and the windowed mask as a slice list.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "../../include/attn_paged.h"
+#include "attn_internal.h"
+#include "paged_plan.cuh"
+
+namespace attn {
+
+// First failure status of the paged attention and cache kernels on this device.
+__device__ unsigned int g_paged_status;
+
+unsigned int *paged_status() {
+  constexpr int kDev = 64;
+  static unsigned int *at[kDev] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDev) return nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!at[dev]) {
+    void *x = nullptr;
+    if (cudaGetSymbolAddress(&x, g_paged_status) != cudaSuccess) return nullptr;
+    at[dev] = static_cast<unsigned int *>(x);
+  }
+  return at[dev];
+}
+
+int paged_status_take(unsigned int *status) {
+  unsigned int zero = 0;
+  if (cudaMemcpyFromSymbol(status, g_paged_status, sizeof(unsigned int)) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (*status && cudaMemcpyToSymbol(g_paged_status, &zero, sizeof(unsigned int)) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  return ATTN_OK;
+}
+
+namespace {
+
+bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+int check_pages(const attn_pages_t *g, int *shift) {
+  if (!g || !g->k || !g->v || g->n_pages < 1 || g->hk < 1) return ATTN_ERR_INVALID_ARG;
+  if (g->d != 64 && g->d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (g->page_size < 16 || (g->page_size & (g->page_size - 1))) return ATTN_ERR_UNSUPPORTED;
+  if (!al16(g->k) || !al16(g->v) || (g->page_stride | g->token_stride | g->head_stride) & 7)
+    return ATTN_ERR_UNSUPPORTED;
+  // strides of 0 (one page seen as many) are fine to read; negative ones are not served
+  if (g->page_stride < 0 || g->token_stride < 0 || g->head_stride < 0) return ATTN_ERR_UNSUPPORTED;
+  *shift = 0;
+  while ((1 << *shift) < g->page_size) ++*shift;
+  return ATTN_OK;
+}
+
+int check_seqs(const attn_seqs_t *s, int page_size) {
+  if (!s || s->n_seqs < 0 || s->n_slots < 0 || s->max_pages < 0) return ATTN_ERR_INVALID_ARG;
+  if (s->n_seqs > ATTN_PAGED_MAX_SEQS) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(s->max_pages) * page_size > ATTN_PAGED_MAX_LEN) return ATTN_ERR_UNSUPPORTED;
+  if (s->n_seqs == 0) return ATTN_OK;
+  if (!s->table || !s->seq_lens) return ATTN_ERR_INVALID_ARG;
+  if (!s->seqs && s->n_seqs > s->n_slots) return ATTN_ERR_INVALID_ARG;
+  if (s->table_stride < s->max_pages) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+int check_call(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq, const attn_pages_t *pages,
+               const attn_seqs_t *seqs, float scale, const void *out, int out_dtype, const float *lse, int *shift) {
+  if (n_tokens < 0 || hq < 1 || max_q < 1) return ATTN_ERR_INVALID_ARG;
+  int rc = check_pages(pages, shift);
+  if (rc != ATTN_OK) return rc;
+  if ((rc = check_seqs(seqs, pages->page_size)) != ATTN_OK) return rc;
+  if (hq % pages->hk != 0) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (out_dtype != ATTN_DTYPE_BF16 && out_dtype != ATTN_DTYPE_F32) return ATTN_ERR_INVALID_ARG;
+  if (!q_ptr && n_tokens != seqs->n_seqs) return ATTN_ERR_INVALID_ARG;
+  if (n_tokens == 0 || seqs->n_seqs == 0) return ATTN_OK;
+  if (!q || !out || !lse) return ATTN_ERR_INVALID_ARG;
+  if (!al16(q) || !al16(out)) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(n_tokens) * (hq / pages->hk) >= (int64_t(1) << 31)) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, const attn_pages_t *g,
+                   const attn_seqs_t *s, float scale, int shift) {
+  PagedParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.k = g->k;
+  p.v = g->v;
+  p.q_ptr = q_ptr;
+  p.seqs = s->seqs;
+  p.seq_lens = s->seq_lens;
+  p.table = s->table;
+  p.table_stride = s->table_stride;
+  p.page_stride = g->page_stride;
+  p.token_stride = g->token_stride;
+  p.head_stride = g->head_stride;
+  p.n_tokens = n_tokens;
+  p.n_seqs = s->n_seqs;
+  p.n_slots = s->n_slots;
+  p.max_pages = s->max_pages;
+  p.n_pages = g->n_pages;
+  p.page_shift = shift;
+  p.hq = hq;
+  p.hk = g->hk;
+  p.G = hq / g->hk;
+  p.causal = 1;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.wait_ns = wait_limit_ns();
+  return p;
+}
+
+// O and lse of the prefix pass, in 32 bits, ahead of the pieces
+size_t prefix_bytes(int n_tokens, int hq, int d) {
+  return up256(static_cast<size_t>(n_tokens) * hq * d * 4) + up256(static_cast<size_t>(n_tokens) * hq * 4);
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" {
+
+int attn_paged_workspace_bytes(int n_tokens, int hq, int d, int prefix, size_t *bytes) {
+  if (!bytes || n_tokens < 0 || hq < 1) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  const size_t w = paged_rows_workspace(d);
+  if (w == 0) return ATTN_ERR_CUDA;
+  *bytes = w + (prefix ? prefix_bytes(n_tokens, hq, d) : 0);
+  return ATTN_OK;
+}
+
+int attn_paged_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
+                   const attn_pages_t *pages, const attn_seqs_t *seqs, float scale, int window, int sinks,
+                   void *out, int out_dtype, float *lse, void *d_ws, size_t ws_bytes, attn_stream_t stream) {
+  if (window < 0 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  int shift = 0;
+  int rc = check_call(q, q_ptr, n_tokens, max_q, hq, pages, seqs, scale, out, out_dtype, lse, &shift);
+  if (rc != ATTN_OK) return rc;
+  if (n_tokens == 0 || seqs->n_seqs == 0) return ATTN_OK;
+  if (!d_ws) return ATTN_ERR_INVALID_ARG;
+  if (!al16(d_ws)) return ATTN_ERR_UNSUPPORTED;
+  size_t need = 0;
+  if ((rc = attn_paged_workspace_bytes(n_tokens, hq, pages->d, 0, &need)) != ATTN_OK) return rc;
+  if (ws_bytes < need) return ATTN_ERR_CAPACITY;
+  PagedParams p = params(q, q_ptr, n_tokens, hq, pages, seqs, scale, shift);
+  // no sequence is longer than ATTN_PAGED_MAX_LEN: larger values say the same
+  p.window = std::min(window, ATTN_PAGED_MAX_LEN);
+  p.sinks = std::min(sinks, ATTN_PAGED_MAX_LEN);
+  p.out = out;
+  p.lse = lse;
+  p.out_f32 = out_dtype == ATTN_DTYPE_F32;
+  p.part_o = static_cast<float *>(d_ws);
+  p.status = paged_status();
+  if (!p.status) return ATTN_ERR_CUDA;
+  return paged_rows_launch(p, pages->d, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
+                    const attn_pages_t *pages, const attn_seqs_t *prefix, const int32_t *group_ptr,
+                    const attn_seqs_t *seqs, float scale, void *out, int out_dtype, float *lse, void *d_ws,
+                    size_t ws_bytes, attn_stream_t stream) {
+  int shift = 0;
+  int rc = check_call(q, q_ptr, n_tokens, max_q, hq, pages, seqs, scale, out, out_dtype, lse, &shift);
+  if (rc != ATTN_OK) return rc;
+  if ((rc = check_seqs(prefix, pages->page_size)) != ATTN_OK) return rc;
+  if (prefix->n_seqs > 0 && !group_ptr) return ATTN_ERR_INVALID_ARG;
+  if (n_tokens == 0 || seqs->n_seqs == 0) return ATTN_OK;
+  if (!d_ws) return ATTN_ERR_INVALID_ARG;
+  if (!al16(d_ws)) return ATTN_ERR_UNSUPPORTED;
+  size_t need = 0;
+  if ((rc = attn_paged_workspace_bytes(n_tokens, hq, pages->d, 1, &need)) != ATTN_OK) return rc;
+  if (ws_bytes < need) return ATTN_ERR_CAPACITY;
+  unsigned int *status = paged_status();
+  if (!status) return ATTN_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t *ws = static_cast<uint8_t *>(d_ws);
+  float *po = reinterpret_cast<float *>(ws);
+  float *plse = reinterpret_cast<float *>(ws + up256(static_cast<size_t>(n_tokens) * hq * pages->d * 4));
+  float *pieces = reinterpret_cast<float *>(ws + prefix_bytes(n_tokens, hq, pages->d));
+  // the prefixes: rows of a whole group against its keys, none of them masked
+  PagedParams p = params(q, q_ptr, n_tokens, hq, pages, prefix, scale, shift);
+  p.group_ptr = group_ptr;
+  p.n_members = seqs->n_seqs;
+  p.causal = 0;
+  p.out = po;
+  p.lse = plse;
+  p.out_f32 = 1;
+  p.part_o = pieces;
+  p.status = status;
+  const bool any = prefix->n_seqs > 0;
+  if (any && (rc = paged_rows_launch(p, pages->d, s)) != ATTN_OK) return rc;
+  // what follows it, each row starting from its prefix's summary
+  PagedParams r = params(q, q_ptr, n_tokens, hq, pages, seqs, scale, shift);
+  r.out = out;
+  r.lse = lse;
+  r.out_f32 = out_dtype == ATTN_DTYPE_F32;
+  r.init_o = any ? po : nullptr;
+  r.init_lse = any ? plse : nullptr;
+  r.part_o = pieces;
+  r.status = status;
+  return paged_rows_launch(r, pages->d, s);
+}
+
+int attn_slices_from_windows(const int32_t *h_lengths, int n, int window, int sinks, attn_slice_t *h_out,
+                             int capacity, int *n_out) {
+  if (n < 0 || (n > 0 && !h_lengths) || window < 0 || sinks < 0 || !n_out || capacity < 0) return ATTN_ERR_INVALID_ARG;
+  int64_t at = 0;
+  for (int i = 0; i < n; ++i) {
+    if (h_lengths[i] < 0) return ATTN_ERR_INVALID_ARG;
+    at += h_lengths[i];
+  }
+  if (at >= (int64_t(1) << 31)) return ATTN_ERR_INVALID_ARG;
+  int64_t count = 0;
+  auto put = [&](int64_t q0, int64_t q1, int64_t k0, int64_t k1, int type) {
+    if (q1 <= q0 || k1 <= k0) return;
+    if (count < capacity && h_out)
+      h_out[count] = attn_slice_t{static_cast<int32_t>(q0), static_cast<int32_t>(q1), static_cast<int32_t>(k0),
+                                  static_cast<int32_t>(k1), type};
+    ++count;
+  };
+  at = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t L = h_lengths[i];
+    // rows before window + sinks see every earlier key; of the others' keys
+    // key `sinks` is the first that no row of theirs sees
+    const int64_t m = window == 0 ? L : std::min<int64_t>(L, static_cast<int64_t>(window) + sinks);
+    put(at, at + m, at, at + m, ATTN_MASK_CAUSAL);
+    put(at + m, at + L, at, at + sinks, ATTN_MASK_FULL);
+    // bi-causal rows a = i - m, keys b = j - (m - window + 1):
+    // a <= b <= a + window - 1
+    put(at + m, at + L, at + m - window + 1, at + L, ATTN_MASK_BI_CAUSAL);
+    at += L;
+  }
+  if (count >= (int64_t(1) << 31)) return ATTN_ERR_INVALID_ARG;
+  *n_out = static_cast<int>(count);
+  return count > capacity ? ATTN_ERR_CAPACITY : ATTN_OK;
+}
+
+}  // extern "C"

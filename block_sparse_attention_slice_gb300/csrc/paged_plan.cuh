@@ -1,0 +1,316 @@
+// How the attention over a paged cache is divided: shared by the kernels that
+// compute it and the one that joins their pieces.
+//
+// A work item is one row tile (a few of one sequence's new tokens, packed with
+// the query heads of one key/value head) against the key tiles that any of
+// its rows sees.  All items' key tiles form one flat list in the order
+// (sequence, key/value head, row tile, key tile), of which every worker takes
+// one contiguous span of equal length, whatever the sequences' lengths.  An
+// item that ends in the span it began in is finished there; one that crosses
+// spans leaves a piece (m, l, unnormalised O) per span, and join_kernel merges
+// them.  The list is never written out: each CTA sums the sequences' tile
+// counts into shared memory and finds its span by bisection, so one launch
+// needs no plan made before it.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn_device.cuh"
+
+namespace attn {
+
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct PagedParams {
+  const void *q, *k, *v;
+  const int32_t *q_ptr;       // null: token b belongs to sequence b
+  const int32_t *group_ptr;   // prefix pass: "sequence" b is group b of sequences; else null
+  const int32_t *seqs, *seq_lens, *table;
+  long long table_stride;
+  long long page_stride, token_stride, head_stride;   // elements
+  int n_tokens, n_seqs, n_members, n_slots, max_pages, n_pages, page_shift;
+  int hq, hk, G;
+  int causal, window, sinks;
+  float scale_log2;
+  void *out;                  // [n_tokens, hq, D]
+  float *lse;                 // [hq, n_tokens]
+  int out_f32;
+  const float *init_o;        // a summary every row starts from (normalised O, lse), or null
+  const float *init_lse;
+  float *part_o;              // pieces: [workers][2][rows][D], [workers][2][rows][2]
+  float *part_ml;
+  int n_workers, min_span;    // min_span: key tiles a span holds at least
+  unsigned int *status;
+  unsigned long long wait_ns;
+};
+
+struct SeqInfo {
+  int slot, q0, nq, len;      // slot < 0: nothing of it may be read
+};
+
+__device__ __forceinline__ void paged_fail(const PagedParams &p, unsigned code) {
+  atomicCAS(p.status, 0u, code);
+}
+
+// Sequence (or group) b as the device arrays give it, every index checked.
+__device__ inline SeqInfo seq_info(const PagedParams &p, int b) {
+  SeqInfo s;
+  bool bad = false;
+  int t0 = b, t1 = b + 1;
+  if (p.group_ptr) {
+    t0 = __ldg(p.group_ptr + b);
+    t1 = __ldg(p.group_ptr + b + 1);
+    if (t0 < 0 || t1 < t0 || t1 > p.n_members) {
+      bad = true;
+      t0 = t1 = 0;
+    }
+  }
+  if (p.q_ptr) {
+    t0 = __ldg(p.q_ptr + t0);
+    t1 = __ldg(p.q_ptr + t1);
+  }
+  if (t0 < 0 || t1 < t0 || t1 > p.n_tokens) {
+    bad = true;
+    t0 = t1 = 0;
+  }
+  s.q0 = t0;
+  s.nq = t1 - t0;
+  s.slot = p.seqs ? __ldg(p.seqs + b) : b;
+  s.len = 0;
+  if (s.slot < 0 || s.slot >= p.n_slots) {
+    bad = true;
+    s.slot = -1;
+  } else {
+    s.len = __ldg(p.seq_lens + s.slot);
+    if (s.len < 0 || s.len > (static_cast<long long>(p.max_pages) << p.page_shift)) {
+      bad = true;
+      s.len = 0;
+    }
+  }
+  if (bad) paged_fail(p, ATTN_ERR_INVALID_ARG);
+  return s;
+}
+
+// Row tiles.  ROWS > 0: rows r = token * G + head of the group, packed ROWS to
+// a tile across token boundaries.  ROWS == 0 (tensor-core tiles): whole
+// tokens, `tpi` of them to a tile.
+template <int ROWS>
+__device__ __forceinline__ int tile_count(int nq, int G, int tpi) {
+  return ROWS > 0 ? (nq * G + ROWS - 1) / (ROWS > 0 ? ROWS : 1) : (nq + tpi - 1) / tpi;
+}
+template <int ROWS>
+__device__ __forceinline__ void tile_tokens(int rt, int nq, int G, int tpi, int &t0, int &t1) {
+  if (ROWS > 0) {
+    t0 = rt * ROWS / G;
+    t1 = min(nq - 1, (rt * ROWS + ROWS - 1) / G);
+  } else {
+    t0 = rt * tpi;
+    t1 = min(nq - 1, t0 + tpi - 1);
+  }
+}
+
+// Key tiles (of 2^KL keys) that tokens t0..t1 of a sequence see: tiles
+// [0, ns) for the first tokens, then [w0, w0 + n - ns).
+struct Span {
+  int ns, w0, n;
+  __device__ __forceinline__ int tile(int i) const { return i < ns ? i : i - ns + w0; }
+};
+template <int KL>
+__device__ __forceinline__ Span key_span(const PagedParams &p, const SeqInfo &s, int t0, int t1) {
+  Span x;
+  const int end = p.causal ? s.len - s.nq + t1 + 1 : s.len;
+  x.ns = x.w0 = x.n = 0;
+  if (end <= 0) return x;
+  const int lo = p.causal && p.window > 0 ? max(0, s.len - s.nq + t0 - p.window + 1) : 0;
+  x.w0 = lo >> KL;
+  const int w1 = (end + (1 << KL) - 1) >> KL;
+  if (lo > 0) x.ns = min((min(p.sinks, end) + (1 << KL) - 1) >> KL, x.w0);
+  x.n = x.ns + w1 - x.w0;
+  return x;
+}
+template <int ROWS, int KL>
+__device__ __forceinline__ Span tile_span(const PagedParams &p, const SeqInfo &s, int rt, int tpi) {
+  int t0, t1;
+  tile_tokens<ROWS>(rt, s.nq, p.G, tpi, t0, t1);
+  return key_span<KL>(p, s, t0, t1);
+}
+// Key tiles of all row tiles of one key/value head.
+template <int ROWS, int KL>
+__device__ inline long long head_tiles(const PagedParams &p, const SeqInfo &s, int tpi) {
+  const int R = tile_count<ROWS>(s.nq, p.G, tpi);
+  if (!p.causal) return R > 0 ? static_cast<long long>(R) * key_span<KL>(p, s, 0, 0).n : 0;
+  long long n = 0;
+  for (int rt = 0; rt < R; ++rt) n += tile_span<ROWS, KL>(p, s, rt, tpi).n;
+  return n;
+}
+
+// The flat list's prefix sums, first[b] = key tiles before sequence b, for
+// every thread of a CTA of NT threads; first has n_seqs + 1 entries in shared
+// memory, info n_seqs.  `scan` holds NT / 32 + 1 values.
+template <int ROWS, int KL, int NT>
+__device__ inline void make_plan(const PagedParams &p, int tpi, long long *first, SeqInfo *info,
+                                 long long *scan) {
+  const int per = (p.n_seqs + NT - 1) / NT, b0 = min(p.n_seqs, static_cast<int>(threadIdx.x) * per),
+            b1 = min(p.n_seqs, b0 + per), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const SeqInfo s = seq_info(p, b);
+    info[b] = s;
+    const long long n = head_tiles<ROWS, KL>(p, s, tpi) * p.hk;
+    first[b + 1] = n;
+    sum += n;
+  }
+  long long x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) scan[warp] = x;
+  __syncthreads();
+  long long base = x - sum;
+  for (int w = 0; w < warp; ++w) base += scan[w];
+  if (threadIdx.x == 0) first[0] = 0;
+  for (int b = b0; b < b1; ++b) {
+    base += first[b + 1];
+    first[b + 1] = base;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ long long span_of(const PagedParams &p, long long total) {
+  const long long s = (total + p.n_workers - 1) / p.n_workers;
+  return s > p.min_span ? s : p.min_span;
+}
+
+// A place in the flat list: key tile i of row tile rt of head h of sequence b.
+template <int ROWS, int KL>
+struct Walk {
+  int b, h, rt, R, i;
+  SeqInfo s;
+  Span sp;
+  __device__ __forceinline__ void load(const PagedParams &p, const SeqInfo *info, int tpi) {
+    s = info[b];
+    R = tile_count<ROWS>(s.nq, p.G, tpi);
+  }
+  // flat < first[n_seqs]
+  __device__ inline void seek(const PagedParams &p, const long long *first, const SeqInfo *info, int tpi,
+                              long long flat) {
+    int lo = 0, hi = p.n_seqs;          // first[lo] <= flat < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= flat) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    load(p, info, tpi);
+    long long rem = flat - first[b];
+    const long long per = (first[b + 1] - first[b]) / p.hk;
+    h = static_cast<int>(rem / per);
+    rem -= h * per;
+    rt = 0;
+    if (!p.causal) {
+      sp = key_span<KL>(p, s, 0, 0);
+      rt = static_cast<int>(rem / sp.n);
+      rem -= static_cast<long long>(rt) * sp.n;
+    } else {
+      for (;; ++rt) {
+        sp = tile_span<ROWS, KL>(p, s, rt, tpi);
+        if (rem < sp.n) break;
+        rem -= sp.n;
+      }
+    }
+    i = static_cast<int>(rem);
+  }
+  // To the next key tile; the caller knows that there is one.
+  __device__ inline void next(const PagedParams &p, const long long *first, const SeqInfo *info, int tpi) {
+    if (++i < sp.n) return;
+    i = 0;
+    do {
+      if (++rt == R) {
+        rt = 0;
+        if (++h == p.hk) {
+          h = 0;
+          do ++b;
+          while (first[b + 1] == first[b]);
+          load(p, info, tpi);
+        }
+      }
+      sp = tile_span<ROWS, KL>(p, s, rt, tpi);
+    } while (sp.n == 0);
+  }
+};
+
+// One row's summary (m in log2 units, l, unnormalised O) made final, with the
+// summary it starts from: the factors of O and of init_o, and its lse.
+__device__ __forceinline__ void row_final(float m, float l, float init_lse, float &fo, float &fi, float &lse) {
+  const float mi = init_lse * kLog2e;          // -inf: nothing to start from
+  const float M = fmaxf(m, mi);
+  if (M == -INFINITY || (l == 0.f && mi == -INFINITY)) {
+    fo = fi = 0.f;
+    lse = -INFINITY;
+    return;
+  }
+  const float a = l > 0.f ? exp2f(m - M) : 0.f, c = exp2f(mi - M), L = a * l + c, inv = 1.f / L;
+  fo = a * inv;
+  fi = c * inv;
+  lse = (M + log2f(L)) * kLn2;
+}
+
+// Writes columns c, c+1 of a finished row.
+template <int D>
+__device__ __forceinline__ void store_pair(const PagedParams &p, long long row, int c, float x, float y, float fo,
+                                           float fi) {
+  x *= fo;
+  y *= fo;
+  const long long at = row * D + c;
+  if (fi != 0.f) {
+    const float2 i = *reinterpret_cast<const float2 *>(p.init_o + at);
+    x += fi * i.x;
+    y += fi * i.y;
+  }
+  if (p.out_f32)
+    *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at) = make_float2(x, y);
+  else
+    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + at) = pack_bf16x2(x, y);
+}
+
+// Rows of items without a key tile: their sequences see nothing (here).
+template <int D, int ROWS, int KL>
+__device__ inline void finish_empty(const PagedParams &p, const SeqInfo *info, int tpi) {
+  if (p.group_ptr) {
+    // tokens before the first group and behind the last have no prefix
+    const int m0 = min(max(__ldg(p.group_ptr), 0), p.n_members);
+    const int m1 = min(max(__ldg(p.group_ptr + p.n_seqs), m0), p.n_members);
+    const int t0 = min(max(p.q_ptr ? __ldg(p.q_ptr + m0) : m0, 0), p.n_tokens);
+    const int t1 = min(max(p.q_ptr ? __ldg(p.q_ptr + m1) : m1, t0), p.n_tokens);
+    const int rest = p.n_tokens - (t1 - t0);
+    for (int t = blockIdx.x; t < rest; t += gridDim.x)
+      for (int h = threadIdx.x; h < p.hq; h += blockDim.x)
+        p.lse[static_cast<long long>(h) * p.n_tokens + (t < t0 ? t : t + t1 - t0)] = -INFINITY;
+  }
+  for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x) {
+    const SeqInfo s = info[b];
+    // causal rows see more keys the later they stand: the empty tiles come first
+    for (int rt = 0; rt < tile_count<ROWS>(s.nq, p.G, tpi); ++rt) {
+      int a, z;
+      tile_tokens<ROWS>(rt, s.nq, p.G, tpi, a, z);
+      if (key_span<KL>(p, s, a, z).n > 0) break;
+      const int rows = ROWS > 0 ? min(ROWS, s.nq * p.G - rt * ROWS) : (z - a + 1) * p.G;
+      for (int x = threadIdx.x; x < rows * p.hk * (D / 2); x += blockDim.x) {
+        const int c = x % (D / 2) * 2, y = x / (D / 2), h = y / rows, r = y - h * rows + (ROWS > 0 ? rt * ROWS : a * p.G);
+        const int t = r / p.G, head = h * p.G + r - t * p.G;
+        const long long row = static_cast<long long>(s.q0 + t) * p.hq + head;
+        const long long li = static_cast<long long>(head) * p.n_tokens + s.q0 + t;
+        float fo, fi, lse;
+        row_final(-INFINITY, 0.f, p.init_lse ? p.init_lse[li] : -INFINITY, fo, fi, lse);
+        store_pair<D>(p, row, c, 0.f, 0.f, fo, fi);
+        if (c == 0) p.lse[li] = lse;
+      }
+    }
+  }
+}
+
+}  // namespace attn

@@ -1,0 +1,485 @@
+// Attention over a paged cache for few rows per key/value head: tiles of 16
+// rows on warp-level matrix instructions, bound by the cache's bandwidth.
+//
+// One row of a decode step does 4 d flops per key read of 4 d bytes; with the
+// G query heads of a group that is G flops a byte, 25 times below what this
+// GPU needs to be bound by arithmetic at G = 4.  So the kernel is a stream:
+// every warp owns a contiguous span of 16-key slabs of the flat list (see
+// paged_plan.cuh) and a ring of NST slabs in shared memory that it alone fills
+// (cp.async, 16 bytes a lane, rows 256 bytes apart with their 16-byte chunks
+// xor-swizzled so that ldmatrix meets no bank conflict) and reads.  Warps never
+// wait for each other.  A slab of 16 keys lies in one page (pages are powers
+// of two of at least 16 tokens), so its address takes one table entry, fetched
+// a slab ahead.
+//
+// Rows of slabs behind the sequence's end are filled with zeros instead of
+// being read: what memory holds there (NaN, other sequences' tokens) must not
+// meet the zero weights of the P V product.
+//
+// Numerics: scores, running maximum, sum and O in 32 bits; P is rounded to
+// bf16 for the product with V (half a step, 2^-9, per weight, of both signs;
+// the row sum takes the unrounded values), as in attn_fwd.  The maximum is
+// only raised when it grew by more than 8 (log2), so P stays below 2^8.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "attn_internal.h"
+#include "paged_plan.cuh"
+
+namespace attn {
+
+constexpr int PR_ROWS = 16, PR_KL = 4, PR_WARPS = 8;
+constexpr float PR_TAU = 8.0f;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D, int NST>
+struct RowsSmem {
+  static constexpr int SLAB = 16 * D * 2;                       // keys or values of one slab
+  static constexpr int RING = PR_WARPS * NST * 2 * SLAB;
+  static constexpr int SCAN = RING;
+  static constexpr int FIRST = SCAN + (PR_WARPS + 1) * 8;
+  static size_t bytes(int n_seqs) { return FIRST + 8ull * (n_seqs + 1) + sizeof(SeqInfo) * n_seqs; }
+};
+
+template <int D, int NST>
+__global__ void __launch_bounds__(PR_WARPS * 32, 1) paged_rows_kernel(const PagedParams p) {
+  using S = RowsSmem<D, NST>;
+  extern __shared__ __align__(128) uint8_t rows_smem[];
+  long long *scan = reinterpret_cast<long long *>(rows_smem + S::SCAN);
+  long long *first = reinterpret_cast<long long *>(rows_smem + S::FIRST);
+  SeqInfo *info = reinterpret_cast<SeqInfo *>(first + p.n_seqs + 1);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  make_plan<PR_ROWS, PR_KL, PR_WARPS * 32>(p, 0, first, info, scan);
+  finish_empty<D, PR_ROWS, PR_KL>(p, info, 0);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long total = first[p.n_seqs], span = span_of(p, total);
+  const long long worker = static_cast<long long>(blockIdx.x) * PR_WARPS + warp;
+  const long long from = worker * span, to = min(total, from + span);
+  if (from >= to) return;
+  const int cnt = static_cast<int>(to - from);
+
+  const uint32_t ring = smem_u32(rows_smem) + warp * (NST * 2 * S::SLAB);
+  Walk<PR_ROWS, PR_KL> in, at;     // slab being fetched, slab being used
+  in.seek(p, first, info, 0, from);
+  at = in;
+  const int page_mask = (1 << p.page_shift) - 1;
+  auto page_of = [&](const Walk<PR_ROWS, PR_KL> &w) -> int {
+    return __ldg(p.table + w.s.slot * p.table_stride + ((w.sp.tile(w.i) << PR_KL) >> p.page_shift));
+  };
+  int page = page_of(in);
+  // fetches the slab `in` stands at and steps on
+  auto fetch = [&](int n) {
+    if (n < cnt) {
+      const int key0 = in.sp.tile(in.i) << PR_KL;
+      const bool good = page >= 0 && page < p.n_pages;
+      if (!good && lane == 0) paged_fail(p, ATTN_ERR_INVALID_ARG);
+      const long long base = (good ? page * p.page_stride : 0) + (key0 & page_mask) * p.token_stride +
+                             in.h * p.head_stride;
+      const int rows = good ? in.s.len - key0 : 0;          // those behind the end read as zeros
+      const uint32_t dst = ring + (n % NST) * (2 * S::SLAB);
+      constexpr int CH = D / 8, RPI = 32 / CH;               // chunks a row, rows an instruction
+      const int c = lane % CH, r0 = lane / CH;
+#pragma unroll
+      for (int i = 0; i < 16 / RPI; ++i) {
+        const int r = i * RPI + r0;
+        const long long off = r < rows ? base + r * p.token_stride + c * 8 : 0;
+        const uint32_t d = dst + r * (D * 2) + ((c ^ (r & 7)) << 4);
+        cp_async16(d, static_cast<const uint16_t *>(p.k) + off, r < rows ? 16u : 0u);
+        cp_async16(d + S::SLAB, static_cast<const uint16_t *>(p.v) + off, r < rows ? 16u : 0u);
+      }
+      if (n + 1 < cnt) {
+        in.next(p, first, info, 0);
+        page = page_of(in);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int n = 0; n < NST - 1; ++n) fetch(n);
+
+  uint32_t qf[D / 16][4];
+  float o[D / 8][4];
+  float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
+  int pos0 = -1, pos1 = -1, lo0 = 0, lo1 = 0;      // last key a row sees, first of its window
+  int all_lo = 0, all_hi = 0;                      // keys in [all_lo, all_hi) are seen by every row
+  long long row0 = -1, row1 = -1;                  // (token * hq + head), -1: no row
+  int rows_here = 0, piece0 = 0;
+  const float sl2 = p.scale_log2;
+  const int lr = lane >> 2, lc = (lane & 3) * 2;
+
+  for (int n = 0; n < cnt; ++n) {
+    cp_wait<NST - 2>();
+    __syncwarp();
+    fetch(n + NST - 1);
+    if (n == 0 || at.i == 0) {
+      // a new item: its rows of Q as matrix fragments, summaries empty
+      piece0 = at.i;
+      rows_here = min(PR_ROWS, at.s.nq * p.G - at.rt * PR_ROWS);
+      auto place = [&](int r, long long &row, int &pos, int &lo) {
+        row = -1;
+        pos = -1;
+        lo = 0;
+        if (r < rows_here) {
+          const int x = at.rt * PR_ROWS + r, t = x / p.G;
+          row = static_cast<long long>(at.s.q0 + t) * p.hq + at.h * p.G + x - t * p.G;
+          pos = p.causal ? at.s.len - at.s.nq + t : at.s.len - 1;
+          lo = p.causal && p.window > 0 ? pos - p.window + 1 : 0;
+        }
+      };
+      place(lr, row0, pos0, lo0);
+      place(lr + 8, row1, pos1, lo1);
+      {
+        int t0, t1;
+        tile_tokens<PR_ROWS>(at.rt, at.s.nq, p.G, 0, t0, t1);
+        all_hi = p.causal ? at.s.len - at.s.nq + t0 + 1 : at.s.len;
+        all_lo = p.causal && p.window > 0 ? at.s.len - at.s.nq + t1 - p.window + 1 : 0;
+      }
+      const uint16_t *q0 = static_cast<const uint16_t *>(p.q) + (row0 < 0 ? 0 : row0) * D + lc;
+      const uint16_t *q1 = static_cast<const uint16_t *>(p.q) + (row1 < 0 ? 0 : row1) * D + lc;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        qf[k][0] = row0 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(q0 + k * 16));
+        qf[k][1] = row1 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(q1 + k * 16));
+        qf[k][2] = row0 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(q0 + k * 16 + 8));
+        qf[k][3] = row1 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(q1 + k * 16 + 8));
+      }
+      m0 = m1 = -INFINITY;
+      l0 = l1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+    }
+    const uint32_t ks = ring + (n % NST) * (2 * S::SLAB), vs = ks + S::SLAB;
+    const int key0 = at.sp.tile(at.i) << PR_KL;
+    // S = Q K^T: 16 rows x 16 keys
+    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      const int r = ((lane >> 4) << 3) + (lane & 7), cb = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t b[4];
+        ldsm4(ks + r * (D * 2) + (((2 * k + cb) ^ (r & 7)) << 4), b);
+        mma16816(s0, qf[k], b[0], b[1]);
+        mma16816(s1, qf[k], b[2], b[3]);
+      }
+    }
+    float x[8] = {s0[0] * sl2, s0[1] * sl2, s1[0] * sl2, s1[1] * sl2,     // row lr
+                  s0[2] * sl2, s0[3] * sl2, s1[2] * sl2, s1[3] * sl2};    // row lr + 8
+    if (key0 + 16 > all_hi || (key0 < all_lo && key0 + 16 > p.sinks)) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = key0 + (e >> 1) * 8 + lc + (e & 1);
+        if (!(j <= pos0 && (j >= lo0 || j < p.sinks))) x[e] = -INFINITY;
+        if (!(j <= pos1 && (j >= lo1 || j < p.sinks))) x[4 + e] = -INFINITY;
+      }
+    }
+    float a0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), a1 = fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]));
+    a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
+    a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
+    a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
+    a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
+    const bool g0 = a0 > m0 + PR_TAU, g1 = a1 > m1 + PR_TAU;
+    if (__any_sync(0xffffffffu, g0 || g1)) {
+      const float f0 = g0 ? ex2_approx(m0 - a0) : 1.f, f1 = g1 ? ex2_approx(m1 - a1) : 1.f;
+      if (g0) m0 = a0;
+      if (g1) m1 = a1;
+      l0 *= f0;
+      l1 *= f1;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        o[j][0] *= f0;
+        o[j][1] *= f0;
+        o[j][2] *= f1;
+        o[j][3] *= f1;
+      }
+    }
+    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = ex2_approx(x[e] - b0);
+      x[4 + e] = ex2_approx(x[4 + e] - b1);
+    }
+    l0 += (x[0] + x[1]) + (x[2] + x[3]);
+    l1 += (x[4] + x[5]) + (x[6] + x[7]);
+    const uint32_t pf[4] = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[2], x[3]),
+                            pack_bf16x2(x[6], x[7])};
+    // O += P V
+    {
+      const int r = (((lane >> 3) & 1) << 3) + (lane & 7), cb = lane >> 4;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t b[4];
+        ldsm4t(vs + r * (D * 2) + (((2 * j + cb) ^ (r & 7)) << 4), b);
+        mma16816(o[2 * j], pf, b[0], b[1]);
+        mma16816(o[2 * j + 1], pf, b[2], b[3]);
+      }
+    }
+    const bool ends = at.i == at.sp.n - 1;
+    if (ends || n == cnt - 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+      if (ends && piece0 == 0) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const long long row = u ? row1 : row0;
+          if (row < 0) continue;
+          const int head = static_cast<int>(row % p.hq);
+          const long long li = static_cast<long long>(head) * p.n_tokens + row / p.hq;
+          float fo, fi, lse;
+          row_final(u ? m1 : m0, u ? l1 : l0, p.init_lse ? p.init_lse[li] : -INFINITY, fo, fi, lse);
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) store_pair<D>(p, row, j * 8 + lc, o[j][2 * u], o[j][2 * u + 1], fo, fi);
+          if (lc == 0) p.lse[li] = lse;
+        }
+      } else {
+        // slot 0: the piece a span begins with; slot 1: one that begins in it and goes on
+        const long long slot = worker * 2 + (n - (at.i - piece0) == 0 ? 0 : 1);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (lr + 8 * u >= rows_here) continue;
+          const long long r = slot * PR_ROWS + lr + 8 * u;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<float2 *>(p.part_o + r * D + j * 8 + lc) = make_float2(o[j][2 * u], o[j][2 * u + 1]);
+          if (lc == 0)
+            *reinterpret_cast<float2 *>(p.part_ml + r * 2) = make_float2(u ? m1 : m0, u ? l1 : l0);
+        }
+      }
+    }
+    if (n + 1 < cnt) at.next(p, first, info, 0);
+  }
+}
+
+// ---------------------------------------------------------------------- join
+
+// Merges the pieces of the items that cross span boundaries: block x looks at
+// the boundary between spans x and x + 1 and, if it is the first inside an
+// item, merges that item's rows (blockIdx.y of gridDim.y takes every
+// gridDim.y-th).  Few pieces: one warp a row.  Many (a long sequence alone in
+// the batch): the block's warps share a row's pieces and add their sums.
+template <int D, int ROWS, int KL, int TILE_ROWS>
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, int tpi) {
+  constexpr int NW = 8, V = D / 32;
+  extern __shared__ __align__(16) uint8_t join_smem[];
+  long long *scan = reinterpret_cast<long long *>(join_smem);
+  float *red = reinterpret_cast<float *>(join_smem + 80);          // [NW][D + 2]
+  long long *first = reinterpret_cast<long long *>(join_smem + 80 + NW * (D + 4) * 4);
+  SeqInfo *info = reinterpret_cast<SeqInfo *>(first + p.n_seqs + 1);
+  make_plan<ROWS, KL, 256>(p, tpi, first, info, scan);
+  // every block waits, those without work too: what follows on the stream
+  // relies on this grid's end for the end of the one before it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long total = first[p.n_seqs], span = span_of(p, total);
+  const long long cut = (blockIdx.x + 1) * span;
+  if (cut >= total) return;
+  Walk<ROWS, KL> w;
+  w.seek(p, first, info, tpi, cut);
+  const long long f0 = cut - w.i, f1 = f0 + w.sp.n;
+  if (w.i == 0 || f0 < cut - span) return;      // the cut lies between items, or is not the item's first
+  const long long wk0 = f0 / span;
+  const int np = static_cast<int>((f1 - 1) / span - wk0) + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int rows, x0;                                  // the tile's rows, its first packed row
+  if (ROWS > 0) {
+    x0 = w.rt * TILE_ROWS;
+    rows = min(TILE_ROWS, w.s.nq * p.G - x0);
+  } else {
+    x0 = w.rt * tpi * p.G;
+    rows = min(tpi, w.s.nq - w.rt * tpi) * p.G;
+  }
+  // a piece's place: the item's first piece is its worker's second slot unless the span begins with it
+  auto place = [&](int i, int r) -> long long {
+    return ((wk0 + i) * 2 + (i == 0 && f0 != wk0 * span ? 1 : 0)) * TILE_ROWS + r;
+  };
+  auto finish = [&](int r, float m, float l, const float (&acc)[V]) {
+    const int x = x0 + r, t = x / p.G, head = w.h * p.G + x - t * p.G;
+    const long long row = static_cast<long long>(w.s.q0 + t) * p.hq + head;
+    const long long li = static_cast<long long>(head) * p.n_tokens + w.s.q0 + t;
+    float fo, fi, lse;
+    row_final(m, l, p.init_lse ? p.init_lse[li] : -INFINITY, fo, fi, lse);
+#pragma unroll
+    for (int c = 0; c < V; c += 2) store_pair<D>(p, row, lane * V + c, acc[c], acc[c + 1], fo, fi);
+    if (lane == 0) p.lse[li] = lse;
+  };
+  // pieces i0, i0 + step, ... of row r summed by one warp
+  auto gather = [&](int r, int i0, int step, float &m, float &l, float (&acc)[V]) {
+    m = -INFINITY;
+    for (int i = i0 + lane * step; i < np; i += 32 * step) m = fmaxf(m, p.part_ml[place(i, r) * 2]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    l = 0.f;
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] = 0.f;
+    const float mb = m == -INFINITY ? 0.f : m;
+    for (int base = i0; base < np; base += 32 * step) {
+      float f = 0.f;
+      if (base + lane * step < np) {
+        const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + place(base + lane * step, r) * 2);
+        f = exp2f(ml.x - mb);
+        l += f * ml.y;
+      }
+      const int k1 = min(32, (np - base + step - 1) / step);
+#pragma unroll 8
+      for (int k = 0; k < k1; ++k) {
+        const float g = __shfl_sync(0xffffffffu, f, k);
+        const float *src = p.part_o + place(base + k * step, r) * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 y = *reinterpret_cast<const float4 *>(src);
+          acc[0] = fmaf(g, y.x, acc[0]);
+          acc[1] = fmaf(g, y.y, acc[1]);
+          acc[2] = fmaf(g, y.z, acc[2]);
+          acc[3] = fmaf(g, y.w, acc[3]);
+        } else {
+          const float2 y = *reinterpret_cast<const float2 *>(src);
+          acc[0] = fmaf(g, y.x, acc[0]);
+          acc[1] = fmaf(g, y.y, acc[1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  };
+  float m, l, acc[V];
+  if (np <= 2 * NW) {
+    for (int r = blockIdx.y * NW + warp; r < rows; r += gridDim.y * NW) {
+      gather(r, 0, 1, m, l, acc);
+      finish(r, m, l, acc);
+    }
+    return;
+  }
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    gather(r, warp, NW, m, l, acc);
+    float *mine = red + warp * (D + 4);
+#pragma unroll
+    for (int c = 0; c < V; ++c) mine[lane * V + c] = acc[c];
+    if (lane == 0) {
+      mine[D] = m;
+      mine[D + 1] = l;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) mt = fmaxf(mt, red[k * (D + 4) + D]);
+      const float mb = mt == -INFINITY ? 0.f : mt;
+#pragma unroll
+      for (int c = 0; c < V; ++c) acc[c] = 0.f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) {
+        const float f = exp2f(red[k * (D + 4) + D] - mb);
+        lt += f * red[k * (D + 4) + D + 1];
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(f, red[k * (D + 4) + lane * V + c], acc[c]);
+      }
+      finish(r, mt, lt, acc);
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------- host
+
+template <typename K>
+static int raise_smem(K kern, size_t bytes, bool *done) {
+  if (*done) return ATTN_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  *done = true;
+  return ATTN_OK;
+}
+
+// A launch that may start while the one before it on the stream drains; it
+// waits for that one's memory before it reads any of it.
+template <typename... A>
+static int launch_after(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+constexpr size_t kSmemMax = 232448;
+
+template <int D, int NST>
+static int launch_rows(PagedParams p, cudaStream_t s) {
+  using S = RowsSmem<D, NST>;
+  constexpr int kDev = 64;
+  static bool done[kDev] = {}, joined[kDev] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDev) return ATTN_ERR_CUDA;
+  auto kern = paged_rows_kernel<D, NST>;
+  auto join = paged_join_kernel<D, PR_ROWS, PR_KL, PR_ROWS>;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (raise_smem(kern, kSmemMax, &done[dev]) != ATTN_OK || raise_smem(join, kSmemMax, &joined[dev]) != ATTN_OK)
+      return ATTN_ERR_CUDA;
+  }
+  const int sms = device_sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  p.n_workers = sms * PR_WARPS;
+  p.min_span = 2;
+  kern<<<sms, PR_WARPS * 32, S::bytes(p.n_seqs), s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  const size_t js = 80 + 8 * (D + 4) * 4 + 8ull * (p.n_seqs + 1) + sizeof(SeqInfo) * p.n_seqs;
+  const unsigned gy = static_cast<unsigned>(p.G < PR_ROWS ? (p.G < 4 ? p.G : 4) : 4);
+  return launch_after(join, dim3(p.n_workers - 1, gy), 256, js, s, p, 0);
+}
+
+// Workers and rows of a piece, for the workspace.
+size_t paged_rows_workspace(int d) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return 0;
+  return static_cast<size_t>(sms) * PR_WARPS * 2 * PR_ROWS * (d + 2) * sizeof(float);
+}
+
+int paged_rows_launch(PagedParams p, int d, cudaStream_t s) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  p.part_ml = p.part_o + static_cast<size_t>(sms) * PR_WARPS * 2 * PR_ROWS * d;
+  if (d == 128)
+    return RowsSmem<128, 3>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<128, 3>(p, s) : launch_rows<128, 2>(p, s);
+  return RowsSmem<64, 6>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<64, 6>(p, s) : launch_rows<64, 4>(p, s);
+}
+
+}  // namespace attn

@@ -1,0 +1,259 @@
+"""Attention over a paged cache against the float64 oracle: window, first
+tokens, ragged batches, shared prefixes, layouts, and what a cache holds in
+places that no token owns."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import paged_cases as P
+from block_sparse_attention_slice_gb300 import (attn_build_tiles, attn_bwd, attn_fwd, attn_last_device_error, attn_paged_fwd,
+                                                attn_prefix_fwd, attn_slices_from_windows)
+from block_sparse_attention_slice_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+
+def paged(c, window=0, sinks=0, **kw):
+    return attn_paged_fwd(c["q"], c["k"], c["v"], c["d_table"], c["d_lens"], c["scale"], q_ptr=kw.pop("q_ptr", c["d_q_ptr"]),
+                          window=window, sinks=sinks, seqs=c["d_seqs"], **kw)
+
+
+def prefix(c, **kw):
+    return attn_prefix_fwd(c["q"], c["k"], c["v"], c["d_ptable"], c["d_plens"], c["d_first"], c["d_table"], c["d_lens"],
+                           c["scale"], q_ptr=kw.pop("q_ptr", c["d_q_ptr"]), seqs=c["d_seqs"], **kw)
+
+
+ONE = [  # lens, page, hq, hk, d, window, sinks
+    ([1], 16, 1, 1, 64, 0, 0), ([17], 16, 4, 1, 128, 0, 0), ([0, 1, 15, 16, 17, 0, 33], 16, 8, 2, 128, 0, 0),
+    ([2000], 64, 32, 8, 128, 0, 0), ([2000, 3, 777], 32, 16, 16, 64, 0, 0), ([1030, 60, 5], 16, 6, 2, 64, 64, 4),
+    ([1030, 60, 5, 68, 69, 70], 128, 5, 1, 128, 64, 5), ([500, 499], 256, 16, 1, 128, 1, 0), ([500, 499], 16, 20, 1, 64, 1, 1),
+    ([513, 40], 16, 4, 2, 128, 37, 100), ([300], 16, 33, 1, 64, 17, 16), ([700], 1024, 8, 8, 128, 2 ** 31 - 1, 2 ** 31 - 1)]
+
+
+@pytest.mark.parametrize("lens,page,hq,hk,d,window,sinks", ONE)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_token_each(lens, page, hq, hk, d, window, sinks, dtype):
+    c = P.make(lens, [1] * len(lens), page, hq, hk, d, seed=len(lens) + d)
+    out, lse = paged(c, window, sinks, q_ptr=None, out_dtype=dtype)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c, window, sinks))
+
+
+MANY = [  # lens, news, page, hq, hk, d, window, sinks
+    ([40, 3, 9], [5, 3, 9], 16, 4, 2, 64, 0, 0), ([40, 3, 0, 9], [5, 6, 2, 0], 16, 4, 2, 64, 0, 0),
+    ([300, 130], [7, 130], 32, 6, 2, 128, 20, 3), ([300, 130], [70, 33], 64, 8, 1, 64, 64, 1),
+    ([257], [257], 16, 5, 1, 128, 16, 2), ([600, 200, 50], [200, 1, 50], 128, 16, 4, 128, 100, 7),
+    ([1000], [300], 16, 8, 2, 128, 0, 0), ([129, 513], [129, 257], 16, 2, 2, 64, 0, 0), ([400], [65], 256, 40, 1, 64, 50, 0)]
+
+
+@pytest.mark.parametrize("lens,news,page,hq,hk,d,window,sinks", MANY)
+@pytest.mark.parametrize("max_q", [1, None])
+def test_several_tokens_each(lens, news, page, hq, hk, d, window, sinks, max_q):
+    c = P.make(lens, news, page, hq, hk, d, seed=sum(news) + d)
+    out, lse = paged(c, window, sinks, max_q=max_q)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c, window, sinks))
+
+
+@pytest.mark.parametrize("layout", ["plain", "joined", "heads"])
+@pytest.mark.parametrize("garbage", [float("nan"), float("inf"), 0.0])
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_layouts_slots_and_rows_of_no_sequence(layout, garbage, max_q):
+    lens, news = [70, 9, 200], [3, 9, 40]
+    c = P.make(lens, news, 32, 8, 2, 128, seed=5, slots=[4, 0, 7], layout=layout, garbage=garbage, extra_tokens=3)
+    T = c["q"].shape[0]
+    out = torch.full((T, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((8, T), 7.0, device="cuda")
+    paged(c, 33, 2, out=out, lse=lse, max_q=max_q)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c, 33, 2))
+    for x in (out[:3], out[-3:], lse[:, :3], lse[:, -3:]):
+        assert torch.all(x == 7.0)
+
+
+@pytest.mark.parametrize("n", [1, 300, 1500, 4096])
+def test_many_sequences(n):
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, 40, n).tolist()
+    c = P.make(lens, [1] * n, 16, 2, 1, 64, seed=n)
+    out, lse = paged(c, 19, 2, q_ptr=None)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c, 19, 2))
+
+
+@pytest.mark.parametrize("hq,hk,d,page,news", [(8, 2, 128, 64, 1), (3, 1, 64, 16, 1), (16, 4, 128, 16, 37), (32, 8, 64, 512, 130)])
+def test_long_sequence_alone(hq, hk, d, page, news):
+    # one sequence: every span of every worker is a piece of its few items
+    c = P.make([20011], [news], page, hq, hk, d, seed=3)
+    ref = P.reference(c)
+    for dtype in (torch.bfloat16, torch.float32):
+        out, lse = paged(c, out_dtype=dtype)
+        P.check(c, out, lse, ref)
+    again = paged(c, out_dtype=torch.float32)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)       # the same bits every time
+    assert attn_last_device_error() == 0
+
+
+PRE = [  # plens, first, lens, news, page, hq, hk, d
+    ([100], [0, 3], [5, 1, 33], [1, 1, 1], 16, 4, 1, 64), ([1000], [0, 16], list(range(1, 17)), [1] * 16, 32, 32, 8, 128),
+    ([0, 50, 129], [0, 1, 1, 4], [7, 8, 9, 40], [1, 2, 3, 4], 16, 8, 2, 128),
+    ([300, 17], [1, 3, 4], [5, 6, 0, 2, 90], [1, 2, 2, 1, 3], 16, 6, 2, 64),     # the first and last in no group
+    ([700], [0, 40], [20] * 40, [5] * 40, 64, 8, 1, 128), ([64, 64], [0, 1, 2], [3, 4], [3, 4], 64, 40, 1, 64),
+    ([2500], [0, 2], [600, 300], [300, 300], 128, 4, 2, 128)]
+
+
+@pytest.mark.parametrize("plens,first,lens,news,page,hq,hk,d", PRE)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_shared_prefix(plens, first, lens, news, page, hq, hk, d, dtype):
+    c = P.make(lens, news, page, hq, hk, d, seed=len(lens), plens=plens, first=first)
+    out, lse = prefix(c, out_dtype=dtype)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c))
+
+
+def test_no_prefix_at_all_equals_the_paged_call():
+    c = P.make([50, 60], [1, 1], 16, 8, 2, 128, seed=1)
+    none = torch.empty((0, 3), dtype=torch.int32, device="cuda")
+    a = attn_prefix_fwd(c["q"], c["k"], c["v"], none, torch.empty(0, dtype=torch.int32, device="cuda"),
+                        torch.zeros(1, dtype=torch.int32, device="cuda"), c["d_table"], c["d_lens"], c["scale"])
+    b = paged(c, q_ptr=None)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_infinite_value_in_a_key_outside_the_window_is_not_met():
+    # token 30 is no key of the last token's window of 40 at length 100, nor
+    # one of its tile's when tiles end at multiples of 16
+    c = P.make([128], [1], 16, 4, 1, 64, seed=2)
+    j = 30
+    c["v"][c["table"][0, j // 16], j % 16] = float("inf")
+    out, lse = paged(c, 40, 4, q_ptr=None)
+    P.check(c, out, lse, P.reference(c, 40, 4))
+
+
+def test_another_stream_and_a_captured_call():
+    c = P.make([300, 40, 900], [1, 1, 1], 16, 8, 2, 128, seed=9)
+    ref = P.reference(c, 100, 4)
+    s = torch.cuda.Stream()
+    out, lse = paged(c, 100, 4, q_ptr=None, stream=s)
+    s.synchronize()
+    P.check(c, out, lse, ref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out2, lse2 = paged(c, 100, 4, q_ptr=None)
+    # the graph reads lengths and pages when it runs
+    c["d_lens"] -= 3
+    g.replay()
+    torch.cuda.synchronize()
+    c["lens"] = c["lens"] - 3
+    P.check(c, out2, lse2, P.reference(c, 100, 4))
+    assert attn_last_device_error() == 0
+
+
+def test_two_calls_at_once_with_their_own_workspaces():
+    c = P.make([3000, 40, 900], [1, 1, 1], 16, 8, 2, 128, seed=9)
+    ref = P.reference(c)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = [paged(c, q_ptr=None, stream=streams[i % 3]) for i in range(9)]
+    torch.cuda.synchronize()
+    for out, lse in got:
+        P.check(c, out, lse, ref)
+
+
+@pytest.mark.parametrize("what", ["slot", "length", "negative length", "page", "negative page", "q_ptr", "q_ptr end"])
+@pytest.mark.parametrize("max_q", [1, 20])
+def test_bad_device_contents_are_reported_and_read_nothing(what, max_q):
+    lens, news = [70, 33, 90], [2, 20, 1]
+    c = P.make(lens, news, 16, 8, 2, 128, seed=8, slots=[0, 1, 2])
+    ref = P.reference(c)
+    if what == "slot":
+        c["d_seqs"][1] = 99
+    elif what == "length":
+        c["d_lens"][1] = 16 * c["table"].shape[1] + 1
+    elif what == "negative length":
+        c["d_lens"][1] = -5
+    elif what == "page":
+        c["d_table"][1, 1] = c["k"].shape[0]
+    elif what == "negative page":
+        c["d_table"][1, 1] = -1
+    elif what == "q_ptr":
+        c["d_q_ptr"][1] = -1
+    elif what == "q_ptr end":
+        c["d_q_ptr"][3] = 10 ** 6
+    out, lse = paged(c, max_q=max_q)
+    assert attn_last_device_error() == B.ATTN_ERR_INVALID_ARG
+    assert attn_last_device_error() == 0
+    fine = {"q_ptr": [2], "q_ptr end": [0, 1]}.get(what, [0, 2])       # sequences that are served
+    for b in range(3):
+        if b not in fine:
+            for x in ref:
+                (x if x.shape[0] == len(c["q"]) else x.T)[c["q_ptr"][b]:c["q_ptr"][b + 1]] = np.nan
+    P.check(c, out, lse, ref)
+    if what in ("slot", "length", "negative length"):
+        rows = slice(c["q_ptr"][1], c["q_ptr"][2])
+        assert torch.all(out[rows] == 0) and torch.all(torch.isneginf(lse[:, rows]))
+
+
+def test_offsets_past_32_bits():
+    # pages far apart: the last one starts beyond 2^31 elements
+    page, hk, d, n_pages = 256, 8, 128, 8300
+    k = torch.empty((n_pages, page, hk, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    table = torch.tensor([[n_pages - 1, 0, n_pages - 2]], dtype=torch.int32, device="cuda")
+    small = {}
+    for name, x in (("k", k), ("v", v)):
+        y = torch.randn((3, page, hk, d), device="cuda").bfloat16()
+        for i, at in enumerate(table[0].tolist()):
+            x[at] = y[i]
+        small[name] = y
+    assert (n_pages - 2) * page * hk * d > 2 ** 31
+    q = torch.randn((1, 32, d), device="cuda").bfloat16()
+    lens = torch.tensor([700], dtype=torch.int32, device="cuda")
+    near = torch.arange(3, dtype=torch.int32, device="cuda")[None]
+    for n in (1, 40):
+        qq = q.repeat(n, 1, 1) if n > 1 else q
+        ptr = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        a = attn_paged_fwd(qq, k, v, table, lens, 0.1, q_ptr=ptr)
+        b = attn_paged_fwd(qq, small["k"], small["v"], near, lens, 0.1, q_ptr=ptr)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert attn_last_device_error() == 0
+
+
+def test_a_prompt_and_its_tokens_agree_with_the_windowed_slices():
+    # the mask of training, through the slice list, and of serving, through
+    # the cache, are one: the same rows of the same sequence
+    n, h, d, window, sinks = 700, 4, 128, 100, 3
+    c = P.make([n], [n], 16, h, h, d, seed=4)
+    k, v = (oracle.paged.cached_rows(c[x], c["table"][0], n) for x in ("k64", "v64"))
+    dev = lambda x: torch.from_numpy(x).bfloat16().cuda()  # noqa: E731
+    tiles = attn_build_tiles(attn_slices_from_windows([n], window, sinks), n, n)
+    out, lse = attn_fwd(c["q"], dev(k), dev(v), tiles, c["scale"])
+    ref = P.reference(c, window, sinks)
+    P.check(c, out, lse, ref)
+    P.check(c, *paged(c, window, sinks), ref)
+
+
+def test_gradients_of_the_windowed_mask():
+    lengths, window, sinks, h, d = [130, 1, 300], 40, 5, 2, 64
+    n = sum(lengths)
+    rng = np.random.default_rng(0)
+    q, k, v, do = (torch.from_numpy(rng.standard_normal((n, h, d)).astype(np.float32)).bfloat16().cuda() for _ in range(4))
+    tiles = attn_build_tiles(attn_slices_from_windows(lengths, window, sinks), n, n)
+    scale = d ** -0.5
+    out, lse = attn_fwd(q, k, v, tiles, scale, out_dtype=torch.float32)
+    got = attn_bwd(q, k, v, out, do, lse, tiles, scale)
+    seen = np.zeros((n, n), bool)
+    at = 0
+    for m in lengths:
+        i, j = np.arange(m)[:, None], np.arange(m)[None]
+        seen[at:at + m, at:at + m] = (j <= i) & ((j > i - window) | (j < sinks))
+        at += m
+    x = [t.double().cpu().requires_grad_() for t in (q, k, v)]
+    s = torch.einsum("ihd,jhd->hij", x[0], x[1]) * scale
+    p = torch.softmax(s.masked_fill(~torch.from_numpy(seen), -np.inf), -1)
+    torch.einsum("hij,jhd->ihd", p, x[2]).backward(do.double().cpu())
+    for a, b in zip(got, x):
+        e = (a.double().cpu() - b.grad).abs().max() / b.grad.abs().max()
+        assert e < 0.02, e
+    assert attn_last_device_error() == 0

@@ -1,0 +1,148 @@
+"""Attention over a paged cache, on the CPU: the oracle against brute force,
+the windowed slice list, and every refusal made before a launch."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import oracle
+from block_sparse_attention_slice_gb300 import binding as B
+from block_sparse_attention_slice_gb300 import paging as G
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from block_sparse_attention_slice_gb300 import _build
+    _build.build()
+    return B.load()
+
+
+@pytest.mark.parametrize("lengths", [[], [0], [1], [7, 0, 30], [64, 33, 100]])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (0, 5), (1, 0), (1, 1), (4, 0), (4, 3), (10, 40), (200, 2), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_windowed_slices_are_the_mask(lib, lengths, window, sinks):
+    got = G.attn_slices_from_windows(lengths, window, sinks)
+    n = sum(lengths)
+    want = np.zeros((n, n), bool)
+    at = 0
+    for m in lengths:
+        for i in range(m):
+            for j in range(i + 1):
+                want[at + i, at + j] = window == 0 or j > i - window or j < sinks
+        at += m
+    if n:
+        assert np.array_equal(oracle.mask_rows(got, np.arange(n), n), want)
+    assert len(got) <= 3 * len(lengths)
+    r = [x for x in got.tolist()]
+    for i, a in enumerate(r):
+        for b in r[i + 1:]:
+            assert not (a[0] < b[1] and b[0] < a[1] and a[2] < b[3] and b[2] < a[3])
+
+
+def test_windowed_slices_refusals(lib):
+    for args in (([-1], 1, 0), ([3], -1, 0), ([3], 1, -1), ([2 ** 31 - 1, 1], 1, 0)):
+        with pytest.raises(B.AttnError) as e:
+            G.attn_slices_from_windows(*args)
+        assert e.value.code == B.ATTN_ERR_INVALID_ARG
+    n = ctypes.c_int(0)
+    a = (ctypes.c_int32 * 1)(100)
+    assert lib.attn_slices_from_windows(a, 1, 4, 1, None, 0, ctypes.byref(n)) == B.ATTN_ERR_CAPACITY
+    assert n.value == 3
+    assert lib.attn_slices_from_windows(a, 1, 4, 1, None, 0, None) == B.ATTN_ERR_INVALID_ARG
+
+
+def test_oracle_paged_is_the_dense_oracle():
+    rng = np.random.default_rng(0)
+    n, H, hk, d, page = 37, 4, 2, 8, 16
+    k, v = rng.standard_normal((2, 5, page, hk, d))
+    table = np.array([[3, 0, 4]])
+    q = rng.standard_normal((n, H, d))
+    O, lse, _, _ = oracle.oracle_paged(q, k, v, table, [n], [0, n], 0.3, 7, 2)
+    kk, vv = (oracle.paged.cached_rows(x, table[0], n) for x in (k, v))
+    i, j = np.arange(n)[:, None], np.arange(n)
+    mask = (j <= i) & ((j > i - 7) | (j < 2))
+    ref = oracle.oracle_attention(q, kk, vv, 0.3, lambda r: mask[r])
+    for h in range(H):
+        assert np.allclose(O[:, h], ref[h][1]) and np.allclose(lse[h], ref[h][2])
+    # the first 20 tokens as a prefix of the others
+    pre = (table, [20], [0, 1])
+    rest = np.array([[1, 2]])
+    k2, v2 = k.copy(), v.copy()
+    for x, y in ((k2, kk), (v2, vv)):
+        for u in range(n - 20):
+            x[rest[0, u // page], u % page] = y[20 + u]
+    O2, l2, _, _ = oracle.oracle_paged(q[20:], k2, v2, rest, [n - 20], [0, n - 20], 0.3, prefix=pre)
+    O1, l1, _, _ = oracle.oracle_paged(q, k, v, table, [n], [0, n], 0.3)
+    assert np.allclose(O2, O1[20:]) and np.allclose(l2, l1[:, 20:])
+
+
+X = ctypes.c_void_p(4096)      # an aligned address that no refused call reads
+
+
+def _args(**kw):
+    pages = G.AttnPages(4096, 4096, 10, 16, 2, 128, 16 * 256, 256, 128)
+    seqs = G.AttnSeqs(4096, 4096, None, 4, 3, 4, 3, 0)
+    pre = G.AttnSeqs(4096, 4096, None, 4, 1, 4, 1, 0)
+    a = dict(q=X, q_ptr=X, n_tokens=5, max_q=2, hq=4, scale=1.0, window=0, sinks=0, out=X, out_dtype=0, lse=X, ws=X, ws_bytes=1 << 40,
+             group_ptr=X, pages=pages, seqs=seqs, pre=pre)
+    for name, value in kw.items():
+        if "__" in name:
+            setattr(a[name.split("__")[0]], name.split("__")[1], value)
+        else:
+            a[name] = value
+    return a
+
+
+def _call(lib, a, prefix):
+    ref = lambda x: None if x is None else ctypes.byref(x)  # noqa: E731
+    if prefix:
+        return lib.attn_prefix_fwd(a["q"], a["q_ptr"], a["n_tokens"], a["max_q"], a["hq"], ref(a["pages"]), ref(a["pre"]), a["group_ptr"],
+                                   ref(a["seqs"]), a["scale"], a["out"], a["out_dtype"], a["lse"], a["ws"], a["ws_bytes"], None)
+    return lib.attn_paged_fwd(a["q"], a["q_ptr"], a["n_tokens"], a["max_q"], a["hq"], ref(a["pages"]), ref(a["seqs"]), a["scale"],
+                              a["window"], a["sinks"], a["out"], a["out_dtype"], a["lse"], a["ws"], a["ws_bytes"], None)
+
+
+INV, UNS = B.ATTN_ERR_INVALID_ARG, B.ATTN_ERR_UNSUPPORTED
+BAD = [({"q": None}, INV), ({"out": None}, INV), ({"lse": None}, INV), ({"ws": None}, INV), ({"pages": None}, INV), ({"seqs": None}, INV),
+       ({"q_ptr": None}, INV), ({"n_tokens": -1}, INV), ({"max_q": 0}, INV), ({"hq": 0}, INV), ({"hq": 3}, INV), ({"scale": 0.0}, INV),
+       ({"scale": -1.0}, INV), ({"scale": float("nan")}, INV), ({"scale": float("inf")}, INV), ({"out_dtype": 2}, INV),
+       ({"pages__k": None}, INV), ({"pages__v": None}, INV), ({"pages__n_pages": 0}, INV), ({"pages__hk": 0}, INV), ({"pages__d": 96}, UNS),
+       ({"pages__page_size": 8}, UNS), ({"pages__page_size": 48}, UNS), ({"pages__page_size": 0}, UNS), ({"pages__k": 4098}, UNS),
+       ({"pages__page_stride": 4100}, UNS), ({"pages__token_stride": 257}, UNS), ({"pages__head_stride": -128}, UNS),
+       ({"seqs__table": None}, INV), ({"seqs__seq_lens": None}, INV), ({"seqs__n_seqs": -1}, INV), ({"seqs__n_slots": 2}, INV),
+       ({"seqs__table_stride": 3}, INV), ({"seqs__max_pages": -1}, INV), ({"q": ctypes.c_void_p(4098)}, UNS),
+       ({"out": ctypes.c_void_p(4104)}, UNS), ({"ws": ctypes.c_void_p(4104)}, UNS)]
+
+
+@pytest.mark.parametrize("change,code", BAD, ids=[str(i) for i in range(len(BAD))])
+@pytest.mark.parametrize("prefix", [False, True])
+def test_refusals(lib, change, code, prefix):
+    assert _call(lib, _args(**change), prefix) == code
+
+
+def test_refusals_of_one_call(lib):
+    for change in ({"window": -1}, {"sinks": -1}):
+        assert _call(lib, _args(**change), False) == INV
+    for change in ({"group_ptr": None}, {"pre": None}, {"pre__table": None}, {"pre__table_stride": 1}, {"pre__n_slots": 0}):
+        assert _call(lib, _args(**change), True) == INV
+    for prefix in (False, True):
+        a = _args()
+        a["seqs"].seqs, a["seqs"].n_seqs = 4096, 4097
+        assert _call(lib, a, prefix) == UNS
+        a = _args()
+        a["seqs"].max_pages = a["seqs"].table_stride = (1 << 26) + 1
+        assert _call(lib, a, prefix) == UNS
+        # an empty batch is no error and launches nothing
+        assert _call(lib, _args(n_tokens=0), prefix) == B.ATTN_OK
+        a = _args(n_tokens=0, q=None, out=None, lse=None, ws=None, q_ptr=None)
+        a["seqs"].n_seqs = 0
+        assert _call(lib, a, prefix) == B.ATTN_OK
+
+
+def test_binding_refuses_wrong_tensors():
+    import torch
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16)
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        G.attn_paged_fwd(torch.zeros((1, 2, 64), dtype=torch.bfloat16), k, k, i[None], i, 1.0)      # not on a GPU
+    with pytest.raises(ValueError):
+        G.attn_paged_fwd(torch.zeros((1, 2, 64), dtype=torch.bfloat16), k, k[:, :, :1], i[None], i, 1.0)

@@ -12,11 +12,15 @@ from .binding import (ATTN_DTYPE_BF16, ATTN_DTYPE_F32, ATTN_FWD_TILE_K, ATTN_FWD
                       attn_merge, attn_selftest_wait_timeout, attn_set_exp2_poly,
                       attn_set_wait_limit_ns, attn_slices_from_block_grid,
                       attn_tiles_workspace_bytes, load)
-from .paging import attn_paged_fwd, attn_prefix_fwd, attn_slices_from_windows
+from .paging import (attn_cache_compact, attn_cache_copy_pages, attn_cache_extend, attn_cache_fork,
+                     attn_cache_free, attn_cache_trim, attn_cache_write, attn_paged_fwd,
+                     attn_prefix_fwd, attn_slices_from_windows)
 
 __all__ = ["attn_build_tiles", "attn_fwd", "attn_bwd", "attn_merge", "attn_slices_from_block_grid",
            "attn_tiles_workspace_bytes", "attn_last_device_error", "attn_set_wait_limit_ns",
            "attn_set_exp2_poly",
            "attn_selftest_wait_timeout", "Tiles", "AttnError", "load",
            "attn_paged_fwd", "attn_prefix_fwd", "attn_slices_from_windows",
+           "attn_cache_extend", "attn_cache_write", "attn_cache_fork", "attn_cache_free", "attn_cache_trim",
+           "attn_cache_compact", "attn_cache_copy_pages",
            "ATTN_DTYPE_BF16", "ATTN_DTYPE_F32", "ATTN_FWD_TILE_Q", "ATTN_FWD_TILE_K"]

@@ -29,7 +29,9 @@ EXPORTS = ["attn_tiles_workspace_bytes", "attn_build_tiles", "attn_build_tiles_n
            "attn_bwd", "attn_last_device_error",
            "attn_set_wait_limit_ns", "attn_set_exp2_poly", "attn_selftest_wait_timeout",
            "attn_strerror",
-           "attn_paged_workspace_bytes", "attn_paged_fwd", "attn_prefix_fwd", "attn_slices_from_windows"]
+           "attn_paged_workspace_bytes", "attn_paged_fwd", "attn_prefix_fwd", "attn_slices_from_windows",
+           "attn_cache_extend", "attn_cache_free", "attn_cache_trim", "attn_cache_workspace_bytes", "attn_cache_fork",
+           "attn_cache_compact", "attn_cache_copy_pages", "attn_cache_write"]
 
 
 class AttnSlice(ctypes.Structure):

@@ -5,7 +5,7 @@
 #include <cstdint>
 #include <vector>
 
-#include "../../include/attn_slice.h"
+#include "../../include/attn_paged.h"
 
 namespace attn {
 
@@ -72,7 +72,10 @@ int merge_launch(const void *const *o_parts, const float *const *lse_parts, int 
                  int part_dtype, int s_len, int h, int d, void *out, int out_dtype, float *lse,
                  cudaStream_t s);
 
-// Attention over a paged cache (paged_api.cu, paged_rows.cu).
+// Attention over a paged cache (paged_api.cu, paged_rows.cu) and its pages
+// (cache_pages.cu).
+int paged_check_pages(const attn_pages_t *g, int *shift);
+int paged_check_seqs(const attn_seqs_t *s, int page_size);
 struct PagedParams;
 size_t paged_rows_workspace(int d);
 int paged_rows_launch(PagedParams p, int d, cudaStream_t s);

@@ -41,11 +41,10 @@ int paged_status_take(unsigned int *status) {
 }
 
 namespace {
-
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+}  // namespace
 
-int check_pages(const attn_pages_t *g, int *shift) {
+int paged_check_pages(const attn_pages_t *g, int *shift) {
   if (!g || !g->k || !g->v || g->n_pages < 1 || g->hk < 1) return ATTN_ERR_INVALID_ARG;
   if (g->d != 64 && g->d != 128) return ATTN_ERR_UNSUPPORTED;
   if (g->page_size < 16 || (g->page_size & (g->page_size - 1))) return ATTN_ERR_UNSUPPORTED;
@@ -58,7 +57,7 @@ int check_pages(const attn_pages_t *g, int *shift) {
   return ATTN_OK;
 }
 
-int check_seqs(const attn_seqs_t *s, int page_size) {
+int paged_check_seqs(const attn_seqs_t *s, int page_size) {
   if (!s || s->n_seqs < 0 || s->n_slots < 0 || s->max_pages < 0) return ATTN_ERR_INVALID_ARG;
   if (s->n_seqs > ATTN_PAGED_MAX_SEQS) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(s->max_pages) * page_size > ATTN_PAGED_MAX_LEN) return ATTN_ERR_UNSUPPORTED;
@@ -69,12 +68,16 @@ int check_seqs(const attn_seqs_t *s, int page_size) {
   return ATTN_OK;
 }
 
+namespace {
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
 int check_call(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq, const attn_pages_t *pages,
                const attn_seqs_t *seqs, float scale, const void *out, int out_dtype, const float *lse, int *shift) {
   if (n_tokens < 0 || hq < 1 || max_q < 1) return ATTN_ERR_INVALID_ARG;
-  int rc = check_pages(pages, shift);
+  int rc = paged_check_pages(pages, shift);
   if (rc != ATTN_OK) return rc;
-  if ((rc = check_seqs(seqs, pages->page_size)) != ATTN_OK) return rc;
+  if ((rc = paged_check_seqs(seqs, pages->page_size)) != ATTN_OK) return rc;
   if (hq % pages->hk != 0) return ATTN_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
   if (out_dtype != ATTN_DTYPE_BF16 && out_dtype != ATTN_DTYPE_F32) return ATTN_ERR_INVALID_ARG;
@@ -170,7 +173,7 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
   int shift = 0;
   int rc = check_call(q, q_ptr, n_tokens, max_q, hq, pages, seqs, scale, out, out_dtype, lse, &shift);
   if (rc != ATTN_OK) return rc;
-  if ((rc = check_seqs(prefix, pages->page_size)) != ATTN_OK) return rc;
+  if ((rc = paged_check_seqs(prefix, pages->page_size)) != ATTN_OK) return rc;
   if (prefix->n_seqs > 0 && !group_ptr) return ATTN_ERR_INVALID_ARG;
   if (n_tokens == 0 || seqs->n_seqs == 0) return ATTN_OK;
   if (!d_ws) return ATTN_ERR_INVALID_ARG;

@@ -67,6 +67,27 @@ def _seqs(device, table, seq_lens, seqs, what=""):
                     n, width, n if seqs is None else seqs.shape[0], 0)
 
 
+class AttnCache(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("n_slots", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+def _cache(table, seq_lens, refs, page_size):
+    s = _seqs(table.device, table, seq_lens, None)
+    if not table.is_cuda:
+        raise ValueError("the cache's arrays must be CUDA tensors")
+    _ints(table.device, refs=refs)
+    return AttnCache(s.table, s.seq_lens, refs.data_ptr(), s.table_stride, s.n_slots, s.max_pages, refs.shape[0],
+                     int(page_size))
+
+
+def _lists(device, a, b=None, names=("seqs", "counts")):
+    _ints(device, **{names[0]: a, names[1]: b})
+    if b is not None and a.shape != b.shape:
+        raise ValueError(f"{names[0]} and {names[1]} must be of one length")
+
+
 class _On:
     """Makes a tensor's device the current one for a call, where it is not."""
 
@@ -175,6 +196,118 @@ def attn_prefix_fwd(q, k_pages, v_pages, prefix_table, prefix_lens, group_ptr, t
     return _attend("attn_prefix_fwd", q, pages, st, device, scale, q_ptr, max_q, out, lse, out_dtype, ws, stream, call, 1)
 
 
+def attn_cache_extend(table, seq_lens, refs, seqs, counts, page_size: int, stream=None):
+    """Adds counts[i] tokens to row seqs[i] of the cache: the lowest free pages
+    are taken for them, in the list's order, and the lengths grow."""
+    c = _cache(table, seq_lens, refs, page_size)
+    _lists(table.device, seqs, counts)
+    with _On(table.device):
+        B._check(B.load().attn_cache_extend(ctypes.byref(c), seqs.data_ptr(), counts.data_ptr(), seqs.shape[0],
+                                            B._stream_ptr(stream)), "attn_cache_extend")
+
+
+def attn_cache_free(table, seq_lens, refs, seqs, page_size: int, stream=None):
+    """Empties the listed rows; pages that nobody else holds become free."""
+    c = _cache(table, seq_lens, refs, page_size)
+    _lists(table.device, seqs)
+    with _On(table.device):
+        B._check(B.load().attn_cache_free(ctypes.byref(c), seqs.data_ptr(), seqs.shape[0], B._stream_ptr(stream)),
+                 "attn_cache_free")
+
+
+def attn_cache_trim(table, seq_lens, refs, page_size: int, window: int, sinks: int = 0, seqs=None, stream=None):
+    """Gives back the pages (of all rows, or the listed ones) that no token at
+    position seq_len - 1 or later sees through the window."""
+    c = _cache(table, seq_lens, refs, page_size)
+    if seqs is not None:
+        _lists(table.device, seqs)
+    with _On(table.device):
+        B._check(B.load().attn_cache_trim(ctypes.byref(c), None if seqs is None else seqs.data_ptr(),
+                                          c.n_slots if seqs is None else seqs.shape[0], int(window), int(sinks),
+                                          B._stream_ptr(stream)), "attn_cache_trim")
+
+
+def _copies(c, device, cap, n, stream):
+    import torch
+    nb = ctypes.c_size_t(0)
+    B._check(B.load().attn_cache_workspace_bytes(ctypes.byref(c), n, ctypes.byref(nb)), "attn_cache_workspace_bytes")
+    copies = torch.empty(1 + 2 * cap, dtype=torch.int32, device=device)
+    ws = torch.empty(nb.value, dtype=torch.uint8, device=device)
+    if stream is not None:
+        _borrowed(stream, copies, ws)
+    return copies, ws
+
+
+def attn_cache_fork(table, seq_lens, refs, src, dst, page_size: int, stream=None):
+    """Row dst[i] becomes what row src[i] was, for all i at once: full pages are
+    shared, partial ones copied.  Returns the copy list for
+    ``attn_cache_copy_pages``."""
+    c = _cache(table, seq_lens, refs, page_size)
+    _lists(table.device, src, dst, ("src", "dst"))
+    n = src.shape[0]
+    with _On(table.device):
+        copies, ws = _copies(c, table.device, n, n, stream)
+        B._check(B.load().attn_cache_fork(ctypes.byref(c), src.data_ptr(), dst.data_ptr(), n, copies.data_ptr(), n,
+                                          ws.data_ptr(), ws.numel(), B._stream_ptr(stream)), "attn_cache_fork")
+    return copies
+
+
+def attn_cache_compact(table, seq_lens, refs, page_size: int, stream=None):
+    """Moves the pages in use to the lowest indices.  Returns the copy list for
+    ``attn_cache_copy_pages``."""
+    c = _cache(table, seq_lens, refs, page_size)
+    cap = c.n_pages // 2
+    with _On(table.device):
+        copies, ws = _copies(c, table.device, cap, 0, stream)
+        B._check(B.load().attn_cache_compact(ctypes.byref(c), copies.data_ptr(), cap, ws.data_ptr(), ws.numel(),
+                                             B._stream_ptr(stream)), "attn_cache_compact")
+    return copies
+
+
+def attn_cache_copy_pages(pools, copies, stream=None):
+    """Copies whole pages inside every tensor of ``pools`` ([n_pages, ...],
+    each page contiguous, alike in size): page copies[1 + i] to page
+    copies[1 + cap + i] for i < copies[0], copies int32 [1 + 2 cap]."""
+    pools = list(pools)
+    if not pools:
+        return
+    x = pools[0]
+    n, page, stride = x.shape[0], x[0].numel() * x.element_size(), x.stride(0) * x.element_size()
+    for y in pools:
+        if not y.is_cuda or y.device != x.device or y.shape[0] != n or not y[0].is_contiguous() or \
+                y[0].numel() * y.element_size() != page or (n > 1 and y.stride(0) * y.element_size() != stride):
+            raise ValueError("pools must be tensors [n_pages, ...] on one CUDA device, alike in page size, each page contiguous")
+    _ints(x.device, copies=copies)
+    if copies.shape[0] % 2 != 1:
+        raise ValueError("copies must be int32 [1 + 2 cap]")
+    ptrs = (ctypes.c_void_p * len(pools))(*[y.data_ptr() for y in pools])
+    with _On(x.device):
+        B._check(B.load().attn_cache_copy_pages(ptrs, len(pools), page, max(stride, page) if n == 1 else stride, n,
+                                                copies.data_ptr(), copies.shape[0] // 2, B._stream_ptr(stream)),
+                 "attn_cache_copy_pages")
+
+
+def attn_cache_write(k_pages, v_pages, k_new, v_new, table, seq_lens, q_ptr=None, seqs=None, stream=None):
+    """Writes the newest tokens' keys and values ([n_tokens,H_k,d] bf16, d
+    contiguous) to the ends of their sequences (q_ptr, seqs as in
+    ``attn_paged_fwd``; seq_lens counts them already)."""
+    import torch
+    pages = _pages(k_pages, v_pages)
+    device = k_pages.device
+    st = _seqs(device, table, seq_lens, seqs)
+    _ints(device, q_ptr=q_ptr)
+    if q_ptr is not None and q_ptr.shape[0] != st.n_seqs + 1:
+        raise ValueError("q_ptr must have one entry a sequence and one more")
+    if k_new.dtype != torch.bfloat16 or v_new.dtype != torch.bfloat16 or k_new.device != device or v_new.device != device or \
+            k_new.dim() != 3 or k_new.shape[1:] != (pages.hk, pages.d) or k_new.shape != v_new.shape or \
+            k_new.stride() != v_new.stride() or k_new.stride(2) != 1:
+        raise ValueError("k_new and v_new must be bf16 [n_tokens, H_k, d] on the pages' device, alike in strides, d contiguous")
+    with _On(device):
+        B._check(B.load().attn_cache_write(ctypes.byref(pages), ctypes.byref(st), None if q_ptr is None else q_ptr.data_ptr(),
+                                           k_new.data_ptr(), v_new.data_ptr(), k_new.shape[0], k_new.stride(0), k_new.stride(1),
+                                           B._stream_ptr(stream)), "attn_cache_write")
+
+
 def attn_slices_from_windows(lengths: Sequence[int], window: int, sinks: int = 0) -> np.ndarray:
     """Windowed causal mask of packed sequences -> slice list (host), for
     ``attn_build_tiles``: a token sees its sequence's keys j <= i with
@@ -193,4 +326,13 @@ def _declare(lib):
     lib.attn_paged_workspace_bytes.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
     lib.attn_paged_fwd.argtypes = [vp, vp, i32, i32, i32, pages, seqs, f32, i32, i32, vp, i32, vp, vp, sz, vp]
     lib.attn_prefix_fwd.argtypes = [vp, vp, i32, i32, i32, pages, seqs, vp, seqs, f32, vp, i32, vp, vp, sz, vp]
+    cache = ctypes.POINTER(AttnCache)
+    lib.attn_cache_extend.argtypes = [cache, vp, vp, i32, vp]
+    lib.attn_cache_free.argtypes = [cache, vp, i32, vp]
+    lib.attn_cache_trim.argtypes = [cache, vp, i32, i32, i32, vp]
+    lib.attn_cache_workspace_bytes.argtypes = [cache, i32, ctypes.POINTER(sz)]
+    lib.attn_cache_fork.argtypes = [cache, vp, vp, i32, vp, i32, vp, sz, vp]
+    lib.attn_cache_compact.argtypes = [cache, vp, i32, vp, sz, vp]
+    lib.attn_cache_copy_pages.argtypes = [vp, i32, sz, sz, i32, vp, i32, vp]
+    lib.attn_cache_write.argtypes = [pages, seqs, vp, vp, vp, i32, ctypes.c_int64, ctypes.c_int64, vp]
     lib.attn_slices_from_windows.argtypes = [vp, i32, i32, i32, vp, i32, ctypes.POINTER(ctypes.c_int)]

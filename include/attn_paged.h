@@ -41,6 +41,8 @@ extern "C" {
 
 #define ATTN_PAGED_MAX_SEQS 4096     /* sequences (or groups) of one call      */
 #define ATTN_PAGED_MAX_LEN (1 << 30) /* max_pages * page_size                  */
+#define ATTN_CACHE_MAX_SLOTS 16384   /* rows of a cache's page table           */
+#define ATTN_CACHE_MAX_PAGES (1 << 30)
 #define ATTN_CACHE_MAX_POOLS 256     /* page arrays of one attn_cache_copy_pages */
 
 /* Keys and values in pages.  Strides are in elements, multiples of 8, alike
@@ -118,6 +120,93 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
  * more), CAPACITY. */
 int attn_slices_from_windows(const int32_t *h_lengths, int n, int window, int sinks,
                              attn_slice_t *h_out, int capacity, int *n_out);
+
+/* ---- pages of the cache --------------------------------------------------
+ * The page table and counts of one cache.  One table serves any number of
+ * page arrays (the keys and values of every layer).  Device pointers. */
+typedef struct {
+  int32_t *table;          /* [n_slots, max_pages], rows table_stride apart    */
+  int32_t *seq_lens;       /* [n_slots]                                        */
+  int32_t *refs;           /* [n_pages]                                        */
+  int64_t table_stride;
+  int32_t n_slots, max_pages, n_pages, page_size;
+} attn_cache_t;
+
+/* An empty cache has every table entry -1, every length and count 0; the
+ * caller makes it so once.  The lists below are int32 device arrays of n <=
+ * ATTN_PAGED_MAX_SEQS entries, read when the call runs.  A call whose list
+ * names a row out of range, or names twice a row that it changes, whose
+ * lengths are out of range (INVALID_ARG), or for which free pages, table
+ * columns or `cap` do not suffice (CAPACITY) changes nothing, sets copies[0]
+ * = 0, and leaves that code for attn_last_device_error().  Page indices out
+ * of range in the table are never followed (INVALID_ARG).  Fresh pages are
+ * the free ones of the lowest index, handed out in the list's order; pages
+ * that a call frees are not handed out by the same call.
+ * Host errors: INVALID_ARG; UNSUPPORTED (page size not a power of two of at
+ * least 16, the limits above, alignment); CAPACITY (ws_bytes); CUDA. */
+
+/* Adds counts[i] >= 0 tokens to row seqs[i]: pages are taken for them and the
+ * length grows; attn_cache_write fills them. */
+int attn_cache_extend(const attn_cache_t *cache, const int32_t *seqs, const int32_t *counts, int n,
+                      attn_stream_t stream);
+
+/* Empties the listed rows: their pages lose a holder each, their lengths
+ * become 0 and their entries -1. */
+int attn_cache_free(const attn_cache_t *cache, const int32_t *seqs, int n, attn_stream_t stream);
+
+/* Gives back, of the listed rows (null: every row, n = n_slots), the pages
+ * that a token at position seq_len - 1 or later never sees through a window
+ * >= 1 and first tokens `sinks`: their entries become -1.  Lengths and
+ * positions stay. */
+int attn_cache_trim(const attn_cache_t *cache, const int32_t *seqs, int n, int window, int sinks,
+                    attn_stream_t stream);
+
+/* Makes row dst[i] hold what row src[i] held before the call, for all i at
+ * once (a source may be named several times, and may itself be replaced; no
+ * dst twice); what the dst rows held before is freed.  Full pages are shared.
+ * A partial last page stays with its source, or with the source's first child
+ * of the list where the source is replaced; every other child gets a fresh
+ * page, and the pair enters the copy list:
+ *   copies [1 + 2 cap] int32: the count, then the pages to copy from, then at
+ *          1 + cap those to copy to; entries behind the count are -1.  n
+ *          copies at most.
+ *   d_ws   attn_cache_workspace_bytes(cache, n) bytes
+ * The pages' contents move with attn_cache_copy_pages, which has to run
+ * before anything is written to the rows. */
+int attn_cache_fork(const attn_cache_t *cache, const int32_t *src, const int32_t *dst, int n,
+                    int32_t *copies, int cap, void *d_ws, size_t ws_bytes, attn_stream_t stream);
+
+/* Moves the pages in use to the lowest indices: with u pages in use, those at
+ * u and above, in ascending order, go to the free ones below u, in ascending
+ * order.  The table, the counts and the copy list (n_pages / 2 copies at
+ * most) say so; attn_cache_copy_pages moves the contents.  Table entries
+ * behind a row's last page have to be -1 or are left alone. */
+int attn_cache_compact(const attn_cache_t *cache, int32_t *copies, int cap, void *d_ws,
+                       size_t ws_bytes, attn_stream_t stream);
+
+/* Workspace of attn_cache_fork with lists of n, and of attn_cache_compact. */
+int attn_cache_workspace_bytes(const attn_cache_t *cache, int n, size_t *bytes);
+
+/* Copies whole pages inside every listed array: copies as above (it may also
+ * be the caller's own).  h_pools: host array of n_pools device pointers, each
+ * to n_pages pages of page_bytes, page_stride_bytes apart (multiples of 16,
+ * 16-byte aligned).  Pairs with an index out of range are left out
+ * (INVALID_ARG on the device).  No page may be copied to twice, nor copied
+ * both to and from: its contents would be either's. */
+int attn_cache_copy_pages(void *const *h_pools, int n_pools, size_t page_bytes,
+                          size_t page_stride_bytes, int n_pages, const int32_t *copies, int cap,
+                          attn_stream_t stream);
+
+/* Writes new keys and values to the ends of their sequences: token t of
+ * sequence b (q_ptr and seqs as in attn_paged_fwd) goes to position
+ * seq_len - n + t.
+ *   k_new, v_new  [n_tokens, hk, d] bf16, 16-byte aligned, strides in elements
+ *                 and multiples of 8, d contiguous
+ * Tokens of no sequence are not read; a token whose slot, position or page is
+ * out of range is not written (INVALID_ARG on the device). */
+int attn_cache_write(const attn_pages_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr,
+                     const void *k_new, const void *v_new, int n_tokens, int64_t new_token_stride,
+                     int64_t new_head_stride, attn_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -22,6 +22,7 @@ printed on the pages (``tests/golden/``), invariants or brute force.
 """
 from .attention import (FULL, CAUSAL, INV_CAUSAL, BI_CAUSAL, mask_rows,
                         mask_rows_grid, oracle_attention, oracle_merge)
+from .cache import CacheOracle
 from .paged import oracle_paged
 from .tiles import (oracle_slices_from_grid, oracle_tiles, oracle_tiles_dense,
                     slice_row_interval)

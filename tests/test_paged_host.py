@@ -146,3 +146,75 @@ def test_binding_refuses_wrong_tensors():
         G.attn_paged_fwd(torch.zeros((1, 2, 64), dtype=torch.bfloat16), k, k, i[None], i, 1.0)      # not on a GPU
     with pytest.raises(ValueError):
         G.attn_paged_fwd(torch.zeros((1, 2, 64), dtype=torch.bfloat16), k, k[:, :, :1], i[None], i, 1.0)
+
+
+def _cache(**kw):
+    c = G.AttnCache(4096, 4096, 4096, 6, 5, 6, 40, 16)
+    for name, value in kw.items():
+        setattr(c, name, value)
+    return ctypes.byref(c)
+
+
+CACHE_BAD = [({"table": None}, INV), ({"seq_lens": None}, INV), ({"refs": None}, INV), ({"n_slots": 0}, INV), ({"max_pages": 0}, INV),
+             ({"n_pages": 0}, INV), ({"table_stride": 5}, INV), ({"page_size": 8}, UNS), ({"page_size": 24}, UNS), ({"n_slots": 16385}, UNS),
+             ({"max_pages": 1 << 27, "table_stride": 1 << 27}, UNS), ({"n_pages": (1 << 30) + 1}, UNS),
+             ({"n_slots": 16384, "max_pages": 1 << 20, "table_stride": 1 << 20}, UNS)]
+
+
+@pytest.mark.parametrize("change,code", CACHE_BAD, ids=[str(i) for i in range(len(CACHE_BAD))])
+def test_cache_refusals(lib, change, code):
+    n = ctypes.c_size_t(0)
+    c = _cache(**change)
+    assert lib.attn_cache_extend(c, X, X, 1, None) == code
+    assert lib.attn_cache_free(c, X, 1, None) == code
+    assert lib.attn_cache_trim(c, X, 1, 4, 0, None) == code
+    assert lib.attn_cache_fork(c, X, X, 1, X, 1, X, 1 << 40, None) == code
+    assert lib.attn_cache_compact(c, X, 1, X, 1 << 40, None) == code
+    assert lib.attn_cache_workspace_bytes(c, 1, ctypes.byref(n)) == code
+
+
+def test_cache_list_refusals(lib):
+    n = ctypes.c_size_t(0)
+    CAP = B.ATTN_ERR_CAPACITY
+    for count, code in ((-1, INV), (6, INV), (4097, UNS)):     # more rows than the table has: one would be named twice
+        assert lib.attn_cache_extend(_cache(), X, X, count, None) == code
+        assert lib.attn_cache_free(_cache(), X, count, None) == code
+        assert lib.attn_cache_trim(_cache(), X, count, 4, 0, None) == code
+        assert lib.attn_cache_fork(_cache(), X, X, count, X, 9, X, 1 << 40, None) == code
+    assert lib.attn_cache_extend(_cache(), None, X, 1, None) == INV
+    assert lib.attn_cache_extend(_cache(), X, None, 1, None) == INV
+    assert lib.attn_cache_free(_cache(), None, 1, None) == INV
+    assert lib.attn_cache_trim(_cache(), None, 4, 4, 0, None) == INV       # every row, or a list
+    assert lib.attn_cache_trim(_cache(), X, 4, 0, 0, None) == INV
+    assert lib.attn_cache_trim(_cache(), X, 4, 4, -1, None) == INV
+    assert lib.attn_cache_fork(_cache(), X, X, 2, None, 2, X, 1 << 40, None) == INV
+    assert lib.attn_cache_fork(_cache(), X, X, 2, X, -1, X, 1 << 40, None) == INV
+    assert lib.attn_cache_fork(_cache(), X, X, 2, X, 2, None, 1 << 40, None) == INV
+    assert lib.attn_cache_fork(_cache(), X, X, 2, X, 2, ctypes.c_void_p(4097), 1 << 40, None) == UNS
+    assert lib.attn_cache_workspace_bytes(_cache(), 2, ctypes.byref(n)) == B.ATTN_OK
+    assert lib.attn_cache_fork(_cache(), X, X, 2, X, 2, X, 4 * 2 * 7 - 1, None) == CAP and n.value >= 4 * 2 * 7
+    assert lib.attn_cache_compact(_cache(), None, 1, X, 1 << 40, None) == INV
+    assert lib.attn_cache_compact(_cache(), X, 1, None, 1 << 40, None) == INV
+    assert lib.attn_cache_compact(_cache(), X, 1, X, 4 * 40 - 1, None) == CAP and n.value >= 4 * 40
+    assert lib.attn_cache_workspace_bytes(_cache(), -1, ctypes.byref(n)) == INV
+    assert lib.attn_cache_extend(_cache(), X, X, 0, None) == B.ATTN_OK
+    assert lib.attn_cache_free(_cache(), X, 0, None) == B.ATTN_OK
+
+
+def test_copy_and_write_refusals(lib):
+    pools = (ctypes.c_void_p * 2)(4096, 8192)
+    copy = lambda p=pools, n=2, size=64, stride=64, pages=4, c=X, cap=3: lib.attn_cache_copy_pages(p, n, size, stride, pages, c, cap, None)  # noqa: E731
+    assert copy(n=0) == B.ATTN_OK and copy(cap=0) == B.ATTN_OK
+    for bad in ({"p": None}, {"n": -1}, {"size": 0}, {"stride": 48}, {"pages": 0}, {"c": None}, {"cap": -1}, {"p": (ctypes.c_void_p * 2)(4096, None)}):
+        assert copy(**bad) == INV
+    for bad in ({"n": 257}, {"size": 60}, {"stride": 72}, {"size": 1 << 31, "stride": 1 << 31}, {"p": (ctypes.c_void_p * 2)(4096, 4104)}):
+        assert copy(**bad) == UNS
+
+    def write(k=X, v=X, q_ptr=X, n=5, ts=256, hs=128, **kw):
+        a = _args(**kw)
+        return lib.attn_cache_write(ctypes.byref(a["pages"]), ctypes.byref(a["seqs"]), q_ptr, k, v, n, ts, hs, None)
+    assert write(n=0) == B.ATTN_OK
+    for bad in ({"k": None}, {"v": None}, {"q_ptr": None}, {"n": -1}, {"pages__hk": 0}, {"seqs__table": None}):
+        assert write(**bad) == INV
+    for bad in ({"k": ctypes.c_void_p(4104)}, {"ts": 100}, {"hs": 12}, {"ts": -256}, {"pages__page_size": 20}):
+        assert write(**bad) == UNS

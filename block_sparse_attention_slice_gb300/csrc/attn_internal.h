@@ -72,13 +72,15 @@ int merge_launch(const void *const *o_parts, const float *const *lse_parts, int 
                  int part_dtype, int s_len, int h, int d, void *out, int out_dtype, float *lse,
                  cudaStream_t s);
 
-// Attention over a paged cache (paged_api.cu, paged_rows.cu) and its pages
+// Attention over a paged cache (paged_api.cu, paged_rows.cu, paged_tiles.cu) and its pages
 // (cache_pages.cu).
 int paged_check_pages(const attn_pages_t *g, int *shift);
 int paged_check_seqs(const attn_seqs_t *s, int page_size);
 struct PagedParams;
 size_t paged_rows_workspace(int d);
 int paged_rows_launch(PagedParams p, int d, cudaStream_t s);
+size_t paged_tiles_workspace(int d);
+int paged_tiles_launch(const PagedParams &p, int d, int tokens, cudaStream_t s);
 // Reads and clears the first failure status of the paged and cache kernels on
 // the current device; its device address for their launches (null on failure).
 int paged_status_take(unsigned int *status);

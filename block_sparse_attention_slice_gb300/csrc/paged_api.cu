@@ -119,6 +119,16 @@ PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, co
   return p;
 }
 
+// Items of up to 16 rows (query heads of one key/value head times tokens) go to
+// the warp-level kernel, larger ones to the tensor-core tiles.
+int paged_launch(const PagedParams &p, int d, int tokens, cudaStream_t s) {
+  if (static_cast<int64_t>(tokens) * p.G > 16) {
+    const int rc = paged_tiles_launch(p, d, tokens, s);
+    if (rc != ATTN_ERR_UNSUPPORTED) return rc;
+  }
+  return paged_rows_launch(p, d, s);
+}
+
 // O and lse of the prefix pass, in 32 bits, ahead of the pieces
 size_t prefix_bytes(int n_tokens, int hq, int d) {
   return up256(static_cast<size_t>(n_tokens) * hq * d * 4) + up256(static_cast<size_t>(n_tokens) * hq * 4);
@@ -134,7 +144,7 @@ extern "C" {
 int attn_paged_workspace_bytes(int n_tokens, int hq, int d, int prefix, size_t *bytes) {
   if (!bytes || n_tokens < 0 || hq < 1) return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
-  const size_t w = paged_rows_workspace(d);
+  const size_t w = std::max(paged_rows_workspace(d), paged_tiles_workspace(d));
   if (w == 0) return ATTN_ERR_CUDA;
   *bytes = w + (prefix ? prefix_bytes(n_tokens, hq, d) : 0);
   return ATTN_OK;
@@ -163,7 +173,7 @@ int attn_paged_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q,
   p.part_o = static_cast<float *>(d_ws);
   p.status = paged_status();
   if (!p.status) return ATTN_ERR_CUDA;
-  return paged_rows_launch(p, pages->d, reinterpret_cast<cudaStream_t>(stream));
+  return paged_launch(p, pages->d, std::min(max_q, n_tokens), reinterpret_cast<cudaStream_t>(stream));
 }
 
 int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
@@ -199,7 +209,7 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
   p.part_o = pieces;
   p.status = status;
   const bool any = prefix->n_seqs > 0;
-  if (any && (rc = paged_rows_launch(p, pages->d, s)) != ATTN_OK) return rc;
+  if (any && (rc = paged_launch(p, pages->d, (n_tokens + prefix->n_seqs - 1) / prefix->n_seqs, s)) != ATTN_OK) return rc;
   // what follows it, each row starting from its prefix's summary
   PagedParams r = params(q, q_ptr, n_tokens, hq, pages, seqs, scale, shift);
   r.out = out;
@@ -209,7 +219,7 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
   r.init_lse = any ? plse : nullptr;
   r.part_o = pieces;
   r.status = status;
-  return paged_rows_launch(r, pages->d, s);
+  return paged_launch(r, pages->d, std::min(max_q, n_tokens), s);
 }
 
 int attn_slices_from_windows(const int32_t *h_lengths, int n, int window, int sinks, attn_slice_t *h_out,

@@ -148,16 +148,36 @@ __device__ inline long long head_tiles(const PagedParams &p, const SeqInfo &s, i
 
 // The flat list's prefix sums, first[b] = key tiles before sequence b, for
 // every thread of a CTA of NT threads; first has n_seqs + 1 entries in shared
-// memory, info n_seqs.  `scan` holds NT / 32 + 1 values.
+// memory, info (null: sequences are read again where needed) n_seqs.  `scan`
+// holds NT / 32 + 1 values.  Few sequences: a warp each, its lanes share the
+// row tiles; else a thread takes one or several.
 template <int ROWS, int KL, int NT>
 __device__ inline void make_plan(const PagedParams &p, int tpi, long long *first, SeqInfo *info,
                                  long long *scan) {
   const int per = (p.n_seqs + NT - 1) / NT, b0 = min(p.n_seqs, static_cast<int>(threadIdx.x) * per),
             b1 = min(p.n_seqs, b0 + per), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool by_warp = p.n_seqs <= NT / 32;
+  if (by_warp && warp < p.n_seqs) {
+    const SeqInfo s = seq_info(p, warp);
+    const int R = tile_count<ROWS>(s.nq, p.G, tpi);
+    long long n = 0;
+    for (int rt = lane; rt < R; rt += 32) n += tile_span<ROWS, KL>(p, s, rt, tpi).n;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0) {
+      if (info) info[warp] = s;
+      first[warp + 1] = n * p.hk;
+    }
+  }
+  if (by_warp) __syncthreads();
   long long sum = 0;
   for (int b = b0; b < b1; ++b) {
+    if (by_warp) {
+      sum += first[b + 1];
+      continue;
+    }
     const SeqInfo s = seq_info(p, b);
-    info[b] = s;
+    if (info) info[b] = s;
     const long long n = head_tiles<ROWS, KL>(p, s, tpi) * p.hk;
     first[b + 1] = n;
     sum += n;
@@ -192,7 +212,7 @@ struct Walk {
   SeqInfo s;
   Span sp;
   __device__ __forceinline__ void load(const PagedParams &p, const SeqInfo *info, int tpi) {
-    s = info[b];
+    s = info ? info[b] : seq_info(p, b);
     R = tile_count<ROWS>(s.nq, p.G, tpi);
   }
   // flat < first[n_seqs]
@@ -277,6 +297,37 @@ __device__ __forceinline__ void store_pair(const PagedParams &p, long long row, 
     *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + at) = pack_bf16x2(x, y);
 }
 
+// Writes columns c .. c + 31 of a finished row, as one thread holds them.
+template <int D>
+__device__ __forceinline__ void store_32(const PagedParams &p, long long row, int c, const uint32_t (&y)[32], float fo,
+                                         float fi) {
+  const long long at = row * D + c;
+  float x[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(y[k]) * fo;
+  if (fi != 0.f) {
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      const float4 i = *reinterpret_cast<const float4 *>(p.init_o + at + k);
+      x[k] += fi * i.x;
+      x[k + 1] += fi * i.y;
+      x[k + 2] += fi * i.z;
+      x[k + 3] += fi * i.w;
+    }
+  }
+  if (p.out_f32) {
+#pragma unroll
+    for (int k = 0; k < 32; k += 4)
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 32; k += 8)
+      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at + k) =
+          make_uint4(pack_bf16x2(x[k], x[k + 1]), pack_bf16x2(x[k + 2], x[k + 3]), pack_bf16x2(x[k + 4], x[k + 5]),
+                     pack_bf16x2(x[k + 6], x[k + 7]));
+  }
+}
+
 // Rows of items without a key tile: their sequences see nothing (here).
 template <int D, int ROWS, int KL>
 __device__ inline void finish_empty(const PagedParams &p, const SeqInfo *info, int tpi) {
@@ -292,7 +343,7 @@ __device__ inline void finish_empty(const PagedParams &p, const SeqInfo *info, i
         p.lse[static_cast<long long>(h) * p.n_tokens + (t < t0 ? t : t + t1 - t0)] = -INFINITY;
   }
   for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x) {
-    const SeqInfo s = info[b];
+    const SeqInfo s = info ? info[b] : seq_info(p, b);
     // causal rows see more keys the later they stand: the empty tiles come first
     for (int rt = 0; rt < tile_count<ROWS>(s.nq, p.G, tpi); ++rt) {
       int a, z;

@@ -1,0 +1,606 @@
+// Attention over a paged cache for many rows per key/value head: prompts taken
+// in pieces, tokens verified together, and a shared prefix against all the
+// rows of its group.  tcgen05 matrix instructions with tensor-memory
+// accumulators, pages fetched by TMA.
+//
+// A row tile is 128 rows of tensor memory: TPT = 128 / G whole tokens with the
+// G query heads of one key/value head (one 3-D TMA box of the query tensor
+// packs them).  TILES = 2: an item is two row tiles that share every key tile,
+// and the tensor core works on one while the softmax warps of the other run
+// (the order of attn_fwd: PV_0(j), QK_0(j+1), PV_1(j), QK_1(j+1)).  TILES = 1,
+// for items of at most TPT tokens: one row tile with two score buffers, QK(j+1)
+// issued before softmax(j) ends.  Bound by the tensor core when an item's rows
+// fill its tiles, by the cache's bandwidth when they do not.
+//
+// One persistent CTA per SM takes an equal span of the flat list of 128-key
+// tiles (paged_plan.cuh); pieces of items that cross spans are joined by
+// paged_join_kernel.  Warps: 4 softmax warps a row tile (thread = row = tensor
+// memory lane), a producer warp (walks the list, publishes each segment to the
+// others, fetches Q, K and V; one lane per page of a tile) and a warp that
+// issues the matrix instructions.
+//
+// What lies behind a sequence's end must not meet the zero weights of the P V
+// product: pages behind it, and pages that no row of the item sees, are
+// fetched from outside the tensor map, which reads as zeros, and the rows
+// behind the end in the last page are zeroed in shared memory by the issuing
+// warp before their product.
+//
+// Numerics as in paged_rows.cu: 32-bit scores, maxima, sums and O; P rounded
+// to bf16 (half a step, 2^-9 of each weight either way) as the operand that the
+// tensor core takes.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "attn_internal.h"
+#include "paged_join.cuh"
+#include "paged_plan.cuh"
+
+namespace attn {
+
+constexpr int PT_KL = 7, PT_BN = 128, PT_IQ = 4;
+constexpr float PT_TAU = 8.0f;
+
+template <int D, int TILES>
+struct TileLayout {
+  static constexpr int NS = TILES == 2 ? 4 : 5;         // K/V ring slots
+  static constexpr int HALF = 128 * 64 * 2, NHALF = D / 64, TILE = NHALF * HALF;
+  static constexpr int Q_OFF = 0, KV_OFF = TILES * TILE, SEG_OFF = KV_OFF + NS * TILE;
+  static constexpr int BAR_OFF = SEG_OFF + PT_IQ * 64;
+  static constexpr int B_Q = 0, B_QE = 1, B_FULL = 2, B_EMPTY = B_FULL + NS, B_S = B_EMPTY + NS, B_P = B_S + 2,
+                       B_O = B_P + 2, B_IF = B_O + TILES, B_IE = B_IF + PT_IQ, B_DRAIN = B_IE + PT_IQ,
+                       B_V = B_DRAIN + 1, NBAR = B_V + 1;
+  static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+  static constexpr int SCAN_OFF = MISC_OFF + 16;
+  static constexpr int FIRST_OFF = SCAN_OFF + 16 * 8;
+  static constexpr int THREADS = TILES * 128 + 64;
+  static size_t bytes(int n_seqs) { return 1024 + FIRST_OFF + 8ull * (n_seqs + 1); }
+  static_assert(MISC_OFF % 8 == 0, "alignment");
+};
+
+// What the producer publishes of a segment: a run of key tiles of one item.
+struct Seg {
+  int tok0, ntok, h, pos0, len, ns, w0, i0, i1, out;    // out: 0 finished here, 1 / 2 piece slot + 1, -1 no more
+};
+static_assert(sizeof(Seg) <= 64, "segment record");
+
+template <int D, int TILES>
+__global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
+    paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int tpt) {
+  using L = TileLayout<D, TILES>;
+  constexpr int NS = L::NS;
+  extern __shared__ uint8_t tiles_smem[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(tiles_smem) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_u32(smem);
+  auto bar = [&](int i) -> uint32_t { return sb + L::BAR_OFF + 8u * i; };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC_OFF);
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + L::MISC_OFF + 4);
+  volatile Seg *segs = reinterpret_cast<volatile Seg *>(smem + L::SEG_OFF);   // 64 bytes apart
+  auto seg_at = [&](int s) -> volatile Seg * {
+    return reinterpret_cast<volatile Seg *>(reinterpret_cast<volatile uint8_t *>(segs) + 64 * s);
+  };
+  long long *scan = reinterpret_cast<long long *>(smem + L::SCAN_OFF);
+  long long *first = reinterpret_cast<long long *>(smem + L::FIRST_OFF);
+  const uint32_t q_smem = sb + L::Q_OFF, kv_smem = sb + L::KV_OFF;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tpi = tpt * TILES;
+  const uint64_t lim = p.wait_ns;
+  constexpr int WP = TILES * 4, WM = TILES * 4 + 1;       // producer, issuer
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    mbar_init(bar(L::B_Q), 1);
+    mbar_init(bar(L::B_QE), 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(bar(L::B_FULL + s), 1);
+      mbar_init(bar(L::B_EMPTY + s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(L::B_S + t), 1);
+      mbar_init(bar(L::B_P + t), 128);
+    }
+    for (int t = 0; t < TILES; ++t) mbar_init(bar(L::B_O + t), 1);
+    for (int u = 0; u < PT_IQ; ++u) {
+      mbar_init(bar(L::B_IF + u), 1);
+      mbar_init(bar(L::B_IE + u), TILES * 4 + 1);
+    }
+    mbar_init(bar(L::B_DRAIN), 1);
+    mbar_init(bar(L::B_V), 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == WM) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == WP && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  make_plan<0, PT_KL, L::THREADS>(p, tpi, first, static_cast<SeqInfo *>(nullptr), scan);
+  finish_empty<D, 0, PT_KL>(p, nullptr, tpi);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const long long total = first[p.n_seqs], span = span_of(p, total);
+  const long long from = blockIdx.x * span, to = min(total, from + span);
+
+  if (warp == WP) {
+    // -------------------------------------------------------------- producer
+    uint32_t ld = 0, nseg = 0;
+    bool ok = true;
+    long long at = from;
+    Walk<0, PT_KL> w;
+    if (at < to) w.seek(p, first, nullptr, tpi, at);
+    const int R = min(1 << p.page_shift, 128), ppt = 128 / R, page_mask = (1 << p.page_shift) - 1;
+    while (ok) {
+      const int qs = nseg % PT_IQ;
+      if (nseg >= PT_IQ && !wait_all(bar(L::B_IE + qs), (nseg / PT_IQ - 1) & 1, abort, lim)) break;
+      const bool more = at < to;
+      int i1 = 0;
+      if (more) i1 = static_cast<int>(min(static_cast<long long>(w.sp.n), w.i + (to - at)));
+      if (lane == 0) {
+        volatile Seg *s = seg_at(qs);
+        if (more) {
+          s->tok0 = w.s.q0 + w.rt * tpi;
+          s->ntok = min(tpi, w.s.nq - w.rt * tpi);
+          s->h = w.h;
+          s->pos0 = w.s.len - w.s.nq + w.rt * tpi;
+          s->len = w.s.len;
+          s->ns = w.sp.ns;
+          s->w0 = w.sp.w0;
+          s->i0 = w.i;
+          s->i1 = i1;
+          s->out = w.i == 0 && i1 == w.sp.n ? 0 : at == from ? 1 : 2;
+        } else {
+          s->out = -1;
+        }
+        mbar_arrive(bar(L::B_IF + qs));
+      }
+      __syncwarp();
+      if (!more) break;
+      // Q of the segment's tokens
+      if (nseg > 0 && !wait_all(bar(L::B_QE), (nseg - 1) & 1, abort, lim)) break;
+      const int tok0 = w.s.q0 + w.rt * tpi;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(L::B_Q), TILES * L::NHALF * tpt * p.G * 128);
+        for (int t = 0; t < TILES; ++t)
+          for (int hh = 0; hh < L::NHALF; ++hh)
+            tma_load_3d(q_smem + t * L::TILE + hh * L::HALF, &tm_q, bar(L::B_Q), hh * 64, w.h * p.G, tok0 + t * tpt);
+      }
+      ++nseg;
+      // keys that some row sees: below `end`, at least `lo` or a first token
+      const int tl = min(tpi, w.s.nq - w.rt * tpi) - 1, pos0 = w.s.len - w.s.nq + w.rt * tpi;
+      const int end = p.causal ? pos0 + tl + 1 : w.s.len, lo = p.causal && p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
+      const long long row = w.s.slot * p.table_stride;
+      auto page_of = [&](int i, int &tok) -> int {      // this lane's page of key tile i; n_pages: zeros
+        const int k0 = (w.sp.tile(i) << PT_KL) + lane * R;
+        tok = k0 & page_mask;
+        const bool seen = lane < ppt && k0 < end && (k0 + R > lo || k0 < p.sinks);
+        if (!seen) return p.n_pages;
+        const int e = __ldg(p.table + row + (k0 >> p.page_shift));
+        if (e < 0 || e >= p.n_pages) {
+          paged_fail(p, ATTN_ERR_INVALID_ARG);
+          return p.n_pages;
+        }
+        return e;
+      };
+      int tok, tok_next = 0, page, page_next = page_of(w.i, tok_next);
+      for (int i = w.i; i < i1 && ok; ++i) {
+        page = page_next;
+        tok = tok_next;
+        if (i + 1 < i1) page_next = page_of(i + 1, tok_next);
+        for (int kv = 0; kv < 2; ++kv, ++ld) {
+          const int slot = ld % NS;
+          if (ld >= NS && !wait_all(bar(L::B_EMPTY + slot), (ld / NS - 1) & 1, abort, lim)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(L::B_FULL + slot), L::TILE);
+          __syncwarp();
+          if (lane < ppt)
+            for (int hh = 0; hh < L::NHALF; ++hh)
+              tma_load_4d(kv_smem + slot * L::TILE + hh * L::HALF + lane * R * 128, kv ? &tm_v : &tm_k,
+                          bar(L::B_FULL + slot), hh * 64, tok, w.h, page);
+        }
+      }
+      if (!ok) break;
+      at += i1 - w.i;
+      w.i = i1 - 1;
+      if (at < to) w.next(p, first, nullptr, tpi);
+    }
+    if (*abort && lane == 0) {
+      // let the loads in flight land before the CTA retires
+      if (nseg > 0) wait_drain(bar(L::B_Q), (nseg - 1) & 1, 20000000ull);
+      for (uint32_t i = ld > NS ? ld - NS : 0; i < ld; ++i) wait_drain(bar(L::B_FULL + i % NS), (i / NS) & 1, 20000000ull);
+    }
+    __syncwarp();
+  } else if (warp == WM) {
+    // ---------------------------------------------------------------- issuer
+    constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, PT_BN, 0), IDESC_PV = idesc_bf16_f32(128, D, 1);
+    auto issue_qk = [=](int t, int sbuf, int slot) {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * L::HALF + (kk & 3) * 32;
+        mma_ss(tmem + sbuf * 128, smem_desc_sw128(q_smem + t * L::TILE + off, 16, 1024),
+               smem_desc_sw128(kv_smem + slot * L::TILE + off, 16, 1024), IDESC_QK, kk > 0);
+      }
+    };
+    auto issue_pv = [=](int t, int sbuf, int slot, bool start) {
+#pragma unroll
+      for (int kk = 0; kk < PT_BN / 16; ++kk)
+        mma_ts(tmem + 256 + t * 128, tmem + sbuf * 128 + kk * 8,
+               smem_desc_sw128(kv_smem + slot * L::TILE + kk * 16 * 128, L::HALF, 1024), IDESC_PV, (start && kk == 0) ? 0u : 1u);
+    };
+    // rows behind the sequence's end of the V tile in `slot`
+    auto clear_tail = [&](int slot, int c0, int len) {
+      const int valid = len - c0;
+      if (valid >= 128) return;
+      for (int hh = 0; hh < L::NHALF; ++hh)
+        for (int x = valid * 128 + lane * 16; x < 128 * 128; x += 512)
+          st_shared_v4(kv_smem + slot * L::TILE + hh * L::HALF + x, make_uint4(0u, 0u, 0u, 0u));
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    uint32_t ld = 0, step = 0, nseg = 0;      // ring position of the segment's next K; key tiles done
+    bool ok = true;
+    auto full = [&](uint32_t pos) { return wait_all(bar(L::B_FULL + pos % NS), (pos / NS) & 1, abort, lim); };
+    while (ok) {
+      const int qs = nseg % PT_IQ;
+      if (!wait_all(bar(L::B_IF + qs), (nseg / PT_IQ) & 1, abort, lim)) break;
+      volatile Seg *s = seg_at(qs);
+      const int out = s->out, len = s->len, ns = s->ns, w0 = s->w0, i0 = s->i0, n = s->i1 - i0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::B_IE + qs));
+      if (out < 0) break;
+      auto c0_of = [&](int j) { return (i0 + j < ns ? i0 + j : i0 + j - ns + w0) << PT_KL; };
+      if (!wait_all(bar(L::B_Q), nseg & 1, abort, lim) || !full(ld)) break;
+      ++nseg;
+      tc_fence_after();
+      if constexpr (TILES == 1) {
+        if (lane == 0) {
+          issue_qk(0, step & 1, ld % NS);
+          mma_commit(bar(L::B_S + (step & 1)));
+          mma_commit(bar(L::B_EMPTY + ld % NS));
+          if (n == 1) mma_commit(bar(L::B_QE));
+        }
+        __syncwarp();
+        for (int j = 0; j < n; ++j, ++step) {
+          const uint32_t v = ld + 2 * j + 1, k = v + 1;
+          if (j + 1 < n) {
+            if (!full(k)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (lane == 0) {
+              issue_qk(0, (step + 1) & 1, k % NS);
+              mma_commit(bar(L::B_S + ((step + 1) & 1)));
+              mma_commit(bar(L::B_EMPTY + k % NS));
+              if (j + 2 == n) mma_commit(bar(L::B_QE));
+            }
+            __syncwarp();
+          }
+          if (!full(v)) {
+            ok = false;
+            break;
+          }
+          clear_tail(v % NS, c0_of(j), len);
+          if (!wait_all(bar(L::B_P + (step & 1)), (step >> 1) & 1, abort, lim)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            issue_pv(0, step & 1, v % NS, j == 0);
+            mma_commit(bar(L::B_EMPTY + v % NS));
+            mma_commit(bar(L::B_V));
+            if (j + 1 == n) mma_commit(bar(L::B_O));
+          }
+          __syncwarp();
+        }
+      } else {
+        if (lane == 0) {
+          issue_qk(0, 0, ld % NS);
+          mma_commit(bar(L::B_S + 0));
+          issue_qk(1, 1, ld % NS);
+          mma_commit(bar(L::B_S + 1));
+          mma_commit(bar(L::B_EMPTY + ld % NS));
+          if (n == 1) mma_commit(bar(L::B_QE));
+        }
+        __syncwarp();
+        for (int j = 0; j < n; ++j, ++step) {
+          const uint32_t v = ld + 2 * j + 1, k = v + 1;
+          const bool more = j + 1 < n;
+          if (!full(v)) {
+            ok = false;
+            break;
+          }
+          clear_tail(v % NS, c0_of(j), len);
+          if (!wait_all(bar(L::B_P + 0), step & 1, abort, lim)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            issue_pv(0, 0, v % NS, j == 0);
+            if (!more) mma_commit(bar(L::B_O + 0));
+          }
+          __syncwarp();
+          if (more) {
+            if (!full(k)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (lane == 0) {
+              issue_qk(0, 0, k % NS);
+              mma_commit(bar(L::B_S + 0));
+            }
+            __syncwarp();
+          }
+          if (!wait_all(bar(L::B_P + 1), step & 1, abort, lim)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            issue_pv(1, 1, v % NS, j == 0);
+            mma_commit(bar(L::B_EMPTY + v % NS));
+            if (!more) {
+              mma_commit(bar(L::B_O + 1));
+            } else {
+              issue_qk(1, 1, k % NS);
+              mma_commit(bar(L::B_S + 1));
+              mma_commit(bar(L::B_EMPTY + k % NS));
+              if (j + 2 == n) mma_commit(bar(L::B_QE));
+            }
+          }
+          __syncwarp();
+        }
+      }
+      ld += 2 * n;
+    }
+    // all matrix instructions are done before tensor memory is freed
+    if (lane == 0) {
+      mma_commit(bar(L::B_DRAIN));
+      wait_drain(bar(L::B_DRAIN), 0, 20000000ull);
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------------- softmax
+    const int t = TILES == 1 ? 0 : warp >> 2, wl = warp & 3, r = wl * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(wl * 32) << 16;
+    const uint32_t tO = tmem + lane_off + 256 + t * 128;
+    const float sl2 = p.scale_log2;
+    const int tl = r / p.G, g = r - tl * p.G;               // token and head of this row in its tile
+    uint32_t step = 0, nseg = 0;
+    bool ok = true;
+    while (ok) {
+      const int qs = nseg % PT_IQ;
+      if (!wait_all(bar(L::B_IF + qs), (nseg / PT_IQ) & 1, abort, lim)) break;
+      volatile Seg *s = seg_at(qs);
+      const int out = s->out, tok0 = s->tok0 + t * tpt, ntok = min(tpt, s->ntok - t * tpt), h = s->h, pos0 = s->pos0 + t * tpt,
+                len = s->len, ns = s->ns, w0 = s->w0, i0 = s->i0, i1 = s->i1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::B_IE + qs));
+      if (out < 0) break;
+      const bool live = tl < ntok, idle = wl * 32 >= ntok * p.G;    // idle: none of the warp's rows is live
+      const int hi = p.causal ? pos0 + tl + 1 : len;               // this row sees keys [lo, hi) and the first ones
+      const int lo = p.causal && p.window > 0 ? hi - p.window : 0;
+      const int all_hi = p.causal ? pos0 + 1 : len, all_lo = p.causal && p.window > 0 ? pos0 + ntok - p.window : 0;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int i = i0; i < i1; ++i, ++step) {
+        const int u = TILES == 1 ? step & 1 : t;
+        const uint32_t ph = TILES == 1 ? (step >> 1) & 1 : step & 1;
+        const uint32_t tS = tmem + lane_off + u * 128;
+        const int c0 = (i < ns ? i : i - ns + w0) << PT_KL;
+        const bool masked = c0 + 128 > all_hi || (c0 < all_lo && c0 + 128 > p.sinks);
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (masked) {
+          or_span(max(lo, 0), hi, c0, w);
+          if (lo > 0) or_span(0, min(p.sinks, hi), c0, w);
+        }
+        if (!wait_all(bar(L::B_S + u), ph, abort, lim)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (!idle) {
+          float x[PT_BN];
+          {
+            uint32_t y[PT_BN];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&y[c * 32]));
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < PT_BN; ++k) {
+              asm volatile("" : "+r"(y[k]));
+              x[k] = __uint_as_float(y[k]);
+            }
+          }
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < PT_BN; ++k)
+              if (!((w[k >> 5] >> (k & 31)) & 1u)) x[k] = -INFINITY;
+          }
+          float m4[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) m4[v] = fmaxf(x[2 * v], x[2 * v + 1]);
+#pragma unroll
+          for (int k = 8; k < PT_BN; k += 8) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) m4[v] = max3f(m4[v], x[k + 2 * v], x[k + 2 * v + 1]);
+          }
+          const float mx = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
+          const float m_old = m_ref;
+          const bool grow = mx > m_ref + PT_TAU;
+          if (grow) m_ref = mx;
+          const float factor = grow ? ex2_approx(m_old - m_ref) : 1.f;
+          l *= factor;
+          const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+          const uint64_t sc2 = f2_make(sl2, sl2), nb2 = f2_make(-mb, -mb);
+          uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float a0, a1;
+              f2_split(f2_fma(f2_make(x[c * 32 + 2 * k], x[c * 32 + 2 * k + 1]), sc2, nb2), a0, a1);
+              a0 = ex2_approx(a0);
+              a1 = ex2_approx(a1);
+              l2[k & 3] = f2_add(l2[k & 3], f2_make(a0, a1));
+              pk[k] = pack_bf16x2(a0, a1);
+            }
+            tmem_st16(tS + c * 16, pk);
+          }
+          float a0, a1;
+          f2_split(f2_add(f2_add(l2[0], l2[1]), f2_add(l2[2], l2[3])), a0, a1);
+          l += a0 + a1;
+          const bool rescale = grow && m_old != -INFINITY && i > i0;
+          if (__any_sync(0xffffffffu, rescale)) {
+            // PV(i-1) has to be done before O is rescaled: with one row tile
+            // S(i) does not say so, its QK was issued before that product
+            if (TILES == 1 && !wait_all(bar(L::B_V), (step - 1) & 1, abort, lim)) {
+              ok = false;
+              break;
+            }
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t y[32];
+              tmem_ld32_wait(tO + c * 32, y);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * factor);
+              tmem_st32(tO + c * 32, y);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(bar(L::B_P + u));
+      }
+      if (!ok) break;
+      if (!wait_all(bar(L::B_O + t), nseg & 1, abort, lim)) break;
+      ++nseg;
+      tc_fence_after();
+      if (!idle) {
+        const long long row = static_cast<long long>(tok0 + tl) * p.hq + h * p.G + g;
+        if (out == 0) {
+          const long long li = static_cast<long long>(h * p.G + g) * p.n_tokens + tok0 + tl;
+          float fo = 0.f, fi = 0.f, lse = 0.f;
+          if (live) {
+            row_final(m_ref, l, p.init_lse ? p.init_lse[li] : -INFINITY, fo, fi, lse);
+            p.lse[li] = lse;
+          }
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t y[32];
+            tmem_ld32_wait(tO + c * 32, y);
+            if (live) store_32<D>(p, row, c * 32, y, fo, fi);
+          }
+        } else {
+          const long long pr = (static_cast<long long>(blockIdx.x) * 2 + out - 1) * (TILES * 128) + t * 128 + r;
+          if (live) *reinterpret_cast<float2 *>(p.part_ml + pr * 2) = make_float2(m_ref, l);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t y[32];
+            tmem_ld32_wait(tO + c * 32, y);
+            if (!live) continue;
+            uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + pr * D + c * 32);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+          }
+        }
+      }
+      tc_fence_before();      // O is read before the next segment's first product
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == WM) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && *abort) paged_fail(p, ATTN_ERR_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------- host
+
+namespace {
+
+int encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+  auto enc = tma_encode_fn();
+  if (!enc) return ATTN_ERR_CUDA;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? ATTN_OK
+             : ATTN_ERR_UNSUPPORTED;
+}
+
+template <int D, int TILES>
+int launch_tiles(PagedParams p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
+  using L = TileLayout<D, TILES>;
+  constexpr int kDev = 64;
+  static bool done[kDev] = {}, joined[kDev] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDev) return ATTN_ERR_CUDA;
+  auto kern = paged_tiles_kernel<D, TILES>;
+  auto join = paged_join_kernel<D, 0, PT_KL, TILES * 128>;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (raise_smem(kern, kSmemMax, &done[dev]) != ATTN_OK || raise_smem(join, kSmemMax, &joined[dev]) != ATTN_OK)
+      return ATTN_ERR_CUDA;
+  }
+  const int sms = device_sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  p.n_workers = sms;
+  p.min_span = 2;
+  p.part_ml = p.part_o + static_cast<size_t>(sms) * 2 * TILES * 128 * D;
+  const int tpt = 128 / p.G;
+  kern<<<sms, L::THREADS, L::bytes(p.n_seqs), s>>>(mq, mk, mv, p, tpt);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  return launch_after(join, dim3(sms - 1, TILES * 8), 256, join_smem_bytes<D>(p.n_seqs, false), s, p, tpt * TILES);
+}
+
+}  // namespace
+
+size_t paged_tiles_workspace(int d) {
+  const int sms = device_sm_count();
+  return sms <= 0 ? 0 : static_cast<size_t>(sms) * 2 * 256 * (d + 2) * sizeof(float);
+}
+
+// UNSUPPORTED, with nothing launched, where the tensor maps cannot say the
+// layout (more than 128 query heads a key/value head, strides of zero).
+int paged_tiles_launch(const PagedParams &p, int d, int tokens, cudaStream_t s) {
+  if (p.G > 128) return ATTN_ERR_UNSUPPORTED;
+  const int page = 1 << p.page_shift, tpt = 128 / p.G;
+  CUtensorMap mq, mk, mv;
+  int rc;
+  {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(p.hq), static_cast<cuuint64_t>(p.n_tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(p.hq) * d * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(tpt)};
+    if ((rc = encode(&mq, p.q, 3, dims, strides, box)) != ATTN_OK) return rc;
+  }
+  {
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(p.hk),
+                                static_cast<cuuint64_t>(p.n_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.token_stride) * 2, static_cast<cuuint64_t>(p.head_stride) * 2,
+                                   static_cast<cuuint64_t>(p.page_stride) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(page < 128 ? page : 128), 1, 1};
+    if ((rc = encode(&mk, p.k, 4, dims, strides, box)) != ATTN_OK) return rc;
+    if ((rc = encode(&mv, p.v, 4, dims, strides, box)) != ATTN_OK) return rc;
+  }
+  const bool two = tokens > tpt;
+  if (d == 128) return two ? launch_tiles<128, 2>(p, mq, mk, mv, s) : launch_tiles<128, 1>(p, mq, mk, mv, s);
+  return two ? launch_tiles<64, 2>(p, mq, mk, mv, s) : launch_tiles<64, 1>(p, mq, mk, mv, s);
+}
+
+}  // namespace attn

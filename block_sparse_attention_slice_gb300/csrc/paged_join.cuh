@@ -11,51 +11,32 @@
 namespace attn {
 
 // Merges the pieces of the items that cross span boundaries: block x looks at
-// the boundary between spans x and x + 1 and, if it is the first inside an
-// item, merges that item's rows (blockIdx.y of gridDim.y takes every
-// gridDim.y-th).  Few pieces: one warp a row.  Many (a long sequence alone in
-// the batch): the block's warps share a row's pieces and add their sums.
-template <int D, int ROWS, int KL, int TILE_ROWS>
-__global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, int tpi) {
+// what worker x left and, where an item begins there and goes on, merges that
+// item's rows (blockIdx.y of gridDim.y takes its part of them).  Few pieces:
+// one warp a row.  Many (a long sequence alone in the batch): the block's
+// warps share a row's pieces and add their sums.  Pieces are added in the
+// order of their keys, so results do not vary from run to run.
+// PACKED: rows stand as they are counted; else 128 / G whole tokens to each
+// 128 rows.
+template <int D, int TILE_ROWS, bool PACKED>
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   constexpr int NW = 8, V = D / 32;
-  extern __shared__ __align__(16) uint8_t join_smem[];
-  long long *scan = reinterpret_cast<long long *>(join_smem);
-  float *red = reinterpret_cast<float *>(join_smem + 80);          // [NW][D + 2]
-  long long *first = reinterpret_cast<long long *>(join_smem + 80 + NW * (D + 4) * 4);
-  SeqInfo *info = ROWS > 0 ? reinterpret_cast<SeqInfo *>(first + p.n_seqs + 1) : nullptr;
-  make_plan<ROWS, KL, 256>(p, tpi, first, info, scan);
+  __shared__ float red[NW][D + 4];
   // every block waits, those without work too: what follows on the stream
   // relies on this grid's end for the end of the one before it
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long total = first[p.n_seqs], span = span_of(p, total);
-  const long long cut = (blockIdx.x + 1) * span;
-  if (cut >= total) return;
-  Walk<ROWS, KL> w;
-  w.seek(p, first, info, tpi, cut);
-  const long long f0 = cut - w.i, f1 = f0 + w.sp.n;
-  if (w.i == 0 || f0 < cut - span) return;      // the cut lies between items, or is not the item's first
-  const long long wk0 = f0 / span;
-  const int np = static_cast<int>((f1 - 1) / span - wk0) + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int rows, x0;                                  // the tile's rows, its first packed row
-  if (ROWS > 0) {
-    x0 = w.rt * TILE_ROWS;
-    rows = min(TILE_ROWS, w.s.nq * p.G - x0);
-  } else {
-    x0 = w.rt * tpi * p.G;
-    rows = min(tpi, w.s.nq - w.rt * tpi) * p.G;
-  }
-  // rows of whole-token tiles stand 128 / G tokens to each 128
-  const int per128 = (128 / p.G > 0 ? 128 / p.G : 1) * p.G;
-  // a piece's place: the item's first piece is its worker's second slot unless the span begins with it
+  const Cut cut = p.cuts[blockIdx.x];
+  if (cut.rows == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, np = cut.np;
+  const int per128 = PACKED ? 128 : 128 / p.G * p.G;
   auto place = [&](int i, int r) -> long long {
-    return ((wk0 + i) * 2 + (i == 0 && f0 != wk0 * span ? 1 : 0)) * TILE_ROWS +
-           (ROWS > 0 ? r : r + r / per128 * (128 - per128));
+    return ((static_cast<long long>(blockIdx.x) + i) * 2 + (i == 0 ? cut.slot0 : 0)) * TILE_ROWS +
+           (PACKED ? r : r + r / per128 * (128 - per128));
   };
   auto finish = [&](int r, float m, float l, const float (&acc)[V]) {
-    const int x = x0 + r, t = x / p.G, head = w.h * p.G + x - t * p.G;
-    const long long row = static_cast<long long>(w.s.q0 + t) * p.hq + head;
-    const long long li = static_cast<long long>(head) * p.n_tokens + w.s.q0 + t;
+    const int x = cut.x0 + r, t = x / p.G, head = cut.h * p.G + x - t * p.G;
+    const long long row = static_cast<long long>(cut.q0 + t) * p.hq + head;
+    const long long li = static_cast<long long>(head) * p.n_tokens + cut.q0 + t;
     float fo, fi, lse;
     row_final(m, l, p.init_lse ? p.init_lse[li] : -INFINITY, fo, fi, lse);
 #pragma unroll
@@ -101,36 +82,35 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   };
   float m, l, acc[V];
-  if (np <= 2 * NW) {
-    for (int r = blockIdx.y * NW + warp; r < rows; r += gridDim.y * NW) {
+  if (np <= NW) {
+    for (int r = blockIdx.y * NW + warp; r < cut.rows; r += gridDim.y * NW) {
       gather(r, 0, 1, m, l, acc);
       finish(r, m, l, acc);
     }
     return;
   }
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+  for (int r = blockIdx.y; r < cut.rows; r += gridDim.y) {
     gather(r, warp, NW, m, l, acc);
-    float *mine = red + warp * (D + 4);
 #pragma unroll
-    for (int c = 0; c < V; ++c) mine[lane * V + c] = acc[c];
+    for (int c = 0; c < V; ++c) red[warp][lane * V + c] = acc[c];
     if (lane == 0) {
-      mine[D] = m;
-      mine[D + 1] = l;
+      red[warp][D] = m;
+      red[warp][D + 1] = l;
     }
     __syncthreads();
     if (warp == 0) {
       float mt = -INFINITY, lt = 0.f;
 #pragma unroll
-      for (int k = 0; k < NW; ++k) mt = fmaxf(mt, red[k * (D + 4) + D]);
+      for (int k = 0; k < NW; ++k) mt = fmaxf(mt, red[k][D]);
       const float mb = mt == -INFINITY ? 0.f : mt;
 #pragma unroll
       for (int c = 0; c < V; ++c) acc[c] = 0.f;
 #pragma unroll
       for (int k = 0; k < NW; ++k) {
-        const float f = exp2f(red[k * (D + 4) + D] - mb);
-        lt += f * red[k * (D + 4) + D + 1];
+        const float f = exp2f(red[k][D] - mb);
+        lt += f * red[k][D + 1];
 #pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = fmaf(f, red[k * (D + 4) + lane * V + c], acc[c]);
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(f, red[k][lane * V + c], acc[c]);
       }
       finish(r, mt, lt, acc);
     }
@@ -165,11 +145,6 @@ inline int launch_after(void (*kern)(A...), dim3 grid, int threads, size_t smem,
 }
 
 constexpr size_t kSmemMax = 232448;
-
-template <int D>
-inline size_t join_smem_bytes(int n_seqs, bool infos) {
-  return 80 + 8 * (D + 4) * 4 + 8ull * (n_seqs + 1) + (infos ? sizeof(SeqInfo) * n_seqs : 0);
-}
 
 
 

@@ -23,6 +23,14 @@ namespace attn {
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Left by each worker for the join: the item that begins in its span and goes
+// on behind it (rows = 0: none).  Row x0 + r, r < rows, of the sequence whose
+// tokens start at q0; np pieces, the first in the worker's slot slot0, the
+// others in the first slots of the workers that follow.
+struct __align__(16) Cut {
+  int q0, h, x0, rows, np, slot0, pad[2];
+};
+
 struct PagedParams {
   const void *q, *k, *v;
   const int32_t *q_ptr;       // null: token b belongs to sequence b
@@ -41,6 +49,7 @@ struct PagedParams {
   const float *init_lse;
   float *part_o;              // pieces: [workers][2][rows][D], [workers][2][rows][2]
   float *part_ml;
+  Cut *cuts;                  // [workers]
   int n_workers, min_span;    // min_span: key tiles a span holds at least
   unsigned int *status;
   unsigned long long wait_ns;
@@ -262,6 +271,26 @@ struct Walk {
     } while (sp.n == 0);
   }
 };
+
+// What worker `worker` with the span [from, to) leaves of the item that w
+// stands in, whose key tile w.i is the span's last.
+template <int ROWS, int KL>
+__device__ __forceinline__ void leave_cut(const PagedParams &p, const Walk<ROWS, KL> &w, int tpi, long long worker,
+                                          long long span, long long from, long long to) {
+  Cut c = {};
+  if (from < to) {
+    const long long f0 = to - 1 - w.i, f1 = f0 + w.sp.n;
+    if (f0 >= from && f1 > to) {
+      c.q0 = w.s.q0;
+      c.h = w.h;
+      c.x0 = ROWS > 0 ? w.rt * ROWS : w.rt * tpi * p.G;
+      c.rows = ROWS > 0 ? min(ROWS, w.s.nq * p.G - c.x0) : min(tpi, w.s.nq - w.rt * tpi) * p.G;
+      c.np = static_cast<int>((f1 - 1) / span - worker) + 1;
+      c.slot0 = f0 == from ? 0 : 1;
+    }
+  }
+  p.cuts[worker] = c;
+}
 
 // One row's summary (m in log2 units, l, unnormalised O) made final, with the
 // summary it starts from: the factors of O and of init_o, and its lse.

@@ -86,7 +86,10 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) paged_rows_kernel(const Page
   const long long total = first[p.n_seqs], span = span_of(p, total);
   const long long worker = static_cast<long long>(blockIdx.x) * PR_WARPS + warp;
   const long long from = worker * span, to = min(total, from + span);
-  if (from >= to) return;
+  if (from >= to) {
+    if (lane == 0) p.cuts[worker] = Cut{};
+    return;
+  }
   const int cnt = static_cast<int>(to - from);
 
   const uint32_t ring = smem_u32(rows_smem) + warp * (NST * 2 * S::SLAB);
@@ -282,6 +285,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) paged_rows_kernel(const Page
     }
     if (n + 1 < cnt) at.next(p, first, info, 0);
   }
+  if (lane == 0) leave_cut<PR_ROWS, PR_KL>(p, at, 0, worker, span, from, to);
 }
 
 // ---------------------------------------------------------------------- host
@@ -290,16 +294,15 @@ template <int D, int NST>
 static int launch_rows(PagedParams p, cudaStream_t s) {
   using S = RowsSmem<D, NST>;
   constexpr int kDev = 64;
-  static bool done[kDev] = {}, joined[kDev] = {};
+  static bool done[kDev] = {};
   static std::mutex mu;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDev) return ATTN_ERR_CUDA;
   auto kern = paged_rows_kernel<D, NST>;
-  auto join = paged_join_kernel<D, PR_ROWS, PR_KL, PR_ROWS>;
+  auto join = paged_join_kernel<D, PR_ROWS, true>;
   {
     std::lock_guard<std::mutex> lock(mu);
-    if (raise_smem(kern, kSmemMax, &done[dev]) != ATTN_OK || raise_smem(join, kSmemMax, &joined[dev]) != ATTN_OK)
-      return ATTN_ERR_CUDA;
+    if (raise_smem(kern, kSmemMax, &done[dev]) != ATTN_OK) return ATTN_ERR_CUDA;
   }
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
@@ -307,21 +310,23 @@ static int launch_rows(PagedParams p, cudaStream_t s) {
   p.min_span = 2;
   kern<<<sms, PR_WARPS * 32, S::bytes(p.n_seqs), s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  const unsigned gy = static_cast<unsigned>(p.G < PR_ROWS ? (p.G < 4 ? p.G : 4) : 4);
-  return launch_after(join, dim3(p.n_workers - 1, gy), 256, join_smem_bytes<D>(p.n_seqs, true), s, p, 0);
+  // few items: each has many pieces, and its rows go to blocks of their own
+  const long long items = static_cast<long long>(p.n_seqs) * p.hk;
+  return launch_after(join, dim3(p.n_workers, items * 8 < p.n_workers ? 4 : 1), 256, 0, s, p);
 }
 
 // Workers and rows of a piece, for the workspace.
 size_t paged_rows_workspace(int d) {
   const int sms = device_sm_count();
   if (sms <= 0) return 0;
-  return static_cast<size_t>(sms) * PR_WARPS * 2 * PR_ROWS * (d + 2) * sizeof(float);
+  return static_cast<size_t>(sms) * PR_WARPS * (2 * PR_ROWS * (d + 2) * sizeof(float) + sizeof(Cut));
 }
 
 int paged_rows_launch(PagedParams p, int d, cudaStream_t s) {
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   p.part_ml = p.part_o + static_cast<size_t>(sms) * PR_WARPS * 2 * PR_ROWS * d;
+  p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * PR_WARPS * 2 * PR_ROWS * 2);
   if (d == 128)
     return RowsSmem<128, 3>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<128, 3>(p, s) : launch_rows<128, 2>(p, s);
   return RowsSmem<64, 6>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<64, 6>(p, s) : launch_rows<64, 4>(p, s);

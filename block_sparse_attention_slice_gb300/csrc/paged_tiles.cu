@@ -22,8 +22,8 @@
 // What lies behind a sequence's end must not meet the zero weights of the P V
 // product: pages behind it, and pages that no row of the item sees, are
 // fetched from outside the tensor map, which reads as zeros, and the rows
-// behind the end in the last page are zeroed in shared memory by the issuing
-// warp before their product.
+// behind the end in the last page are zeroed in shared memory by the softmax
+// warps of row tile 0 before they let the product begin.
 //
 // Numerics as in paged_rows.cu: 32-bit scores, maxima, sums and O; P rounded
 // to bf16 (half a step, 2^-9 of each weight either way) as the operand that the
@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     long long at = from;
     Walk<0, PT_KL> w;
     if (at < to) w.seek(p, first, nullptr, tpi, at);
+    else if (lane == 0) p.cuts[blockIdx.x] = Cut{};
     const int R = min(1 << p.page_shift, 128), ppt = 128 / R, page_mask = (1 << p.page_shift) - 1;
     while (ok) {
       const int qs = nseg % PT_IQ;
@@ -212,6 +213,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       if (!ok) break;
       at += i1 - w.i;
       w.i = i1 - 1;
+      if (at == to && lane == 0) leave_cut<0, PT_KL>(p, w, tpi, blockIdx.x, span, from, to);
       if (at < to) w.next(p, first, nullptr, tpi);
     }
     if (*abort && lane == 0) {
@@ -237,137 +239,111 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         mma_ts(tmem + 256 + t * 128, tmem + sbuf * 128 + kk * 8,
                smem_desc_sw128(kv_smem + slot * L::TILE + kk * 16 * 128, L::HALF, 1024), IDESC_PV, (start && kk == 0) ? 0u : 1u);
     };
-    // rows behind the sequence's end of the V tile in `slot`
-    auto clear_tail = [&](int slot, int c0, int len) {
-      const int valid = len - c0;
-      if (valid >= 128) return;
-      for (int hh = 0; hh < L::NHALF; ++hh)
-        for (int x = valid * 128 + lane * 16; x < 128 * 128; x += 512)
-          st_shared_v4(kv_smem + slot * L::TILE + hh * L::HALF + x, make_uint4(0u, 0u, 0u, 0u));
-      fence_proxy_async_smem();
-      __syncwarp();
-    };
-    uint32_t ld = 0, step = 0, nseg = 0;      // ring position of the segment's next K; key tiles done
-    bool ok = true;
-    auto full = [&](uint32_t pos) { return wait_all(bar(L::B_FULL + pos % NS), (pos / NS) & 1, abort, lim); };
-    while (ok) {
-      const int qs = nseg % PT_IQ;
-      if (!wait_all(bar(L::B_IF + qs), (nseg / PT_IQ) & 1, abort, lim)) break;
-      volatile Seg *s = seg_at(qs);
-      const int out = s->out, len = s->len, ns = s->ns, w0 = s->w0, i0 = s->i0, n = s->i1 - i0;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::B_IE + qs));
-      if (out < 0) break;
-      auto c0_of = [&](int j) { return (i0 + j < ns ? i0 + j : i0 + j - ns + w0) << PT_KL; };
-      if (!wait_all(bar(L::B_Q), nseg & 1, abort, lim) || !full(ld)) break;
-      ++nseg;
-      tc_fence_after();
-      if constexpr (TILES == 1) {
-        if (lane == 0) {
-          issue_qk(0, step & 1, ld % NS);
-          mma_commit(bar(L::B_S + (step & 1)));
-          mma_commit(bar(L::B_EMPTY + ld % NS));
-          if (n == 1) mma_commit(bar(L::B_QE));
+    if (lane == 0) {
+      // ring position as (slot, phase), advanced without divisions: between
+      // groups of matrix instructions this lane's time is the tensor core's
+      struct Pos {
+        uint32_t slot, ph;
+        __device__ __forceinline__ void next() {
+          if (++slot == static_cast<uint32_t>(NS)) {
+            slot = 0;
+            ph ^= 1u;
+          }
         }
-        __syncwarp();
+      };
+      Pos k{0, 0};
+      uint32_t step = 0, nseg = 0;
+      auto wait = [&](uint32_t b, uint32_t ph) { return mbar_wait_bounded(b, ph, abort, lim); };
+      // both phases looked at once; the bounded waits only where one is not complete
+      auto wait2 = [&](uint32_t a, uint32_t pa, uint32_t b, uint32_t pb) {
+        const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
+        return (x || wait(a, pa)) && (y || wait(b, pb));
+      };
+      bool ok = true;
+      while (ok) {
+        const int qs = nseg % PT_IQ;
+        if (!wait(bar(L::B_IF + qs), (nseg / PT_IQ) & 1)) break;
+        volatile Seg *s = seg_at(qs);
+        const int out = s->out, n = s->i1 - s->i0;
+        mbar_arrive(bar(L::B_IE + qs));
+        if (out < 0) break;
+        if (!wait2(bar(L::B_Q), nseg & 1, bar(L::B_FULL + k.slot), k.ph)) break;
+        ++nseg;
+        tc_fence_after();
+        issue_qk(0, TILES == 1 ? step & 1 : 0, k.slot);
+        mma_commit(bar(L::B_S + (TILES == 1 ? step & 1 : 0)));
+        if (TILES == 2) {
+          issue_qk(1, 1, k.slot);
+          mma_commit(bar(L::B_S + 1));
+        }
+        mma_commit(bar(L::B_EMPTY + k.slot));
+        if (n == 1) mma_commit(bar(L::B_QE));
         for (int j = 0; j < n; ++j, ++step) {
-          const uint32_t v = ld + 2 * j + 1, k = v + 1;
-          if (j + 1 < n) {
-            if (!full(k)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            if (lane == 0) {
-              issue_qk(0, (step + 1) & 1, k % NS);
+          const bool more = j + 1 < n;
+          Pos v = k;
+          v.next();
+          k = v;
+          k.next();
+          if constexpr (TILES == 1) {
+            if (more) {
+              if (!wait(bar(L::B_FULL + k.slot), k.ph)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              issue_qk(0, (step + 1) & 1, k.slot);
               mma_commit(bar(L::B_S + ((step + 1) & 1)));
-              mma_commit(bar(L::B_EMPTY + k % NS));
+              mma_commit(bar(L::B_EMPTY + k.slot));
               if (j + 2 == n) mma_commit(bar(L::B_QE));
             }
-            __syncwarp();
-          }
-          if (!full(v)) {
-            ok = false;
-            break;
-          }
-          clear_tail(v % NS, c0_of(j), len);
-          if (!wait_all(bar(L::B_P + (step & 1)), (step >> 1) & 1, abort, lim)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            issue_pv(0, step & 1, v % NS, j == 0);
-            mma_commit(bar(L::B_EMPTY + v % NS));
-            mma_commit(bar(L::B_V));
-            if (j + 1 == n) mma_commit(bar(L::B_O));
-          }
-          __syncwarp();
-        }
-      } else {
-        if (lane == 0) {
-          issue_qk(0, 0, ld % NS);
-          mma_commit(bar(L::B_S + 0));
-          issue_qk(1, 1, ld % NS);
-          mma_commit(bar(L::B_S + 1));
-          mma_commit(bar(L::B_EMPTY + ld % NS));
-          if (n == 1) mma_commit(bar(L::B_QE));
-        }
-        __syncwarp();
-        for (int j = 0; j < n; ++j, ++step) {
-          const uint32_t v = ld + 2 * j + 1, k = v + 1;
-          const bool more = j + 1 < n;
-          if (!full(v)) {
-            ok = false;
-            break;
-          }
-          clear_tail(v % NS, c0_of(j), len);
-          if (!wait_all(bar(L::B_P + 0), step & 1, abort, lim)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            issue_pv(0, 0, v % NS, j == 0);
-            if (!more) mma_commit(bar(L::B_O + 0));
-          }
-          __syncwarp();
-          if (more) {
-            if (!full(k)) {
+            if (!wait2(bar(L::B_FULL + v.slot), v.ph, bar(L::B_P + (step & 1)), (step >> 1) & 1)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            if (lane == 0) {
-              issue_qk(0, 0, k % NS);
+            issue_pv(0, step & 1, v.slot, j == 0);
+            mma_commit(bar(L::B_EMPTY + v.slot));
+            mma_commit(bar(L::B_V));
+            if (!more) mma_commit(bar(L::B_O));
+          } else {
+            if (!wait2(bar(L::B_FULL + v.slot), v.ph, bar(L::B_P + 0), step & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_pv(0, 0, v.slot, j == 0);
+            if (!more) mma_commit(bar(L::B_O + 0));
+            bool have_p1 = false;
+            if (more) {
+              const bool have_k = mbar_try_wait(bar(L::B_FULL + k.slot), k.ph);
+              have_p1 = mbar_test_wait(bar(L::B_P + 1), step & 1);
+              if (!have_k && !wait(bar(L::B_FULL + k.slot), k.ph)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              issue_qk(0, 0, k.slot);
               mma_commit(bar(L::B_S + 0));
             }
-            __syncwarp();
-          }
-          if (!wait_all(bar(L::B_P + 1), step & 1, abort, lim)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            issue_pv(1, 1, v % NS, j == 0);
-            mma_commit(bar(L::B_EMPTY + v % NS));
+            if (!have_p1 && !wait(bar(L::B_P + 1), step & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_pv(1, 1, v.slot, j == 0);
+            mma_commit(bar(L::B_EMPTY + v.slot));
             if (!more) {
               mma_commit(bar(L::B_O + 1));
             } else {
-              issue_qk(1, 1, k % NS);
+              issue_qk(1, 1, k.slot);
               mma_commit(bar(L::B_S + 1));
-              mma_commit(bar(L::B_EMPTY + k % NS));
+              mma_commit(bar(L::B_EMPTY + k.slot));
               if (j + 2 == n) mma_commit(bar(L::B_QE));
             }
           }
-          __syncwarp();
         }
       }
-      ld += 2 * n;
-    }
-    // all matrix instructions are done before tensor memory is freed
-    if (lane == 0) {
+      // all matrix instructions are done before tensor memory is freed
       mma_commit(bar(L::B_DRAIN));
       wait_drain(bar(L::B_DRAIN), 0, 20000000ull);
     }
@@ -482,6 +458,19 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           }
           tmem_wait_st();
         }
+        if (t == 0 && c0 + 128 > len) {
+          // the last tile: rows of V behind the sequence's end become zeros
+          // before the product that P's arrival admits
+          const uint32_t pos = 2 * step + 1, slot = pos % NS;
+          if (!wait_all(bar(L::B_FULL + slot), (pos / NS) & 1, abort, lim)) {
+            ok = false;
+            break;
+          }
+          for (int hh = 0; hh < L::NHALF; ++hh)
+            for (int y = max(len - c0, 0) * 128 + r * 16; y < 128 * 128; y += 128 * 16)
+              st_shared_v4(kv_smem + slot * L::TILE + hh * L::HALF + y, make_uint4(0u, 0u, 0u, 0u));
+          fence_proxy_async_smem();
+        }
         tc_fence_before();
         mbar_arrive(bar(L::B_P + u));
       }
@@ -547,33 +536,33 @@ template <int D, int TILES>
 int launch_tiles(PagedParams p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
   using L = TileLayout<D, TILES>;
   constexpr int kDev = 64;
-  static bool done[kDev] = {}, joined[kDev] = {};
+  static bool done[kDev] = {};
   static std::mutex mu;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDev) return ATTN_ERR_CUDA;
   auto kern = paged_tiles_kernel<D, TILES>;
-  auto join = paged_join_kernel<D, 0, PT_KL, TILES * 128>;
+  auto join = paged_join_kernel<D, TILES * 128, false>;
   {
     std::lock_guard<std::mutex> lock(mu);
-    if (raise_smem(kern, kSmemMax, &done[dev]) != ATTN_OK || raise_smem(join, kSmemMax, &joined[dev]) != ATTN_OK)
-      return ATTN_ERR_CUDA;
+    if (raise_smem(kern, kSmemMax, &done[dev]) != ATTN_OK) return ATTN_ERR_CUDA;
   }
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   p.n_workers = sms;
   p.min_span = 2;
   p.part_ml = p.part_o + static_cast<size_t>(sms) * 2 * TILES * 128 * D;
+  p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * 2 * TILES * 128 * 2);
   const int tpt = 128 / p.G;
   kern<<<sms, L::THREADS, L::bytes(p.n_seqs), s>>>(mq, mk, mv, p, tpt);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  return launch_after(join, dim3(sms - 1, TILES * 8), 256, join_smem_bytes<D>(p.n_seqs, false), s, p, tpt * TILES);
+  return launch_after(join, dim3(sms, TILES * 8), 256, 0, s, p);
 }
 
 }  // namespace
 
 size_t paged_tiles_workspace(int d) {
   const int sms = device_sm_count();
-  return sms <= 0 ? 0 : static_cast<size_t>(sms) * 2 * 256 * (d + 2) * sizeof(float);
+  return sms <= 0 ? 0 : static_cast<size_t>(sms) * (2 * 256 * (d + 2) * sizeof(float) + sizeof(Cut));
 }
 
 // UNSUPPORTED, with nothing launched, where the tensor maps cannot say the

@@ -10,6 +10,7 @@
 
 #include "../../include/attn_paged.h"
 #include "attn_internal.h"
+#include "paged_join.cuh"
 #include "paged_plan.cuh"
 
 namespace attn {
@@ -120,18 +121,40 @@ PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, co
 }
 
 // Items of up to 16 rows (query heads of one key/value head times tokens) go to
-// the warp-level kernel, larger ones to the tensor-core tiles.
-int paged_launch(const PagedParams &p, int d, int tokens, cudaStream_t s) {
+// the warp-level kernel, larger ones to the tensor-core tiles.  The rows of a
+// piece in `tile_rows`.
+int paged_launch(const PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
   if (static_cast<int64_t>(tokens) * p.G > 16) {
-    const int rc = paged_tiles_launch(p, d, tokens, s);
+    const int rc = paged_tiles_launch(p, d, tokens, s, tile_rows);
     if (rc != ATTN_ERR_UNSUPPORTED) return rc;
   }
+  *tile_rows = 16;
   return paged_rows_launch(p, d, s);
 }
 
-// O and lse of the prefix pass, in 32 bits, ahead of the pieces
-size_t prefix_bytes(int n_tokens, int hq, int d) {
-  return up256(static_cast<size_t>(n_tokens) * hq * d * 4) + up256(static_cast<size_t>(n_tokens) * hq * 4);
+size_t pieces_bytes(int d) { return up256(std::max(paged_rows_workspace(d), paged_tiles_workspace(d))); }
+
+// attn_prefix_fwd's workspace: for each of the two passes where every row's
+// pieces are, the rows finished within a span, and the pieces.
+struct PairLayout {
+  size_t rec[2], ml[2], o[2], pieces[2], rec_bytes, total;
+};
+PairLayout pair_layout(int n_tokens, int hq, int d) {
+  PairLayout L;
+  const size_t rows = static_cast<size_t>(n_tokens) * hq;
+  size_t at = 0;
+  auto put = [&](size_t bytes) {
+    const size_t x = at;
+    at += up256(bytes);
+    return x;
+  };
+  for (size_t &x : L.rec) x = put(rows * sizeof(Rec4));
+  L.rec_bytes = at;
+  for (size_t &x : L.ml) x = put(rows * 8);
+  for (size_t &x : L.o) x = put(rows * d * 4);
+  for (size_t &x : L.pieces) x = put(pieces_bytes(d));
+  L.total = at;
+  return L;
 }
 
 }  // namespace
@@ -144,9 +167,8 @@ extern "C" {
 int attn_paged_workspace_bytes(int n_tokens, int hq, int d, int prefix, size_t *bytes) {
   if (!bytes || n_tokens < 0 || hq < 1) return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
-  const size_t w = std::max(paged_rows_workspace(d), paged_tiles_workspace(d));
-  if (w == 0) return ATTN_ERR_CUDA;
-  *bytes = w + (prefix ? prefix_bytes(n_tokens, hq, d) : 0);
+  if (paged_rows_workspace(d) == 0) return ATTN_ERR_CUDA;
+  *bytes = prefix ? pair_layout(n_tokens, hq, d).total : pieces_bytes(d);
   return ATTN_OK;
 }
 
@@ -173,7 +195,8 @@ int attn_paged_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q,
   p.part_o = static_cast<float *>(d_ws);
   p.status = paged_status();
   if (!p.status) return ATTN_ERR_CUDA;
-  return paged_launch(p, pages->d, std::min(max_q, n_tokens), reinterpret_cast<cudaStream_t>(stream));
+  int tile_rows;
+  return paged_launch(p, pages->d, std::min(max_q, n_tokens), reinterpret_cast<cudaStream_t>(stream), &tile_rows);
 }
 
 int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
@@ -195,31 +218,50 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
   if (!status) return ATTN_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(d_ws);
-  float *po = reinterpret_cast<float *>(ws);
-  float *plse = reinterpret_cast<float *>(ws + up256(static_cast<size_t>(n_tokens) * hq * pages->d * 4));
-  float *pieces = reinterpret_cast<float *>(ws + prefix_bytes(n_tokens, hq, pages->d));
+  int tile_rows;
+  // what follows the prefix
+  PagedParams r = params(q, q_ptr, n_tokens, hq, pages, seqs, scale, shift);
+  r.out = out;
+  r.lse = lse;
+  r.out_f32 = out_dtype == ATTN_DTYPE_F32;
+  r.status = status;
+  const int tokens = std::min(max_q, n_tokens);
+  if (prefix->n_seqs == 0) {
+    r.part_o = reinterpret_cast<float *>(ws);
+    return paged_launch(r, pages->d, tokens, s, &tile_rows);
+  }
   // the prefixes: rows of a whole group against its keys, none of them masked
   PagedParams p = params(q, q_ptr, n_tokens, hq, pages, prefix, scale, shift);
   p.group_ptr = group_ptr;
   p.n_members = seqs->n_seqs;
   p.causal = 0;
-  p.out = po;
-  p.lse = plse;
-  p.out_f32 = 1;
-  p.part_o = pieces;
   p.status = status;
-  const bool any = prefix->n_seqs > 0;
-  if (any && (rc = paged_launch(p, pages->d, (n_tokens + prefix->n_seqs - 1) / prefix->n_seqs, s)) != ATTN_OK) return rc;
-  // what follows it, each row starting from its prefix's summary
-  PagedParams r = params(q, q_ptr, n_tokens, hq, pages, seqs, scale, shift);
-  r.out = out;
-  r.lse = lse;
-  r.out_f32 = out_dtype == ATTN_DTYPE_F32;
-  r.init_o = any ? po : nullptr;
-  r.init_lse = any ? plse : nullptr;
-  r.part_o = pieces;
-  r.status = status;
-  return paged_launch(r, pages->d, std::min(max_q, n_tokens), s);
+  const PairLayout L = pair_layout(n_tokens, hq, pages->d);
+  JoinPair pair;
+  PagedParams *pass[2] = {&p, &r};
+  for (int i = 0; i < 2; ++i) {
+    pass[i]->rec = reinterpret_cast<Rec4 *>(ws + L.rec[i]);
+    pass[i]->dense_ml = reinterpret_cast<float *>(ws + L.ml[i]);
+    pass[i]->dense_o = reinterpret_cast<float *>(ws + L.o[i]);
+    pass[i]->part_o = reinterpret_cast<float *>(ws + L.pieces[i]);
+  }
+  // neither pass reads what the other writes: the second starts on each SM as
+  // the first leaves it, and waits for its end before its own
+  r.wait_end = 1;
+  if (cudaMemsetAsync(ws, 0xff, L.rec_bytes, s) != cudaSuccess) return ATTN_ERR_CUDA;
+  if ((rc = paged_launch(p, pages->d, (n_tokens + prefix->n_seqs - 1) / prefix->n_seqs, s, &pair.tile_rows[0])) != ATTN_OK ||
+      (rc = paged_launch(r, pages->d, tokens, s, &pair.tile_rows[1])) != ATTN_OK)
+    return rc;
+  for (int i = 0; i < 2; ++i) {
+    pair.rec[i] = pass[i]->rec;
+    pair.dense_ml[i] = pass[i]->dense_ml;
+    pair.dense_o[i] = pass[i]->dense_o;
+    pair.part_o[i] = pass[i]->part_o;
+    pair.part_ml[i] = pass[i]->part_o + paged_piece_floats(pair.tile_rows[i], pages->d);
+  }
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n_tokens) * hq + 7) / 8));
+  return pages->d == 128 ? launch_after(paged_join_pair_kernel<128>, grid, 256, 0, s, r, pair)
+                         : launch_after(paged_join_pair_kernel<64>, grid, 256, 0, s, r, pair);
 }
 
 int attn_slices_from_windows(const int32_t *h_lengths, int n, int window, int sinks, attn_slice_t *h_out,

@@ -31,6 +31,15 @@ struct __align__(16) Cut {
   int q0, h, x0, rows, np, slot0, pad[2];
 };
 
+// Where a row's pieces are: np > 0 pieces, the first at row `row` of slot slot0
+// of worker `worker`, the others at that row of the first slots of the workers
+// that follow; np = 0: the dense arrays; REC_EMPTY: it sees nothing; -1 (the
+// arrays are filled with all bits set beforehand): it is no row of the pass.
+struct __align__(16) Rec4 {
+  int worker, slot0, np, row;
+};
+constexpr int REC_EMPTY = -2;
+
 struct PagedParams {
   const void *q, *k, *v;
   const int32_t *q_ptr;       // null: token b belongs to sequence b
@@ -45,8 +54,12 @@ struct PagedParams {
   void *out;                  // [n_tokens, hq, D]
   float *lse;                 // [hq, n_tokens]
   int out_f32;
-  const float *init_o;        // a summary every row starts from (normalised O, lse), or null
-  const float *init_lse;
+  // one of several passes over the same rows (prefix, then what follows it):
+  // rows finished within a span go to dense_o [n_tokens, hq, D] and dense_ml
+  // as (m, l, unnormalised O), and rec says where every row's pieces are
+  float *dense_o, *dense_ml;
+  Rec4 *rec;                  // [n_tokens, hq]; null: rows are finished to out and lse
+  int wait_end;               // launched beside the kernel before it, whose end it has to wait for
   float *part_o;              // pieces: [workers][2][rows][D], [workers][2][rows][2]
   float *part_ml;
   Cut *cuts;                  // [workers]
@@ -292,34 +305,18 @@ __device__ __forceinline__ void leave_cut(const PagedParams &p, const Walk<ROWS,
   p.cuts[worker] = c;
 }
 
-// One row's summary (m in log2 units, l, unnormalised O) made final, with the
-// summary it starts from: the factors of O and of init_o, and its lse.
-__device__ __forceinline__ void row_final(float m, float l, float init_lse, float &fo, float &fi, float &lse) {
-  const float mi = init_lse * kLog2e;          // -inf: nothing to start from
-  const float M = fmaxf(m, mi);
-  if (M == -INFINITY || (l == 0.f && mi == -INFINITY)) {
-    fo = fi = 0.f;
-    lse = -INFINITY;
-    return;
-  }
-  const float a = l > 0.f ? exp2f(m - M) : 0.f, c = exp2f(mi - M), L = a * l + c, inv = 1.f / L;
-  fo = a * inv;
-  fi = c * inv;
-  lse = (M + log2f(L)) * kLn2;
+// One row's summary (m in log2 units, l) made final: the factor of its
+// unnormalised O, and its lse.
+__device__ __forceinline__ void row_final(float m, float l, float &fo, float &lse) {
+  fo = l > 0.f ? 1.f / l : 0.f;
+  lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (!(l == l)) fo = lse = l;      // what is not a number stays so
 }
 
 // Writes columns c, c+1 of a finished row.
 template <int D>
-__device__ __forceinline__ void store_pair(const PagedParams &p, long long row, int c, float x, float y, float fo,
-                                           float fi) {
-  x *= fo;
-  y *= fo;
+__device__ __forceinline__ void store_pair(const PagedParams &p, long long row, int c, float x, float y) {
   const long long at = row * D + c;
-  if (fi != 0.f) {
-    const float2 i = *reinterpret_cast<const float2 *>(p.init_o + at);
-    x += fi * i.x;
-    y += fi * i.y;
-  }
   if (p.out_f32)
     *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at) = make_float2(x, y);
   else
@@ -328,22 +325,11 @@ __device__ __forceinline__ void store_pair(const PagedParams &p, long long row, 
 
 // Writes columns c .. c + 31 of a finished row, as one thread holds them.
 template <int D>
-__device__ __forceinline__ void store_32(const PagedParams &p, long long row, int c, const uint32_t (&y)[32], float fo,
-                                         float fi) {
+__device__ __forceinline__ void store_32(const PagedParams &p, long long row, int c, const uint32_t (&y)[32], float fo) {
   const long long at = row * D + c;
   float x[32];
 #pragma unroll
   for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(y[k]) * fo;
-  if (fi != 0.f) {
-#pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-      const float4 i = *reinterpret_cast<const float4 *>(p.init_o + at + k);
-      x[k] += fi * i.x;
-      x[k + 1] += fi * i.y;
-      x[k + 2] += fi * i.z;
-      x[k + 3] += fi * i.w;
-    }
-  }
   if (p.out_f32) {
 #pragma unroll
     for (int k = 0; k < 32; k += 4)
@@ -357,20 +343,18 @@ __device__ __forceinline__ void store_32(const PagedParams &p, long long row, in
   }
 }
 
+// Pieces of the item that starts at flat index f0 in the span [from, ..) of
+// `worker`: their number, and the slot of the first (np = 0: it ends there).
+__device__ __forceinline__ void item_pieces(long long f0, int n, long long worker, long long span, long long from,
+                                            int &np, int &slot0) {
+  np = static_cast<int>((f0 + n - 1) / span - worker) + 1;
+  slot0 = f0 == from ? 0 : 1;
+  if (np == 1) np = 0;
+}
+
 // Rows of items without a key tile: their sequences see nothing (here).
 template <int D, int ROWS, int KL>
 __device__ inline void finish_empty(const PagedParams &p, const SeqInfo *info, int tpi) {
-  if (p.group_ptr) {
-    // tokens before the first group and behind the last have no prefix
-    const int m0 = min(max(__ldg(p.group_ptr), 0), p.n_members);
-    const int m1 = min(max(__ldg(p.group_ptr + p.n_seqs), m0), p.n_members);
-    const int t0 = min(max(p.q_ptr ? __ldg(p.q_ptr + m0) : m0, 0), p.n_tokens);
-    const int t1 = min(max(p.q_ptr ? __ldg(p.q_ptr + m1) : m1, t0), p.n_tokens);
-    const int rest = p.n_tokens - (t1 - t0);
-    for (int t = blockIdx.x; t < rest; t += gridDim.x)
-      for (int h = threadIdx.x; h < p.hq; h += blockDim.x)
-        p.lse[static_cast<long long>(h) * p.n_tokens + (t < t0 ? t : t + t1 - t0)] = -INFINITY;
-  }
   for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x) {
     const SeqInfo s = info ? info[b] : seq_info(p, b);
     // causal rows see more keys the later they stand: the empty tiles come first
@@ -383,11 +367,12 @@ __device__ inline void finish_empty(const PagedParams &p, const SeqInfo *info, i
         const int c = x % (D / 2) * 2, y = x / (D / 2), h = y / rows, r = y - h * rows + (ROWS > 0 ? rt * ROWS : a * p.G);
         const int t = r / p.G, head = h * p.G + r - t * p.G;
         const long long row = static_cast<long long>(s.q0 + t) * p.hq + head;
-        const long long li = static_cast<long long>(head) * p.n_tokens + s.q0 + t;
-        float fo, fi, lse;
-        row_final(-INFINITY, 0.f, p.init_lse ? p.init_lse[li] : -INFINITY, fo, fi, lse);
-        store_pair<D>(p, row, c, 0.f, 0.f, fo, fi);
-        if (c == 0) p.lse[li] = lse;
+        if (p.rec) {
+          if (c == 0) p.rec[row] = Rec4{0, 0, REC_EMPTY, 0};
+          continue;
+        }
+        store_pair<D>(p, row, c, 0.f, 0.f);
+        if (c == 0) p.lse[static_cast<long long>(head) * p.n_tokens + s.q0 + t] = -INFINITY;
       }
     }
   }

@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) paged_rows_kernel(const Page
   const long long worker = static_cast<long long>(blockIdx.x) * PR_WARPS + warp;
   const long long from = worker * span, to = min(total, from + span);
   if (from >= to) {
-    if (lane == 0) p.cuts[worker] = Cut{};
+    if (lane == 0 && !p.rec) p.cuts[worker] = Cut{};
+    if (p.wait_end) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   const int cnt = static_cast<int>(to - from);
@@ -255,18 +256,32 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) paged_rows_kernel(const Page
       l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
       l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
       l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+      if (p.rec && piece0 == 0 && lc == 0) {
+        int np, slot0;
+        item_pieces(from + n - at.i, at.sp.n, worker, span, from, np, slot0);
+        if (row0 >= 0) p.rec[row0] = Rec4{static_cast<int>(worker), slot0, np, lr};
+        if (row1 >= 0) p.rec[row1] = Rec4{static_cast<int>(worker), slot0, np, lr + 8};
+      }
       if (ends && piece0 == 0) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const long long row = u ? row1 : row0;
           if (row < 0) continue;
-          const int head = static_cast<int>(row % p.hq);
-          const long long li = static_cast<long long>(head) * p.n_tokens + row / p.hq;
-          float fo, fi, lse;
-          row_final(u ? m1 : m0, u ? l1 : l0, p.init_lse ? p.init_lse[li] : -INFINITY, fo, fi, lse);
+          if (p.rec) {
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) store_pair<D>(p, row, j * 8 + lc, o[j][2 * u], o[j][2 * u + 1], fo, fi);
-          if (lc == 0) p.lse[li] = lse;
+            for (int j = 0; j < D / 8; ++j)
+              *reinterpret_cast<float2 *>(p.dense_o + row * D + j * 8 + lc) = make_float2(o[j][2 * u], o[j][2 * u + 1]);
+            if (lc == 0) *reinterpret_cast<float2 *>(p.dense_ml + row * 2) = make_float2(u ? m1 : m0, u ? l1 : l0);
+            continue;
+          }
+          float fo, lse;
+          row_final(u ? m1 : m0, u ? l1 : l0, fo, lse);
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) store_pair<D>(p, row, j * 8 + lc, o[j][2 * u] * fo, o[j][2 * u + 1] * fo);
+          if (lc == 0) {
+            const int t = static_cast<int>(row / p.hq), head = static_cast<int>(row - static_cast<long long>(t) * p.hq);
+            p.lse[static_cast<long long>(head) * p.n_tokens + t] = lse;
+          }
         }
       } else {
         // slot 0: the piece a span begins with; slot 1: one that begins in it and goes on
@@ -285,7 +300,8 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) paged_rows_kernel(const Page
     }
     if (n + 1 < cnt) at.next(p, first, info, 0);
   }
-  if (lane == 0) leave_cut<PR_ROWS, PR_KL>(p, at, 0, worker, span, from, to);
+  if (lane == 0 && !p.rec) leave_cut<PR_ROWS, PR_KL>(p, at, 0, worker, span, from, to);
+  if (p.wait_end) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------- host
@@ -308,14 +324,20 @@ static int launch_rows(PagedParams p, cudaStream_t s) {
   if (sms <= 0) return ATTN_ERR_CUDA;
   p.n_workers = sms * PR_WARPS;
   p.min_span = 2;
+  if (p.wait_end) return launch_after(kern, dim3(sms), PR_WARPS * 32, S::bytes(p.n_seqs), s, p);
   kern<<<sms, PR_WARPS * 32, S::bytes(p.n_seqs), s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (p.rec) return ATTN_OK;
   // few items: each has many pieces, and its rows go to blocks of their own
   const long long items = static_cast<long long>(p.n_seqs) * p.hk;
   return launch_after(join, dim3(p.n_workers, items * 8 < p.n_workers ? 4 : 1), 256, 0, s, p);
 }
 
-// Workers and rows of a piece, for the workspace.
+// Floats of all workers' pieces of `tile_rows` rows.
+size_t paged_piece_floats(int tile_rows, int d) {
+  return static_cast<size_t>(device_sm_count()) * (tile_rows == PR_ROWS ? PR_WARPS : 1) * 2 * tile_rows * d;
+}
+
 size_t paged_rows_workspace(int d) {
   const int sms = device_sm_count();
   if (sms <= 0) return 0;
@@ -325,7 +347,7 @@ size_t paged_rows_workspace(int d) {
 int paged_rows_launch(PagedParams p, int d, cudaStream_t s) {
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  p.part_ml = p.part_o + static_cast<size_t>(sms) * PR_WARPS * 2 * PR_ROWS * d;
+  p.part_ml = p.part_o + paged_piece_floats(PR_ROWS, d);
   p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * PR_WARPS * 2 * PR_ROWS * 2);
   if (d == 128)
     return RowsSmem<128, 3>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<128, 3>(p, s) : launch_rows<128, 2>(p, s);

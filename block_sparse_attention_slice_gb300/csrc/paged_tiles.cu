@@ -62,7 +62,9 @@ struct TileLayout {
 
 // What the producer publishes of a segment: a run of key tiles of one item.
 struct Seg {
-  int tok0, ntok, h, pos0, len, ns, w0, i0, i1, out;    // out: 0 finished here, 1 / 2 piece slot + 1, -1 no more
+  int tok0, ntok, h, pos0, len, ns, w0, i0, i1;
+  int out;              // 0 finished here, 1 / 2 piece slot + 1, -1 no more
+  int np, slot0;        // of an item that begins here (i0 = 0): see Rec4
 };
 static_assert(sizeof(Seg) <= 64, "segment record");
 
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     long long at = from;
     Walk<0, PT_KL> w;
     if (at < to) w.seek(p, first, nullptr, tpi, at);
-    else if (lane == 0) p.cuts[blockIdx.x] = Cut{};
+    else if (lane == 0 && !p.rec) p.cuts[blockIdx.x] = Cut{};
     const int R = min(1 << p.page_shift, 128), ppt = 128 / R, page_mask = (1 << p.page_shift) - 1;
     while (ok) {
       const int qs = nseg % PT_IQ;
@@ -158,6 +160,10 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           s->i0 = w.i;
           s->i1 = i1;
           s->out = w.i == 0 && i1 == w.sp.n ? 0 : at == from ? 1 : 2;
+          int np, slot0;
+          item_pieces(at - w.i, w.sp.n, blockIdx.x, span, from, np, slot0);
+          s->np = np;
+          s->slot0 = slot0;
         } else {
           s->out = -1;
         }
@@ -213,7 +219,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       if (!ok) break;
       at += i1 - w.i;
       w.i = i1 - 1;
-      if (at == to && lane == 0) leave_cut<0, PT_KL>(p, w, tpi, blockIdx.x, span, from, to);
+      if (at == to && lane == 0 && !p.rec) leave_cut<0, PT_KL>(p, w, tpi, blockIdx.x, span, from, to);
       if (at < to) w.next(p, first, nullptr, tpi);
     }
     if (*abort && lane == 0) {
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       if (!wait_all(bar(L::B_IF + qs), (nseg / PT_IQ) & 1, abort, lim)) break;
       volatile Seg *s = seg_at(qs);
       const int out = s->out, tok0 = s->tok0 + t * tpt, ntok = min(tpt, s->ntok - t * tpt), h = s->h, pos0 = s->pos0 + t * tpt,
-                len = s->len, ns = s->ns, w0 = s->w0, i0 = s->i0, i1 = s->i1;
+                len = s->len, ns = s->ns, w0 = s->w0, i0 = s->i0, i1 = s->i1, np = s->np, slot0 = s->slot0;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::B_IE + qs));
       if (out < 0) break;
@@ -480,28 +486,29 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       tc_fence_after();
       if (!idle) {
         const long long row = static_cast<long long>(tok0 + tl) * p.hq + h * p.G + g;
-        if (out == 0) {
-          const long long li = static_cast<long long>(h * p.G + g) * p.n_tokens + tok0 + tl;
-          float fo = 0.f, fi = 0.f, lse = 0.f;
+        if (p.rec && live && i0 == 0) p.rec[row] = Rec4{static_cast<int>(blockIdx.x), slot0, np, t * 128 + r};
+        if (out == 0 && !p.rec) {
+          float fo = 0.f, lse = 0.f;
           if (live) {
-            row_final(m_ref, l, p.init_lse ? p.init_lse[li] : -INFINITY, fo, fi, lse);
-            p.lse[li] = lse;
+            row_final(m_ref, l, fo, lse);
+            p.lse[static_cast<long long>(h * p.G + g) * p.n_tokens + tok0 + tl] = lse;
           }
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t y[32];
             tmem_ld32_wait(tO + c * 32, y);
-            if (live) store_32<D>(p, row, c * 32, y, fo, fi);
+            if (live) store_32<D>(p, row, c * 32, y, fo);
           }
         } else {
           const long long pr = (static_cast<long long>(blockIdx.x) * 2 + out - 1) * (TILES * 128) + t * 128 + r;
-          if (live) *reinterpret_cast<float2 *>(p.part_ml + pr * 2) = make_float2(m_ref, l);
+          float *po = out ? p.part_o + pr * D : p.dense_o + row * D, *pml = out ? p.part_ml + pr * 2 : p.dense_ml + row * 2;
+          if (live) *reinterpret_cast<float2 *>(pml) = make_float2(m_ref, l);
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t y[32];
             tmem_ld32_wait(tO + c * 32, y);
             if (!live) continue;
-            uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + pr * D + c * 32);
+            uint4 *dst = reinterpret_cast<uint4 *>(po + c * 32);
 #pragma unroll
             for (int k = 0; k < 8; ++k) dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
           }
@@ -515,6 +522,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   tc_fence_after();
   if (warp == WM) tmem_dealloc(tmem, 512);
   if (threadIdx.x == 0 && *abort) paged_fail(p, ATTN_ERR_TIMEOUT);
+  if (p.wait_end) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------- host
@@ -550,11 +558,13 @@ int launch_tiles(PagedParams p, const CUtensorMap &mq, const CUtensorMap &mk, co
   if (sms <= 0) return ATTN_ERR_CUDA;
   p.n_workers = sms;
   p.min_span = 2;
-  p.part_ml = p.part_o + static_cast<size_t>(sms) * 2 * TILES * 128 * D;
+  p.part_ml = p.part_o + paged_piece_floats(TILES * 128, D);
   p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * 2 * TILES * 128 * 2);
   const int tpt = 128 / p.G;
+  if (p.wait_end) return launch_after(kern, dim3(sms), L::THREADS, L::bytes(p.n_seqs), s, mq, mk, mv, p, tpt);
   kern<<<sms, L::THREADS, L::bytes(p.n_seqs), s>>>(mq, mk, mv, p, tpt);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (p.rec) return ATTN_OK;
   return launch_after(join, dim3(sms, TILES * 8), 256, 0, s, p);
 }
 
@@ -567,7 +577,7 @@ size_t paged_tiles_workspace(int d) {
 
 // UNSUPPORTED, with nothing launched, where the tensor maps cannot say the
 // layout (more than 128 query heads a key/value head, strides of zero).
-int paged_tiles_launch(const PagedParams &p, int d, int tokens, cudaStream_t s) {
+int paged_tiles_launch(const PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
   if (p.G > 128) return ATTN_ERR_UNSUPPORTED;
   const int page = 1 << p.page_shift, tpt = 128 / p.G;
   CUtensorMap mq, mk, mv;
@@ -588,6 +598,7 @@ int paged_tiles_launch(const PagedParams &p, int d, int tokens, cudaStream_t s) 
     if ((rc = encode(&mv, p.v, 4, dims, strides, box)) != ATTN_OK) return rc;
   }
   const bool two = tokens > tpt;
+  *tile_rows = two ? 256 : 128;
   if (d == 128) return two ? launch_tiles<128, 2>(p, mq, mk, mv, s) : launch_tiles<128, 1>(p, mq, mk, mv, s);
   return two ? launch_tiles<64, 2>(p, mq, mk, mv, s) : launch_tiles<64, 1>(p, mq, mk, mv, s);
 }

@@ -75,13 +75,35 @@ def test_oracle_paged_is_the_dense_oracle():
     assert np.allclose(O2, O1[20:]) and np.allclose(l2, l1[:, 20:])
 
 
+class Pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("hk", ctypes.c_int32), ("d", ctypes.c_int32), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Seqs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("seqs", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("n_slots", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("n_slots", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+def test_packed_structs_are_the_headers():
+    assert bytes(Pages(1, 2, 3, 4, 5, 6, 7, 8, 9)) == G._PAGES(1, 2, 3, 4, 5, 6, 7, 8, 9)
+    assert bytes(Seqs(1, 2, 3, 4, 5, 6, 7, 8)) == G._SEQS(1, 2, 3, 4, 5, 6, 7, 8)
+    assert bytes(Cache(1, 2, 3, 4, 5, 6, 7, 8)) == G._CACHE(1, 2, 3, 4, 5, 6, 7, 8)
+
+
 X = ctypes.c_void_p(4096)      # an aligned address that no refused call reads
 
 
 def _args(**kw):
-    pages = G.AttnPages(4096, 4096, 10, 16, 2, 128, 16 * 256, 256, 128)
-    seqs = G.AttnSeqs(4096, 4096, None, 4, 3, 4, 3, 0)
-    pre = G.AttnSeqs(4096, 4096, None, 4, 1, 4, 1, 0)
+    pages = Pages(4096, 4096, 10, 16, 2, 128, 16 * 256, 256, 128)
+    seqs = Seqs(4096, 4096, None, 4, 3, 4, 3, 0)
+    pre = Seqs(4096, 4096, None, 4, 1, 4, 1, 0)
     a = dict(q=X, q_ptr=X, n_tokens=5, max_q=2, hq=4, scale=1.0, window=0, sinks=0, out=X, out_dtype=0, lse=X, ws=X, ws_bytes=1 << 40,
              group_ptr=X, pages=pages, seqs=seqs, pre=pre)
     for name, value in kw.items():
@@ -149,7 +171,7 @@ def test_binding_refuses_wrong_tensors():
 
 
 def _cache(**kw):
-    c = G.AttnCache(4096, 4096, 4096, 6, 5, 6, 40, 16)
+    c = Cache(4096, 4096, 4096, 6, 5, 6, 40, 16)
     for name, value in kw.items():
         setattr(c, name, value)
     return ctypes.byref(c)

@@ -26,6 +26,7 @@
 #include "../../include/attn_paged.h"
 #include "attn_device.cuh"
 #include "attn_internal.h"
+#include "launch.cuh"
 
 namespace attn {
 
@@ -209,6 +210,8 @@ extern __shared__ __align__(16) int cache_smem[];
 // ---------------------------------------------------------------- extend
 
 __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_extend_kernel(const CacheParams p) {
+  after_previous();
+  admit_next();
   __shared__ CacheSmem s;
   cluster_started();
   const int rank = cluster_ctarank();
@@ -270,6 +273,8 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_extend
 // tokens that no token at position len - 1 or later sees.
 template <bool TRIM>
 __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_free_kernel(const CacheParams p) {
+  after_previous();
+  admit_next();
   __shared__ CacheSmem s;
   const int rank = cluster_ctarank();
   int *first = cache_smem;
@@ -317,6 +322,8 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_free_k
 // a source and be replaced), fresh pages are chosen, then the barrier, then
 // rows and counts are written.
 __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_fork_kernel(const CacheParams p) {
+  after_previous();
+  admit_next();
   __shared__ CacheSmem s;
   cluster_started();
   const int rank = cluster_ctarank(), n = p.n;
@@ -419,6 +426,8 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_fork_k
 // Pages in use move to the lowest indices: those at `used` and above, in
 // ascending order, into the free ones below it, in ascending order.
 __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_compact_kernel(const CacheParams p) {
+  after_previous();
+  admit_next();
   __shared__ CacheSmem s;
   cluster_started();
   const int rank = cluster_ctarank();
@@ -499,6 +508,8 @@ constexpr int COPY_T = 256, COPY_U = 4, COPY_CHUNK = COPY_T * COPY_U * 16;
 // Streams pages: a unit is 16 KB of one page of one pool, four 16-byte words a
 // thread, all loaded before the first is stored.
 __global__ void __launch_bounds__(COPY_T) cache_copy_kernel(const __grid_constant__ CopyParams p) {
+  after_previous();
+  admit_next();
   const int count = min(max(__ldg(p.copies), 0), p.cap);
   const long long units = static_cast<long long>(count) * p.chunks * p.n_pools;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
@@ -535,6 +546,8 @@ struct WriteParams {
 // A warp takes tokens one by one: finds its sequence (32 candidates a step),
 // its page, and moves the rows of all heads.
 __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
+  after_previous();
+  admit_next();
   const int lane = threadIdx.x & 31;
   for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.n_tokens; t += gridDim.x * 8) {
     int b = t, q0 = t, q1 = t + 1;
@@ -625,8 +638,7 @@ int cache_launch(void (*kern)(const CacheParams), bool (&done)[kDev], CacheParam
     }
   }
   if (!(p.status = paged_status())) return ATTN_ERR_CUDA;
-  kern<<<CC, CT, smem, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_after(kern, dim3(CC), CT, smem, s, p);
 }
 
 size_t bits(int n_slots) { return 4ull * ((n_slots + 31) / 32); }
@@ -741,8 +753,8 @@ int attn_cache_copy_pages(void *const *h_pools, int n_pools, size_t page_bytes, 
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   const long long most = static_cast<long long>(cap) * p.chunks * n_pools, grid = sms * 8;
-  cache_copy_kernel<<<static_cast<unsigned>(most < grid ? most : grid), COPY_T, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_after(cache_copy_kernel, dim3(static_cast<unsigned>(most < grid ? most : grid)), COPY_T, 0,
+                      reinterpret_cast<cudaStream_t>(stream), p);
 }
 
 int attn_cache_write(const attn_pages_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr, const void *k_new,
@@ -783,8 +795,8 @@ int attn_cache_write(const attn_pages_t *pages, const attn_seqs_t *seqs, const i
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   const int blocks = (n_tokens + 7) / 8, grid = sms * 8;
-  cache_write_kernel<<<blocks < grid ? blocks : grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_after(cache_write_kernel, dim3(blocks < grid ? blocks : grid), 256, 0,
+                      reinterpret_cast<cudaStream_t>(stream), p);
 }
 
 }  // extern "C"

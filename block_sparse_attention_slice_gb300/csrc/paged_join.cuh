@@ -1,11 +1,11 @@
-// Joining the pieces of the items that cross span boundaries, and the launch
-// helpers of the kernels that make them.
+// Joining the pieces of the items that cross span boundaries.
 #pragma once
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
 
+#include "launch.cuh"
 #include "paged_plan.cuh"
 
 namespace attn {
@@ -80,9 +80,8 @@ template <int D, int TILE_ROWS, bool PACKED>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   constexpr int NW = 8, V = D / 32;
   __shared__ float red[NW][D + 4];
-  // every block waits, those without work too: what follows on the stream
-  // relies on this grid's end for the end of the one before it
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  admit_next();
+  after_previous();
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.rows == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, np = cut.np;
@@ -146,7 +145,8 @@ struct JoinPair {
 template <int D>
 __global__ void __launch_bounds__(256) paged_join_pair_kernel(const PagedParams p, const JoinPair q) {
   constexpr int V = D / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  admit_next();
+  after_previous();
   const int lane = threadIdx.x & 31;
   const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= static_cast<long long>(p.n_tokens) * p.hq) return;
@@ -184,35 +184,5 @@ __global__ void __launch_bounds__(256) paged_join_pair_kernel(const PagedParams 
   for (int c = 0; c < V; c += 2) store_pair<D>(p, row, lane * V + c, g.acc[c] * fo, g.acc[c + 1] * fo);
   if (lane == 0) p.lse[row % p.hq * p.n_tokens + row / p.hq] = lse;
 }
-
-template <typename K>
-inline int raise_smem(K kern, size_t bytes, bool *done) {
-  if (*done) return ATTN_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
-    return ATTN_ERR_CUDA;
-  *done = true;
-  return ATTN_OK;
-}
-
-// A launch that may start while the one before it on the stream drains; it
-// waits for that one's memory before it reads any of it.
-template <typename... A>
-inline int launch_after(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
-}
-
-constexpr size_t kSmemMax = 232448;
-
-
 
 }  // namespace attn

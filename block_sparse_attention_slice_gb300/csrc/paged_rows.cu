@@ -32,7 +32,9 @@
 
 namespace attn {
 
-constexpr int PR_ROWS = 16, PR_KL = 4, PR_WARPS = 8;
+constexpr int PR_ROWS = 16, PR_KL = 4;
+// warps of a CTA: as many as the registers of a head dim's accumulators leave
+constexpr int rows_warps(int d) { return d == 128 ? 8 : 12; }
 constexpr float PR_TAU = 8.0f;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -64,31 +66,33 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 
 template <int D, int NST>
 struct RowsSmem {
+  static constexpr int W = rows_warps(D);
   static constexpr int SLAB = 16 * D * 2;                       // keys or values of one slab
-  static constexpr int RING = PR_WARPS * NST * 2 * SLAB;
+  static constexpr int RING = W * NST * 2 * SLAB;
   static constexpr int SCAN = RING;
-  static constexpr int FIRST = SCAN + (PR_WARPS + 1) * 8;
+  static constexpr int FIRST = SCAN + (W + 2) / 2 * 16;
   static size_t bytes(int n_seqs) { return FIRST + 8ull * (n_seqs + 1) + sizeof(SeqInfo) * n_seqs; }
 };
 
 template <int D, int NST>
-__global__ void __launch_bounds__(PR_WARPS * 32, 1) paged_rows_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const PagedParams p) {
   using S = RowsSmem<D, NST>;
   extern __shared__ __align__(128) uint8_t rows_smem[];
   long long *scan = reinterpret_cast<long long *>(rows_smem + S::SCAN);
   long long *first = reinterpret_cast<long long *>(rows_smem + S::FIRST);
   SeqInfo *info = reinterpret_cast<SeqInfo *>(first + p.n_seqs + 1);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  make_plan<PR_ROWS, PR_KL, PR_WARPS * 32>(p, 0, first, info, scan);
+  if (!p.wait_end) after_previous();
+  admit_next();
+  make_plan<PR_ROWS, PR_KL, S::W * 32>(p, 0, first, info, scan);
   finish_empty<D, PR_ROWS, PR_KL>(p, info, 0);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long total = first[p.n_seqs], span = span_of(p, total);
-  const long long worker = static_cast<long long>(blockIdx.x) * PR_WARPS + warp;
+  const long long worker = static_cast<long long>(blockIdx.x) * S::W + warp;
   const long long from = worker * span, to = min(total, from + span);
   if (from >= to) {
     if (lane == 0 && !p.rec) p.cuts[worker] = Cut{};
-    if (p.wait_end) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (p.wait_end) after_previous();
     return;
   }
   const int cnt = static_cast<int>(to - from);
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(PR_WARPS * 32, 1) paged_rows_kernel(const Page
     if (n + 1 < cnt) at.next(p, first, info, 0);
   }
   if (lane == 0 && !p.rec) leave_cut<PR_ROWS, PR_KL>(p, at, 0, worker, span, from, to);
-  if (p.wait_end) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.wait_end) after_previous();
 }
 
 // ---------------------------------------------------------------------- host
@@ -322,12 +326,10 @@ static int launch_rows(PagedParams p, cudaStream_t s) {
   }
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  p.n_workers = sms * PR_WARPS;
+  p.n_workers = sms * S::W;
   p.min_span = 2;
-  if (p.wait_end) return launch_after(kern, dim3(sms), PR_WARPS * 32, S::bytes(p.n_seqs), s, p);
-  kern<<<sms, PR_WARPS * 32, S::bytes(p.n_seqs), s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  if (p.rec) return ATTN_OK;
+  const int rc = launch_after(kern, dim3(sms), S::W * 32, S::bytes(p.n_seqs), s, p);
+  if (rc != ATTN_OK || p.rec) return rc;
   // few items: each has many pieces, and its rows go to blocks of their own
   const long long items = static_cast<long long>(p.n_seqs) * p.hk;
   return launch_after(join, dim3(p.n_workers, items * 8 < p.n_workers ? 4 : 1), 256, 0, s, p);
@@ -335,23 +337,23 @@ static int launch_rows(PagedParams p, cudaStream_t s) {
 
 // Floats of all workers' pieces of `tile_rows` rows.
 size_t paged_piece_floats(int tile_rows, int d) {
-  return static_cast<size_t>(device_sm_count()) * (tile_rows == PR_ROWS ? PR_WARPS : 1) * 2 * tile_rows * d;
+  return static_cast<size_t>(device_sm_count()) * (tile_rows == PR_ROWS ? rows_warps(d) : 1) * 2 * tile_rows * d;
 }
 
 size_t paged_rows_workspace(int d) {
   const int sms = device_sm_count();
   if (sms <= 0) return 0;
-  return static_cast<size_t>(sms) * PR_WARPS * (2 * PR_ROWS * (d + 2) * sizeof(float) + sizeof(Cut));
+  return static_cast<size_t>(sms) * rows_warps(d) * (2 * PR_ROWS * (d + 2) * sizeof(float) + sizeof(Cut));
 }
 
 int paged_rows_launch(PagedParams p, int d, cudaStream_t s) {
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   p.part_ml = p.part_o + paged_piece_floats(PR_ROWS, d);
-  p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * PR_WARPS * 2 * PR_ROWS * 2);
+  p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * rows_warps(d) * 2 * PR_ROWS * 2);
   if (d == 128)
     return RowsSmem<128, 3>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<128, 3>(p, s) : launch_rows<128, 2>(p, s);
-  return RowsSmem<64, 6>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<64, 6>(p, s) : launch_rows<64, 4>(p, s);
+  return RowsSmem<64, 4>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<64, 4>(p, s) : launch_rows<64, 2>(p, s);
 }
 
 }  // namespace attn

@@ -92,7 +92,6 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   const uint64_t lim = p.wait_ns;
   constexpr int WP = TILES * 4, WM = TILES * 4 + 1;       // producer, issuer
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     mbar_init(bar(L::B_Q), 1);
     mbar_init(bar(L::B_QE), 1);
@@ -123,6 +122,8 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  if (!p.wait_end) after_previous();
+  admit_next();
   make_plan<0, PT_KL, L::THREADS>(p, tpi, first, static_cast<SeqInfo *>(nullptr), scan);
   finish_empty<D, 0, PT_KL>(p, nullptr, tpi);
   tc_fence_before();
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   tc_fence_after();
   if (warp == WM) tmem_dealloc(tmem, 512);
   if (threadIdx.x == 0 && *abort) paged_fail(p, ATTN_ERR_TIMEOUT);
-  if (p.wait_end) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.wait_end) after_previous();
 }
 
 // ---------------------------------------------------------------------- host
@@ -561,10 +562,8 @@ int launch_tiles(PagedParams p, const CUtensorMap &mq, const CUtensorMap &mk, co
   p.part_ml = p.part_o + paged_piece_floats(TILES * 128, D);
   p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * 2 * TILES * 128 * 2);
   const int tpt = 128 / p.G;
-  if (p.wait_end) return launch_after(kern, dim3(sms), L::THREADS, L::bytes(p.n_seqs), s, mq, mk, mv, p, tpt);
-  kern<<<sms, L::THREADS, L::bytes(p.n_seqs), s>>>(mq, mk, mv, p, tpt);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  if (p.rec) return ATTN_OK;
+  const int rc = launch_after(kern, dim3(sms), L::THREADS, L::bytes(p.n_seqs), s, mq, mk, mv, p, tpt);
+  if (rc != ATTN_OK || p.rec) return rc;
   return launch_after(join, dim3(sms, TILES * 8), 256, 0, s, p);
 }
 

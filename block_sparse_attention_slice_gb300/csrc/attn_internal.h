@@ -78,9 +78,9 @@ int paged_check_pages(const attn_pages_t *g, int *shift);
 int paged_check_seqs(const attn_seqs_t *s, int page_size);
 struct PagedParams;
 size_t paged_rows_workspace(int d);
-int paged_rows_launch(PagedParams p, int d, cudaStream_t s);
+int paged_rows_launch(PagedParams &p, int d, cudaStream_t s);
 size_t paged_tiles_workspace(int d);
-int paged_tiles_launch(const PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows);
+int paged_tiles_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows);
 size_t paged_piece_floats(int tile_rows, int d);
 // Reads and clears the first failure status of the paged and cache kernels on
 // the current device; its device address for their launches (null on failure).

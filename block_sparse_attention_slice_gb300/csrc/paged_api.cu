@@ -121,9 +121,9 @@ PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, co
 }
 
 // Items of up to 16 rows (query heads of one key/value head times tokens) go to
-// the warp-level kernel, larger ones to the tensor-core tiles.  The rows of a
-// piece in `tile_rows`.
-int paged_launch(const PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
+// the warp-level kernel, larger ones to the tensor-core tiles.  What the kernel
+// chose is left in p and, the rows of a piece, in `tile_rows`.
+int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
   if (static_cast<int64_t>(tokens) * p.G > 16) {
     const int rc = paged_tiles_launch(p, d, tokens, s, tile_rows);
     if (rc != ATTN_ERR_UNSUPPORTED) return rc;
@@ -257,7 +257,8 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
     pair.dense_ml[i] = pass[i]->dense_ml;
     pair.dense_o[i] = pass[i]->dense_o;
     pair.part_o[i] = pass[i]->part_o;
-    pair.part_ml[i] = pass[i]->part_o + paged_piece_floats(pair.tile_rows[i], pages->d);
+    pair.part_ml[i] = pass[i]->part_ml;
+    pair.hp[i] = pass[i]->hp;
   }
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n_tokens) * hq + 7) / 8));
   return pages->d == 128 ? launch_after(paged_join_pair_kernel<128>, grid, 256, 0, s, r, pair)

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, np = cut.np;
   const int per128 = PACKED ? 128 : 128 / p.G * p.G;
   auto place = [&](int i, int r) -> long long {
-    return ((static_cast<long long>(blockIdx.x) + i) * 2 + (i == 0 ? cut.slot0 : 0)) * TILE_ROWS +
+    return ((static_cast<long long>(blockIdx.x) + i * p.hp) * 2 + (i == 0 ? cut.slot0 : 0)) * TILE_ROWS +
            (PACKED ? r : r + r / per128 * (128 - per128));
   };
   auto finish = [&](int r, float m, float l, const float (&acc)[V]) {
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
 struct JoinPair {
   const Rec4 *rec[2];
   const float *dense_o[2], *dense_ml[2], *part_o[2], *part_ml[2];
-  int tile_rows[2];
+  int tile_rows[2], hp[2];
 };
 template <int D>
 __global__ void __launch_bounds__(256) paged_join_pair_kernel(const PagedParams p, const JoinPair q) {
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(256) paged_join_pair_kernel(const PagedParams 
     const int k = x ? i - na : i;
     dense = r.np == 0;
     if (dense) return row;
-    return ((static_cast<long long>(r.worker) + k) * 2 + (k == 0 ? r.slot0 : 0)) * q.tile_rows[x] + r.row;
+    return ((static_cast<long long>(r.worker) + k * q.hp[x]) * 2 + (k == 0 ? r.slot0 : 0)) * q.tile_rows[x] + r.row;
   };
   Gather<D> g;
   for (int base = 0; base < np; base += 32) {

@@ -4,8 +4,11 @@
 // A work item is one row tile (a few of one sequence's new tokens, packed with
 // the query heads of one key/value head) against the key tiles that any of
 // its rows sees.  All items' key tiles form one flat list in the order
-// (sequence, key/value head, row tile, key tile), of which every worker takes
-// one contiguous span of equal length, whatever the sequences' lengths.  An
+// (sequence, group of hp key/value heads, row tile, key tile), of which every
+// worker takes one contiguous span of equal length, whatever the sequences'
+// lengths; hp workers side by side take the same span, one for each head of the
+// group, so that rows of neighbouring heads, which lie side by side in a page,
+// are read at the same time.  An
 // item that ends in the span it began in is finished there; one that crosses
 // spans leaves a piece (m, l, unnormalised O) per span, and join_kernel merges
 // them.  The list is never written out: each CTA sums the sequences' tile
@@ -26,14 +29,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Left by each worker for the join: the item that begins in its span and goes
 // on behind it (rows = 0: none).  Row x0 + r, r < rows, of the sequence whose
 // tokens start at q0; np pieces, the first in the worker's slot slot0, the
-// others in the first slots of the workers that follow.
+// others in the first slots of every hp-th worker that follows.
 struct __align__(16) Cut {
-  int q0, h, x0, rows, np, slot0, pad[2];
+  int q0, h, x0, rows, np, slot0, pad[2];   // h: the key/value head
 };
 
 // Where a row's pieces are: np > 0 pieces, the first at row `row` of slot slot0
-// of worker `worker`, the others at that row of the first slots of the workers
-// that follow; np = 0: the dense arrays; REC_EMPTY: it sees nothing; -1 (the
+// of worker `worker`, the others at that row of the first slots of every hp-th
+// worker that follows; np = 0: the dense arrays; REC_EMPTY: it sees nothing; -1 (the
 // arrays are filled with all bits set beforehand): it is no row of the pass.
 struct __align__(16) Rec4 {
   int worker, slot0, np, row;
@@ -63,7 +66,7 @@ struct PagedParams {
   float *part_o;              // pieces: [workers][2][rows][D], [workers][2][rows][2]
   float *part_ml;
   Cut *cuts;                  // [workers]
-  int n_workers, min_span;    // min_span: key tiles a span holds at least
+  int hp, n_spans, min_span;  // heads side by side; spans; key tiles a span holds at least
   unsigned int *status;
   unsigned long long wait_ns;
 };
@@ -188,7 +191,7 @@ __device__ inline void make_plan(const PagedParams &p, int tpi, long long *first
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     if (lane == 0) {
       if (info) info[warp] = s;
-      first[warp + 1] = n * p.hk;
+      first[warp + 1] = n * (p.hk / p.hp);
     }
   }
   if (by_warp) __syncthreads();
@@ -200,7 +203,7 @@ __device__ inline void make_plan(const PagedParams &p, int tpi, long long *first
     }
     const SeqInfo s = seq_info(p, b);
     if (info) info[b] = s;
-    const long long n = head_tiles<ROWS, KL>(p, s, tpi) * p.hk;
+    const long long n = head_tiles<ROWS, KL>(p, s, tpi) * (p.hk / p.hp);
     first[b + 1] = n;
     sum += n;
   }
@@ -223,11 +226,11 @@ __device__ inline void make_plan(const PagedParams &p, int tpi, long long *first
 }
 
 __device__ __forceinline__ long long span_of(const PagedParams &p, long long total) {
-  const long long s = (total + p.n_workers - 1) / p.n_workers;
+  const long long s = (total + p.n_spans - 1) / p.n_spans;
   return s > p.min_span ? s : p.min_span;
 }
 
-// A place in the flat list: key tile i of row tile rt of head h of sequence b.
+// A place in the flat list: key tile i of row tile rt of head group h of sequence b.
 template <int ROWS, int KL>
 struct Walk {
   int b, h, rt, R, i;
@@ -249,7 +252,7 @@ struct Walk {
     b = lo;
     load(p, info, tpi);
     long long rem = flat - first[b];
-    const long long per = (first[b + 1] - first[b]) / p.hk;
+    const long long per = (first[b + 1] - first[b]) / (p.hk / p.hp);
     h = static_cast<int>(rem / per);
     rem -= h * per;
     rt = 0;
@@ -273,7 +276,7 @@ struct Walk {
     do {
       if (++rt == R) {
         rt = 0;
-        if (++h == p.hk) {
+        if (++h == p.hk / p.hp) {
           h = 0;
           do ++b;
           while (first[b + 1] == first[b]);
@@ -285,20 +288,20 @@ struct Walk {
   }
 };
 
-// What worker `worker` with the span [from, to) leaves of the item that w
-// stands in, whose key tile w.i is the span's last.
+// What worker `worker` (of span `at`, [from, to)) leaves for head h of the item
+// that w stands in, whose key tile w.i is the span's last.
 template <int ROWS, int KL>
-__device__ __forceinline__ void leave_cut(const PagedParams &p, const Walk<ROWS, KL> &w, int tpi, long long worker,
-                                          long long span, long long from, long long to) {
+__device__ __forceinline__ void leave_cut(const PagedParams &p, const Walk<ROWS, KL> &w, int tpi, int h, long long worker,
+                                          long long at, long long span, long long from, long long to) {
   Cut c = {};
   if (from < to) {
     const long long f0 = to - 1 - w.i, f1 = f0 + w.sp.n;
     if (f0 >= from && f1 > to) {
       c.q0 = w.s.q0;
-      c.h = w.h;
+      c.h = h;
       c.x0 = ROWS > 0 ? w.rt * ROWS : w.rt * tpi * p.G;
       c.rows = ROWS > 0 ? min(ROWS, w.s.nq * p.G - c.x0) : min(tpi, w.s.nq - w.rt * tpi) * p.G;
-      c.np = static_cast<int>((f1 - 1) / span - worker) + 1;
+      c.np = static_cast<int>((f1 - 1) / span - at) + 1;
       c.slot0 = f0 == from ? 0 : 1;
     }
   }
@@ -343,11 +346,10 @@ __device__ __forceinline__ void store_32(const PagedParams &p, long long row, in
   }
 }
 
-// Pieces of the item that starts at flat index f0 in the span [from, ..) of
-// `worker`: their number, and the slot of the first (np = 0: it ends there).
-__device__ __forceinline__ void item_pieces(long long f0, int n, long long worker, long long span, long long from,
+// Pieces of the item that starts at flat index f0 in span `at`, [from, ..): their number, and the slot of the first (np = 0: it ends there).
+__device__ __forceinline__ void item_pieces(long long f0, int n, long long at, long long span, long long from,
                                             int &np, int &slot0) {
-  np = static_cast<int>((f0 + n - 1) / span - worker) + 1;
+  np = static_cast<int>((f0 + n - 1) / span - at) + 1;
   slot0 = f0 == from ? 0 : 1;
   if (np == 1) np = 0;
 }

@@ -22,6 +22,7 @@
 // only raised when it grew by more than 8 (log2), so P stays below 2^8.
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -32,9 +33,9 @@
 
 namespace attn {
 
-constexpr int PR_ROWS = 16, PR_KL = 4;
+constexpr int PR_ROWS = 16;
 // warps of a CTA: as many as the registers of a head dim's accumulators leave
-constexpr int rows_warps(int d) { return d == 128 ? 8 : 12; }
+__host__ __device__ constexpr int rows_warps(int) { return 8; }
 constexpr float PR_TAU = 8.0f;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -64,12 +65,23 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// A slab is 16 keys at head dim 128 and 32 at 64: 8 KB of keys and values.
+__host__ __device__ constexpr int rows_kl(int d) { return d == 128 ? 4 : 5; }
+
+// What the fetching side of a warp tells its computing side about a slab.
+struct __align__(16) Slab {
+  int key0, i, n, h;          // first key; key tile i of the item's n; head
+  int rt, q0, nq, len;        // row tile; the sequence's tokens and length
+};
+
 template <int D, int NST>
 struct RowsSmem {
   static constexpr int W = rows_warps(D);
-  static constexpr int SLAB = 16 * D * 2;                       // keys or values of one slab
-  static constexpr int RING = W * NST * 2 * SLAB;
-  static constexpr int SCAN = RING;
+  static constexpr int KEYS = 1 << rows_kl(D);
+  static constexpr int PART = KEYS * D * 2;                     // keys or values of one slab
+  static constexpr int RING = W * NST * 2 * PART;
+  static constexpr int NOTE = RING;                             // Slab [W][NST]
+  static constexpr int SCAN = NOTE + W * NST * static_cast<int>(sizeof(Slab));
   static constexpr int FIRST = SCAN + (W + 2) / 2 * 16;
   static size_t bytes(int n_seqs) { return FIRST + 8ull * (n_seqs + 1) + sizeof(SeqInfo) * n_seqs; }
 };
@@ -77,19 +89,22 @@ struct RowsSmem {
 template <int D, int NST>
 __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const PagedParams p) {
   using S = RowsSmem<D, NST>;
-  extern __shared__ __align__(128) uint8_t rows_smem[];
+  constexpr int KL = rows_kl(D), KEYS = S::KEYS, NSUB = KEYS / 16, NB = KEYS / 8;
+  constexpr int NOT_SEEN = INT_MIN;
+  extern __shared__ __align__(256) uint8_t rows_smem[];
   long long *scan = reinterpret_cast<long long *>(rows_smem + S::SCAN);
   long long *first = reinterpret_cast<long long *>(rows_smem + S::FIRST);
   SeqInfo *info = reinterpret_cast<SeqInfo *>(first + p.n_seqs + 1);
   if (!p.wait_end) after_previous();
   admit_next();
-  make_plan<PR_ROWS, PR_KL, S::W * 32>(p, 0, first, info, scan);
-  finish_empty<D, PR_ROWS, PR_KL>(p, info, 0);
+  make_plan<PR_ROWS, KL, S::W * 32>(p, 0, first, info, scan);
+  finish_empty<D, PR_ROWS, KL>(p, info, 0);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long total = first[p.n_seqs], span = span_of(p, total);
-  const long long worker = static_cast<long long>(blockIdx.x) * S::W + warp;
-  const long long from = worker * span, to = min(total, from + span);
+  const long long worker = static_cast<long long>(blockIdx.x) * S::W + warp, mine = worker / p.hp;
+  const int sub = static_cast<int>(worker - mine * p.hp);       // this warp's head of a group
+  const long long from = mine * span, to = min(total, from + span);
   if (from >= to) {
     if (lane == 0 && !p.rec) p.cuts[worker] = Cut{};
     if (p.wait_end) after_previous();
@@ -97,43 +112,74 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
   }
   const int cnt = static_cast<int>(to - from);
 
-  const uint32_t ring = smem_u32(rows_smem) + warp * (NST * 2 * S::SLAB);
-  Walk<PR_ROWS, PR_KL> in, at;     // slab being fetched, slab being used
+  const uint32_t ring = smem_u32(rows_smem) + warp * (NST * 2 * S::PART);
+  Slab *note = reinterpret_cast<Slab *>(rows_smem + S::NOTE) + warp * NST;
+  Walk<PR_ROWS, KL> in;            // the slab to be fetched next
   in.seek(p, first, info, 0, from);
-  at = in;
-  const int page_mask = (1 << p.page_shift) - 1;
-  auto page_of = [&](const Walk<PR_ROWS, PR_KL> &w) -> int {
-    return __ldg(p.table + w.s.slot * p.table_stride + ((w.sp.tile(w.i) << PR_KL) >> p.page_shift));
+  int in_lo, in_end;               // keys that some row of its item sees (and the first ones)
+  auto bounds = [&]() {
+    int t0, t1;
+    tile_tokens<PR_ROWS>(in.rt, in.s.nq, p.G, 0, t0, t1);
+    const int pos0 = in.s.len - in.s.nq;
+    in_end = p.causal ? pos0 + t1 + 1 : in.s.len;
+    in_lo = p.causal && p.window > 0 ? max(0, pos0 + t0 - p.window + 1) : 0;
   };
-  int page = page_of(in);
-  // fetches the slab `in` stands at and steps on
+  bounds();
+  const int page_mask = (1 << p.page_shift) - 1;
+  int page[NSUB];                  // of each 16 keys, read a slab ahead
+  auto look_up = [&]() {
+#pragma unroll
+    for (int j = 0; j < NSUB; ++j) {
+      const int k0 = (in.sp.tile(in.i) << KL) + 16 * j;
+      if (j > 0 && p.page_shift > 4) {
+        page[j] = k0 < in_end ? page[0] : NOT_SEEN;
+      } else if (NSUB == 1 || (k0 < in_end && (k0 + (1 << p.page_shift) > in_lo || k0 < p.sinks))) {
+        page[j] = __ldg(p.table + in.s.slot * p.table_stride + (k0 >> p.page_shift));
+      } else {
+        page[j] = NOT_SEEN;
+      }
+    }
+  };
+  look_up();
+  constexpr int CH = D / 8, RPI = 32 / CH;                 // 16-byte words a row, rows an instruction
+  const int fc = lane % CH, fr = lane / CH;
+  const long long lane_off = (fr * p.token_stride + fc * 8) * 2, row_step = RPI * p.token_stride * 2;
+  const char *kbase = static_cast<const char *>(p.k) + lane_off, *vbase = static_cast<const char *>(p.v) + lane_off;
+  const uint32_t lane_dst = fr * (D * 2) + ((fc ^ fr) << 4);
+  // fetches slab n of this worker, where `in` stands, and steps on
   auto fetch = [&](int n) {
     if (n < cnt) {
-      const int key0 = in.sp.tile(in.i) << PR_KL;
-      const bool good = page >= 0 && page < p.n_pages;
-      if (!good && lane == 0) paged_fail(p, ATTN_ERR_INVALID_ARG);
-      const long long base = (good ? page * p.page_stride : 0) + (key0 & page_mask) * p.token_stride +
-                             in.h * p.head_stride;
-      const int rows = good ? in.s.len - key0 : 0;          // those behind the end read as zeros
-      const uint32_t dst = ring + (n % NST) * (2 * S::SLAB);
-      constexpr int CH = D / 8, RPI = 32 / CH;               // chunks a row, rows an instruction
-      const int c = lane % CH, r0 = lane / CH;
+      const int key0 = in.sp.tile(in.i) << KL, slot = n % NST;
+      const uint32_t dst = ring + slot * (2 * S::PART) + lane_dst;
+      if (lane == 0) {
+        note[slot] = Slab{key0, in.i, in.sp.n, in.h * p.hp + sub, in.rt, in.s.q0, in.s.nq, in.s.len};
+      }
 #pragma unroll
-      for (int i = 0; i < 16 / RPI; ++i) {
-        const int r = i * RPI + r0;
-        const long long off = r < rows ? base + r * p.token_stride + c * 8 : 0;
-        const uint32_t d = dst + r * (D * 2) + ((c ^ (r & 7)) << 4);
-        cp_async16(d, static_cast<const uint16_t *>(p.k) + off, r < rows ? 16u : 0u);
-        cp_async16(d + S::SLAB, static_cast<const uint16_t *>(p.v) + off, r < rows ? 16u : 0u);
+      for (int j = 0; j < NSUB; ++j) {
+        const int k0 = key0 + 16 * j;
+        const bool good = page[j] >= 0 && page[j] < p.n_pages;
+        if (!good && page[j] != NOT_SEEN && lane == 0) paged_fail(p, ATTN_ERR_INVALID_ARG);
+        const int left = good ? in.s.len - k0 - fr : -64;   // of this lane's rows; those behind the end read as zeros
+        const long long at = good ? (page[j] * p.page_stride + (k0 & page_mask) * p.token_stride + (in.h * p.hp + sub) * p.head_stride) * 2 : 0;
+        const char *ks = kbase + at, *vs = vbase + at;
+#pragma unroll
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const int r = i * RPI;
+          const uint32_t d = (dst ^ ((r & 7) << 4)) + (16 * j + r) * (D * 2);
+          const bool live = r < left;
+          cp_async16(d, live ? ks + i * row_step : p.k, live ? 16u : 0u);
+          cp_async16(d + S::PART, live ? vs + i * row_step : p.v, live ? 16u : 0u);
+        }
       }
       if (n + 1 < cnt) {
         in.next(p, first, info, 0);
-        page = page_of(in);
+        if (in.i == 0) bounds();
+        look_up();
       }
     }
     cp_commit();
   };
-#pragma unroll
+#pragma unroll 1
   for (int n = 0; n < NST - 1; ++n) fetch(n);
 
   uint32_t qf[D / 16][4];
@@ -145,42 +191,47 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
   int rows_here = 0, piece0 = 0;
   const float sl2 = p.scale_log2;
   const int lr = lane >> 2, lc = (lane & 3) * 2;
+  // this lane's places in the keys and (transposed) the values of a slab
+  const uint32_t k_place = (((lane >> 4) << 3) + (lane & 7)) * (D * 2) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+  const uint32_t v_place = ((((lane >> 3) & 1) << 3) + (lane & 7)) * (D * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
 
+#pragma unroll 1
   for (int n = 0; n < cnt; ++n) {
     cp_wait<NST - 2>();
     __syncwarp();
     fetch(n + NST - 1);
-    if (n == 0 || at.i == 0) {
+    const Slab &sl = note[n % NST];
+    const int key0 = sl.key0, tile_i = sl.i, tile_n = sl.n;
+    if (n == 0 || tile_i == 0) {
       // a new item: its rows of Q as matrix fragments, summaries empty
-      piece0 = at.i;
-      rows_here = min(PR_ROWS, at.s.nq * p.G - at.rt * PR_ROWS);
+      const int rt = sl.rt, q0 = sl.q0, nq = sl.nq, len = sl.len, h = sl.h;
+      piece0 = tile_i;
+      rows_here = min(PR_ROWS, nq * p.G - rt * PR_ROWS);
       auto place = [&](int r, long long &row, int &pos, int &lo) {
         row = -1;
         pos = -1;
         lo = 0;
         if (r < rows_here) {
-          const int x = at.rt * PR_ROWS + r, t = x / p.G;
-          row = static_cast<long long>(at.s.q0 + t) * p.hq + at.h * p.G + x - t * p.G;
-          pos = p.causal ? at.s.len - at.s.nq + t : at.s.len - 1;
+          const int x = rt * PR_ROWS + r, t = x / p.G;
+          row = static_cast<long long>(q0 + t) * p.hq + h * p.G + x - t * p.G;
+          pos = p.causal ? len - nq + t : len - 1;
           lo = p.causal && p.window > 0 ? pos - p.window + 1 : 0;
         }
       };
       place(lr, row0, pos0, lo0);
       place(lr + 8, row1, pos1, lo1);
-      {
-        int t0, t1;
-        tile_tokens<PR_ROWS>(at.rt, at.s.nq, p.G, 0, t0, t1);
-        all_hi = p.causal ? at.s.len - at.s.nq + t0 + 1 : at.s.len;
-        all_lo = p.causal && p.window > 0 ? at.s.len - at.s.nq + t1 - p.window + 1 : 0;
-      }
-      const uint16_t *q0 = static_cast<const uint16_t *>(p.q) + (row0 < 0 ? 0 : row0) * D + lc;
-      const uint16_t *q1 = static_cast<const uint16_t *>(p.q) + (row1 < 0 ? 0 : row1) * D + lc;
+      int t0, t1;
+      tile_tokens<PR_ROWS>(rt, nq, p.G, 0, t0, t1);
+      all_hi = p.causal ? len - nq + t0 + 1 : len;
+      all_lo = p.causal && p.window > 0 ? len - nq + t1 - p.window + 1 : 0;
+      const uint16_t *qa = static_cast<const uint16_t *>(p.q) + (row0 < 0 ? 0 : row0) * D + lc;
+      const uint16_t *qb = static_cast<const uint16_t *>(p.q) + (row1 < 0 ? 0 : row1) * D + lc;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        qf[k][0] = row0 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(q0 + k * 16));
-        qf[k][1] = row1 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(q1 + k * 16));
-        qf[k][2] = row0 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(q0 + k * 16 + 8));
-        qf[k][3] = row1 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(q1 + k * 16 + 8));
+        qf[k][0] = row0 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(qa + k * 16));
+        qf[k][1] = row1 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(qb + k * 16));
+        qf[k][2] = row0 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(qa + k * 16 + 8));
+        qf[k][3] = row1 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(qb + k * 16 + 8));
       }
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.f;
@@ -189,35 +240,43 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
     }
-    const uint32_t ks = ring + (n % NST) * (2 * S::SLAB), vs = ks + S::SLAB;
-    const int key0 = at.sp.tile(at.i) << PR_KL;
-    // S = Q K^T: 16 rows x 16 keys
-    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-    {
-      const int r = ((lane >> 4) << 3) + (lane & 7), cb = (lane >> 3) & 1;
+    const uint32_t ks = ring + (n % NST) * (2 * S::PART), vs = ks + S::PART;
+    // S = Q K^T: 16 rows x KEYS keys, in blocks of 8 keys; x[b][0..1] row lr, x[b][2..3] row lr + 8
+    float x[NB][4];
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[b][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+#pragma unroll
+      for (int j = 0; j < NSUB; ++j) {
         uint32_t b[4];
-        ldsm4(ks + r * (D * 2) + (((2 * k + cb) ^ (r & 7)) << 4), b);
-        mma16816(s0, qf[k], b[0], b[1]);
-        mma16816(s1, qf[k], b[2], b[3]);
+        ldsm4(((ks + k_place) ^ (k << 5)) + j * 16 * (D * 2), b);
+        mma16816(x[2 * j], qf[k], b[0], b[1]);
+        mma16816(x[2 * j + 1], qf[k], b[2], b[3]);
       }
     }
-    float x[8] = {s0[0] * sl2, s0[1] * sl2, s1[0] * sl2, s1[1] * sl2,     // row lr
-                  s0[2] * sl2, s0[3] * sl2, s1[2] * sl2, s1[3] * sl2};    // row lr + 8
-    if (key0 + 16 > all_hi || (key0 < all_lo && key0 + 16 > p.sinks)) {
+    if (key0 + KEYS > all_hi || (key0 < all_lo && key0 + KEYS > p.sinks)) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = key0 + (e >> 1) * 8 + lc + (e & 1);
-        if (!(j <= pos0 && (j >= lo0 || j < p.sinks))) x[e] = -INFINITY;
-        if (!(j <= pos1 && (j >= lo1 || j < p.sinks))) x[4 + e] = -INFINITY;
-      }
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = key0 + b * 8 + lc + e;
+          if (!(j <= pos0 && (j >= lo0 || j < p.sinks))) x[b][e] = -INFINITY;
+          if (!(j <= pos1 && (j >= lo1 || j < p.sinks))) x[b][2 + e] = -INFINITY;
+        }
     }
-    float a0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), a1 = fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]));
+    float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      a0 = max3f(a0, x[b][0], x[b][1]);
+      a1 = max3f(a1, x[b][2], x[b][3]);
+    }
     a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
     a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
-    a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
-    a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
+    a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2)) * sl2;
+    a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2)) * sl2;
     const bool g0 = a0 > m0 + PR_TAU, g1 = a1 > m1 + PR_TAU;
     if (__any_sync(0xffffffffu, g0 || g1)) {
       const float f0 = g0 ? ex2_approx(m0 - a0) : 1.f, f1 = g1 ? ex2_approx(m1 - a1) : 1.f;
@@ -233,28 +292,30 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
         o[j][3] *= f1;
       }
     }
-    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+    const float b0 = m0 == -INFINITY ? 0.f : -m0, b1 = m1 == -INFINITY ? 0.f : -m1;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = ex2_approx(x[e] - b0);
-      x[4 + e] = ex2_approx(x[4 + e] - b1);
+    for (int b = 0; b < NB; ++b) {
+      x[b][0] = ex2_approx(fmaf(x[b][0], sl2, b0));
+      x[b][1] = ex2_approx(fmaf(x[b][1], sl2, b0));
+      x[b][2] = ex2_approx(fmaf(x[b][2], sl2, b1));
+      x[b][3] = ex2_approx(fmaf(x[b][3], sl2, b1));
+      l0 += x[b][0] + x[b][1];
+      l1 += x[b][2] + x[b][3];
     }
-    l0 += (x[0] + x[1]) + (x[2] + x[3]);
-    l1 += (x[4] + x[5]) + (x[6] + x[7]);
-    const uint32_t pf[4] = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[2], x[3]),
-                            pack_bf16x2(x[6], x[7])};
     // O += P V
-    {
-      const int r = (((lane >> 3) & 1) << 3) + (lane & 7), cb = lane >> 4;
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
+    for (int j = 0; j < NSUB; ++j) {
+      const uint32_t pf[4] = {pack_bf16x2(x[2 * j][0], x[2 * j][1]), pack_bf16x2(x[2 * j][2], x[2 * j][3]),
+                              pack_bf16x2(x[2 * j + 1][0], x[2 * j + 1][1]), pack_bf16x2(x[2 * j + 1][2], x[2 * j + 1][3])};
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
         uint32_t b[4];
-        ldsm4t(vs + r * (D * 2) + (((2 * j + cb) ^ (r & 7)) << 4), b);
-        mma16816(o[2 * j], pf, b[0], b[1]);
-        mma16816(o[2 * j + 1], pf, b[2], b[3]);
+        ldsm4t(((vs + v_place) ^ (c << 5)) + j * 16 * (D * 2), b);
+        mma16816(o[2 * c], pf, b[0], b[1]);
+        mma16816(o[2 * c + 1], pf, b[2], b[3]);
       }
     }
-    const bool ends = at.i == at.sp.n - 1;
+    const bool ends = tile_i == tile_n - 1;
     if (ends || n == cnt - 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
       l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
@@ -262,22 +323,16 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
       l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
       if (p.rec && piece0 == 0 && lc == 0) {
         int np, slot0;
-        item_pieces(from + n - at.i, at.sp.n, worker, span, from, np, slot0);
+        item_pieces(from + n - tile_i, tile_n, mine, span, from, np, slot0);
         if (row0 >= 0) p.rec[row0] = Rec4{static_cast<int>(worker), slot0, np, lr};
         if (row1 >= 0) p.rec[row1] = Rec4{static_cast<int>(worker), slot0, np, lr + 8};
       }
-      if (ends && piece0 == 0) {
+      const bool whole = ends && piece0 == 0;
+      if (whole && !p.rec) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const long long row = u ? row1 : row0;
           if (row < 0) continue;
-          if (p.rec) {
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-              *reinterpret_cast<float2 *>(p.dense_o + row * D + j * 8 + lc) = make_float2(o[j][2 * u], o[j][2 * u + 1]);
-            if (lc == 0) *reinterpret_cast<float2 *>(p.dense_ml + row * 2) = make_float2(u ? m1 : m0, u ? l1 : l0);
-            continue;
-          }
           float fo, lse;
           row_final(u ? m1 : m0, u ? l1 : l0, fo, lse);
 #pragma unroll
@@ -288,30 +343,29 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
           }
         }
       } else {
-        // slot 0: the piece a span begins with; slot 1: one that begins in it and goes on
-        const long long slot = worker * 2 + (n - (at.i - piece0) == 0 ? 0 : 1);
+        // to the dense arrays, or to a piece: slot 0 the one a span begins
+        // with, slot 1 one that begins in it and goes on
+        const long long slot = worker * 2 + (n - (tile_i - piece0) == 0 ? 0 : 1);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           if (lr + 8 * u >= rows_here) continue;
-          const long long r = slot * PR_ROWS + lr + 8 * u;
+          const long long r = whole ? (u ? row1 : row0) : slot * PR_ROWS + lr + 8 * u;
+          float *po = (whole ? p.dense_o : p.part_o) + r * D + lc;
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j)
-            *reinterpret_cast<float2 *>(p.part_o + r * D + j * 8 + lc) = make_float2(o[j][2 * u], o[j][2 * u + 1]);
-          if (lc == 0)
-            *reinterpret_cast<float2 *>(p.part_ml + r * 2) = make_float2(u ? m1 : m0, u ? l1 : l0);
+          for (int j = 0; j < D / 8; ++j) *reinterpret_cast<float2 *>(po + j * 8) = make_float2(o[j][2 * u], o[j][2 * u + 1]);
+          if (lc == 0) *reinterpret_cast<float2 *>((whole ? p.dense_ml : p.part_ml) + r * 2) = make_float2(u ? m1 : m0, u ? l1 : l0);
         }
       }
     }
-    if (n + 1 < cnt) at.next(p, first, info, 0);
   }
-  if (lane == 0 && !p.rec) leave_cut<PR_ROWS, PR_KL>(p, at, 0, worker, span, from, to);
+  if (lane == 0 && !p.rec) leave_cut<PR_ROWS, KL>(p, in, 0, in.h * p.hp + sub, worker, mine, span, from, to);
   if (p.wait_end) after_previous();
 }
 
 // ---------------------------------------------------------------------- host
 
 template <int D, int NST>
-static int launch_rows(PagedParams p, cudaStream_t s) {
+static int launch_rows(PagedParams &p, cudaStream_t s) {
   using S = RowsSmem<D, NST>;
   constexpr int kDev = 64;
   static bool done[kDev] = {};
@@ -326,13 +380,16 @@ static int launch_rows(PagedParams p, cudaStream_t s) {
   }
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  p.n_workers = sms * S::W;
+  // as many heads side by side as divide both the heads and a CTA's warps
+  p.hp = 1;
+  while (p.hp < S::W && p.hk % (2 * p.hp) == 0) p.hp *= 2;
+  p.n_spans = sms * S::W / p.hp;
   p.min_span = 2;
   const int rc = launch_after(kern, dim3(sms), S::W * 32, S::bytes(p.n_seqs), s, p);
   if (rc != ATTN_OK || p.rec) return rc;
   // few items: each has many pieces, and its rows go to blocks of their own
   const long long items = static_cast<long long>(p.n_seqs) * p.hk;
-  return launch_after(join, dim3(p.n_workers, items * 8 < p.n_workers ? 4 : 1), 256, 0, s, p);
+  return launch_after(join, dim3(sms * S::W, items * 8 < sms * S::W ? 4 : 1), 256, 0, s, p);
 }
 
 // Floats of all workers' pieces of `tile_rows` rows.
@@ -346,14 +403,14 @@ size_t paged_rows_workspace(int d) {
   return static_cast<size_t>(sms) * rows_warps(d) * (2 * PR_ROWS * (d + 2) * sizeof(float) + sizeof(Cut));
 }
 
-int paged_rows_launch(PagedParams p, int d, cudaStream_t s) {
+int paged_rows_launch(PagedParams &p, int d, cudaStream_t s) {
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   p.part_ml = p.part_o + paged_piece_floats(PR_ROWS, d);
   p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * rows_warps(d) * 2 * PR_ROWS * 2);
   if (d == 128)
     return RowsSmem<128, 3>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<128, 3>(p, s) : launch_rows<128, 2>(p, s);
-  return RowsSmem<64, 4>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<64, 4>(p, s) : launch_rows<64, 2>(p, s);
+  return RowsSmem<64, 3>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<64, 3>(p, s) : launch_rows<64, 2>(p, s);
 }
 
 }  // namespace attn

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       if (!ok) break;
       at += i1 - w.i;
       w.i = i1 - 1;
-      if (at == to && lane == 0 && !p.rec) leave_cut<0, PT_KL>(p, w, tpi, blockIdx.x, span, from, to);
+      if (at == to && lane == 0 && !p.rec) leave_cut<0, PT_KL>(p, w, tpi, w.h, blockIdx.x, blockIdx.x, span, from, to);
       if (at < to) w.next(p, first, nullptr, tpi);
     }
     if (*abort && lane == 0) {
@@ -542,7 +542,7 @@ int encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, c
 }
 
 template <int D, int TILES>
-int launch_tiles(PagedParams p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
+int launch_tiles(PagedParams &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
   using L = TileLayout<D, TILES>;
   constexpr int kDev = 64;
   static bool done[kDev] = {};
@@ -557,7 +557,8 @@ int launch_tiles(PagedParams p, const CUtensorMap &mq, const CUtensorMap &mk, co
   }
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  p.n_workers = sms;
+  p.hp = 1;
+  p.n_spans = sms;
   p.min_span = 2;
   p.part_ml = p.part_o + paged_piece_floats(TILES * 128, D);
   p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * 2 * TILES * 128 * 2);
@@ -576,7 +577,7 @@ size_t paged_tiles_workspace(int d) {
 
 // UNSUPPORTED, with nothing launched, where the tensor maps cannot say the
 // layout (more than 128 query heads a key/value head, strides of zero).
-int paged_tiles_launch(const PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
+int paged_tiles_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
   if (p.G > 128) return ATTN_ERR_UNSUPPORTED;
   const int page = 1 << p.page_shift, tpt = 128 / p.G;
   CUtensorMap mq, mk, mv;

@@ -32,21 +32,28 @@ def oracle_paged(q, k_pages, v_pages, table, seq_lens, q_ptr, scale, window=0, s
                     m = int(plens[g])
                     k, v = (np.concatenate([cached_rows(x, ptable[g], m), y])
                             for x, y in ((k_pages, k), (v_pages, v)))
-        for t in range(new):
-            i = n - new + t
-            j = np.arange(n)
-            own = (j <= i) & ((j > i - window) | (j < sinks)) if window else j <= i
-            seen = np.concatenate([np.ones(m, bool), own])
-            row = int(q_ptr[b]) + t
-            for h in range(H):
-                kk, vv = k[seen][:, h // (H // hk)], v[seen][:, h // (H // hk)]
-                if len(kk) == 0:
-                    O[row, h], lse[h, row] = 0.0, -np.inf
-                    continue
-                s = kk @ q[row, h] * scale
-                top = s.max()
-                p = np.exp(s - top)
-                O[row, h], A[row, h] = p @ vv / p.sum(), p @ np.abs(vv) / p.sum()
-                lse[h, row] = top + np.log(p.sum())
-                big[h, row] = (np.abs(kk) @ np.abs(q[row, h])).max() * scale
+        if new == 0:
+            continue
+        i = np.arange(n - new, n)[:, None]
+        j = np.arange(n)[None]
+        own = (j <= i) & ((j > i - window) | (j < sinks)) if window else j <= i
+        seen = np.concatenate([np.ones((new, m), bool), own], 1)
+        some = seen.any(1)
+        rows = slice(int(q_ptr[b]), int(q_ptr[b + 1]))
+        O[rows], lse[:, rows] = 0.0, -np.inf
+        if not some.any():
+            continue
+        used = seen.any(0)                    # what no row sees takes no part, whatever it is
+        seen, kk, vv = seen[some][:, used], k[used], v[used]
+        for h in range(H):
+            g = h // (H // hk)
+            qq = q[rows][some, h]
+            s = np.where(seen, qq @ kk[:, g].T * scale, -np.inf)
+            top = s.max(1, keepdims=True)
+            p = np.exp(s - top)
+            total = p.sum(1, keepdims=True)
+            O[rows][some, h] = p @ vv[:, g] / total
+            A[rows][some, h] = p @ np.abs(vv[:, g]) / total
+            lse[h, rows][some] = (top + np.log(total))[:, 0]
+            big[h, rows][some] = np.where(seen, np.abs(qq) @ np.abs(kk[:, g]).T, 0.0).max(1) * scale
     return O, lse, A, big

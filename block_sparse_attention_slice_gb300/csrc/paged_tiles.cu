@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const long long total = first[p.n_seqs], span = span_of(p, total);
-  const long long from = blockIdx.x * span, to = min(total, from + span);
+  const int mine = blockIdx.x / p.hp, sub = blockIdx.x - mine * p.hp;      // span, and head of a group
+  const long long from = mine < p.n_spans ? mine * span : total, to = min(total, from + span);
 
   if (warp == WP) {
     // -------------------------------------------------------------- producer
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         if (more) {
           s->tok0 = w.s.q0 + w.rt * tpi;
           s->ntok = min(tpi, w.s.nq - w.rt * tpi);
-          s->h = w.h;
+          s->h = w.h * p.hp + sub;
           s->pos0 = w.s.len - w.s.nq + w.rt * tpi;
           s->len = w.s.len;
           s->ns = w.sp.ns;
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           s->i1 = i1;
           s->out = w.i == 0 && i1 == w.sp.n ? 0 : at == from ? 1 : 2;
           int np, slot0;
-          item_pieces(at - w.i, w.sp.n, blockIdx.x, span, from, np, slot0);
+          item_pieces(at - w.i, w.sp.n, mine, span, from, np, slot0);
           s->np = np;
           s->slot0 = slot0;
         } else {
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         mbar_arrive_expect_tx(bar(L::B_Q), TILES * L::NHALF * tpt * p.G * 128);
         for (int t = 0; t < TILES; ++t)
           for (int hh = 0; hh < L::NHALF; ++hh)
-            tma_load_3d(q_smem + t * L::TILE + hh * L::HALF, &tm_q, bar(L::B_Q), hh * 64, w.h * p.G, tok0 + t * tpt);
+            tma_load_3d(q_smem + t * L::TILE + hh * L::HALF, &tm_q, bar(L::B_Q), hh * 64, (w.h * p.hp + sub) * p.G, tok0 + t * tpt);
       }
       ++nseg;
       // keys that some row sees: below `end`, at least `lo` or a first token
@@ -214,13 +215,13 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           if (lane < ppt)
             for (int hh = 0; hh < L::NHALF; ++hh)
               tma_load_4d(kv_smem + slot * L::TILE + hh * L::HALF + lane * R * 128, kv ? &tm_v : &tm_k,
-                          bar(L::B_FULL + slot), hh * 64, tok, w.h, page);
+                          bar(L::B_FULL + slot), hh * 64, tok, w.h * p.hp + sub, page);
         }
       }
       if (!ok) break;
       at += i1 - w.i;
       w.i = i1 - 1;
-      if (at == to && lane == 0 && !p.rec) leave_cut<0, PT_KL>(p, w, tpi, w.h, blockIdx.x, blockIdx.x, span, from, to);
+      if (at == to && lane == 0 && !p.rec) leave_cut<0, PT_KL>(p, w, tpi, w.h * p.hp + sub, blockIdx.x, mine, span, from, to);
       if (at < to) w.next(p, first, nullptr, tpi);
     }
     if (*abort && lane == 0) {
@@ -557,8 +558,10 @@ int launch_tiles(PagedParams &p, const CUtensorMap &mq, const CUtensorMap &mk, c
   }
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
+  // heads side by side while that leaves no more than a few SMs idle
   p.hp = 1;
-  p.n_spans = sms;
+  while (p.hp < 8 && p.hk % (2 * p.hp) == 0 && sms % (2 * p.hp) <= sms / 32) p.hp *= 2;
+  p.n_spans = sms / p.hp;
   p.min_span = 2;
   p.part_ml = p.part_o + paged_piece_floats(TILES * 128, D);
   p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * 2 * TILES * 128 * 2);

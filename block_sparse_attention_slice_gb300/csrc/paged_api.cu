@@ -137,7 +137,7 @@ size_t pieces_bytes(int d) { return up256(std::max(paged_rows_workspace(d), page
 // attn_prefix_fwd's workspace: for each of the two passes where every row's
 // pieces are, the rows finished within a span, and the pieces.
 struct PairLayout {
-  size_t rec[2], ml[2], o[2], pieces[2], rec_bytes, total;
+  size_t rec[2], ml[2], o[2], pieces[2], total;
 };
 PairLayout pair_layout(int n_tokens, int hq, int d) {
   PairLayout L;
@@ -149,7 +149,6 @@ PairLayout pair_layout(int n_tokens, int hq, int d) {
     return x;
   };
   for (size_t &x : L.rec) x = put(rows * sizeof(Rec4));
-  L.rec_bytes = at;
   for (size_t &x : L.ml) x = put(rows * 8);
   for (size_t &x : L.o) x = put(rows * d * 4);
   for (size_t &x : L.pieces) x = put(pieces_bytes(d));
@@ -237,7 +236,6 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
   p.causal = 0;
   p.status = status;
   const PairLayout L = pair_layout(n_tokens, hq, pages->d);
-  JoinPair pair;
   PagedParams *pass[2] = {&p, &r};
   for (int i = 0; i < 2; ++i) {
     pass[i]->rec = reinterpret_cast<Rec4 *>(ws + L.rec[i]);
@@ -248,21 +246,13 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
   // neither pass reads what the other writes: the second starts on each SM as
   // the first leaves it, and waits for its end before its own
   r.wait_end = 1;
-  if (cudaMemsetAsync(ws, 0xff, L.rec_bytes, s) != cudaSuccess) return ATTN_ERR_CUDA;
-  if ((rc = paged_launch(p, pages->d, (n_tokens + prefix->n_seqs - 1) / prefix->n_seqs, s, &pair.tile_rows[0])) != ATTN_OK ||
-      (rc = paged_launch(r, pages->d, tokens, s, &pair.tile_rows[1])) != ATTN_OK)
+  int pre_rows;
+  if ((rc = paged_launch(p, pages->d, (n_tokens + prefix->n_seqs - 1) / prefix->n_seqs, s, &pre_rows)) != ATTN_OK ||
+      (rc = paged_launch(r, pages->d, tokens, s, &tile_rows)) != ATTN_OK)
     return rc;
-  for (int i = 0; i < 2; ++i) {
-    pair.rec[i] = pass[i]->rec;
-    pair.dense_ml[i] = pass[i]->dense_ml;
-    pair.dense_o[i] = pass[i]->dense_o;
-    pair.part_o[i] = pass[i]->part_o;
-    pair.part_ml[i] = pass[i]->part_ml;
-    pair.hp[i] = pass[i]->hp;
-  }
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n_tokens) * hq + 7) / 8));
-  return pages->d == 128 ? launch_after(paged_join_pair_kernel<128>, grid, 256, 0, s, r, pair)
-                         : launch_after(paged_join_pair_kernel<64>, grid, 256, 0, s, r, pair);
+  auto join = pages->d == 128 ? paged_join_pair_kernel<128> : paged_join_pair_kernel<64>;
+  return launch_after(join, grid, 256, 0, s, p, r, pre_rows, tile_rows);
 }
 
 int attn_slices_from_windows(const int32_t *h_lengths, int n, int window, int sinks, attn_slice_t *h_out,

@@ -77,7 +77,7 @@ struct Gather {
 // PACKED: rows stand as they are counted; else 128 / G whole tokens to each
 // 128 rows.
 template <int D, int TILE_ROWS, bool PACKED>
-__global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(256, 3) paged_join_kernel(const PagedParams p) {
   constexpr int NW = 8, V = D / 32;
   __shared__ float red[NW][D + 4];
   admit_next();
@@ -136,53 +136,75 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   }
 }
 
-// Merges the pieces of two passes over the same rows: a warp a row.
-struct JoinPair {
-  const Rec4 *rec[2];
-  const float *dense_o[2], *dense_ml[2], *part_o[2], *part_ml[2];
-  int tile_rows[2], hp[2];
-};
+// The largest i < n with a[i] <= x, where a does not decrease; 0 if there is none.
+__device__ __forceinline__ int last_not_above(const int32_t *a, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a + mid) <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Merges what two passes over the same rows left, the prefix's and that of
+// what follows it: a warp a row.  A row's records were written in this call
+// exactly if the row belongs to a sequence (and to a group), which is looked
+// up here, while the passes still run, rather than having the records cleared
+// before them.
 template <int D>
-__global__ void __launch_bounds__(256) paged_join_pair_kernel(const PagedParams p, const JoinPair q) {
+__global__ void __launch_bounds__(256, 4) paged_join_pair_kernel(const PagedParams pre, const PagedParams p,
+                                                                 const int pre_rows, const int rows) {
   constexpr int V = D / 32;
   admit_next();
-  after_previous();
   const int lane = threadIdx.x & 31;
   const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.n_tokens) * p.hq) return;
-  const Rec4 a = q.rec[0][row], b = q.rec[1][row];
-  if (b.np == -1) return;                          // of no sequence: left as it is
+  const int t = static_cast<int>(row / p.hq);
+  bool mine = false, grouped = false;
+  if (t < p.n_tokens) {
+    const int b = p.q_ptr ? last_not_above(p.q_ptr, p.n_seqs, t) : t;
+    const SeqInfo s = seq_info(p, b);
+    mine = t >= s.q0 && t < s.q0 + s.nq;
+    const SeqInfo g = seq_info(pre, last_not_above(pre.group_ptr, pre.n_seqs, b));
+    grouped = t >= g.q0 && t < g.q0 + g.nq;
+  }
+  after_previous();
+  if (!mine) return;                               // of no sequence: left as it is
+  Rec4 a{0, 0, REC_EMPTY, 0};
+  if (grouped) a = pre.rec[row];
+  const Rec4 b = p.rec[row];
   const int na = a.np < 0 ? 0 : a.np ? a.np : 1, nb = b.np < 0 ? 0 : b.np ? b.np : 1, np = na + nb;
   // row of piece i in its pass's pieces, or (np = 0) in the dense arrays
-  auto place = [&](int i, int &x, bool &dense) -> long long {
-    x = i < na ? 0 : 1;
-    const Rec4 &r = x ? b : a;
-    const int k = x ? i - na : i;
+  auto place = [&](int i, bool &first, bool &dense) -> long long {
+    first = i < na;
+    const Rec4 &r = first ? a : b;
+    const int k = first ? i : i - na;
     dense = r.np == 0;
     if (dense) return row;
-    return ((static_cast<long long>(r.worker) + k * q.hp[x]) * 2 + (k == 0 ? r.slot0 : 0)) * q.tile_rows[x] + r.row;
+    return ((static_cast<long long>(r.worker) + k * (first ? pre.hp : p.hp)) * 2 + (k == 0 ? r.slot0 : 0)) *
+               (first ? pre_rows : rows) + r.row;
   };
   Gather<D> g;
   for (int base = 0; base < np; base += 32) {
     float2 ml = make_float2(-INFINITY, 0.f);
     if (base + lane < np) {
-      int x;
-      bool dense;
-      const long long at = place(base + lane, x, dense);
-      ml = *reinterpret_cast<const float2 *>((dense ? q.dense_ml[x] : q.part_ml[x]) + at * 2);
+      bool first, dense;
+      const long long at = place(base + lane, first, dense);
+      const PagedParams &x = first ? pre : p;
+      ml = *reinterpret_cast<const float2 *>((dense ? x.dense_ml : x.part_ml) + at * 2);
     }
     g.add(min(32, np - base), ml, [&](int k) -> const float * {
-      int x;
-      bool dense;
-      const long long at = place(base + k, x, dense);
-      return (dense ? q.dense_o[x] : q.part_o[x]) + at * D;
+      bool first, dense;
+      const long long at = place(base + k, first, dense);
+      const PagedParams &x = first ? pre : p;
+      return (dense ? x.dense_o : x.part_o) + at * D;
     });
   }
   float fo, lse;
   row_final(g.m, g.l, fo, lse);
 #pragma unroll
   for (int c = 0; c < V; c += 2) store_pair<D>(p, row, lane * V + c, g.acc[c] * fo, g.acc[c + 1] * fo);
-  if (lane == 0) p.lse[row % p.hq * p.n_tokens + row / p.hq] = lse;
+  if (lane == 0) p.lse[(row - static_cast<long long>(t) * p.hq) * p.n_tokens + t] = lse;
 }
 
 }  // namespace attn

@@ -36,12 +36,11 @@ struct __align__(16) Cut {
 
 // Where a row's pieces are: np > 0 pieces, the first at row `row` of slot slot0
 // of worker `worker`, the others at that row of the first slots of every hp-th
-// worker that follows; np = 0: the dense arrays; REC_EMPTY: it sees nothing; -1 (the
-// arrays are filled with all bits set beforehand): it is no row of the pass.
+// worker worker that follows; np = 0: the dense arrays; REC_EMPTY: it sees nothing.
 struct __align__(16) Rec4 {
   int worker, slot0, np, row;
 };
-constexpr int REC_EMPTY = -2;
+constexpr int REC_EMPTY = -1;
 
 struct PagedParams {
   const void *q, *k, *v;
@@ -324,26 +323,6 @@ __device__ __forceinline__ void store_pair(const PagedParams &p, long long row, 
     *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at) = make_float2(x, y);
   else
     *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + at) = pack_bf16x2(x, y);
-}
-
-// Writes columns c .. c + 31 of a finished row, as one thread holds them.
-template <int D>
-__device__ __forceinline__ void store_32(const PagedParams &p, long long row, int c, const uint32_t (&y)[32], float fo) {
-  const long long at = row * D + c;
-  float x[32];
-#pragma unroll
-  for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(y[k]) * fo;
-  if (p.out_f32) {
-#pragma unroll
-    for (int k = 0; k < 32; k += 4)
-      *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 32; k += 8)
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at + k) =
-          make_uint4(pack_bf16x2(x[k], x[k + 1]), pack_bf16x2(x[k + 2], x[k + 3]), pack_bf16x2(x[k + 4], x[k + 5]),
-                     pack_bf16x2(x[k + 6], x[k + 7]));
-  }
 }
 
 // Pieces of the item that starts at flat index f0 in span `at`, [from, ..): their number, and the slot of the first (np = 0: it ends there).

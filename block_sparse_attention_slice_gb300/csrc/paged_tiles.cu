@@ -60,6 +60,28 @@ struct TileLayout {
   static_assert(MISC_OFF % 8 == 0, "alignment");
 };
 
+// Transposes 4 x 4 words of 16 bytes among four neighbouring lanes: lane q's
+// word k becomes lane k's word q.
+__device__ __forceinline__ void exchange4(uint4 (&w)[4], int q) {
+#pragma unroll
+  for (int s = 1; s < 4; s <<= 1) {
+    const bool up = q & s;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & s) continue;
+      uint4 &lo = w[k], &hi = w[k | s];
+      const uint4 give = up ? lo : hi;
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, give.x, s);
+      got.y = __shfl_xor_sync(0xffffffffu, give.y, s);
+      got.z = __shfl_xor_sync(0xffffffffu, give.z, s);
+      got.w = __shfl_xor_sync(0xffffffffu, give.w, s);
+      if (up) lo = got;
+      else hi = got;
+    }
+  }
+}
+
 // What the producer publishes of a segment: a run of key tiles of one item.
 struct Seg {
   int tok0, ntok, h, pos0, len, ns, w0, i0, i1;
@@ -487,32 +509,63 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       ++nseg;
       tc_fence_after();
       if (!idle) {
-        const long long row = static_cast<long long>(tok0 + tl) * p.hq + h * p.G + g;
-        if (p.rec && live && i0 == 0) p.rec[row] = Rec4{static_cast<int>(blockIdx.x), slot0, np, t * 128 + r};
-        if (out == 0 && !p.rec) {
-          float fo = 0.f, lse = 0.f;
-          if (live) {
+        // Four lanes exchange 16-byte words so that each row leaves in 64-byte
+        // runs: a lane alone has 16 bytes of 32 different rows an instruction,
+        // half sectors that L2 has to merge (4 us a segment instead of 1).
+        const int q4 = lane & 3;
+        const bool final = out == 0 && !p.rec, f32 = !final || p.out_f32;
+        float fo = 1.f, lse;
+        if (live) {
+          const long long row = static_cast<long long>(tok0 + tl) * p.hq + h * p.G + g;
+          if (final) {
             row_final(m_ref, l, fo, lse);
             p.lse[static_cast<long long>(h * p.G + g) * p.n_tokens + tok0 + tl] = lse;
+          } else {
+            const long long pr = (static_cast<long long>(blockIdx.x) * 2 + out - 1) * (TILES * 128) + t * 128 + r;
+            *reinterpret_cast<float2 *>(out ? p.part_ml + pr * 2 : p.dense_ml + row * 2) = make_float2(m_ref, l);
           }
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t y[32];
-            tmem_ld32_wait(tO + c * 32, y);
-            if (live) store_32<D>(p, row, c * 32, y, fo);
-          }
-        } else {
-          const long long pr = (static_cast<long long>(blockIdx.x) * 2 + out - 1) * (TILES * 128) + t * 128 + r;
-          float *po = out ? p.part_o + pr * D : p.dense_o + row * D, *pml = out ? p.part_ml + pr * 2 : p.dense_ml + row * 2;
-          if (live) *reinterpret_cast<float2 *>(pml) = make_float2(m_ref, l);
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t y[32];
-            tmem_ld32_wait(tO + c * 32, y);
-            if (!live) continue;
-            uint4 *dst = reinterpret_cast<uint4 *>(po + c * 32);
+          if (p.rec && i0 == 0) p.rec[row] = Rec4{static_cast<int>(blockIdx.x), slot0, np, t * 128 + r};
+        }
+        uint8_t *dst[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+        for (int k = 0; k < 4; ++k) {
+          const int x = r - q4 + k, xt = x / p.G;
+          const long long row = static_cast<long long>(tok0 + xt) * p.hq + h * p.G + x - xt * p.G;
+          const long long pr = (static_cast<long long>(blockIdx.x) * 2 + out - 1) * (TILES * 128) + t * 128 + x;
+          uint8_t *base = static_cast<uint8_t *>(final ? p.out : out ? static_cast<void *>(p.part_o) : static_cast<void *>(p.dense_o));
+          dst[k] = xt < ntok ? base + (out ? pr : row) * (D * (f32 ? 4 : 2)) + q4 * 16 : nullptr;
+        }
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t y[32];
+          tmem_ld32_wait(tO + c * 32, y);
+          if (f32) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint4 w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t *z = y + half * 16 + 4 * k;
+                w[k] = make_uint4(__float_as_uint(__uint_as_float(z[0]) * fo), __float_as_uint(__uint_as_float(z[1]) * fo),
+                                  __float_as_uint(__uint_as_float(z[2]) * fo), __float_as_uint(__uint_as_float(z[3]) * fo));
+              }
+              exchange4(w, q4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (dst[k]) *reinterpret_cast<uint4 *>(dst[k] + c * 128 + half * 64) = w[k];
+            }
+          } else {
+            uint4 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t *z = y + 8 * k;
+              auto two = [&](int e) { return pack_bf16x2(__uint_as_float(z[e]) * fo, __uint_as_float(z[e + 1]) * fo); };
+              w[k] = make_uint4(two(0), two(2), two(4), two(6));
+            }
+            exchange4(w, q4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (dst[k]) *reinterpret_cast<uint4 *>(dst[k] + c * 64) = w[k];
           }
         }
       }

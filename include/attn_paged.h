@@ -101,9 +101,9 @@ int attn_paged_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q,
  * sequence's keys j <= i as in attn_paged_fwd (seq_lens counts the tokens
  * behind the prefix).  A sequence before the first group or behind the last
  * has no prefix.  Each prefix is read once for its whole group.  Other
- * arguments, outputs and errors as in attn_paged_fwd; with a group_ptr that
- * decreases or leaves the batch (INVALID_ARG on the device) the outputs of the
- * groups' tokens mean nothing. */
+ * arguments, outputs and errors as in attn_paged_fwd; with a group_ptr or
+ * q_ptr that decreases or leaves the batch (INVALID_ARG on the device) the
+ * outputs mean nothing. */
 int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
                     const attn_pages_t *pages, const attn_seqs_t *prefix, const int32_t *group_ptr,
                     const attn_seqs_t *seqs, float scale, void *out, int out_dtype, float *lse,

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
   };
 #pragma unroll 1
   for (int n = 0; n < NST - 1; ++n) fetch(n);
+  __syncwarp();
 
   uint32_t qf[D / 16][4];
   float o[D / 8][4];
@@ -197,13 +198,11 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
 
 #pragma unroll 1
   for (int n = 0; n < cnt; ++n) {
-    cp_wait<NST - 2>();
-    __syncwarp();
-    fetch(n + NST - 1);
     const Slab &sl = note[n % NST];
     const int key0 = sl.key0, tile_i = sl.i, tile_n = sl.n;
     if (n == 0 || tile_i == 0) {
-      // a new item: its rows of Q as matrix fragments, summaries empty
+      // a new item: its rows of Q as matrix fragments, requested while its keys
+      // are on their way; summaries empty
       const int rt = sl.rt, q0 = sl.q0, nq = sl.nq, len = sl.len, h = sl.h;
       piece0 = tile_i;
       rows_here = min(PR_ROWS, nq * p.G - rt * PR_ROWS);
@@ -240,6 +239,9 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
     }
+    cp_wait<NST - 2>();
+    __syncwarp();
+    fetch(n + NST - 1);
     const uint32_t ks = ring + (n % NST) * (2 * S::PART), vs = ks + S::PART;
     // S = Q K^T: 16 rows x KEYS keys, in blocks of 8 keys; x[b][0..1] row lr, x[b][2..3] row lr + 8
     float x[NB][4];
@@ -384,7 +386,7 @@ static int launch_rows(PagedParams &p, cudaStream_t s) {
   p.hp = 1;
   while (p.hp < S::W && p.hk % (2 * p.hp) == 0) p.hp *= 2;
   p.n_spans = sms * S::W / p.hp;
-  p.min_span = 2;
+  p.min_span = 1;
   const int rc = launch_after(kern, dim3(sms), S::W * 32, S::bytes(p.n_seqs), s, p);
   if (rc != ATTN_OK || p.rec) return rc;
   // few items: each has many pieces, and its rows go to blocks of their own

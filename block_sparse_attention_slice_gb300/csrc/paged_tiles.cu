@@ -615,7 +615,7 @@ int launch_tiles(PagedParams &p, const CUtensorMap &mq, const CUtensorMap &mk, c
   p.hp = 1;
   while (p.hp < 8 && p.hk % (2 * p.hp) == 0 && sms % (2 * p.hp) <= sms / 32) p.hp *= 2;
   p.n_spans = sms / p.hp;
-  p.min_span = 2;
+  p.min_span = 1;
   p.part_ml = p.part_o + paged_piece_floats(TILES * 128, D);
   p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * 2 * TILES * 128 * 2);
   const int tpt = 128 / p.G;

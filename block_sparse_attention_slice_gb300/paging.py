@@ -12,6 +12,7 @@ stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 from typing import Sequence
 
@@ -104,7 +105,16 @@ def _borrowed(stream, *tensors):
                 x.record_stream(stream)
 
 
-def _attend(name, q, device, hk, d, q_ptr, n_seqs, max_q, out, lse, out_dtype, ws, stream, prefix):
+@functools.lru_cache(maxsize=1024)
+def _workspace(index, t, hq, d, prefix):
+    """Bytes of workspace of a call of these sizes on device `index`."""
+    nb = ctypes.c_size_t(0)
+    with torch.cuda.device(index):
+        B._check(B.load().attn_paged_workspace_bytes(t, hq, d, prefix, ctypes.byref(nb)), "attn_paged_workspace_bytes")
+    return nb.value
+
+
+def _attend(q, device, hk, d, q_ptr, n_seqs, max_q, out, lse, out_dtype, ws, stream, prefix):
     """Checks and outputs that both attention calls share: the C arguments before and behind their own."""
     if q.dtype is not _BF16 or q.dim() != 3 or q.device != device or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous bf16 [n_tokens, H, d] tensor on {device}")
@@ -116,7 +126,7 @@ def _attend(name, q, device, hk, d, q_ptr, n_seqs, max_q, out, lse, out_dtype, w
         raise ValueError("q_ptr must have one entry a sequence and one more")
     made = []
     if out is None:
-        out = torch.empty((t, hq, d), dtype=out_dtype or _BF16, device=device)
+        out = torch.empty_like(q, dtype=out_dtype)
         made.append(out)
     elif out.shape != q.shape or out.device != device or not out.is_contiguous() or out_dtype not in (None, out.dtype):
         raise ValueError("out must be a contiguous bf16 or f32 tensor like q")
@@ -128,13 +138,7 @@ def _attend(name, q, device, hk, d, q_ptr, n_seqs, max_q, out, lse, out_dtype, w
     elif lse.shape != (hq, t) or lse.dtype is not _F32 or lse.device != device or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous f32 [H, n_tokens] tensor")
     if ws is None:
-        nb = ctypes.c_size_t(0)
-        if torch.cuda.current_device() == device.index:
-            B._check(B.load().attn_paged_workspace_bytes(t, hq, d, prefix, ctypes.byref(nb)), "attn_paged_workspace_bytes")
-        else:
-            with torch.cuda.device(device):
-                B._check(B.load().attn_paged_workspace_bytes(t, hq, d, prefix, ctypes.byref(nb)), "attn_paged_workspace_bytes")
-        ws = torch.empty(nb.value, dtype=torch.uint8, device=device)
+        ws = torch.empty(_workspace(device.index, t, hq, d, prefix), dtype=torch.uint8, device=device)
         made.append(ws)
     elif ws.device != device or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on the queries' device")
@@ -160,7 +164,7 @@ def attn_paged_fwd(q, k_pages, v_pages, table, seq_lens, scale: float, q_ptr=Non
     sequence and only picks the kernel."""
     pages, device, hk, d = _pages(k_pages, v_pages)
     rows, n = _seqs(device, table, seq_lens, seqs)
-    out, lse, before, behind = _attend("attn_paged_fwd", q, device, hk, d, q_ptr, n, max_q, out, lse, out_dtype, ws, stream, 0)
+    out, lse, before, behind = _attend(q, device, hk, d, q_ptr, n, max_q, out, lse, out_dtype, ws, stream, 0)
     _call(device, stream, "attn_paged_fwd", *before, pages, rows, scale, window, sinks, *behind)
     return out, lse
 
@@ -178,7 +182,7 @@ def attn_prefix_fwd(q, k_pages, v_pages, prefix_table, prefix_lens, group_ptr, t
     first = _ints(device, "group_ptr", group_ptr)
     if group_ptr.shape[0] != groups + 1:
         raise ValueError("group_ptr must have one entry a prefix and one more")
-    out, lse, before, behind = _attend("attn_prefix_fwd", q, device, hk, d, q_ptr, n, max_q, out, lse, out_dtype, ws, stream, 1)
+    out, lse, before, behind = _attend(q, device, hk, d, q_ptr, n, max_q, out, lse, out_dtype, ws, stream, 1)
     _call(device, stream, "attn_prefix_fwd", *before, pages, pre, first, rows, scale, *behind)
     return out, lse
 

@@ -13,11 +13,44 @@ namespace attn {
 // A running summary over pieces, held by one warp: lane's V columns of O.
 template <int D>
 struct Gather {
-  static constexpr int V = D / 32, BATCH = 8;
+  static constexpr int V = D / 32, BATCH = 4;
   float m = -INFINITY, l = 0.f, acc[V];
   __device__ __forceinline__ Gather() {
 #pragma unroll
     for (int c = 0; c < V; ++c) acc[c] = 0.f;
+  }
+  // Sets the sum of n <= 4 pieces: every lane reads their (m, l) itself, all
+  // loads at once, and no shuffle is needed.
+  template <typename FO, typename FM>
+  __device__ __forceinline__ void few(int n, FO o_of, FM ml_of) {
+    const int lane = threadIdx.x & 31;
+    float2 ml[4];
+    float y[4][V];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) {
+        ml[k] = *reinterpret_cast<const float2 *>(ml_of(k));
+        const float *src = o_of(k) + lane * V;
+        if constexpr (V == 4) {
+          const float4 z = *reinterpret_cast<const float4 *>(src);
+          y[k][0] = z.x, y[k][1] = z.y, y[k][2] = z.z, y[k][3] = z.w;
+        } else {
+          const float2 z = *reinterpret_cast<const float2 *>(src);
+          y[k][0] = z.x, y[k][1] = z.y;
+        }
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) m = fmaxf(m, ml[k].x);
+    const float mb = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) {
+        const float f = exp2f(ml[k].x - mb);
+        l = fmaf(f, ml[k].y, l);
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(f, y[k][c], acc[c]);
+      }
   }
   // Adds n <= 32 pieces in order; o_of(i) is the address of piece i's O row,
   // and lane i has its (m, l).  The first rows are requested before the
@@ -77,7 +110,7 @@ struct Gather {
 // PACKED: rows stand as they are counted; else 128 / G whole tokens to each
 // 128 rows.
 template <int D, int TILE_ROWS, bool PACKED>
-__global__ void __launch_bounds__(256, 3) paged_join_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(256, 4) paged_join_kernel(const PagedParams p) {
   constexpr int NW = 8, V = D / 32;
   __shared__ float red[NW][D + 4];
   admit_next();
@@ -108,6 +141,14 @@ __global__ void __launch_bounds__(256, 3) paged_join_kernel(const PagedParams p)
       g.add(n, ml, [&](int k) { return p.part_o + place(base + k * step, r) * D; });
     }
   };
+  if (np <= 4) {
+    for (int r = blockIdx.y * NW + warp; r < cut.rows; r += gridDim.y * NW) {
+      Gather<D> g;
+      g.few(np, [&](int k) { return p.part_o + place(k, r) * D; }, [&](int k) { return p.part_ml + place(k, r) * 2; });
+      finish(r, g.m, g.l, g.acc);
+    }
+    return;
+  }
   if (np <= NW) {
     for (int r = blockIdx.y * NW + warp; r < cut.rows; r += gridDim.y * NW) {
       Gather<D> g;

@@ -79,9 +79,13 @@ __device__ __forceinline__ void paged_fail(const PagedParams &p, unsigned code) 
 }
 
 // Sequence (or group) b as the device arrays give it, every index checked.
+// The loads that do not depend on one another are issued together.
 __device__ inline SeqInfo seq_info(const PagedParams &p, int b) {
   SeqInfo s;
-  bool bad = false;
+  s.slot = p.seqs ? __ldg(p.seqs + b) : b;
+  const bool in_table = s.slot >= 0 && s.slot < p.n_slots;
+  s.len = p.n_slots > 0 ? __ldg(p.seq_lens + (in_table ? s.slot : 0)) : 0;
+  bool bad = !in_table;
   int t0 = b, t1 = b + 1;
   if (p.group_ptr) {
     t0 = __ldg(p.group_ptr + b);
@@ -101,17 +105,12 @@ __device__ inline SeqInfo seq_info(const PagedParams &p, int b) {
   }
   s.q0 = t0;
   s.nq = t1 - t0;
-  s.slot = p.seqs ? __ldg(p.seqs + b) : b;
-  s.len = 0;
-  if (s.slot < 0 || s.slot >= p.n_slots) {
-    bad = true;
+  if (!in_table) {
     s.slot = -1;
-  } else {
-    s.len = __ldg(p.seq_lens + s.slot);
-    if (s.len < 0 || s.len > (static_cast<long long>(p.max_pages) << p.page_shift)) {
-      bad = true;
-      s.len = 0;
-    }
+    s.len = 0;
+  } else if (s.len < 0 || s.len > (static_cast<long long>(p.max_pages) << p.page_shift)) {
+    bad = true;
+    s.len = 0;
   }
   if (bad) paged_fail(p, ATTN_ERR_INVALID_ARG);
   return s;

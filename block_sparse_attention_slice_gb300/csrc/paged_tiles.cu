@@ -56,7 +56,9 @@ struct TileLayout {
   static constexpr int SCAN_OFF = MISC_OFF + 16;
   static constexpr int FIRST_OFF = SCAN_OFF + 16 * 8;
   static constexpr int THREADS = TILES * 128 + 64;
-  static size_t bytes(int n_seqs) { return 1024 + FIRST_OFF + 8ull * (n_seqs + 1); }
+  static size_t bytes(int n_seqs, bool infos) {
+    return 1024 + FIRST_OFF + 8ull * (n_seqs + 1) + (infos ? sizeof(SeqInfo) * n_seqs : 0);
+  }
   static_assert(MISC_OFF % 8 == 0, "alignment");
 };
 
@@ -87,13 +89,20 @@ struct Seg {
   int tok0, ntok, h, pos0, len, ns, w0, i0, i1;
   int out;              // 0 finished here, 1 / 2 piece slot + 1, -1 no more
   int np, slot0;        // of an item that begins here (i0 = 0): see Rec4
+  int rot;              // its key tiles are taken in the order i0 + rot, .., i1 - 1, i0, .., i0 + rot - 1
+  // the j-th key tile (of 128 keys) of the segment
+  static __device__ __forceinline__ int key_tile(int j, int i0, int i1, int rot, const Span &sp) {
+    const int i = i0 + rot + j;
+    return sp.tile(i < i1 ? i : i - (i1 - i0));
+  }
 };
 static_assert(sizeof(Seg) <= 64, "segment record");
 
 template <int D, int TILES>
 __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int tpt) {
+                       const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int tpt,
+                       const int keep_infos) {
   using L = TileLayout<D, TILES>;
   constexpr int NS = L::NS;
   extern __shared__ uint8_t tiles_smem[];
@@ -108,6 +117,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   };
   long long *scan = reinterpret_cast<long long *>(smem + L::SCAN_OFF);
   long long *first = reinterpret_cast<long long *>(smem + L::FIRST_OFF);
+  SeqInfo *info = keep_infos ? reinterpret_cast<SeqInfo *>(first + p.n_seqs + 1) : nullptr;
   const uint32_t q_smem = sb + L::Q_OFF, kv_smem = sb + L::KV_OFF;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpi = tpt * TILES;
@@ -146,8 +156,8 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   }
   if (!p.wait_end) after_previous();
   admit_next();
-  make_plan<0, PT_KL, L::THREADS>(p, tpi, first, static_cast<SeqInfo *>(nullptr), scan);
-  finish_empty<D, 0, PT_KL>(p, nullptr, tpi);
+  make_plan<0, PT_KL, L::THREADS>(p, tpi, first, info, scan);
+  finish_empty<D, 0, PT_KL>(p, info, tpi);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -162,7 +172,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     bool ok = true;
     long long at = from;
     Walk<0, PT_KL> w;
-    if (at < to) w.seek(p, first, nullptr, tpi, at);
+    if (at < to) w.seek(p, first, info, tpi, at);
     else if (lane == 0 && !p.rec) p.cuts[blockIdx.x] = Cut{};
     const int R = min(1 << p.page_shift, 128), ppt = 128 / R, page_mask = (1 << p.page_shift) - 1;
     while (ok) {
@@ -170,7 +180,17 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       if (nseg >= PT_IQ && !wait_all(bar(L::B_IE + qs), (nseg / PT_IQ - 1) & 1, abort, lim)) break;
       const bool more = at < to;
       int i1 = 0;
-      if (more) i1 = static_cast<int>(min(static_cast<long long>(w.sp.n), w.i + (to - at)));
+      // Row tiles of one group read the same keys.  Taking key tile k of an item
+      // at the time k mod span lets the CTAs that share it read it together, so
+      // that all but the first find it in L2.
+      int rot = 0;
+      if (more) {
+        i1 = static_cast<int>(min(static_cast<long long>(w.sp.n), w.i + (to - at)));
+        if (!p.causal) {
+          const int ahead = static_cast<int>((span - w.i % span) % span);
+          rot = w.i + ahead < i1 ? ahead : 0;
+        }
+      }
       if (lane == 0) {
         volatile Seg *s = seg_at(qs);
         if (more) {
@@ -188,6 +208,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           item_pieces(at - w.i, w.sp.n, mine, span, from, np, slot0);
           s->np = np;
           s->slot0 = slot0;
+          s->rot = rot;
         } else {
           s->out = -1;
         }
@@ -209,8 +230,9 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       const int tl = min(tpi, w.s.nq - w.rt * tpi) - 1, pos0 = w.s.len - w.s.nq + w.rt * tpi;
       const int end = p.causal ? pos0 + tl + 1 : w.s.len, lo = p.causal && p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
       const long long row = w.s.slot * p.table_stride;
-      auto page_of = [&](int i, int &tok) -> int {      // this lane's page of key tile i; n_pages: zeros
-        const int k0 = (w.sp.tile(i) << PT_KL) + lane * R;
+      const int i0 = w.i, steps = i1 - i0;
+      auto page_of = [&](int j, int &tok) -> int {      // this lane's page of the j-th key tile; n_pages: zeros
+        const int k0 = (Seg::key_tile(j, i0, i1, rot, w.sp) << PT_KL) + lane * R;
         tok = k0 & page_mask;
         const bool seen = lane < ppt && k0 < end && (k0 + R > lo || k0 < p.sinks);
         if (!seen) return p.n_pages;
@@ -221,11 +243,11 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         }
         return e;
       };
-      int tok, tok_next = 0, page, page_next = page_of(w.i, tok_next);
-      for (int i = w.i; i < i1 && ok; ++i) {
+      int tok, tok_next = 0, page, page_next = page_of(0, tok_next);
+      for (int j = 0; j < steps && ok; ++j) {
         page = page_next;
         tok = tok_next;
-        if (i + 1 < i1) page_next = page_of(i + 1, tok_next);
+        if (j + 1 < steps) page_next = page_of(j + 1, tok_next);
         for (int kv = 0; kv < 2; ++kv, ++ld) {
           const int slot = ld % NS;
           if (ld >= NS && !wait_all(bar(L::B_EMPTY + slot), (ld / NS - 1) & 1, abort, lim)) {
@@ -241,10 +263,10 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         }
       }
       if (!ok) break;
-      at += i1 - w.i;
+      at += steps;
       w.i = i1 - 1;
       if (at == to && lane == 0 && !p.rec) leave_cut<0, PT_KL>(p, w, tpi, w.h * p.hp + sub, blockIdx.x, mine, span, from, to);
-      if (at < to) w.next(p, first, nullptr, tpi);
+      if (at < to) w.next(p, first, info, tpi);
     }
     if (*abort && lane == 0) {
       // let the loads in flight land before the CTA retires
@@ -392,7 +414,8 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       if (!wait_all(bar(L::B_IF + qs), (nseg / PT_IQ) & 1, abort, lim)) break;
       volatile Seg *s = seg_at(qs);
       const int out = s->out, tok0 = s->tok0 + t * tpt, ntok = min(tpt, s->ntok - t * tpt), h = s->h, pos0 = s->pos0 + t * tpt,
-                len = s->len, ns = s->ns, w0 = s->w0, i0 = s->i0, i1 = s->i1, np = s->np, slot0 = s->slot0;
+                len = s->len, i0 = s->i0, i1 = s->i1, np = s->np, slot0 = s->slot0, rot = s->rot;
+      const Span sp{s->ns, s->w0, 0};
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::B_IE + qs));
       if (out < 0) break;
@@ -401,11 +424,11 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       const int lo = p.causal && p.window > 0 ? hi - p.window : 0;
       const int all_hi = p.causal ? pos0 + 1 : len, all_lo = p.causal && p.window > 0 ? pos0 + ntok - p.window : 0;
       float m_ref = -INFINITY, l = 0.f;
-      for (int i = i0; i < i1; ++i, ++step) {
+      for (int j = 0; j < i1 - i0; ++j, ++step) {
         const int u = TILES == 1 ? step & 1 : t;
         const uint32_t ph = TILES == 1 ? (step >> 1) & 1 : step & 1;
         const uint32_t tS = tmem + lane_off + u * 128;
-        const int c0 = (i < ns ? i : i - ns + w0) << PT_KL;
+        const int c0 = Seg::key_tile(j, i0, i1, rot, sp) << PT_KL;
         const bool masked = c0 + 128 > all_hi || (c0 < all_lo && c0 + 128 > p.sinks);
         uint32_t w[4] = {0u, 0u, 0u, 0u};
         if (masked) {
@@ -469,7 +492,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           float a0, a1;
           f2_split(f2_add(f2_add(l2[0], l2[1]), f2_add(l2[2], l2[3])), a0, a1);
           l += a0 + a1;
-          const bool rescale = grow && m_old != -INFINITY && i > i0;
+          const bool rescale = grow && m_old != -INFINITY && j > 0;
           if (__any_sync(0xffffffffu, rescale)) {
             // PV(i-1) has to be done before O is rescaled: with one row tile
             // S(i) does not say so, its QK was issued before that product
@@ -619,7 +642,8 @@ int launch_tiles(PagedParams &p, const CUtensorMap &mq, const CUtensorMap &mk, c
   p.part_ml = p.part_o + paged_piece_floats(TILES * 128, D);
   p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * 2 * TILES * 128 * 2);
   const int tpt = 128 / p.G;
-  const int rc = launch_after(kern, dim3(sms), L::THREADS, L::bytes(p.n_seqs), s, mq, mk, mv, p, tpt);
+  const bool infos = L::bytes(p.n_seqs, true) <= kSmemMax;
+  const int rc = launch_after(kern, dim3(sms), L::THREADS, L::bytes(p.n_seqs, infos), s, mq, mk, mv, p, tpt, infos ? 1 : 0);
   if (rc != ATTN_OK || p.rec) return rc;
   return launch_after(join, dim3(sms, TILES * 8), 256, 0, s, p);
 }

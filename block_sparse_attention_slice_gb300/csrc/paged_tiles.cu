@@ -8,13 +8,15 @@
 // packs them).  TILES = 2: an item is two row tiles that share every key tile,
 // and the tensor core works on one while the softmax warps of the other run
 // (the order of attn_fwd: PV_0(j), QK_0(j+1), PV_1(j), QK_1(j+1)).  TILES = 1,
-// for items of at most TPT tokens: one row tile with two score buffers, QK(j+1)
-// issued before softmax(j) ends.  Bound by the tensor core when an item's rows
-// fill its tiles, by the cache's bandwidth when they do not.
+// for items of at most TPT tokens: one row tile whose key tiles go by turns to
+// two groups of softmax warps, each with its own scores, maximum, sum and O,
+// merged when the segment ends.  (One group alone takes 1.1 us a key tile, which
+// at head dim 64 is 4.3 TB/s.)  Bound by the tensor core and the softmax when an
+// item's rows fill its tiles, by the cache's bandwidth when they do not.
 //
 // One persistent CTA per SM takes an equal span of the flat list of 128-key
 // tiles (paged_plan.cuh); pieces of items that cross spans are joined by
-// paged_join_kernel.  Warps: 4 softmax warps a row tile (thread = row = tensor
+// paged_join_kernel.  Warps: two groups of 4 softmax warps (thread = row = tensor
 // memory lane), a producer warp (walks the list, publishes each segment to the
 // others, fetches Q, K and V; one lane per page of a tile) and a warp that
 // issues the matrix instructions.
@@ -50,12 +52,13 @@ struct TileLayout {
   static constexpr int Q_OFF = 0, KV_OFF = TILES * TILE, SEG_OFF = KV_OFF + NS * TILE;
   static constexpr int BAR_OFF = SEG_OFF + PT_IQ * 64;
   static constexpr int B_Q = 0, B_QE = 1, B_FULL = 2, B_EMPTY = B_FULL + NS, B_S = B_EMPTY + NS, B_P = B_S + 2,
-                       B_O = B_P + 2, B_IF = B_O + TILES, B_IE = B_IF + PT_IQ, B_DRAIN = B_IE + PT_IQ,
-                       B_V = B_DRAIN + 1, NBAR = B_V + 1;
+                       B_O = B_P + 2, B_IF = B_O + 2, B_IE = B_IF + PT_IQ, B_DRAIN = B_IE + PT_IQ,
+                       B_X = B_DRAIN + 1, NBAR = B_X + 2;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
-  static constexpr int SCAN_OFF = MISC_OFF + 16;
+  static constexpr int XML_OFF = MISC_OFF + 16;               // TILES = 1: (m, l) of both groups
+  static constexpr int SCAN_OFF = XML_OFF + (TILES == 1 ? 2 * 128 * 8 : 0);
   static constexpr int FIRST_OFF = SCAN_OFF + 16 * 8;
-  static constexpr int THREADS = TILES * 128 + 64;
+  static constexpr int THREADS = 256 + 64;
   static size_t bytes(int n_seqs, bool infos) {
     return 1024 + FIRST_OFF + 8ull * (n_seqs + 1) + (infos ? sizeof(SeqInfo) * n_seqs : 0);
   }
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpi = tpt * TILES;
   const uint64_t lim = p.wait_ns;
-  constexpr int WP = TILES * 4, WM = TILES * 4 + 1;       // producer, issuer
+  constexpr int WP = 8, WM = 9;       // producer, issuer
 
   if (threadIdx.x == 0) {
     mbar_init(bar(L::B_Q), 1);
@@ -135,13 +138,15 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       mbar_init(bar(L::B_S + t), 1);
       mbar_init(bar(L::B_P + t), 128);
     }
-    for (int t = 0; t < TILES; ++t) mbar_init(bar(L::B_O + t), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(L::B_O + t), 1);
+      mbar_init(bar(L::B_X + t), 256);
+    }
     for (int u = 0; u < PT_IQ; ++u) {
       mbar_init(bar(L::B_IF + u), 1);
-      mbar_init(bar(L::B_IE + u), TILES * 4 + 1);
+      mbar_init(bar(L::B_IE + u), 9);
     }
     mbar_init(bar(L::B_DRAIN), 1);
-    mbar_init(bar(L::B_V), 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -191,31 +196,14 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           rot = w.i + ahead < i1 ? ahead : 0;
         }
       }
-      if (lane == 0) {
-        volatile Seg *s = seg_at(qs);
-        if (more) {
-          s->tok0 = w.s.q0 + w.rt * tpi;
-          s->ntok = min(tpi, w.s.nq - w.rt * tpi);
-          s->h = w.h * p.hp + sub;
-          s->pos0 = w.s.len - w.s.nq + w.rt * tpi;
-          s->len = w.s.len;
-          s->ns = w.sp.ns;
-          s->w0 = w.sp.w0;
-          s->i0 = w.i;
-          s->i1 = i1;
-          s->out = w.i == 0 && i1 == w.sp.n ? 0 : at == from ? 1 : 2;
-          int np, slot0;
-          item_pieces(at - w.i, w.sp.n, mine, span, from, np, slot0);
-          s->np = np;
-          s->slot0 = slot0;
-          s->rot = rot;
-        } else {
-          s->out = -1;
+      if (!more) {
+        if (lane == 0) {
+          seg_at(qs)->out = -1;
+          mbar_arrive(bar(L::B_IF + qs));
         }
-        mbar_arrive(bar(L::B_IF + qs));
+        __syncwarp();
+        break;
       }
-      __syncwarp();
-      if (!more) break;
       // Q of the segment's tokens
       if (nseg > 0 && !wait_all(bar(L::B_QE), (nseg - 1) & 1, abort, lim)) break;
       const int tok0 = w.s.q0 + w.rt * tpi;
@@ -244,6 +232,27 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         return e;
       };
       int tok, tok_next = 0, page, page_next = page_of(0, tok_next);
+      // what the others need to know; by now Q and the first page are on their way
+      if (lane == 0) {
+        volatile Seg *s = seg_at(qs);
+        s->tok0 = tok0;
+        s->ntok = tl + 1;
+        s->h = w.h * p.hp + sub;
+        s->pos0 = pos0;
+        s->len = w.s.len;
+        s->ns = w.sp.ns;
+        s->w0 = w.sp.w0;
+        s->i0 = i0;
+        s->i1 = i1;
+        s->out = i0 == 0 && i1 == w.sp.n ? 0 : at == from ? 1 : 2;
+        int np, slot0;
+        item_pieces(at - i0, w.sp.n, mine, span, from, np, slot0);
+        s->np = np;
+        s->slot0 = slot0;
+        s->rot = rot;
+        mbar_arrive(bar(L::B_IF + qs));
+      }
+      __syncwarp();
       for (int j = 0; j < steps && ok; ++j) {
         page = page_next;
         tok = tok_next;
@@ -322,42 +331,66 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         if (!wait2(bar(L::B_Q), nseg & 1, bar(L::B_FULL + k.slot), k.ph)) break;
         ++nseg;
         tc_fence_after();
-        issue_qk(0, TILES == 1 ? step & 1 : 0, k.slot);
-        mma_commit(bar(L::B_S + (TILES == 1 ? step & 1 : 0)));
-        if (TILES == 2) {
-          issue_qk(1, 1, k.slot);
-          mma_commit(bar(L::B_S + 1));
-        }
-        mma_commit(bar(L::B_EMPTY + k.slot));
-        if (n == 1) mma_commit(bar(L::B_QE));
-        for (int j = 0; j < n; ++j, ++step) {
-          const bool more = j + 1 < n;
+        if constexpr (TILES == 1) {
+          // scores of key tile j go to buffer and group (step + j) & 1
+          auto qk = [&](int j, uint32_t buf) {
+            issue_qk(0, buf, k.slot);
+            mma_commit(bar(L::B_S + buf));
+            mma_commit(bar(L::B_EMPTY + k.slot));
+            if (j + 1 == n) mma_commit(bar(L::B_QE));
+          };
           Pos v = k;
           v.next();
-          k = v;
-          k.next();
-          if constexpr (TILES == 1) {
-            if (more) {
-              if (!wait(bar(L::B_FULL + k.slot), k.ph)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              issue_qk(0, (step + 1) & 1, k.slot);
-              mma_commit(bar(L::B_S + ((step + 1) & 1)));
-              mma_commit(bar(L::B_EMPTY + k.slot));
-              if (j + 2 == n) mma_commit(bar(L::B_QE));
-            }
+          qk(0, step & 1);
+          if (n > 1) {
+            k = v;
+            k.next();
+            if (!wait(bar(L::B_FULL + k.slot), k.ph)) break;
+            tc_fence_after();
+            qk(1, (step + 1) & 1);
+          }
+          for (int j = 0; j < n; ++j, ++step) {
             if (!wait2(bar(L::B_FULL + v.slot), v.ph, bar(L::B_P + (step & 1)), (step >> 1) & 1)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            issue_pv(0, step & 1, v.slot, j == 0);
+            issue_pv(step & 1, step & 1, v.slot, j < 2);
             mma_commit(bar(L::B_EMPTY + v.slot));
-            mma_commit(bar(L::B_V));
-            if (!more) mma_commit(bar(L::B_O));
-          } else {
+            if (j + 1 == n) {
+              mma_commit(bar(L::B_O + 0));
+              mma_commit(bar(L::B_O + 1));
+            }
+            if (j + 2 < n) {
+              k.next();
+              k.next();
+              if (!wait(bar(L::B_FULL + k.slot), k.ph)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              qk(j + 2, step & 1);
+            }
+            if (j + 1 < n) {
+              v.next();
+              v.next();
+            }
+          }
+          k = v;      // behind the segment's last V
+          k.next();
+        } else {
+          issue_qk(0, 0, k.slot);
+          mma_commit(bar(L::B_S + 0));
+          issue_qk(1, 1, k.slot);
+          mma_commit(bar(L::B_S + 1));
+          mma_commit(bar(L::B_EMPTY + k.slot));
+          if (n == 1) mma_commit(bar(L::B_QE));
+          for (int j = 0; j < n; ++j, ++step) {
+            const bool more = j + 1 < n;
+            Pos v = k;
+            v.next();
+            k = v;
+            k.next();
             if (!wait2(bar(L::B_FULL + v.slot), v.ph, bar(L::B_P + 0), step & 1)) {
               ok = false;
               break;
@@ -402,9 +435,11 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     __syncwarp();
   } else {
     // --------------------------------------------------------------- softmax
-    const int t = TILES == 1 ? 0 : warp >> 2, wl = warp & 3, r = wl * 32 + lane;
+    // u: group, score buffer and O; t: row tile
+    const int u = warp >> 2, t = TILES == 1 ? 0 : u, wl = warp & 3, r = wl * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wl * 32) << 16;
-    const uint32_t tO = tmem + lane_off + 256 + t * 128;
+    const uint32_t tS = tmem + lane_off + u * 128, tO = tmem + lane_off + 256 + u * 128;
+    float2 *xml = reinterpret_cast<float2 *>(smem + L::XML_OFF);
     const float sl2 = p.scale_log2;
     const int tl = r / p.G, g = r - tl * p.G;               // token and head of this row in its tile
     uint32_t step = 0, nseg = 0;
@@ -424,10 +459,10 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       const int lo = p.causal && p.window > 0 ? hi - p.window : 0;
       const int all_hi = p.causal ? pos0 + 1 : len, all_lo = p.causal && p.window > 0 ? pos0 + ntok - p.window : 0;
       float m_ref = -INFINITY, l = 0.f;
+      const uint32_t step0 = step;
       for (int j = 0; j < i1 - i0; ++j, ++step) {
-        const int u = TILES == 1 ? step & 1 : t;
+        if (TILES == 1 && static_cast<int>(step & 1) != u) continue;      // the other group's
         const uint32_t ph = TILES == 1 ? (step >> 1) & 1 : step & 1;
-        const uint32_t tS = tmem + lane_off + u * 128;
         const int c0 = Seg::key_tile(j, i0, i1, rot, sp) << PT_KL;
         const bool masked = c0 + 128 > all_hi || (c0 < all_lo && c0 + 128 > p.sinks);
         uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -492,14 +527,9 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           float a0, a1;
           f2_split(f2_add(f2_add(l2[0], l2[1]), f2_add(l2[2], l2[3])), a0, a1);
           l += a0 + a1;
-          const bool rescale = grow && m_old != -INFINITY && j > 0;
+          // S of this tile follows the last product into this O on the tensor core
+          const bool rescale = grow && m_old != -INFINITY && j >= (TILES == 1 ? 2 : 1);
           if (__any_sync(0xffffffffu, rescale)) {
-            // PV(i-1) has to be done before O is rescaled: with one row tile
-            // S(i) does not say so, its QK was issued before that product
-            if (TILES == 1 && !wait_all(bar(L::B_V), (step - 1) & 1, abort, lim)) {
-              ok = false;
-              break;
-            }
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t y[32];
@@ -511,7 +541,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           }
           tmem_wait_st();
         }
-        if (t == 0 && c0 + 128 > len) {
+        if ((TILES == 1 || t == 0) && c0 + 128 > len) {
           // the last tile: rows of V behind the sequence's end become zeros
           // before the product that P's arrival admits
           const uint32_t pos = 2 * step + 1, slot = pos % NS;
@@ -528,7 +558,24 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         mbar_arrive(bar(L::B_P + u));
       }
       if (!ok) break;
-      if (!wait_all(bar(L::B_O + t), nseg & 1, abort, lim)) break;
+      if (!wait_all(bar(L::B_O + u), nseg & 1, abort, lim)) break;
+      // TILES = 1: both groups learn each other's (m, l); each then merges and
+      // stores its half of the columns.  has[]: the group had a key tile here.
+      float f0 = 1.f, f1 = 0.f;
+      bool has0 = true, has1 = false;
+      if constexpr (TILES == 1) {
+        has0 = i1 - i0 > 1 || (step0 & 1) == 0;
+        has1 = i1 - i0 > 1 || (step0 & 1) == 1;
+        xml[u * 128 + r] = make_float2(m_ref, l);
+        mbar_arrive(bar(L::B_X + 0));
+        if (!wait_all(bar(L::B_X + 0), nseg & 1, abort, lim)) break;
+        const float2 a = xml[r], b = xml[128 + r];
+        m_ref = fmaxf(a.x, b.x);
+        const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+        f0 = ex2_approx(a.x - mb);
+        f1 = ex2_approx(b.x - mb);
+        l = a.y * f0 + b.y * f1;
+      }
       ++nseg;
       tc_fence_after();
       if (!idle) {
@@ -539,15 +586,16 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         const bool final = out == 0 && !p.rec, f32 = !final || p.out_f32;
         float fo = 1.f, lse;
         if (live) {
+          const bool tell = TILES == 2 || u == 0;
           const long long row = static_cast<long long>(tok0 + tl) * p.hq + h * p.G + g;
           if (final) {
             row_final(m_ref, l, fo, lse);
-            p.lse[static_cast<long long>(h * p.G + g) * p.n_tokens + tok0 + tl] = lse;
-          } else {
+            if (tell) p.lse[static_cast<long long>(h * p.G + g) * p.n_tokens + tok0 + tl] = lse;
+          } else if (tell) {
             const long long pr = (static_cast<long long>(blockIdx.x) * 2 + out - 1) * (TILES * 128) + t * 128 + r;
             *reinterpret_cast<float2 *>(out ? p.part_ml + pr * 2 : p.dense_ml + row * 2) = make_float2(m_ref, l);
           }
-          if (p.rec && i0 == 0) p.rec[row] = Rec4{static_cast<int>(blockIdx.x), slot0, np, t * 128 + r};
+          if (p.rec && i0 == 0 && tell) p.rec[row] = Rec4{static_cast<int>(blockIdx.x), slot0, np, t * 128 + r};
         }
         uint8_t *dst[4];
 #pragma unroll
@@ -559,9 +607,28 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           dst[k] = xt < ntok ? base + (out ? pr : row) * (D * (f32 ? 4 : 2)) + q4 * 16 : nullptr;
         }
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = TILES == 1 ? u * (D / 64) : 0; c < (TILES == 1 ? (u + 1) * (D / 64) : D / 32); ++c) {
           uint32_t y[32];
-          tmem_ld32_wait(tO + c * 32, y);
+          if constexpr (TILES == 1) {
+            const uint32_t at = tmem + lane_off + 256 + c * 32;
+            float z[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) z[k] = 0.f;
+            if (has0) {
+              tmem_ld32_wait(at, y);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) z[k] = __uint_as_float(y[k]) * f0;
+            }
+            if (has1) {
+              tmem_ld32_wait(at + 128, y);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) z[k] = fmaf(__uint_as_float(y[k]), f1, z[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(z[k]);
+          } else {
+            tmem_ld32_wait(tO + c * 32, y);
+          }
           if (f32) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -593,6 +660,12 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         }
       }
       tc_fence_before();      // O is read before the next segment's first product
+      if constexpr (TILES == 1) {
+        // by both groups, of both O
+        mbar_arrive(bar(L::B_X + 1));
+        if (!wait_all(bar(L::B_X + 1), (nseg - 1) & 1, abort, lim)) break;
+        tc_fence_after();
+      }
     }
   }
   tc_fence_before();
@@ -621,6 +694,7 @@ int encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, c
 template <int D, int TILES>
 int launch_tiles(PagedParams &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
   using L = TileLayout<D, TILES>;
+  if (L::bytes(p.n_seqs, false) > kSmemMax) return ATTN_ERR_UNSUPPORTED;    // above 4000 sequences
   constexpr int kDev = 64;
   static bool done[kDev] = {};
   static std::mutex mu;
@@ -656,7 +730,8 @@ size_t paged_tiles_workspace(int d) {
 }
 
 // UNSUPPORTED, with nothing launched, where the tensor maps cannot say the
-// layout (more than 128 query heads a key/value head, strides of zero).
+// layout (more than 128 query heads a key/value head, strides of zero) or the
+// sequences' sums do not fit into shared memory.
 int paged_tiles_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
   if (p.G > 128) return ATTN_ERR_UNSUPPORTED;
   const int page = 1 << p.page_shift, tpt = 128 / p.G;

@@ -47,7 +47,7 @@ constexpr float PT_TAU = 8.0f;
 
 template <int D, int TILES>
 struct TileLayout {
-  static constexpr int NS = TILES == 2 ? 4 : 5;         // K/V ring slots
+  static constexpr int NS = D == 64 ? 10 : TILES == 2 ? 4 : 5;   // K/V ring slots: 128 to 160 KB
   static constexpr int HALF = 128 * 64 * 2, NHALF = D / 64, TILE = NHALF * HALF;
   static constexpr int Q_OFF = 0, KV_OFF = TILES * TILE, SEG_OFF = KV_OFF + NS * TILE;
   static constexpr int BAR_OFF = SEG_OFF + PT_IQ * 64;

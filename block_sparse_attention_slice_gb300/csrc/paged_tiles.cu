@@ -253,23 +253,32 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         mbar_arrive(bar(L::B_IF + qs));
       }
       __syncwarp();
+      // the tile of this lane's page into the next ring slot
+      auto load = [&](const CUtensorMap *tm, int tok, int page) {
+        const int slot = ld % NS;
+        if (ld >= NS && !wait_all(bar(L::B_EMPTY + slot), (ld / NS - 1) & 1, abort, lim)) {
+          ok = false;
+          return;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bar(L::B_FULL + slot), L::TILE);
+        __syncwarp();
+        if (lane < ppt)
+          for (int hh = 0; hh < L::NHALF; ++hh)
+            tma_load_4d(kv_smem + slot * L::TILE + hh * L::HALF + lane * R * 128, tm, bar(L::B_FULL + slot), hh * 64, tok,
+                        w.h * p.hp + sub, page);
+        ++ld;
+      };
+      // In the order in which the tensor core takes them, so that no slot waits
+      // behind one that is needed later: K_0 V_0 K_1 V_1 .. for two row tiles,
+      // K_0 K_1 V_0 K_2 V_1 .. for one.
+      if (TILES == 1) load(&tm_k, tok_next, page_next);
       for (int j = 0; j < steps && ok; ++j) {
         page = page_next;
         tok = tok_next;
         if (j + 1 < steps) page_next = page_of(j + 1, tok_next);
-        for (int kv = 0; kv < 2; ++kv, ++ld) {
-          const int slot = ld % NS;
-          if (ld >= NS && !wait_all(bar(L::B_EMPTY + slot), (ld / NS - 1) & 1, abort, lim)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(bar(L::B_FULL + slot), L::TILE);
-          __syncwarp();
-          if (lane < ppt)
-            for (int hh = 0; hh < L::NHALF; ++hh)
-              tma_load_4d(kv_smem + slot * L::TILE + hh * L::HALF + lane * R * 128, kv ? &tm_v : &tm_k,
-                          bar(L::B_FULL + slot), hh * 64, tok, w.h * p.hp + sub, page);
-        }
+        if (TILES == 2) load(&tm_k, tok, page);
+        if (TILES == 1 && j + 1 < steps) load(&tm_k, tok_next, page_next);
+        if (ok) load(&tm_v, tok, page);
       }
       if (!ok) break;
       at += steps;
@@ -339,45 +348,37 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
             mma_commit(bar(L::B_EMPTY + k.slot));
             if (j + 1 == n) mma_commit(bar(L::B_QE));
           };
-          Pos v = k;
-          v.next();
           qk(0, step & 1);
+          k.next();
           if (n > 1) {
-            k = v;
-            k.next();
             if (!wait(bar(L::B_FULL + k.slot), k.ph)) break;
             tc_fence_after();
             qk(1, (step + 1) & 1);
+            k.next();
           }
           for (int j = 0; j < n; ++j, ++step) {
-            if (!wait2(bar(L::B_FULL + v.slot), v.ph, bar(L::B_P + (step & 1)), (step >> 1) & 1)) {
+            if (!wait2(bar(L::B_FULL + k.slot), k.ph, bar(L::B_P + (step & 1)), (step >> 1) & 1)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            issue_pv(step & 1, step & 1, v.slot, j < 2);
-            mma_commit(bar(L::B_EMPTY + v.slot));
+            issue_pv(step & 1, step & 1, k.slot, j < 2);
+            mma_commit(bar(L::B_EMPTY + k.slot));
+            k.next();
             if (j + 1 == n) {
               mma_commit(bar(L::B_O + 0));
               mma_commit(bar(L::B_O + 1));
             }
             if (j + 2 < n) {
-              k.next();
-              k.next();
               if (!wait(bar(L::B_FULL + k.slot), k.ph)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
               qk(j + 2, step & 1);
-            }
-            if (j + 1 < n) {
-              v.next();
-              v.next();
+              k.next();
             }
           }
-          k = v;      // behind the segment's last V
-          k.next();
         } else {
           issue_qk(0, 0, k.slot);
           mma_commit(bar(L::B_S + 0));
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         if ((TILES == 1 || t == 0) && c0 + 128 > len) {
           // the last tile: rows of V behind the sequence's end become zeros
           // before the product that P's arrival admits
-          const uint32_t pos = 2 * step + 1, slot = pos % NS;
+          const uint32_t pos = 2 * step + (TILES == 1 && j + 1 < i1 - i0 ? 2 : 1), slot = pos % NS;
           if (!wait_all(bar(L::B_FULL + slot), (pos / NS) & 1, abort, lim)) {
             ok = false;
             break;

@@ -91,12 +91,6 @@ class Cache(ctypes.Structure):
                 ("n_slots", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
 
 
-def test_packed_structs_are_the_headers():
-    assert bytes(Pages(1, 2, 3, 4, 5, 6, 7, 8, 9)) == G._PAGES(1, 2, 3, 4, 5, 6, 7, 8, 9)
-    assert bytes(Seqs(1, 2, 3, 4, 5, 6, 7, 8)) == G._SEQS(1, 2, 3, 4, 5, 6, 7, 8)
-    assert bytes(Cache(1, 2, 3, 4, 5, 6, 7, 8)) == G._CACHE(1, 2, 3, 4, 5, 6, 7, 8)
-
-
 X = ctypes.c_void_p(4096)      # an aligned address that no refused call reads
 
 
@@ -160,14 +154,26 @@ def test_refusals_of_one_call(lib):
         assert _call(lib, a, prefix) == B.ATTN_OK
 
 
-def test_binding_refuses_wrong_tensors():
+def test_binding_refuses_wrong_tensors(lib):
     import torch
     k = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16)
+    q = torch.zeros((1, 2, 64), dtype=torch.bfloat16)
     i = torch.zeros(1, dtype=torch.int32)
-    with pytest.raises(ValueError):
-        G.attn_paged_fwd(torch.zeros((1, 2, 64), dtype=torch.bfloat16), k, k, i[None], i, 1.0)      # not on a GPU
-    with pytest.raises(ValueError):
-        G.attn_paged_fwd(torch.zeros((1, 2, 64), dtype=torch.bfloat16), k, k[:, :, :1], i[None], i, 1.0)
+    for bad in ((q, k, k), (q, k, k[:, :, :1]), (q, k.float(), k.float()), (q, k[0], k[0])):        # not on a GPU, or worse
+        with pytest.raises(ValueError):
+            G.attn_paged_fwd(*bad, i[None], i, 1.0)
+        with pytest.raises(ValueError):
+            G.attn_prefix_fwd(*bad, i[None], i, i, i[None], i, 1.0)
+    with pytest.raises(TypeError):
+        G.attn_paged_fwd(q, None, k, i[None], i, 1.0)
+    for call in (lambda: G.attn_cache_free(i[None], i, i, i, 16), lambda: G.attn_cache_extend(i[None], i, i, i, i, 16),
+                 lambda: G.attn_cache_trim(i[None], i, i, 16, 1), lambda: G.attn_cache_fork(i[None], i, i, i, i, 16),
+                 lambda: G.attn_cache_compact(i[None], i, i, 16), lambda: G.attn_cache_copy_pages([k], i),
+                 lambda: G.attn_cache_write(k, k, q, q, i[None], i)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        G.attn_cache_copy_pages(7, i)
 
 
 def _cache(**kw):

@@ -65,6 +65,7 @@ struct PagedParams {
   float *part_o;              // pieces: [workers][2][rows][D], [workers][2][rows][2]
   float *part_ml;
   Cut *cuts;                  // [workers]
+  int warp_plan;              // make_warp_plan, not make_plan
   int hp, n_spans, min_span;  // heads side by side; spans; key tiles a span holds at least
   unsigned int *status;
   unsigned long long wait_ns;
@@ -167,6 +168,31 @@ __device__ inline long long head_tiles(const PagedParams &p, const SeqInfo &s, i
   long long n = 0;
   for (int rt = 0; rt < R; ++rt) n += tile_span<ROWS, KL>(p, s, rt, tpi).n;
   return n;
+}
+
+// Up to 32 sequences of few row tiles: each warp makes its own copy of the sums
+// (in `mine`, PLAN_WARP bytes of shared memory), a lane a sequence, and the
+// block need not meet.  Worth 1 to 2 us of a call of 13.
+constexpr int PLAN_WARP = 33 * 8 + 8 + 32 * 16;
+template <int ROWS, int KL>
+__device__ inline void make_warp_plan(const PagedParams &p, int tpi, uint8_t *mine, long long *&first, SeqInfo *&info) {
+  first = reinterpret_cast<long long *>(mine);
+  info = reinterpret_cast<SeqInfo *>(mine + 33 * 8 + 8);
+  const int lane = threadIdx.x & 31;
+  long long x = 0;
+  if (lane < p.n_seqs) {
+    const SeqInfo s = seq_info(p, lane);
+    info[lane] = s;
+    x = head_tiles<ROWS, KL>(p, s, tpi) * (p.hk / p.hp);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  first[lane + 1] = x;
+  if (lane == 0) first[0] = 0;
+  __syncwarp();
 }
 
 // The flat list's prefix sums, first[b] = key tiles before sequence b, for

@@ -83,7 +83,9 @@ struct RowsSmem {
   static constexpr int NOTE = RING;                             // Slab [W][NST]
   static constexpr int SCAN = NOTE + W * NST * static_cast<int>(sizeof(Slab));
   static constexpr int FIRST = SCAN + (W + 2) / 2 * 16;
-  static size_t bytes(int n_seqs) { return FIRST + 8ull * (n_seqs + 1) + sizeof(SeqInfo) * n_seqs; }
+  static size_t bytes(const PagedParams &p) {
+    return FIRST + (p.warp_plan ? static_cast<size_t>(W) * PLAN_WARP : 8ull * (p.n_seqs + 1) + sizeof(SeqInfo) * p.n_seqs);
+  }
 };
 
 template <int D, int NST>
@@ -97,10 +99,11 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
   SeqInfo *info = reinterpret_cast<SeqInfo *>(first + p.n_seqs + 1);
   if (!p.wait_end) after_previous();
   admit_next();
-  make_plan<PR_ROWS, KL, S::W * 32>(p, 0, first, info, scan);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (p.warp_plan) make_warp_plan<PR_ROWS, KL>(p, 0, rows_smem + S::FIRST + warp * PLAN_WARP, first, info);
+  else make_plan<PR_ROWS, KL, S::W * 32>(p, 0, first, info, scan);
   finish_empty<D, PR_ROWS, KL>(p, info, 0);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long total = first[p.n_seqs], span = span_of(p, total);
   const long long worker = static_cast<long long>(blockIdx.x) * S::W + warp, mine = worker / p.hp;
   const int sub = static_cast<int>(worker - mine * p.hp);       // this warp's head of a group
@@ -386,8 +389,9 @@ static int launch_rows(PagedParams &p, cudaStream_t s) {
   p.hp = 1;
   while (p.hp < S::W && p.hk % (2 * p.hp) == 0) p.hp *= 2;
   p.n_spans = sms * S::W / p.hp;
+  p.warp_plan = p.n_seqs <= 32 && (!p.causal || static_cast<long long>(p.n_tokens) * p.G <= 64 * PR_ROWS);
   p.min_span = 1;
-  const int rc = launch_after(kern, dim3(sms), S::W * 32, S::bytes(p.n_seqs), s, p);
+  const int rc = launch_after(kern, dim3(sms), S::W * 32, S::bytes(p), s, p);
   if (rc != ATTN_OK || p.rec) return rc;
   // few items: each has many pieces, and its rows go to blocks of their own
   const long long items = static_cast<long long>(p.n_seqs) * p.hk;
@@ -410,9 +414,10 @@ int paged_rows_launch(PagedParams &p, int d, cudaStream_t s) {
   if (sms <= 0) return ATTN_ERR_CUDA;
   p.part_ml = p.part_o + paged_piece_floats(PR_ROWS, d);
   p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * rows_warps(d) * 2 * PR_ROWS * 2);
-  if (d == 128)
-    return RowsSmem<128, 3>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<128, 3>(p, s) : launch_rows<128, 2>(p, s);
-  return RowsSmem<64, 3>::bytes(p.n_seqs) <= kSmemMax ? launch_rows<64, 3>(p, s) : launch_rows<64, 2>(p, s);
+  // a ring of 192 KB, or 128 where thousands of sequences take the room
+  const bool many = p.n_seqs > 1024;
+  if (d == 128) return many ? launch_rows<128, 2>(p, s) : launch_rows<128, 3>(p, s);
+  return many ? launch_rows<64, 2>(p, s) : launch_rows<64, 3>(p, s);
 }
 
 }  // namespace attn

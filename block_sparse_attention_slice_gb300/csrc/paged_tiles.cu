@@ -8,15 +8,13 @@
 // packs them).  TILES = 2: an item is two row tiles that share every key tile,
 // and the tensor core works on one while the softmax warps of the other run
 // (the order of attn_fwd: PV_0(j), QK_0(j+1), PV_1(j), QK_1(j+1)).  TILES = 1,
-// for items of at most TPT tokens: one row tile whose key tiles go by turns to
-// two groups of softmax warps, each with its own scores, maximum, sum and O,
-// merged when the segment ends.  (One group alone takes 1.1 us a key tile, which
-// at head dim 64 is 4.3 TB/s.)  Bound by the tensor core and the softmax when an
-// item's rows fill its tiles, by the cache's bandwidth when they do not.
+// for items of at most TPT tokens: one row tile with two score buffers, QK(j+1)
+// issued before softmax(j) ends.  Bound by the tensor core when an item's rows
+// fill its tiles, by the cache's bandwidth when they do not.
 //
 // One persistent CTA per SM takes an equal span of the flat list of 128-key
 // tiles (paged_plan.cuh); pieces of items that cross spans are joined by
-// paged_join_kernel.  Warps: two groups of 4 softmax warps (thread = row = tensor
+// paged_join_kernel.  Warps: 4 softmax warps a row tile (thread = row = tensor
 // memory lane), a producer warp (walks the list, publishes each segment to the
 // others, fetches Q, K and V; one lane per page of a tile) and a warp that
 // issues the matrix instructions.
@@ -32,6 +30,7 @@
 // tensor core takes.
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -52,15 +51,15 @@ struct TileLayout {
   static constexpr int Q_OFF = 0, KV_OFF = TILES * TILE, SEG_OFF = KV_OFF + NS * TILE;
   static constexpr int BAR_OFF = SEG_OFF + PT_IQ * 64;
   static constexpr int B_Q = 0, B_QE = 1, B_FULL = 2, B_EMPTY = B_FULL + NS, B_S = B_EMPTY + NS, B_P = B_S + 2,
-                       B_O = B_P + 2, B_IF = B_O + 2, B_IE = B_IF + PT_IQ, B_DRAIN = B_IE + PT_IQ,
-                       B_X = B_DRAIN + 1, NBAR = B_X + 2;
+                       B_O = B_P + 2, B_IF = B_O + TILES, B_IE = B_IF + PT_IQ, B_DRAIN = B_IE + PT_IQ,
+                       B_V = B_DRAIN + 1, NBAR = B_V + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
-  static constexpr int XML_OFF = MISC_OFF + 16;               // TILES = 1: (m, l) of both groups
-  static constexpr int SCAN_OFF = XML_OFF + (TILES == 1 ? 2 * 128 * 8 : 0);
+  static constexpr int SCAN_OFF = MISC_OFF + 16;
   static constexpr int FIRST_OFF = SCAN_OFF + 16 * 8;
-  static constexpr int THREADS = 256 + 64;
-  static size_t bytes(int n_seqs, bool infos) {
-    return 1024 + FIRST_OFF + 8ull * (n_seqs + 1) + (infos ? sizeof(SeqInfo) * n_seqs : 0);
+  static constexpr int THREADS = TILES * 128 + 64;
+  static size_t bytes(const PagedParams &p, bool infos) {
+    return 1024 + FIRST_OFF + (p.warp_plan ? THREADS / 32 * static_cast<size_t>(PLAN_WARP)
+                                           : 8ull * (p.n_seqs + 1) + (infos ? sizeof(SeqInfo) * p.n_seqs : 0));
   }
   static_assert(MISC_OFF % 8 == 0, "alignment");
 };
@@ -125,7 +124,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpi = tpt * TILES;
   const uint64_t lim = p.wait_ns;
-  constexpr int WP = 8, WM = 9;       // producer, issuer
+  constexpr int WP = TILES * 4, WM = TILES * 4 + 1;       // producer, issuer
 
   if (threadIdx.x == 0) {
     mbar_init(bar(L::B_Q), 1);
@@ -138,15 +137,13 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       mbar_init(bar(L::B_S + t), 1);
       mbar_init(bar(L::B_P + t), 128);
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(L::B_O + t), 1);
-      mbar_init(bar(L::B_X + t), 256);
-    }
+    for (int t = 0; t < TILES; ++t) mbar_init(bar(L::B_O + t), 1);
     for (int u = 0; u < PT_IQ; ++u) {
       mbar_init(bar(L::B_IF + u), 1);
-      mbar_init(bar(L::B_IE + u), 9);
+      mbar_init(bar(L::B_IE + u), TILES * 4 + 1);
     }
     mbar_init(bar(L::B_DRAIN), 1);
+    mbar_init(bar(L::B_V), 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -161,7 +158,8 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   }
   if (!p.wait_end) after_previous();
   admit_next();
-  make_plan<0, PT_KL, L::THREADS>(p, tpi, first, info, scan);
+  if (TILES == 1 && p.warp_plan) make_warp_plan<0, PT_KL>(p, tpi, smem + L::FIRST_OFF + warp * PLAN_WARP, first, info);
+  else make_plan<0, PT_KL, L::THREADS>(p, tpi, first, info, scan);
   finish_empty<D, 0, PT_KL>(p, info, tpi);
   tc_fence_before();
   __syncthreads();
@@ -219,19 +217,22 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       const int end = p.causal ? pos0 + tl + 1 : w.s.len, lo = p.causal && p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
       const long long row = w.s.slot * p.table_stride;
       const int i0 = w.i, steps = i1 - i0;
-      auto page_of = [&](int j, int &tok) -> int {      // this lane's page of the j-th key tile; n_pages: zeros
+      // this lane's page of the j-th key tile, as the table has it; NOT_SEEN:
+      // nothing to fetch.  Requested a tile ahead and looked at only when used,
+      // or each tile would cost the latency of its table entry.
+      constexpr int NOT_SEEN = INT_MIN;
+      auto look_up = [&](int j, int &tok) -> int {
         const int k0 = (Seg::key_tile(j, i0, i1, rot, w.sp) << PT_KL) + lane * R;
         tok = k0 & page_mask;
         const bool seen = lane < ppt && k0 < end && (k0 + R > lo || k0 < p.sinks);
-        if (!seen) return p.n_pages;
-        const int e = __ldg(p.table + row + (k0 >> p.page_shift));
-        if (e < 0 || e >= p.n_pages) {
-          paged_fail(p, ATTN_ERR_INVALID_ARG);
-          return p.n_pages;
-        }
-        return e;
+        return seen ? __ldg(p.table + row + (k0 >> p.page_shift)) : NOT_SEEN;
       };
-      int tok, tok_next = 0, page, page_next = page_of(0, tok_next);
+      auto checked = [&](int e) -> int {      // n_pages: zeros
+        if (e >= 0 && e < p.n_pages) return e;
+        if (e != NOT_SEEN) paged_fail(p, ATTN_ERR_INVALID_ARG);
+        return p.n_pages;
+      };
+      int tok_next = 0, raw_next = look_up(0, tok_next);
       // what the others need to know; by now Q and the first page are on their way
       if (lane == 0) {
         volatile Seg *s = seg_at(qs);
@@ -271,14 +272,21 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       // In the order in which the tensor core takes them, so that no slot waits
       // behind one that is needed later: K_0 V_0 K_1 V_1 .. for two row tiles,
       // K_0 K_1 V_0 K_2 V_1 .. for one.
-      if (TILES == 1) load(&tm_k, tok_next, page_next);
+      int tok = tok_next, page = checked(raw_next);
+      if (steps > 1) raw_next = look_up(1, tok_next);
+      if (TILES == 1) load(&tm_k, tok, page);
       for (int j = 0; j < steps && ok; ++j) {
-        page = page_next;
-        tok = tok_next;
-        if (j + 1 < steps) page_next = page_of(j + 1, tok_next);
+        int tok1 = 0, page1 = 0;
+        if (j + 1 < steps) {
+          page1 = checked(raw_next);
+          tok1 = tok_next;
+          if (j + 2 < steps) raw_next = look_up(j + 2, tok_next);
+        }
         if (TILES == 2) load(&tm_k, tok, page);
-        if (TILES == 1 && j + 1 < steps) load(&tm_k, tok_next, page_next);
+        if (TILES == 1 && j + 1 < steps) load(&tm_k, tok1, page1);
         if (ok) load(&tm_v, tok, page);
+        tok = tok1;
+        page = page1;
       }
       if (!ok) break;
       at += steps;
@@ -341,43 +349,34 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         ++nseg;
         tc_fence_after();
         if constexpr (TILES == 1) {
-          // scores of key tile j go to buffer and group (step + j) & 1
+          // scores of key tile j go to buffer (step + j) & 1
           auto qk = [&](int j, uint32_t buf) {
             issue_qk(0, buf, k.slot);
             mma_commit(bar(L::B_S + buf));
             mma_commit(bar(L::B_EMPTY + k.slot));
             if (j + 1 == n) mma_commit(bar(L::B_QE));
+            k.next();
           };
           qk(0, step & 1);
-          k.next();
-          if (n > 1) {
-            if (!wait(bar(L::B_FULL + k.slot), k.ph)) break;
-            tc_fence_after();
-            qk(1, (step + 1) & 1);
-            k.next();
-          }
           for (int j = 0; j < n; ++j, ++step) {
-            if (!wait2(bar(L::B_FULL + k.slot), k.ph, bar(L::B_P + (step & 1)), (step >> 1) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            issue_pv(step & 1, step & 1, k.slot, j < 2);
-            mma_commit(bar(L::B_EMPTY + k.slot));
-            k.next();
-            if (j + 1 == n) {
-              mma_commit(bar(L::B_O + 0));
-              mma_commit(bar(L::B_O + 1));
-            }
-            if (j + 2 < n) {
+            if (j + 1 < n) {
               if (!wait(bar(L::B_FULL + k.slot), k.ph)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-              qk(j + 2, step & 1);
-              k.next();
+              qk(j + 1, (step + 1) & 1);
             }
+            if (!wait2(bar(L::B_FULL + k.slot), k.ph, bar(L::B_P + (step & 1)), (step >> 1) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_pv(0, step & 1, k.slot, j == 0);
+            mma_commit(bar(L::B_EMPTY + k.slot));
+            mma_commit(bar(L::B_V));
+            if (j + 1 == n) mma_commit(bar(L::B_O));
+            k.next();
           }
         } else {
           issue_qk(0, 0, k.slot);
@@ -436,11 +435,9 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     __syncwarp();
   } else {
     // --------------------------------------------------------------- softmax
-    // u: group, score buffer and O; t: row tile
-    const int u = warp >> 2, t = TILES == 1 ? 0 : u, wl = warp & 3, r = wl * 32 + lane;
+    const int t = TILES == 1 ? 0 : warp >> 2, wl = warp & 3, r = wl * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wl * 32) << 16;
-    const uint32_t tS = tmem + lane_off + u * 128, tO = tmem + lane_off + 256 + u * 128;
-    float2 *xml = reinterpret_cast<float2 *>(smem + L::XML_OFF);
+    const uint32_t tO = tmem + lane_off + 256 + t * 128;
     const float sl2 = p.scale_log2;
     const int tl = r / p.G, g = r - tl * p.G;               // token and head of this row in its tile
     uint32_t step = 0, nseg = 0;
@@ -460,10 +457,10 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       const int lo = p.causal && p.window > 0 ? hi - p.window : 0;
       const int all_hi = p.causal ? pos0 + 1 : len, all_lo = p.causal && p.window > 0 ? pos0 + ntok - p.window : 0;
       float m_ref = -INFINITY, l = 0.f;
-      const uint32_t step0 = step;
       for (int j = 0; j < i1 - i0; ++j, ++step) {
-        if (TILES == 1 && static_cast<int>(step & 1) != u) continue;      // the other group's
+        const int u = TILES == 1 ? step & 1 : t;
         const uint32_t ph = TILES == 1 ? (step >> 1) & 1 : step & 1;
+        const uint32_t tS = tmem + lane_off + u * 128;
         const int c0 = Seg::key_tile(j, i0, i1, rot, sp) << PT_KL;
         const bool masked = c0 + 128 > all_hi || (c0 < all_lo && c0 + 128 > p.sinks);
         uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -528,9 +525,14 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           float a0, a1;
           f2_split(f2_add(f2_add(l2[0], l2[1]), f2_add(l2[2], l2[3])), a0, a1);
           l += a0 + a1;
-          // S of this tile follows the last product into this O on the tensor core
-          const bool rescale = grow && m_old != -INFINITY && j >= (TILES == 1 ? 2 : 1);
+          const bool rescale = grow && m_old != -INFINITY && j > 0;
           if (__any_sync(0xffffffffu, rescale)) {
+            // PV(i-1) has to be done before O is rescaled: with one row tile
+            // S(i) does not say so, its QK was issued before that product
+            if (TILES == 1 && !wait_all(bar(L::B_V), (step - 1) & 1, abort, lim)) {
+              ok = false;
+              break;
+            }
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t y[32];
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           }
           tmem_wait_st();
         }
-        if ((TILES == 1 || t == 0) && c0 + 128 > len) {
+        if (t == 0 && c0 + 128 > len) {
           // the last tile: rows of V behind the sequence's end become zeros
           // before the product that P's arrival admits
           const uint32_t pos = 2 * step + (TILES == 1 && j + 1 < i1 - i0 ? 2 : 1), slot = pos % NS;
@@ -559,24 +561,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         mbar_arrive(bar(L::B_P + u));
       }
       if (!ok) break;
-      if (!wait_all(bar(L::B_O + u), nseg & 1, abort, lim)) break;
-      // TILES = 1: both groups learn each other's (m, l); each then merges and
-      // stores its half of the columns.  has[]: the group had a key tile here.
-      float f0 = 1.f, f1 = 0.f;
-      bool has0 = true, has1 = false;
-      if constexpr (TILES == 1) {
-        has0 = i1 - i0 > 1 || (step0 & 1) == 0;
-        has1 = i1 - i0 > 1 || (step0 & 1) == 1;
-        xml[u * 128 + r] = make_float2(m_ref, l);
-        mbar_arrive(bar(L::B_X + 0));
-        if (!wait_all(bar(L::B_X + 0), nseg & 1, abort, lim)) break;
-        const float2 a = xml[r], b = xml[128 + r];
-        m_ref = fmaxf(a.x, b.x);
-        const float mb = m_ref == -INFINITY ? 0.f : m_ref;
-        f0 = ex2_approx(a.x - mb);
-        f1 = ex2_approx(b.x - mb);
-        l = a.y * f0 + b.y * f1;
-      }
+      if (!wait_all(bar(L::B_O + t), nseg & 1, abort, lim)) break;
       ++nseg;
       tc_fence_after();
       if (!idle) {
@@ -587,16 +572,15 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         const bool final = out == 0 && !p.rec, f32 = !final || p.out_f32;
         float fo = 1.f, lse;
         if (live) {
-          const bool tell = TILES == 2 || u == 0;
           const long long row = static_cast<long long>(tok0 + tl) * p.hq + h * p.G + g;
           if (final) {
             row_final(m_ref, l, fo, lse);
-            if (tell) p.lse[static_cast<long long>(h * p.G + g) * p.n_tokens + tok0 + tl] = lse;
-          } else if (tell) {
+            p.lse[static_cast<long long>(h * p.G + g) * p.n_tokens + tok0 + tl] = lse;
+          } else {
             const long long pr = (static_cast<long long>(blockIdx.x) * 2 + out - 1) * (TILES * 128) + t * 128 + r;
             *reinterpret_cast<float2 *>(out ? p.part_ml + pr * 2 : p.dense_ml + row * 2) = make_float2(m_ref, l);
           }
-          if (p.rec && i0 == 0 && tell) p.rec[row] = Rec4{static_cast<int>(blockIdx.x), slot0, np, t * 128 + r};
+          if (p.rec && i0 == 0) p.rec[row] = Rec4{static_cast<int>(blockIdx.x), slot0, np, t * 128 + r};
         }
         uint8_t *dst[4];
 #pragma unroll
@@ -608,28 +592,9 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           dst[k] = xt < ntok ? base + (out ? pr : row) * (D * (f32 ? 4 : 2)) + q4 * 16 : nullptr;
         }
 #pragma unroll 1
-        for (int c = TILES == 1 ? u * (D / 64) : 0; c < (TILES == 1 ? (u + 1) * (D / 64) : D / 32); ++c) {
+        for (int c = 0; c < D / 32; ++c) {
           uint32_t y[32];
-          if constexpr (TILES == 1) {
-            const uint32_t at = tmem + lane_off + 256 + c * 32;
-            float z[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) z[k] = 0.f;
-            if (has0) {
-              tmem_ld32_wait(at, y);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) z[k] = __uint_as_float(y[k]) * f0;
-            }
-            if (has1) {
-              tmem_ld32_wait(at + 128, y);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) z[k] = fmaf(__uint_as_float(y[k]), f1, z[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(z[k]);
-          } else {
-            tmem_ld32_wait(tO + c * 32, y);
-          }
+          tmem_ld32_wait(tO + c * 32, y);
           if (f32) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -661,12 +626,6 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         }
       }
       tc_fence_before();      // O is read before the next segment's first product
-      if constexpr (TILES == 1) {
-        // by both groups, of both O
-        mbar_arrive(bar(L::B_X + 1));
-        if (!wait_all(bar(L::B_X + 1), (nseg - 1) & 1, abort, lim)) break;
-        tc_fence_after();
-      }
     }
   }
   tc_fence_before();
@@ -695,7 +654,9 @@ int encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, c
 template <int D, int TILES>
 int launch_tiles(PagedParams &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
   using L = TileLayout<D, TILES>;
-  if (L::bytes(p.n_seqs, false) > kSmemMax) return ATTN_ERR_UNSUPPORTED;    // above 4000 sequences
+  const int tpt = 128 / p.G;
+  p.warp_plan = TILES == 1 && p.n_seqs <= 32 && (!p.causal || p.n_tokens <= 64ll * tpt);
+  if (L::bytes(p, false) > kSmemMax) return ATTN_ERR_UNSUPPORTED;    // above 4000 sequences
   constexpr int kDev = 64;
   static bool done[kDev] = {};
   static std::mutex mu;
@@ -716,9 +677,8 @@ int launch_tiles(PagedParams &p, const CUtensorMap &mq, const CUtensorMap &mk, c
   p.min_span = 1;
   p.part_ml = p.part_o + paged_piece_floats(TILES * 128, D);
   p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * 2 * TILES * 128 * 2);
-  const int tpt = 128 / p.G;
-  const bool infos = L::bytes(p.n_seqs, true) <= kSmemMax;
-  const int rc = launch_after(kern, dim3(sms), L::THREADS, L::bytes(p.n_seqs, infos), s, mq, mk, mv, p, tpt, infos ? 1 : 0);
+  const bool infos = L::bytes(p, true) <= kSmemMax;
+  const int rc = launch_after(kern, dim3(sms), L::THREADS, L::bytes(p, infos), s, mq, mk, mv, p, tpt, infos ? 1 : 0);
   if (rc != ATTN_OK || p.rec) return rc;
   return launch_after(join, dim3(sms, TILES * 8), 256, 0, s, p);
 }
@@ -731,8 +691,7 @@ size_t paged_tiles_workspace(int d) {
 }
 
 // UNSUPPORTED, with nothing launched, where the tensor maps cannot say the
-// layout (more than 128 query heads a key/value head, strides of zero) or the
-// sequences' sums do not fit into shared memory.
+// layout (more than 128 query heads a key/value head, strides of zero).
 int paged_tiles_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
   if (p.G > 128) return ATTN_ERR_UNSUPPORTED;
   const int page = 1 << p.page_shift, tpt = 128 / p.G;

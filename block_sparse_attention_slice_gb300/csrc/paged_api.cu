@@ -62,6 +62,7 @@ int paged_check_seqs(const attn_seqs_t *s, int page_size) {
   if (!s || s->n_seqs < 0 || s->n_slots < 0 || s->max_pages < 0) return ATTN_ERR_INVALID_ARG;
   if (s->n_seqs > ATTN_PAGED_MAX_SEQS) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(s->max_pages) * page_size > ATTN_PAGED_MAX_LEN) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(s->max_pages) * page_size * s->n_seqs > ATTN_PAGED_MAX_KEYS) return ATTN_ERR_UNSUPPORTED;
   if (s->n_seqs == 0) return ATTN_OK;
   if (!s->table || !s->seq_lens) return ATTN_ERR_INVALID_ARG;
   if (!s->seqs && s->n_seqs > s->n_slots) return ATTN_ERR_INVALID_ARG;
@@ -86,7 +87,7 @@ int check_call(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int
   if (n_tokens == 0 || seqs->n_seqs == 0) return ATTN_OK;
   if (!q || !out || !lse) return ATTN_ERR_INVALID_ARG;
   if (!al16(q) || !al16(out)) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(n_tokens) * (hq / pages->hk) >= (int64_t(1) << 31)) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(n_tokens) * hq >= (int64_t(1) << 31)) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 

@@ -188,6 +188,13 @@ __device__ __forceinline__ int last_not_above(const int32_t *a, int n, int x) {
   return lo;
 }
 
+// Whether a record names pieces that the pass has.
+__device__ __forceinline__ bool in_bounds(const Rec4 &r, const PagedParams &p, int rows) {
+  const long long workers = static_cast<long long>(p.n_spans) * p.hp;
+  return r.np <= 0 || (r.np <= p.n_spans && r.worker >= 0 && r.worker + (r.np - 1ll) * p.hp < workers && (r.slot0 & ~1) == 0 &&
+                       r.row >= 0 && r.row < rows);
+}
+
 // Merges what two passes over the same rows left, the prefix's and that of
 // what follows it: a warp a row.  A row's records were written in this call
 // exactly if the row belongs to a sequence (and to a group), which is looked
@@ -211,9 +218,11 @@ __global__ void __launch_bounds__(256, 4) paged_join_pair_kernel(const PagedPara
   }
   after_previous();
   if (!mine) return;                               // of no sequence: left as it is
-  Rec4 a{0, 0, REC_EMPTY, 0};
+  Rec4 a{0, 0, REC_EMPTY, 0}, b = p.rec[row];
   if (grouped) a = pre.rec[row];
-  const Rec4 b = p.rec[row];
+  // a pass that gave up (a bounded wait ran out) left some records unwritten
+  if (!in_bounds(a, pre, pre_rows)) a.np = REC_EMPTY;
+  if (!in_bounds(b, p, rows)) b.np = REC_EMPTY;
   const int na = a.np < 0 ? 0 : a.np ? a.np : 1, nb = b.np < 0 ? 0 : b.np ? b.np : 1, np = na + nb;
   // row of piece i in its pass's pieces, or (np = 0) in the dense arrays
   auto place = [&](int i, bool &first, bool &dense) -> long long {

@@ -67,6 +67,7 @@ struct PagedParams {
   Cut *cuts;                  // [workers]
   int warp_plan;              // make_warp_plan, not make_plan
   int hp, n_spans, min_span;  // heads side by side; spans; key tiles a span holds at least
+  int test_stall;             // failure-path test: leave one load out
   unsigned int *status;
   unsigned long long wait_ns;
 };

@@ -19,11 +19,12 @@
 // others, fetches Q, K and V; one lane per page of a tile) and a warp that
 // issues the matrix instructions.
 //
-// What lies behind a sequence's end must not meet the zero weights of the P V
-// product: pages behind it, and pages that no row of the item sees, are
-// fetched from outside the tensor map, which reads as zeros, and the rows
-// behind the end in the last page are zeroed in shared memory by the softmax
-// warps of row tile 0 before they let the product begin.
+// Keys that no row of an item sees (behind the sequence's end, before the
+// window) must not meet the zero weights of the P V product, whatever memory
+// holds there: whole pages of them are fetched from outside the tensor map,
+// which reads as zeros, and their rows of V in pages that are fetched are zeroed
+// in shared memory by the softmax warps of row tile 0 before they let the
+// product begin.
 //
 // Numerics as in paged_rows.cu: 32-bit scores, maxima, sums and O; P rounded
 // to bf16 (half a step, 2^-9 of each weight either way) as the operand that the
@@ -33,6 +34,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <mutex>
 
 #include "attn_internal.h"
@@ -175,8 +177,9 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     bool ok = true;
     long long at = from;
     Walk<0, PT_KL> w;
+    // stands if the launch gives up, too: the join then reads no stale record
+    if (lane == 0 && !p.rec) p.cuts[blockIdx.x] = Cut{};
     if (at < to) w.seek(p, first, info, tpi, at);
-    else if (lane == 0 && !p.rec) p.cuts[blockIdx.x] = Cut{};
     const int R = min(1 << p.page_shift, 128), ppt = 128 / R, page_mask = (1 << p.page_shift) - 1;
     while (ok) {
       const int qs = nseg % PT_IQ;
@@ -259,6 +262,12 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         const int slot = ld % NS;
         if (ld >= NS && !wait_all(bar(L::B_EMPTY + slot), (ld / NS - 1) & 1, abort, lim)) {
           ok = false;
+          return;
+        }
+        // failure-path test only: every CTA leaves its second load out, so that
+        // the issuer's bounded wait for it runs out
+        if (p.test_stall && ld == 1) {
+          ++ld;
           return;
         }
         if (lane == 0) mbar_arrive_expect_tx(bar(L::B_FULL + slot), L::TILE);
@@ -449,6 +458,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       const int out = s->out, tok0 = s->tok0 + t * tpt, ntok = min(tpt, s->ntok - t * tpt), h = s->h, pos0 = s->pos0 + t * tpt,
                 len = s->len, i0 = s->i0, i1 = s->i1, np = s->np, slot0 = s->slot0, rot = s->rot;
       const Span sp{s->ns, s->w0, 0};
+      const int it_ntok = s->ntok;         // of both row tiles
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::B_IE + qs));
       if (out < 0) break;
@@ -544,17 +554,22 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           }
           tmem_wait_st();
         }
-        if (t == 0 && c0 + 128 > len) {
-          // the last tile: rows of V behind the sequence's end become zeros
-          // before the product that P's arrival admits
+        // keys that no row of the item sees, if the tile has any: their rows of V
+        // become zeros before the product that P's arrival admits
+        const int it_end = p.causal ? pos0 + it_ntok : len, it_lo = p.causal && p.window > 0 ? pos0 - p.window + 1 : 0;
+        if (t == 0 && masked && (c0 + 128 > it_end || (c0 < it_lo && c0 + 128 > p.sinks))) {
           const uint32_t pos = 2 * step + (TILES == 1 && j + 1 < i1 - i0 ? 2 : 1), slot = pos % NS;
           if (!wait_all(bar(L::B_FULL + slot), (pos / NS) & 1, abort, lim)) {
             ok = false;
             break;
           }
-          for (int hh = 0; hh < L::NHALF; ++hh)
-            for (int y = max(len - c0, 0) * 128 + r * 16; y < 128 * 128; y += 128 * 16)
-              st_shared_v4(kv_smem + slot * L::TILE + hh * L::HALF + y, make_uint4(0u, 0u, 0u, 0u));
+#pragma unroll 1
+          for (int x = r * 16; x < 128 * 128; x += 128 * 16) {
+            const int key = c0 + (x >> 7);
+            if (key < it_end && (key >= it_lo || key < p.sinks)) continue;
+            for (int hh = 0; hh < L::NHALF; ++hh)
+              st_shared_v4(kv_smem + slot * L::TILE + hh * L::HALF + x, make_uint4(0u, 0u, 0u, 0u));
+          }
           fence_proxy_async_smem();
         }
         tc_fence_before();
@@ -694,6 +709,10 @@ size_t paged_tiles_workspace(int d) {
 // layout (more than 128 query heads a key/value head, strides of zero).
 int paged_tiles_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
   if (p.G > 128) return ATTN_ERR_UNSUPPORTED;
+  // ATTN_TEST_STALL_PAGED=1 in the environment: the launch ends by its bounded
+  // waits running out, which is how the tests drive its abort path
+  const char *stall = std::getenv("ATTN_TEST_STALL_PAGED");
+  p.test_stall = stall && stall[0] == '1';
   const int page = 1 << p.page_shift, tpt = 128 / p.G;
   CUtensorMap mq, mk, mv;
   int rc;

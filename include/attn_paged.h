@@ -41,6 +41,7 @@ extern "C" {
 
 #define ATTN_PAGED_MAX_SEQS 4096     /* sequences (or groups) of one call      */
 #define ATTN_PAGED_MAX_LEN (1 << 30) /* max_pages * page_size                  */
+#define ATTN_PAGED_MAX_KEYS (INT64_C(1) << 36) /* n_seqs * max_pages * page_size */
 #define ATTN_CACHE_MAX_SLOTS 16384   /* rows of a cache's page table           */
 #define ATTN_CACHE_MAX_PAGES (1 << 30)
 #define ATTN_CACHE_MAX_POOLS 256     /* page arrays of one attn_cache_copy_pages */
@@ -82,13 +83,19 @@ int attn_paged_workspace_bytes(int n_tokens, int hq, int d, int prefix, size_t *
  *   out       [n_tokens, hq, d] bf16 or f32: softmax(scale q k^T) v over them
  *   lse       [hq, n_tokens] f32: ln sum exp(scale q.k)
  * A token that sees nothing (L = 0, or i < 0) gets out = 0, lse = -inf.
- * Cached rows at and behind L are never used, whatever they hold.
+ * Cached rows at and behind L, and those that no token of the sequence sees,
+ * are never used, whatever they hold.  (A key that some tokens of a sequence
+ * see and others do not is masked for those by a weight of zero: a value of it
+ * that is not finite can reach them, as in attn_fwd.)
  * Errors: INVALID_ARG; UNSUPPORTED (d not 64 or 128, page size, strides,
  * alignment, n_seqs > ATTN_PAGED_MAX_SEQS, max_pages * page_size >
- * ATTN_PAGED_MAX_LEN); CAPACITY (ws_bytes); CUDA.  On the device INVALID_ARG:
+ * ATTN_PAGED_MAX_LEN, times n_seqs > ATTN_PAGED_MAX_KEYS, n_tokens * hq >=
+ * 2^31); CAPACITY (ws_bytes); CUDA.  On the device INVALID_ARG:
  * a slot, length, q_ptr entry or needed page index out of range.  A sequence
  * with a bad slot, length or q_ptr is taken as one of length 0 or of no
- * tokens; one with a bad page gets outputs of no meaning; others are served. */
+ * tokens; one with a bad page gets outputs of no meaning; others are served.
+ * TIMEOUT where a bounded wait of the tensor-core kernel ran out
+ * (attn_set_wait_limit_ns): outputs are then incomplete. */
 int attn_paged_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
                    const attn_pages_t *pages, const attn_seqs_t *seqs, float scale, int window,
                    int sinks, void *out, int out_dtype, float *lse, void *d_ws, size_t ws_bytes,

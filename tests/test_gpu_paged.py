@@ -8,7 +8,7 @@ import torch
 import oracle
 import paged_cases as P
 from block_sparse_attention_slice_gb300 import (attn_build_tiles, attn_bwd, attn_fwd, attn_last_device_error, attn_paged_fwd,
-                                                attn_prefix_fwd, attn_slices_from_windows)
+                                                attn_prefix_fwd, attn_set_wait_limit_ns, attn_slices_from_windows)
 from block_sparse_attention_slice_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
@@ -121,14 +121,74 @@ def test_no_prefix_at_all_equals_the_paged_call():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_infinite_value_in_a_key_outside_the_window_is_not_met():
-    # token 30 is no key of the last token's window of 40 at length 100, nor
-    # one of its tile's when tiles end at multiples of 16
-    c = P.make([128], [1], 16, 4, 1, 64, seed=2)
-    j = 30
-    c["v"][c["table"][0, j // 16], j % 16] = float("inf")
-    out, lse = paged(c, 40, 4, q_ptr=None)
-    P.check(c, out, lse, P.reference(c, 40, 4))
+@pytest.mark.parametrize("lens,news,page,hq,hk,d,window,sinks", [
+    ([300, 47], [1, 1], 16, 8, 2, 128, 40, 4), ([300, 47], [1, 1], 16, 8, 2, 64, 40, 17), ([500], [1], 64, 8, 1, 128, 100, 3),
+    ([500, 90], [20, 30], 64, 8, 2, 128, 40, 5), ([500, 90], [70, 3], 16, 2, 2, 64, 64, 0), ([900], [300], 128, 4, 1, 128, 70, 9)])
+@pytest.mark.parametrize("garbage", [float("nan"), float("inf")])
+def test_keys_that_no_token_sees_are_not_met(lens, news, page, hq, hk, d, window, sinks, garbage):
+    # whatever stands in cached keys and values before the window of a
+    # sequence's first new token (and behind the first tokens)
+    c = P.make(lens, news, page, hq, hk, d, seed=2, garbage=garbage)
+    for b, (n, new) in enumerate(zip(lens, news)):
+        for j in range(sinks, max(sinks, n - new - window + 1)):
+            for x in "kv":
+                c[x][int(c["table"][b, j // page]), j % page] = garbage
+    out, lse = paged(c, window, sinks, max_q=max(news))
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c, window, sinks))
+
+
+def test_more_heads_to_a_group_than_a_row_tile_holds():
+    c = P.make([200, 20], [3, 1], 32, 130, 1, 64, seed=6)
+    out, lse = paged(c, 50, 2, max_q=3)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c, 50, 2))
+
+
+def test_rows_of_no_sequence_are_left_by_the_prefix_call():
+    c = P.make([5, 9, 33], [2, 1, 30], 16, 8, 2, 128, seed=3, plens=[100, 40], first=[0, 1, 3], slots=[4, 0, 2], extra_tokens=2)
+    T = c["q"].shape[0]
+    out = torch.full((T, 8, 128), 7.0, dtype=torch.float32, device="cuda")
+    lse = torch.full((8, T), 7.0, device="cuda")
+    prefix(c, out=out, lse=lse)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c))
+    for x in (out[:2], out[-2:], lse[:, :2], lse[:, -2:]):
+        assert torch.all(x == 7.0)
+
+
+def test_prefix_bad_groups_read_nothing_out_of_range():
+    c = P.make([5, 9, 33], [2, 1, 30], 16, 8, 2, 128, seed=3, plens=[100, 40], first=[0, 1, 3])
+    for bad in ([0, 5, 3], [2, 1, 3], [-1, 1, 3], [0, 1, 99]):
+        c["d_first"].copy_(torch.tensor(bad, dtype=torch.int32))
+        prefix(c)
+        assert attn_last_device_error() == B.ATTN_ERR_INVALID_ARG
+    c["d_first"].copy_(torch.from_numpy(c["first"]))
+    P.check(c, *prefix(c), P.reference(c))
+    assert attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("news", [6, 100])       # one row tile an item, two
+def test_a_load_that_never_comes_ends_in_a_timeout(news, monkeypatch):
+    # with ATTN_TEST_STALL_PAGED=1 every CTA leaves its second load out: the
+    # bounded wait for it runs out, all roles leave their waits, tensor memory
+    # is freed and the status says so; the next call is as before
+    c = P.make([5000, 3000], [news, news], 64, 16, 2, 128, seed=7)
+    pre = P.make([news, news], [news, news], 64, 16, 2, 128, seed=7, plens=[4000], first=[0, 2])
+    a, b = paged(c), prefix(pre)
+    assert attn_last_device_error() == 0
+    attn_set_wait_limit_ns(50_000_000)
+    monkeypatch.setenv("ATTN_TEST_STALL_PAGED", "1")
+    try:
+        for call in (lambda: paged(c), lambda: prefix(pre)):
+            call()
+            assert attn_last_device_error() == B.ATTN_ERR_TIMEOUT
+    finally:
+        monkeypatch.delenv("ATTN_TEST_STALL_PAGED")
+        attn_set_wait_limit_ns(4_000_000_000)
+    for x, y in zip(a + b, paged(c) + prefix(pre)):
+        assert torch.equal(x, y)
+    assert attn_last_device_error() == 0
 
 
 def test_another_stream_and_a_captured_call():

@@ -147,6 +147,10 @@ def test_refusals_of_one_call(lib):
         a = _args()
         a["seqs"].max_pages = a["seqs"].table_stride = (1 << 26) + 1
         assert _call(lib, a, prefix) == UNS
+        a = _args()
+        a["seqs"].seqs, a["seqs"].n_seqs, a["seqs"].max_pages, a["seqs"].table_stride = 4096, 4096, 1 << 21, 1 << 21
+        assert _call(lib, a, prefix) == UNS
+        assert _call(lib, _args(n_tokens=1 << 29, hq=4), prefix) == UNS
         # an empty batch is no error and launches nothing
         assert _call(lib, _args(n_tokens=0), prefix) == B.ATTN_OK
         a = _args(n_tokens=0, q=None, out=None, lse=None, ws=None, q_ptr=None)

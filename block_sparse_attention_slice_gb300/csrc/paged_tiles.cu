@@ -9,12 +9,16 @@
 // and the tensor core works on one while the softmax warps of the other run
 // (the order of attn_fwd: PV_0(j), QK_0(j+1), PV_1(j), QK_1(j+1)).  TILES = 1,
 // for items of at most TPT tokens: one row tile with two score buffers, QK(j+1)
-// issued before softmax(j) ends.  Bound by the tensor core when an item's rows
-// fill its tiles, by the cache's bandwidth when they do not.
+// issued before softmax(j) ends, and the 128 keys of a tile shared by two
+// softmax groups of 64, each with its own maximum, sum and O, which are merged
+// when the segment ends: with few rows the step is one warp's pass over a row
+// of scores, and halving the row halves it.  Bound by the tensor core and the
+// softmax when an item's rows fill its tiles, by the cache's bandwidth when they
+// do not.
 //
 // One persistent CTA per SM takes an equal span of the flat list of 128-key
 // tiles (paged_plan.cuh); pieces of items that cross spans are joined by
-// paged_join_kernel.  Warps: 4 softmax warps a row tile (thread = row = tensor
+// paged_join_kernel.  Warps: two groups of 4 softmax warps (thread = row = tensor
 // memory lane), a producer warp (walks the list, publishes each segment to the
 // others, fetches Q, K and V; one lane per page of a tile) and a warp that
 // issues the matrix instructions.
@@ -54,11 +58,12 @@ struct TileLayout {
   static constexpr int BAR_OFF = SEG_OFF + PT_IQ * 64;
   static constexpr int B_Q = 0, B_QE = 1, B_FULL = 2, B_EMPTY = B_FULL + NS, B_S = B_EMPTY + NS, B_P = B_S + 2,
                        B_O = B_P + 2, B_IF = B_O + TILES, B_IE = B_IF + PT_IQ, B_DRAIN = B_IE + PT_IQ,
-                       B_V = B_DRAIN + 1, NBAR = B_V + 1;
+                       B_V = B_DRAIN + 1, B_X = B_V + 1, NBAR = B_X + 2;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
-  static constexpr int SCAN_OFF = MISC_OFF + 16;
+  static constexpr int XML_OFF = MISC_OFF + 16;               // TILES = 1: (m, l) of both groups
+  static constexpr int SCAN_OFF = XML_OFF + (TILES == 1 ? 2 * 128 * 8 : 0);
   static constexpr int FIRST_OFF = SCAN_OFF + 16 * 8;
-  static constexpr int THREADS = TILES * 128 + 64;
+  static constexpr int THREADS = 256 + 64;
   static size_t bytes(const PagedParams &p, bool infos) {
     return 1024 + FIRST_OFF + (p.warp_plan ? THREADS / 32 * static_cast<size_t>(PLAN_WARP)
                                            : 8ull * (p.n_seqs + 1) + (infos ? sizeof(SeqInfo) * p.n_seqs : 0));
@@ -126,7 +131,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpi = tpt * TILES;
   const uint64_t lim = p.wait_ns;
-  constexpr int WP = TILES * 4, WM = TILES * 4 + 1;       // producer, issuer
+  constexpr int WP = 8, WM = 9;       // producer, issuer
 
   if (threadIdx.x == 0) {
     mbar_init(bar(L::B_Q), 1);
@@ -137,12 +142,13 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(L::B_S + t), 1);
-      mbar_init(bar(L::B_P + t), 128);
+      mbar_init(bar(L::B_P + t), TILES == 1 ? 256 : 128);
+      mbar_init(bar(L::B_X + t), 256);
     }
     for (int t = 0; t < TILES; ++t) mbar_init(bar(L::B_O + t), 1);
     for (int u = 0; u < PT_IQ; ++u) {
       mbar_init(bar(L::B_IF + u), 1);
-      mbar_init(bar(L::B_IE + u), TILES * 4 + 1);
+      mbar_init(bar(L::B_IE + u), 9);
     }
     mbar_init(bar(L::B_DRAIN), 1);
     mbar_init(bar(L::B_V), 1);
@@ -381,7 +387,14 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
               break;
             }
             tc_fence_after();
-            issue_pv(0, step & 1, k.slot, j == 0);
+            // each group's 64 keys into its own O
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(tmem + 256 + u * 128, tmem + (step & 1) * 128 + u * 64 + kk * 8,
+                       smem_desc_sw128(kv_smem + k.slot * L::TILE + (u * 64 + kk * 16) * 128, L::HALF, 1024), IDESC_PV,
+                       (j == 0 && kk == 0) ? 0u : 1u);
+            }
             mma_commit(bar(L::B_EMPTY + k.slot));
             mma_commit(bar(L::B_V));
             if (j + 1 == n) mma_commit(bar(L::B_O));
@@ -444,9 +457,13 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     __syncwarp();
   } else {
     // --------------------------------------------------------------- softmax
-    const int t = TILES == 1 ? 0 : warp >> 2, wl = warp & 3, r = wl * 32 + lane;
+    // grp: softmax group and its O; t: row tile.  A group takes NC columns of a
+    // tile's scores.
+    constexpr int NC = TILES == 1 ? 64 : 128;
+    const int grp = warp >> 2, t = TILES == 1 ? 0 : grp, wl = warp & 3, r = wl * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wl * 32) << 16;
-    const uint32_t tO = tmem + lane_off + 256 + t * 128;
+    const uint32_t tO = tmem + lane_off + 256 + grp * 128;
+    float2 *xml = reinterpret_cast<float2 *>(smem + L::XML_OFF);
     const float sl2 = p.scale_log2;
     const int tl = r / p.G, g = r - tl * p.G;               // token and head of this row in its tile
     uint32_t step = 0, nseg = 0;
@@ -470,7 +487,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       for (int j = 0; j < i1 - i0; ++j, ++step) {
         const int u = TILES == 1 ? step & 1 : t;
         const uint32_t ph = TILES == 1 ? (step >> 1) & 1 : step & 1;
-        const uint32_t tS = tmem + lane_off + u * 128;
+        const uint32_t tS = tmem + lane_off + u * 128 + (TILES == 1 ? grp * 64 : 0);
         const int c0 = Seg::key_tile(j, i0, i1, rot, sp) << PT_KL;
         const bool masked = c0 + 128 > all_hi || (c0 < all_lo && c0 + 128 > p.sinks);
         uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -484,28 +501,32 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         }
         tc_fence_after();
         if (!idle) {
-          float x[PT_BN];
+          float x[NC];
           {
-            uint32_t y[PT_BN];
+            uint32_t y[NC];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&y[c * 32]));
+            for (int c = 0; c < NC / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&y[c * 32]));
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < PT_BN; ++k) {
+            for (int k = 0; k < NC; ++k) {
               asm volatile("" : "+r"(y[k]));
               x[k] = __uint_as_float(y[k]);
             }
           }
           if (masked) {
+            if (TILES == 1 && grp == 1) {
+              w[0] = w[2];
+              w[1] = w[3];
+            }
 #pragma unroll
-            for (int k = 0; k < PT_BN; ++k)
+            for (int k = 0; k < NC; ++k)
               if (!((w[k >> 5] >> (k & 31)) & 1u)) x[k] = -INFINITY;
           }
           float m4[4];
 #pragma unroll
           for (int v = 0; v < 4; ++v) m4[v] = fmaxf(x[2 * v], x[2 * v + 1]);
 #pragma unroll
-          for (int k = 8; k < PT_BN; k += 8) {
+          for (int k = 8; k < NC; k += 8) {
 #pragma unroll
             for (int v = 0; v < 4; ++v) m4[v] = max3f(m4[v], x[k + 2 * v], x[k + 2 * v + 1]);
           }
@@ -519,7 +540,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           const uint64_t sc2 = f2_make(sl2, sl2), nb2 = f2_make(-mb, -mb);
           uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < NC / 32; ++c) {
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -557,7 +578,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         // keys that no row of the item sees, if the tile has any: their rows of V
         // become zeros before the product that P's arrival admits
         const int it_end = p.causal ? pos0 + it_ntok : len, it_lo = p.causal && p.window > 0 ? pos0 - p.window + 1 : 0;
-        if (t == 0 && masked && (c0 + 128 > it_end || (c0 < it_lo && c0 + 128 > p.sinks))) {
+        if (grp == 0 && masked && (c0 + 128 > it_end || (c0 < it_lo && c0 + 128 > p.sinks))) {
           const uint32_t pos = 2 * step + (TILES == 1 && j + 1 < i1 - i0 ? 2 : 1), slot = pos % NS;
           if (!wait_all(bar(L::B_FULL + slot), (pos / NS) & 1, abort, lim)) {
             ok = false;
@@ -577,6 +598,20 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       }
       if (!ok) break;
       if (!wait_all(bar(L::B_O + t), nseg & 1, abort, lim)) break;
+      // TILES = 1: both groups learn each other's (m, l); each then merges and
+      // stores its half of the columns
+      float f0 = 1.f, f1 = 0.f;
+      if constexpr (TILES == 1) {
+        xml[grp * 128 + r] = make_float2(m_ref, l);
+        mbar_arrive(bar(L::B_X + 0));
+        if (!wait_all(bar(L::B_X + 0), nseg & 1, abort, lim)) break;
+        const float2 a = xml[r], b = xml[128 + r];
+        m_ref = fmaxf(a.x, b.x);
+        const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+        f0 = ex2_approx(a.x - mb);
+        f1 = ex2_approx(b.x - mb);
+        l = a.y * f0 + b.y * f1;
+      }
       ++nseg;
       tc_fence_after();
       if (!idle) {
@@ -586,16 +621,17 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         const int q4 = lane & 3;
         const bool final = out == 0 && !p.rec, f32 = !final || p.out_f32;
         float fo = 1.f, lse;
+        const bool tell = TILES == 2 || grp == 0;
         if (live) {
           const long long row = static_cast<long long>(tok0 + tl) * p.hq + h * p.G + g;
           if (final) {
             row_final(m_ref, l, fo, lse);
-            p.lse[static_cast<long long>(h * p.G + g) * p.n_tokens + tok0 + tl] = lse;
-          } else {
+            if (tell) p.lse[static_cast<long long>(h * p.G + g) * p.n_tokens + tok0 + tl] = lse;
+          } else if (tell) {
             const long long pr = (static_cast<long long>(blockIdx.x) * 2 + out - 1) * (TILES * 128) + t * 128 + r;
             *reinterpret_cast<float2 *>(out ? p.part_ml + pr * 2 : p.dense_ml + row * 2) = make_float2(m_ref, l);
           }
-          if (p.rec && i0 == 0) p.rec[row] = Rec4{static_cast<int>(blockIdx.x), slot0, np, t * 128 + r};
+          if (p.rec && i0 == 0 && tell) p.rec[row] = Rec4{static_cast<int>(blockIdx.x), slot0, np, t * 128 + r};
         }
         uint8_t *dst[4];
 #pragma unroll
@@ -607,9 +643,21 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           dst[k] = xt < ntok ? base + (out ? pr : row) * (D * (f32 ? 4 : 2)) + q4 * 16 : nullptr;
         }
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = TILES == 1 ? grp * (D / 64) : 0; c < (TILES == 1 ? (grp + 1) * (D / 64) : D / 32); ++c) {
           uint32_t y[32];
-          tmem_ld32_wait(tO + c * 32, y);
+          if constexpr (TILES == 1) {
+            uint32_t z[32];
+            tmem_ld32(tmem + lane_off + 256 + c * 32, y);
+            tmem_ld32(tmem + lane_off + 384 + c * 32, z);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              asm volatile("" : "+r"(y[k]), "+r"(z[k]));
+              y[k] = __float_as_uint(fmaf(__uint_as_float(y[k]), f0, __uint_as_float(z[k]) * f1));
+            }
+          } else {
+            tmem_ld32_wait(tO + c * 32, y);
+          }
           if (f32) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -641,6 +689,12 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         }
       }
       tc_fence_before();      // O is read before the next segment's first product
+      if constexpr (TILES == 1) {
+        // both O by both groups
+        mbar_arrive(bar(L::B_X + 1));
+        if (!wait_all(bar(L::B_X + 1), (nseg - 1) & 1, abort, lim)) break;
+        tc_fence_after();
+      }
     }
   }
   tc_fence_before();

@@ -491,9 +491,13 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         const int c0 = Seg::key_tile(j, i0, i1, rot, sp) << PT_KL;
         const bool masked = c0 + 128 > all_hi || (c0 < all_lo && c0 + 128 > p.sinks);
         uint32_t w[4] = {0u, 0u, 0u, 0u};
+        bool clear = false;
         if (masked) {
           or_span(max(lo, 0), hi, c0, w);
           if (lo > 0) or_span(0, min(p.sinks, hi), c0, w);
+          // does the tile hold keys that no row of the item sees?
+          const int it_end = p.causal ? pos0 + it_ntok : len, it_lo = p.causal && p.window > 0 ? pos0 - p.window + 1 : 0;
+          clear = grp == 0 && (c0 + 128 > it_end || (c0 < it_lo && c0 + 128 > p.sinks));
         }
         if (!wait_all(bar(L::B_S + u), ph, abort, lim)) {
           ok = false;
@@ -575,10 +579,9 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           }
           tmem_wait_st();
         }
-        // keys that no row of the item sees, if the tile has any: their rows of V
-        // become zeros before the product that P's arrival admits
-        const int it_end = p.causal ? pos0 + it_ntok : len, it_lo = p.causal && p.window > 0 ? pos0 - p.window + 1 : 0;
-        if (grp == 0 && masked && (c0 + 128 > it_end || (c0 < it_lo && c0 + 128 > p.sinks))) {
+        if (clear) {
+          // their rows of V become zeros before the product that P's arrival admits
+          const int it_end = p.causal ? pos0 + it_ntok : len, it_lo = p.causal && p.window > 0 ? pos0 - p.window + 1 : 0;
           const uint32_t pos = 2 * step + (TILES == 1 && j + 1 < i1 - i0 ? 2 : 1), slot = pos % NS;
           if (!wait_all(bar(L::B_FULL + slot), (pos / NS) & 1, abort, lim)) {
             ok = false;

@@ -127,7 +127,8 @@ attn_stream_t stream_of(PyObject *o, at::Device device) {
   return static_cast<attn_stream_t>(p);
 }
 
-// Calls f() on `device`, without the interpreter's lock, and raises its error.
+// Calls f() on `device`, without the interpreter's lock (f neither throws nor
+// refuses), and raises its error.
 template <typename F>
 void call(const char *name, at::Device device, F f) {
   int code;
@@ -268,10 +269,11 @@ PyObject *prefix_fwd(PyObject *const *a) {
 PyObject *cache_extend(PyObject *const *a) {
   const CacheArg c = cache_of(a[0], a[1], a[2], a[5]);
   const Tensor &seqs = tensor(a[3], "seqs"), &counts = tensor(a[4], "counts");
-  const int32_t *s = ints(&seqs, "seqs", c.device), *n = ints(&counts, "counts", c.device);
+  const int32_t *s = ints(&seqs, "seqs", c.device), *add = ints(&counts, "counts", c.device);
   if (seqs.size(0) != counts.size(0)) refuse("seqs and counts must be of one length");
+  const int n = narrow(seqs.size(0), "n");
   attn_stream_t st = stream_of(a[6], c.device);
-  call("attn_cache_extend", c.device, [&] { return attn_cache_extend(&c.c, s, n, narrow(seqs.size(0), "n"), st); });
+  call("attn_cache_extend", c.device, [&] { return attn_cache_extend(&c.c, s, add, n, st); });
   Py_RETURN_NONE;
 }
 

@@ -143,6 +143,16 @@ def test_bad_lists_change_nothing(what):
     b.same(B.ATTN_ERR_INVALID_ARG)
 
 
+def test_lists_of_more_entries_than_32_bits_count_are_refused():
+    b = Both(2, 2, 4, 16)
+    x = torch.empty(2 ** 31, dtype=torch.int32, device="cuda")
+    for call in (lambda: attn_cache_extend(*b.c, x, x, b.page), lambda: attn_cache_free(*b.c, x, b.page),
+                 lambda: attn_cache_trim(*b.c, b.page, 1, 0, x), lambda: attn_cache_fork(*b.c, x, x, b.page)):
+        with pytest.raises(ValueError, match="out of range"):
+            call()
+    b.same()
+
+
 def test_bad_lengths_and_pages_are_not_followed():
     b = Both(4, 4, 10, 16)
     b.extend([0, 1], [40, 16])

@@ -370,8 +370,9 @@ __device__ inline void finish_empty(const PagedParams &p, const SeqInfo *info, i
       tile_tokens<ROWS>(rt, s.nq, p.G, tpi, a, z);
       if (key_span<KL>(p, s, a, z).n > 0) break;
       const int rows = ROWS > 0 ? min(ROWS, s.nq * p.G - rt * ROWS) : (z - a + 1) * p.G;
-      for (int x = threadIdx.x; x < rows * p.hk * (D / 2); x += blockDim.x) {
-        const int c = x % (D / 2) * 2, y = x / (D / 2), h = y / rows, r = y - h * rows + (ROWS > 0 ? rt * ROWS : a * p.G);
+      for (long long x = threadIdx.x; x < static_cast<long long>(rows) * p.hk * (D / 2); x += blockDim.x) {
+        const int c = static_cast<int>(x % (D / 2)) * 2, y = static_cast<int>(x / (D / 2)), h = y / rows,
+                  r = y - h * rows + (ROWS > 0 ? rt * ROWS : a * p.G);
         const int t = r / p.G, head = h * p.G + r - t * p.G;
         const long long row = static_cast<long long>(s.q0 + t) * p.hq + head;
         if (p.rec) {

@@ -138,6 +138,18 @@ def test_keys_that_no_token_sees_are_not_met(lens, news, page, hq, hk, d, window
     P.check(c, out, lse, P.reference(c, window, sinks))
 
 
+def test_rows_that_see_nothing_past_32_bits_of_outputs():
+    # 256 tokens of 2^18 heads of an empty sequence: 2^32 outputs of one item's rows
+    hq, n = 1 << 18, 256
+    kv = torch.zeros((2, 1, 16, hq, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((n, hq, 64), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    out, lse = attn_paged_fwd(q, kv[0], kv[1], ints(0).view(1, 1), ints(0), 0.125, q_ptr=ints(0, n), out=out)
+    assert attn_last_device_error() == 0
+    assert not out.any() and bool((lse == -torch.inf).all())
+
+
 def test_more_heads_to_a_group_than_a_row_tile_holds():
     c = P.make([200, 20], [3, 1], 32, 130, 1, 64, seed=6)
     out, lse = paged(c, 50, 2, max_q=3)

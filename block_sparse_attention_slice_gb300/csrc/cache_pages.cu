@@ -768,6 +768,10 @@ int attn_cache_write(const attn_pages_t *pages, const attn_seqs_t *seqs, const i
   if (!k_new || !v_new) return ATTN_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15) return ATTN_ERR_UNSUPPORTED;
   if ((new_token_stride | new_head_stride) & 7 || new_token_stride < 0 || new_head_stride < 0) return ATTN_ERR_UNSUPPORTED;
+  // one place of memory seen as several is fine to read, not to write
+  if ((pages->page_stride == 0 && pages->n_pages > 1) || pages->token_stride == 0 || (pages->head_stride == 0 && pages->hk > 1))
+    return ATTN_ERR_UNSUPPORTED;
+  if (n_tokens > ATTN_PAGED_MAX_LEN) return ATTN_ERR_UNSUPPORTED;
   WriteParams p;
   p.k = static_cast<uint16_t *>(const_cast<void *>(pages->k));
   p.v = static_cast<uint16_t *>(const_cast<void *>(pages->v));

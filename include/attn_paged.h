@@ -210,7 +210,9 @@ int attn_cache_copy_pages(void *const *h_pools, int n_pools, size_t page_bytes,
  *   k_new, v_new  [n_tokens, hk, d] bf16, 16-byte aligned, strides in elements
  *                 and multiples of 8, d contiguous
  * Tokens of no sequence are not read; a token whose slot, position or page is
- * out of range is not written (INVALID_ARG on the device). */
+ * out of range is not written (INVALID_ARG on the device).  Where `seqs` names a
+ * row twice, both write its last positions, which then hold either's tokens.
+ * UNSUPPORTED also: pages with a stride of zero, n_tokens > ATTN_PAGED_MAX_LEN. */
 int attn_cache_write(const attn_pages_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr,
                      const void *k_new, const void *v_new, int n_tokens, int64_t new_token_stride,
                      int64_t new_head_stride, attn_stream_t stream);

@@ -222,6 +222,48 @@ def test_another_stream_and_a_captured_call():
     assert attn_last_device_error() == 0
 
 
+@pytest.mark.parametrize("news", [[1, 1, 1, 1], [3, 20, 1, 40]])
+def test_a_captured_prefix_call_reads_its_arrays_when_replayed(news):
+    lens = [n + 5 for n in news]
+    c = P.make(lens, news, 16, 8, 2, 128, seed=11, plens=[300, 45], first=[0, 2, 4])
+    s = torch.cuda.Stream()
+    out, lse = prefix(c, stream=s)
+    s.synchronize()
+    P.check(c, out, lse, P.reference(c))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = prefix(c)
+    # shorter prefixes, one of them empty, and a sequence whose first tokens see the prefix alone
+    for plens, lens in (([299, 0], lens), ([17, 45], [lens[0], 0, lens[2], lens[3] - 4])):
+        c["plens"], c["lens"] = np.asarray(plens, np.int32), np.asarray(lens, np.int32)
+        c["d_plens"].copy_(torch.from_numpy(c["plens"]))
+        c["d_lens"].copy_(torch.from_numpy(c["lens"]))
+        g.replay()
+        torch.cuda.synchronize()
+        P.check(c, out, lse, P.reference(c))
+    assert attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_a_row_of_the_table_named_twice(max_q):
+    c = P.make([70, 9, 200], [3, 3, 3], 32, 8, 2, 128, seed=5)
+    c["seqs"] = np.asarray([2, 2, 0], np.int32)
+    c["d_seqs"] = torch.from_numpy(c["seqs"]).cuda()
+    out, lse = paged(c, 33, 2, max_q=max_q)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c, 33, 2))
+
+
+def test_many_groups_of_many_sequences():
+    rng = np.random.default_rng(1)
+    n = 2000
+    first = np.sort(rng.integers(0, n + 1, 701)).tolist()       # empty groups among them
+    c = P.make(rng.integers(0, 30, n).tolist(), [1] * n, 16, 2, 1, 64, seed=1, plens=rng.integers(0, 60, 700).tolist(), first=first)
+    out, lse = prefix(c)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c))
+
+
 def test_two_calls_at_once_with_their_own_workspaces():
     c = P.make([3000, 40, 900], [1, 1, 1], 16, 8, 2, 128, seed=9)
     ref = P.reference(c)

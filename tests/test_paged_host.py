@@ -250,3 +250,11 @@ def test_copy_and_write_refusals(lib):
         assert write(**bad) == INV
     for bad in ({"k": ctypes.c_void_p(4104)}, {"ts": 100}, {"hs": 12}, {"ts": -256}, {"pages__page_size": 20}):
         assert write(**bad) == UNS
+
+
+def test_write_refuses_places_seen_as_several(lib):
+    for bad in ({"pages__page_stride": 0}, {"pages__token_stride": 0}, {"pages__head_stride": 0}):
+        a = _args(**bad)
+        assert lib.attn_cache_write(ctypes.byref(a["pages"]), ctypes.byref(a["seqs"]), X, X, X, 5, 256, 128, None) == UNS
+    a = _args()
+    assert lib.attn_cache_write(ctypes.byref(a["pages"]), ctypes.byref(a["seqs"]), X, X, X, (1 << 30) + 1, 0, 128, None) == UNS

@@ -91,6 +91,20 @@ int check_call(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int
   return ATTN_OK;
 }
 
+// Whether q or the memory that the pages span meets out, which is written while
+// they are read.
+bool meets_out(const void *q, int n_tokens, int hq, const attn_pages_t *g, const void *out, int out_dtype) {
+  const size_t n = static_cast<size_t>(n_tokens) * hq * g->d;
+  const char *ob = static_cast<const char *>(out), *oe = ob + n * (out_dtype == ATTN_DTYPE_F32 ? 4 : 2);
+  const size_t span = 2 * (static_cast<size_t>(g->n_pages - 1) * g->page_stride + static_cast<size_t>(g->page_size - 1) * g->token_stride +
+                           static_cast<size_t>(g->hk - 1) * g->head_stride + g->d);
+  auto meets = [&](const void *x, size_t bytes) {
+    const char *b = static_cast<const char *>(x);
+    return b < oe && ob < b + bytes;
+  };
+  return meets(q, 2 * n) || meets(g->k, span) || meets(g->v, span);
+}
+
 PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, const attn_pages_t *g,
                    const attn_seqs_t *s, float scale, int shift) {
   PagedParams p;
@@ -182,6 +196,7 @@ int attn_paged_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q,
   if (n_tokens == 0 || seqs->n_seqs == 0) return ATTN_OK;
   if (!d_ws) return ATTN_ERR_INVALID_ARG;
   if (!al16(d_ws)) return ATTN_ERR_UNSUPPORTED;
+  if (meets_out(q, n_tokens, hq, pages, out, out_dtype)) return ATTN_ERR_INVALID_ARG;
   size_t need = 0;
   if ((rc = attn_paged_workspace_bytes(n_tokens, hq, pages->d, 0, &need)) != ATTN_OK) return rc;
   if (ws_bytes < need) return ATTN_ERR_CAPACITY;
@@ -211,6 +226,7 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
   if (n_tokens == 0 || seqs->n_seqs == 0) return ATTN_OK;
   if (!d_ws) return ATTN_ERR_INVALID_ARG;
   if (!al16(d_ws)) return ATTN_ERR_UNSUPPORTED;
+  if (meets_out(q, n_tokens, hq, pages, out, out_dtype)) return ATTN_ERR_INVALID_ARG;
   size_t need = 0;
   if ((rc = attn_paged_workspace_bytes(n_tokens, hq, pages->d, 1, &need)) != ATTN_OK) return rc;
   if (ws_bytes < need) return ATTN_ERR_CAPACITY;

@@ -82,6 +82,8 @@ int attn_paged_workspace_bytes(int n_tokens, int hq, int d, int prefix, size_t *
  * keys j <= i with j > i - window or j < sinks; window = 0: every j <= i.
  *   out       [n_tokens, hq, d] bf16 or f32: softmax(scale q k^T) v over them
  *   lse       [hq, n_tokens] f32: ln sum exp(scale q.k)
+ * q and the memory between the pages' first byte and last must not overlap
+ * out (INVALID_ARG).
  * A token that sees nothing (L = 0, or i < 0) gets out = 0, lse = -inf.
  * Cached rows at and behind L, and those that no token of the sequence sees,
  * are never used, whatever they hold.  (A key that some tokens of a sequence

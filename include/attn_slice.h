@@ -276,17 +276,18 @@ int attn_bwd(const void *q, const void *k, const void *v, const void *out, int o
              size_t ws_bytes, attn_stream_t stream);
 
 /* Synchronises `stream`, then returns and clears the device-side failure
- * status of the metadata build, forward and backward kernels on the current
- * device: ATTN_OK, ATTN_ERR_TIMEOUT when a bounded wait ran out (a build's
- * grid barrier, a forward or backward pipeline stage), or the status of
- * refused metadata.  The first failure of each kernel family is kept.  The
+ * status of the metadata build, forward and backward kernels, and of those of
+ * attn_paged.h, on the current device: ATTN_OK, ATTN_ERR_TIMEOUT when a bounded
+ * wait ran out (a build's grid barrier, a forward, backward or paged pipeline
+ * stage), the status of refused metadata, or what a kernel of attn_paged.h found
+ * wrong with its device arrays.  The first failure of each kernel family is kept.  The
  * status words are per device, not per stream: a caller that runs launches
  * on several streams cannot tell from here which launch failed, and should
  * synchronise all of them before reading. */
 int attn_last_device_error(attn_stream_t stream);
 
-/* Sets the bound on every device-side wait of later attn_fwd launches on the
- * current process (nanoseconds; default 4e9).  Used to test the timeout path
+/* Sets the bound on every device-side wait of later launches of the current
+ * process (nanoseconds; default 4e9).  Used to test the timeout path
  * with a short limit. */
 int attn_set_wait_limit_ns(int64_t ns);
 

@@ -258,3 +258,15 @@ def test_write_refuses_places_seen_as_several(lib):
         assert lib.attn_cache_write(ctypes.byref(a["pages"]), ctypes.byref(a["seqs"]), X, X, X, 5, 256, 128, None) == UNS
     a = _args()
     assert lib.attn_cache_write(ctypes.byref(a["pages"]), ctypes.byref(a["seqs"]), X, X, X, (1 << 30) + 1, 0, 128, None) == UNS
+
+
+@pytest.mark.parametrize("prefix", [False, True])
+def test_outputs_on_top_of_inputs_are_refused(lib, prefix):
+    # q: 5 x 4 x 128 bf16 = 5120 bytes; pages: (9 x 4096 + 15 x 256 + 128 + 128) x 2 = 81920 bytes
+    p = lambda at: ctypes.c_void_p(at)  # noqa: E731
+    clear = dict(q=p(1 << 20), out=p((1 << 20) + 5120), ws=p(1 << 30))
+    assert _call(lib, _args(**clear), prefix) not in (INV, UNS)
+    for bad in (dict(q=p(1 << 20), out=p(1 << 20)), dict(q=p(1 << 20), out=p((1 << 20) + 5104)),
+                dict(q=p(1 << 20), out=p((1 << 20) - 10224), out_dtype=1), dict(q=p(1 << 20), out=p(4096 + 81904)),
+                dict(q=p(1 << 20), out=p(1 << 24), pages__v=(1 << 24) - 16)):
+        assert _call(lib, _args(**{**clear, **bad}), prefix) == INV

@@ -4,8 +4,13 @@
     out, lse   = attn_fwd(q, k, v, tiles, scale)           # softmax(scale QK^T + mask) V, row LSE
     out, lse   = attn_merge([o_1, o_2, ...], [lse_1, ...]) # exact KV-split merge
 
-All three run as hand-written CUDA kernels in ``libattn_slice.so`` (see
-``include/attn_slice.h``); this package only marshals arguments.
+    out, lse   = attn_paged_fwd(q, k_pages, v_pages, table, seq_lens, scale, ...)   # over a paged cache
+    out, lse   = attn_prefix_fwd(...)                      # groups that share a prefix
+    attn_cache_extend / write / fork / free / trim / compact / copy_pages           # that cache's pages
+
+All run as hand-written CUDA kernels in ``libattn_slice.so`` (see
+``include/attn_slice.h`` and ``include/attn_paged.h``); this package only
+marshals arguments.
 """
 from .binding import (ATTN_DTYPE_BF16, ATTN_DTYPE_F32, ATTN_FWD_TILE_K, ATTN_FWD_TILE_Q,
                       AttnError, Tiles, attn_build_tiles, attn_bwd, attn_fwd, attn_last_device_error,

@@ -6,7 +6,10 @@
 // of 1024 threads, whose hardware barrier (about a microsecond for both halves)
 // takes the place of grid barriers or further launches, and whose distributed
 // shared memory carries the counts between CTAs.  Nothing is kept between
-// calls.  Work over the sequences of a list is flattened: a block-wide prefix
+// calls.  32 rows of up to 128 pages fork in 8 us, 64 rows free and extend in 5
+// and 6; half a million pages take 68 us to free and extend, 137 to fork, bound
+// by the cluster's 8 SMs.  Clusters of 1, 2 or 4 CTAs gave the small calls 1 us
+// and the large ones up to 8 times their time.  Work over the sequences of a list is flattened: a block-wide prefix
 // sum of their page counts, then every thread takes flat indices 8192 apart and
 // finds its sequence by bisection in shared memory, so one long sequence costs
 // no more than many short ones.  Results are exact and do not depend on the
@@ -506,7 +509,10 @@ struct CopyParams {
 constexpr int COPY_T = 256, COPY_U = 4, COPY_CHUNK = COPY_T * COPY_U * 16;
 
 // Streams pages: a unit is 16 KB of one page of one pool, four 16-byte words a
-// thread, all loaded before the first is stored.
+// thread, all loaded before the first is stored.  Bound by HBM: 1570 pages of
+// 128 KB in 4 pools, 1646 MB read and written, in 265 us (6.2 TB/s; a plain copy
+// of as many bytes takes 240).  Bulk copies through shared memory took
+// 263 to 267, 8 words a thread 262 here and 7 % more on a fragmented pool.
 __global__ void __launch_bounds__(COPY_T) cache_copy_kernel(const __grid_constant__ CopyParams p) {
   after_previous();
   admit_next();
@@ -544,7 +550,9 @@ struct WriteParams {
 };
 
 // A warp takes tokens one by one: finds its sequence (32 candidates a step),
-// its page, and moves the rows of all heads.
+// its page, and moves the rows of all heads.  Bound by HBM and L2:
+// 42753 tokens of 8 heads of 128, keys and values (175 MB in and as many out, of
+// which L2 keeps a part), in 33 us.
 __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
   after_previous();
   admit_next();

@@ -107,6 +107,8 @@ struct Gather {
 // one warp a row.  Many (a long sequence alone in the batch): the block's
 // warps share a row's pieces and add their sums.  Pieces are added in a fixed
 // order, so results do not vary from run to run.
+// Bound by L2 and latency: its pieces were written just before.  12 us behind
+// 152 spans of 256 rows (38 MB of pieces), 3 us behind a single sequence.
 // PACKED: rows stand as they are counted; else 128 / G whole tokens to each
 // 128 rows.
 template <int D, int TILE_ROWS, bool PACKED>
@@ -199,7 +201,7 @@ __device__ __forceinline__ bool in_bounds(const Rec4 &r, const PagedParams &p, i
 // what follows it: a warp a row.  A row's records were written in this call
 // exactly if the row belongs to a sequence (and to a group), which is looked
 // up here, while the passes still run, rather than having the records cleared
-// before them.
+// before them.  9 us for 8192 rows of 128 columns, 7 for 6400 of 64.
 template <int D>
 __global__ void __launch_bounds__(256, 4) paged_join_pair_kernel(const PagedParams pre, const PagedParams p,
                                                                  const int pre_rows, const int rows) {

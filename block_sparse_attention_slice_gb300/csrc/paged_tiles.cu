@@ -11,10 +11,18 @@
 // for items of at most TPT tokens: one row tile with two score buffers, QK(j+1)
 // issued before softmax(j) ends, and the 128 keys of a tile shared by two
 // softmax groups of 64, each with its own maximum, sum and O, which are merged
-// when the segment ends: with few rows the step is one warp's pass over a row
-// of scores, and halving the row halves it.  Bound by the tensor core and the
-// softmax when an item's rows fill its tiles, by the cache's bandwidth when they
-// do not.
+// when the segment ends: with few rows a step is one warp's pass over a row of
+// scores, and half the row took 1 to 6 % off calls of 24 to 128 rows against one
+// group for the whole tile (1 % more on very long calls at head dim 64).
+//
+// What bounds it.  Rows that fill their tiles: the chain of products and softmax
+// that attn_fwd has.  4 x 1021 new tokens, window 4096, 32 query and 8 key/value
+// heads of 128 columns: 173 us, 73 steps a CTA of 256 rows by 128 keys at 1.70 us
+// (1.5 PFLOP/s over all SMs; tensor pipe 51 % active over the launch), and
+// around them 10 us before the first product, 4.4 at a change of item, 12 for
+// the join.  256 rows of a group's sequences against a prefix of 32768 keys: 107
+// of the call's 174 us.  A 128-key step of TILES = 1 at head dim 64 takes 0.85 to
+// 0.9 us (100 rows, 16384 keys, 16 heads, 4 groups: 36 us).
 //
 // One persistent CTA per SM takes an equal span of the flat list of 128-key
 // tiles (paged_plan.cuh); pieces of items that cross spans are joined by
@@ -31,7 +39,7 @@
 // product begin.
 //
 // Numerics as in paged_rows.cu: 32-bit scores, maxima, sums and O; P rounded
-// to bf16 (half a step, 2^-9 of each weight either way) as the operand that the
+// to bf16 (half a step, 2^-8 of each weight either way) as the operand that the
 // tensor core takes.
 #include <cuda_runtime.h>
 
@@ -620,7 +628,8 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       if (!idle) {
         // Four lanes exchange 16-byte words so that each row leaves in 64-byte
         // runs: a lane alone has 16 bytes of 32 different rows an instruction,
-        // half sectors that L2 has to merge (4 us a segment instead of 1).
+        // half sectors that L2 has to merge.  Neither was faster by more than the noise; a segment's epilogue takes 2.1 us to bf16
+        // and 3.7 to f32 pieces.
         const int q4 = lane & 3;
         const bool final = out == 0 && !p.rec, f32 = !final || p.out_f32;
         float fo = 1.f, lse;

@@ -267,7 +267,7 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
   if ((rc = paged_launch(p, pages->d, (n_tokens + prefix->n_seqs - 1) / prefix->n_seqs, s, &pre_rows)) != ATTN_OK ||
       (rc = paged_launch(r, pages->d, tokens, s, &tile_rows)) != ATTN_OK)
     return rc;
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n_tokens) * hq + 7) / 8));
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n_tokens) * hq + 15) / 16));
   auto join = pages->d == 128 ? paged_join_pair_kernel<128> : paged_join_pair_kernel<64>;
   return launch_after(join, grid, 256, 0, s, p, r, pre_rows, tile_rows);
 }

@@ -80,6 +80,7 @@ struct PagedParams;
 size_t paged_rows_workspace(int d);
 int paged_rows_launch(PagedParams &p, int d, cudaStream_t s);
 size_t paged_tiles_workspace(int d);
+int paged_tiles_heads(int sms, int hk);
 int paged_tiles_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows);
 size_t paged_piece_floats(int tile_rows, int d);
 // Reads and clears the first failure status of the paged and cache kernels on

@@ -143,8 +143,35 @@ int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_ro
     const int rc = paged_tiles_launch(p, d, tokens, s, tile_rows);
     if (rc != ATTN_ERR_UNSUPPORTED) return rc;
   }
+  if (p.share.side == 1) p.share.side = 0;     // two passes share the SMs only where tiles are the first
   *tile_rows = 16;
   return paged_rows_launch(p, d, s);
+}
+
+// The prefix's tiles are bound by their products, what follows it by the cache's
+// bandwidth; one after the other each leaves idle what the other wants.  So they
+// run side by side: the tiles take T SMs, the others go to the rows kernel, whose
+// blocks start there at once.  T balances A / T and B / (SMs - T): A from the time
+// of a 128-key step of a row tile, B from the 64 (head dim 128) or 53 GB/s that
+// one SM streams when the bandwidth is not what binds it, a tenth on top, and 4 us
+// an SM on either side.  That T is within 3 us of the best of all at seven shapes.
+// Against one pass after the other (32 query and 8 key/value heads of 128): 16
+// sequences with 2048 keys before 52 each, 25.6 -> 21.6 us; 32 with 32768 before
+// 109, 59 -> 46; 32 with 4096 before 1755, 77 -> 61; 256 with 32768 before 219,
+// 174.7 -> 164.  Of 16 heads of 64: 128 with 16384 before 219, 70 -> 63; 50 with
+// 6817 before 150, two tokens each, 51.3 -> 50.
+Share share_of(const PagedParams &p, int p_tokens, const PagedParams &r, int r_tokens, int d) {
+  Share s;
+  std::memset(&s, 0, sizeof(s));
+  s.unit = paged_tiles_heads(device_sm_count(), p.hk);
+  auto side = [](const PagedParams &x, float cost) {
+    return Share::Side{x.seqs, x.seq_lens, x.n_seqs, x.n_slots, x.max_pages << x.page_shift, cost, 4000.f * device_sm_count()};
+  };
+  const int tpt = std::max(1, 128 / p.G), two = p_tokens > tpt, tpi = tpt << two;
+  const float step = d == 128 ? (two ? 1700.f : 1000.f) : (two ? 1200.f : 870.f);
+  s.of[0] = side(p, step / 128 * ((p_tokens + tpi - 1) / tpi) * p.hk);
+  s.of[1] = side(r, (d == 128 ? 8.8f : 5.3f) * ((r_tokens * r.G + 15) / 16) * r.hk);
+  return s;
 }
 
 size_t pieces_bytes(int d) { return up256(std::max(paged_rows_workspace(d), paged_tiles_workspace(d))); }
@@ -260,13 +287,21 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
     pass[i]->dense_o = reinterpret_cast<float *>(ws + L.o[i]);
     pass[i]->part_o = reinterpret_cast<float *>(ws + L.pieces[i]);
   }
-  // neither pass reads what the other writes: the second starts on each SM as
-  // the first leaves it, and waits for its end before its own
+  // neither pass reads what the other writes: the second starts on each SM that
+  // the first leaves or does not take, and waits for its end before its own
   r.wait_end = 1;
   int pre_rows;
-  if ((rc = paged_launch(p, pages->d, (n_tokens + prefix->n_seqs - 1) / prefix->n_seqs, s, &pre_rows)) != ATTN_OK ||
-      (rc = paged_launch(r, pages->d, tokens, s, &tile_rows)) != ATTN_OK)
-    return rc;
+  const int pre_tokens = (n_tokens + prefix->n_seqs - 1) / prefix->n_seqs, G = hq / pages->hk;
+  if (static_cast<int64_t>(tokens) * G <= 16) {
+    p.share = share_of(p, pre_tokens, r, tokens, pages->d);
+    p.share.side = 1;
+  }
+  if ((rc = paged_launch(p, pages->d, pre_tokens, s, &pre_rows)) != ATTN_OK) return rc;
+  if (p.share.side == 1) {
+    r.share = p.share;
+    r.share.side = 2;
+  }
+  if ((rc = paged_launch(r, pages->d, tokens, s, &tile_rows)) != ATTN_OK) return rc;
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n_tokens) * hq + 15) / 16));
   auto join = pages->d == 128 ? paged_join_pair_kernel<128> : paged_join_pair_kernel<64>;
   return launch_after(join, grid, 256, 0, s, p, r, pre_rows, tile_rows);

@@ -20,6 +20,7 @@
 #include <cstdint>
 
 #include "attn_device.cuh"
+#include "launch.cuh"
 
 namespace attn {
 
@@ -41,6 +42,18 @@ struct __align__(16) Rec4 {
   int worker, slot0, np, row;
 };
 constexpr int REC_EMPTY = -1;
+
+// Two passes that share the GPU's SMs, each in proportion to what its sequences'
+// keys cost it.
+struct Share {
+  int side;                   // 0: the pass has all SMs; 1, 2: the first, the second of the two
+  int unit;                   // the first takes a multiple of so many SMs
+  struct Side {
+    const int32_t *seqs, *lens;
+    int n, n_slots, max_len;
+    float cost, base;         // ns of one SM's time: for a key, and whatever the keys
+  } of[2];
+};
 
 struct PagedParams {
   const void *q, *k, *v;
@@ -67,6 +80,7 @@ struct PagedParams {
   Cut *cuts;                  // [workers]
   int warp_plan;              // make_warp_plan, not make_plan
   int hp, n_spans, min_span;  // heads side by side; spans; key tiles a span holds at least
+  Share share;
   int test_stall;             // failure-path test: leave one load out
   unsigned int *status;
   unsigned long long wait_ns;
@@ -75,6 +89,12 @@ struct PagedParams {
 struct SeqInfo {
   int slot, q0, nq, len;      // slot < 0: nothing of it may be read
 };
+
+// Where the launch waits for the one before it only at its end: one block is
+// enough, the others leave their SMs (2 us of a call of 52 against all waiting).
+__device__ __forceinline__ void end_after_previous(const PagedParams &p) {
+  if (p.wait_end && blockIdx.x == gridDim.x - 1) after_previous();
+}
 
 __device__ __forceinline__ void paged_fail(const PagedParams &p, unsigned code) {
   atomicCAS(p.status, 0u, code);
@@ -251,8 +271,42 @@ __device__ inline void make_plan(const PagedParams &p, int tpi, long long *first
   __syncthreads();
 }
 
-__device__ __forceinline__ long long span_of(const PagedParams &p, long long total) {
-  const long long s = (total + p.n_spans - 1) / p.n_spans;
+// SMs of this pass, of `sms`: a function of the sequences' lengths alone.  All NT
+// threads of the block come here; `sums` has NT / 32 places.  Out of line: in line
+// it cost the calls that do not share 0.4 to 1.5 us.
+template <int NT>
+__device__ __noinline__ int my_sms(const PagedParams &p, int sms, float2 *sums) {
+  float keys[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const Share::Side &s = p.share.of[k];
+    long long n = 0;
+    for (int b = threadIdx.x; b < s.n; b += NT) {
+      const int slot = s.seqs ? __ldg(s.seqs + b) : b;
+      if (slot >= 0 && slot < s.n_slots) n += min(max(__ldg(s.lens + slot), 0), s.max_len);
+    }
+    keys[k] = static_cast<float>(n) * s.cost + (threadIdx.x ? 0.f : s.base);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    keys[0] += __shfl_xor_sync(0xffffffffu, keys[0], o);
+    keys[1] += __shfl_xor_sync(0xffffffffu, keys[1], o);
+  }
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = make_float2(keys[0], keys[1]);
+  __syncthreads();
+  float a = 0.f, b = 0.f;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    a += sums[w].x;
+    b += sums[w].y;
+  }
+  const int u = p.share.unit, most = (sms - 1) / u;      // at least one unit, and one SM for the other
+  const int first = u * min(max(static_cast<int>(sms * (a / (a + b)) / u + 0.5f), 1), most);
+  return p.share.side == 1 ? first : sms - first;
+}
+
+__device__ __forceinline__ long long span_of(const PagedParams &p, long long total, int n_spans) {
+  const long long s = (total + n_spans - 1) / n_spans;
   return s > p.min_span ? s : p.min_span;
 }
 
@@ -362,8 +416,8 @@ __device__ __forceinline__ void item_pieces(long long f0, int n, long long at, l
 
 // Rows of items without a key tile: their sequences see nothing (here).
 template <int D, int ROWS, int KL>
-__device__ inline void finish_empty(const PagedParams &p, const SeqInfo *info, int tpi) {
-  for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x) {
+__device__ inline void finish_empty(const PagedParams &p, const SeqInfo *info, int tpi, int blocks) {
+  for (int b = blockIdx.x; b < p.n_seqs; b += blocks) {
     const SeqInfo s = info ? info[b] : seq_info(p, b);
     // causal rows see more keys the later they stand: the empty tiles come first
     for (int rt = 0; rt < tile_count<ROWS>(s.nq, p.G, tpi); ++rt) {

@@ -113,17 +113,27 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
   if (!p.wait_end) after_previous();
   admit_next();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int sms = gridDim.x;
+  if (p.share.side) {
+    sms = my_sms<S::W * 32>(p, sms, reinterpret_cast<float2 *>(rows_smem));
+    if (static_cast<int>(blockIdx.x) >= sms) {
+      end_after_previous(p);
+      return;
+    }
+    __syncthreads();
+  }
   if (p.warp_plan) make_warp_plan<PR_ROWS, KL>(p, 0, rows_smem + S::FIRST + warp * PLAN_WARP, first, info);
   else make_plan<PR_ROWS, KL, S::W * 32>(p, 0, first, info, scan);
-  finish_empty<D, PR_ROWS, KL>(p, info, 0);
+  finish_empty<D, PR_ROWS, KL>(p, info, 0, sms);
 
-  const long long total = first[p.n_seqs], span = span_of(p, total);
+  const int n_spans = p.share.side ? sms * S::W / p.hp : p.n_spans;
+  const long long total = first[p.n_seqs], span = span_of(p, total, n_spans);
   const long long worker = static_cast<long long>(blockIdx.x) * S::W + warp, span_no = worker / p.hp;
   const int sub = static_cast<int>(worker - span_no * p.hp);    // this warp's head of a group
-  const long long from = span_no * span, to = min(total, from + span);
+  const long long from = min(span_no * span, total), to = min(total, from + span);
   if (from >= to) {
     if (lane == 0 && !p.rec) p.cuts[worker] = Cut{};
-    if (p.wait_end) after_previous();
+    end_after_previous(p);
     return;
   }
   const int cnt = static_cast<int>(to - from);
@@ -381,7 +391,7 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
     }
   }
   if (lane == 0 && !p.rec) leave_cut<PR_ROWS, KL>(p, in, 0, in.h * p.hp + sub, worker, span_no, span, from, to);
-  if (p.wait_end) after_previous();
+  end_after_previous(p);
 }
 
 // ---------------------------------------------------------------------- host

@@ -17,11 +17,11 @@
 //
 // What bounds it.  Rows that fill their tiles: the chain of products and softmax
 // that attn_fwd has.  4 x 1021 new tokens, window 4096, 32 query and 8 key/value
-// heads of 128 columns: 173 us, 73 steps a CTA of 256 rows by 128 keys at 1.70 us
+// heads of 128 columns: 167 us, 73 steps a CTA of 256 rows by 128 keys at 1.70 us
 // (1.5 PFLOP/s over all SMs; tensor pipe 51 % active over the launch), and
-// around them 10 us before the first product, 4.4 at a change of item, 12 for
-// the join.  256 rows of a group's sequences against a prefix of 32768 keys: 107
-// of the call's 174 us.  A 128-key step of TILES = 1 at head dim 64 takes 0.85 to
+// around them 10 us before the first product, 4.4 at a change of item, 8 for
+// the join.  256 rows of a group's sequences against a prefix of 32768 keys: 107 us
+// on all SMs.  A 128-key step of TILES = 1 at head dim 64 takes 0.85 to
 // 0.9 us (100 rows, 16384 keys, 16 heads, 4 groups: 36 us).
 //
 // One persistent CTA per SM takes an equal span of the flat list of 128-key
@@ -141,6 +141,17 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   const uint64_t lim = p.wait_ns;
   constexpr int WP = 8, WM = 9;       // producer, issuer
 
+  int sms = gridDim.x;
+  if (p.share.side) {
+    if (!p.wait_end) after_previous();
+    admit_next();
+    sms = my_sms<L::THREADS>(p, sms, reinterpret_cast<float2 *>(scan));
+    if (static_cast<int>(blockIdx.x) >= sms) {
+      end_after_previous(p);
+      return;
+    }
+    __syncthreads();
+  }
   if (threadIdx.x == 0) {
     mbar_init(bar(L::B_Q), 1);
     mbar_init(bar(L::B_QE), 1);
@@ -176,14 +187,15 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   admit_next();
   if (TILES == 1 && p.warp_plan) make_warp_plan<0, PT_KL>(p, tpi, smem + L::FIRST_OFF + warp * PLAN_WARP, first, info);
   else make_plan<0, PT_KL, L::THREADS>(p, tpi, first, info, scan);
-  finish_empty<D, 0, PT_KL>(p, info, tpi);
+  finish_empty<D, 0, PT_KL>(p, info, tpi, sms);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const long long total = first[p.n_seqs], span = span_of(p, total);
+  const int n_spans = p.share.side ? sms / p.hp : p.n_spans;
+  const long long total = first[p.n_seqs], span = span_of(p, total, n_spans);
   const int mine = blockIdx.x / p.hp, sub = blockIdx.x - mine * p.hp;      // span, and head of a group
-  const long long from = mine < p.n_spans ? mine * span : total, to = min(total, from + span);
+  const long long from = mine < n_spans ? mine * span : total, to = min(total, from + span);
 
   if (warp == WP) {
     // -------------------------------------------------------------- producer
@@ -714,7 +726,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   tc_fence_after();
   if (warp == WM) tmem_dealloc(tmem, 512);
   if (threadIdx.x == 0 && *abort) paged_fail(p, ATTN_ERR_TIMEOUT);
-  if (p.wait_end) after_previous();
+  end_after_previous(p);
 }
 
 // ---------------------------------------------------------------------- host
@@ -751,9 +763,7 @@ int launch_tiles(PagedParams &p, const CUtensorMap &mq, const CUtensorMap &mk, c
   }
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  // heads side by side while that leaves no more than a few SMs idle
-  p.hp = 1;
-  while (p.hp < 8 && p.hk % (2 * p.hp) == 0 && sms % (2 * p.hp) <= sms / 32) p.hp *= 2;
+  p.hp = paged_tiles_heads(sms, p.hk);
   p.n_spans = sms / p.hp;
   p.min_span = 1;
   p.part_ml = p.part_o + paged_piece_floats(TILES * 128, D);
@@ -765,6 +775,14 @@ int launch_tiles(PagedParams &p, const CUtensorMap &mq, const CUtensorMap &mk, c
 }
 
 }  // namespace
+
+// Heads side by side: as many as divide them while that leaves no more than a
+// few SMs idle.
+int paged_tiles_heads(int sms, int hk) {
+  int hp = 1;
+  while (hp < 8 && hk % (2 * hp) == 0 && sms % (2 * hp) <= sms / 32) hp *= 2;
+  return hp;
+}
 
 size_t paged_tiles_workspace(int d) {
   const int sms = device_sm_count();

@@ -112,6 +112,20 @@ def test_shared_prefix(plens, first, lens, news, page, hq, hk, d, dtype):
     P.check(c, out, lse, P.reference(c))
 
 
+@pytest.mark.parametrize("plens,first,lens,news,hq,hk,d", [
+    ([20000], [0, 20], [1] * 20, [1] * 20, 32, 8, 128), ([20000], [0, 20], [0] * 20, [1] * 20, 32, 8, 128),
+    ([1], [0, 6], [9000] * 6, [1] * 6, 32, 8, 128), ([0], [0, 6], [9000] * 6, [1] * 6, 32, 8, 128),
+    ([0, 0], [0, 9, 20], [0] * 20, [1] * 20, 16, 4, 64), ([9000, 0, 3], [0, 7, 30, 40], [7000] + [1] * 39, [2] * 40, 8, 8, 64)])
+def test_prefixes_and_what_follows_of_any_proportion(plens, first, lens, news, hq, hk, d):
+    # the two passes of the call share the GPU by how many keys each has
+    c = P.make(lens, news, 16, hq, hk, d, seed=4, plens=plens, first=first)
+    out, lse = prefix(c)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c))
+    again = prefix(c)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 def test_no_prefix_at_all_equals_the_paged_call():
     c = P.make([50, 60], [1, 1], 16, 8, 2, 128, seed=1)
     none = torch.empty((0, 3), dtype=torch.int32, device="cuda")

@@ -208,6 +208,28 @@ __device__ __forceinline__ void drop(const CacheParams &p, int page) {
   else atomicCAS(p.status, 0u, static_cast<unsigned>(ATTN_ERR_INVALID_ARG));
 }
 
+// Reads what the kernel will need first, all at once: list entries, the lengths
+// they name and this CTA's first page counts.  The reads that follow, one after
+// the other, then find them in L1.
+struct Ahead {
+  int x[3] = {0, 0, 0};
+  int4 refs = {0, 0, 0, 0};
+  __device__ __forceinline__ Ahead(const CacheParams &p, int page_from, int page_to) {
+    const int i = threadIdx.x, page = page_from + 4 * i;
+    if (page + 4 <= page_to && (reinterpret_cast<uintptr_t>(p.refs + page) & 15) == 0)
+      refs = *reinterpret_cast<const int4 *>(p.refs + page);
+    if (i < p.n) {
+      const int a = p.a ? p.a[i] : i, b = p.b ? p.b[i] : -1;
+      x[0] = b;
+      if (a >= 0 && a < p.n_slots) x[1] = p.lens[a];
+      if (p.copies && b >= 0 && b < p.n_slots) x[2] = p.lens[b];
+    }
+  }
+  __device__ __forceinline__ void arrived() {
+    asm volatile("" ::"r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(refs.x), "r"(refs.y), "r"(refs.z), "r"(refs.w) : "memory");
+  }
+};
+
 extern __shared__ __align__(16) int cache_smem[];
 
 // ---------------------------------------------------------------- extend
@@ -218,9 +240,13 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_extend
   __shared__ CacheSmem s;
   cluster_started();
   const int rank = cluster_ctarank();
+  int from, to;
+  page_share(p, rank, from, to);
+  Ahead ahead(p, from, to);
   int *first = cache_smem, *have = first + p.n + 1;
   uint32_t *seen = reinterpret_cast<uint32_t *>(have + p.n);
   check_rows(s, p, p.a, seen);
+  ahead.arrived();
   unsigned code = s.bad ? ATTN_ERR_INVALID_ARG : 0u;
   if (code == 0) {
     __shared__ int full;
@@ -242,8 +268,6 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_extend
     });
     code = s.bad ? ATTN_ERR_INVALID_ARG : full ? ATTN_ERR_CAPACITY : 0u;
   }
-  int from, to;
-  page_share(p, rank, from, to);
   auto is_free = [](int, int r) { return r == 0; };
   const int mine = code ? 0 : count_pages(s, p, from, to, is_free);
   cluster_wait_started();
@@ -280,6 +304,7 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_free_k
   admit_next();
   __shared__ CacheSmem s;
   const int rank = cluster_ctarank();
+  Ahead ahead(p, 0, 0);
   int *first = cache_smem;
   uint32_t *seen = reinterpret_cast<uint32_t *>(first + p.n + 1);
   if (p.a) {
@@ -288,6 +313,7 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_free_k
     if (threadIdx.x == 0) s.bad = 0;
     __syncthreads();
   }
+  ahead.arrived();
   auto slot = [&](int i) { return p.a ? p.a[i] : i; };
   auto begin = [&]() { return TRIM ? pages_of(p, p.sinks) : 0; };
   if (!s.bad)
@@ -336,7 +362,11 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_fork_k
   int *heir = len + n;                       // [n_slots] first child of each source
   uint32_t *seen = reinterpret_cast<uint32_t *>(heir + p.n_slots);
   int32_t *fresh = p.ws, *rows = p.ws + n;
+  int from, to;
+  page_share(p, rank, from, to);
+  Ahead ahead(p, from, to);
   check_rows(s, p, p.b, seen);               // seen: the rows that are replaced
+  ahead.arrived();
   for (int i = threadIdx.x; i < p.n_slots; i += CT) heir[i] = INT_MAX;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += CT) {
@@ -368,8 +398,6 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_fork_k
     if (s.bad) code = ATTN_ERR_INVALID_ARG;
     else if (want > p.cap) code = ATTN_ERR_CAPACITY;
   }
-  int from, to;
-  page_share(p, rank, from, to);
   auto is_free = [](int, int r) { return r == 0; };
   const int mine = code ? 0 : count_pages(s, p, from, to, is_free);
   cluster_wait_started();
@@ -384,8 +412,16 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_fork_k
     else
       rank_pages(s, p, from, to, before, want, is_free, [&](int r, int page) { fresh[r] = page; });
   }
-  const int total = code ? 0 : first[n];
-  for (int x = rank * CT + threadIdx.x; x < total; x += CALL) {
+  const int total = code ? 0 : first[n], x0 = rank * CT + threadIdx.x;
+  // the thread's first entry waits for the barrier in registers, others in the workspace
+  int i0 = 0, page0 = -1, old0 = -1;
+  if (x0 < total) {
+    i0 = list_find(first, n, x0);
+    const int j = x0 - first[i0];
+    if (j < pages_of(p, len[i0])) page0 = p.table[p.a[i0] * p.stride + j];
+    old0 = p.table[p.b[i0] * p.stride + j];
+  }
+  for (int x = x0 + CALL; x < total; x += CALL) {
     const int i = list_find(first, n, x), j = x - first[i];
     if (j < pages_of(p, len[i])) rows[x] = p.table[p.a[i] * p.stride + j];
   }
@@ -394,13 +430,13 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_fork_k
     refuse(p, rank, code);
     return;
   }
-  for (int x = rank * CT + threadIdx.x; x < total; x += CALL) {
-    const int i = list_find(first, n, x), j = x - first[i], np = pages_of(p, len[i]);
+  for (int x = x0; x < total; x += CALL) {
+    const int i = x == x0 ? i0 : list_find(first, n, x), j = x - first[i], np = pages_of(p, len[i]);
     int32_t *e = p.table + p.b[i] * p.stride + j;
-    const int old = *e;
+    const int old = x == x0 ? old0 : *e;
     int page = -1;
     if (j < np) {
-      page = rows[x];
+      page = x == x0 ? page0 : rows[x];
       if (j == np - 1 && copied(i)) {
         const int r = rank_of[i];
         p.copies[1 + r] = page;
@@ -437,8 +473,12 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_compac
   int *first = cache_smem;                   // [n_slots + 1]
   int32_t *moved = p.ws;                     // [n_pages] where a page at `used` or above goes
   int32_t *src = p.copies + 1, *dst = src + p.cap;
+  int from, to;
+  page_share(p, rank, from, to);
+  Ahead ahead(p, from, to);
   if (threadIdx.x == 0) s.bad = 0;
   __syncthreads();
+  ahead.arrived();
   list_scan(s, p.n_slots, first, [&](int i) {
     const int len = p.lens[i];
     if (!good_len(p, len)) {
@@ -447,8 +487,6 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_compac
     }
     return pages_of(p, len);
   });
-  int from, to;
-  page_share(p, rank, from, to);
   const int in_use = count_pages(s, p, from, to, [](int, int r) { return r != 0; });
   cluster_wait_started();
   share_count(s.count, in_use, rank);

@@ -82,6 +82,31 @@ def test_many_sequences(n):
     P.check(c, out, lse, P.reference(c, 19, 2))
 
 
+@pytest.mark.parametrize("n,d", [(40, 64), (1500, 128), (2500, 64), (4096, 64), (4096, 128)])
+@pytest.mark.parametrize("max_q", [3, 40])       # one row tile an item, two
+def test_many_sequences_of_several_tokens(n, d, max_q):
+    rng = np.random.default_rng(n)
+    news = rng.integers(0, 4, n).tolist()
+    c = P.make(rng.integers(0, 60, n).tolist(), news, 16, 8, 1, d, seed=n)
+    out, lse = paged(c, 19, 2, max_q=max_q)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c, 19, 2))
+
+
+@pytest.mark.parametrize("n,groups", [(600, 130), (4096, 1500)])
+def test_many_groups_of_several_tokens(n, groups):
+    # the prefixes on the tensor cores, and what follows them on either kernel
+    rng = np.random.default_rng(n)
+    first = np.sort(rng.integers(0, n + 1, groups + 1)).tolist()
+    c = P.make(rng.integers(0, 40, n).tolist(), rng.integers(0, 4, n).tolist(), 16, 8, 1, 64, seed=n,
+               plens=rng.integers(0, 60, groups).tolist(), first=first)
+    ref = P.reference(c)
+    for max_q in (1, 3):
+        out, lse = prefix(c, max_q=max_q)
+        assert attn_last_device_error() == 0
+        P.check(c, out, lse, ref)
+
+
 @pytest.mark.parametrize("hq,hk,d,page,news", [(8, 2, 128, 64, 1), (3, 1, 64, 16, 1), (16, 4, 128, 16, 37), (32, 8, 64, 512, 130)])
 def test_long_sequence_alone(hq, hk, d, page, news):
     # one sequence: every span of every worker is a piece of its few items
@@ -287,6 +312,20 @@ def test_two_calls_at_once_with_their_own_workspaces():
     torch.cuda.synchronize()
     for out, lse in got:
         P.check(c, out, lse, ref)
+
+
+def test_prefix_calls_at_once():
+    lens, news = [1000, 40, 900, 5] * 6, [1] * 24
+    c = P.make(lens, news, 16, 32, 8, 128, seed=9, plens=[5000, 700], first=[0, 16, 24])
+    ref = P.reference(c)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = [prefix(c, stream=streams[i % 3]) for i in range(9)]
+    torch.cuda.synchronize()
+    P.check(c, *got[0], ref)
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+    assert attn_last_device_error() == 0
 
 
 @pytest.mark.parametrize("what", ["slot", "length", "negative length", "page", "negative page", "q_ptr", "q_ptr end"])

@@ -338,19 +338,24 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   } else if (warp == WM) {
     // ---------------------------------------------------------------- issuer
     constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, PT_BN, 0), IDESC_PV = idesc_bf16_f32(128, D, 1);
+    // Descriptors as a constant high word and a low word (address and leading
+    // offset, in units of 16 bytes) to which each instruction adds a constant:
+    // whole descriptors cost the issuing lane more than the tensor core took.
+    const uint32_t q_lo = (q_smem >> 4) | 1u << 16, k_lo = (kv_smem >> 4) | 1u << 16,
+                   v_lo = (kv_smem >> 4) | (L::HALF >> 4) << 16;
     auto issue_qk = [=](int t, int sbuf, int slot) {
+      const uint32_t a = q_lo + t * (L::TILE >> 4), b = k_lo + slot * (L::TILE >> 4), d = tmem + sbuf * 128;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * L::HALF + (kk & 3) * 32;
-        mma_ss(tmem + sbuf * 128, smem_desc_sw128(q_smem + t * L::TILE + off, 16, 1024),
-               smem_desc_sw128(kv_smem + slot * L::TILE + off, 16, 1024), IDESC_QK, kk > 0);
+        const uint32_t off = ((kk >> 2) * L::HALF + (kk & 3) * 32) >> 4;
+        mma_ss_lo(d, a + off, b + off, IDESC_QK, kk > 0);
       }
     };
-    auto issue_pv = [=](int t, int sbuf, int slot, bool start) {
+    // keys kk0 * 16 on, n * 16 of them
+    auto issue_pv = [=](int o, int sbuf, int slot, int kk0, int n, bool start) {
+      const uint32_t b = v_lo + slot * (L::TILE >> 4) + kk0 * (16 * 128 >> 4), d = tmem + 256 + o * 128, a = tmem + sbuf * 128 + kk0 * 16;
 #pragma unroll
-      for (int kk = 0; kk < PT_BN / 16; ++kk)
-        mma_ts(tmem + 256 + t * 128, tmem + sbuf * 128 + kk * 8,
-               smem_desc_sw128(kv_smem + slot * L::TILE + kk * 16 * 128, L::HALF, 1024), IDESC_PV, (start && kk == 0) ? 0u : 1u);
+      for (int kk = 0; kk < n; ++kk) mma_ts_lo(d, a + kk * 8, b + kk * (16 * 128 >> 4), IDESC_PV, (start && kk == 0) ? 0u : 1u);
     };
     if (lane == 0) {
       // ring position as (slot, phase), advanced without divisions: between
@@ -408,13 +413,8 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
             }
             tc_fence_after();
             // each group's 64 keys into its own O
-            for (int u = 0; u < 2; ++u) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ts(tmem + 256 + u * 128, tmem + (step & 1) * 128 + u * 64 + kk * 8,
-                       smem_desc_sw128(kv_smem + k.slot * L::TILE + (u * 64 + kk * 16) * 128, L::HALF, 1024), IDESC_PV,
-                       (j == 0 && kk == 0) ? 0u : 1u);
-            }
+            issue_pv(0, step & 1, k.slot, 0, 4, j == 0);
+            issue_pv(1, step & 1, k.slot, 4, 4, j == 0);
             mma_commit(bar(L::B_EMPTY + k.slot));
             mma_commit(bar(L::B_V));
             if (j + 1 == n) mma_commit(bar(L::B_O));
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
               break;
             }
             tc_fence_after();
-            issue_pv(0, 0, v.slot, j == 0);
+            issue_pv(0, 0, v.slot, 0, 8, j == 0);
             if (!more) mma_commit(bar(L::B_O + 0));
             bool have_p1 = false;
             if (more) {
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
               break;
             }
             tc_fence_after();
-            issue_pv(1, 1, v.slot, j == 0);
+            issue_pv(1, 1, v.slot, 0, 8, j == 0);
             mma_commit(bar(L::B_EMPTY + v.slot));
             if (!more) {
               mma_commit(bar(L::B_O + 1));

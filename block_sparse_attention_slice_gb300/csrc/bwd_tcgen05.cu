@@ -368,25 +368,25 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
     if (lane == 0 && nc > 0) {
       constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, 0);
       constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, 1);
-      const uint32_t ks = sb + L::K_OFF, vs = sb + L::V_OFF;
+      const uint32_t k_lo = desc_lo(sb + L::K_OFF, 16), v_lo = desc_lo(sb + L::V_OFF, 16);
       auto qst = [&](uint32_t s) { return sb + L::Q_OFF + (s & 1) * BL::TILE; };
       auto dost = [&](uint32_t s) { return sb + L::DO_OFF + (s & 1) * BL::TILE; };
       // dV += P^T(s) dO(s), then dO's stage is free
       auto issue_dv = [&](uint32_t s) {
+        const uint32_t b = desc_lo(dost(s), BL::HALF);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + 256, tmem + (kk >> 2) * 64 + (kk & 3) * 8,
-                 smem_desc_sw128(dost(s) + kk * 16 * 128, BL::HALF, 1024),
-                 IDESC_PV, (s > 0 || kk > 0) ? 1u : 0u);
+          mma_ts_lo(tmem + 256, tmem + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * (16 * 128 >> 4), IDESC_PV,
+                    (s > 0 || kk > 0) ? 1u : 0u);
         mma_commit(bar(L::B_DE + (s & 1)));
       };
       // dK += dS^T(s) Q(s), then Q's stage is free
       auto issue_dk = [&](uint32_t s) {
+        const uint32_t b = desc_lo(qst(s), BL::HALF);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + 384, tmem + 128 + (kk >> 2) * 64 + (kk & 3) * 8,
-                 smem_desc_sw128(qst(s) + kk * 16 * 128, BL::HALF, 1024),
-                 IDESC_PV, (s > 0 || kk > 0) ? 1u : 0u);
+          mma_ts_lo(tmem + 384, tmem + 128 + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * (16 * 128 >> 4), IDESC_PV,
+                    (s > 0 || kk > 0) ? 1u : 0u);
         mma_commit(bar(L::B_QE + (s & 1)));
       };
       bool ok = mbar_wait_bounded(bar(L::B_KV), 0, abort, lim);
@@ -418,11 +418,11 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         }
         tc_fence_after();
         // S^T(s) = K Q(s)^T
+        const uint32_t q_lo = desc_lo(qst(s), 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * BL::HALF + (kk & 3) * 32;
-          mma_ss(tmem, smem_desc_sw128(ks + off, 16, 1024), smem_desc_sw128(qst(s) + off, 16, 1024),
-                 IDESC_QK, kk > 0);
+          const uint32_t off = ((kk >> 2) * BL::HALF + (kk & 3) * 32) >> 4;
+          mma_ss_lo(tmem, k_lo + off, q_lo + off, IDESC_QK, kk > 0);
         }
         mma_commit(bar(L::B_SR));
         if (s > 0) {
@@ -441,11 +441,11 @@ __global__ void __launch_bounds__(KV_THREADS, 1)
         }
         tc_fence_after();
         // dP^T(s) = V dO(s)^T
+        const uint32_t do_lo = desc_lo(dost(s), 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * BL::HALF + (kk & 3) * 32;
-          mma_ss(tmem + 128, smem_desc_sw128(vs + off, 16, 1024), smem_desc_sw128(dost(s) + off, 16, 1024),
-                 IDESC_QK, kk > 0);
+          const uint32_t off = ((kk >> 2) * BL::HALF + (kk & 3) * 32) >> 4;
+          mma_ss_lo(tmem + 128, v_lo + off, do_lo + off, IDESC_QK, kk > 0);
         }
         mma_commit(bar(L::B_DPR));
         ++s;
@@ -779,29 +779,29 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
     if (lane == 0 && n > 0) {
       constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, 0);
       constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, 1);
-      const uint32_t qs = sb + L::Q_OFF, dos = sb + L::DO_OFF;
+      const uint32_t q_lo = desc_lo(sb + L::Q_OFF, 16), do_lo = desc_lo(sb + L::DO_OFF, 16);
       // S(j) = Q K^T and dP = dO V^T (SS); dQ += dS(j) K (TS, K MN-major)
       auto mma_s = [=](int j, uint32_t kb) {
+        const uint32_t k_lo = desc_lo(kb, 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * BL::HALF + (kk & 3) * 32;
-          mma_ss(tmem + q_s_col(j), smem_desc_sw128(qs + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024),
-                 IDESC_QK, kk > 0);
+          const uint32_t off = ((kk >> 2) * BL::HALF + (kk & 3) * 32) >> 4;
+          mma_ss_lo(tmem + q_s_col(j), q_lo + off, k_lo + off, IDESC_QK, kk > 0);
         }
       };
       auto mma_dp = [=](uint32_t vb) {
+        const uint32_t v_lo = desc_lo(vb, 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * BL::HALF + (kk & 3) * 32;
-          mma_ss(tmem + 128, smem_desc_sw128(dos + off, 16, 1024), smem_desc_sw128(vb + off, 16, 1024),
-                 IDESC_QK, kk > 0);
+          const uint32_t off = ((kk >> 2) * BL::HALF + (kk & 3) * 32) >> 4;
+          mma_ss_lo(tmem + 128, do_lo + off, v_lo + off, IDESC_QK, kk > 0);
         }
       };
       auto mma_dq = [=](int j, uint32_t kb) {
+        const uint32_t b = desc_lo(kb, BL::HALF);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + 256, tmem + q_s_col(j) + kk * 8, smem_desc_sw128(kb + kk * 16 * 128, BL::HALF, 1024),
-                 IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+          mma_ts_lo(tmem + 256, tmem + q_s_col(j) + kk * 8, b + kk * (16 * 128 >> 4), IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
       };
       // ring positions of a half: K_j at ld + 2j, V_j at ld + 2j + 1.  The
       // position ld + 2j is kept as (slot bs, round br), advanced by 2 per

@@ -341,8 +341,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     // Descriptors as a constant high word and a low word (address and leading
     // offset, in units of 16 bytes) to which each instruction adds a constant:
     // whole descriptors cost the issuing lane more than the tensor core took.
-    const uint32_t q_lo = (q_smem >> 4) | 1u << 16, k_lo = (kv_smem >> 4) | 1u << 16,
-                   v_lo = (kv_smem >> 4) | (L::HALF >> 4) << 16;
+    const uint32_t q_lo = desc_lo(q_smem, 16), k_lo = desc_lo(kv_smem, 16), v_lo = desc_lo(kv_smem, L::HALF);
     auto issue_qk = [=](int t, int sbuf, int slot) {
       const uint32_t a = q_lo + t * (L::TILE >> 4), b = k_lo + slot * (L::TILE >> 4), d = tmem + sbuf * 128;
 #pragma unroll

@@ -190,8 +190,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 
-// The same with descriptors given by their low words; the high word is that of
-// smem_desc_sw128 with a stride byte offset of 1024.
+// The same with descriptors given by their low words (address and leading byte
+// offset, in units of 16 bytes), to which a run of MMAs adds constants; the high
+// word is that of smem_desc_sw128 with a stride byte offset of 1024.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return saddr >> 4 | (lbo_bytes >> 4) << 16;
+}
 constexpr uint32_t kDescHi1024 = (1024u >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(

@@ -158,8 +158,8 @@ int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_ro
 // Against one pass after the other (32 query and 8 key/value heads of 128): 16
 // sequences with 2048 keys before 52 each, 25.6 -> 21.6 us; 32 with 32768 before
 // 109, 59 -> 46; 32 with 4096 before 1755, 77 -> 61; 256 with 32768 before 219,
-// 174.7 -> 164.  Of 16 heads of 64: 128 with 16384 before 219, 70 -> 63; 50 with
-// 6817 before 150, two tokens each, 51.3 -> 50.
+// 174.7 -> 164 (154 since).  Of 16 heads of 64: 128 with 16384 before 219, 70 ->
+// 63; 50 with 6817 before 150, two tokens each, 51.3 -> 50.
 Share share_of(const PagedParams &p, int p_tokens, const PagedParams &r, int r_tokens, int d) {
   Share s;
   std::memset(&s, 0, sizeof(s));
@@ -168,7 +168,7 @@ Share share_of(const PagedParams &p, int p_tokens, const PagedParams &r, int r_t
     return Share::Side{x.seqs, x.seq_lens, x.n_seqs, x.n_slots, x.max_pages << x.page_shift, cost, 4000.f * device_sm_count()};
   };
   const int tpt = std::max(1, 128 / p.G), two = p_tokens > tpt, tpi = tpt << two;
-  const float step = d == 128 ? (two ? 1700.f : 1000.f) : (two ? 1200.f : 870.f);
+  const float step = d == 128 ? (two ? 1560.f : 1000.f) : (two ? 1200.f : 820.f);
   s.of[0] = side(p, step / 128 * ((p_tokens + tpi - 1) / tpi) * p.hk);
   s.of[1] = side(r, (d == 128 ? 8.8f : 5.3f) * ((r_tokens * r.G + 15) / 16) * r.hk);
   return s;

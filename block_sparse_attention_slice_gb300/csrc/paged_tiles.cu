@@ -17,12 +17,13 @@
 //
 // What bounds it.  Rows that fill their tiles: the chain of products and softmax
 // that attn_fwd has.  4 x 1021 new tokens, window 4096, 32 query and 8 key/value
-// heads of 128 columns: 167 us, 73 steps a CTA of 256 rows by 128 keys at 1.70 us
-// (1.5 PFLOP/s over all SMs; tensor pipe 51 % active over the launch), and
-// around them 10 us before the first product, 4.4 at a change of item, 8 for
-// the join.  256 rows of a group's sequences against a prefix of 32768 keys: 107 us
-// on all SMs.  A 128-key step of TILES = 1 at head dim 64 takes 0.85 to
-// 0.9 us (100 rows, 16384 keys, 16 heads, 4 groups: 36 us).
+// heads of 128 columns: 157 us, 73 steps a CTA of 256 rows by 128 keys at 1.56 us
+// (1.6 PFLOP/s over all SMs), and around them 10 us before the first product, 4.4
+// at a change of item, 8 for the join.  The lane that issues is busy nearly all of
+// a step: a commit takes it some 95 cycles, an instruction what the tensor core
+// does.  A 128-key step of TILES = 1 at head dim 64 takes 0.8 to 0.85 us, of which
+// the softmax of 64 columns is 0.6 (100 rows, 16384 keys, 16 heads, 4 groups: 34
+// us on all SMs).
 //
 // One persistent CTA per SM takes an equal span of the flat list of 128-key
 // tiles (paged_plan.cuh); pieces of items that cross spans are joined by
@@ -76,7 +77,7 @@ struct TileLayout {
     return 1024 + FIRST_OFF + (p.warp_plan ? THREADS / 32 * static_cast<size_t>(PLAN_WARP)
                                            : 8ull * (p.n_seqs + 1) + (infos ? sizeof(SeqInfo) * p.n_seqs : 0));
   }
-  static_assert(MISC_OFF % 8 == 0, "alignment");
+  static_assert(MISC_OFF % 8 == 0 && (TILES == 1 || NS % 2 == 0), "alignment; keys in even slots");
 };
 
 // Transposes 4 x 4 words of 16 bytes among four neighbouring lanes: lane q's
@@ -283,10 +284,14 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         mbar_arrive(bar(L::B_IF + qs));
       }
       __syncwarp();
-      // the tile of this lane's page into the next ring slot
-      auto load = [&](const CUtensorMap *tm, int tok, int page) {
+      // The tile of this lane's page into the next ring slot.  With two row tiles
+      // the scores of K(j+1) follow the products of V(j), which lies before it in
+      // the ring (NS is even): once they are done, both slots are free, by one
+      // commit (1 % of the call).
+      auto load = [&](const CUtensorMap *tm, int tok, int page, bool values) {
         const int slot = ld % NS;
-        if (ld >= NS && !wait_all(bar(L::B_EMPTY + slot), (ld / NS - 1) & 1, abort, lim)) {
+        const uint32_t was = ld - NS + (TILES == 2 && values ? 1 : 0);
+        if (ld >= NS && !wait_all(bar(L::B_EMPTY + was % NS), (was / NS) & 1, abort, lim)) {
           ok = false;
           return;
         }
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       // K_0 K_1 V_0 K_2 V_1 .. for one.
       int tok = tok_next, page = checked(raw_next);
       if (steps > 1) raw_next = look_up(1, tok_next);
-      if (TILES == 1) load(&tm_k, tok, page);
+      if (TILES == 1) load(&tm_k, tok, page, false);
       for (int j = 0; j < steps && ok; ++j) {
         int tok1 = 0, page1 = 0;
         if (j + 1 < steps) {
@@ -317,9 +322,9 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           tok1 = tok_next;
           if (j + 2 < steps) raw_next = look_up(j + 2, tok_next);
         }
-        if (TILES == 2) load(&tm_k, tok, page);
-        if (TILES == 1 && j + 1 < steps) load(&tm_k, tok1, page1);
-        if (ok) load(&tm_v, tok, page);
+        if (TILES == 2) load(&tm_k, tok, page, false);
+        if (TILES == 1 && j + 1 < steps) load(&tm_k, tok1, page1, false);
+        if (ok) load(&tm_v, tok, page, true);
         tok = tok1;
         page = page1;
       }
@@ -340,7 +345,8 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, PT_BN, 0), IDESC_PV = idesc_bf16_f32(128, D, 1);
     // Descriptors as a constant high word and a low word (address and leading
     // offset, in units of 16 bytes) to which each instruction adds a constant:
-    // whole descriptors cost the issuing lane more than the tensor core took.
+    // whole descriptors cost the issuing lane more than the tensor core took (the
+    // call above took 167 us, not 158).
     const uint32_t q_lo = desc_lo(q_smem, 16), k_lo = desc_lo(kv_smem, 16), v_lo = desc_lo(kv_smem, L::HALF);
     auto issue_qk = [=](int t, int sbuf, int slot) {
       const uint32_t a = q_lo + t * (L::TILE >> 4), b = k_lo + slot * (L::TILE >> 4), d = tmem + sbuf * 128;
@@ -457,7 +463,6 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
             }
             tc_fence_after();
             issue_pv(1, 1, v.slot, 0, 8, j == 0);
-            mma_commit(bar(L::B_EMPTY + v.slot));
             if (!more) {
               mma_commit(bar(L::B_O + 1));
             } else {

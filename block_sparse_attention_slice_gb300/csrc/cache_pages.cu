@@ -316,7 +316,11 @@ __global__ void __cluster_dims__(CC, 1, 1) __launch_bounds__(CT, 1) cache_free_k
   ahead.arrived();
   auto slot = [&](int i) { return p.a ? p.a[i] : i; };
   auto begin = [&]() { return TRIM ? pages_of(p, p.sinks) : 0; };
-  if (!s.bad)
+  // Read by every thread before any writes it again below: a thread that saw a
+  // bad length flagged here would pass by the barriers that the others wait at.
+  const bool listed = !s.bad;
+  __syncthreads();
+  if (listed)
     list_scan(s, p.n, first, [&](int i) {
       const int len = p.lens[slot(i)];
       if (!good_len(p, len)) {

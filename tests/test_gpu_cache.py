@@ -344,3 +344,24 @@ def test_a_shared_prefix_is_that_of_forked_rows():
     # P's roundings fall differently only where the running maxima differ: 2^-8 of sum p |v| on each side
     assert (a[0] - c[0]).abs().max() <= 2 * 2.0 ** -8 * float(kv[1].abs().max())
     assert torch.allclose(a[1], c[1], atol=1e-5, rtol=1e-6)
+
+
+@pytest.mark.parametrize("n", [33, 64, 1000, 1025, 4096])
+@pytest.mark.parametrize("bad", [-1, 16 * 3 + 1])
+def test_one_bad_length_in_a_long_list_changes_nothing(n, bad):
+    # the row with the bad length in the first warp of the list, in the middle and in the last one
+    b = Both(n, 3, 4096, 16)
+    b.extend(list(range(0, n, 7)), [1 + i % 40 for i in range(0, n, 7)])
+    rows = np.random.default_rng(n).permutation(n).tolist()
+    for at in (0, n // 2, n - 1):
+        good = int(b.lens[rows[at]])
+        calls = [lambda: attn_cache_free(*b.c, ints(rows), 16), lambda: attn_cache_trim(*b.c, 16, 1, 0, ints(rows)),
+                 lambda: attn_cache_trim(*b.c, 16, 1, 0), lambda: attn_cache_extend(*b.c, ints(rows), ints([1] * n), 16),
+                 lambda: attn_cache_fork(*b.c, ints(rows), ints(rows[1:] + rows[:1]), 16), lambda: attn_cache_compact(*b.c, 16)]
+        for call in calls:
+            b.lens[rows[at]] = bad
+            call()
+            assert attn_last_device_error() == B.ATTN_ERR_INVALID_ARG
+            assert int(b.lens[rows[at]]) == bad
+            b.lens[rows[at]] = good
+            b.same()

@@ -560,13 +560,13 @@ constexpr int COPY_T = 256, COPY_U = 4, COPY_CHUNK = COPY_T * COPY_U * 16;
 __global__ void __launch_bounds__(COPY_T) cache_copy_kernel(const __grid_constant__ CopyParams p) {
   after_previous();
   admit_next();
-  const int count = min(max(__ldg(p.copies), 0), p.cap);
+  const int count = min(max(p.copies[0], 0), p.cap);
   const long long units = static_cast<long long>(count) * p.chunks * p.n_pools;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
     const int c = static_cast<int>(u % p.chunks);
     const long long y = u / p.chunks;
     const int pool = static_cast<int>(y % p.n_pools), r = static_cast<int>(y / p.n_pools);
-    const int a = __ldg(p.copies + 1 + r), b = __ldg(p.copies + 1 + p.cap + r);
+    const int a = p.copies[1 + r], b = p.copies[1 + p.cap + r];
     if (a < 0 || b < 0 || a >= p.n_pages || b >= p.n_pages) {
       if (threadIdx.x == 0) atomicCAS(p.status, 0u, static_cast<unsigned>(ATTN_ERR_INVALID_ARG));
       continue;
@@ -616,20 +616,20 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
         b = 0;
         for (int hi = p.n_seqs; hi - b > 1;) {
           const int mid = (b + hi) >> 1;
-          if (__ldg(p.q_ptr + mid) <= t) b = mid;
+          if (p.q_ptr[mid] <= t) b = mid;
           else hi = mid;
         }
-        q0 = __ldg(p.q_ptr + b);
-        q1 = __ldg(p.q_ptr + b + 1);
+        q0 = p.q_ptr[b];
+        q1 = p.q_ptr[b + 1];
       }
       if (t >= q0 && t < q1) {                    // else of no sequence
-        const int slot = p.seqs ? __ldg(p.seqs + b) : b;
+        const int slot = p.seqs ? p.seqs[b] : b;
         bool good = slot >= 0 && slot < p.n_slots && q0 >= 0 && q1 <= p.n_tokens;
         if (good) {
-          const int pos = __ldg(p.lens + slot) - (q1 - t);
+          const int pos = p.lens[slot] - (q1 - t);
           good = pos >= 0 && (pos >> p.shift) < p.max_pages;
           if (good) {
-            const int page = __ldg(p.table + slot * p.table_stride + (pos >> p.shift));
+            const int page = p.table[slot * p.table_stride + (pos >> p.shift)];
             good = page >= 0 && page < p.n_pages;
             at = page * p.page_stride + (pos & ((1 << p.shift) - 1)) * p.token_stride;
           }

@@ -7,7 +7,9 @@
 namespace attn {
 
 // Waits until the grids before this one on the stream have ended and their
-// memory is visible.
+// memory is visible: to ordinary loads, not to those of the read-only path
+// (ld.global.nc), which may give what the SM read before.  So whatever an earlier
+// call may have written (lengths, tables, lists, queries) is read by ordinary ones.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Lets the next grid on the stream start where it asks to start early.
 __device__ __forceinline__ void admit_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

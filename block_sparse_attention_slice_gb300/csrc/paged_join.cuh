@@ -197,7 +197,7 @@ __device__ __forceinline__ int last_not_above(const int32_t *a, int n, int x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(a + mid) <= x) lo = mid;
+    if (a[mid] <= x) lo = mid;
     else hi = mid;
   }
   return lo;

@@ -104,22 +104,22 @@ __device__ __forceinline__ void paged_fail(const PagedParams &p, unsigned code) 
 // The loads that do not depend on one another are issued together.
 __device__ inline SeqInfo seq_info(const PagedParams &p, int b) {
   SeqInfo s;
-  s.slot = p.seqs ? __ldg(p.seqs + b) : b;
+  s.slot = p.seqs ? p.seqs[b] : b;
   const bool in_table = s.slot >= 0 && s.slot < p.n_slots;
-  s.len = p.n_slots > 0 ? __ldg(p.seq_lens + (in_table ? s.slot : 0)) : 0;
+  s.len = p.n_slots > 0 ? p.seq_lens[in_table ? s.slot : 0] : 0;
   bool bad = !in_table;
   int t0 = b, t1 = b + 1;
   if (p.group_ptr) {
-    t0 = __ldg(p.group_ptr + b);
-    t1 = __ldg(p.group_ptr + b + 1);
+    t0 = p.group_ptr[b];
+    t1 = p.group_ptr[b + 1];
     if (t0 < 0 || t1 < t0 || t1 > p.n_members) {
       bad = true;
       t0 = t1 = 0;
     }
   }
   if (p.q_ptr) {
-    t0 = __ldg(p.q_ptr + t0);
-    t1 = __ldg(p.q_ptr + t1);
+    t0 = p.q_ptr[t0];
+    t1 = p.q_ptr[t1];
   }
   if (t0 < 0 || t1 < t0 || t1 > p.n_tokens) {
     bad = true;
@@ -282,8 +282,8 @@ __device__ __noinline__ int my_sms(const PagedParams &p, int sms, float2 *sums) 
     const Share::Side &s = p.share.of[k];
     long long n = 0;
     for (int b = threadIdx.x; b < s.n; b += NT) {
-      const int slot = s.seqs ? __ldg(s.seqs + b) : b;
-      if (slot >= 0 && slot < s.n_slots) n += min(max(__ldg(s.lens + slot), 0), s.max_len);
+      const int slot = s.seqs ? s.seqs[b] : b;
+      if (slot >= 0 && slot < s.n_slots) n += min(max(s.lens[slot], 0), s.max_len);
     }
     keys[k] = static_cast<float>(n) * s.cost + (threadIdx.x ? 0.f : s.base);
   }

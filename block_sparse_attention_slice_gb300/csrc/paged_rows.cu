@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
       if (j > 0 && p.page_shift > 4) {
         page[j] = k0 < in_end ? page[0] : NOT_SEEN;
       } else if (NSUB == 1 || (k0 < in_end && (k0 + (1 << p.page_shift) > in_lo || k0 < p.sinks))) {
-        page[j] = __ldg(p.table + in.s.slot * p.table_stride + (k0 >> p.page_shift));
+        page[j] = p.table[in.s.slot * p.table_stride + (k0 >> p.page_shift)];
       } else {
         page[j] = NOT_SEEN;
       }
@@ -257,10 +257,10 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
       const uint16_t *qb = static_cast<const uint16_t *>(p.q) + (row1 < 0 ? 0 : row1) * D + lc;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        qf[k][0] = row0 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(qa + k * 16));
-        qf[k][1] = row1 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(qb + k * 16));
-        qf[k][2] = row0 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(qa + k * 16 + 8));
-        qf[k][3] = row1 < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(qb + k * 16 + 8));
+        qf[k][0] = row0 < 0 ? 0u : *reinterpret_cast<const uint32_t *>(qa + k * 16);
+        qf[k][1] = row1 < 0 ? 0u : *reinterpret_cast<const uint32_t *>(qb + k * 16);
+        qf[k][2] = row0 < 0 ? 0u : *reinterpret_cast<const uint32_t *>(qa + k * 16 + 8);
+        qf[k][3] = row1 < 0 ? 0u : *reinterpret_cast<const uint32_t *>(qb + k * 16 + 8);
       }
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.f;

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         const int k0 = (Seg::key_tile(j, i0, i1, rot, w.sp) << PT_KL) + lane * R;
         tok = k0 & page_mask;
         const bool seen = lane < ppt && k0 < end && (k0 + R > lo || k0 < p.sinks);
-        return seen ? __ldg(p.table + row + (k0 >> p.page_shift)) : NOT_SEEN;
+        return seen ? p.table[row + (k0 >> p.page_shift)] : NOT_SEEN;
       };
       auto checked = [&](int e) -> int {      // n_pages: zeros
         if (e >= 0 && e < p.n_pages) return e;

@@ -365,3 +365,60 @@ def test_one_bad_length_in_a_long_list_changes_nothing(n, bad):
             assert int(b.lens[rows[at]]) == bad
             b.lens[rows[at]] = good
             b.same()
+
+
+@pytest.mark.parametrize("n,hq,hk,d,new", [(6, 8, 2, 128, 1), (40, 4, 4, 64, 1), (6, 8, 1, 128, 40)])
+def test_calls_behind_one_another_read_what_the_one_before_wrote(n, hq, hk, d, new):
+    # each call starts while the one before drains; the same rounds with the
+    # GPU waited for behind every call, one after the other, and in one graph
+    rng, page, n_pages, rounds = np.random.default_rng(n), 16, 40 * n, 24
+    start = Both(2 * n, 20, n_pages, page)
+    kv = [torch.zeros((n_pages, page, hk, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    plans = []
+    for _ in range(rounds):
+        ids = rng.permutation(2 * n)[:n]
+        counts = rng.integers(new, 200, n)
+        x = torch.from_numpy(rng.standard_normal((2, int(counts.sum()), hk, d)).astype(np.float32)).bfloat16().cuda()
+        q = torch.from_numpy(rng.standard_normal((2, n * new, hq, d)).astype(np.float32)).bfloat16().cuda()
+        src, dst = rng.permutation(2 * n)[:n // 2], rng.permutation(2 * n)[:n // 2]
+        plans.append([ints(ids), ints(counts), ints(np.concatenate([[0], np.cumsum(counts)])), x, q, ints(src), ints(dst)])
+    ptr, groups = ints(list(range(0, n * new + 1, new))), ints([0, n // 2, n])
+
+    def go(table, lens, refs, pools, wait):
+        got = []
+        for ids, counts, starts, x, q, src, dst in plans:
+            attn_cache_free(table, lens, refs, ids, page)
+            wait()
+            attn_cache_extend(table, lens, refs, ids, counts, page)
+            wait()
+            attn_cache_write(pools[0], pools[1], x[0], x[1], table, lens, q_ptr=starts, seqs=ids)
+            wait()
+            got += attn_paged_fwd(q[0], *pools, table, lens, 0.1, q_ptr=ptr, seqs=ids, max_q=new, out_dtype=torch.float32)
+            wait()
+            copies = attn_cache_fork(table, lens, refs, src, dst, page)
+            wait()
+            attn_cache_copy_pages(pools, copies)
+            wait()
+            got += attn_prefix_fwd(q[1], *pools, table[:2], lens[:2], groups, table, lens, 0.1, q_ptr=ptr, seqs=ids, max_q=new,
+                                   out_dtype=torch.float32)
+            wait()
+        return got + [copies]
+
+    def fresh():
+        return [x.clone() for x in start.c] + [[x.clone() for x in kv]]
+
+    want_state = fresh()
+    want = go(*want_state, torch.cuda.synchronize)
+    assert attn_last_device_error() == 0
+    state = fresh()
+    torch.cuda.synchronize()
+    got = go(*state, lambda: None)
+    captured = fresh()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        replayed = go(*captured, lambda: None)
+    g.replay()
+    assert attn_last_device_error() == 0
+    for mine, s in ((got, state), (replayed, captured)):
+        for a, b in zip(mine + s[:3] + s[3], want + want_state[:3] + want_state[3]):
+            assert torch.equal(a, b)

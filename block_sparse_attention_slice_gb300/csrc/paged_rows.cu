@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
 
 #pragma unroll 1
   for (int n = 0; n < cnt; ++n) {
+    // with three slots a slab's note was left before the __syncwarp of the step before; with two, after it
+    if constexpr (NST == 2) __syncwarp();
     const Slab &sl = note[n % NST];
     const int key0 = sl.key0, tile_i = sl.i, tile_n = sl.n;
     if (n == 0 || tile_i == 0) {

@@ -424,3 +424,14 @@ def test_gradients_of_the_windowed_mask():
         e = (a.double().cpu() - b.grad).abs().max() / b.grad.abs().max()
         assert e < 0.02, e
     assert attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("n,hq,hk,d", [(1025, 2, 1, 128), (1400, 4, 2, 64)])
+def test_many_sequences_of_many_slabs(n, hq, hk, d):
+    # above 1024 sequences each warp's ring has two slots
+    rng = np.random.default_rng(n)
+    c = P.make(rng.integers(0, 300, n).tolist(), [1] * n, 16, hq, hk, d, seed=n)
+    for window, sinks in ((0, 0), (70, 20)):
+        out, lse = paged(c, window, sinks, q_ptr=None)
+        assert attn_last_device_error() == 0
+        P.check(c, out, lse, P.reference(c, window, sinks))

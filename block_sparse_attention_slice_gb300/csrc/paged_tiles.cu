@@ -102,6 +102,15 @@ __device__ __forceinline__ void exchange4(uint4 (&w)[4], int q) {
   }
 }
 
+// The end of a launch that gave up: lets the loads in flight, the last of nq into
+// Q and of ld into the ring, land before the CTA retires.  Called where every role
+// has come to its end: the producer may have issued its last loads before another
+// role's wait ran out.
+__device__ __noinline__ void land_loads(uint32_t q_full, uint32_t ring_full, uint32_t ns, uint32_t nq, uint32_t ld) {
+  if (nq > 0) wait_drain(q_full, (nq - 1) & 1, 20000000ull);
+  for (uint32_t i = ld > ns ? ld - ns : 0; i < ld; ++i) wait_drain(ring_full + 8 * (i % ns), (i / ns) & 1, 20000000ull);
+}
+
 // What the producer publishes of a segment: a run of key tiles of one item.
 struct Seg {
   int tok0, ntok, h, pos0, len, ns, w0, i0, i1;
@@ -129,6 +138,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   auto bar = [&](int i) -> uint32_t { return sb + L::BAR_OFF + 8u * i; };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC_OFF);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + L::MISC_OFF + 4);
+  volatile uint32_t *loads = reinterpret_cast<volatile uint32_t *>(smem + L::MISC_OFF + 8);   // of Q and of K/V, in the end
   volatile Seg *segs = reinterpret_cast<volatile Seg *>(smem + L::SEG_OFF);   // 64 bytes apart
   auto seg_at = [&](int s) -> volatile Seg * {
     return reinterpret_cast<volatile Seg *>(reinterpret_cast<volatile uint8_t *>(segs) + 64 * s);
@@ -334,10 +344,9 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       if (at == to && lane == 0 && !p.rec) leave_cut<0, PT_KL>(p, w, tpi, w.h * p.hp + sub, blockIdx.x, mine, span, from, to);
       if (at < to) w.next(p, first, info, tpi);
     }
-    if (*abort && lane == 0) {
-      // let the loads in flight land before the CTA retires
-      if (nseg > 0) wait_drain(bar(L::B_Q), (nseg - 1) & 1, 20000000ull);
-      for (uint32_t i = ld > NS ? ld - NS : 0; i < ld; ++i) wait_drain(bar(L::B_FULL + i % NS), (i / NS) & 1, 20000000ull);
+    if (lane == 0) {
+      loads[0] = nseg;
+      loads[1] = ld;
     }
     __syncwarp();
   } else if (warp == WM) {
@@ -729,7 +738,10 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == WM) tmem_dealloc(tmem, 512);
-  if (threadIdx.x == 0 && *abort) paged_fail(p, ATTN_ERR_TIMEOUT);
+  if (threadIdx.x == 0 && *abort) {
+    paged_fail(p, ATTN_ERR_TIMEOUT);
+    land_loads(bar(L::B_Q), bar(L::B_FULL), NS, loads[0], loads[1]);
+  }
   end_after_previous(p);
 }
 

@@ -435,3 +435,25 @@ def test_many_sequences_of_many_slabs(n, hq, hk, d):
         out, lse = paged(c, window, sinks, q_ptr=None)
         assert attn_last_device_error() == 0
         P.check(c, out, lse, P.reference(c, window, sinks))
+
+
+@pytest.mark.parametrize("news", [6, 100])       # one row tile an item, two
+def test_the_shortest_wait_limit_ends_a_call_in_its_result_or_in_a_timeout(news):
+    # whichever role gives up first, the launch ends with its loads landed, and
+    # the calls behind it are as ever
+    c = P.make([5000, 3000], [news, news], 64, 16, 2, 128, seed=7)
+    pre = P.make([news, news], [news, news], 64, 16, 2, 128, seed=7, plens=[4000], first=[0, 2])
+    want = paged(c) + prefix(pre)
+    assert attn_last_device_error() == 0
+    for _ in range(20):
+        attn_set_wait_limit_ns(1000)         # the least that is taken
+        try:
+            got = paged(c) + prefix(pre)
+            status = attn_last_device_error()
+        finally:
+            attn_set_wait_limit_ns(4_000_000_000)
+        assert status in (0, B.ATTN_ERR_TIMEOUT)
+        if status == 0:
+            assert all(torch.equal(x, y) for x, y in zip(want, got))
+        assert all(torch.equal(x, y) for x, y in zip(want, paged(c) + prefix(pre)))
+        assert attn_last_device_error() == 0

@@ -101,12 +101,13 @@ struct Gather {
 #pragma unroll
     for (int c = 0; c < V; c += 4) {
       const long long at = row * D + column(c);
+      const float y[4] = {finished(acc[c], fo), finished(acc[c + 1], fo), finished(acc[c + 2], fo), finished(acc[c + 3], fo)};
       if (p.out_f32)
         *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
-            make_float4(acc[c] * fo, acc[c + 1] * fo, acc[c + 2] * fo, acc[c + 3] * fo);
+            make_float4(y[0], y[1], y[2], y[3]);
       else
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
-            make_uint2(pack_bf16x2(acc[c] * fo, acc[c + 1] * fo), pack_bf16x2(acc[c + 2] * fo, acc[c + 3] * fo));
+            make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
     }
     if (lane() == 0) p.lse[static_cast<long long>(head) * p.n_tokens + t] = lse;
   }

@@ -395,6 +395,9 @@ __device__ __forceinline__ void row_final(float m, float l, float &fo, float &ls
   lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   if (!(l == l)) fo = lse = l;      // what is not a number stays so
 }
+// A column of a finished row: fo = 0 is a row that sees nothing, whose O is not
+// zero where a value that other rows see is not finite.
+__device__ __forceinline__ float finished(float o, float fo) { return fo == 0.f ? 0.f : o * fo; }
 
 // Writes columns c, c+1 of a finished row.
 template <int D>

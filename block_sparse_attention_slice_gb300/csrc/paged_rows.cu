@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
           float fo, lse;
           row_final(u ? m1 : m0, u ? l1 : l0, fo, lse);
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) store_pair<D>(p, row, j * 8 + lc, o[j][2 * u] * fo, o[j][2 * u + 1] * fo);
+          for (int j = 0; j < D / 8; ++j) store_pair<D>(p, row, j * 8 + lc, finished(o[j][2 * u], fo), finished(o[j][2 * u + 1], fo));
           if (lc == 0) {
             const int t = static_cast<int>(row / p.hq), head = static_cast<int>(row - static_cast<long long>(t) * p.hq);
             p.lse[static_cast<long long>(head) * p.n_tokens + t] = lse;

@@ -111,6 +111,20 @@ __device__ __noinline__ void land_loads(uint32_t q_full, uint32_t ring_full, uin
   for (uint32_t i = ld > ns ? ld - ns : 0; i < ld; ++i) wait_drain(ring_full + 8 * (i % ns), (i / ns) & 1, 20000000ull);
 }
 
+// Zeros over what this thread's row was given, if it sees nothing (`none`): the
+// products of its zero weights are not zero where a value that other rows see is
+// not finite.  TILES = 1: over the group's half of the columns.  A warp together,
+// behind its stores and out of line: that costs a call of 156.5 us 1.2, a choice
+// for each column in the stores cost it 5.
+template <int D, int TILES>
+__device__ __noinline__ void zero_row(const PagedParams &p, bool none, long long row, int grp) {
+  __syncwarp();
+  const int bytes = (TILES == 1 ? D / 2 : D) * (p.out_f32 ? 4 : 2);
+  uint8_t *at = static_cast<uint8_t *>(p.out) + row * (D * (p.out_f32 ? 4 : 2)) + (TILES == 1 ? grp * bytes : 0);
+  for (int x = none ? 0 : bytes; x < bytes; x += 16) *reinterpret_cast<uint4 *>(at + x) = make_uint4(0u, 0u, 0u, 0u);
+  __syncwarp();
+}
+
 // What the producer publishes of a segment: a run of key tiles of one item.
 struct Seg {
   int tok0, ntok, h, pos0, len, ns, w0, i0, i1;
@@ -724,6 +738,8 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
               if (dst[k]) *reinterpret_cast<uint4 *>(dst[k] + c * 64) = w[k];
           }
         }
+        if (final && pos0 < 0)      // the tile's first tokens stand before the sequence's first key
+          zero_row<D, TILES>(p, live && pos0 + tl < 0, static_cast<long long>(tok0 + tl) * p.hq + h * p.G + g, grp);
       }
       tc_fence_before();      // O is read before the next segment's first product
       if constexpr (TILES == 1) {

@@ -88,7 +88,8 @@ int attn_paged_workspace_bytes(int n_tokens, int hq, int d, int prefix, size_t *
  * Cached rows at and behind L, and those that no token of the sequence sees,
  * are never used, whatever they hold.  (A key that some tokens of a sequence
  * see and others do not is masked for those by a weight of zero: a value of it
- * that is not finite can reach them, as in attn_fwd.)
+ * that is not finite can reach them, as in attn_fwd; a token that sees nothing
+ * gets its zeros all the same.)
  * Errors: INVALID_ARG; UNSUPPORTED (d not 64 or 128, page size, strides,
  * alignment, n_seqs > ATTN_PAGED_MAX_SEQS, max_pages * page_size >
  * ATTN_PAGED_MAX_LEN, times n_seqs > ATTN_PAGED_MAX_KEYS, n_tokens * hq >=

@@ -457,3 +457,30 @@ def test_the_shortest_wait_limit_ends_a_call_in_its_result_or_in_a_timeout(news)
             assert all(torch.equal(x, y) for x, y in zip(want, got))
         assert all(torch.equal(x, y) for x, y in zip(want, paged(c) + prefix(pre)))
         assert attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("lens,news,hq,hk,d,max_q", [
+    ([3, 40], [6, 2], 4, 2, 64, 1), ([3, 0], [6, 2], 8, 1, 128, 6), ([20, 9], [50, 12], 8, 2, 128, 50), ([20, 9], [90, 100], 8, 2, 64, 100),
+    ([1500, 5], [1700, 3], 4, 1, 128, 1700), ([1500, 5], [1700, 3], 4, 1, 64, 1)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_token_that_sees_nothing_gets_zeros_whatever_the_others_see(lens, news, hq, hk, d, max_q, dtype):
+    # the cached values of the sequence are infinite: its later tokens get that,
+    # its first ones, which stand before its first key, zeros
+    c = P.make(lens, news, 16, hq, hk, d, seed=3)
+    none = np.concatenate([np.arange(new) < new - n for n, new in zip(lens, news)])
+    c["v"].fill_(float("inf"))
+    out, lse = paged(c, max_q=max_q, out_dtype=dtype)
+    assert attn_last_device_error() == 0
+    none = torch.from_numpy(none).cuda()
+    assert torch.all(out[none] == 0) and torch.all(torch.isneginf(lse[:, none]))
+    assert not torch.isfinite(out[~none]).any() and torch.isfinite(lse[:, ~none]).all()
+
+
+def test_a_token_without_prefix_and_keys_gets_zeros_whatever_the_others_see():
+    c = P.make([3, 2], [6, 7], 16, 8, 2, 128, seed=3, plens=[0, 0], first=[0, 1, 2])
+    c["v"].fill_(float("inf"))
+    out, lse = prefix(c, out_dtype=torch.float32)
+    assert attn_last_device_error() == 0
+    none = torch.tensor([True] * 3 + [False] * 3 + [True] * 5 + [False] * 2, device="cuda")
+    assert torch.all(out[none] == 0) and torch.all(torch.isneginf(lse[:, none]))
+    assert torch.isfinite(lse[:, ~none]).all()

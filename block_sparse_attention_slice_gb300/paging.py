@@ -154,15 +154,25 @@ def attn_cache_write(k_pages, v_pages, k_new, v_new, table, seq_lens, q_ptr=None
     (_module or _m()).cache_write(k_pages, v_pages, k_new, v_new, table, seq_lens, q_ptr, seqs, stream and stream.cuda_stream)
 
 
+def _int32(x, name):
+    """x as int32, refused where that would change a value."""
+    a = np.asarray(x)
+    with np.errstate(invalid="ignore"):
+        b = a.astype(np.int32, order="C")
+    if not np.array_equal(a, b):
+        raise ValueError(f"{name}: whole numbers of 32 bits are needed")
+    return b
+
+
 def attn_slices_from_windows(lengths: Sequence[int], window: int, sinks: int = 0) -> np.ndarray:
     """Windowed causal mask of packed sequences -> slice list (host), for
     ``attn_build_tiles``: a token sees its sequence's keys j <= i with
     j > i - window or j < sinks (window 0: all)."""
-    a = np.ascontiguousarray(np.asarray(lengths, dtype=np.int32).reshape(-1))
+    a = _int32(lengths, "lengths").reshape(-1)
     n = ctypes.c_int(0)
     out = np.zeros((max(1, 3 * len(a)), 5), dtype=np.int32)
-    B._check(B.load().attn_slices_from_windows(a.ctypes.data, len(a), int(window), int(sinks), out.ctypes.data,
-                                               3 * len(a), ctypes.byref(n)), "attn_slices_from_windows")
+    B._check(B.load().attn_slices_from_windows(a.ctypes.data, len(a), int(_int32(window, "window")), int(_int32(sinks, "sinks")),
+                                               out.ctypes.data, 3 * len(a), ctypes.byref(n)), "attn_slices_from_windows")
     return out[:n.value]
 
 

@@ -270,3 +270,21 @@ def test_outputs_on_top_of_inputs_are_refused(lib, prefix):
                 dict(q=p(1 << 20), out=p((1 << 20) - 10224), out_dtype=1), dict(q=p(1 << 20), out=p(4096 + 81904)),
                 dict(q=p(1 << 20), out=p(1 << 24), pages__v=(1 << 24) - 16)):
         assert _call(lib, _args(**{**clear, **bad}), prefix) == INV
+
+
+@pytest.mark.parametrize("args", [([100], 2 ** 32 + 3, 0), ([100], 2 ** 31, 0), ([100], 4, 2 ** 32), ([100], -2 ** 32 + 4, 0), ([100], 4, 2 ** 64),
+                                  (np.array([2 ** 32 + 5]), 4, 0), (np.array([7, 2 ** 31]), 4, 0), (np.array([-2 ** 32 + 5]), 4, 0),
+                                  (np.array([2 ** 63 + 5], np.uint64), 4, 0), ([2 ** 70], 4, 0), ([7.5], 4, 0), ([7], 4.5, 0),
+                                  ([float("nan")], 4, 0), ([7], float("inf"), 0)], ids=str)
+def test_windowed_slices_refuse_what_32_bits_do_not_hold(lib, args):
+    with pytest.raises((ValueError, OverflowError)):
+        G.attn_slices_from_windows(*args)
+
+
+def test_windowed_slices_take_whole_numbers_of_any_type(lib):
+    want = G.attn_slices_from_windows([70, 9], 33, 2)
+    for lengths, window, sinks in ((np.array([70, 9], np.int64), 33, 2), (np.array([70, 9], np.uint8), np.int64(33), np.int8(2)),
+                                   ([70.0, 9.0], 33.0, 2), ((70, 9), 33, 2)):
+        assert np.array_equal(G.attn_slices_from_windows(lengths, window, sinks), want)
+    import torch
+    assert np.array_equal(G.attn_slices_from_windows(torch.tensor([70, 9]), torch.tensor(33), 2), want)

@@ -16,7 +16,6 @@ import ctypes
 from typing import Sequence
 
 import numpy as np
-import torch
 
 from . import binding as B
 
@@ -27,6 +26,7 @@ def _m():
     """The marshalling module (built by ``__graft_entry__.build()``)."""
     global _module
     if _module is None:
+        import torch  # noqa: F401 -- the module's libraries are PyTorch's
         B.load()
         try:
             from . import _paging
@@ -39,6 +39,7 @@ def _m():
 
 def _on(stream, *tensors):
     """The raw handle of `stream`; tensors allocated on the current stream become its too."""
+    import torch
     here = torch.cuda.current_stream(tensors[0].device)
     if stream != here:
         stream.wait_stream(here)
@@ -49,6 +50,7 @@ def _on(stream, *tensors):
 
 def _made(q, out, lse, out_dtype, ws, d, prefix, stream):
     """Outputs and workspace for a call on another stream than the current one."""
+    import torch
     t, hq = q.shape[0], q.shape[1]
     made = []
     if out is None:
@@ -115,6 +117,7 @@ def attn_cache_trim(table, seq_lens, refs, page_size: int, window: int, sinks: i
 
 def _list_on(stream, table, cap, bytes_):
     """Copy list and workspace for a call on another stream than the current one."""
+    import torch
     copies = torch.empty(1 + 2 * cap, dtype=torch.int32, device=table.device)
     ws = torch.empty(bytes_, dtype=torch.uint8, device=table.device)
     return copies, ws, _on(stream, copies, ws)

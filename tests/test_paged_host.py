@@ -1,6 +1,9 @@
 """Attention over a paged cache, on the CPU: the oracle against brute force,
 the windowed slice list, and every refusal made before a launch."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -288,3 +291,15 @@ def test_windowed_slices_take_whole_numbers_of_any_type(lib):
         assert np.array_equal(G.attn_slices_from_windows(lengths, window, sinks), want)
     import torch
     assert np.array_equal(G.attn_slices_from_windows(torch.tensor([70, 9]), torch.tensor(33), 2), want)
+
+
+def test_the_package_and_its_host_functions_do_without_torch(lib):
+    # PyTorch is needed where tensors are taken, not to import the package or to make a slice list
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import block_sparse_attention_slice_gb300 as attn\n"
+            "attn.load()\n"
+            "print(len(attn.attn_slices_from_windows([70, 9], 33, 2)), len(attn.attn_slices_from_block_grid([[1, 0], [1, 2]], 64, 64)))\n")
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert done.returncode == 0, done.stderr
+    assert done.stdout.split() == [str(len(G.attn_slices_from_windows([70, 9], 33, 2))), "3"]

@@ -3,13 +3,14 @@ marshalling module ``_paging.so`` with g++ against PyTorch's headers.
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel, then linked
 into one shared library next to this file; ``csrc/paging_module.cpp`` compiles
-beside them.  Rebuilds only when a source or header is newer than what is
-built.
+beside them.  The library needs nvcc alone.  Rebuilds only when a source or
+header is newer than what is built.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -22,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattn_slice.so")
 MODULE = os.path.join(HERE, "_paging.so")
+MODULE_SRC = os.path.join(CSRC, "paging_module.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "-I" + os.path.join(ROOT, "include")]
@@ -34,20 +36,29 @@ def _nvcc():
     return cand
 
 
+def _cxx():
+    return os.environ.get("CXX") or "g++"
+
+
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
+def _newer(built, deps) -> bool:
+    return os.path.exists(built) and all(os.path.getmtime(p) <= os.path.getmtime(built) for p in deps)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
+                  glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
+
+
+def module_up_to_date() -> bool:
+    return _newer(MODULE, [MODULE_SRC] + glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MODULE):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return library_up_to_date() and module_up_to_date()
 
 
 def _module_flags(nvcc):
@@ -64,14 +75,25 @@ def _module_flags(nvcc):
 
 
 def _run(cmd, what):
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"{what}: {e}") from e
     if r.returncode != 0:
         raise RuntimeError(f"{what}:\n{r.stderr[-4000:]}")
+    return r
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compiles the library if needed and returns its path."""
-    if not force and up_to_date():
+def _has_torch() -> bool:
+    try:
+        return importlib.util.find_spec("torch") is not None
+    except ValueError:          # sys.modules holds None for it
+        return False
+
+
+def build_library(force: bool = False) -> str:
+    """Compiles the C library if needed, with nvcc alone, and returns its path."""
+    if not force and library_up_to_date():
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -87,25 +109,39 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr[-4000:]}")
         return obj
 
-    cc, ld = _module_flags(nvcc)
-    cxx = os.environ.get("CXX") or "g++"
-    module_obj = os.path.join(BUILD, "paging_module.o")
-    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        module = ex.submit(_run, [cxx, *cc, "-c", os.path.join(CSRC, "paging_module.cpp"), "-o", module_obj],
-                           "compiling paging_module.cpp failed")
+    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
         objs = list(ex.map(compile_one, srcs))
-        module.result()
-    tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
-    os.replace(tmp, LIB)
-    _run([cxx, "-shared", "-o", MODULE + ".tmp", module_obj, *ld], "linking _paging.so failed")
-    os.replace(MODULE + ".tmp", MODULE)
+    _run([nvcc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs], "linking libattn_slice.so failed")
+    os.replace(LIB + ".tmp", LIB)
+    return LIB
+
+
+def _compile_module() -> str:
+    os.makedirs(BUILD, exist_ok=True)
+    cc, _ = _module_flags(_nvcc())
+    obj = os.path.join(BUILD, "paging_module.o")
+    _run([_cxx(), *cc, "-c", MODULE_SRC, "-o", obj], "compiling paging_module.cpp failed")
+    return obj
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compiles what is needed, the library first, and returns its path.
+
+    The module needs a C++ compiler and the headers of PyTorch and Python: it is
+    left out where there is no PyTorch, whose tensors alone it serves, and what
+    goes wrong with it is raised once the library stands."""
+    todo = _has_torch() and (force or not module_up_to_date())
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        module = ex.submit(_compile_module) if todo else None
+        build_library(force)
+        if module:
+            obj = module.result()
+            _, ld = _module_flags(_nvcc())
+            _run([_cxx(), "-shared", "-o", MODULE + ".tmp", obj, *ld], "linking _paging.so failed")
+            os.replace(MODULE + ".tmp", MODULE)
     if verbose:
-        for o in objs:
-            sys.stdout.write(open(o + ".log").read())
+        for log in sorted(glob.glob(os.path.join(BUILD, "*.log"))):
+            sys.stdout.write(open(log).read())
     return LIB
 
 

@@ -422,3 +422,28 @@ def test_calls_behind_one_another_read_what_the_one_before_wrote(n, hq, hk, d, n
     for mine, s in ((got, state), (replayed, captured)):
         for a, b in zip(mine + s[:3] + s[3], want + want_state[:3] + want_state[3]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bad_page", [-7, -1, 10 ** 8, "n_pages"])
+@pytest.mark.parametrize("bad_slot", [-1, "n_slots", 2 ** 31 - 1])
+@pytest.mark.parametrize("hk,d", [(3, 64), (8, 128)])
+def test_a_write_leaves_out_just_the_tokens_that_have_no_place(bad_page, bad_slot, hk, d):
+    # sequence 0: its second page is good, its third not; 1: a slot that is none;
+    # 2: as it should be; 3: two new tokens, but one in its length
+    page, lens, news = 16, [40, 20, 17, 1], [20, 5, 17, 2]
+    c = P.make(lens, news, page, hk, hk, d, seed=1, slots=[3, 0, 1, 5], garbage=0.0)
+    n_pages, n_slots = c["k"].shape[0], c["table"].shape[0]
+    k_new, v_new = torch.randn((2, sum(news), hk, d), device="cuda").bfloat16()
+    want = [c["k"].clone(), c["v"].clone()]
+    t = 0
+    for b, (n, new) in enumerate(zip(lens, news)):
+        for j in range(n - new, n):
+            if j >= 0 and b != 1 and (b, j // page) != (0, 2):
+                at = int(c["table"][c["seqs"][b], j // page])
+                want[0][at, j % page], want[1][at, j % page] = k_new[t], v_new[t]
+            t += 1
+    c["d_table"][3, 2] = n_pages if bad_page == "n_pages" else bad_page
+    c["d_seqs"][1] = n_slots if bad_slot == "n_slots" else bad_slot
+    attn_cache_write(c["k"], c["v"], k_new, v_new, c["d_table"], c["d_lens"], q_ptr=c["d_q_ptr"], seqs=c["d_seqs"])
+    assert attn_last_device_error() == B.ATTN_ERR_INVALID_ARG
+    assert torch.equal(c["k"], want[0]) and torch.equal(c["v"], want[1])

@@ -271,12 +271,13 @@ __device__ inline void make_plan(const PagedParams &p, int tpi, long long *first
   __syncthreads();
 }
 
-// SMs of this pass, of `sms`: a function of the sequences' lengths alone.  All NT
+// SMs of this pass, of `sms`: a function of the sequences' lengths alone, summed in
+// whole numbers, so that both passes come to one answer whatever their NT.  All NT
 // threads of the block come here; `sums` has NT / 32 places.  Out of line: in line
 // it cost the calls that do not share 0.4 to 1.5 us.
 template <int NT>
-__device__ __noinline__ int my_sms(const PagedParams &p, int sms, float2 *sums) {
-  float keys[2];
+__device__ __noinline__ int my_sms(const PagedParams &p, int sms, longlong2 *sums) {
+  long long keys[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const Share::Side &s = p.share.of[k];
@@ -285,21 +286,23 @@ __device__ __noinline__ int my_sms(const PagedParams &p, int sms, float2 *sums) 
       const int slot = s.seqs ? s.seqs[b] : b;
       if (slot >= 0 && slot < s.n_slots) n += min(max(s.lens[slot], 0), s.max_len);
     }
-    keys[k] = static_cast<float>(n) * s.cost + (threadIdx.x ? 0.f : s.base);
+    keys[k] = n;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     keys[0] += __shfl_xor_sync(0xffffffffu, keys[0], o);
     keys[1] += __shfl_xor_sync(0xffffffffu, keys[1], o);
   }
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = make_float2(keys[0], keys[1]);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = make_longlong2(keys[0], keys[1]);
   __syncthreads();
-  float a = 0.f, b = 0.f;
+  keys[0] = keys[1] = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
-    a += sums[w].x;
-    b += sums[w].y;
+    keys[0] += sums[w].x;
+    keys[1] += sums[w].y;
   }
+  const Share::Side &f = p.share.of[0], &g = p.share.of[1];
+  const float a = __fmaf_rn(static_cast<float>(keys[0]), f.cost, f.base), b = __fmaf_rn(static_cast<float>(keys[1]), g.cost, g.base);
   const int u = p.share.unit, most = (sms - 1) / u;      // at least one unit, and one SM for the other
   const int first = u * min(max(static_cast<int>(sms * (a / (a + b)) / u + 0.5f), 1), most);
   return p.share.side == 1 ? first : sms - first;

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int sms = gridDim.x;
   if (p.share.side) {
-    sms = my_sms<S::W * 32>(p, sms, reinterpret_cast<float2 *>(rows_smem));
+    sms = my_sms<S::W * 32>(p, sms, reinterpret_cast<longlong2 *>(rows_smem));
     if (static_cast<int>(blockIdx.x) >= sms) {
       end_after_previous(p);
       return;

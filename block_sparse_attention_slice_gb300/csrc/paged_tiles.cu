@@ -77,6 +77,7 @@ struct TileLayout {
     return 1024 + FIRST_OFF + (p.warp_plan ? THREADS / 32 * static_cast<size_t>(PLAN_WARP)
                                            : 8ull * (p.n_seqs + 1) + (infos ? sizeof(SeqInfo) * p.n_seqs : 0));
   }
+  static_assert(PT_IQ * 64 >= THREADS / 32 * 16, "my_sms puts its sums where the segments will be");
   static_assert(MISC_OFF % 8 == 0 && (TILES == 1 || NS % 2 == 0), "alignment; keys in even slots");
 };
 
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   if (p.share.side) {
     if (!p.wait_end) after_previous();
     admit_next();
-    sms = my_sms<L::THREADS>(p, sms, reinterpret_cast<float2 *>(scan));
+    sms = my_sms<L::THREADS>(p, sms, reinterpret_cast<longlong2 *>(smem + L::SEG_OFF));      // no segment is published yet
     if (static_cast<int>(blockIdx.x) >= sms) {
       end_after_previous(p);
       return;

@@ -484,3 +484,17 @@ def test_a_token_without_prefix_and_keys_gets_zeros_whatever_the_others_see():
     none = torch.tensor([True] * 3 + [False] * 3 + [True] * 5 + [False] * 2, device="cuda")
     assert torch.all(out[none] == 0) and torch.all(torch.isneginf(lse[:, none]))
     assert torch.isfinite(lse[:, ~none]).all()
+
+
+@pytest.mark.parametrize("seed", range(3))
+def test_hundreds_of_sequences_behind_prefixes_of_any_length(seed):
+    # both passes add up the lengths of all sequences, with blocks of different sizes, to share the SMs
+    rng = np.random.default_rng(seed)
+    n, groups = int(rng.integers(300, 900)), int(rng.integers(1, 12))
+    first = np.sort(rng.integers(0, n + 1, groups + 1)).tolist()
+    c = P.make(rng.integers(0, 120, n).tolist(), [1] * n, 16, 8, 2, 64, seed=seed, plens=rng.integers(0, 3000, groups).tolist(), first=first)
+    out, lse = prefix(c)
+    assert attn_last_device_error() == 0
+    P.check(c, out, lse, P.reference(c))
+    again = prefix(c)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)

@@ -9,12 +9,13 @@
 // calls.  32 rows of up to 128 pages fork in 8 us, 64 rows free and extend in 5
 // and 6; half a million pages take 68 us to free and extend, 137 to fork, bound
 // by the cluster's 8 SMs.  Clusters of 1, 2 or 4 CTAs gave the small calls 1 us
-// and the large ones up to 8 times their time.  Work over the sequences of a list is flattened: a block-wide prefix
-// sum of their page counts, then every thread takes flat indices 8192 apart and
-// finds its sequence by bisection in shared memory, so one long sequence costs
-// no more than many short ones.  Results are exact and do not depend on the
-// order of atomics: adding and subtracting counts commutes, and fresh pages
-// are chosen from the counts as they stood before the call.
+// and the large ones up to 8 times their time.  Work over the sequences of a list
+// is flattened: a block-wide prefix sum of their page counts, then every thread
+// takes flat indices 8192 apart and finds its sequence by bisection in shared
+// memory, so one long sequence costs no more than many short ones.  Results are
+// exact and do not depend on the order of atomics: adding and subtracting counts
+// commutes, and fresh pages are chosen from the counts as they stood before the
+// call.
 //
 // A call either does all it was asked for or, when a list names a row out of
 // range or twice, or free pages or table columns run out, changes nothing and
@@ -595,12 +596,12 @@ struct WriteParams {
 
 // A warp takes p.run tokens at a time: 2 where that leaves every SM 32 warps, else
 // 1.  Its lanes find the tokens' sequences and pages, a token a lane, then move
-// token after token together, a token's 16-byte words (WORDS a lane, keys and
+// token after token together, a token's 16-byte words (WRITE_WORDS a lane, keys and
 // values) all loaded before the first is stored.  Bound by HBM: 43200 tokens of 8
 // heads of 128 read and written (354 MB) in 58 us, 6.1 TB/s; word by word 61, one
 // token at a time 59.5, four 57.4 but more where the tokens are still in L2
 // (48.4 us of a server's round of arrivals with two, 49.1 with one, 49.9 with four).
-template <int WORDS>
+constexpr int WRITE_WORDS = 4;
 __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
   after_previous();
   admit_next();
@@ -646,10 +647,10 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
       const long long to = __shfl_sync(0xffffffffu, at, i);
       if (to < 0) continue;
       const long long from = (t0 + i) * p.new_token;
-      for (int w0 = lane; w0 < all; w0 += 32 * WORDS) {
-        int4 x[WORDS], y[WORDS];
+      for (int w0 = lane; w0 < all; w0 += 32 * WRITE_WORDS) {
+        int4 x[WRITE_WORDS], y[WRITE_WORDS];
 #pragma unroll
-        for (int k = 0; k < WORDS; ++k) {
+        for (int k = 0; k < WRITE_WORDS; ++k) {
           const int w = w0 + 32 * k, h = w / p.words, c = (w - h * p.words) * 8;
           if (w < all) {
             x[k] = __ldcs(reinterpret_cast<const int4 *>(p.k_new + from + h * p.new_head + c));
@@ -657,7 +658,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
           }
         }
 #pragma unroll
-        for (int k = 0; k < WORDS; ++k) {
+        for (int k = 0; k < WRITE_WORDS; ++k) {
           const int w = w0 + 32 * k, h = w / p.words, c = (w - h * p.words) * 8;
           if (w < all) {
             *reinterpret_cast<int4 *>(p.k + to + h * p.head_stride + c) = x[k];
@@ -879,7 +880,7 @@ int attn_cache_write(const attn_pages_t *pages, const attn_seqs_t *seqs, const i
   if (sms <= 0) return ATTN_ERR_CUDA;
   p.run = n_tokens >= sms * 64 ? 2 : 1;
   const int blocks = (n_tokens + 8 * p.run - 1) / (8 * p.run), grid = sms * 8;
-  return launch_after(cache_write_kernel<4>, dim3(blocks < grid ? blocks : grid), 256, 0,
+  return launch_after(cache_write_kernel, dim3(blocks < grid ? blocks : grid), 256, 0,
                       reinterpret_cast<cudaStream_t>(stream), p);
 }
 

@@ -25,7 +25,6 @@
 namespace attn {
 
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kLog2e = 1.4426950408889634f;
 
 // Left by each worker for the join: the item that begins in its span and goes
 // on behind it (rows = 0: none).  Row x0 + r, r < rows, of the sequence whose
@@ -79,7 +78,7 @@ struct PagedParams {
   float *part_ml;
   Cut *cuts;                  // [workers]
   int warp_plan;              // make_warp_plan, not make_plan
-  int hp, n_spans, min_span;  // heads side by side; spans; key tiles a span holds at least
+  int hp, n_spans;            // heads side by side; spans
   Share share;
   int test_stall;             // failure-path test: leave one load out
   unsigned int *status;
@@ -308,9 +307,9 @@ __device__ __noinline__ int my_sms(const PagedParams &p, int sms, longlong2 *sum
   return p.share.side == 1 ? first : sms - first;
 }
 
-__device__ __forceinline__ long long span_of(const PagedParams &p, long long total, int n_spans) {
+__device__ __forceinline__ long long span_of(long long total, int n_spans) {
   const long long s = (total + n_spans - 1) / n_spans;
-  return s > p.min_span ? s : p.min_span;
+  return s > 1 ? s : 1;
 }
 
 // A place in the flat list: key tile i of row tile rt of head group h of sequence b.

@@ -47,8 +47,7 @@
 namespace attn {
 
 constexpr int PR_ROWS = 16;
-// warps of a CTA: as many as the registers of a head dim's accumulators leave
-__host__ __device__ constexpr int rows_warps(int) { return 8; }
+constexpr int PR_WARPS = 8;        // warps of a CTA (12 at head dim 64: no faster)
 constexpr float PR_TAU = 8.0f;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -89,7 +88,7 @@ struct __align__(16) Slab {
 
 template <int D, int NST>
 struct RowsSmem {
-  static constexpr int W = rows_warps(D);
+  static constexpr int W = PR_WARPS;
   static constexpr int KEYS = 1 << rows_kl(D);
   static constexpr int PART = KEYS * D * 2;                     // keys or values of one slab
   static constexpr int RING = W * NST * 2 * PART;
@@ -102,7 +101,7 @@ struct RowsSmem {
 };
 
 template <int D, int NST>
-__global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(PR_WARPS * 32, 1) paged_rows_kernel(const PagedParams p) {
   using S = RowsSmem<D, NST>;
   constexpr int KL = rows_kl(D), KEYS = S::KEYS, NSUB = KEYS / 16, NB = KEYS / 8;
   constexpr int NOT_SEEN = INT_MIN;
@@ -127,7 +126,7 @@ __global__ void __launch_bounds__(rows_warps(D) * 32, 1) paged_rows_kernel(const
   finish_empty<D, PR_ROWS, KL>(p, info, 0, sms);
 
   const int n_spans = p.share.side ? sms * S::W / p.hp : p.n_spans;
-  const long long total = first[p.n_seqs], span = span_of(p, total, n_spans);
+  const long long total = first[p.n_seqs], span = span_of(total, n_spans);
   const long long worker = static_cast<long long>(blockIdx.x) * S::W + warp, span_no = worker / p.hp;
   const int sub = static_cast<int>(worker - span_no * p.hp);    // this warp's head of a group
   const long long from = min(span_no * span, total), to = min(total, from + span);
@@ -419,7 +418,6 @@ static int launch_rows(PagedParams &p, cudaStream_t s) {
   while (p.hp < S::W && p.hk % (2 * p.hp) == 0) p.hp *= 2;
   p.n_spans = sms * S::W / p.hp;
   p.warp_plan = p.n_seqs <= 32 && (!p.causal || static_cast<long long>(p.n_tokens) * p.G <= 64 * PR_ROWS);
-  p.min_span = 1;
   const int rc = launch_after(kern, dim3(sms), S::W * 32, S::bytes(p), s, p);
   if (rc != ATTN_OK || p.rec) return rc;
   // few items: each has many pieces, and its rows go to blocks of their own
@@ -429,20 +427,20 @@ static int launch_rows(PagedParams &p, cudaStream_t s) {
 
 // Floats of all workers' pieces of `tile_rows` rows.
 size_t paged_piece_floats(int tile_rows, int d) {
-  return static_cast<size_t>(device_sm_count()) * (tile_rows == PR_ROWS ? rows_warps(d) : 1) * 2 * tile_rows * d;
+  return static_cast<size_t>(device_sm_count()) * (tile_rows == PR_ROWS ? PR_WARPS : 1) * 2 * tile_rows * d;
 }
 
 size_t paged_rows_workspace(int d) {
   const int sms = device_sm_count();
   if (sms <= 0) return 0;
-  return static_cast<size_t>(sms) * rows_warps(d) * (2 * PR_ROWS * (d + 2) * sizeof(float) + sizeof(Cut));
+  return static_cast<size_t>(sms) * PR_WARPS * (2 * PR_ROWS * (d + 2) * sizeof(float) + sizeof(Cut));
 }
 
 int paged_rows_launch(PagedParams &p, int d, cudaStream_t s) {
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   p.part_ml = p.part_o + paged_piece_floats(PR_ROWS, d);
-  p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * rows_warps(d) * 2 * PR_ROWS * 2);
+  p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * PR_WARPS * 2 * PR_ROWS * 2);
   // a ring of 192 KB, or 128 where thousands of sequences take the room
   const bool many = p.n_seqs > 1024;
   if (d == 128) return many ? launch_rows<128, 2>(p, s) : launch_rows<128, 3>(p, s);

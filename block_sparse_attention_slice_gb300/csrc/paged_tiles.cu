@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int n_spans = p.share.side ? sms / p.hp : p.n_spans;
-  const long long total = first[p.n_seqs], span = span_of(p, total, n_spans);
+  const long long total = first[p.n_seqs], span = span_of(total, n_spans);
   const int mine = blockIdx.x / p.hp, sub = blockIdx.x - mine * p.hp;      // span, and head of a group
   const long long from = mine < n_spans ? mine * span : total, to = min(total, from + span);
 
@@ -668,8 +668,8 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       if (!idle) {
         // Four lanes exchange 16-byte words so that each row leaves in 64-byte
         // runs: a lane alone has 16 bytes of 32 different rows an instruction,
-        // half sectors that L2 has to merge.  Neither was faster by more than the noise; a segment's epilogue takes 2.1 us to bf16
-        // and 3.7 to f32 pieces.
+        // half sectors that L2 has to merge.  Faster than that by no more than
+        // the noise; a segment's epilogue takes 2.1 us to bf16 and 3.7 to f32 pieces.
         const int q4 = lane & 3;
         const bool final = out == 0 && !p.rec, f32 = !final || p.out_f32;
         float fo = 1.f, lse;
@@ -798,7 +798,6 @@ int launch_tiles(PagedParams &p, const CUtensorMap &mq, const CUtensorMap &mk, c
   if (sms <= 0) return ATTN_ERR_CUDA;
   p.hp = paged_tiles_heads(sms, p.hk);
   p.n_spans = sms / p.hp;
-  p.min_span = 1;
   p.part_ml = p.part_o + paged_piece_floats(TILES * 128, D);
   p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * 2 * TILES * 128 * 2);
   const bool infos = L::bytes(p, true) <= kSmemMax;

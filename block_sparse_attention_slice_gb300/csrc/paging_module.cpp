@@ -294,6 +294,7 @@ PyObject *cache_trim(PyObject *const *a) {
   const int window = integer(a[4], "window"), sinks = integer(a[5], "sinks");
   const Tensor *seqs = maybe(a[6], "seqs");
   const int32_t *s = ints(seqs, "seqs", c.device);
+  if (seqs && !s) s = c.c.seq_lens;      // a list of no rows has no address; to the call a null one is all rows
   const int n = seqs ? narrow(seqs->size(0), "n") : c.c.n_slots;
   attn_stream_t st = stream_of(a[7], c.device);
   call("attn_cache_trim", c.device, [&] { return attn_cache_trim(&c.c, s, n, window, sinks, st); });

@@ -447,3 +447,26 @@ def test_a_write_leaves_out_just_the_tokens_that_have_no_place(bad_page, bad_slo
     attn_cache_write(c["k"], c["v"], k_new, v_new, c["d_table"], c["d_lens"], q_ptr=c["d_q_ptr"], seqs=c["d_seqs"])
     assert attn_last_device_error() == B.ATTN_ERR_INVALID_ARG
     assert torch.equal(c["k"], want[0]) and torch.equal(c["v"], want[1])
+
+
+def test_lists_of_no_rows_change_nothing():
+    b = Both(3, 6, 20, 16)
+    b.extend([0, 2], [70, 33])
+    b.extend([], [])
+    b.free([])
+    b.trim(5, 0, [])
+    b.fork([], [])
+    empty = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros((2, 20, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = attn_paged_fwd(empty, kv[0], kv[1], b.table, b.lens, 0.1, seqs=ints([]))
+    assert out.shape == (0, 2, 64) and lse.shape == (2, 0)
+    out, lse = attn_prefix_fwd(empty, kv[0], kv[1], b.table[:1], b.lens[:1], ints([0, 0]), b.table, b.lens, 0.1, seqs=ints([]))
+    assert out.shape == (0, 2, 64) and lse.shape == (2, 0)
+    attn_cache_write(kv[0], kv[1], empty, empty, b.table, b.lens, seqs=ints([]))
+    attn_cache_copy_pages([], ints([0]))
+    attn_cache_copy_pages([kv[0]], ints([0]))
+    b.same()
+    assert not kv.any()
+    with pytest.raises(B.AttnError):
+        attn_cache_trim(*b.c, 16, 0, 0, ints([]))      # its other arguments are looked at all the same
+    b.trim(5, 0)

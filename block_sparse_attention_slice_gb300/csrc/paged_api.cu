@@ -158,7 +158,7 @@ int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_ro
 // Against one pass after the other (32 query and 8 key/value heads of 128): 16
 // sequences with 2048 keys before 52 each, 25.6 -> 21.6 us; 32 with 32768 before
 // 109, 59 -> 46; 32 with 4096 before 1755, 77 -> 61; 256 with 32768 before 219,
-// 174.7 -> 164 (154 since).  Of 16 heads of 64: 128 with 16384 before 219, 70 ->
+// 174.7 -> 164 (155 since).  Of 16 heads of 64: 128 with 16384 before 219, 70 ->
 // 63; 50 with 6817 before 150, two tokens each, 51.3 -> 50.
 Share share_of(const PagedParams &p, int p_tokens, const PagedParams &r, int r_tokens, int d) {
   Share s;

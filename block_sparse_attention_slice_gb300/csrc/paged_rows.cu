@@ -14,9 +14,9 @@
 //
 // The 8 warps of a CTA take neighbouring heads of the same keys, whose rows lie
 // side by side in a page: a CTA reads runs of 1 to 2 KB a token instead of 128
-// or 256 bytes.  At 2.9 GB of keys and values that took the kernel from 441 to
-// 408 us (7.2 TB/s), at 250 MB of 64-column heads from 52 to 47 us.  64 sequences
-// with a window of 4096 (763 MB): 115 to 120 us, 6.5 TB/s, 95 % of what a plain
+// or 256 bytes.  At 2.9 GB of keys and values that took 33 us off the 441 of the
+// kernel (a call now 412, 7.0 TB/s), at 250 MB of 64-column heads 5 off 52.  64
+// sequences with a window of 4096 (763 MB): 119 us, 6.4 TB/s, 95 % of what a plain
 // copy reaches.  One sequence (1028 keys) takes 12 us, all of it latency: the
 // launch, then slot, length, table entry and keys one after the other, then the
 // join.

@@ -17,7 +17,7 @@
 //
 // What bounds it.  Rows that fill their tiles: the chain of products and softmax
 // that attn_fwd has.  4 x 1021 new tokens, window 4096, 32 query and 8 key/value
-// heads of 128 columns: 157 us, 73 steps a CTA of 256 rows by 128 keys at 1.56 us
+// heads of 128 columns: 159 us, 73 steps a CTA of 256 rows by 128 keys at 1.56 us
 // (1.6 PFLOP/s over all SMs), and around them 10 us before the first product, 4.4
 // at a change of item, 8 for the join.  The lane that issues is busy nearly all of
 // a step: a commit takes it some 95 cycles, an instruction what the tensor core

@@ -78,7 +78,9 @@ def attn_paged_fwd(q, k_pages, v_pages, table, seq_lens, scale: float, q_ptr=Non
     one token a sequence); seqs int32 [n_seqs] table rows (None: all, in
     order).  A token at position i sees keys j <= i with j > i - window or
     j < sinks (window 0: all).  ``max_q`` is about the most tokens of one
-    sequence and only picks the kernel."""
+    sequence and only picks the kernel.  None: 1 without q_ptr, n_tokens with
+    it, so give it for batches of short sequences, which otherwise run on the
+    kernel of long ones."""
     if stream is not None:
         out, lse, ws, stream = _made(q, out, lse, out_dtype, ws, k_pages.shape[-1], 0, stream)
     return (_module or _m()).paged_fwd(q, k_pages, v_pages, table, seq_lens, scale, q_ptr, max_q, window, sinks, seqs, out, lse,

@@ -29,6 +29,12 @@
  *   attn_cache_trim, are -1.  seq_lens[slot] counts the tokens.  refs[p]
  *   counts the table rows that hold page p; a page is free when it is 0.
  *   A page that is not full belongs to one sequence only.
+ *   The attn_cache_* calls keep all of this, and lengths change by them alone.
+ *   There is no call that takes single tokens back.  A caller that lowers a
+ *   length itself (rejected tokens of a verified batch) may do so only where the
+ *   row keeps its number of pages and no other row holds its last one.  A page
+ *   that the length leaves behind stays counted for good: attn_cache_free passes
+ *   it by, attn_cache_extend writes over its entry.
  */
 #ifndef ATTN_PAGED_H
 #define ATTN_PAGED_H
@@ -76,14 +82,17 @@ int attn_paged_workspace_bytes(int n_tokens, int hq, int d, int prefix, size_t *
  *             n_tokens == n_seqs).  Rows outside every sequence's range are
  *             not read, and their outputs are left as they were.
  *   max_q     about the largest number of tokens of one sequence; only picks
- *             the kernel, any value >= 1 gives the same result up to rounding
+ *             the kernel, any value >= 1 gives the same result up to rounding.
+ *             Far too large a value costs time: many short sequences then run
+ *             on tiles made for long ones
  * With L = seq_lens[slot] and n = q_ptr[b+1] - q_ptr[b], token t of sequence b
  * stands at position i = L - n + t (its own key is cached already) and sees the
  * keys j <= i with j > i - window or j < sinks; window = 0: every j <= i.
  *   out       [n_tokens, hq, d] bf16 or f32: softmax(scale q k^T) v over them
  *   lse       [hq, n_tokens] f32: ln sum exp(scale q.k)
  * q and the memory between the pages' first byte and last must not overlap
- * out (INVALID_ARG).
+ * out (INVALID_ARG); lse and d_ws, which are written too, must not overlap
+ * anything else (not looked at).
  * A token that sees nothing (L = 0, or i < 0) gets out = 0, lse = -inf.
  * Cached rows at and behind L, and those that no token of the sequence sees,
  * are never used, whatever they hold.  (A key that some tokens of a sequence
@@ -215,6 +224,7 @@ int attn_cache_copy_pages(void *const *h_pools, int n_pools, size_t page_bytes,
  * Tokens of no sequence are not read; a token whose slot, position or page is
  * out of range is not written (INVALID_ARG on the device).  Where `seqs` names a
  * row twice, both write its last positions, which then hold either's tokens.
+ * k_new and v_new must not lie where the call writes (not looked at).
  * UNSUPPORTED also: pages with a stride of zero, n_tokens > ATTN_PAGED_MAX_LEN. */
 int attn_cache_write(const attn_pages_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr,
                      const void *k_new, const void *v_new, int n_tokens, int64_t new_token_stride,

@@ -22,7 +22,7 @@ ATTN_DTYPE_BF16, ATTN_DTYPE_F32 = 0, 1
 ATTN_FWD_TILE_Q, ATTN_FWD_TILE_K = 256, 128
 ATTN_MERGE_MAX_PARTS = 16
 
-# every entry point declared in include/attn_slice.h and include/attn_paged.h
+# every entry point declared in include/*.h
 EXPORTS = ["attn_tiles_workspace_bytes", "attn_build_tiles", "attn_build_tiles_noalloc",
            "attn_tiles_totals",
            "attn_slices_from_block_grid", "attn_fwd", "attn_merge", "attn_bwd_workspace_bytes",
@@ -31,7 +31,9 @@ EXPORTS = ["attn_tiles_workspace_bytes", "attn_build_tiles", "attn_build_tiles_n
            "attn_strerror",
            "attn_paged_workspace_bytes", "attn_paged_fwd", "attn_prefix_fwd", "attn_slices_from_windows",
            "attn_cache_extend", "attn_cache_free", "attn_cache_trim", "attn_cache_workspace_bytes", "attn_cache_fork",
-           "attn_cache_compact", "attn_cache_copy_pages", "attn_cache_write"]
+           "attn_cache_compact", "attn_cache_copy_pages", "attn_cache_write", "attn_cache_read",
+           "attn_paged8_fwd", "attn_prefix8_fwd", "attn_cache8_write", "attn_cache8_read",
+           "attn_beam_workspace_bytes", "attn_beam_select", "attn_beam_reorder"]
 
 
 class AttnSlice(ctypes.Structure):
@@ -89,8 +91,9 @@ def load(path: Optional[str] = None):
     lib.attn_selftest_wait_timeout.argtypes = [vp]
     lib.attn_strerror.argtypes = [i32]
     lib.attn_strerror.restype = ctypes.c_char_p
-    from . import paging
+    from . import beam, paging
     paging._declare(lib)
+    beam._declare(lib)
     for name in EXPORTS:
         if name != "attn_strerror":
             getattr(lib, name).restype = ctypes.c_int

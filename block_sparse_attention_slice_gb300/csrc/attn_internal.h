@@ -72,13 +72,15 @@ int merge_launch(const void *const *o_parts, const float *const *lse_parts, int 
                  int part_dtype, int s_len, int h, int d, void *out, int out_dtype, float *lse,
                  cudaStream_t s);
 
-// Attention over a paged cache (paged_api.cu, paged_rows.cu, paged_tiles.cu) and its pages
-// (cache_pages.cu).
+// Attention over a paged cache (paged_api.cu, paged_rows.cu, paged_rows8.cu, paged_tiles.cu)
+// and its pages (cache_pages.cu, cache_codes.cu).
 int paged_check_pages(const attn_pages_t *g, int *shift);
+int paged_check_pages8(const attn_pages8_t *g, int *shift);
 int paged_check_seqs(const attn_seqs_t *s, int page_size);
 struct PagedParams;
 size_t paged_rows_workspace(int d);
 int paged_rows_launch(PagedParams &p, int d, cudaStream_t s);
+int paged_rows8_launch(PagedParams &p, int d, cudaStream_t s);
 size_t paged_tiles_workspace(int d);
 int paged_tiles_heads(int sms, int hk);
 int paged_tiles_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows);

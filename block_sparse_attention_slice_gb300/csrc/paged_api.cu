@@ -75,9 +75,10 @@ namespace {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 int check_call(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq, const attn_pages_t *pages,
-               const attn_seqs_t *seqs, float scale, const void *out, int out_dtype, const float *lse, int *shift) {
+               const attn_pages8_t *pages8, const attn_seqs_t *seqs, float scale, const void *out, int out_dtype, const float *lse,
+               int *shift) {
   if (n_tokens < 0 || hq < 1 || max_q < 1) return ATTN_ERR_INVALID_ARG;
-  int rc = paged_check_pages(pages, shift);
+  int rc = pages8 ? paged_check_pages8(pages8, shift) : paged_check_pages(pages, shift);
   if (rc != ATTN_OK) return rc;
   if ((rc = paged_check_seqs(seqs, pages->page_size)) != ATTN_OK) return rc;
   if (hq % pages->hk != 0) return ATTN_ERR_INVALID_ARG;
@@ -91,24 +92,39 @@ int check_call(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int
   return ATTN_OK;
 }
 
-// Whether q or the memory that the pages span meets out, which is written while
-// they are read.
-bool meets_out(const void *q, int n_tokens, int hq, const attn_pages_t *g, const void *out, int out_dtype) {
+// Whether q or the memory that the pages span (and, in 8 bits, their scales) meets
+// out, which is written while they are read.
+bool meets_out(const void *q, int n_tokens, int hq, const attn_pages_t *g, const attn_pages8_t *g8, const void *out, int out_dtype) {
   const size_t n = static_cast<size_t>(n_tokens) * hq * g->d;
   const char *ob = static_cast<const char *>(out), *oe = ob + n * (out_dtype == ATTN_DTYPE_F32 ? 4 : 2);
-  const size_t span = 2 * (static_cast<size_t>(g->n_pages - 1) * g->page_stride + static_cast<size_t>(g->page_size - 1) * g->token_stride +
-                           static_cast<size_t>(g->hk - 1) * g->head_stride + g->d);
+  auto last = [&](int64_t page, int64_t token, int64_t head) {
+    return static_cast<size_t>(g->n_pages - 1) * page + static_cast<size_t>(g->page_size - 1) * token + static_cast<size_t>(g->hk - 1) * head;
+  };
+  const size_t span = (g8 ? 1 : 2) * (last(g->page_stride, g->token_stride, g->head_stride) + g->d);
   auto meets = [&](const void *x, size_t bytes) {
     const char *b = static_cast<const char *>(x);
     return b < oe && ob < b + bytes;
   };
+  if (g8) {
+    const size_t scales = 4 * (last(g8->scale_page_stride, g8->scale_token_stride, g8->scale_head_stride) + 1);
+    if (meets(g8->k_scales, scales) || meets(g8->v_scales, scales)) return true;
+  }
   return meets(q, 2 * n) || meets(g->k, span) || meets(g->v, span);
 }
 
-PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, const attn_pages_t *g,
+PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, const attn_pages_t *g, const attn_pages8_t *g8,
                    const attn_seqs_t *s, float scale, int shift) {
   PagedParams p;
   std::memset(&p, 0, sizeof(p));
+  if (g8) {
+    p.bits8 = 1;
+    p.format = g8->format;
+    p.k_scales = g8->k_scales;
+    p.v_scales = g8->v_scales;
+    p.scale_page = g8->scale_page_stride;
+    p.scale_token = g8->scale_token_stride;
+    p.scale_head = g8->scale_head_stride;
+  }
   p.q = q;
   p.k = g->k;
   p.v = g->v;
@@ -139,13 +155,13 @@ PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, co
 // the warp-level kernel, larger ones to the tensor-core tiles.  What the kernel
 // chose is left in p and, the rows of a piece, in `tile_rows`.
 int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
-  if (static_cast<int64_t>(tokens) * p.G > 16) {
+  if (!p.bits8 && static_cast<int64_t>(tokens) * p.G > 16) {
     const int rc = paged_tiles_launch(p, d, tokens, s, tile_rows);
     if (rc != ATTN_ERR_UNSUPPORTED) return rc;
   }
   if (p.share.side == 1) p.share.side = 0;     // two passes share the SMs only where tiles are the first
   *tile_rows = 16;
-  return paged_rows_launch(p, d, s);
+  return p.bits8 ? paged_rows8_launch(p, d, s) : paged_rows_launch(p, d, s);
 }
 
 // The prefix's tiles are bound by their products, what follows it by the cache's
@@ -213,21 +229,21 @@ int attn_paged_workspace_bytes(int n_tokens, int hq, int d, int prefix, size_t *
   return ATTN_OK;
 }
 
-int attn_paged_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
-                   const attn_pages_t *pages, const attn_seqs_t *seqs, float scale, int window, int sinks,
-                   void *out, int out_dtype, float *lse, void *d_ws, size_t ws_bytes, attn_stream_t stream) {
+static int paged_call(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq, const attn_pages_t *pages,
+                      const attn_pages8_t *pages8, const attn_seqs_t *seqs, float scale, int window, int sinks, void *out,
+                      int out_dtype, float *lse, void *d_ws, size_t ws_bytes, attn_stream_t stream) {
   if (window < 0 || sinks < 0) return ATTN_ERR_INVALID_ARG;
   int shift = 0;
-  int rc = check_call(q, q_ptr, n_tokens, max_q, hq, pages, seqs, scale, out, out_dtype, lse, &shift);
+  int rc = check_call(q, q_ptr, n_tokens, max_q, hq, pages, pages8, seqs, scale, out, out_dtype, lse, &shift);
   if (rc != ATTN_OK) return rc;
   if (n_tokens == 0 || seqs->n_seqs == 0) return ATTN_OK;
   if (!d_ws) return ATTN_ERR_INVALID_ARG;
   if (!al16(d_ws)) return ATTN_ERR_UNSUPPORTED;
-  if (meets_out(q, n_tokens, hq, pages, out, out_dtype)) return ATTN_ERR_INVALID_ARG;
+  if (meets_out(q, n_tokens, hq, pages, pages8, out, out_dtype)) return ATTN_ERR_INVALID_ARG;
   size_t need = 0;
   if ((rc = attn_paged_workspace_bytes(n_tokens, hq, pages->d, 0, &need)) != ATTN_OK) return rc;
   if (ws_bytes < need) return ATTN_ERR_CAPACITY;
-  PagedParams p = params(q, q_ptr, n_tokens, hq, pages, seqs, scale, shift);
+  PagedParams p = params(q, q_ptr, n_tokens, hq, pages, pages8, seqs, scale, shift);
   // no sequence is longer than ATTN_PAGED_MAX_LEN: larger values say the same
   p.window = std::min(window, ATTN_PAGED_MAX_LEN);
   p.sinks = std::min(sinks, ATTN_PAGED_MAX_LEN);
@@ -241,19 +257,18 @@ int attn_paged_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q,
   return paged_launch(p, pages->d, std::min(max_q, n_tokens), reinterpret_cast<cudaStream_t>(stream), &tile_rows);
 }
 
-int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
-                    const attn_pages_t *pages, const attn_seqs_t *prefix, const int32_t *group_ptr,
-                    const attn_seqs_t *seqs, float scale, void *out, int out_dtype, float *lse, void *d_ws,
-                    size_t ws_bytes, attn_stream_t stream) {
+static int prefix_call(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq, const attn_pages_t *pages,
+                       const attn_pages8_t *pages8, const attn_seqs_t *prefix, const int32_t *group_ptr, const attn_seqs_t *seqs,
+                       float scale, void *out, int out_dtype, float *lse, void *d_ws, size_t ws_bytes, attn_stream_t stream) {
   int shift = 0;
-  int rc = check_call(q, q_ptr, n_tokens, max_q, hq, pages, seqs, scale, out, out_dtype, lse, &shift);
+  int rc = check_call(q, q_ptr, n_tokens, max_q, hq, pages, pages8, seqs, scale, out, out_dtype, lse, &shift);
   if (rc != ATTN_OK) return rc;
   if ((rc = paged_check_seqs(prefix, pages->page_size)) != ATTN_OK) return rc;
   if (prefix->n_seqs > 0 && !group_ptr) return ATTN_ERR_INVALID_ARG;
   if (n_tokens == 0 || seqs->n_seqs == 0) return ATTN_OK;
   if (!d_ws) return ATTN_ERR_INVALID_ARG;
   if (!al16(d_ws)) return ATTN_ERR_UNSUPPORTED;
-  if (meets_out(q, n_tokens, hq, pages, out, out_dtype)) return ATTN_ERR_INVALID_ARG;
+  if (meets_out(q, n_tokens, hq, pages, pages8, out, out_dtype)) return ATTN_ERR_INVALID_ARG;
   size_t need = 0;
   if ((rc = attn_paged_workspace_bytes(n_tokens, hq, pages->d, 1, &need)) != ATTN_OK) return rc;
   if (ws_bytes < need) return ATTN_ERR_CAPACITY;
@@ -263,7 +278,7 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
   uint8_t *ws = static_cast<uint8_t *>(d_ws);
   int tile_rows;
   // what follows the prefix
-  PagedParams r = params(q, q_ptr, n_tokens, hq, pages, seqs, scale, shift);
+  PagedParams r = params(q, q_ptr, n_tokens, hq, pages, pages8, seqs, scale, shift);
   r.out = out;
   r.lse = lse;
   r.out_f32 = out_dtype == ATTN_DTYPE_F32;
@@ -274,7 +289,7 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
     return paged_launch(r, pages->d, tokens, s, &tile_rows);
   }
   // the prefixes: rows of a whole group against its keys, none of them masked
-  PagedParams p = params(q, q_ptr, n_tokens, hq, pages, prefix, scale, shift);
+  PagedParams p = params(q, q_ptr, n_tokens, hq, pages, pages8, prefix, scale, shift);
   p.group_ptr = group_ptr;
   p.n_members = seqs->n_seqs;
   p.causal = 0;
@@ -305,6 +320,34 @@ int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n_tokens) * hq + 15) / 16));
   auto join = pages->d == 128 ? paged_join_pair_kernel<128> : paged_join_pair_kernel<64>;
   return launch_after(join, grid, 256, 0, s, p, r, pre_rows, tile_rows);
+}
+
+int attn_paged_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
+                   const attn_pages_t *pages, const attn_seqs_t *seqs, float scale, int window, int sinks,
+                   void *out, int out_dtype, float *lse, void *d_ws, size_t ws_bytes, attn_stream_t stream) {
+  return paged_call(q, q_ptr, n_tokens, max_q, hq, pages, nullptr, seqs, scale, window, sinks, out, out_dtype, lse, d_ws, ws_bytes, stream);
+}
+
+int attn_paged8_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
+                    const attn_pages8_t *pages, const attn_seqs_t *seqs, float scale, int window, int sinks,
+                    void *out, int out_dtype, float *lse, void *d_ws, size_t ws_bytes, attn_stream_t stream) {
+  if (!pages) return ATTN_ERR_INVALID_ARG;
+  return paged_call(q, q_ptr, n_tokens, max_q, hq, &pages->pages, pages, seqs, scale, window, sinks, out, out_dtype, lse, d_ws, ws_bytes, stream);
+}
+
+int attn_prefix_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
+                    const attn_pages_t *pages, const attn_seqs_t *prefix, const int32_t *group_ptr,
+                    const attn_seqs_t *seqs, float scale, void *out, int out_dtype, float *lse, void *d_ws,
+                    size_t ws_bytes, attn_stream_t stream) {
+  return prefix_call(q, q_ptr, n_tokens, max_q, hq, pages, nullptr, prefix, group_ptr, seqs, scale, out, out_dtype, lse, d_ws, ws_bytes, stream);
+}
+
+int attn_prefix8_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
+                     const attn_pages8_t *pages, const attn_seqs_t *prefix, const int32_t *group_ptr,
+                     const attn_seqs_t *seqs, float scale, void *out, int out_dtype, float *lse, void *d_ws,
+                     size_t ws_bytes, attn_stream_t stream) {
+  if (!pages) return ATTN_ERR_INVALID_ARG;
+  return prefix_call(q, q_ptr, n_tokens, max_q, hq, &pages->pages, pages, prefix, group_ptr, seqs, scale, out, out_dtype, lse, d_ws, ws_bytes, stream);
 }
 
 int attn_slices_from_windows(const int32_t *h_lengths, int n, int window, int sinks, attn_slice_t *h_out,

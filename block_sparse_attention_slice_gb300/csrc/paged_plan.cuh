@@ -81,6 +81,10 @@ struct PagedParams {
   int hp, n_spans;            // heads side by side; spans
   Share share;
   int test_stall;             // failure-path test: leave one load out
+  // pages in 8 bits: strides above are bytes too, codes have scales
+  const float *k_scales, *v_scales;
+  long long scale_page, scale_token, scale_head;      // elements
+  int bits8, format;          // bits8 = 0: bf16, no scales; format: ATTN_CODES_*
   unsigned int *status;
   unsigned long long wait_ns;
 };

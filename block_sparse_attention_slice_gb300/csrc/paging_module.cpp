@@ -1,5 +1,5 @@
-// The marshalling of paging.py in C++: checks tensors, allocates outputs and
-// workspaces, and calls the C ABI of include/attn_paged.h on the tensors'
+// The marshalling of paging.py and beam.py in C++: checks tensors, allocates outputs
+// and workspaces, and calls the C ABI of include/attn_paged.h and attn_beam.h on the tensors'
 // device and the given or current stream.  A call of the paged attention runs
 // for 10 us on the GPU at its smallest; the same marshalling in Python took 25.
 // Nothing is kept from one call to the next.
@@ -15,6 +15,7 @@
 #include <string>
 #include <vector>
 
+#include "../../include/attn_beam.h"
 #include "../../include/attn_paged.h"
 
 namespace {
@@ -55,13 +56,36 @@ const int32_t *ints(const Tensor *t, const char *name, at::Device device) {
   return static_cast<const int32_t *>(t->data_ptr());
 }
 
-attn_pages_t pages_of(PyObject *ko, PyObject *vo) {
+// Pages of either kind: with scales they hold 8 bits a value.
+struct PagesArg {
+  attn_pages8_t p8;
+  bool is8;
+  const attn_pages_t &pages() const { return p8.pages; }
+};
+PagesArg pages_of(PyObject *ko, PyObject *vo, PyObject *kso, PyObject *vso) {
   const Tensor &k = tensor(ko, "k_pages"), &v = tensor(vo, "v_pages");
+  const Tensor *ks = maybe(kso, "k_scales"), *vs = maybe(vso, "v_scales");
   if (k.dim() != 4 || k.sizes() != v.sizes() || k.strides() != v.strides() || k.stride(3) != 1)
     refuse("k_pages and v_pages must be [n_pages, page_size, H_k, d], alike in strides, d contiguous");
-  if (k.scalar_type() != at::kBFloat16 || v.scalar_type() != at::kBFloat16 || !k.is_cuda() || v.device() != k.device())
-    refuse("k_pages and v_pages must be bf16 tensors on one CUDA device");
-  attn_pages_t p;
+  PagesArg a;
+  a.is8 = ks || vs;
+  const at::ScalarType want = a.is8 && k.scalar_type() == at::kChar ? at::kChar : a.is8 ? at::kFloat8_e4m3fn : at::kBFloat16;
+  if (k.scalar_type() != want || v.scalar_type() != want || !k.is_cuda() || v.device() != k.device())
+    refuse("k_pages and v_pages must be bf16 tensors, or int8 or float8_e4m3fn ones with k_scales and v_scales, on one CUDA device");
+  if (a.is8) {
+    if (!ks || !vs) refuse("k_scales and v_scales must be given together");
+    if (ks->dim() != 3 || ks->sizes() != k.sizes().slice(0, 3) || vs->sizes() != ks->sizes() || vs->strides() != ks->strides() ||
+        ks->scalar_type() != at::kFloat || vs->scalar_type() != at::kFloat || ks->device() != k.device() || vs->device() != k.device())
+      refuse("k_scales and v_scales must be f32 [n_pages, page_size, H_k] on the pages' device, alike in strides");
+    a.p8.k_scales = static_cast<const float *>(ks->data_ptr());
+    a.p8.v_scales = static_cast<const float *>(vs->data_ptr());
+    a.p8.scale_page_stride = ks->stride(0);
+    a.p8.scale_token_stride = ks->stride(1);
+    a.p8.scale_head_stride = ks->stride(2);
+    a.p8.format = want == at::kChar ? ATTN_CODES_INT8 : ATTN_CODES_E4M3;
+    a.p8.reserved = 0;
+  }
+  attn_pages_t &p = a.p8.pages;
   p.k = k.data_ptr();
   p.v = v.data_ptr();
   p.n_pages = narrow(k.size(0), "n_pages");
@@ -71,7 +95,7 @@ attn_pages_t pages_of(PyObject *ko, PyObject *vo) {
   p.page_stride = k.stride(0);
   p.token_stride = k.stride(1);
   p.head_stride = k.stride(2);
-  return p;
+  return a;
 }
 
 void check_rows(const Tensor &table, const Tensor &lens, at::Device device, const char *what) {
@@ -232,24 +256,32 @@ struct Attend {
   }
 };
 
-// q, k_pages, v_pages, table, seq_lens, scale, q_ptr, max_q, window, sinks, seqs, out, lse, out_dtype, ws, stream
+// q, k_pages, v_pages, table, seq_lens, scale, q_ptr, max_q, window, sinks, seqs, out, lse, out_dtype, ws, stream, k_scales, v_scales
 PyObject *paged_fwd(PyObject *const *a) {
-  const attn_pages_t pages = pages_of(a[1], a[2]);
+  const PagesArg of = pages_of(a[1], a[2], a[16], a[17]);
+  const attn_pages_t &pages = of.pages();
   const at::Device device = THPVariable_Unpack(a[1]).device();
   const attn_seqs_t seqs = seqs_of(a[3], a[4], maybe(a[10], "seqs"), device, "");
   const int window = integer(a[8], "window"), sinks = integer(a[9], "sinks");
   Attend x(device, pages, seqs.n_seqs, a[0], a[5], a[6], a[7], a[11], a[12], a[13], a[14], 0);
   attn_stream_t s = stream_of(a[15], device);
-  call("attn_paged_fwd", device, [&] {
+  if (of.is8)
+    call("attn_paged8_fwd", device, [&] {
+      return attn_paged8_fwd(x.q->data_ptr(), x.q_ptr, x.t, x.max_q, x.hq, &of.p8, &seqs, x.scale, window, sinks, x.out.data_ptr(),
+                             x.out_dtype, static_cast<float *>(x.lse.data_ptr()), x.ws.data_ptr(), x.ws_bytes(), s);
+    });
+  else call("attn_paged_fwd", device, [&] {
     return attn_paged_fwd(x.q->data_ptr(), x.q_ptr, x.t, x.max_q, x.hq, &pages, &seqs, x.scale, window, sinks, x.out.data_ptr(),
                           x.out_dtype, static_cast<float *>(x.lse.data_ptr()), x.ws.data_ptr(), x.ws_bytes(), s);
   });
   return x.result();
 }
 
-// q, k_pages, v_pages, prefix_table, prefix_lens, group_ptr, table, seq_lens, scale, q_ptr, max_q, seqs, out, lse, out_dtype, ws, stream
+// q, k_pages, v_pages, prefix_table, prefix_lens, group_ptr, table, seq_lens, scale, q_ptr, max_q, seqs, out, lse, out_dtype, ws, stream,
+// k_scales, v_scales
 PyObject *prefix_fwd(PyObject *const *a) {
-  const attn_pages_t pages = pages_of(a[1], a[2]);
+  const PagesArg of = pages_of(a[1], a[2], a[17], a[18]);
+  const attn_pages_t &pages = of.pages();
   const at::Device device = THPVariable_Unpack(a[1]).device();
   const attn_seqs_t pre = seqs_of(a[3], a[4], nullptr, device, "prefix_");
   const attn_seqs_t seqs = seqs_of(a[6], a[7], maybe(a[11], "seqs"), device, "");
@@ -258,7 +290,12 @@ PyObject *prefix_fwd(PyObject *const *a) {
   if (group.size(0) != static_cast<int64_t>(pre.n_seqs) + 1) refuse("group_ptr must have one entry a prefix and one more");
   Attend x(device, pages, seqs.n_seqs, a[0], a[8], a[9], a[10], a[12], a[13], a[14], a[15], 1);
   attn_stream_t s = stream_of(a[16], device);
-  call("attn_prefix_fwd", device, [&] {
+  if (of.is8)
+    call("attn_prefix8_fwd", device, [&] {
+      return attn_prefix8_fwd(x.q->data_ptr(), x.q_ptr, x.t, x.max_q, x.hq, &of.p8, &pre, group_ptr, &seqs, x.scale, x.out.data_ptr(),
+                              x.out_dtype, static_cast<float *>(x.lse.data_ptr()), x.ws.data_ptr(), x.ws_bytes(), s);
+    });
+  else call("attn_prefix_fwd", device, [&] {
     return attn_prefix_fwd(x.q->data_ptr(), x.q_ptr, x.t, x.max_q, x.hq, &pages, &pre, group_ptr, &seqs, x.scale, x.out.data_ptr(),
                            x.out_dtype, static_cast<float *>(x.lse.data_ptr()), x.ws.data_ptr(), x.ws_bytes(), s);
   });
@@ -380,9 +417,10 @@ PyObject *cache_copy_pages(PyObject *const *a) {
   Py_RETURN_NONE;
 }
 
-// k_pages, v_pages, k_new, v_new, table, seq_lens, q_ptr, seqs, stream
+// k_pages, v_pages, k_new, v_new, table, seq_lens, q_ptr, seqs, stream, k_scales, v_scales
 PyObject *cache_write(PyObject *const *a) {
-  const attn_pages_t pages = pages_of(a[0], a[1]);
+  const PagesArg of = pages_of(a[0], a[1], a[9], a[10]);
+  const attn_pages_t &pages = of.pages();
   const at::Device device = THPVariable_Unpack(a[0]).device();
   const attn_seqs_t seqs = seqs_of(a[4], a[5], maybe(a[7], "seqs"), device, "");
   const Tensor *ptr = maybe(a[6], "q_ptr");
@@ -395,8 +433,140 @@ PyObject *cache_write(PyObject *const *a) {
     refuse("k_new and v_new must be bf16 [n_tokens, H_k, d] on the pages' device, alike in strides, d contiguous");
   const int t = narrow(k.size(0), "n_tokens");
   attn_stream_t st = stream_of(a[8], device);
-  call("attn_cache_write", device,
-       [&] { return attn_cache_write(&pages, &seqs, q_ptr, k.data_ptr(), v.data_ptr(), t, k.stride(0), k.stride(1), st); });
+  if (of.is8)
+    call("attn_cache8_write", device,
+         [&] { return attn_cache8_write(&of.p8, &seqs, q_ptr, k.data_ptr(), v.data_ptr(), t, k.stride(0), k.stride(1), st); });
+  else
+    call("attn_cache_write", device,
+         [&] { return attn_cache_write(&pages, &seqs, q_ptr, k.data_ptr(), v.data_ptr(), t, k.stride(0), k.stride(1), st); });
+  Py_RETURN_NONE;
+}
+
+// k_pages, v_pages, table, seq_lens, n_tokens, q_ptr, seqs, k_out, v_out, out_dtype, stream, k_scales, v_scales
+PyObject *cache_read(PyObject *const *a) {
+  const PagesArg of = pages_of(a[0], a[1], a[11], a[12]);
+  const attn_pages_t &pages = of.pages();
+  const at::Device device = THPVariable_Unpack(a[0]).device();
+  const attn_seqs_t seqs = seqs_of(a[2], a[3], maybe(a[6], "seqs"), device, "");
+  const int t = integer(a[4], "n_tokens");
+  if (t < 0) refuse("n_tokens must not be negative");
+  const Tensor *ptr = maybe(a[5], "q_ptr");
+  const int32_t *q_ptr = ints(ptr, "q_ptr", device);
+  if (ptr && ptr->size(0) != static_cast<int64_t>(seqs.n_seqs) + 1) refuse("q_ptr must have one entry a sequence and one more");
+  at::ScalarType want = at::kBFloat16;
+  if (a[9] != Py_None) {
+    if (!THPDtype_Check(a[9])) refuse("out_dtype must be a dtype", PyExc_TypeError);
+    want = reinterpret_cast<THPDtype *>(a[9])->scalar_type;
+  }
+  if ((a[7] == Py_None) != (a[8] == Py_None)) refuse("k_out and v_out must be given together");
+  const std::vector<int64_t> sizes{t, pages.hk, pages.d};
+  Tensor out[2];
+  for (int i = 0; i < 2; ++i) {
+    PyObject *o = a[7 + i];
+    if (o == Py_None) continue;
+    out[i] = tensor(o, i ? "v_out" : "k_out");
+    if (out[i].sizes() != at::IntArrayRef(sizes) || out[i].device() != device || !out[i].is_contiguous() ||
+        (a[9] != Py_None && out[i].scalar_type() != want) || out[i].scalar_type() != out[0].scalar_type())
+      refuse("k_out and v_out must be contiguous bf16 or f32 [n_tokens, H_k, d] tensors, of one type, on the pages' device");
+    if (i == 0) want = out[0].scalar_type();
+  }
+  if (want != at::kBFloat16 && want != at::kFloat) refuse("the rows must be bf16 or f32");
+  if (a[7] == Py_None)
+    for (Tensor &x : out) x = at::empty(sizes, at::TensorOptions().device(device).dtype(want));
+  const int dtype = want == at::kFloat ? ATTN_DTYPE_F32 : ATTN_DTYPE_BF16;
+  attn_stream_t st = stream_of(a[10], device);
+  if (of.is8)
+    call("attn_cache8_read", device,
+         [&] { return attn_cache8_read(&of.p8, &seqs, q_ptr, t, out[0].data_ptr(), out[1].data_ptr(), dtype, st); });
+  else
+    call("attn_cache_read", device,
+         [&] { return attn_cache_read(&pages, &seqs, q_ptr, t, out[0].data_ptr(), out[1].data_ptr(), dtype, st); });
+  PyObject *k = a[7] == Py_None ? THPVariable_Wrap(out[0]) : Py_NewRef(a[7]), *v = a[8] == Py_None ? THPVariable_Wrap(out[1]) : Py_NewRef(a[8]);
+  PyObject *r = k && v ? PyTuple_Pack(2, k, v) : nullptr;
+  Py_XDECREF(k);
+  Py_XDECREF(v);
+  return r;
+}
+
+// logits, scores, done, eos, slots, keep, ws, stream
+PyObject *beam_select(PyObject *const *a) {
+  const Tensor &logits = tensor(a[0], "logits"), &scores = tensor(a[1], "scores");
+  const Tensor *done = maybe(a[2], "done"), *slots = maybe(a[4], "slots");
+  if (!logits.is_cuda() || (logits.scalar_type() != at::kFloat && logits.scalar_type() != at::kBFloat16) || logits.dim() != 2 ||
+      (logits.stride(1) != 1 && logits.size(1) != 1))
+    refuse("logits must be f32 or bf16 [groups * beams, vocab] on a CUDA device, rows contiguous");
+  const at::Device device = logits.device();
+  if (scores.scalar_type() != at::kFloat || scores.dim() != 2 || scores.device() != device || !scores.is_contiguous())
+    refuse("scores must be a contiguous f32 [groups, beams] tensor on " + device.str());
+  const int groups = narrow(scores.size(0), "groups"), beams = narrow(scores.size(1), "beams"), vocab = narrow(logits.size(1), "vocab");
+  if (logits.size(0) != static_cast<int64_t>(groups) * beams) refuse("logits must have one row a beam");
+  if (done && ((done->scalar_type() != at::kBool && done->scalar_type() != at::kByte) || done->sizes() != scores.sizes() || done->device() != device ||
+               !done->is_contiguous()))
+    refuse("done must be a contiguous bool or uint8 tensor like scores");
+  const int32_t *slot = ints(slots, "slots", device);
+  if (slots && slots->size(0) != logits.size(0)) refuse("slots must have one entry a beam");
+  const int eos = integer(a[3], "eos"), keep = a[5] == Py_None ? beams : integer(a[5], "keep");
+  size_t bytes = 0;
+  call("attn_beam_workspace_bytes", device, [&] { return attn_beam_workspace_bytes(groups, beams, vocab, keep, &bytes); });
+  const auto on = at::TensorOptions().device(device);
+  Tensor ws = a[6] == Py_None ? at::empty({static_cast<int64_t>(bytes)}, on.dtype(at::kByte)) : tensor(a[6], "ws");
+  if (ws.device() != device || !ws.is_contiguous()) refuse("ws must be a contiguous tensor on the logits' device");
+  Tensor out[5];
+  const at::ScalarType types[5] = {at::kFloat, at::kInt, at::kInt, at::kBool, at::kInt};
+  const int n = slots ? 5 : 4;
+  for (int i = 0; i < n; ++i) out[i] = at::empty({groups, keep}, on.dtype(types[i]));
+  attn_stream_t st = stream_of(a[7], device);
+  const int64_t stride = logits.size(0) > 1 ? logits.stride(0) : std::max<int64_t>(vocab, logits.stride(0));
+  call("attn_beam_select", device, [&] {
+    return attn_beam_select(logits.data_ptr(), logits.scalar_type() == at::kFloat ? ATTN_DTYPE_F32 : ATTN_DTYPE_BF16, stride, groups, beams, vocab,
+                            static_cast<const float *>(scores.data_ptr()), done ? static_cast<const uint8_t *>(done->data_ptr()) : nullptr, eos, slot,
+                            keep, static_cast<float *>(out[0].data_ptr()), static_cast<int32_t *>(out[1].data_ptr()),
+                            static_cast<int32_t *>(out[2].data_ptr()), static_cast<uint8_t *>(out[3].data_ptr()),
+                            slots ? static_cast<int32_t *>(out[4].data_ptr()) : nullptr, ws.data_ptr(), ws.nbytes(), st);
+  });
+  PyObject *r = PyTuple_New(n);
+  for (int i = 0; r && i < n; ++i) {
+    PyObject *o = THPVariable_Wrap(out[i]);
+    if (!o) Py_CLEAR(r);
+    else PyTuple_SET_ITEM(r, i, o);
+  }
+  return r;
+}
+
+// states, parents, stream
+PyObject *beam_reorder(PyObject *const *a) {
+  const Tensor &parents = tensor(a[1], "parents");
+  if (parents.scalar_type() != at::kInt || parents.dim() != 2 || !parents.is_cuda() || !parents.is_contiguous())
+    refuse("parents must be a contiguous int32 [groups, beams] CUDA tensor");
+  const at::Device device = parents.device();
+  PyObject *seq = PySequence_Fast(a[0], "states must be a sequence of tensors");
+  if (!seq) throw Raised();
+  struct Drop {
+    PyObject *o;
+    ~Drop() { Py_DECREF(o); }
+  } drop{seq};
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+  std::vector<void *> at;
+  std::vector<int64_t> bytes, strides;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    const Tensor &x = tensor(PySequence_Fast_GET_ITEM(seq, i), "a state");
+    bool whole = x.device() == device && x.dim() >= 1 && x.size(0) == parents.numel();
+    int64_t run = 1;
+    for (int64_t k = x.dim() - 1; whole && k >= 1; --k) {
+      if (x.size(k) != 1 && x.stride(k) != run) whole = false;
+      run *= x.size(k);
+    }
+    if (!whole) refuse("states must be [groups * beams, ...] on " + device.str() + ", each row contiguous");
+    at.push_back(x.data_ptr());
+    bytes.push_back(run * static_cast<int64_t>(x.element_size()));
+    strides.push_back(x.size(0) > 1 ? x.stride(0) * static_cast<int64_t>(x.element_size()) : bytes.back());
+  }
+  const int groups = narrow(parents.size(0), "groups"), beams = narrow(parents.size(1), "beams");
+  attn_stream_t st = stream_of(a[2], device);
+  call("attn_beam_reorder", device, [&] {
+    return attn_beam_reorder(at.data(), bytes.data(), strides.data(), static_cast<int>(n > INT_MAX ? INT_MAX : n),
+                             static_cast<const int32_t *>(parents.data_ptr()), groups, beams, st);
+  });
   Py_RETURN_NONE;
 }
 
@@ -406,9 +576,9 @@ PyObject *set_error(PyObject *, PyObject *cls) {
 }
 
 #define ENTRY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<n, name>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(paged_fwd, 16),  ENTRY(prefix_fwd, 17),   ENTRY(cache_extend, 7),     ENTRY(cache_free, 6),
-                         ENTRY(cache_trim, 8),  ENTRY(cache_fork, 9),    ENTRY(cache_compact, 7),    ENTRY(cache_copy_pages, 3),
-                         ENTRY(cache_write, 9), {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {ENTRY(paged_fwd, 18),   ENTRY(prefix_fwd, 19), ENTRY(cache_extend, 7), ENTRY(cache_free, 6),        ENTRY(cache_trim, 8),
+                         ENTRY(cache_fork, 9),   ENTRY(cache_compact, 7), ENTRY(cache_copy_pages, 3), ENTRY(cache_write, 11), ENTRY(cache_read, 13),
+                         ENTRY(beam_select, 8),  ENTRY(beam_reorder, 3), {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paging", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

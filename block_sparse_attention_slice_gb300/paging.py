@@ -69,10 +69,13 @@ def _made(q, out, lse, out_dtype, ws, d, prefix, stream):
 
 
 def attn_paged_fwd(q, k_pages, v_pages, table, seq_lens, scale: float, q_ptr=None, max_q=None, window: int = 0,
-                   sinks: int = 0, seqs=None, out=None, lse=None, out_dtype=None, ws=None, stream=None):
+                   sinks: int = 0, seqs=None, out=None, lse=None, out_dtype=None, ws=None, stream=None, k_scales=None,
+                   v_scales=None):
     """O, lse of each sequence's newest tokens over its cached keys.
 
-    q [n_tokens,H,d] bf16; k_pages/v_pages [n_pages,page_size,H_k,d] bf16;
+    q [n_tokens,H,d] bf16; k_pages/v_pages [n_pages,page_size,H_k,d] bf16, or
+    int8 or float8_e4m3fn with k_scales/v_scales [n_pages,page_size,H_k] f32
+    (a value is code * scale);
     table int32 [n_slots,max_pages]; seq_lens int32 [n_slots] (the new tokens,
     whose keys are cached already, included); q_ptr int32 [n_seqs+1] (None:
     one token a sequence); seqs int32 [n_seqs] table rows (None: all, in
@@ -84,20 +87,21 @@ def attn_paged_fwd(q, k_pages, v_pages, table, seq_lens, scale: float, q_ptr=Non
     if stream is not None:
         out, lse, ws, stream = _made(q, out, lse, out_dtype, ws, k_pages.shape[-1], 0, stream)
     return (_module or _m()).paged_fwd(q, k_pages, v_pages, table, seq_lens, scale, q_ptr, max_q, window, sinks, seqs, out, lse,
-                                       out_dtype, ws, stream)
+                                       out_dtype, ws, stream, k_scales, v_scales)
 
 
 def attn_prefix_fwd(q, k_pages, v_pages, prefix_table, prefix_lens, group_ptr, table, seq_lens, scale: float,
-                    q_ptr=None, max_q=None, seqs=None, out=None, lse=None, out_dtype=None, ws=None, stream=None):
+                    q_ptr=None, max_q=None, seqs=None, out=None, lse=None, out_dtype=None, ws=None, stream=None, k_scales=None,
+                    v_scales=None):
     """O, lse of sequences whose groups share a prefix that is read once.
 
     Sequences group_ptr[g] .. group_ptr[g+1] see the prefix of row g of
     prefix_table / prefix_lens, then their own keys as in ``attn_paged_fwd``
-    (seq_lens counts the tokens behind the prefix)."""
+    (seq_lens counts the tokens behind the prefix); pages and scales as there."""
     if stream is not None:
         out, lse, ws, stream = _made(q, out, lse, out_dtype, ws, k_pages.shape[-1], 1, stream)
     return (_module or _m()).prefix_fwd(q, k_pages, v_pages, prefix_table, prefix_lens, group_ptr, table, seq_lens, scale, q_ptr,
-                                        max_q, seqs, out, lse, out_dtype, ws, stream)
+                                        max_q, seqs, out, lse, out_dtype, ws, stream, k_scales, v_scales)
 
 
 def attn_cache_extend(table, seq_lens, refs, seqs, counts, page_size: int, stream=None):
@@ -152,11 +156,35 @@ def attn_cache_copy_pages(pools, copies, stream=None):
     (_module or _m()).cache_copy_pages(pools, copies, stream and stream.cuda_stream)
 
 
-def attn_cache_write(k_pages, v_pages, k_new, v_new, table, seq_lens, q_ptr=None, seqs=None, stream=None):
+def attn_cache_write(k_pages, v_pages, k_new, v_new, table, seq_lens, q_ptr=None, seqs=None, stream=None, k_scales=None,
+                     v_scales=None):
     """Writes the newest tokens' keys and values ([n_tokens,H_k,d] bf16, d
     contiguous) to the ends of their sequences (q_ptr, seqs as in
-    ``attn_paged_fwd``; seq_lens counts them already)."""
-    (_module or _m()).cache_write(k_pages, v_pages, k_new, v_new, table, seq_lens, q_ptr, seqs, stream and stream.cuda_stream)
+    ``attn_paged_fwd``; seq_lens counts them already).
+
+    Pages in 8 bits (int8 or float8_e4m3fn, with k_scales/v_scales) get codes:
+    of each token's head the largest magnitude a has the largest code M (127 or
+    448), its scale is a / M and a value the code nearest to x M / a."""
+    (_module or _m()).cache_write(k_pages, v_pages, k_new, v_new, table, seq_lens, q_ptr, seqs, stream and stream.cuda_stream,
+                                  k_scales, v_scales)
+
+
+def attn_cache_read(k_pages, v_pages, table, seq_lens, n_tokens: int, q_ptr=None, seqs=None, k_out=None, v_out=None,
+                    out_dtype=None, stream=None, k_scales=None, v_scales=None):
+    """Keys and values [n_tokens,H_k,d] (bf16, or f32 by out_dtype) of the
+    places that ``attn_cache_write`` fills: the last q_ptr[b+1] - q_ptr[b]
+    tokens of each sequence, all of them where that is its length.  n_tokens is
+    the outputs' rows; rows of no sequence are left as they were.  Pages of
+    either kind; code * scale is rounded once."""
+    if stream is not None and k_out is None and v_out is None:
+        import torch
+        shape = (n_tokens, *k_pages.shape[2:])
+        k_out, v_out = (torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=k_pages.device) for _ in range(2))
+        stream = _on(stream, k_out, v_out)
+    elif stream is not None:
+        stream = stream.cuda_stream
+    return (_module or _m()).cache_read(k_pages, v_pages, table, seq_lens, n_tokens, q_ptr, seqs, k_out, v_out, out_dtype, stream,
+                                        k_scales, v_scales)
 
 
 def _int32(x, name):
@@ -194,4 +222,8 @@ def _declare(lib):
     lib.attn_cache_compact.argtypes = [vp, vp, i32, vp, sz, vp]
     lib.attn_cache_copy_pages.argtypes = [vp, i32, sz, sz, i32, vp, i32, vp]
     lib.attn_cache_write.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, vp]
+    lib.attn_cache_read.argtypes = lib.attn_cache8_read.argtypes = [vp, vp, vp, i32, vp, vp, i32, vp]
+    lib.attn_paged8_fwd.argtypes = lib.attn_paged_fwd.argtypes
+    lib.attn_prefix8_fwd.argtypes = lib.attn_prefix_fwd.argtypes
+    lib.attn_cache8_write.argtypes = lib.attn_cache_write.argtypes
     lib.attn_slices_from_windows.argtypes = [vp, i32, i32, i32, vp, i32, ctypes.POINTER(ctypes.c_int)]

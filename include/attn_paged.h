@@ -7,8 +7,10 @@
  *                       read once for the whole group
  *   attn_slices_from_windows  the windowed mask as a slice list, for attn_fwd
  *                       and attn_bwd over packed sequences
- *   attn_cache_*        pages of the cache: grow, write, fork, free, trim,
- *                       compact, copy
+ *   attn_cache_*        pages of the cache: grow, write, read, fork, free,
+ *                       trim, compact, copy
+ *   attn_paged8_fwd, attn_prefix8_fwd, attn_cache8_write, attn_cache8_read
+ *                       the same over pages that hold 8 bits a value
  *
  * Conventions are those of attn_slice.h: the caller owns every buffer, calls
  * are enqueued on `stream` of the current device and return ATTN_OK or an
@@ -229,6 +231,59 @@ int attn_cache_copy_pages(void *const *h_pools, int n_pools, size_t page_bytes,
 int attn_cache_write(const attn_pages_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr,
                      const void *k_new, const void *v_new, int n_tokens, int64_t new_token_stride,
                      int64_t new_head_stride, attn_stream_t stream);
+
+/* Reads cached keys and values back as rows: token t of sequence b (q_ptr and
+ * seqs as above, n = q_ptr[b+1] - q_ptr[b]) is position seq_len - n + t, the
+ * places that attn_cache_write fills; n = seq_len reads a whole sequence.
+ *   k_out, v_out  [n_tokens, hk, d] bf16 or f32 (out_dtype), 16-byte aligned
+ * Rows of no sequence are left as they were; so is a row whose slot, position
+ * or page is out of range (INVALID_ARG on the device).  The outputs must not lie
+ * where the call reads (not looked at). */
+int attn_cache_read(const attn_pages_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr,
+                    int n_tokens, void *k_out, void *v_out, int out_dtype, attn_stream_t stream);
+
+/* ---- pages in 8 bits -------------------------------------------------------
+ * k and v of `pages` are codes of one byte, strides in elements (bytes) and
+ * multiples of 16; every token and key/value head has one scale for its keys
+ * and one for its values, [n_pages, page_size, hk] f32, strides in elements,
+ * alike for both and not negative.  A value is code * scale.
+ * The table operations above serve these pages as they are: attn_cache_copy_pages
+ * moves the codes in one call and the scales in another. */
+enum { ATTN_CODES_INT8 = 0, ATTN_CODES_E4M3 = 1 };
+typedef struct {
+  attn_pages_t pages;
+  const float *k_scales, *v_scales;
+  int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+  int32_t format, reserved;   /* ATTN_CODES_* */
+} attn_pages8_t;
+
+/* attn_paged_fwd and attn_prefix_fwd over such pages.  Scores and weights take
+ * the scales in 32 bits; codes enter the products as they are, so that nothing
+ * is rounded that the codes had not been.  Scales are expected not to be
+ * negative, finite and, but for 0, above 1e-24; codes and scales behind a
+ * sequence's end, and those that no token of the sequence sees, are never used,
+ * whatever they hold.  The workspace is that of the calls above. */
+int attn_paged8_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
+                    const attn_pages8_t *pages, const attn_seqs_t *seqs, float scale, int window,
+                    int sinks, void *out, int out_dtype, float *lse, void *d_ws, size_t ws_bytes,
+                    attn_stream_t stream);
+int attn_prefix8_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
+                     const attn_pages8_t *pages, const attn_seqs_t *prefix, const int32_t *group_ptr,
+                     const attn_seqs_t *seqs, float scale, void *out, int out_dtype, float *lse,
+                     void *d_ws, size_t ws_bytes, attn_stream_t stream);
+
+/* attn_cache_write into such pages.  Of a token's head with the largest
+ * magnitude a, M = 127 (int8) or 448 (e4m3): its scale is a / M, and x becomes
+ * the code next to x M / a, the even one of two as near (a = 0: scale and codes
+ * 0).  Where a value is not finite the scale is NaN and the codes are 0: the
+ * head's whole row reads as NaN. */
+int attn_cache8_write(const attn_pages8_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr,
+                      const void *k_new, const void *v_new, int n_tokens, int64_t new_token_stride,
+                      int64_t new_head_stride, attn_stream_t stream);
+
+/* attn_cache_read from such pages: code * scale, rounded once. */
+int attn_cache8_read(const attn_pages8_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr,
+                     int n_tokens, void *k_out, void *v_out, int out_dtype, attn_stream_t stream);
 
 #ifdef __cplusplus
 }

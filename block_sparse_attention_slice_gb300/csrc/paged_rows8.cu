@@ -223,9 +223,9 @@ __global__ void __launch_bounds__(R8_WARPS * 32, 1) paged_rows8_kernel(const Pag
 
   uint32_t qf[D / 16][4];
   float o[D / 8][4];
-  // A row's reference is m - lc: p = 2^(s - m + lc), w = p vs.  m is the lazy maximum,
-  // lc the row's power of two; unset: no weight other than 0 has been met since m last
-  // grew, so lc may not suit what comes.
+  // p = 2^(s - m), m the lazy maximum; a value's weight is p vs 2^lc, and so O holds
+  // 2^lc times its sum.  unset: no weight other than 0 has been met since m last grew,
+  // so lc may not suit what comes.
   float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f, rs0 = 0.f, rs1 = 0.f;
   int lc0 = 0, lc1 = 0;
   bool unset0 = true, unset1 = true;
@@ -344,23 +344,23 @@ __global__ void __launch_bounds__(R8_WARPS * 32, 1) paged_rows8_kernel(const Pag
         }
       }
     }
-    float4 vsc[NSUB];
+    // the keys' scales and the rows' factors: x becomes the score in log2 units
+    const uint64_t rr0 = f2_make(rs0, rs0), rr1 = f2_make(rs1, rs1);
+    auto scales = [&](uint32_t a, uint64_t &lo, uint64_t &hi) {      // in the order of the lane's keys
+      const uint4 w = lds16(a);
+      lo = flip ? f2_make_u(w.y, w.x) : f2_make_u(w.x, w.y);
+      hi = flip ? f2_make_u(w.w, w.z) : f2_make_u(w.z, w.w);
+    };
+    auto times = [&](float &a, float &b, uint64_t f) { f2_split(f2_mul(f2_make(a, b), f), a, b); };
 #pragma unroll
     for (int j = 0; j < NSUB; ++j) {
-      auto turned = [&](uint4 w) {       // in the order of the lane's keys
-        const float4 y = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-        return flip ? make_float4(y.y, y.x, y.w, y.z) : y;
-      };
-      const float4 k4 = turned(lds16(sc + j * 64));
-      vsc[j] = turned(lds16(sc + KEYS * 4 + j * 64));
-      x[2 * j][0] *= k4.x;
-      x[2 * j][1] *= k4.y;
-      x[2 * j][2] *= k4.x;
-      x[2 * j][3] *= k4.y;
-      x[2 * j + 1][0] *= k4.z;
-      x[2 * j + 1][1] *= k4.w;
-      x[2 * j + 1][2] *= k4.z;
-      x[2 * j + 1][3] *= k4.w;
+      uint64_t k2[2];
+      scales(sc + j * 64, k2[0], k2[1]);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        times(x[2 * j + b][0], x[2 * j + b][1], f2_mul(k2[b], rr0));
+        times(x[2 * j + b][2], x[2 * j + b][3], f2_mul(k2[b], rr1));
+      }
     }
     if (key0 + KEYS > all_hi || (key0 < all_lo && key0 + KEYS > p.sinks)) {
 #pragma unroll
@@ -380,11 +380,9 @@ __global__ void __launch_bounds__(R8_WARPS * 32, 1) paged_rows8_kernel(const Pag
     }
     a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
     a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
-    a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2)) * rs0;
-    a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2)) * rs1;
+    a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
+    a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
     auto rescale = [&](float f0, float f1) {
-      l0 *= f0;
-      l1 *= f1;
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
         o[j][0] *= f0;
@@ -400,25 +398,31 @@ __global__ void __launch_bounds__(R8_WARPS * 32, 1) paged_rows8_kernel(const Pag
       if (g1) m1 = a1;
       unset0 |= g0;
       unset1 |= g1;
+      l0 *= f0;
+      l1 *= f1;
       rescale(f0, f1);
     }
-    const float b0 = m0 == -INFINITY ? 0.f : static_cast<float>(lc0) - m0, b1 = m1 == -INFINITY ? 0.f : static_cast<float>(lc1) - m1;
+    const float b0 = m0 == -INFINITY ? 0.f : -m0, b1 = m1 == -INFINITY ? 0.f : -m1;
+    const float c0 = pow2_of(lc0), c1 = pow2_of(lc1);
     float w0 = 0.f, w1 = 0.f;            // largest weights, of this lane's keys
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const float s0 = b & 1 ? vsc[b >> 1].z : vsc[b >> 1].x, s1 = b & 1 ? vsc[b >> 1].w : vsc[b >> 1].y;
-      x[b][0] = ex2_approx(fmaf(x[b][0], rs0, b0));
-      x[b][1] = ex2_approx(fmaf(x[b][1], rs0, b0));
-      x[b][2] = ex2_approx(fmaf(x[b][2], rs1, b1));
-      x[b][3] = ex2_approx(fmaf(x[b][3], rs1, b1));
-      l0 += x[b][0] + x[b][1];
-      l1 += x[b][2] + x[b][3];
-      x[b][0] *= s0;
-      x[b][1] *= s1;
-      x[b][2] *= s0;
-      x[b][3] *= s1;
-      w0 = max3f(w0, fabsf(x[b][0]), fabsf(x[b][1]));
-      w1 = max3f(w1, fabsf(x[b][2]), fabsf(x[b][3]));
+    for (int j = 0; j < NSUB; ++j) {
+      uint64_t v2[2];
+      scales(sc + KEYS * 4 + j * 64, v2[0], v2[1]);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float(&y)[4] = x[2 * j + b];
+        f2_split(f2_add(f2_make(y[0], y[1]), f2_make(b0, b0)), y[0], y[1]);
+        f2_split(f2_add(f2_make(y[2], y[3]), f2_make(b1, b1)), y[2], y[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = ex2_approx(y[e]);
+        l0 += y[0] + y[1];
+        l1 += y[2] + y[3];
+        times(y[0], y[1], f2_mul(v2[b], f2_make(c0, c0)));
+        times(y[2], y[3], f2_mul(v2[b], f2_make(c1, c1)));
+        w0 = max3f(w0, fabsf(y[0]), fabsf(y[1]));
+        w1 = max3f(w1, fabsf(y[2]), fabsf(y[3]));
+      }
     }
     if (__any_sync(0xffffffffu, unset0 || unset1 || w0 > 32768.f || w1 > 32768.f)) {
       // the rows' powers of two are looked at: the largest weight to 2^7 .. 2^8
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(R8_WARPS * 32, 1) paged_rows8_kernel(const Pag
         w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 2));
         float f = 1.f;
         if (w > 32768.f || (unset && w > 0.f && w < 1.f)) {
-          const int by = min(max(134 - static_cast<int>(__float_as_uint(w) >> 23), max(-100 - lc, -126)), min(80 - lc, 127));
+          const int by = min(max(134 - static_cast<int>(__float_as_uint(w) >> 23), max(-126 - lc, -126)), min(126 - lc, 126));
           f = pow2_of(by);
           lc += by;
         }
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(R8_WARPS * 32, 1) paged_rows8_kernel(const Pag
         if (row1 >= 0) p.rec[row1] = Rec4{static_cast<int>(worker), slot0, np, lr + 8};
       }
       const bool whole = ends && piece0 == 0;
-      // the rows' powers of two leave: pieces are joined by their true maxima
+      // the rows' powers of two leave
       rescale(pow2_of(-lc0), pow2_of(-lc1));
       lc0 = lc1 = 0;
       // this lane has D / 4 columns in a row of either row, the first half of them in [..][0]

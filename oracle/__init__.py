@@ -22,7 +22,9 @@ printed on the pages (``tests/golden/``), invariants or brute force.
 """
 from .attention import (FULL, CAUSAL, INV_CAUSAL, BI_CAUSAL, mask_rows,
                         mask_rows_grid, oracle_attention, oracle_merge)
+from .beam import oracle_beam_select
 from .cache import CacheOracle
+from .codes import oracle_encode
 from .paged import oracle_paged
 from .tiles import (oracle_slices_from_grid, oracle_tiles, oracle_tiles_dense,
                     slice_row_interval)

@@ -155,7 +155,7 @@ PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, co
 // the warp-level kernel, larger ones to the tensor-core tiles.  What the kernel
 // chose is left in p and, the rows of a piece, in `tile_rows`.
 int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
-  if (!p.bits8 && static_cast<int64_t>(tokens) * p.G > 16) {
+  if (static_cast<int64_t>(tokens) * p.G > 16) {
     const int rc = paged_tiles_launch(p, d, tokens, s, tile_rows);
     if (rc != ATTN_ERR_UNSUPPORTED) return rc;
   }

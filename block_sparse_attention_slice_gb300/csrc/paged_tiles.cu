@@ -49,6 +49,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "paged_join.cuh"
@@ -59,27 +60,68 @@ namespace attn {
 constexpr int PT_KL = 7, PT_BN = 128, PT_IQ = 4;
 constexpr float PT_TAU = 8.0f;
 
-template <int D, int TILES>
+template <int D, int TILES, bool B8>
 struct TileLayout {
-  static constexpr int NS = D == 64 ? 10 : TILES == 2 ? 4 : 5;   // K/V ring slots: 128 to 160 KB
+  static constexpr int NS = B8 ? (D == 64 ? 6 - 2 * (TILES == 1) : 3) : D == 64 ? 10 : TILES == 2 ? 4 : 5;   // K/V ring slots: 64 to 160 KB
   static constexpr int HALF = 128 * 64 * 2, NHALF = D / 64, TILE = NHALF * HALF;
-  static constexpr int Q_OFF = 0, KV_OFF = TILES * TILE, SEG_OFF = KV_OFF + NS * TILE;
+  // pages in 8 bits: slots of codes, and of the scales of a tile's keys and values
+  static constexpr int NG = !B8 ? 0 : D == 64 ? 8 : TILES == 2 ? 3 : 4, CODES = TILE / 2, NC = B8 ? 4 : 0, SCALES = 2 * 128 * 4;
+  static constexpr int Q_OFF = 0, KV_OFF = TILES * TILE, G_OFF = KV_OFF + NS * TILE, C_OFF = G_OFF + NG * CODES,
+                       SEG_OFF = C_OFF + NC * SCALES;
   static constexpr int BAR_OFF = SEG_OFF + PT_IQ * 64;
   static constexpr int B_Q = 0, B_QE = 1, B_FULL = 2, B_EMPTY = B_FULL + NS, B_S = B_EMPTY + NS, B_P = B_S + 2,
                        B_O = B_P + 2, B_IF = B_O + TILES, B_IE = B_IF + PT_IQ, B_DRAIN = B_IE + PT_IQ,
-                       B_V = B_DRAIN + 1, B_X = B_V + 1, NBAR = B_X + 2;
+                       B_V = B_DRAIN + 1, B_X = B_V + 1, B_GF = B_X + 2, B_GE = B_GF + NG, B_CF = B_GE + NG, B_CE = B_CF + NC,
+                       NBAR = B_CE + NC;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int XML_OFF = MISC_OFF + 16;               // TILES = 1: (m, l) of both groups
   static constexpr int SCAN_OFF = XML_OFF + (TILES == 1 ? 2 * 128 * 8 : 0);
   static constexpr int FIRST_OFF = SCAN_OFF + 16 * 8;
-  static constexpr int THREADS = 256 + 64;
+  static constexpr int THREADS = B8 ? 512 : 256 + 64;
   static size_t bytes(const PagedParams &p, bool infos) {
     return 1024 + FIRST_OFF + (p.warp_plan ? THREADS / 32 * static_cast<size_t>(PLAN_WARP)
                                            : 8ull * (p.n_seqs + 1) + (infos ? sizeof(SeqInfo) * p.n_seqs : 0));
   }
   static_assert(PT_IQ * 64 >= THREADS / 32 * 16, "my_sms puts its sums where the segments will be");
-  static_assert(MISC_OFF % 8 == 0 && (TILES == 1 || NS % 2 == 0), "alignment; keys in even slots");
+  static_assert(MISC_OFF % 8 == 0 && (B8 || TILES == 1 || NS % 2 == 0), "alignment; keys in even slots");
 };
+
+// Four codes of 8 bits (lowest byte first) as bf16, exactly.  An int8 x: 0x4300 | its
+// low 7 bits is the number 128 + those, less 128, or 256 where x is negative.  An
+// e4m3: its exponent and fraction in bf16's places are the number times 2^-120.
+template <bool E4M3>
+__device__ __forceinline__ uint2 bf16_of_codes(uint32_t w) {
+  uint2 r;
+  if constexpr (E4M3) {
+    const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
+    const uint32_t x = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u), y = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(x), "r"(0x7b807b80u));      // 2^120
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(y), "r"(0x7b807b80u));
+  } else {
+    const uint32_t a = __byte_perm(w, 0x43434343u, 0x4140), b = __byte_perm(w, 0x43434343u, 0x4342);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(a & 0xff7fff7fu), "r"(a & 0xff80ff80u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(b & 0xff7fff7fu), "r"(b & 0xff80ff80u));
+  }
+  return r;
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void fetch_scale(uint32_t dst, const float *src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4u : 0u) : "memory");
+}
+// Registers of the executing warpgroup's threads from here on.
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // Transposes 4 x 4 words of 16 bytes among four neighbouring lanes: lane q's
 // word k becomes lane k's word q.
@@ -140,13 +182,13 @@ struct Seg {
 };
 static_assert(sizeof(Seg) <= 64, "segment record");
 
-template <int D, int TILES>
-__global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
+template <int D, int TILES, bool B8>
+__global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int tpt,
                        const int keep_infos) {
-  using L = TileLayout<D, TILES>;
-  constexpr int NS = L::NS;
+  using L = TileLayout<D, TILES, B8>;
+  constexpr int NS = L::NS, NG = B8 ? L::NG : 1, NC8 = B8 ? L::NC : 1;       // the last two of codes alone
   extern __shared__ uint8_t tiles_smem[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(tiles_smem) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
@@ -165,7 +207,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpi = tpt * TILES;
   const uint64_t lim = p.wait_ns;
-  constexpr int WP = 8, WM = 9;       // producer, issuer
+  constexpr int WP = 8, WM = 9, WC = 12;       // producer, issuer; of codes: those who turn them into operands
 
   int sms = gridDim.x;
   if (p.share.side) {
@@ -182,7 +224,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     mbar_init(bar(L::B_Q), 1);
     mbar_init(bar(L::B_QE), 1);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(bar(L::B_FULL + s), 1);
+      mbar_init(bar(L::B_FULL + s), B8 ? 4 : 1);
       mbar_init(bar(L::B_EMPTY + s), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -193,7 +235,15 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     for (int t = 0; t < TILES; ++t) mbar_init(bar(L::B_O + t), 1);
     for (int u = 0; u < PT_IQ; ++u) {
       mbar_init(bar(L::B_IF + u), 1);
-      mbar_init(bar(L::B_IE + u), 9);
+      mbar_init(bar(L::B_IE + u), B8 ? 13 : 9);
+    }
+    for (int s = 0; s < L::NG; ++s) {
+      mbar_init(bar(L::B_GF + s), 1);
+      mbar_init(bar(L::B_GE + s), 4);
+    }
+    for (int s = 0; s < L::NC; ++s) {
+      mbar_init(bar(L::B_CF + s), 32);
+      mbar_init(bar(L::B_CE + s), 8);
     }
     mbar_init(bar(L::B_DRAIN), 1);
     mbar_init(bar(L::B_V), 1);
@@ -223,16 +273,20 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   const int mine = blockIdx.x / p.hp, sub = blockIdx.x - mine * p.hp;      // span, and head of a group
   const long long from = mine < n_spans ? mine * span : total, to = min(total, from + span);
 
+  // Codes: 512 threads of 128 registers, of which the softmax takes 184 and the others
+  // 72, each warpgroup by one instruction.
+  if (warp >= 8) {
+  if constexpr (B8) fewer_registers<72>();
   if (warp == WP) {
     // -------------------------------------------------------------- producer
-    uint32_t ld = 0, nseg = 0;
+    uint32_t ld = 0, nseg = 0, tiles = 0;
     bool ok = true;
     long long at = from;
     Walk<0, PT_KL> w;
     // stands if the launch gives up, too: the join then reads no stale record
     if (lane == 0 && !p.rec) p.cuts[blockIdx.x] = Cut{};
     if (at < to) w.seek(p, first, info, tpi, at);
-    const int R = min(1 << p.page_shift, 128), ppt = 128 / R, page_mask = (1 << p.page_shift) - 1;
+    const int r_shift = min(p.page_shift, 7), R = 1 << r_shift, ppt = 128 / R, page_mask = (1 << p.page_shift) - 1;
     while (ok) {
       const int qs = nseg % PT_IQ;
       if (nseg >= PT_IQ && !wait_all(bar(L::B_IE + qs), (nseg / PT_IQ - 1) & 1, abort, lim)) break;
@@ -314,11 +368,18 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       // the ring (NS is even): once they are done, both slots are free, by one
       // commit (1 % of the call).
       auto load = [&](const CUtensorMap *tm, int tok, int page, bool values) {
-        const int slot = ld % NS;
-        const uint32_t was = ld - NS + (TILES == 2 && values ? 1 : 0);
-        if (ld >= NS && !wait_all(bar(L::B_EMPTY + was % NS), (was / NS) & 1, abort, lim)) {
-          ok = false;
-          return;
+        const int slot = ld % (B8 ? NG : NS);
+        if constexpr (B8) {
+          if (ld >= static_cast<uint32_t>(NG) && !wait_all(bar(L::B_GE + slot), (ld / NG - 1) & 1, abort, lim)) {
+            ok = false;
+            return;
+          }
+        } else {
+          const uint32_t was = ld - NS + (TILES == 2 && values ? 1 : 0);
+          if (ld >= NS && !wait_all(bar(L::B_EMPTY + was % NS), (was / NS) & 1, abort, lim)) {
+            ok = false;
+            return;
+          }
         }
         // failure-path test only: every CTA leaves its second load out, so that
         // the issuer's bounded wait for it runs out
@@ -326,13 +387,40 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           ++ld;
           return;
         }
-        if (lane == 0) mbar_arrive_expect_tx(bar(L::B_FULL + slot), L::TILE);
-        __syncwarp();
-        if (lane < ppt)
-          for (int hh = 0; hh < L::NHALF; ++hh)
-            tma_load_4d(kv_smem + slot * L::TILE + hh * L::HALF + lane * R * 128, tm, bar(L::B_FULL + slot), hh * 64, tok,
-                        w.h * p.hp + sub, page);
+        if constexpr (B8) {
+          if (lane == 0) mbar_arrive_expect_tx(bar(L::B_GF + slot), L::CODES);
+          __syncwarp();
+          if (lane < ppt) tma_load_4d(sb + L::G_OFF + slot * L::CODES + lane * R * D, tm, bar(L::B_GF + slot), 0, tok, w.h * p.hp + sub, page);
+        } else {
+          if (lane == 0) mbar_arrive_expect_tx(bar(L::B_FULL + slot), L::TILE);
+          __syncwarp();
+          if (lane < ppt)
+            for (int hh = 0; hh < L::NHALF; ++hh)
+              tma_load_4d(kv_smem + slot * L::TILE + hh * L::HALF + lane * R * 128, tm, bar(L::B_FULL + slot), hh * 64, tok,
+                          w.h * p.hp + sub, page);
+        }
         ++ld;
+      };
+      // The scales of the j-th tile's keys and values, 0 for keys that no row sees.
+      auto load_scales = [&](int j, int tok, int page) {
+        const uint32_t s = tiles % NC8;
+        if (tiles >= static_cast<uint32_t>(NC8) && !wait_all(bar(L::B_CE + s), (tiles / NC8 - 1) & 1, abort, lim)) {
+          ok = false;
+          return;
+        }
+        const uint32_t dst = sb + L::C_OFF + s * L::SCALES + lane * 4;
+        const int c0 = Seg::key_tile(j, i0, i1, rot, w.sp) << PT_KL;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int x = k * 32 + lane, of = x >> r_shift, pg = __shfl_sync(0xffffffffu, page, of), t = __shfl_sync(0xffffffffu, tok, of) + (x & (R - 1)),
+                    key = c0 + x;
+          const bool live = pg < p.n_pages && key < end && (key >= lo || key < p.sinks);
+          const long long at = live ? pg * p.scale_page + t * p.scale_token + (w.h * p.hp + sub) * p.scale_head : 0;
+          fetch_scale(dst + k * 128, p.k_scales + at, live);
+          fetch_scale(dst + 512 + k * 128, p.v_scales + at, live);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(L::B_CF + s)) : "memory");
+        ++tiles;
       };
       // In the order in which the tensor core takes them, so that no slot waits
       // behind one that is needed later: K_0 V_0 K_1 V_1 .. for two row tiles,
@@ -340,6 +428,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       int tok = tok_next, page = checked(raw_next);
       if (steps > 1) raw_next = look_up(1, tok_next);
       if (TILES == 1) load(&tm_k, tok, page, false);
+      if (B8 && TILES == 1 && ok) load_scales(0, tok, page);
       for (int j = 0; j < steps && ok; ++j) {
         int tok1 = 0, page1 = 0;
         if (j + 1 < steps) {
@@ -348,7 +437,9 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           if (j + 2 < steps) raw_next = look_up(j + 2, tok_next);
         }
         if (TILES == 2) load(&tm_k, tok, page, false);
-        if (TILES == 1 && j + 1 < steps) load(&tm_k, tok1, page1, false);
+        if (B8 && TILES == 2 && ok) load_scales(j, tok, page);
+        if (TILES == 1 && j + 1 < steps && ok) load(&tm_k, tok1, page1, false);
+        if (B8 && TILES == 1 && j + 1 < steps && ok) load_scales(j + 1, tok1, page1);
         if (ok) load(&tm_v, tok, page, true);
         tok = tok1;
         page = page1;
@@ -363,6 +454,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       loads[0] = nseg;
       loads[1] = ld;
     }
+    if constexpr (B8) asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
   } else if (warp == WM) {
     // ---------------------------------------------------------------- issuer
@@ -487,6 +579,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
             }
             tc_fence_after();
             issue_pv(1, 1, v.slot, 0, 8, j == 0);
+            if constexpr (B8) mma_commit(bar(L::B_EMPTY + v.slot));
             if (!more) {
               mma_commit(bar(L::B_O + 1));
             } else {
@@ -503,8 +596,63 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
       wait_drain(bar(L::B_DRAIN), 0, 20000000ull);
     }
     __syncwarp();
+  } else if (B8 && warp >= WC) {
+    // ------------------------------------------------- codes become operands
+    // In the order of the loads.  Eight lanes take 4 words of 16 codes each of rows a and
+    // a ^ 5: with TMA's 128-byte swizzle where they are read, and the operands' where
+    // they are written, neither meets a bank twice (rows of 64 codes: by a's parity).
+    // e4m3's codes that are no numbers become +-480: no weight but 0 meets them.
+    const bool e4m3 = p.format == ATTN_CODES_E4M3;
+    const int q = lane >> 3, i = lane & 7, a = i < 4 ? q : q ^ 5, row0 = (warp - WC) * 32 + a, ch = i & 3;
+    uint32_t pos = 0, nseg = 0;
+    bool ok = true;
+    while (ok) {
+      const int qs = nseg % PT_IQ;
+      if (!wait_all(bar(L::B_IF + qs), (nseg / PT_IQ) & 1, abort, lim)) break;
+      volatile Seg *s = seg_at(qs);
+      const int out = s->out, n = 2 * (s->i1 - s->i0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::B_IE + qs));
+      if (out < 0) break;
+      ++nseg;
+      for (int j = 0; j < n; ++j, ++pos) {
+        const uint32_t g = pos % NG, slot = pos % NS;
+        if (!wait_all(bar(L::B_GF + g), (pos / NG) & 1, abort, lim) ||
+            (pos >= static_cast<uint32_t>(NS) && !wait_all(bar(L::B_EMPTY + slot), (pos / NS - 1) & 1, abort, lim))) {
+          ok = false;
+          break;
+        }
+        const uint32_t src = sb + L::G_OFF + g * L::CODES + row0 * D, dst = kv_smem + slot * L::TILE + row0 * 128;
+        auto turn = [&](auto fmt) {
+          constexpr bool E4M3 = decltype(fmt)::value;
+#pragma unroll
+          for (int hh = 0; hh < L::NHALF; ++hh) {
+            uint4 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = ld_shared_v4(src + k * 8 * D + ((D == 128 ? (hh * 4 + ch) ^ a : ch) << 4));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint2 x = bf16_of_codes<E4M3>(w[k].x), y = bf16_of_codes<E4M3>(w[k].y), z = bf16_of_codes<E4M3>(w[k].z), u = bf16_of_codes<E4M3>(w[k].w);
+              const uint32_t to = dst + hh * L::HALF + k * 8 * 128;
+              st_shared_v4(to + (((2 * ch) ^ a) << 4), make_uint4(x.x, x.y, y.x, y.y));
+              st_shared_v4(to + (((2 * ch + 1) ^ a) << 4), make_uint4(z.x, z.y, u.x, u.y));
+            }
+          }
+        };
+        if (e4m3) turn(std::true_type());
+        else turn(std::false_type());
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(L::B_GE + g));
+          mbar_arrive(bar(L::B_FULL + slot));
+        }
+      }
+    }
+  }
   } else {
     // --------------------------------------------------------------- softmax
+    if constexpr (B8) more_registers<184>();
     // grp: softmax group and its O; t: row tile.  A group takes NC columns of a
     // tile's scores.
     constexpr int NC = TILES == 1 ? 64 : 128;
@@ -512,7 +660,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
     const uint32_t lane_off = static_cast<uint32_t>(wl * 32) << 16;
     const uint32_t tO = tmem + lane_off + 256 + grp * 128;
     float2 *xml = reinterpret_cast<float2 *>(smem + L::XML_OFF);
-    const float sl2 = p.scale_log2;
+    const float sl2 = p.scale_log2, tau = PT_TAU / sl2;
     const int tl = r / p.G, g = r - tl * p.G;               // token and head of this row in its tile
     uint32_t step = 0, nseg = 0;
     bool ok = true;
@@ -543,15 +691,23 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
         if (masked) {
           or_span(max(lo, 0), hi, c0, w);
           if (lo > 0) or_span(0, min(p.sinks, hi), c0, w);
-          // does the tile hold keys that no row of the item sees?
+          // does the tile hold keys that no row of the item sees?  (Of codes they have scales of 0.)
           const int it_end = p.causal ? pos0 + it_ntok : len, it_lo = p.causal && p.window > 0 ? pos0 - p.window + 1 : 0;
-          clear = grp == 0 && (c0 + 128 > it_end || (c0 < it_lo && c0 + 128 > p.sinks));
+          clear = !B8 && grp == 0 && (c0 + 128 > it_end || (c0 < it_lo && c0 + 128 > p.sinks));
         }
         if (!wait_all(bar(L::B_S + u), ph, abort, lim)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        // this group's columns' scales of keys and, 512 bytes on, of values
+        const uint32_t sc = sb + L::C_OFF + (step % NC8) * L::SCALES + (TILES == 1 ? grp * 256 : 0);
+        if constexpr (B8) {
+          if (!wait_all(bar(L::B_CF + step % NC8), (step / NC8) & 1, abort, lim)) {
+            ok = false;
+            break;
+          }
+        }
         if (!idle) {
           float x[NC];
           {
@@ -563,6 +719,15 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
             for (int k = 0; k < NC; ++k) {
               asm volatile("" : "+r"(y[k]));
               x[k] = __uint_as_float(y[k]);
+            }
+          }
+          if constexpr (B8) {
+            // by the scales' products, so that a row's maximum is one of its rounded scores
+#pragma unroll
+            for (int k = 0; k < NC; k += 4) {
+              const uint4 s4 = ld_shared_v4(sc + k * 4);
+              f2_split(f2_mul(f2_make(x[k], x[k + 1]), f2_make_u(s4.x, s4.y)), x[k], x[k + 1]);
+              f2_split(f2_mul(f2_make(x[k + 2], x[k + 3]), f2_make_u(s4.z, s4.w)), x[k + 2], x[k + 3]);
             }
           }
           if (masked) {
@@ -582,11 +747,12 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
 #pragma unroll
             for (int v = 0; v < 4; ++v) m4[v] = max3f(m4[v], x[k + 2 * v], x[k + 2 * v + 1]);
           }
-          const float mx = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
+          // codes: the maximum is kept unscaled until the segment's end
+          const float mx = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3])) * (B8 ? 1.f : sl2);
           const float m_old = m_ref;
-          const bool grow = mx > m_ref + PT_TAU;
+          const bool grow = mx > m_ref + (B8 ? tau : PT_TAU);
           if (grow) m_ref = mx;
-          const float factor = grow ? ex2_approx(m_old - m_ref) : 1.f;
+          const float factor = grow ? ex2_approx((m_old - m_ref) * (B8 ? sl2 : 1.f)) : 1.f;
           l *= factor;
           const float mb = m_ref == -INFINITY ? 0.f : m_ref;
           const uint64_t sc2 = f2_make(sl2, sl2), nb2 = f2_make(-mb, -mb);
@@ -594,13 +760,19 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < NC / 32; ++c) {
             uint32_t pk[16];
+            uint4 v4;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               float a0, a1;
-              f2_split(f2_fma(f2_make(x[c * 32 + 2 * k], x[c * 32 + 2 * k + 1]), sc2, nb2), a0, a1);
+              const uint64_t x2 = f2_make(x[c * 32 + 2 * k], x[c * 32 + 2 * k + 1]);
+              f2_split(B8 ? f2_mul(f2_add(x2, nb2), sc2) : f2_fma(x2, sc2, nb2), a0, a1);
               a0 = ex2_approx(a0);
               a1 = ex2_approx(a1);
               l2[k & 3] = f2_add(l2[k & 3], f2_make(a0, a1));
+              if constexpr (B8) {
+                if (k % 2 == 0) v4 = ld_shared_v4(sc + 512 + (c * 32 + 2 * k) * 4);
+                f2_split(f2_mul(f2_make(a0, a1), k % 2 ? f2_make_u(v4.z, v4.w) : f2_make_u(v4.x, v4.y)), a0, a1);
+              }
               pk[k] = pack_bf16x2(a0, a1);
             }
             tmem_st16(tS + c * 16, pk);
@@ -644,11 +816,16 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
           }
           fence_proxy_async_smem();
         }
+        if constexpr (B8) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::B_CE + step % NC8));
+        }
         tc_fence_before();
         mbar_arrive(bar(L::B_P + u));
       }
       if (!ok) break;
       if (!wait_all(bar(L::B_O + t), nseg & 1, abort, lim)) break;
+      if constexpr (B8) m_ref *= sl2;
       // TILES = 1: both groups learn each other's (m, l); each then merges and
       // stores its half of the columns
       float f0 = 1.f, f1 = 0.f;
@@ -757,7 +934,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
   if (warp == WM) tmem_dealloc(tmem, 512);
   if (threadIdx.x == 0 && *abort) {
     paged_fail(p, ATTN_ERR_TIMEOUT);
-    land_loads(bar(L::B_Q), bar(L::B_FULL), NS, loads[0], loads[1]);
+    land_loads(bar(L::B_Q), bar(B8 ? L::B_GF : L::B_FULL), B8 ? NG : NS, loads[0], loads[1]);
   }
   end_after_previous(p);
 }
@@ -766,29 +943,30 @@ __global__ void __launch_bounds__(TileLayout<D, TILES>::THREADS, 1)
 
 namespace {
 
-int encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+int encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+           CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto enc = tma_encode_fn();
   if (!enc) return ATTN_ERR_CUDA;
   const cuuint32_t one[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc(m, type, rank, const_cast<void *>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? ATTN_OK
              : ATTN_ERR_UNSUPPORTED;
 }
 
-template <int D, int TILES>
+template <int D, int TILES, bool B8>
 int launch_tiles(PagedParams &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
-  using L = TileLayout<D, TILES>;
+  using L = TileLayout<D, TILES, B8>;
   const int tpt = 128 / p.G;
   p.warp_plan = TILES == 1 && p.n_seqs <= 32 && (!p.causal || p.n_tokens <= 64ll * tpt);
-  if (L::bytes(p, false) > kSmemMax) return ATTN_ERR_UNSUPPORTED;    // above 4000 sequences
+  if (L::bytes(p, false) > kSmemMax) return ATTN_ERR_UNSUPPORTED;    // above 4000 sequences (codes, two row tiles of 128 columns: 1600)
   constexpr int kDev = 64;
   static bool done[kDev] = {};
   static std::mutex mu;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDev) return ATTN_ERR_CUDA;
-  auto kern = paged_tiles_kernel<D, TILES>;
+  auto kern = paged_tiles_kernel<D, TILES, B8>;
   auto join = paged_join_kernel<D, TILES * 128, false>;
   {
     std::lock_guard<std::mutex> lock(mu);
@@ -841,16 +1019,23 @@ int paged_tiles_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *t
   {
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(p.hk),
                                 static_cast<cuuint64_t>(p.n_pages)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.token_stride) * 2, static_cast<cuuint64_t>(p.head_stride) * 2,
-                                   static_cast<cuuint64_t>(p.page_stride) * 2};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(page < 128 ? page : 128), 1, 1};
-    if ((rc = encode(&mk, p.k, 4, dims, strides, box)) != ATTN_OK) return rc;
-    if ((rc = encode(&mv, p.v, 4, dims, strides, box)) != ATTN_OK) return rc;
+    const cuuint64_t size = p.bits8 ? 1 : 2;
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.token_stride) * size, static_cast<cuuint64_t>(p.head_stride) * size,
+                                   static_cast<cuuint64_t>(p.page_stride) * size};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(p.bits8 ? d : 64), static_cast<cuuint32_t>(page < 128 ? page : 128), 1, 1};
+    const auto type = p.bits8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const auto swizzle = p.bits8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    if ((rc = encode(&mk, p.k, 4, dims, strides, box, type, swizzle)) != ATTN_OK) return rc;
+    if ((rc = encode(&mv, p.v, 4, dims, strides, box, type, swizzle)) != ATTN_OK) return rc;
   }
   const bool two = tokens > tpt;
   *tile_rows = two ? 256 : 128;
-  if (d == 128) return two ? launch_tiles<128, 2>(p, mq, mk, mv, s) : launch_tiles<128, 1>(p, mq, mk, mv, s);
-  return two ? launch_tiles<64, 2>(p, mq, mk, mv, s) : launch_tiles<64, 1>(p, mq, mk, mv, s);
+  if (p.bits8) {
+    if (d == 128) return two ? launch_tiles<128, 2, true>(p, mq, mk, mv, s) : launch_tiles<128, 1, true>(p, mq, mk, mv, s);
+    return two ? launch_tiles<64, 2, true>(p, mq, mk, mv, s) : launch_tiles<64, 1, true>(p, mq, mk, mv, s);
+  }
+  if (d == 128) return two ? launch_tiles<128, 2, false>(p, mq, mk, mv, s) : launch_tiles<128, 1, false>(p, mq, mk, mv, s);
+  return two ? launch_tiles<64, 2, false>(p, mq, mk, mv, s) : launch_tiles<64, 1, false>(p, mq, mk, mv, s);
 }
 
 }  // namespace attn

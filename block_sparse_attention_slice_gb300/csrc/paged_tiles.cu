@@ -64,8 +64,8 @@ template <int D, int TILES, bool B8>
 struct TileLayout {
   static constexpr int NS = B8 ? (D == 64 ? 6 - 2 * (TILES == 1) : 3) : D == 64 ? 10 : TILES == 2 ? 4 : 5;   // K/V ring slots: 64 to 160 KB
   static constexpr int HALF = 128 * 64 * 2, NHALF = D / 64, TILE = NHALF * HALF;
-  // pages in 8 bits: slots of codes, and of the scales of a tile's keys and values
-  static constexpr int NG = !B8 ? 0 : D == 64 ? 8 : TILES == 2 ? 3 : 4, CODES = TILE / 2, NC = B8 ? 4 : 0, SCALES = 2 * 128 * 4;
+  // pages in 8 bits: slots of codes, and of what the softmax needs of a tile's scales
+  static constexpr int NG = !B8 ? 0 : D == 64 ? 8 : TILES == 2 ? 3 : 4, CODES = TILE / 2, NC = B8 ? 4 : 0, SCALES = 3 * 128 * 4;
   static constexpr int Q_OFF = 0, KV_OFF = TILES * TILE, G_OFF = KV_OFF + NS * TILE, C_OFF = G_OFF + NG * CODES,
                        SEG_OFF = C_OFF + NC * SCALES;
   static constexpr int BAR_OFF = SEG_OFF + PT_IQ * 64;
@@ -109,9 +109,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
-}
-__device__ __forceinline__ void fetch_scale(uint32_t dst, const float *src, bool live) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4u : 0u) : "memory");
 }
 // Registers of the executing warpgroup's threads from here on.
 template <int N>
@@ -173,6 +170,7 @@ struct Seg {
   int tok0, ntok, h, pos0, len, ns, w0, i0, i1;
   int out;              // 0 finished here, 1 / 2 piece slot + 1, -1 no more
   int np, slot0;        // of an item that begins here (i0 = 0): see Rec4
+  int slot;             // its row of the table
   int rot;              // its key tiles are taken in the order i0 + rot, .., i1 - 1, i0, .., i0 + rot - 1
   // the j-th key tile (of 128 keys) of the segment
   static __device__ __forceinline__ int key_tile(int j, int i0, int i1, int rot, const Span &sp) {
@@ -207,7 +205,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpi = tpt * TILES;
   const uint64_t lim = p.wait_ns;
-  constexpr int WP = 8, WM = 9, WC = 12;       // producer, issuer; of codes: those who turn them into operands
+  constexpr int WP = 8, WM = 9, WS = 10, WC = 12;       // producer, issuer; of codes: who fetches scales, those who make operands
 
   int sms = gridDim.x;
   if (p.share.side) {
@@ -235,14 +233,14 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
     for (int t = 0; t < TILES; ++t) mbar_init(bar(L::B_O + t), 1);
     for (int u = 0; u < PT_IQ; ++u) {
       mbar_init(bar(L::B_IF + u), 1);
-      mbar_init(bar(L::B_IE + u), B8 ? 13 : 9);
+      mbar_init(bar(L::B_IE + u), B8 ? 14 : 9);
     }
     for (int s = 0; s < L::NG; ++s) {
       mbar_init(bar(L::B_GF + s), 1);
       mbar_init(bar(L::B_GE + s), 4);
     }
     for (int s = 0; s < L::NC; ++s) {
-      mbar_init(bar(L::B_CF + s), 32);
+      mbar_init(bar(L::B_CF + s), 1);
       mbar_init(bar(L::B_CE + s), 8);
     }
     mbar_init(bar(L::B_DRAIN), 1);
@@ -273,20 +271,19 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
   const int mine = blockIdx.x / p.hp, sub = blockIdx.x - mine * p.hp;      // span, and head of a group
   const long long from = mine < n_spans ? mine * span : total, to = min(total, from + span);
 
-  // Codes: 512 threads of 128 registers, of which the softmax takes 184 and the others
-  // 72, each warpgroup by one instruction.
+  // Codes: 512 threads of 128 registers, of which the softmax takes 184, the others 72.
   if (warp >= 8) {
   if constexpr (B8) fewer_registers<72>();
   if (warp == WP) {
     // -------------------------------------------------------------- producer
-    uint32_t ld = 0, nseg = 0, tiles = 0;
+    uint32_t ld = 0, nseg = 0;
     bool ok = true;
     long long at = from;
     Walk<0, PT_KL> w;
     // stands if the launch gives up, too: the join then reads no stale record
     if (lane == 0 && !p.rec) p.cuts[blockIdx.x] = Cut{};
     if (at < to) w.seek(p, first, info, tpi, at);
-    const int r_shift = min(p.page_shift, 7), R = 1 << r_shift, ppt = 128 / R, page_mask = (1 << p.page_shift) - 1;
+    const int R = min(1 << p.page_shift, 128), ppt = 128 / R, page_mask = (1 << p.page_shift) - 1;
     while (ok) {
       const int qs = nseg % PT_IQ;
       if (nseg >= PT_IQ && !wait_all(bar(L::B_IE + qs), (nseg / PT_IQ - 1) & 1, abort, lim)) break;
@@ -348,6 +345,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
         s->tok0 = tok0;
         s->ntok = tl + 1;
         s->h = w.h * p.hp + sub;
+        if constexpr (B8) s->slot = w.s.slot;
         s->pos0 = pos0;
         s->len = w.s.len;
         s->ns = w.sp.ns;
@@ -401,34 +399,12 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
         }
         ++ld;
       };
-      // The scales of the j-th tile's keys and values, 0 for keys that no row sees.
-      auto load_scales = [&](int j, int tok, int page) {
-        const uint32_t s = tiles % NC8;
-        if (tiles >= static_cast<uint32_t>(NC8) && !wait_all(bar(L::B_CE + s), (tiles / NC8 - 1) & 1, abort, lim)) {
-          ok = false;
-          return;
-        }
-        const uint32_t dst = sb + L::C_OFF + s * L::SCALES + lane * 4;
-        const int c0 = Seg::key_tile(j, i0, i1, rot, w.sp) << PT_KL;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int x = k * 32 + lane, of = x >> r_shift, pg = __shfl_sync(0xffffffffu, page, of), t = __shfl_sync(0xffffffffu, tok, of) + (x & (R - 1)),
-                    key = c0 + x;
-          const bool live = pg < p.n_pages && key < end && (key >= lo || key < p.sinks);
-          const long long at = live ? pg * p.scale_page + t * p.scale_token + (w.h * p.hp + sub) * p.scale_head : 0;
-          fetch_scale(dst + k * 128, p.k_scales + at, live);
-          fetch_scale(dst + 512 + k * 128, p.v_scales + at, live);
-        }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(L::B_CF + s)) : "memory");
-        ++tiles;
-      };
       // In the order in which the tensor core takes them, so that no slot waits
       // behind one that is needed later: K_0 V_0 K_1 V_1 .. for two row tiles,
       // K_0 K_1 V_0 K_2 V_1 .. for one.
       int tok = tok_next, page = checked(raw_next);
       if (steps > 1) raw_next = look_up(1, tok_next);
       if (TILES == 1) load(&tm_k, tok, page, false);
-      if (B8 && TILES == 1 && ok) load_scales(0, tok, page);
       for (int j = 0; j < steps && ok; ++j) {
         int tok1 = 0, page1 = 0;
         if (j + 1 < steps) {
@@ -437,9 +413,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
           if (j + 2 < steps) raw_next = look_up(j + 2, tok_next);
         }
         if (TILES == 2) load(&tm_k, tok, page, false);
-        if (B8 && TILES == 2 && ok) load_scales(j, tok, page);
-        if (TILES == 1 && j + 1 < steps && ok) load(&tm_k, tok1, page1, false);
-        if (B8 && TILES == 1 && j + 1 < steps && ok) load_scales(j + 1, tok1, page1);
+        if (TILES == 1 && j + 1 < steps) load(&tm_k, tok1, page1, false);
         if (ok) load(&tm_v, tok, page, true);
         tok = tok1;
         page = page1;
@@ -454,7 +428,6 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
       loads[0] = nseg;
       loads[1] = ld;
     }
-    if constexpr (B8) asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
   } else if (warp == WM) {
     // ---------------------------------------------------------------- issuer
@@ -596,6 +569,79 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
       wait_drain(bar(L::B_DRAIN), 0, 20000000ull);
     }
     __syncwarp();
+  } else if (B8 && warp == WS) {
+    // ---------------------------------------------------------------- scales
+    // Of a key's scale ks and its value's scale vs the softmax takes a = ks scale log2 e,
+    // b = log2 vs and c = 1 / vs: a score S gives y = S a + b, the logarithm of its
+    // value's weight w = p vs = 2^(y - m), and p = w c goes to the row's sum.  So a scaled
+    // softmax costs one operation a pair of scores more than a plain one, not three.  (vs
+    // = 0 counts as 2^-90, whose codes are zeros.)  A lane has four neighbouring keys,
+    // which lie in one page; its entry is read two tiles ahead, the scales one.  Keys that
+    // no row sees get 0.
+    uint32_t tiles = 0, nseg = 0;
+    bool ok = true;
+    while (ok) {
+      const int qs = nseg % PT_IQ;
+      if (!wait_all(bar(L::B_IF + qs), (nseg / PT_IQ) & 1, abort, lim)) break;
+      volatile Seg *s = seg_at(qs);
+      const int out = s->out, h = s->h, pos0 = s->pos0, ntok = s->ntok, len = s->len, i0 = s->i0, i1 = s->i1, rot = s->rot, steps = i1 - i0;
+      const long long row = s->slot * p.table_stride;
+      const Span sp{s->ns, s->w0, 0};
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::B_IE + qs));
+      if (out < 0) break;
+      ++nseg;
+      const int end = p.causal ? pos0 + ntok : len, lo = p.causal && p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
+      const int page_mask = (1 << p.page_shift) - 1;
+      auto seen = [&](int key) { return key < end && (key >= lo || key < p.sinks); };
+      auto first_key = [&](int j) { return (Seg::key_tile(j, i0, i1, rot, sp) << PT_KL) + 4 * lane; };
+      auto look_up = [&](int j) -> int {
+        if (j >= steps) return -1;
+        const int k0 = first_key(j);
+        return k0 < end && (k0 + 3 >= lo || k0 < p.sinks) ? p.table[row + (k0 >> p.page_shift)] : -1;
+      };
+      float ks[4], vs[4];
+      auto fetch = [&](int j, int pg) {
+        const int k0 = j < steps ? first_key(j) : 0;
+        const bool good = j < steps && pg >= 0 && pg < p.n_pages;
+        const long long at = good ? pg * p.scale_page + (k0 & page_mask) * p.scale_token + h * p.scale_head : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool live = good && seen(k0 + k);
+          ks[k] = live ? p.k_scales[at + k * p.scale_token] : 0.f;
+          vs[k] = live ? p.v_scales[at + k * p.scale_token] : 1.f;
+        }
+      };
+      fetch(0, look_up(0));
+      int pg = look_up(1);
+      for (int j = 0; j < steps; ++j, ++tiles) {
+        float a[4], b[4], c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          a[k] = ks[k] * p.scale_log2;
+          float y;
+          asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(vs[k]));
+          b[k] = y < -90.f ? -90.f : y;
+          c[k] = ex2_approx(-b[k]);
+        }
+        fetch(j + 1, pg);
+        pg = look_up(j + 2);
+        const uint32_t st = tiles % NC8;
+        if (tiles >= static_cast<uint32_t>(NC8) && !wait_all(bar(L::B_CE + st), (tiles / NC8 - 1) & 1, abort, lim)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = sb + L::C_OFF + st * L::SCALES;
+        auto put = [](uint32_t at, float x, float y, float z, float u) {
+          st_shared_v4(at, make_uint4(__float_as_uint(x), __float_as_uint(y), __float_as_uint(z), __float_as_uint(u)));
+        };
+        put(dst + lane * 32, a[0], a[1], b[0], b[1]);
+        put(dst + lane * 32 + 16, a[2], a[3], b[2], b[3]);
+        put(dst + 1024 + lane * 16, c[0], c[1], c[2], c[3]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::B_CF + st));
+      }
+    }
   } else if (B8 && warp >= WC) {
     // ------------------------------------------------- codes become operands
     // In the order of the loads.  Eight lanes take 4 words of 16 codes each of rows a and
@@ -623,20 +669,20 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
           break;
         }
         const uint32_t src = sb + L::G_OFF + g * L::CODES + row0 * D, dst = kv_smem + slot * L::TILE + row0 * 128;
+        // not unrolled: the softmax's instructions need the cache
         auto turn = [&](auto fmt) {
           constexpr bool E4M3 = decltype(fmt)::value;
-#pragma unroll
-          for (int hh = 0; hh < L::NHALF; ++hh) {
-            uint4 w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = ld_shared_v4(src + k * 8 * D + ((D == 128 ? (hh * 4 + ch) ^ a : ch) << 4));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint2 x = bf16_of_codes<E4M3>(w[k].x), y = bf16_of_codes<E4M3>(w[k].y), z = bf16_of_codes<E4M3>(w[k].z), u = bf16_of_codes<E4M3>(w[k].w);
-              const uint32_t to = dst + hh * L::HALF + k * 8 * 128;
-              st_shared_v4(to + (((2 * ch) ^ a) << 4), make_uint4(x.x, x.y, y.x, y.y));
-              st_shared_v4(to + (((2 * ch + 1) ^ a) << 4), make_uint4(z.x, z.y, u.x, u.y));
-            }
+          constexpr int N = 4 * L::NHALF;
+          auto from = [&](int x) { return src + (x & 3) * 8 * D + ((D == 128 ? ((x >> 2) * 4 + ch) ^ a : ch) << 4); };
+          uint4 w = ld_shared_v4(from(0));
+#pragma unroll 1
+          for (int x = 0; x < N; ++x) {
+            const uint4 v = w;
+            if (x + 1 < N) w = ld_shared_v4(from(x + 1));
+            const uint2 b0 = bf16_of_codes<E4M3>(v.x), b1 = bf16_of_codes<E4M3>(v.y), b2 = bf16_of_codes<E4M3>(v.z), b3 = bf16_of_codes<E4M3>(v.w);
+            const uint32_t to = dst + (x >> 2) * L::HALF + (x & 3) * 8 * 128;
+            st_shared_v4(to + (((2 * ch) ^ a) << 4), make_uint4(b0.x, b0.y, b1.x, b1.y));
+            st_shared_v4(to + (((2 * ch + 1) ^ a) << 4), make_uint4(b2.x, b2.y, b3.x, b3.y));
           }
         };
         if (e4m3) turn(std::true_type());
@@ -660,7 +706,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
     const uint32_t lane_off = static_cast<uint32_t>(wl * 32) << 16;
     const uint32_t tO = tmem + lane_off + 256 + grp * 128;
     float2 *xml = reinterpret_cast<float2 *>(smem + L::XML_OFF);
-    const float sl2 = p.scale_log2, tau = PT_TAU / sl2;
+    const float sl2 = p.scale_log2;
     const int tl = r / p.G, g = r - tl * p.G;               // token and head of this row in its tile
     uint32_t step = 0, nseg = 0;
     bool ok = true;
@@ -695,19 +741,20 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
           const int it_end = p.causal ? pos0 + it_ntok : len, it_lo = p.causal && p.window > 0 ? pos0 - p.window + 1 : 0;
           clear = !B8 && grp == 0 && (c0 + 128 > it_end || (c0 < it_lo && c0 + 128 > p.sinks));
         }
-        if (!wait_all(bar(L::B_S + u), ph, abort, lim)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        // this group's columns' scales of keys and, 512 bytes on, of values
-        const uint32_t sc = sb + L::C_OFF + (step % NC8) * L::SCALES + (TILES == 1 ? grp * 256 : 0);
         if constexpr (B8) {
           if (!wait_all(bar(L::B_CF + step % NC8), (step / NC8) & 1, abort, lim)) {
             ok = false;
             break;
           }
         }
+        if (!wait_all(bar(L::B_S + u), ph, abort, lim)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // of this group's columns: a and b of each pair, and c
+        const uint32_t sab = sb + L::C_OFF + (step % NC8) * L::SCALES + (TILES == 1 ? grp * 512 : 0),
+                       sc = sb + L::C_OFF + (step % NC8) * L::SCALES + 1024 + (TILES == 1 ? grp * 256 : 0);
         if (!idle) {
           float x[NC];
           {
@@ -722,12 +769,11 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
             }
           }
           if constexpr (B8) {
-            // by the scales' products, so that a row's maximum is one of its rounded scores
+            // the logarithms of weights; their maximum is one of these rounded numbers
 #pragma unroll
-            for (int k = 0; k < NC; k += 4) {
-              const uint4 s4 = ld_shared_v4(sc + k * 4);
-              f2_split(f2_mul(f2_make(x[k], x[k + 1]), f2_make_u(s4.x, s4.y)), x[k], x[k + 1]);
-              f2_split(f2_mul(f2_make(x[k + 2], x[k + 3]), f2_make_u(s4.z, s4.w)), x[k + 2], x[k + 3]);
+            for (int k = 0; k < NC; k += 2) {
+              const uint4 ab = ld_shared_v4(sab + k * 8);
+              f2_split(f2_fma(f2_make(x[k], x[k + 1]), f2_make_u(ab.x, ab.y), f2_make_u(ab.z, ab.w)), x[k], x[k + 1]);
             }
           }
           if (masked) {
@@ -747,12 +793,11 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
 #pragma unroll
             for (int v = 0; v < 4; ++v) m4[v] = max3f(m4[v], x[k + 2 * v], x[k + 2 * v + 1]);
           }
-          // codes: the maximum is kept unscaled until the segment's end
           const float mx = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3])) * (B8 ? 1.f : sl2);
           const float m_old = m_ref;
-          const bool grow = mx > m_ref + (B8 ? tau : PT_TAU);
+          const bool grow = mx > m_ref + PT_TAU;
           if (grow) m_ref = mx;
-          const float factor = grow ? ex2_approx((m_old - m_ref) * (B8 ? sl2 : 1.f)) : 1.f;
+          const float factor = grow ? ex2_approx(m_old - m_ref) : 1.f;
           l *= factor;
           const float mb = m_ref == -INFINITY ? 0.f : m_ref;
           const uint64_t sc2 = f2_make(sl2, sl2), nb2 = f2_make(-mb, -mb);
@@ -760,18 +805,19 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < NC / 32; ++c) {
             uint32_t pk[16];
-            uint4 v4;
+            uint4 c4;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               float a0, a1;
               const uint64_t x2 = f2_make(x[c * 32 + 2 * k], x[c * 32 + 2 * k + 1]);
-              f2_split(B8 ? f2_mul(f2_add(x2, nb2), sc2) : f2_fma(x2, sc2, nb2), a0, a1);
+              f2_split(B8 ? f2_add(x2, nb2) : f2_fma(x2, sc2, nb2), a0, a1);
               a0 = ex2_approx(a0);
               a1 = ex2_approx(a1);
-              l2[k & 3] = f2_add(l2[k & 3], f2_make(a0, a1));
               if constexpr (B8) {
-                if (k % 2 == 0) v4 = ld_shared_v4(sc + 512 + (c * 32 + 2 * k) * 4);
-                f2_split(f2_mul(f2_make(a0, a1), k % 2 ? f2_make_u(v4.z, v4.w) : f2_make_u(v4.x, v4.y)), a0, a1);
+                if (k % 2 == 0) c4 = ld_shared_v4(sc + (c * 32 + 2 * k) * 4);
+                l2[k & 3] = f2_fma(f2_make(a0, a1), k % 2 ? f2_make_u(c4.z, c4.w) : f2_make_u(c4.x, c4.y), l2[k & 3]);
+              } else {
+                l2[k & 3] = f2_add(l2[k & 3], f2_make(a0, a1));
               }
               pk[k] = pack_bf16x2(a0, a1);
             }
@@ -825,7 +871,6 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
       }
       if (!ok) break;
       if (!wait_all(bar(L::B_O + t), nseg & 1, abort, lim)) break;
-      if constexpr (B8) m_ref *= sl2;
       // TILES = 1: both groups learn each other's (m, l); each then merges and
       // stores its half of the columns
       float f0 = 1.f, f1 = 0.f;

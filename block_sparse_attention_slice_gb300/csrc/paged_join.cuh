@@ -132,7 +132,9 @@ __global__ void __launch_bounds__(256, 4) paged_join_kernel(const PagedParams p)
   using G = Gather<D, PACKED ? D / 4 : 16>;
   constexpr int NG = 256 / G::LN;
   __shared__ __align__(16) float red[NG][D + 4];
-  admit_next();
+  // The tiles of codes take an SM's whole register file.  Started beside a join they are
+  // slower throughout (back to back 275 us a call, 238 behind its end).
+  if (PACKED || !p.bits8) admit_next();
   after_previous();
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.rows == 0) return;

@@ -4,18 +4,20 @@
 // A continuation's score is c_b + logit, with c_b = score_b - ln sum exp(logit): of one
 // beam's continuations the best are those of its largest logits, so one pass over the
 // logits gives both the sum and, for every part of a row, its `keep` largest.  The rest
-// is small: a block a prompt adds the parts' sums in 64 bits, compares the parts' best
-// as 64-bit scores and keeps the best of them all.
+// is small: a block a prompt adds the parts' sums, compares the parts' best as 64-bit
+// scores and keeps the best of them all.
 //
-// beam_scan_kernel: a block holds a part of a row in registers (its logits are read
-// once) and has from it maximum, sum and the best.  For those it finds a threshold that
-// `keep` values reach by bisection on the threads' maxima: `keep` threads whose maximum
-// reaches it have as many values that do, and few others are there.  What reaches it
-// goes to a list in shared memory and is ranked there.  Values are compared as whole
-// numbers in the order of the floats.  Where the list overflows (values that are equal by
-// the thousand, as where most of a vocabulary is ruled out) the best are taken one by one.
+// The best of a block's values: its threads form at least `keep` groups, and the
+// smallest of the groups' maxima is a threshold that `keep` values reach and few more
+// (n groups: some n (ln n + 0.6) of them, where values come in no order).  What reaches
+// it goes to a list in shared memory and is ranked there.  That takes one exchange
+// between the warps; a bisection for the exact threshold took ten.  Values are compared
+// as whole numbers in the order of the floats, -0 as 0.  Where the list overflows (values
+// that are equal by the thousand, as where most of a vocabulary is ruled out) the best
+// are taken one by one.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -31,58 +33,46 @@ namespace attn {
 namespace {
 
 constexpr int BS_T = 256;            // threads of a scanning block
-constexpr int BS_CAP = 1024;         // places of its list
+constexpr int BS_CAP = 2048;         // places of its list
 constexpr int BP_T = 256;            // of a choosing block
 constexpr int BP_CAP = 1024;
 
 // The order of the floats as whole numbers; -inf is 0x007fffff, 0 stands for no value.
 __device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t b = __float_as_uint(x);
+  const uint32_t b = __float_as_uint(x + 0.f);
   return max((b & 0x80000000u) ? ~b : b | 0x80000000u, 1u);
 }
 __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 __device__ __forceinline__ unsigned long long key_of(double x) {
-  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x));
+  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
   return (b >> 63) ? ~b : b | 1ull << 63;
 }
 __device__ __forceinline__ double value_of(unsigned long long k) {
   return __longlong_as_double(static_cast<long long>((k >> 63) ? k ^ 1ull << 63 : ~k));
 }
 
-// A threshold that at least min(keep, values there are) of the block's `top`, one a
-// thread, reach, and not many more: bisection between the largest and the smallest.
+// A key, not 0, that at least min(keep, keys there are) of the block's keys reach, given
+// the largest of each thread's (0: none); keep <= 64.  `sums` has a place a warp.
 template <int T, typename K>
 __device__ __forceinline__ K threshold(K top, int keep, K *sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  K hi = top, lo = top;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const K a = __shfl_xor_sync(0xffffffffu, hi, o), b = __shfl_xor_sync(0xffffffffu, lo, o);
-    hi = a > hi ? a : hi;
-    lo = b < lo ? b : lo;
+  // groups of as many threads as leave `keep` of them, a warp at most
+  int width = 32;
+  while (width > 1 && T / width < keep) width >>= 1;
+  for (int o = 1; o < width; o <<= 1) {
+    const K a = __shfl_xor_sync(0xffffffffu, top, o);
+    top = a > top ? a : top;
   }
-  if (lane == 0) sums[2 * warp] = hi, sums[2 * warp + 1] = lo;
+  for (int o = width; o < 32; o <<= 1) {
+    const K a = __shfl_xor_sync(0xffffffffu, top, o);
+    top = a < top ? a : top;
+  }
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < T / 32; ++w) {
-    hi = sums[2 * w] > hi ? sums[2 * w] : hi;
-    lo = sums[2 * w + 1] < lo ? sums[2 * w + 1] : lo;
-  }
-  // all reach lo; fewer than keep reach hi + 1
-  if (lo < 1) lo = 1;
-  while (lo < hi) {
-    const K mid = lo + (hi - lo + 1) / 2;
-    const int n = __syncthreads_count(top >= mid);
-    if (n >= keep) {
-      lo = mid;
-      if (n <= keep + keep / 2) break;
-    } else {
-      hi = mid - 1;
-    }
-  }
-  return lo;
+  for (int w = 0; w < T / 32; ++w) top = sums[w] < top ? sums[w] : top;
+  return top < 1 ? 1 : top;
 }
 
 // Whether (a, i) stands before (b, j).
@@ -108,157 +98,187 @@ __device__ __forceinline__ void block_best(K &k, int &i, K *ks, int *is) {
     if (before(ks[w], is[w], k, i)) k = ks[w], i = is[w];
 }
 
+// Writes the best of n listed keys: a warp takes an entry at a time and counts those that
+// stand before it, 32 together.
+template <int T, typename K, typename B, typename W>
+__device__ __forceinline__ void rank_list(int n, int keep, B stands_before, W write) {
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < n; i += T / 32) {
+    int rank = 0;
+    for (int j0 = 0; j0 < n && rank < keep; j0 += 32) rank += __popc(__ballot_sync(0xffffffffu, j0 + lane < n && stands_before(j0 + lane, i)));
+    if (lane == 0 && rank < keep) write(rank, i);
+  }
+}
+
 struct ScanParams {
   const void *logits;
   const uint8_t *done;
   long long row_stride;      // elements
-  int vocab, splits, keep;
+  int vocab, splits, keep, parts;       // parts: of all rows
   float2 *ms;                // [rows][splits]: maximum, sum of exp(x - maximum)
   uint32_t *keys;            // [rows][splits][keep], best first
   int *ids;                  // their tokens; -1: none
 };
 
 template <typename E>
-struct Vec;
+struct Vec;                  // a 16-byte word of logits
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void unpack(const uint4 &w, float *x) {
-    x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
+  static __device__ __forceinline__ float get(const uint4 &w, int e) {
+    return __uint_as_float(e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w);
   }
-  static __device__ __forceinline__ float one(const float *p) { return *p; }
+  static __device__ __forceinline__ uint32_t bits(const float *p) { return __float_as_uint(*p); }
 };
 template <>
 struct Vec<uint16_t> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void unpack(const uint4 &w, float *x) {
-    const uint32_t y[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(y[i] << 16), x[2 * i + 1] = __uint_as_float(y[i] & 0xffff0000u);
+  static __device__ __forceinline__ float get(const uint4 &w, int e) {
+    const uint32_t y = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
+    return __uint_as_float(e & 1 ? y & 0xffff0000u : y << 16);
   }
-  static __device__ __forceinline__ float one(const uint16_t *p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
+  static __device__ __forceinline__ uint32_t bits(const uint16_t *p) { return *p; }
 };
 
-// Bound by HBM where there are many rows.  E: the logits' type; PER values a thread.
-// A row is taken by its 16-byte words wherever it begins: a word that the row's ends cut
-// is read value by value.
-template <typename E, int PER>
-__global__ void __launch_bounds__(BS_T) beam_scan_kernel(const ScanParams p) {
-  constexpr int N = Vec<E>::N, WORDS = PER / N;
-  __shared__ uint32_t sums[2 * BS_T / 32];
-  __shared__ float part[BS_T / 32];
+// A block takes part after part, the next one's words on their way while it works on one
+// (without that, and with a part a block, 512 rows of 131072 bf16 took 88 us).  E: the
+// logits' type; WORDS: 16-byte words a thread, which stay in registers as they were read.
+// A row is taken by its 16-byte words wherever it begins; of a word that the row's ends
+// cut the values outside count as -inf and are no candidates.
+template <typename E, int WORDS>
+__global__ void __launch_bounds__(BS_T, 4) beam_scan_kernel(const ScanParams p) {
+  constexpr int N = Vec<E>::N;
+  __shared__ uint32_t sums[BS_T / 32];
+  __shared__ float part[2][BS_T / 32];
+  __shared__ int parti[BS_T / 32];
   __shared__ uint32_t list_k[BS_CAP];
   __shared__ int list_i[BS_CAP];
   __shared__ int listed;
   after_previous();
   admit_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long row = blockIdx.x / p.splits;
-  const int split = static_cast<int>(blockIdx.x - row * p.splits);
-  if (p.done && p.done[row]) return;
-  const E *base = static_cast<const E *>(p.logits) + row * p.row_stride;
-  const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(E));
-  const E *aligned = base - skew;            // not read before base
-  float x[PER];
-#pragma unroll
-  for (int w = 0; w < WORDS; ++w) {
-    // the word's first value is number v of the row
-    const long long v = (static_cast<long long>(split) * (BS_T * WORDS) + w * BS_T + threadIdx.x) * N - skew;
-    if (v >= 0 && v + N <= p.vocab) {
-      Vec<E>::unpack(__ldcs(reinterpret_cast<const uint4 *>(aligned + skew + v)), x + w * N);
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e) x[w * N + e] = v + e >= 0 && v + e < p.vocab ? Vec<E>::one(base + v + e) : 0.f;
-    }
-  }
-  auto id_of = [&](int w, int e) -> long long {
-    return (static_cast<long long>(split) * (BS_T * WORDS) + w * BS_T + threadIdx.x) * N - skew + e;
+  struct Part {
+    uint4 x[WORDS];
+    uint32_t there;          // bit w * N + e: the value is the row's
+    int first;               // word w begins with number first + w * BS_T * N of the row
   };
-  auto there = [&](int w, int e) {
-    const long long v = id_of(w, e);
-    return v >= 0 && v < p.vocab;
-  };
-  if (threadIdx.x == 0) listed = 0;
-  // maximum (a NaN is passed by, and spoils the sum), this thread's best
-  float m = -INFINITY;
-  uint32_t top = 0;
+  // the part's words; none of a beam that has ended
+  auto load = [&](int at, Part &y) {
+    y.there = 0;
+    y.first = INT_MIN;
+    if (at >= p.parts) return;
+    const int row = at / p.splits, split = at - row * p.splits;
+    if (p.done && p.done[row]) return;
+    const E *base = static_cast<const E *>(p.logits) + row * p.row_stride;
+    const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(E));
+    y.first = (split * (BS_T * WORDS) + static_cast<int>(threadIdx.x)) * N - skew;
 #pragma unroll
-  for (int w = 0; w < WORDS; ++w)
+    for (int w = 0; w < WORDS; ++w) {
+      const int v = y.first + w * (BS_T * N);
+      if (v >= 0 && v + N <= p.vocab) {
+        y.x[w] = __ldcs(reinterpret_cast<const uint4 *>(base + v));
+        y.there |= ((1u << N) - 1) << (w * N);
+      } else {
+        uint32_t z[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (there(w, e)) {
-        m = fmaxf(m, x[w * N + e]);
-        top = max(top, key_of(x[w * N + e]));
-      }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) part[warp] = m;
-  const uint32_t least = threshold<BS_T>(top, p.keep, sums);      // has a barrier
-#pragma unroll
-  for (int w = 0; w < BS_T / 32; ++w) m = fmaxf(m, part[w]);
-  __syncthreads();
-  const float mb = m == -INFINITY ? 0.f : m;
-  float s = 0.f;
-#pragma unroll
-  for (int w = 0; w < WORDS; ++w) {
-    float t = 0.f;
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (there(w, e)) {
-        const float y = x[w * N + e];
-        t += ex2_approx((y - mb) * 1.44269504f);
-        if (key_of(y) >= least) {
-          const int at = atomicAdd(&listed, 1);
-          if (at < BS_CAP) {
-            list_k[at] = key_of(y);
-            list_i[at] = static_cast<int>(id_of(w, e));
-          }
+        for (int e = 0; e < N; ++e) {
+          const bool in = v + e >= 0 && v + e < p.vocab;
+          const uint32_t b = in ? Vec<E>::bits(base + v + e) : N == 4 ? 0xff800000u : 0xff80u;
+          z[e * 4 / N] |= N == 4 ? b : b << (16 * (e & 1));
+          y.there |= static_cast<uint32_t>(in) << (w * N + e);
         }
+        y.x[w] = make_uint4(z[0], z[1], z[2], z[3]);
       }
-    s += t;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) part[warp] = s;
-  __syncthreads();
-  const long long at = row * p.splits + split;
-  if (threadIdx.x == 0) {
-    s = 0.f;
-#pragma unroll
-    for (int w = 0; w < BS_T / 32; ++w) s += part[w];
-    p.ms[at] = make_float2(m, s);
-  }
-  uint32_t *keys = p.keys + at * p.keep;
-  int *ids = p.ids + at * p.keep;
-  const int n = listed;
-  if (n <= BS_CAP) {
-    for (int i = threadIdx.x; i < n; i += BS_T) {
-      const uint32_t k = list_k[i];
-      const int id = list_i[i];
-      int rank = 0;
-      for (int j = 0; j < n && rank < p.keep; ++j) rank += before(list_k[j], list_i[j], k, id);
-      if (rank < p.keep) keys[rank] = k, ids[rank] = id;
     }
-    for (int i = n + threadIdx.x; i < p.keep; i += BS_T) ids[i] = -1;
-    return;
-  }
-  uint32_t last_k = 0xffffffffu;
-  int last_i = -1;
-  for (int r = 0; r < p.keep; ++r) {      // more than `keep` values are there
-    uint32_t k = 0;
-    int id = INT_MAX;
+  };
+  Part next;
+  load(blockIdx.x, next);
+  for (int at = blockIdx.x; at < p.parts; at += gridDim.x) {
+    const Part y = next;
+    load(at + gridDim.x, next);
+    if (y.first == INT_MIN) continue;      // for the whole block
+    // maximum (a NaN is passed by, and spoils the sum)
+    float m = -INFINITY;
 #pragma unroll
     for (int w = 0; w < WORDS; ++w)
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const uint32_t a = key_of(x[w * N + e]);
-        const int i = static_cast<int>(id_of(w, e));
-        if (there(w, e) && before(last_k, last_i, a, i) && before(a, i, k, id)) k = a, id = i;
+      for (int e = 0; e < N; e += 2) m = max3f(m, Vec<E>::get(y.x[w], e), Vec<E>::get(y.x[w], e + 1));
+    const uint32_t top = y.there ? key_of(m) : 0u;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) part[0][warp] = m;
+    if (threadIdx.x == 0) listed = 0;
+    const uint32_t least = threshold<BS_T>(top, p.keep, sums);      // has a barrier
+#pragma unroll
+    for (int w = 0; w < BS_T / 32; ++w) m = fmaxf(m, part[0][w]);
+    const float mb = m == -INFINITY ? 0.f : m;
+    const uint64_t nm = f2_make(-mb, -mb), c2 = f2_make(1.44269504f, 1.44269504f);
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w) {
+      float t = 0.f;
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        float a, b;
+        f2_split(f2_mul(f2_add(f2_make(Vec<E>::get(y.x[w], e), Vec<E>::get(y.x[w], e + 1)), nm), c2), a, b);
+        t += ex2_approx(a) + ex2_approx(b);
       }
-    block_best<BS_T>(k, id, sums, reinterpret_cast<int *>(part));
-    if (threadIdx.x == 0) keys[r] = k, ids[r] = id;
-    last_k = k;
-    last_i = id;
+      s += t;
+    }
+    if (top >= least) {
+#pragma unroll
+      for (int w = 0; w < WORDS; ++w)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const uint32_t k = key_of(Vec<E>::get(y.x[w], e));
+          if ((y.there >> (w * N + e) & 1u) && k >= least) {
+            const int to = atomicAdd(&listed, 1);
+            if (to < BS_CAP) {
+              list_k[to] = k;
+              list_i[to] = y.first + w * (BS_T * N) + e;
+            }
+          }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) part[1][warp] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s = 0.f;
+#pragma unroll
+      for (int w = 0; w < BS_T / 32; ++w) s += part[1][w];
+      p.ms[at] = make_float2(m, s);
+    }
+    uint32_t *keys = p.keys + static_cast<long long>(at) * p.keep;
+    int *ids = p.ids + static_cast<long long>(at) * p.keep;
+    const int n = listed;
+    if (n <= BS_CAP) {
+      rank_list<BS_T, uint32_t>(
+          n, p.keep, [&](int a, int b) { return before(list_k[a], list_i[a], list_k[b], list_i[b]); },
+          [&](int rank, int i) { keys[rank] = list_k[i], ids[rank] = list_i[i]; });
+      for (int i = n + threadIdx.x; i < p.keep; i += BS_T) ids[i] = -1;
+    } else {
+      uint32_t last_k = 0xffffffffu;
+      int last_i = -1;
+      for (int r = 0; r < p.keep; ++r) {      // more than `keep` values are there
+        uint32_t k = 0;
+        int id = INT_MAX;
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w)
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const uint32_t a = key_of(Vec<E>::get(y.x[w], e));
+            const int i = y.first + w * (BS_T * N) + e;
+            if ((y.there >> (w * N + e) & 1u) && before(last_k, last_i, a, i) && before(a, i, k, id)) k = a, id = i;
+          }
+        block_best<BS_T>(k, id, sums, parti);
+        if (threadIdx.x == 0) keys[r] = k, ids[r] = id;
+        last_k = k;
+        last_i = id;
+      }
+    }
+    __syncthreads();         // the list and the sums have been read
   }
 }
 
@@ -280,10 +300,10 @@ struct PickParams {
 // those), so that the choice needs no other rule.
 __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
   __shared__ double offset[ATTN_BEAM_MAX];      // score - ln sum; NaN: the beam offers nothing but -inf
-  __shared__ unsigned long long sums[2 * BP_T / 32];
+  __shared__ unsigned long long sums[BP_T / 32];
   __shared__ int isum[BP_T / 32];
   __shared__ unsigned long long list_k[BP_CAP];
-  __shared__ int list_i[BP_CAP];
+  __shared__ int list_b[BP_CAP], list_v[BP_CAP];
   __shared__ int listed;
   after_previous();
   admit_next();
@@ -294,35 +314,46 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
     double c = __longlong_as_double(0x7ff8000000000000ll);
     const float score = p.scores[row];
     if (!(p.done && p.done[row]) && score > -INFINITY && score < INFINITY) {
-      float m = -INFINITY;
-      for (int i = lane; i < p.splits; i += 32) m = fmaxf(m, p.ms[row * p.splits + i].x);
+      // the parts' sums brought to the largest maximum
+      float m = -INFINITY, s = 0.f;
+      for (int i0 = 0; i0 < p.splits; i0 += 32) {
+        const float2 y = i0 + lane < p.splits ? p.ms[row * p.splits + i0 + lane] : make_float2(-INFINITY, 0.f);
+        float top = y.x;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      double s = 0.0;
-      for (int i = lane; i < p.splits; i += 32) {
-        const float2 y = p.ms[row * p.splits + i];
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, m);
+        const float mb = top == -INFINITY ? 0.f : top;
         // a part of -inf alone has the sum 0; one with a NaN keeps it
-        s += y.x == -INFINITY ? static_cast<double>(y.y) * 0.0 : static_cast<double>(y.y) * exp(static_cast<double>(y.x) - static_cast<double>(m));
+        s = s * ex2_approx((m - mb) * 1.44269504f) + y.y * (y.x == -INFINITY ? 0.f : ex2_approx((y.x - mb) * 1.44269504f));
+        m = top;
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      c = static_cast<double>(score) - (static_cast<double>(m) + log(s));
+      // ln s = e ln 2 + ln f with f in [3/4, 3/2): to 2^-24 of 1, not of ln s; few
+      // operations in 64 bits, which take a warp 16 cycles each here
+      const int e = static_cast<int>(__float_as_uint(s) - 0x3f400000u) >> 23;
+      const float f = __uint_as_float(__float_as_uint(s) - (static_cast<uint32_t>(e) << 23));
+      if (s > 0.f && s < INFINITY)
+        c = static_cast<double>(score) - (static_cast<double>(m) + (e * 0.69314718055994530942 + static_cast<double>(log1pf(f - 1.f))));
       if (!(c > -INFINITY && c < INFINITY)) c = __longlong_as_double(0x7ff8000000000000ll);
     }
     if (lane == 0) offset[b] = c;
   }
   __syncthreads();
-  // continuation j: its score as a key (0: none) and its place, kept as beam and token
+  // Continuation j: its score as a key (0: none), beam and token.  Neighbours are of
+  // different beams, and then the parts' best in turn, so that every group of threads has
+  // good ones.
   auto get = [&](int j, unsigned long long &k, int &b, int &v) {
-    b = j / per;
+    const int i = j / p.beams;
+    b = j - i * p.beams;
     const long long row = static_cast<long long>(g) * p.beams + b;
-    const int i = j - b * per;
     const double c = offset[b];
     k = 0;
     v = 0;
     if (c == c) {
       v = p.ids[row * per + i];
-      if (v >= 0) k = key_of(c + static_cast<double>(value_of(p.keys[row * per + i])));
+      const float x = value_of(p.keys[row * per + i]);
+      if (v >= 0) k = key_of(c + static_cast<double>(x));
     } else if (i < p.keep) {
       const float score = p.scores[row];
       const bool ended = p.done && p.done[row] && score > -INFINITY && score < INFINITY;
@@ -335,22 +366,35 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
       }
     }
   };
-  unsigned long long top = 0;
-  for (int j = threadIdx.x; j < n; j += BP_T) {
+  constexpr int HELD = 4;      // a thread's first ones are looked up once
+  unsigned long long hk[HELD], top = 0;
+  int hb[HELD], hv[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    hk[i] = 0;
+    const int j = threadIdx.x + i * BP_T;
+    if (j < n) get(j, hk[i], hb[i], hv[i]);
+    top = hk[i] > top ? hk[i] : top;
+  }
+  for (int j = threadIdx.x + HELD * BP_T; j < n; j += BP_T) {
     unsigned long long k;
     int b, v;
     get(j, k, b, v);
     top = k > top ? k : top;
   }
   const unsigned long long least = threshold<BP_T>(top, p.keep, sums);
-  for (int j = threadIdx.x; j < n; j += BP_T) {
+  auto list = [&](unsigned long long k, int b, int v) {
+    if (k < least) return;
+    const int at = atomicAdd(&listed, 1);
+    if (at < BP_CAP) list_k[at] = k, list_b[at] = b, list_v[at] = v;
+  };
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) list(hk[i], hb[i], hv[i]);
+  for (int j = threadIdx.x + HELD * BP_T; j < n; j += BP_T) {
     unsigned long long k;
     int b, v;
     get(j, k, b, v);
-    if (k >= least && k) {
-      const int at = atomicAdd(&listed, 1);
-      if (at < BP_CAP) list_k[at] = k, list_i[at] = j;
-    }
+    list(k, b, v);
   }
   __syncthreads();
   auto write = [&](int r, unsigned long long k, int b, int v) {
@@ -363,23 +407,12 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
   };
   const int m = listed;
   if (m <= BP_CAP) {
-    for (int i = threadIdx.x; i < m; i += BP_T) {
-      unsigned long long k;
-      int b, v, rank = 0;
-      get(list_i[i], k, b, v);
-      for (int j = 0; j < m && rank < p.keep; ++j) {
-        const unsigned long long a = list_k[j];
-        if (a > k) {
-          ++rank;
-        } else if (a == k && j != i) {
-          unsigned long long y;
-          int c, w;
-          get(list_i[j], y, c, w);
-          rank += c < b || (c == b && w < v);
-        }
-      }
-      if (rank < p.keep) write(rank, k, b, v);
-    }
+    rank_list<BP_T, unsigned long long>(
+        m, p.keep,
+        [&](int x, int y) {
+          return list_k[x] > list_k[y] || (list_k[x] == list_k[y] && (list_b[x] < list_b[y] || (list_b[x] == list_b[y] && list_v[x] < list_v[y])));
+        },
+        [&](int rank, int i) { write(rank, list_k[i], list_b[i], list_v[i]); });
     return;
   }
   unsigned long long last_k = ~0ull;
@@ -411,9 +444,8 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
 
 struct State {
   uint8_t *at;
-  long long stride;          // bytes from row to row
-  long long words;           // of a row
-  int word, first;           // bytes of a word; the state's first unit
+  long long stride, bytes;   // from row to row, of a row
+  int loose, first;          // not in words of 16 bytes; the state's first unit
 };
 struct ReorderParams {
   State s[ATTN_BEAM_MAX_STATES];
@@ -421,58 +453,117 @@ struct ReorderParams {
   int n_states, groups, beams, units;
   unsigned int *status;
 };
-constexpr int RE_T = 256;
+constexpr int RE_T = 256, RE_BUF = 32768;
+// Bytes of a row that a unit moves: a word a thread, or what room there is for all rows.
+__host__ __device__ __forceinline__ int unit_bytes(bool loose, int beams) { return loose ? min(2048, RE_BUF / beams & ~15) : RE_T * 16; }
 
 // All parents' words of one column of a group, then all rows': the column is this
 // thread's alone, so the rows may change places in memory.  Rows that stay are not
 // touched.
-template <typename W, int MOST>
-__device__ __forceinline__ void move_column(const State &s, long long row0, long long word, const int *par, int beams) {
-  W x[MOST];
-  uint8_t *base = s.at + row0 * s.stride + word * sizeof(W);
+template <int MOST>
+__device__ __forceinline__ void move_column(uint8_t *base, long long stride, const int *par, int beams) {
+  uint4 x[MOST];
 #pragma unroll
   for (int b = 0; b < MOST; ++b)
-    if (b < beams && par[b] != b) x[b] = *reinterpret_cast<const W *>(base + par[b] * s.stride);
+    if (b < beams && par[b] != b) x[b] = *reinterpret_cast<const uint4 *>(base + par[b] * stride);
 #pragma unroll
   for (int b = 0; b < MOST; ++b)
-    if (b < beams && par[b] != b) *reinterpret_cast<W *>(base + b * s.stride) = x[b];
+    if (b < beams && par[b] != b) *reinterpret_cast<uint4 *>(base + b * stride) = x[b];
+}
+
+// The same for `n` bytes of rows at any address, or of more than 16 beams, through shared
+// memory: words of 4 bytes where they lie in memory, read as they are and written as two
+// of them shifted into the new row's place (a vocabulary of an odd number of bytes: bytes
+// one by one took four times as long).  Bytes at the ends of the run are moved alone,
+// those outside it neither read nor written.
+__device__ __forceinline__ void move_run(uint8_t *base, long long stride, int n, const int *par, const int *used, int beams, uint32_t *buf) {
+  const int pitch = unit_bytes(true, beams) / 4 + 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = warp; r < beams; r += RE_T / 32) {
+    if (!used[r]) continue;
+    const uint8_t *from = base + r * stride;
+    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 3);
+    for (int j = lane; 4 * j < skew + n; j += 32) {
+      const int t = 4 * j - skew;            // the word's first byte in the run
+      uint32_t w = 0;
+      if (t >= 0 && t + 4 <= n) {
+        w = *reinterpret_cast<const uint32_t *>(from + t);
+      } else {
+        for (int k = 0; k < 4; ++k)
+          if (t + k >= 0 && t + k < n) w |= static_cast<uint32_t>(from[t + k]) << (8 * k);
+      }
+      buf[r * pitch + j] = w;
+    }
+  }
+  __syncthreads();
+  for (int b = warp; b < beams; b += RE_T / 32) {
+    if (par[b] == b) continue;
+    uint8_t *to = base + b * stride;
+    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(to) & 3),
+              off = static_cast<int>(reinterpret_cast<uintptr_t>(base + par[b] * stride) & 3) - skew;
+    const uint32_t *src = buf + par[b] * pitch;
+    for (int j = lane; 4 * j < skew + n; j += 32) {
+      const int t = 4 * j - skew, i = off < 0 ? j - 1 : j;
+      const uint32_t w = __funnelshift_r(src[max(i, 0)], src[i + 1], 8 * (off & 3));
+      if (t >= 0 && t + 4 <= n) {
+        *reinterpret_cast<uint32_t *>(to + t) = w;
+      } else {
+        for (int k = 0; k < 4; ++k)
+          if (t + k >= 0 && t + k < n) to[t + k] = static_cast<uint8_t>(w >> (8 * k));
+      }
+    }
+  }
 }
 
 template <int MOST>
 __global__ void __launch_bounds__(RE_T) beam_reorder_kernel(const __grid_constant__ ReorderParams p) {
-  __shared__ int par[ATTN_BEAM_MAX];
+  __shared__ int par[ATTN_BEAM_MAX], used[ATTN_BEAM_MAX];
+  __shared__ uint32_t buf[RE_BUF / 4 + 2 * ATTN_BEAM_MAX];
   after_previous();
   admit_next();
   int s = 0;
   for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
     while (s + 1 < p.n_states && u >= p.s[s + 1].first) ++s;
     const State &st = p.s[s];
-    const int per = static_cast<int>((st.words + RE_T - 1) / RE_T), g = (u - st.first) / per;
-    const long long word = static_cast<long long>(u - st.first - g * per) * RE_T + threadIdx.x, row0 = static_cast<long long>(g) * p.beams;
+    const int each = unit_bytes(st.loose, p.beams);
+    const long long per = (st.bytes + each - 1) / each, g = (u - st.first) / per, row0 = g * p.beams;
+    const long long at = (u - st.first - g * per) * each;
     __syncthreads();
+    const int b = threadIdx.x;
     int off = 0;
-    if (threadIdx.x < static_cast<unsigned>(p.beams)) {
-      const long long a = p.parents[row0 + threadIdx.x] - row0;
+    if (b < p.beams) {
+      const long long a = p.parents[row0 + b] - row0;
       off = a < 0 || a >= p.beams;
-      par[threadIdx.x] = off ? static_cast<int>(threadIdx.x) : static_cast<int>(a);
+      par[b] = off ? b : static_cast<int>(a);
+      used[b] = 0;
     }
     if (__syncthreads_or(off)) {
       if (threadIdx.x == 0) atomicCAS(p.status, 0u, static_cast<unsigned>(ATTN_ERR_INVALID_ARG));
       continue;
     }
-    if (word >= st.words) continue;
-    if (MOST <= 16 && st.word == 16) move_column<uint4, MOST <= 16 ? MOST : 1>(st, row0, word, par, p.beams);
-    else if (st.word == 4) move_column<uint32_t, MOST>(st, row0, word, par, p.beams);
-    else move_column<uint8_t, MOST>(st, row0, word, par, p.beams);
+    uint8_t *base = st.at + row0 * st.stride + at;
+    if (!st.loose) {
+      if (at + 16 * threadIdx.x < st.bytes) move_column<MOST>(base + 16 * threadIdx.x, st.stride, par, p.beams);
+    } else {
+      if (b < p.beams && par[b] != b) used[par[b]] = 1;
+      __syncthreads();
+      move_run(base, st.stride, static_cast<int>(min(static_cast<long long>(each), st.bytes - at)), par, used, p.beams, buf);
+    }
   }
 }
 
-int splits_of(int rows, int vocab, int dtype, int *per) {
-  // 8 values a thread where 32 would leave SMs without a block
+// Parts of a row: of 4 words of 16 bytes a thread, or 1 where those would leave SMs
+// without a block.
+int splits_of(int rows, int vocab, int dtype, int sms, int *words) {
   const int n = dtype == ATTN_DTYPE_F32 ? 4 : 8;
-  auto parts = [&](int each) { return static_cast<int>((static_cast<long long>(vocab) + n - 1 + BS_T * each - 1) / (BS_T * each)); };
-  *per = static_cast<long long>(rows) * parts(32) >= 2 * 152 ? 32 : 8;
-  return parts(*per);
+  auto parts = [&](int w) { return static_cast<int>((static_cast<long long>(vocab) + n - 1 + BS_T * w * n - 1) / (BS_T * w * n)); };
+  *words = static_cast<long long>(rows) * parts(4) >= 2 * sms ? 4 : 1;
+  return parts(*words);
+}
+
+int check_beams(int groups, int beams, int vocab, int keep) {
+  if (groups < 0 || beams < 1 || vocab < 1 || keep < 1) return ATTN_ERR_INVALID_ARG;
+  if (beams > ATTN_BEAM_MAX || keep > ATTN_BEAM_MAX || static_cast<int64_t>(groups) * beams >= (1 << 24) || vocab > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -485,12 +576,15 @@ using namespace attn;
 extern "C" {
 
 int attn_beam_workspace_bytes(int groups, int beams, int vocab, int keep, size_t *bytes) {
-  if (!bytes || groups < 0 || beams < 1 || vocab < 1 || keep < 1) return ATTN_ERR_INVALID_ARG;
-  if (beams > ATTN_BEAM_MAX || keep > ATTN_BEAM_MAX || static_cast<int64_t>(groups) * beams >= (1 << 24)) return ATTN_ERR_UNSUPPORTED;
+  if (!bytes) return ATTN_ERR_INVALID_ARG;
+  const int rc = check_beams(groups, beams, vocab, keep);
+  if (rc != ATTN_OK) return rc;
+  const int sms = device_sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
   size_t most = 0;
   for (int dtype : {ATTN_DTYPE_F32, ATTN_DTYPE_BF16}) {
-    int per;
-    const size_t parts = static_cast<size_t>(groups) * beams * splits_of(groups * beams, vocab, dtype, &per);
+    int words;
+    const size_t parts = static_cast<size_t>(groups) * beams * splits_of(groups * beams, vocab, dtype, sms, &words);
     const size_t need = up256(parts * 8) + 2 * up256(parts * keep * 4);
     most = need > most ? need : most;
   }
@@ -502,8 +596,7 @@ int attn_beam_select(const void *logits, int logits_dtype, int64_t row_stride, i
                      const uint8_t *done, int eos, const int32_t *slots, int keep, float *out_scores, int32_t *out_parents,
                      int32_t *out_tokens, uint8_t *out_done, int32_t *out_src, void *d_ws, size_t ws_bytes, attn_stream_t stream) {
   if (logits_dtype != ATTN_DTYPE_F32 && logits_dtype != ATTN_DTYPE_BF16) return ATTN_ERR_INVALID_ARG;
-  size_t need = 0;
-  int rc = attn_beam_workspace_bytes(groups, beams, vocab, keep, &need);
+  int rc = check_beams(groups, beams, vocab, keep);
   if (rc != ATTN_OK) return rc;
   if (static_cast<int64_t>(beams) * vocab < keep || eos < -1 || eos >= vocab || (done && eos < 0)) return ATTN_ERR_INVALID_ARG;
   if (row_stride < vocab) return ATTN_ERR_INVALID_ARG;
@@ -514,21 +607,26 @@ int attn_beam_select(const void *logits, int logits_dtype, int64_t row_stride, i
   if (off(logits, esize) || off(scores, 4) || off(slots, 4) || off(out_scores, 4) || off(out_parents, 4) || off(out_tokens, 4) ||
       off(out_src, 4) || off(d_ws, 16))
     return ATTN_ERR_UNSUPPORTED;
+  size_t need = 0;
+  if ((rc = attn_beam_workspace_bytes(groups, beams, vocab, keep, &need)) != ATTN_OK) return rc;
   if (ws_bytes < need) return ATTN_ERR_CAPACITY;
   const int rows = groups * beams;
-  int per;
-  const int splits = splits_of(rows, vocab, logits_dtype, &per);
+  const int sms = device_sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  int words;
+  const int splits = splits_of(rows, vocab, logits_dtype, sms, &words);
   const size_t parts = static_cast<size_t>(rows) * splits;
-  if (parts >= (size_t(1) << 31) || static_cast<int64_t>(beams) * splits * keep >= INT_MAX) return ATTN_ERR_UNSUPPORTED;
+  if (parts >= (size_t(1) << 30) || static_cast<int64_t>(beams) * splits * keep >= INT_MAX) return ATTN_ERR_UNSUPPORTED;
   uint8_t *ws = static_cast<uint8_t *>(d_ws);
   float2 *ms = reinterpret_cast<float2 *>(ws);
   uint32_t *keys = reinterpret_cast<uint32_t *>(ws + up256(parts * 8));
   int *ids = reinterpret_cast<int *>(ws + up256(parts * 8) + up256(parts * keep * 4));
-  const ScanParams sp{logits, done, row_stride, vocab, splits, keep, ms, keys, ids};
+  const ScanParams sp{logits, done, row_stride, vocab, splits, keep, static_cast<int>(parts), ms, keys, ids};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto scan = logits_dtype == ATTN_DTYPE_F32 ? (per == 32 ? beam_scan_kernel<float, 32> : beam_scan_kernel<float, 8>)
-                                             : (per == 32 ? beam_scan_kernel<uint16_t, 32> : beam_scan_kernel<uint16_t, 8>);
-  if ((rc = launch_after(scan, dim3(static_cast<unsigned>(parts)), BS_T, 0, s, sp)) != ATTN_OK) return rc;
+  auto scan = logits_dtype == ATTN_DTYPE_F32 ? (words == 4 ? beam_scan_kernel<float, 4> : beam_scan_kernel<float, 1>)
+                                             : (words == 4 ? beam_scan_kernel<uint16_t, 4> : beam_scan_kernel<uint16_t, 1>);
+  const size_t grid = std::min<size_t>(parts, static_cast<size_t>(sms) * 4);
+  if ((rc = launch_after(scan, dim3(static_cast<unsigned>(grid)), BS_T, 0, s, sp)) != ATTN_OK) return rc;
   const PickParams pp{scores, done, slots, ms, keys, ids, beams, vocab, splits, keep, eos, out_scores, out_parents, out_tokens, out_src, out_done};
   return launch_after(beam_pick_kernel, dim3(groups), BP_T, 0, s, pp);
 }
@@ -548,9 +646,10 @@ int attn_beam_reorder(void *const *h_states, const int64_t *h_row_bytes, const i
     if (bytes == 0 || groups == 0) continue;
     if (!h_states[i]) return ATTN_ERR_INVALID_ARG;
     const uint64_t all = reinterpret_cast<uintptr_t>(h_states[i]) | static_cast<uint64_t>(bytes) | static_cast<uint64_t>(stride);
-    const int word = !(all & 15) && beams <= 16 ? 16 : !(all & 3) ? 4 : 1;
-    p.s[p.n_states++] = State{static_cast<uint8_t *>(h_states[i]), stride, bytes / word, word, static_cast<int>(units)};
-    units += (bytes / word + RE_T - 1) / RE_T * groups;
+    const int loose = (all & 15) || beams > 16;
+    const int64_t each = unit_bytes(loose, beams);
+    p.s[p.n_states++] = State{static_cast<uint8_t *>(h_states[i]), stride, bytes, loose, static_cast<int>(units)};
+    units += (bytes + each - 1) / each * groups;
     if (units >= INT_MAX) return ATTN_ERR_UNSUPPORTED;
   }
   if (units == 0) return ATTN_OK;
@@ -561,7 +660,7 @@ int attn_beam_reorder(void *const *h_states, const int64_t *h_row_bytes, const i
   if (!(p.status = paged_status())) return ATTN_ERR_CUDA;
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  auto kern = beams <= 4 ? beam_reorder_kernel<4> : beams <= 8 ? beam_reorder_kernel<8> : beams <= 16 ? beam_reorder_kernel<16> : beam_reorder_kernel<64>;
+  auto kern = beams <= 4 ? beam_reorder_kernel<4> : beams <= 8 ? beam_reorder_kernel<8> : beam_reorder_kernel<16>;
   const int64_t grid = sms * 16;
   return launch_after(kern, dim3(static_cast<unsigned>(units < grid ? units : grid)), RE_T, 0, reinterpret_cast<cudaStream_t>(stream), p);
 }

@@ -46,8 +46,8 @@ int attn_beam_workspace_bytes(int groups, int beams, int vocab, int keep, size_t
  * beam does not offer) has the score -inf and stands behind all others, by its
  * place as well.  groups = 0 does nothing.
  * Errors: INVALID_ARG (keep > beams * vocab, eos >= vocab, null arrays, ..);
- * UNSUPPORTED (beams or keep > ATTN_BEAM_MAX, groups * beams >= 2^24, alignment
- * of an array to its elements, of d_ws to 16); CAPACITY (ws_bytes); CUDA. */
+ * UNSUPPORTED (beams or keep > ATTN_BEAM_MAX, groups * beams >= 2^24, vocab >
+ * 2^30, alignment of an array to its elements, of d_ws to 16); CAPACITY (ws_bytes); CUDA. */
 int attn_beam_select(const void *logits, int logits_dtype, int64_t row_stride, int groups, int beams,
                      int vocab, const float *scores, const uint8_t *done, int eos, const int32_t *slots,
                      int keep, float *out_scores, int32_t *out_parents, int32_t *out_tokens,

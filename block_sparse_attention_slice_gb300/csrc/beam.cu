@@ -33,7 +33,8 @@ namespace attn {
 namespace {
 
 constexpr int BS_T = 256;            // threads of a scanning block
-constexpr int BS_CAP = 2048;         // places of its list
+constexpr int BS_CAP = 1024;         // places of its list
+constexpr int BS_WORDS = 512;        // and of that of its words
 constexpr int BP_T = 256;            // of a choosing block
 constexpr int BP_CAP = 1024;
 
@@ -46,33 +47,46 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 __device__ __forceinline__ unsigned long long key_of(double x) {
-  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
-  return (b >> 63) ? ~b : b | 1ull << 63;
+  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x)), top = 1ull << 63;
+  return b >= top ? b == top ? top : ~b : b | top;
 }
 __device__ __forceinline__ double value_of(unsigned long long k) {
   return __longlong_as_double(static_cast<long long>((k >> 63) ? k ^ 1ull << 63 : ~k));
 }
 
 // A key, not 0, that at least min(keep, keys there are) of the block's keys reach, given
-// the largest of each thread's (0: none); keep <= 64.  `sums` has a place a warp.
+// the largest of each thread's (0: none), of which the first `active` have some;
+// keep <= 64.  `sums` has a place a warp.
 template <int T, typename K>
-__device__ __forceinline__ K threshold(K top, int keep, K *sums) {
+__device__ __forceinline__ K threshold(K top, int keep, int active, K *sums) {
   // groups of as many threads as leave `keep` of them, a warp at most
   int width = 32;
-  while (width > 1 && T / width < keep) width >>= 1;
-  for (int o = 1; o < width; o <<= 1) {
-    const K a = __shfl_xor_sync(0xffffffffu, top, o);
-    top = a > top ? a : top;
+  while (width > 1 && active < keep * width) width >>= 1;
+  const int lane = threadIdx.x & 31;
+  if constexpr (sizeof(K) == 4) {
+    top = __reduce_max_sync(width == 32 ? 0xffffffffu : ((1u << width) - 1) << (lane & ~(width - 1)), top);
+  } else {
+    for (int o = 1; o < width; o <<= 1) {
+      const K a = __shfl_xor_sync(0xffffffffu, top, o);
+      top = a > top ? a : top;
+    }
   }
-  for (int o = width; o < 32; o <<= 1) {
-    const K a = __shfl_xor_sync(0xffffffffu, top, o);
-    top = a < top ? a : top;
+  if (static_cast<int>(threadIdx.x & ~(width - 1)) >= active) top = ~K(0);
+  if (width < 32) {
+    if constexpr (sizeof(K) == 4) {
+      top = __reduce_min_sync(0xffffffffu, top);
+    } else {
+      for (int o = width; o < 32; o <<= 1) {
+        const K a = __shfl_xor_sync(0xffffffffu, top, o);
+        top = a < top ? a : top;
+      }
+    }
   }
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = top;
+  if (lane == 0) sums[threadIdx.x >> 5] = top;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < T / 32; ++w) top = sums[w] < top ? sums[w] : top;
-  return top < 1 ? 1 : top;
+  return top < 1 || active < keep ? 1 : top;
 }
 
 // Whether (a, i) stands before (b, j).
@@ -105,6 +119,11 @@ __device__ __forceinline__ void rank_list(int n, int keep, B stands_before, W wr
   const int lane = threadIdx.x & 31;
   for (int i = threadIdx.x >> 5; i < n; i += T / 32) {
     int rank = 0;
+    if (n <= 32) {
+      rank = __popc(__ballot_sync(0xffffffffu, lane < n && stands_before(lane, i)));
+      if (lane == 0 && rank < keep) write(rank, i);
+      continue;
+    }
     for (int j0 = 0; j0 < n && rank < keep; j0 += 32) rank += __popc(__ballot_sync(0xffffffffu, j0 + lane < n && stands_before(j0 + lane, i)));
     if (lane == 0 && rank < keep) write(rank, i);
   }
@@ -114,7 +133,7 @@ struct ScanParams {
   const void *logits;
   const uint8_t *done;
   long long row_stride;      // elements
-  int vocab, splits, keep, parts;       // parts: of all rows
+  int vocab, splits, keep, words, rest, parts;       // a part: `words` 16-byte words, the first `rest` of a row one more; parts: of all rows
   float2 *ms;                // [rows][splits]: maximum, sum of exp(x - maximum)
   uint32_t *keys;            // [rows][splits][keep], best first
   int *ids;                  // their tokens; -1: none
@@ -129,6 +148,7 @@ struct Vec<float> {
     return __uint_as_float(e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w);
   }
   static __device__ __forceinline__ uint32_t bits(const float *p) { return __float_as_uint(*p); }
+  static __device__ __forceinline__ float top(const uint4 &w) { return fmaxf(max3f(get(w, 0), get(w, 1), get(w, 2)), get(w, 3)); }
 };
 template <>
 struct Vec<uint16_t> {
@@ -138,6 +158,13 @@ struct Vec<uint16_t> {
     return __uint_as_float(e & 1 ? y & 0xffff0000u : y << 16);
   }
   static __device__ __forceinline__ uint32_t bits(const uint16_t *p) { return *p; }
+  static __device__ __forceinline__ float top(const uint4 &w) {
+    uint32_t a, b;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w.z), "r"(w.w));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  }
 };
 
 // A block takes part after part, the next one's words on their way while it works on one
@@ -149,35 +176,48 @@ template <typename E, int WORDS>
 __global__ void __launch_bounds__(BS_T, 4) beam_scan_kernel(const ScanParams p) {
   constexpr int N = Vec<E>::N;
   __shared__ uint32_t sums[BS_T / 32];
-  __shared__ float part[2][BS_T / 32];
+  __shared__ uint32_t tops[BS_T / 32];
+  __shared__ float part[BS_T / 32];
   __shared__ int parti[BS_T / 32];
   __shared__ uint32_t list_k[BS_CAP];
   __shared__ int list_i[BS_CAP];
-  __shared__ int listed;
+  __shared__ __align__(16) uint4 words_x[BS_WORDS];       // words that reach the threshold, and their first numbers
+  __shared__ int words_i[BS_WORDS];
+  __shared__ int listed, noted;
   after_previous();
   admit_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   struct Part {
     uint4 x[WORDS];
-    uint32_t there;          // bit w * N + e: the value is the row's
     int first;               // word w begins with number first + w * BS_T * N of the row
+    int words;
+    bool last;               // of its row
   };
   // the part's words; none of a beam that has ended
   auto load = [&](int at, Part &y) {
-    y.there = 0;
     y.first = INT_MIN;
     if (at >= p.parts) return;
     const int row = at / p.splits, split = at - row * p.splits;
     if (p.done && p.done[row]) return;
     const E *base = static_cast<const E *>(p.logits) + row * p.row_stride;
     const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(E));
-    y.first = (split * (BS_T * WORDS) + static_cast<int>(threadIdx.x)) * N - skew;
+    y.words = p.words + (split < p.rest);
+    y.last = split + 1 == p.splits;
+    y.first = (split * p.words + min(split, p.rest) + static_cast<int>(threadIdx.x)) * N - skew;
+    if (split > 0 && !y.last) {            // all of its words are whole
+#pragma unroll
+      for (int w = 0; w < WORDS; ++w) {
+        constexpr uint32_t none = N == 4 ? 0xff800000u : 0xff80ff80u;
+        y.x[w] = make_uint4(none, none, none, none);
+        if (w * BS_T + static_cast<int>(threadIdx.x) < y.words) y.x[w] = __ldcs(reinterpret_cast<const uint4 *>(base + y.first + w * (BS_T * N)));
+      }
+      return;
+    }
 #pragma unroll
     for (int w = 0; w < WORDS; ++w) {
-      const int v = y.first + w * (BS_T * N);
+      const int v = w * BS_T + static_cast<int>(threadIdx.x) < y.words ? y.first + w * (BS_T * N) : p.vocab;
       if (v >= 0 && v + N <= p.vocab) {
         y.x[w] = __ldcs(reinterpret_cast<const uint4 *>(base + v));
-        y.there |= ((1u << N) - 1) << (w * N);
       } else {
         uint32_t z[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -185,7 +225,6 @@ __global__ void __launch_bounds__(BS_T, 4) beam_scan_kernel(const ScanParams p) 
           const bool in = v + e >= 0 && v + e < p.vocab;
           const uint32_t b = in ? Vec<E>::bits(base + v + e) : N == 4 ? 0xff800000u : 0xff80u;
           z[e * 4 / N] |= N == 4 ? b : b << (16 * (e & 1));
-          y.there |= static_cast<uint32_t>(in) << (w * N + e);
         }
         y.x[w] = make_uint4(z[0], z[1], z[2], z[3]);
       }
@@ -198,62 +237,73 @@ __global__ void __launch_bounds__(BS_T, 4) beam_scan_kernel(const ScanParams p) 
     load(at + gridDim.x, next);
     if (y.first == INT_MIN) continue;      // for the whole block
     // maximum (a NaN is passed by, and spoils the sum)
-    float m = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < WORDS; ++w)
-#pragma unroll
-      for (int e = 0; e < N; e += 2) m = max3f(m, Vec<E>::get(y.x[w], e), Vec<E>::get(y.x[w], e + 1));
-    const uint32_t top = y.there ? key_of(m) : 0u;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) part[0][warp] = m;
-    if (threadIdx.x == 0) listed = 0;
-    const uint32_t least = threshold<BS_T>(top, p.keep, sums);      // has a barrier
-#pragma unroll
-    for (int w = 0; w < BS_T / 32; ++w) m = fmaxf(m, part[0][w]);
-    const float mb = m == -INFINITY ? 0.f : m;
-    const uint64_t nm = f2_make(-mb, -mb), c2 = f2_make(1.44269504f, 1.44269504f);
-    float s = 0.f;
+    float mw[WORDS], m = -INFINITY;
 #pragma unroll
     for (int w = 0; w < WORDS; ++w) {
-      float t = 0.f;
+      mw[w] = Vec<E>::top(y.x[w]);
+      m = fmaxf(m, mw[w]);
+    }
+    const uint32_t top = static_cast<int>(threadIdx.x) < y.words && y.first < p.vocab ? key_of(m) : 0u;
+    if (threadIdx.x == 0) listed = noted = 0;
+    const uint32_t warp_top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) tops[warp] = warp_top;
+    // the row's last word may hold none of its values
+    const uint32_t least = threshold<BS_T>(top, p.keep, min(BS_T, y.words - y.last), sums);      // has a barrier
+    uint32_t most = tops[0];
+#pragma unroll
+    for (int w = 1; w < BS_T / 32; ++w) most = max(most, tops[w]);
+    m = value_of(most);
+    const float mb = m == -INFINITY ? 0.f : m;
+    const uint64_t nm = f2_make(-mb, -mb), c2 = f2_make(1.44269504f, 1.44269504f);
+    // every group has a thread that reaches the threshold, so every warp: the words that
+    // do are noted, and looked into by all threads together
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w)
+      if (key_of(mw[w]) >= least) {
+        const int to = atomicAdd(&noted, 1);
+        if (to < BS_WORDS) words_x[to] = y.x[w], words_i[to] = y.first + w * (BS_T * N);
+      }
+    uint64_t s2 = 0ull;
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w) {
+      uint64_t t2 = 0ull;
 #pragma unroll
       for (int e = 0; e < N; e += 2) {
         float a, b;
         f2_split(f2_mul(f2_add(f2_make(Vec<E>::get(y.x[w], e), Vec<E>::get(y.x[w], e + 1)), nm), c2), a, b);
-        t += ex2_approx(a) + ex2_approx(b);
+        t2 = f2_add(t2, f2_make(ex2_approx(a), ex2_approx(b)));
       }
-      s += t;
+      s2 = f2_add(s2, t2);
     }
-    if (top >= least) {
-#pragma unroll
-      for (int w = 0; w < WORDS; ++w)
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const uint32_t k = key_of(Vec<E>::get(y.x[w], e));
-          if ((y.there >> (w * N + e) & 1u) && k >= least) {
-            const int to = atomicAdd(&listed, 1);
-            if (to < BS_CAP) {
-              list_k[to] = k;
-              list_i[to] = y.first + w * (BS_T * N) + e;
-            }
-          }
-        }
-    }
+    float s, s1;
+    f2_split(s2, s, s1);
+    s += s1;
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) part[1][warp] = s;
+    if (lane == 0) part[warp] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
       s = 0.f;
 #pragma unroll
-      for (int w = 0; w < BS_T / 32; ++w) s += part[1][w];
+      for (int w = 0; w < BS_T / 32; ++w) s += part[w];
       p.ms[at] = make_float2(m, s);
     }
+    if (noted <= BS_WORDS) {
+      for (int i = threadIdx.x; i < noted * N; i += BS_T) {
+        const E *x = reinterpret_cast<const E *>(words_x);
+        const int id = words_i[i / N] + i % N;
+        const uint32_t b = Vec<E>::bits(x + i), k = key_of(__uint_as_float(N == 4 ? b : b << 16));
+        if (id >= 0 && id < p.vocab && k >= least) {
+          const int to = atomicAdd(&listed, 1);
+          if (to < BS_CAP) list_k[to] = k, list_i[to] = id;
+        }
+      }
+    }
+    __syncthreads();
     uint32_t *keys = p.keys + static_cast<long long>(at) * p.keep;
     int *ids = p.ids + static_cast<long long>(at) * p.keep;
     const int n = listed;
-    if (n <= BS_CAP) {
+    if (noted <= BS_WORDS && n <= BS_CAP) {
       rank_list<BS_T, uint32_t>(
           n, p.keep, [&](int a, int b) { return before(list_k[a], list_i[a], list_k[b], list_i[b]); },
           [&](int rank, int i) { keys[rank] = list_k[i], ids[rank] = list_i[i]; });
@@ -261,7 +311,7 @@ __global__ void __launch_bounds__(BS_T, 4) beam_scan_kernel(const ScanParams p) 
     } else {
       uint32_t last_k = 0xffffffffu;
       int last_i = -1;
-      for (int r = 0; r < p.keep; ++r) {      // more than `keep` values are there
+      for (int r = 0; r < p.keep; ++r) {
         uint32_t k = 0;
         int id = INT_MAX;
 #pragma unroll
@@ -270,10 +320,10 @@ __global__ void __launch_bounds__(BS_T, 4) beam_scan_kernel(const ScanParams p) 
           for (int e = 0; e < N; ++e) {
             const uint32_t a = key_of(Vec<E>::get(y.x[w], e));
             const int i = y.first + w * (BS_T * N) + e;
-            if ((y.there >> (w * N + e) & 1u) && before(last_k, last_i, a, i) && before(a, i, k, id)) k = a, id = i;
+            if (i >= 0 && i < p.vocab && before(last_k, last_i, a, i) && before(a, i, k, id)) k = a, id = i;
           }
         block_best<BS_T>(k, id, sums, parti);
-        if (threadIdx.x == 0) keys[r] = k, ids[r] = id;
+        if (threadIdx.x == 0) keys[r] = k, ids[r] = k ? id : -1;
         last_k = k;
         last_i = id;
       }
@@ -309,6 +359,33 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
   admit_next();
   const int g = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = p.splits * p.keep, n = p.beams * per;
   if (threadIdx.x == 0) listed = 0;
+  // a thread's first candidates are on their way while the beams' sums are made
+  // In the order beam, part, rank: neighbours are of different beams and parts, so that
+  // every group of threads has good ones.
+  auto entry = [&](int c) { return (c % p.splits) * p.keep + c / p.splits; };
+  constexpr int HELD = 4;
+  int hb[HELD], hv[HELD];
+  uint32_t hx[HELD];
+  int hc[HELD];
+  const int c_step = BP_T / p.beams, b_step = BP_T - c_step * p.beams;
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    if (i == 0) {
+      hc[0] = threadIdx.x / p.beams;
+      hb[0] = threadIdx.x - hc[0] * p.beams;
+    } else {
+      const int b = hb[i - 1] + b_step;
+      hb[i] = b - (b >= p.beams ? p.beams : 0);
+      hc[i] = hc[i - 1] + c_step + (b >= p.beams);
+    }
+    hv[i] = -1;
+    hx[i] = 0;
+    if (static_cast<int>(threadIdx.x) + i * BP_T < n) {
+      const long long at = (static_cast<long long>(g) * p.beams + hb[i]) * per + entry(hc[i]);
+      hv[i] = p.ids[at];
+      hx[i] = p.keys[at];
+    }
+  }
   for (int b = warp; b < p.beams; b += BP_T / 32) {
     const long long row = static_cast<long long>(g) * p.beams + b;
     double c = __longlong_as_double(0x7ff8000000000000ll);
@@ -340,21 +417,13 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
     if (lane == 0) offset[b] = c;
   }
   __syncthreads();
-  // Continuation j: its score as a key (0: none), beam and token.  Neighbours are of
-  // different beams, and then the parts' best in turn, so that every group of threads has
-  // good ones.
-  auto get = [&](int j, unsigned long long &k, int &b, int &v) {
-    const int i = j / p.beams;
-    b = j - i * p.beams;
+  // Continuation j: its score as a key (0: none), beam and token.
+  auto score_of = [&](int i, int b, uint32_t x, int &v) -> unsigned long long {
     const long long row = static_cast<long long>(g) * p.beams + b;
     const double c = offset[b];
-    k = 0;
-    v = 0;
-    if (c == c) {
-      v = p.ids[row * per + i];
-      const float x = value_of(p.keys[row * per + i]);
-      if (v >= 0) k = key_of(c + static_cast<double>(x));
-    } else if (i < p.keep) {
+    if (c == c) return v >= 0 ? key_of(c + static_cast<double>(value_of(x))) : 0ull;
+    unsigned long long k = 0;
+    if (i < p.keep) {
       const float score = p.scores[row];
       const bool ended = p.done && p.done[row] && score > -INFINITY && score < INFINITY;
       if (ended && i == 0) {
@@ -365,15 +434,19 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
         if (v < p.vocab) k = key_of(-static_cast<double>(INFINITY));
       }
     }
+    return k;
   };
-  constexpr int HELD = 4;      // a thread's first ones are looked up once
+  auto get = [&](int j, unsigned long long &k, int &b, int &v) {
+    const int i = j / p.beams;
+    b = j - i * p.beams;
+    const long long at = (static_cast<long long>(g) * p.beams + b) * per + entry(i);
+    v = p.ids[at];
+    k = score_of(i, b, p.keys[at], v);
+  };
   unsigned long long hk[HELD], top = 0;
-  int hb[HELD], hv[HELD];
 #pragma unroll
   for (int i = 0; i < HELD; ++i) {
-    hk[i] = 0;
-    const int j = threadIdx.x + i * BP_T;
-    if (j < n) get(j, hk[i], hb[i], hv[i]);
+    hk[i] = static_cast<int>(threadIdx.x) + i * BP_T < n ? score_of(hc[i], hb[i], hx[i], hv[i]) : 0ull;
     top = hk[i] > top ? hk[i] : top;
   }
   for (int j = threadIdx.x + HELD * BP_T; j < n; j += BP_T) {
@@ -382,7 +455,7 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
     get(j, k, b, v);
     top = k > top ? k : top;
   }
-  const unsigned long long least = threshold<BP_T>(top, p.keep, sums);
+  const unsigned long long least = threshold<BP_T>(top, p.keep, min(BP_T, n), sums);
   auto list = [&](unsigned long long k, int b, int v) {
     if (k < least) return;
     const int at = atomicAdd(&listed, 1);
@@ -553,11 +626,13 @@ __global__ void __launch_bounds__(RE_T) beam_reorder_kernel(const __grid_constan
 
 // Parts of a row: of 4 words of 16 bytes a thread, or 1 where those would leave SMs
 // without a block.
-int splits_of(int rows, int vocab, int dtype, int sms, int *words) {
+// words: of a row, wherever it begins.
+int splits_of(int rows, int vocab, int dtype, int sms, int *each, int *words) {
   const int n = dtype == ATTN_DTYPE_F32 ? 4 : 8;
-  auto parts = [&](int w) { return static_cast<int>((static_cast<long long>(vocab) + n - 1 + BS_T * w * n - 1) / (BS_T * w * n)); };
-  *words = static_cast<long long>(rows) * parts(4) >= 2 * sms ? 4 : 1;
-  return parts(*words);
+  *words = (vocab + 2 * n - 2) / n;
+  auto parts = [&](int w) { return (*words + BS_T * w - 1) / (BS_T * w); };
+  *each = static_cast<long long>(rows) * parts(4) >= 2 * sms ? 4 : 1;
+  return parts(*each);
 }
 
 int check_beams(int groups, int beams, int vocab, int keep) {
@@ -583,8 +658,8 @@ int attn_beam_workspace_bytes(int groups, int beams, int vocab, int keep, size_t
   if (sms <= 0) return ATTN_ERR_CUDA;
   size_t most = 0;
   for (int dtype : {ATTN_DTYPE_F32, ATTN_DTYPE_BF16}) {
-    int words;
-    const size_t parts = static_cast<size_t>(groups) * beams * splits_of(groups * beams, vocab, dtype, sms, &words);
+    int each, words;
+    const size_t parts = static_cast<size_t>(groups) * beams * splits_of(groups * beams, vocab, dtype, sms, &each, &words);
     const size_t need = up256(parts * 8) + 2 * up256(parts * keep * 4);
     most = need > most ? need : most;
   }
@@ -613,18 +688,18 @@ int attn_beam_select(const void *logits, int logits_dtype, int64_t row_stride, i
   const int rows = groups * beams;
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  int words;
-  const int splits = splits_of(rows, vocab, logits_dtype, sms, &words);
+  int each, words;
+  const int splits = splits_of(rows, vocab, logits_dtype, sms, &each, &words);
   const size_t parts = static_cast<size_t>(rows) * splits;
   if (parts >= (size_t(1) << 30) || static_cast<int64_t>(beams) * splits * keep >= INT_MAX) return ATTN_ERR_UNSUPPORTED;
   uint8_t *ws = static_cast<uint8_t *>(d_ws);
   float2 *ms = reinterpret_cast<float2 *>(ws);
   uint32_t *keys = reinterpret_cast<uint32_t *>(ws + up256(parts * 8));
   int *ids = reinterpret_cast<int *>(ws + up256(parts * 8) + up256(parts * keep * 4));
-  const ScanParams sp{logits, done, row_stride, vocab, splits, keep, static_cast<int>(parts), ms, keys, ids};
+  const ScanParams sp{logits, done, row_stride, vocab, splits, keep, words / splits, words % splits, static_cast<int>(parts), ms, keys, ids};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto scan = logits_dtype == ATTN_DTYPE_F32 ? (words == 4 ? beam_scan_kernel<float, 4> : beam_scan_kernel<float, 1>)
-                                             : (words == 4 ? beam_scan_kernel<uint16_t, 4> : beam_scan_kernel<uint16_t, 1>);
+  auto scan = logits_dtype == ATTN_DTYPE_F32 ? (each == 4 ? beam_scan_kernel<float, 4> : beam_scan_kernel<float, 1>)
+                                             : (each == 4 ? beam_scan_kernel<uint16_t, 4> : beam_scan_kernel<uint16_t, 1>);
   const size_t grid = std::min<size_t>(parts, static_cast<size_t>(sms) * 4);
   if ((rc = launch_after(scan, dim3(static_cast<unsigned>(grid)), BS_T, 0, s, sp)) != ATTN_OK) return rc;
   const PickParams pp{scores, done, slots, ms, keys, ids, beams, vocab, splits, keep, eos, out_scores, out_parents, out_tokens, out_src, out_done};

@@ -152,10 +152,11 @@ PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, co
 }
 
 // Items of up to 16 rows (query heads of one key/value head times tokens) go to
-// the warp-level kernel, larger ones to the tensor-core tiles.  What the kernel
+// the warp-level kernel, larger ones to the tensor-core tiles; of codes up to 32, in
+// two passes over the keys (RULE).  What the kernel
 // chose is left in p and, the rows of a piece, in `tile_rows`.
 int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
-  if (static_cast<int64_t>(tokens) * p.G > 16) {
+  if (static_cast<int64_t>(tokens) * p.G > (p.bits8 ? 32 : 16)) {
     const int rc = paged_tiles_launch(p, d, tokens, s, tile_rows);
     if (rc != ATTN_ERR_UNSUPPORTED) return rc;
   }

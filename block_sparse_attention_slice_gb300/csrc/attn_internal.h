@@ -1,5 +1,6 @@
 // Declarations shared by the translation units of the library (host side).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -81,6 +82,8 @@ struct PagedParams;
 size_t paged_rows_workspace(int d);
 int paged_rows_launch(PagedParams &p, int d, cudaStream_t s);
 int paged_rows8_launch(PagedParams &p, int d, cudaStream_t s);
+int paged_few8_launch(PagedParams &p, int d, cudaStream_t s);
+int paged_map8(CUtensorMap *m, const void *base, const PagedParams &p, int d, int keys);
 size_t paged_tiles_workspace(int d);
 int paged_tiles_heads(int sms, int hk);
 int paged_tiles_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows);

@@ -19,7 +19,9 @@ struct F16Codes<ATTN_CODES_INT8> {
   static constexpr int A0 = 0, A1 = 2, B0 = 1, B1 = 3;
   // 0x6400 | (x + 128) is the f16 number 1024 + 128 + x
   static __device__ __forceinline__ uint32_t pair(uint32_t bytes) {
-    uint32_t y = (bytes & 0x00ff00ffu) ^ 0x64806480u, z;
+    uint32_t y, z;
+    // (bytes & mask) ^ bias: one operation, where two constants in C became two
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(y) : "r"(bytes), "r"(0x00ff00ffu), "r"(0x64806480u));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(z) : "r"(y), "r"(0x64806480u));
     return z;
   }

@@ -151,6 +151,14 @@ PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, co
   return p;
 }
 
+// Whether no warp of the row kernels can have more than a slab of 32 keys: what counts then
+// is their start (SHORT).
+bool short_call(const PagedParams &p) {
+  long long keys = static_cast<long long>(p.max_pages) << p.page_shift;
+  if (p.causal && p.window > 0) keys = std::min<long long>(keys, static_cast<long long>(p.window) + p.sinks + 32);
+  return keys * p.n_seqs * p.hk <= 32ll * 8 * device_sm_count();
+}
+
 // Items of up to 16 rows (query heads of one key/value head times tokens) go to
 // the warp-level kernel, larger ones to the tensor-core tiles; of codes up to 32, in
 // two passes over the keys (RULE).  What the kernel
@@ -161,6 +169,11 @@ int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_ro
     if (rc != ATTN_ERR_UNSUPPORTED) return rc;
   }
   if (p.share.side == 1) p.share.side = 0;     // two passes share the SMs only where tiles are the first
+  if (p.bits8 && static_cast<int64_t>(tokens) * p.G <= 8 && !short_call(p)) {
+    *tile_rows = 8;
+    const int rc = paged_few8_launch(p, d, s);
+    if (rc != ATTN_ERR_UNSUPPORTED) return rc;
+  }
   *tile_rows = 16;
   return p.bits8 ? paged_rows8_launch(p, d, s) : paged_rows_launch(p, d, s);
 }

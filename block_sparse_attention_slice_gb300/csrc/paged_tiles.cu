@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
         auto turn = [&](auto fmt) {
           constexpr bool E4M3 = decltype(fmt)::value;
           constexpr int N = 4 * L::NHALF;
-          auto from = [&](int x) { return src + (x & 3) * 8 * D + ((D == 128 ? ((x >> 2) * 4 + ch) ^ a : ch) << 4); };
+          auto from = [&](int x) { return src + (x & 3) * 8 * D + ((D == 128 ? ((x >> 2) * 4 + ch) ^ a : ch ^ (a >> 1)) << 4); };
           uint4 w = ld_shared_v4(from(0));
 #pragma unroll 1
           for (int x = 0; x < N; ++x) {
@@ -1044,6 +1044,18 @@ size_t paged_tiles_workspace(int d) {
   return sms <= 0 ? 0 : static_cast<size_t>(sms) * (2 * 256 * (d + 2) * sizeof(float) + sizeof(Cut));
 }
 
+// Boxes of up to `keys` keys of one page, of one head's codes: rows of 128 bytes under the
+// 128-byte swizzle, of 64 under the 64-byte one.
+int paged_map8(CUtensorMap *m, const void *base, const PagedParams &p, int d, int keys) {
+  const int page = 1 << p.page_shift;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(p.hk),
+                              static_cast<cuuint64_t>(p.n_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.token_stride), static_cast<cuuint64_t>(p.head_stride),
+                                 static_cast<cuuint64_t>(p.page_stride)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(page < keys ? page : keys), 1, 1};
+  return encode(m, base, 4, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8, d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // UNSUPPORTED, with nothing launched, where the tensor maps cannot say the
 // layout (more than 128 query heads a key/value head, strides of zero).
 int paged_tiles_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
@@ -1064,14 +1076,11 @@ int paged_tiles_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *t
   {
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(p.hk),
                                 static_cast<cuuint64_t>(p.n_pages)};
-    const cuuint64_t size = p.bits8 ? 1 : 2;
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.token_stride) * size, static_cast<cuuint64_t>(p.head_stride) * size,
-                                   static_cast<cuuint64_t>(p.page_stride) * size};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(p.bits8 ? d : 64), static_cast<cuuint32_t>(page < 128 ? page : 128), 1, 1};
-    const auto type = p.bits8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const auto swizzle = p.bits8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
-    if ((rc = encode(&mk, p.k, 4, dims, strides, box, type, swizzle)) != ATTN_OK) return rc;
-    if ((rc = encode(&mv, p.v, 4, dims, strides, box, type, swizzle)) != ATTN_OK) return rc;
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.token_stride) * 2, static_cast<cuuint64_t>(p.head_stride) * 2,
+                                   static_cast<cuuint64_t>(p.page_stride) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(page < 128 ? page : 128), 1, 1};
+    if ((rc = p.bits8 ? paged_map8(&mk, p.k, p, d, 128) : encode(&mk, p.k, 4, dims, strides, box)) != ATTN_OK) return rc;
+    if ((rc = p.bits8 ? paged_map8(&mv, p.v, p, d, 128) : encode(&mv, p.v, 4, dims, strides, box)) != ATTN_OK) return rc;
   }
   const bool two = tokens > tpt;
   *tile_rows = two ? 256 : 128;

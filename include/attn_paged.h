@@ -262,7 +262,8 @@ typedef struct {
  * is rounded that the codes had not been.  Scales are expected not to be
  * negative, finite and, but for 0, above 1e-24; codes and scales behind a
  * sequence's end, and those that no token of the sequence sees, are never used,
- * whatever they hold.  The workspace is that of the calls above. */
+ * whatever they hold.  Pages with a stride of zero are not served here
+ * (UNSUPPORTED).  The workspace is that of the calls above. */
 int attn_paged8_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
                     const attn_pages8_t *pages, const attn_seqs_t *seqs, float scale, int window,
                     int sinks, void *out, int out_dtype, float *lse, void *d_ws, size_t ws_bytes,

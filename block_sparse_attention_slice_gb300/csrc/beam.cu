@@ -7,16 +7,14 @@
 // is small: a block a prompt adds the parts' sums, compares the parts' best as 64-bit
 // scores and keeps the best of them all.
 //
-// The best of a block's values: its threads form at least `keep` groups, and the
-// smallest of the groups' maxima is a threshold that `keep` values reach and few more
-// (n groups: some n (ln n + 0.6) of them, where values come in no order).  What reaches
-// it goes to a list in shared memory and is ranked there.  That takes one exchange
-// between the warps; a bisection for the exact threshold took ten.  Values are compared
-// as whole numbers in the order of the floats, -0 as 0.  Where the list overflows (values
-// that are equal by the thousand, as where most of a vocabulary is ruled out) the best
-// are taken one by one.
-#include <cuda_runtime.h>
-
+// beam_scan_kernel: a warp takes a part of a row as a stream, keeps the running maximum and
+// sum of each lane, and the best so far, one or two a lane in their order.  A word is
+// looked into only where its largest value beats the last of them, which gets rare: 512
+// rows of 131072 bf16 take SCAN us (a block a part, its threshold by an exchange and its
+// candidates ranked in shared memory, took 64, five times the instructions).  The first
+// words have a threshold of their own: the lanes form at least `keep` groups, and the
+// smallest of the groups' maxima is reached by `keep` values and few more.  Values are
+// compared as whole numbers in the order of the floats, -0 as 0.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -33,8 +31,7 @@ namespace attn {
 namespace {
 
 constexpr int BS_T = 256;            // threads of a scanning block
-constexpr int BS_CAP = 1024;         // places of its list
-constexpr int BS_WORDS = 512;        // and of that of its words
+constexpr int BS_WORDS = 4;          // 16-byte words that a lane of it takes at a time
 constexpr int BP_T = 256;            // of a choosing block
 constexpr int BP_CAP = 1024;
 
@@ -167,168 +164,175 @@ struct Vec<uint16_t> {
   }
 };
 
-// A block takes part after part, the next one's words on their way while it works on one
-// (without that, and with a part a block, 512 rows of 131072 bf16 took 88 us).  E: the
-// logits' type; WORDS: 16-byte words a thread, which stay in registers as they were read.
-// A row is taken by its 16-byte words wherever it begins; of a word that the row's ends
-// cut the values outside count as -inf and are no candidates.
-template <typename E, int WORDS>
-__global__ void __launch_bounds__(BS_T, 4) beam_scan_kernel(const ScanParams p) {
-  constexpr int N = Vec<E>::N;
-  __shared__ uint32_t sums[BS_T / 32];
-  __shared__ uint32_t tops[BS_T / 32];
-  __shared__ float part[BS_T / 32];
-  __shared__ int parti[BS_T / 32];
-  __shared__ uint32_t list_k[BS_CAP];
-  __shared__ int list_i[BS_CAP];
-  __shared__ __align__(16) uint4 words_x[BS_WORDS];       // words that reach the threshold, and their first numbers
-  __shared__ int words_i[BS_WORDS];
-  __shared__ int listed, noted;
+// The best `keep` so far of a warp's part: place lane + 32 i of their order is best i of a
+// lane; key 0: none.
+template <int R>
+struct Best {
+  uint32_t k[R];
+  int id[R];
+  __device__ __forceinline__ Best() {
+#pragma unroll
+    for (int i = 0; i < R; ++i) k[i] = 0, id[i] = INT_MAX;
+  }
+  // the last of them: what a new one has to beat
+  __device__ __forceinline__ void last(int keep, uint32_t &lk, int &li) const {
+    const int i = R == 2 && keep > 32;
+    lk = __shfl_sync(0xffffffffu, i ? k[R - 1] : k[0], (keep - 1) & 31);
+    li = __shfl_sync(0xffffffffu, i ? id[R - 1] : id[0], (keep - 1) & 31);
+  }
+  __device__ __forceinline__ void insert(uint32_t ck, int ci) {
+    const int lane = threadIdx.x & 31;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) at += __popc(__ballot_sync(0xffffffffu, before(k[i], id[i], ck, ci)));
+#pragma unroll
+    for (int i = R - 1; i >= 0; --i) {
+      uint32_t pk = __shfl_up_sync(0xffffffffu, k[i], 1);
+      int pi = __shfl_up_sync(0xffffffffu, id[i], 1);
+      if (i > 0) {
+        const uint32_t ok = __shfl_sync(0xffffffffu, k[i - 1], 31);
+        const int oi = __shfl_sync(0xffffffffu, id[i - 1], 31);
+        if (lane == 0) pk = ok, pi = oi;
+      }
+      const int place = lane + 32 * i;
+      if (place > at) k[i] = pk, id[i] = pi;
+      if (place == at) k[i] = ck, id[i] = ci;
+    }
+  }
+};
+
+// E: the logits' type; R: best a lane.  A row is taken by its 16-byte words wherever it
+// begins; of a word that the row's ends cut the values outside count as -inf and are no
+// candidates.
+template <typename E, int R>
+__global__ void __launch_bounds__(BS_T, 3) beam_scan_kernel(const ScanParams p) {
+  constexpr int N = Vec<E>::N, W = BS_WORDS;
   after_previous();
   admit_next();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  struct Part {
-    uint4 x[WORDS];
-    int first;               // word w begins with number first + w * BS_T * N of the row
-    int words;
-    bool last;               // of its row
-  };
-  // the part's words; none of a beam that has ended
-  auto load = [&](int at, Part &y) {
-    y.first = INT_MIN;
-    if (at >= p.parts) return;
-    const int row = at / p.splits, split = at - row * p.splits;
-    if (p.done && p.done[row]) return;
-    const E *base = static_cast<const E *>(p.logits) + row * p.row_stride;
-    const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(E));
-    y.words = p.words + (split < p.rest);
-    y.last = split + 1 == p.splits;
-    y.first = (split * p.words + min(split, p.rest) + static_cast<int>(threadIdx.x)) * N - skew;
-    if (split > 0 && !y.last) {            // all of its words are whole
+  const int lane = threadIdx.x & 31;
+  const int at = blockIdx.x * (BS_T / 32) + (threadIdx.x >> 5);
+  if (at >= p.parts) return;
+  const int row = at / p.splits, split = at - row * p.splits;
+  if (p.done && p.done[row]) return;
+  const E *base = static_cast<const E *>(p.logits) + row * p.row_stride;
+  const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(E));
+  const int begin = split * p.words + min(split, p.rest), end = begin + p.words + (split < p.rest);      // words
+  // words w of them, w = at + 32 i + lane
+  auto load = [&](int from, uint4 (&x)[W]) {
+    const bool inner = from > 0 && (from + 32 * W) * N - skew <= p.vocab && from + 32 * W <= end;
+    if (inner) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(base - skew + static_cast<long long>(from) * N) + lane;
 #pragma unroll
-      for (int w = 0; w < WORDS; ++w) {
-        constexpr uint32_t none = N == 4 ? 0xff800000u : 0xff80ff80u;
-        y.x[w] = make_uint4(none, none, none, none);
-        if (w * BS_T + static_cast<int>(threadIdx.x) < y.words) y.x[w] = __ldcs(reinterpret_cast<const uint4 *>(base + y.first + w * (BS_T * N)));
-      }
+      for (int i = 0; i < W; ++i) x[i] = __ldcs(src + 32 * i);
       return;
     }
 #pragma unroll
-    for (int w = 0; w < WORDS; ++w) {
-      const int v = w * BS_T + static_cast<int>(threadIdx.x) < y.words ? y.first + w * (BS_T * N) : p.vocab;
+    for (int i = 0; i < W; ++i) {
+      const int w = from + 32 * i + lane;
+      const long long v = w < end ? static_cast<long long>(w) * N - skew : p.vocab;
       if (v >= 0 && v + N <= p.vocab) {
-        y.x[w] = __ldcs(reinterpret_cast<const uint4 *>(base + v));
-      } else {
-        uint32_t z[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const bool in = v + e >= 0 && v + e < p.vocab;
-          const uint32_t b = in ? Vec<E>::bits(base + v + e) : N == 4 ? 0xff800000u : 0xff80u;
-          z[e * 4 / N] |= N == 4 ? b : b << (16 * (e & 1));
-        }
-        y.x[w] = make_uint4(z[0], z[1], z[2], z[3]);
+        x[i] = __ldcs(reinterpret_cast<const uint4 *>(base + v));
+        continue;
       }
+      uint32_t z[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const uint32_t b = v + e >= 0 && v + e < p.vocab ? Vec<E>::bits(base + v + e) : N == 4 ? 0xff800000u : 0xff80u;
+        z[e * 4 / N] |= N == 4 ? b : b << (16 * (e & 1));
+      }
+      x[i] = make_uint4(z[0], z[1], z[2], z[3]);
     }
   };
-  Part next;
-  load(blockIdx.x, next);
-  for (int at = blockIdx.x; at < p.parts; at += gridDim.x) {
-    const Part y = next;
-    load(at + gridDim.x, next);
-    if (y.first == INT_MIN) continue;      // for the whole block
+  uint4 next[W];
+  load(begin, next);
+  Best<R> best;
+  uint32_t last_k = 0;       // what a candidate has to beat: this key, with a lower token
+  int last_i = INT_MAX;
+  float m = -INFINITY, s = 0.f;
+  bool first = true;
+  for (int from = begin; from < end; from += 32 * W) {
+    uint4 x[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = next[i];
+    if (from + 32 * W < end) load(from + 32 * W, next);
     // maximum (a NaN is passed by, and spoils the sum)
-    float mw[WORDS], m = -INFINITY;
+    float mw[W];
 #pragma unroll
-    for (int w = 0; w < WORDS; ++w) {
-      mw[w] = Vec<E>::top(y.x[w]);
-      m = fmaxf(m, mw[w]);
+    for (int i = 0; i < W; ++i) mw[i] = Vec<E>::top(x[i]);
+    const float top = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
+    static_assert(W == 4, "the maximum of a lane's words");
+    const uint32_t key = key_of(top);
+    // tokens ascend: what is equal to the last of the best comes behind it
+    uint32_t least = max(last_k, last_k + 1);
+    if (first) {
+      // groups of lanes that have a word, as many as `keep` at least
+      const int active = min(32, end - begin);
+      int width = 32;
+      while (width > 1 && active < p.keep * width) width >>= 1;
+      uint32_t k = key;
+      for (int o = 1; o < width; o <<= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, o));
+      if ((lane & ~(width - 1)) >= active) k = 0xffffffffu;
+      least = active < p.keep ? 0u : __reduce_min_sync(0xffffffffu, k);
+      // of fewer whole groups than values to keep, and of words without one, every value counts
     }
-    const uint32_t top = static_cast<int>(threadIdx.x) < y.words && y.first < p.vocab ? key_of(m) : 0u;
-    if (threadIdx.x == 0) listed = noted = 0;
-    const uint32_t warp_top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) tops[warp] = warp_top;
-    // the row's last word may hold none of its values
-    const uint32_t least = threshold<BS_T>(top, p.keep, min(BS_T, y.words - y.last), sums);      // has a barrier
-    uint32_t most = tops[0];
+    if (__any_sync(0xffffffffu, key >= least)) {
 #pragma unroll
-    for (int w = 1; w < BS_T / 32; ++w) most = max(most, tops[w]);
-    m = value_of(most);
-    const float mb = m == -INFINITY ? 0.f : m;
-    const uint64_t nm = f2_make(-mb, -mb), c2 = f2_make(1.44269504f, 1.44269504f);
-    // every group has a thread that reaches the threshold, so every warp: the words that
-    // do are noted, and looked into by all threads together
-#pragma unroll
-    for (int w = 0; w < WORDS; ++w)
-      if (key_of(mw[w]) >= least) {
-        const int to = atomicAdd(&noted, 1);
-        if (to < BS_WORDS) words_x[to] = y.x[w], words_i[to] = y.first + w * (BS_T * N);
+      for (int i = 0; i < W; ++i) {
+        for (unsigned hot = __ballot_sync(0xffffffffu, key_of(mw[i]) >= least); hot; hot &= hot - 1) {
+          // the word's values to as many lanes
+          const int src = __ffs(hot) - 1;
+          const uint32_t y0 = __shfl_sync(0xffffffffu, x[i].x, src), y1 = __shfl_sync(0xffffffffu, x[i].y, src),
+                         y2 = __shfl_sync(0xffffffffu, x[i].z, src), y3 = __shfl_sync(0xffffffffu, x[i].w, src);
+          const int part = N == 4 ? lane : lane >> 1;
+          const uint32_t bits = part & 2 ? (part & 1 ? y3 : y2) : (part & 1 ? y1 : y0);
+          const uint32_t k = key_of(__uint_as_float(N == 4 || (lane & 1) ? bits & (N == 4 ? 0xffffffffu : 0xffff0000u) : bits << 16));
+          const long long token = static_cast<long long>(from + 32 * i + src) * N - skew + lane;
+          const int id = static_cast<int>(token);
+          const bool there = lane < N && from + 32 * i + src < end && token >= 0 && token < p.vocab && k >= least;
+          for (unsigned c = __ballot_sync(0xffffffffu, there && before(k, id, last_k, last_i)); c; c &= c - 1) {
+            const int e = __ffs(c) - 1;
+            const uint32_t ck = __shfl_sync(0xffffffffu, k, e);
+            const int ci = __shfl_sync(0xffffffffu, id, e);
+            if (!before(ck, ci, last_k, last_i)) continue;       // the ones before it left no room
+            best.insert(ck, ci);
+            best.last(p.keep, last_k, last_i);
+            least = max(least, max(last_k, last_k + 1));
+          }
+        }
       }
+    }
+    first = false;
+    // the lane's maximum and sum
+    const float to = fmaxf(m, top), mb = to == -INFINITY ? 0.f : to;
+    s *= ex2_approx((m - mb) * 1.44269504f);
+    m = to;
+    const uint64_t nm = f2_make(-mb, -mb), c2 = f2_make(1.44269504f, 1.44269504f);
     uint64_t s2 = 0ull;
 #pragma unroll
-    for (int w = 0; w < WORDS; ++w) {
-      uint64_t t2 = 0ull;
+    for (int i = 0; i < W; ++i)
 #pragma unroll
       for (int e = 0; e < N; e += 2) {
         float a, b;
-        f2_split(f2_mul(f2_add(f2_make(Vec<E>::get(y.x[w], e), Vec<E>::get(y.x[w], e + 1)), nm), c2), a, b);
-        t2 = f2_add(t2, f2_make(ex2_approx(a), ex2_approx(b)));
+        f2_split(f2_mul(f2_add(f2_make(Vec<E>::get(x[i], e), Vec<E>::get(x[i], e + 1)), nm), c2), a, b);
+        s2 = f2_add(s2, f2_make(ex2_approx(a), ex2_approx(b)));
       }
-      s2 = f2_add(s2, t2);
-    }
-    float s, s1;
-    f2_split(s2, s, s1);
-    s += s1;
+    float a, b;
+    f2_split(s2, a, b);
+    s += a + b;
+  }
+  float most = m;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) part[warp] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s = 0.f;
+  for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  s *= ex2_approx((m - (most == -INFINITY ? 0.f : most)) * 1.44269504f);
 #pragma unroll
-      for (int w = 0; w < BS_T / 32; ++w) s += part[w];
-      p.ms[at] = make_float2(m, s);
-    }
-    if (noted <= BS_WORDS) {
-      for (int i = threadIdx.x; i < noted * N; i += BS_T) {
-        const E *x = reinterpret_cast<const E *>(words_x);
-        const int id = words_i[i / N] + i % N;
-        const uint32_t b = Vec<E>::bits(x + i), k = key_of(__uint_as_float(N == 4 ? b : b << 16));
-        if (id >= 0 && id < p.vocab && k >= least) {
-          const int to = atomicAdd(&listed, 1);
-          if (to < BS_CAP) list_k[to] = k, list_i[to] = id;
-        }
-      }
-    }
-    __syncthreads();
-    uint32_t *keys = p.keys + static_cast<long long>(at) * p.keep;
-    int *ids = p.ids + static_cast<long long>(at) * p.keep;
-    const int n = listed;
-    if (noted <= BS_WORDS && n <= BS_CAP) {
-      rank_list<BS_T, uint32_t>(
-          n, p.keep, [&](int a, int b) { return before(list_k[a], list_i[a], list_k[b], list_i[b]); },
-          [&](int rank, int i) { keys[rank] = list_k[i], ids[rank] = list_i[i]; });
-      for (int i = n + threadIdx.x; i < p.keep; i += BS_T) ids[i] = -1;
-    } else {
-      uint32_t last_k = 0xffffffffu;
-      int last_i = -1;
-      for (int r = 0; r < p.keep; ++r) {
-        uint32_t k = 0;
-        int id = INT_MAX;
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) p.ms[at] = make_float2(most, s);
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w)
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const uint32_t a = key_of(Vec<E>::get(y.x[w], e));
-            const int i = y.first + w * (BS_T * N) + e;
-            if (i >= 0 && i < p.vocab && before(last_k, last_i, a, i) && before(a, i, k, id)) k = a, id = i;
-          }
-        block_best<BS_T>(k, id, sums, parti);
-        if (threadIdx.x == 0) keys[r] = k, ids[r] = k ? id : -1;
-        last_k = k;
-        last_i = id;
-      }
-    }
-    __syncthreads();         // the list and the sums have been read
+  for (int i = 0; i < R; ++i) {
+    const int place = lane + 32 * i;
+    if (place >= p.keep) continue;
+    p.keys[static_cast<long long>(at) * p.keep + place] = best.k[i];
+    p.ids[static_cast<long long>(at) * p.keep + place] = best.k[i] ? best.id[i] : -1;
   }
 }
 
@@ -549,47 +553,55 @@ __device__ __forceinline__ void move_column(uint8_t *base, long long stride, con
 // of them shifted into the new row's place (a vocabulary of an odd number of bytes: bytes
 // one by one took four times as long).  Bytes at the ends of the run are moved alone,
 // those outside it neither read nor written.
-__device__ __forceinline__ void move_run(uint8_t *base, long long stride, int n, const int *par, const int *used, int beams, uint32_t *buf) {
-  const int pitch = unit_bytes(true, beams) / 4 + 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < beams; r += RE_T / 32) {
-    if (!used[r]) continue;
-    const uint8_t *from = base + r * stride;
-    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 3);
-    for (int j = lane; 4 * j < skew + n; j += 32) {
-      const int t = 4 * j - skew;            // the word's first byte in the run
-      uint32_t w = 0;
+__device__ __forceinline__ void move_run(uint8_t *base, long long stride, int n, const int *par, const int *used, int n_used, int beams, uint32_t *buf) {
+  constexpr int BATCH = 4;
+  const int pitch = unit_bytes(true, beams) / 4 + 2, words = n / 4 + 2;        // as many as n bytes can lie in
+  for (int i0 = threadIdx.x; i0 < n_used * words; i0 += RE_T * BATCH) {
+    uint32_t w[BATCH];
+    int to[BATCH];
+#pragma unroll
+    for (int q = 0; q < BATCH; ++q) {
+      const int i = i0 + q * RE_T, x = i / words, j = i - x * words;
+      to[q] = -1;
+      w[q] = 0;
+      if (x >= n_used) continue;
+      const uint8_t *from = base + used[x] * stride;
+      const int t = 4 * j - static_cast<int>(reinterpret_cast<uintptr_t>(from) & 3);        // the word's first byte in the run
+      to[q] = used[x] * pitch + j;
       if (t >= 0 && t + 4 <= n) {
-        w = *reinterpret_cast<const uint32_t *>(from + t);
+        w[q] = *reinterpret_cast<const uint32_t *>(from + t);
       } else {
         for (int k = 0; k < 4; ++k)
-          if (t + k >= 0 && t + k < n) w |= static_cast<uint32_t>(from[t + k]) << (8 * k);
+          if (t + k >= 0 && t + k < n) w[q] |= static_cast<uint32_t>(from[t + k]) << (8 * k);
       }
-      buf[r * pitch + j] = w;
     }
+#pragma unroll
+    for (int q = 0; q < BATCH; ++q)
+      if (to[q] >= 0) buf[to[q]] = w[q];
   }
   __syncthreads();
-  for (int b = warp; b < beams; b += RE_T / 32) {
+  for (int i = threadIdx.x; i < beams * words; i += RE_T) {
+    const int b = i / words, j = i - b * words;
     if (par[b] == b) continue;
     uint8_t *to = base + b * stride;
     const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(to) & 3),
               off = static_cast<int>(reinterpret_cast<uintptr_t>(base + par[b] * stride) & 3) - skew;
     const uint32_t *src = buf + par[b] * pitch;
-    for (int j = lane; 4 * j < skew + n; j += 32) {
-      const int t = 4 * j - skew, i = off < 0 ? j - 1 : j;
-      const uint32_t w = __funnelshift_r(src[max(i, 0)], src[i + 1], 8 * (off & 3));
-      if (t >= 0 && t + 4 <= n) {
-        *reinterpret_cast<uint32_t *>(to + t) = w;
-      } else {
-        for (int k = 0; k < 4; ++k)
-          if (t + k >= 0 && t + k < n) to[t + k] = static_cast<uint8_t>(w >> (8 * k));
-      }
+    const int t = 4 * j - skew, x = off < 0 ? j - 1 : j;
+    if (t >= n) continue;
+    const uint32_t w = __funnelshift_r(src[max(x, 0)], src[x + 1], 8 * (off & 3));
+    if (t >= 0 && t + 4 <= n) {
+      *reinterpret_cast<uint32_t *>(to + t) = w;
+    } else {
+      for (int k = 0; k < 4; ++k)
+        if (t + k >= 0 && t + k < n) to[t + k] = static_cast<uint8_t>(w >> (8 * k));
     }
   }
 }
 
 template <int MOST>
 __global__ void __launch_bounds__(RE_T) beam_reorder_kernel(const __grid_constant__ ReorderParams p) {
-  __shared__ int par[ATTN_BEAM_MAX], used[ATTN_BEAM_MAX];
+  __shared__ int par[ATTN_BEAM_MAX], used[ATTN_BEAM_MAX], n_used;
   __shared__ uint32_t buf[RE_BUF / 4 + 2 * ATTN_BEAM_MAX];
   after_previous();
   admit_next();
@@ -607,7 +619,6 @@ __global__ void __launch_bounds__(RE_T) beam_reorder_kernel(const __grid_constan
       const long long a = p.parents[row0 + b] - row0;
       off = a < 0 || a >= p.beams;
       par[b] = off ? b : static_cast<int>(a);
-      used[b] = 0;
     }
     if (__syncthreads_or(off)) {
       if (threadIdx.x == 0) atomicCAS(p.status, 0u, static_cast<unsigned>(ATTN_ERR_INVALID_ARG));
@@ -617,22 +628,33 @@ __global__ void __launch_bounds__(RE_T) beam_reorder_kernel(const __grid_constan
     if (!st.loose) {
       if (at + 16 * threadIdx.x < st.bytes) move_column<MOST>(base + 16 * threadIdx.x, st.stride, par, p.beams);
     } else {
-      if (b < p.beams && par[b] != b) used[par[b]] = 1;
+      if (b < 32) {          // the rows that others become
+        int count = 0;
+        for (int r0 = 0; r0 < p.beams; r0 += 32) {
+          const int r = r0 + b;
+          bool on = false;
+          for (int k = 0; k < p.beams; ++k) on |= r < p.beams && k != r && par[k] == r;
+          const unsigned all = __ballot_sync(0xffffffffu, on);
+          if (on) used[count + __popc(all & ((1u << b) - 1))] = r;
+          count += __popc(all);
+        }
+        if (b == 0) n_used = count;
+      }
       __syncthreads();
-      move_run(base, st.stride, static_cast<int>(min(static_cast<long long>(each), st.bytes - at)), par, used, p.beams, buf);
+      move_run(base, st.stride, static_cast<int>(min(static_cast<long long>(each), st.bytes - at)), par, used, n_used, p.beams, buf);
     }
   }
 }
 
-// Parts of a row: of 4 words of 16 bytes a thread, or 1 where those would leave SMs
-// without a block.
-// words: of a row, wherever it begins.
-int splits_of(int rows, int vocab, int dtype, int sms, int *each, int *words) {
+// Parts of a row, a warp each: as many as fill the SMs with 24 warps
+// (32, of 64 registers a thread, were slower), of 32 BS_WORDS words at
+// least.  words: of a row, wherever it begins.
+// Not more than leave a group's choice 16384 candidates.
+int splits_of(int groups, int beams, int vocab, int keep, int dtype, int sms, int *words) {
   const int n = dtype == ATTN_DTYPE_F32 ? 4 : 8;
   *words = (vocab + 2 * n - 2) / n;
-  auto parts = [&](int w) { return (*words + BS_T * w - 1) / (BS_T * w); };
-  *each = static_cast<long long>(rows) * parts(4) >= 2 * sms ? 4 : 1;
-  return parts(*each);
+  const int most = (*words + 32 * BS_WORDS - 1) / (32 * BS_WORDS);
+  return std::max(1, std::min({most, sms * 24 / std::max(groups * beams, 1), 16384 / (beams * keep)}));
 }
 
 int check_beams(int groups, int beams, int vocab, int keep) {
@@ -658,8 +680,8 @@ int attn_beam_workspace_bytes(int groups, int beams, int vocab, int keep, size_t
   if (sms <= 0) return ATTN_ERR_CUDA;
   size_t most = 0;
   for (int dtype : {ATTN_DTYPE_F32, ATTN_DTYPE_BF16}) {
-    int each, words;
-    const size_t parts = static_cast<size_t>(groups) * beams * splits_of(groups * beams, vocab, dtype, sms, &each, &words);
+    int words;
+    const size_t parts = static_cast<size_t>(groups) * beams * splits_of(groups, beams, vocab, keep, dtype, sms, &words);
     const size_t need = up256(parts * 8) + 2 * up256(parts * keep * 4);
     most = need > most ? need : most;
   }
@@ -688,8 +710,8 @@ int attn_beam_select(const void *logits, int logits_dtype, int64_t row_stride, i
   const int rows = groups * beams;
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  int each, words;
-  const int splits = splits_of(rows, vocab, logits_dtype, sms, &each, &words);
+  int words;
+  const int splits = splits_of(groups, beams, vocab, keep, logits_dtype, sms, &words);
   const size_t parts = static_cast<size_t>(rows) * splits;
   if (parts >= (size_t(1) << 30) || static_cast<int64_t>(beams) * splits * keep >= INT_MAX) return ATTN_ERR_UNSUPPORTED;
   uint8_t *ws = static_cast<uint8_t *>(d_ws);
@@ -698,10 +720,10 @@ int attn_beam_select(const void *logits, int logits_dtype, int64_t row_stride, i
   int *ids = reinterpret_cast<int *>(ws + up256(parts * 8) + up256(parts * keep * 4));
   const ScanParams sp{logits, done, row_stride, vocab, splits, keep, words / splits, words % splits, static_cast<int>(parts), ms, keys, ids};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto scan = logits_dtype == ATTN_DTYPE_F32 ? (each == 4 ? beam_scan_kernel<float, 4> : beam_scan_kernel<float, 1>)
-                                             : (each == 4 ? beam_scan_kernel<uint16_t, 4> : beam_scan_kernel<uint16_t, 1>);
-  const size_t grid = std::min<size_t>(parts, static_cast<size_t>(sms) * 4);
-  if ((rc = launch_after(scan, dim3(static_cast<unsigned>(grid)), BS_T, 0, s, sp)) != ATTN_OK) return rc;
+  auto scan = logits_dtype == ATTN_DTYPE_F32 ? (keep <= 32 ? beam_scan_kernel<float, 1> : beam_scan_kernel<float, 2>)
+                                             : (keep <= 32 ? beam_scan_kernel<uint16_t, 1> : beam_scan_kernel<uint16_t, 2>);
+  const unsigned grid = static_cast<unsigned>((parts + BS_T / 32 - 1) / (BS_T / 32));
+  if ((rc = launch_after(scan, dim3(grid), BS_T, 0, s, sp)) != ATTN_OK) return rc;
   const PickParams pp{scores, done, slots, ms, keys, ids, beams, vocab, splits, keep, eos, out_scores, out_parents, out_tokens, out_src, out_done};
   return launch_after(beam_pick_kernel, dim3(groups), BP_T, 0, s, pp);
 }

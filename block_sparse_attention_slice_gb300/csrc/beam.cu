@@ -11,7 +11,7 @@
 // sum of each lane, and the best so far, one or two a lane in their order.  A word is
 // looked into only where its largest value beats the last of them, which gets rare: 512
 // rows of 131072 bf16 take SCAN us (a block a part, its threshold by an exchange and its
-// candidates ranked in shared memory, took 64, five times the instructions).  The first
+// candidates ranked in shared memory, took half as long again).  The first
 // words have a threshold of their own: the lanes form at least `keep` groups, and the
 // smallest of the groups' maxima is reached by `keep` values and few more.  Values are
 // compared as whole numbers in the order of the floats, -0 as 0.
@@ -742,6 +742,8 @@ int attn_beam_reorder(void *const *h_states, const int64_t *h_row_bytes, const i
     if (bytes < 0 || stride < bytes) return ATTN_ERR_INVALID_ARG;
     if (bytes == 0 || groups == 0) continue;
     if (!h_states[i]) return ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < p.n_states; ++j)
+      if (p.s[j].at == h_states[i]) return ATTN_ERR_INVALID_ARG;
     const uint64_t all = reinterpret_cast<uintptr_t>(h_states[i]) | static_cast<uint64_t>(bytes) | static_cast<uint64_t>(stride);
     const int loose = (all & 15) || beams > 16;
     const int64_t each = unit_bytes(loose, beams);

@@ -145,7 +145,7 @@ __device__ __forceinline__ uint32_t top8(const int4 &x) {
   return max(a & 0xffffu, a >> 16);
 }
 
-constexpr int TOKEN_WORDS = 4;
+constexpr int TOKEN_WORDS = 4, MAX_HEADS = 1024;
 
 // A warp takes p.run tokens at a time: its lanes find their places, a token a lane, then
 // the tokens' words of 8 values, one after the other, are shared out to them, up to
@@ -329,7 +329,8 @@ TokenParams token_params(const attn_pages_t *g, const attn_pages8_t *g8, const a
   p.shift = shift;
   p.hk = g->hk;
   p.words = g->d / 8;
-  // x / n for x < 32 n is the upper half of x times this: right where 32 n^2 < 2^32
+  // x / n for x < 4 n (a warp's tokens) is the upper half of x times this: right where
+  // 4 n^2 < 2^32, and n is 16 MAX_HEADS at most
   p.per_token = static_cast<uint32_t>(((uint64_t(1) << 32) + p.hk * p.words - 1) / (p.hk * p.words));
   p.per_head = static_cast<uint32_t>(((uint64_t(1) << 32) + p.words - 1) / p.words);
   return p;
@@ -341,19 +342,19 @@ int launch_tokens(void (*kern)(const TokenParams), TokenParams &p, attn_stream_t
   if (sms <= 0) return ATTN_ERR_CUDA;
   // as many tokens a warp as leave every SM 32 warps, up to 4 (2, 4, 8, 16: 24 prompts written in
   // 63.1, 61.5, 68.3, 68.3 us, a batch of 32 sequences read back in 79.3, 64.2, 67.1, 63.4)
-  p.run = std::max(1, std::min(4, p.n_tokens / (sms * 32)));
+  p.run = std::max(1, std::min(4, p.n_tokens / (sms * 32)));        // 4: see token_params
   const int blocks = (p.n_tokens + 8 * p.run - 1) / (8 * p.run), grid = sms * 8;
   return launch_after(kern, dim3(blocks < grid ? blocks : grid), 256, 0, reinterpret_cast<cudaStream_t>(stream), p);
 }
 
 // What reads and writes of tokens share; *go: there is something to do.
-int check_tokens(const attn_seqs_t *seqs, int page_size, const int32_t *q_ptr, int n_tokens, bool *go) {
+int check_tokens(const attn_seqs_t *seqs, int page_size, int hk, const int32_t *q_ptr, int n_tokens, bool *go) {
   *go = false;
   if (n_tokens < 0) return ATTN_ERR_INVALID_ARG;
   const int rc = paged_check_seqs(seqs, page_size);
   if (rc != ATTN_OK) return rc;
   if (!q_ptr && n_tokens != seqs->n_seqs) return ATTN_ERR_INVALID_ARG;
-  if (n_tokens > ATTN_PAGED_MAX_LEN) return ATTN_ERR_UNSUPPORTED;
+  if (n_tokens > ATTN_PAGED_MAX_LEN || hk > MAX_HEADS) return ATTN_ERR_UNSUPPORTED;
   *go = n_tokens > 0 && seqs->n_seqs > 0;
   return ATTN_OK;
 }
@@ -361,7 +362,7 @@ int check_tokens(const attn_seqs_t *seqs, int page_size, const int32_t *q_ptr, i
 int read_tokens(const attn_pages_t *g, const attn_pages8_t *g8, const attn_seqs_t *seqs, const int32_t *q_ptr, int n_tokens, void *k_out,
                 void *v_out, int out_dtype, int shift, attn_stream_t stream) {
   bool go;
-  const int rc = check_tokens(seqs, g->page_size, q_ptr, n_tokens, &go);
+  const int rc = check_tokens(seqs, g->page_size, g->hk, q_ptr, n_tokens, &go);
   if (rc != ATTN_OK) return rc;
   if (out_dtype != ATTN_DTYPE_BF16 && out_dtype != ATTN_DTYPE_F32) return ATTN_ERR_INVALID_ARG;
   if (!go) return ATTN_OK;
@@ -401,7 +402,7 @@ int attn_cache8_write(const attn_pages8_t *pages, const attn_seqs_t *seqs, const
   int shift = 0, rc;
   bool go;
   if ((rc = paged_check_pages8(pages, &shift)) != ATTN_OK) return rc;
-  if ((rc = check_tokens(seqs, pages->pages.page_size, q_ptr, n_tokens, &go)) != ATTN_OK || !go) return rc;
+  if ((rc = check_tokens(seqs, pages->pages.page_size, pages->pages.hk, q_ptr, n_tokens, &go)) != ATTN_OK || !go) return rc;
   if (!k_new || !v_new) return ATTN_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15) return ATTN_ERR_UNSUPPORTED;
   if ((new_token_stride | new_head_stride) & 7 || new_token_stride < 0 || new_head_stride < 0) return ATTN_ERR_UNSUPPORTED;

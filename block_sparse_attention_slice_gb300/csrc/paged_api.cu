@@ -151,18 +151,26 @@ PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, co
   return p;
 }
 
-// Whether no warp of the row kernels can have more than a slab of 32 keys: what counts then
-// is their start (SHORT).
+// Whether no warp of the row kernels can have more than 6 slabs of 32 keys: what counts then
+// is their start, and the kernel for few rows has the longer one (12 warps, tensor maps).
+// One sequence of 4 query heads to each of 8 key/value heads of 128, it against the kernel
+// for 16 rows: 512 keys 16.9, 14.2 us; 8192 20.7, 18.0; 16384 23.9, 22.7; 32768 29.2, 28.6.
+// Four sequences: 4096 keys 24.3, 22.1; 6144 25.8, 26.0; 8192 29.8, 31.1; 32768 64.1, 75.5.
+// Of 64 columns: 4096 keys 21.9, 18.8; 8192 25.5, 24.8; 12288 29.2, 30.4; 32768 50.6, 56.1.
 bool short_call(const PagedParams &p) {
   long long keys = static_cast<long long>(p.max_pages) << p.page_shift;
   if (p.causal && p.window > 0) keys = std::min<long long>(keys, static_cast<long long>(p.window) + p.sinks + 32);
-  return keys * p.n_seqs * p.hk <= 32ll * 8 * device_sm_count();
+  return keys * p.n_seqs * p.hk <= 6 * 32ll * 8 * device_sm_count();
 }
 
 // Items of up to 16 rows (query heads of one key/value head times tokens) go to
 // the warp-level kernel, larger ones to the tensor-core tiles; of codes up to 32, in
-// two passes over the keys (RULE).  What the kernel
-// chose is left in p and, the rows of a piece, in `tile_rows`.
+// two passes over the keys, since the tiles turn every code into an operand before they
+// begin and fill 128 rows.  16 sequences of 8192 keys, 8 key/value heads of 128, e4m3, rows
+// against tiles: 20 rows 120, 144 us; 32 rows 123, 145; 40 rows 169, 150.  int8: 32 rows 130,
+// 138; 40 rows 181, 143.  Of 64 columns, int8: 32 rows 96, 93; 40 rows 136, 97; 32 sequences
+// of 1500 keys: 43, 45; 58, 46.  What the kernel chose is left in p and, the rows of a piece,
+// in `tile_rows`.
 int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
   if (static_cast<int64_t>(tokens) * p.G > (p.bits8 ? 32 : 16)) {
     const int rc = paged_tiles_launch(p, d, tokens, s, tile_rows);

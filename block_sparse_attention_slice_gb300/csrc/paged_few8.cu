@@ -12,7 +12,7 @@
 //     key/value head; with them as the 16 rows (16 x 8 keys) twice the products and
 //     half of all softmax work went to rows that are not there, and twice the registers,
 //     which left room for 8 warps where 12 hide more latency (64 sequences, window 4096:
-//     BEFORE us).  P^T comes out of the scores by transposing 8 x 8 matrices in registers;
+//     104 us so, 84 now).  P^T comes out of the scores by transposing 8 x 8 matrices in registers;
 //   - operands are f16, not bf16: e4m3 converts by one instruction a pair, int8 by
 //     one logical operation and one addition (bf16 would take four);
 //   - a lane reads 16 codes at once and they are its operands as they lie: the sum
@@ -23,7 +23,6 @@
 //   - slabs are fetched by TMA, one box of a slab's keys or values for each page, whose
 //     swizzle serves the reads (two lanes of eight meet a bank twice where keys are
 //     read): 9 % fewer instructions than copies of 16 bytes.
-// Up to 32 rows at head dim 64 and 16 at 128 are one pass over the keys.
 //
 // Numerics.  Codes become f16 exactly.  A row of Q becomes f16 times a power of
 // two that brings its largest value to 2^14 .. 2^15: exact but for values 2^-29
@@ -187,9 +186,9 @@ __global__ void __launch_bounds__(W * 32, 1) paged_few8_kernel(const __grid_cons
         note[slot] = FewSlab{key0, in.i, in.sp.n, head, in.rt, in.s.q0, in.s.nq, in.s.len, seen, {}};
         mbar_arrive_expect_tx(bar, S::STAGE);
         const int tok = key0 & page_mask;
-        // failure-path test only: the second slab's keys are left out, so that the wait for
+        // failure-path test only: the first slab's keys are left out, so that the wait for
         // them runs out
-        if (!(p.test_stall && n == 1)) tma_load_4d(stage, &tm_k, bar, 0, tok, head, page[0]);
+        if (!(p.test_stall && n == 0)) tma_load_4d(stage, &tm_k, bar, 0, tok, head, page[0]);
         tma_load_4d(stage + S::PART, &tm_v, bar, 0, tok, head, page[0]);
         if (box < KEYS) {
           tma_load_4d(stage + 16 * D, &tm_k, bar, 0, 0, head, page[NSUB - 1]);

@@ -44,7 +44,8 @@ int attn_beam_workspace_bytes(int groups, int beams, int vocab, int keep, size_t
  * A continuation that cannot be (a logit of -inf; a beam whose score, or whose
  * sum, is not finite: a NaN or +inf among its logits, -inf alone; what an ended
  * beam does not offer) has the score -inf and stands behind all others, by its
- * place as well.  groups = 0 does nothing.
+ * place as well.  groups = 0 does nothing.  No output may lie on an input, the
+ * workspace or another output (not looked at).
  * Errors: INVALID_ARG (keep > beams * vocab, eos >= vocab, null arrays, ..);
  * UNSUPPORTED (beams or keep > ATTN_BEAM_MAX, groups * beams >= 2^24, vocab >
  * 2^30, alignment of an array to its elements, of d_ws to 16); CAPACITY (ws_bytes); CUDA. */
@@ -60,7 +61,8 @@ int attn_beam_select(const void *logits, int logits_dtype, int64_t row_stride, i
  *   h_states, h_row_bytes, h_row_strides  host arrays of n_states: a state's
  *            address, the bytes of a row (>= 0) and from row to row (>= those)
  * Rows of any size and alignment are served; multiples of 16 bytes are fastest.
- * No two states may share memory (not looked at).  A group one of whose parents
+ * No two states may share memory (of this only two that begin at one address are
+ * seen: INVALID_ARG), nor one with the parents.  A group one of whose parents
  * lies outside it is left as it was (INVALID_ARG on the device).
  * Errors: INVALID_ARG; UNSUPPORTED (beams > ATTN_BEAM_MAX, n_states >
  * ATTN_BEAM_MAX_STATES, groups * beams >= 2^24); CUDA. */

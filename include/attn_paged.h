@@ -238,7 +238,8 @@ int attn_cache_write(const attn_pages_t *pages, const attn_seqs_t *seqs, const i
  *   k_out, v_out  [n_tokens, hk, d] bf16 or f32 (out_dtype), 16-byte aligned
  * Rows of no sequence are left as they were; so is a row whose slot, position
  * or page is out of range (INVALID_ARG on the device).  The outputs must not lie
- * where the call reads (not looked at). */
+ * where the call reads (not looked at).  UNSUPPORTED also: n_tokens >
+ * ATTN_PAGED_MAX_LEN, hk > 1024. */
 int attn_cache_read(const attn_pages_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr,
                     int n_tokens, void *k_out, void *v_out, int out_dtype, attn_stream_t stream);
 
@@ -262,8 +263,9 @@ typedef struct {
  * is rounded that the codes had not been.  Scales are expected not to be
  * negative, finite and, but for 0, above 1e-24; codes and scales behind a
  * sequence's end, and those that no token of the sequence sees, are never used,
- * whatever they hold.  Pages with a stride of zero are not served here
- * (UNSUPPORTED).  The workspace is that of the calls above. */
+ * whatever they hold; a key that some tokens of a sequence see and others do not
+ * has to have a value and scale that are finite, as above.  The workspace is that
+ * of the calls above. */
 int attn_paged8_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
                     const attn_pages8_t *pages, const attn_seqs_t *seqs, float scale, int window,
                     int sinks, void *out, int out_dtype, float *lse, void *d_ws, size_t ws_bytes,
@@ -277,7 +279,8 @@ int attn_prefix8_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_
  * magnitude a, M = 127 (int8) or 448 (e4m3): its scale is a / M, and x becomes
  * the code next to x M / a, the even one of two as near (a = 0: scale and codes
  * 0).  Where a value is not finite the scale is NaN and the codes are 0: the
- * head's whole row reads as NaN. */
+ * head's whole row reads as NaN.  UNSUPPORTED also: scales with a stride of zero,
+ * hk > 1024. */
 int attn_cache8_write(const attn_pages8_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr,
                       const void *k_new, const void *v_new, int n_tokens, int64_t new_token_stride,
                       int64_t new_head_stride, attn_stream_t stream);

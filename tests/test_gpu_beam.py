@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import oracle
-from block_sparse_attention_slice_gb300 import attn_beam_reorder, attn_beam_select, attn_last_device_error
+from block_sparse_attention_slice_gb300 import AttnError, attn_beam_reorder, attn_beam_select, attn_last_device_error
 from block_sparse_attention_slice_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
@@ -189,3 +189,66 @@ def test_reorder_of_rows_past_four_gigabytes():
     attn_beam_reorder([x], torch.tensor([[2, 0, 0]], dtype=torch.int32, device="cuda"))
     assert attn_last_device_error() == 0
     assert x[:, -1].tolist() == [3, 1, 1] and x[:, n // 2 + 5].tolist() == [6, 4, 4]
+
+
+@pytest.mark.parametrize("G,Bm,V,keep", [(1, 64, 5000, 64), (20000, 2, 40, 2), (3000, 5, 70, 7), (1, 1, 1 << 21, 64), (700, 3, 3001, 3)])
+def test_the_most_beams_prompts_and_tokens(G, Bm, V, keep):
+    logits, scores = make(G, Bm, V, 3)
+    run(logits, scores, keep=keep)
+
+
+def test_calls_at_once():
+    logits, scores = make(9, 4, 30000, 6)
+    want = attn_beam_select(logits, scores)
+    states = [torch.arange(36 * 7, device="cuda").view(36, 7) + i for i in range(3)]
+    first = [x.clone() for x in states]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for x, s in zip(states, streams):
+        got.append(attn_beam_select(logits, scores, stream=s))
+        attn_beam_reorder([x], got[-1][1], stream=s)
+    torch.cuda.synchronize()
+    for g, x, y in zip(got, states, first):
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+        assert torch.equal(x, y[want[1].view(-1).long()])
+    assert attn_last_device_error() == 0
+
+
+def test_refusals_of_tensors():
+    logits, scores = make(2, 3, 100, 0)
+    done = torch.zeros((2, 3), dtype=torch.bool, device="cuda")
+    for bad in (dict(logits=logits.half()), dict(logits=logits.t().contiguous().t()), dict(logits=logits[:5]), dict(logits=logits[None]), dict(scores=scores.cpu()),
+                dict(scores=scores.double()), dict(scores=scores.t()), dict(done=done.int()), dict(done=done[:1]), dict(done=done.cpu()), dict(slots=scores),
+                dict(slots=torch.zeros(5, dtype=torch.int32, device="cuda")), dict(ws=torch.zeros(1 << 16))):
+        with pytest.raises(ValueError):
+            attn_beam_select(**{**dict(logits=logits, scores=scores, eos=1), **bad})
+    for bad in (dict(keep=0), dict(keep=65), dict(eos=100), dict(done=done), dict(ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(AttnError):
+            attn_beam_select(logits, scores, **bad)
+    parents = parents_of(2, 3, 0)
+    x = torch.zeros((6, 4, 5), device="cuda")
+    for bad in ([x[:5]], [x.cpu()], [x.transpose(1, 2)], [x[0, 0, 0]], [x, x[:, :, ::2]]):
+        with pytest.raises(ValueError):
+            attn_beam_reorder(bad, parents)
+    for bad in ([x, x], [x[:1].expand(6, -1, -1)], [x.clone() for _ in range(65)]):
+        with pytest.raises(AttnError):
+            attn_beam_reorder(bad, parents)
+    for bad in (parents.long(), parents.view(-1), parents.cpu(), parents.t()):
+        with pytest.raises(ValueError):
+            attn_beam_reorder([x], bad)
+    with pytest.raises(TypeError):
+        attn_beam_reorder([x, 7], parents)
+    attn_beam_reorder([], parents)
+    attn_beam_reorder([x[:, :0], x], parents)
+    assert attn_last_device_error() == 0
+
+
+def test_states_side_by_side_in_one_tensor():
+    """Columns of one tensor as states of their own."""
+    x = torch.randint(0, 100, (12, 40), generator=torch.Generator().manual_seed(0)).cuda()
+    parents = parents_of(3, 4, 1)
+    want = x[parents.view(-1).long()]
+    y = x.clone()
+    attn_beam_reorder([y[:, :8], y[:, 8:17], y[:, 17:]], parents)
+    assert torch.equal(y, want)

@@ -10,10 +10,9 @@
 // beam_scan_kernel: a warp takes a part of a row as a stream, keeps the running maximum and
 // sum of each lane, and the best so far, one or two a lane in their order.  A word is
 // looked into only where its largest value beats the last of them, which gets rare: 512
-// rows of 131072 bf16 take SCAN us (a block a part, its threshold by an exchange and its
+// rows of 131072 bf16 take 38 us (a block a part, its threshold by an exchange and its
 // candidates ranked in shared memory, took half as long again).  The first
-// words have a threshold of their own: the lanes form at least `keep` groups, and the
-// smallest of the groups' maxima is reached by `keep` values and few more.  Values are
+// words have a threshold of their own, the `keep`-th of the lanes' largest values.  Values are
 // compared as whole numbers in the order of the floats, -0 as 0.
 #include <algorithm>
 #include <climits>
@@ -265,15 +264,14 @@ __global__ void __launch_bounds__(BS_T, 3) beam_scan_kernel(const ScanParams p) 
     // tokens ascend: what is equal to the last of the best comes behind it
     uint32_t least = max(last_k, last_k + 1);
     if (first) {
-      // groups of lanes that have a word, as many as `keep` at least
-      const int active = min(32, end - begin);
-      int width = 32;
-      while (width > 1 && active < p.keep * width) width >>= 1;
+      // the `keep`-th of the lanes' largest: `keep` values reach it, and few more (equal ones
+      // leave together, so that it may be less); of fewer lanes every value counts
       uint32_t k = key;
-      for (int o = 1; o < width; o <<= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, o));
-      if ((lane & ~(width - 1)) >= active) k = 0xffffffffu;
-      least = active < p.keep ? 0u : __reduce_min_sync(0xffffffffu, k);
-      // of fewer whole groups than values to keep, and of words without one, every value counts
+      least = p.keep <= 32 ? 0xffffffffu : 0u;
+      for (int i = 0; i < p.keep && least; ++i) {
+        least = __reduce_max_sync(0xffffffffu, k);
+        if (k == least) k = 0u;
+      }
     }
     if (__any_sync(0xffffffffu, key >= least)) {
 #pragma unroll
@@ -530,9 +528,14 @@ struct ReorderParams {
   int n_states, groups, beams, units;
   unsigned int *status;
 };
-constexpr int RE_T = 256, RE_BUF = 32768;
-// Bytes of a row that a unit moves: a word a thread, or what room there is for all rows.
-__host__ __device__ __forceinline__ int unit_bytes(bool loose, int beams) { return loose ? min(2048, RE_BUF / beams & ~15) : RE_T * 16; }
+constexpr int RE_T = 256;
+// Bytes of a row that a unit moves: a word of 16 bytes a thread; or a power of two that leaves
+// all rows room for 32 KB.
+__host__ __device__ __forceinline__ int unit_bytes(bool loose, int beams) {
+  return !loose ? RE_T * 16 : beams <= 16 ? 2048 : beams <= 32 ? 1024 : 512;
+}
+// A row of it in shared memory lies as in memory, up to 15 bytes behind a word's beginning.
+__host__ __device__ __forceinline__ int run_pitch(int beams) { return unit_bytes(true, beams) + 32; }
 
 // All parents' words of one column of a group, then all rows': the column is this
 // thread's alone, so the rows may change places in memory.  Rows that stay are not
@@ -548,61 +551,79 @@ __device__ __forceinline__ void move_column(uint8_t *base, long long stride, con
     if (b < beams && par[b] != b) *reinterpret_cast<uint4 *>(base + b * stride) = x[b];
 }
 
+// Words of 16 bytes that lie wholly in n bytes that begin `skew` behind a word: of `head`
+// bytes before the first, and how many.
+__device__ __forceinline__ int whole_words(int n, int skew, int &head) {
+  head = min((16 - skew) & 15, n);
+  return (n - head) >> 4;
+}
+
 // The same for `n` bytes of rows at any address, or of more than 16 beams, through shared
-// memory: words of 4 bytes where they lie in memory, read as they are and written as two
-// of them shifted into the new row's place (a vocabulary of an odd number of bytes: bytes
-// one by one took four times as long).  Bytes at the ends of the run are moved alone,
-// those outside it neither read nor written.
-__device__ __forceinline__ void move_run(uint8_t *base, long long stride, int n, const int *par, const int *used, int n_used, int beams, uint32_t *buf) {
+// memory: words of 16 bytes where they lie in memory, read as they are and written as two of
+// them shifted into the new row's place.  (24 groups of 5 rows of 100003 bytes: 10.7 us;
+// words of 4 bytes, whose instructions bound it, took 20, bytes four times that.)  The bytes at the
+// ends of the run are moved alone, those outside it neither read nor written.
+__device__ __forceinline__ void move_run(uint8_t *base, long long stride, int n, const int *par, const int *used, int n_used, int beams, uint8_t *buf) {
   constexpr int BATCH = 4;
-  const int pitch = unit_bytes(true, beams) / 4 + 2, words = n / 4 + 2;        // as many as n bytes can lie in
-  for (int i0 = threadIdx.x; i0 < n_used * words; i0 += RE_T * BATCH) {
-    uint32_t w[BATCH];
-    int to[BATCH];
+  const int pitch = run_pitch(beams), slots = unit_bytes(true, beams) / 16, shift = 31 - __clz(slots);
+  auto skew_of = [&](int row) { return static_cast<int>(reinterpret_cast<uintptr_t>(base + row * stride) & 15); };
+  for (int i0 = threadIdx.x; i0 < n_used << shift; i0 += RE_T * BATCH) {
+    uint4 w[BATCH];
+    uint8_t *to[BATCH];
 #pragma unroll
     for (int q = 0; q < BATCH; ++q) {
-      const int i = i0 + q * RE_T, x = i / words, j = i - x * words;
-      to[q] = -1;
-      w[q] = 0;
+      const int i = i0 + q * RE_T, x = i >> shift, j = i & (slots - 1);
+      to[q] = nullptr;
       if (x >= n_used) continue;
-      const uint8_t *from = base + used[x] * stride;
-      const int t = 4 * j - static_cast<int>(reinterpret_cast<uintptr_t>(from) & 3);        // the word's first byte in the run
-      to[q] = used[x] * pitch + j;
-      if (t >= 0 && t + 4 <= n) {
-        w[q] = *reinterpret_cast<const uint32_t *>(from + t);
-      } else {
-        for (int k = 0; k < 4; ++k)
-          if (t + k >= 0 && t + k < n) w[q] |= static_cast<uint32_t>(from[t + k]) << (8 * k);
-      }
+      const int row = used[x], skew = skew_of(row);
+      int head;
+      if (j >= whole_words(n, skew, head)) continue;
+      w[q] = *reinterpret_cast<const uint4 *>(base + row * stride + head + 16 * j);
+      to[q] = buf + row * pitch + skew + head + 16 * j;
     }
 #pragma unroll
     for (int q = 0; q < BATCH; ++q)
-      if (to[q] >= 0) buf[to[q]] = w[q];
+      if (to[q]) *reinterpret_cast<uint4 *>(to[q]) = w[q];
+  }
+  // place e of 32 of the bytes before and behind the whole words; -1: none
+  auto end_byte = [&](int e, int skew) -> int {
+    int head;
+    const int behind = 16 * whole_words(n, skew, head) + head + e - 16;
+    return e < 16 ? (e < head ? e : -1) : behind < n ? behind : -1;
+  };
+  for (int i = threadIdx.x; i < n_used * 32; i += RE_T) {
+    const int row = used[i >> 5], skew = skew_of(row), t = end_byte(i & 31, skew);
+    if (t >= 0) buf[row * pitch + skew + t] = base[row * stride + t];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < beams * words; i += RE_T) {
-    const int b = i / words, j = i - b * words;
-    if (par[b] == b) continue;
-    uint8_t *to = base + b * stride;
-    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(to) & 3),
-              off = static_cast<int>(reinterpret_cast<uintptr_t>(base + par[b] * stride) & 3) - skew;
-    const uint32_t *src = buf + par[b] * pitch;
-    const int t = 4 * j - skew, x = off < 0 ? j - 1 : j;
-    if (t >= n) continue;
-    const uint32_t w = __funnelshift_r(src[max(x, 0)], src[x + 1], 8 * (off & 3));
-    if (t >= 0 && t + 4 <= n) {
-      *reinterpret_cast<uint32_t *>(to + t) = w;
-    } else {
-      for (int k = 0; k < 4; ++k)
-        if (t + k >= 0 && t + k < n) to[t + k] = static_cast<uint8_t>(w >> (8 * k));
-    }
+  for (int i = threadIdx.x; i < beams << shift; i += RE_T) {
+    const int row = i >> shift, j = i & (slots - 1), from = par[row];
+    if (from == row) continue;
+    int head;
+    if (j >= whole_words(n, skew_of(row), head)) continue;
+    const int at = skew_of(from) + head + 16 * j;
+    const uint4 *src = reinterpret_cast<const uint4 *>(buf + from * pitch + (at & ~15));
+    const uint4 a = src[0], b = at & 15 ? src[1] : make_uint4(0u, 0u, 0u, 0u);
+    // of the eight words the four from at / 4 on, and one more
+    const bool two = at & 8, one = at & 4;
+    const uint32_t x0 = two ? a.z : a.x, x1 = two ? a.w : a.y, x2 = two ? b.x : a.z, x3 = two ? b.y : a.w, x4 = two ? b.z : b.x, x5 = two ? b.w : b.y;
+    const uint32_t y0 = one ? x1 : x0, y1 = one ? x2 : x1, y2 = one ? x3 : x2, y3 = one ? x4 : x3, y4 = one ? x5 : x4;
+    const int by = 8 * (at & 3);
+    *reinterpret_cast<uint4 *>(base + row * stride + head + 16 * j) =
+        make_uint4(__funnelshift_r(y0, y1, by), __funnelshift_r(y1, y2, by), __funnelshift_r(y2, y3, by), __funnelshift_r(y3, y4, by));
+  }
+  for (int i = threadIdx.x; i < beams * 32; i += RE_T) {
+    const int row = i >> 5, from = par[row], t = end_byte(i & 31, skew_of(row));
+    if (from != row && t >= 0) base[row * stride + t] = buf[from * pitch + skew_of(from) + t];
   }
 }
 
-template <int MOST>
-__global__ void __launch_bounds__(RE_T) beam_reorder_kernel(const __grid_constant__ ReorderParams p) {
+// RUNS: some state is loose; 64 registers then, for more blocks an SM (runs of 5 rows: 15.6, 10.7
+// us), which columns of 8 rows would pay for (15.0, 24.5).
+template <int MOST, bool RUNS>
+__global__ void __launch_bounds__(RE_T, !RUNS ? 1 : MOST <= 8 ? 4 : 2) beam_reorder_kernel(const __grid_constant__ ReorderParams p) {
   __shared__ int par[ATTN_BEAM_MAX], used[ATTN_BEAM_MAX], n_used;
-  __shared__ uint32_t buf[RE_BUF / 4 + 2 * ATTN_BEAM_MAX];
+  extern __shared__ uint4 runs[];       // run_pitch(beams) bytes a row, where some state is loose
   after_previous();
   admit_next();
   int s = 0;
@@ -625,7 +646,7 @@ __global__ void __launch_bounds__(RE_T) beam_reorder_kernel(const __grid_constan
       continue;
     }
     uint8_t *base = st.at + row0 * st.stride + at;
-    if (!st.loose) {
+    if (!RUNS || !st.loose) {
       if (at + 16 * threadIdx.x < st.bytes) move_column<MOST>(base + 16 * threadIdx.x, st.stride, par, p.beams);
     } else {
       if (b < 32) {          // the rows that others become
@@ -641,7 +662,7 @@ __global__ void __launch_bounds__(RE_T) beam_reorder_kernel(const __grid_constan
         if (b == 0) n_used = count;
       }
       __syncthreads();
-      move_run(base, st.stride, static_cast<int>(min(static_cast<long long>(each), st.bytes - at)), par, used, n_used, p.beams, buf);
+      move_run(base, st.stride, static_cast<int>(min(static_cast<long long>(each), st.bytes - at)), par, used, n_used, p.beams, reinterpret_cast<uint8_t *>(runs));
     }
   }
 }
@@ -737,6 +758,7 @@ int attn_beam_reorder(void *const *h_states, const int64_t *h_row_bytes, const i
   ReorderParams p;
   std::memset(&p, 0, sizeof(p));
   int64_t units = 0;
+  bool runs = false;
   for (int i = 0; i < n_states; ++i) {
     const int64_t bytes = h_row_bytes[i], stride = h_row_strides[i];
     if (bytes < 0 || stride < bytes) return ATTN_ERR_INVALID_ARG;
@@ -746,6 +768,7 @@ int attn_beam_reorder(void *const *h_states, const int64_t *h_row_bytes, const i
       if (p.s[j].at == h_states[i]) return ATTN_ERR_INVALID_ARG;
     const uint64_t all = reinterpret_cast<uintptr_t>(h_states[i]) | static_cast<uint64_t>(bytes) | static_cast<uint64_t>(stride);
     const int loose = (all & 15) || beams > 16;
+    runs |= loose;
     const int64_t each = unit_bytes(loose, beams);
     p.s[p.n_states++] = State{static_cast<uint8_t *>(h_states[i]), stride, bytes, loose, static_cast<int>(units)};
     units += (bytes + each - 1) / each * groups;
@@ -759,9 +782,10 @@ int attn_beam_reorder(void *const *h_states, const int64_t *h_row_bytes, const i
   if (!(p.status = paged_status())) return ATTN_ERR_CUDA;
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  auto kern = beams <= 4 ? beam_reorder_kernel<4> : beams <= 8 ? beam_reorder_kernel<8> : beam_reorder_kernel<16>;
+  auto kern = runs ? beams <= 4 ? beam_reorder_kernel<4, true> : beams <= 8 ? beam_reorder_kernel<8, true> : beam_reorder_kernel<16, true>
+                   : beams <= 4 ? beam_reorder_kernel<4, false> : beams <= 8 ? beam_reorder_kernel<8, false> : beam_reorder_kernel<16, false>;
   const int64_t grid = sms * 16;
-  return launch_after(kern, dim3(static_cast<unsigned>(units < grid ? units : grid)), RE_T, 0, reinterpret_cast<cudaStream_t>(stream), p);
+  return launch_after(kern, dim3(static_cast<unsigned>(units < grid ? units : grid)), RE_T, runs ? beams * run_pitch(beams) : 0, reinterpret_cast<cudaStream_t>(stream), p);
 }
 
 }  // extern "C"

@@ -168,8 +168,8 @@ bool short_call(const PagedParams &p) {
 // two passes over the keys, since the tiles turn every code into an operand before they
 // begin and fill 128 rows.  16 sequences of 8192 keys, 8 key/value heads of 128, e4m3, rows
 // against tiles: 20 rows 120, 144 us; 32 rows 123, 145; 40 rows 169, 150.  int8: 32 rows 130,
-// 138; 40 rows 181, 143.  Of 64 columns, int8: 32 rows 96, 93; 40 rows 136, 97; 32 sequences
-// of 1500 keys: 43, 45; 58, 46.  What the kernel chose is left in p and, the rows of a piece,
+// 138; 40 rows 181, 143.  Of 64 columns, int8: 32 rows 85, 93; 40 rows 118, 97; 32 sequences
+// of 1500 keys: 40, 45; 51, 46.  What the kernel chose is left in p and, the rows of a piece,
 // in `tile_rows`.
 int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
   if (static_cast<int64_t>(tokens) * p.G > (p.bits8 ? 32 : 16)) {

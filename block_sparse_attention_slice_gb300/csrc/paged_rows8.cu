@@ -41,7 +41,6 @@
 namespace attn {
 
 constexpr int R8_ROWS = 16;
-constexpr int R8_WARPS = 8;
 constexpr int R8_KL = 5;           // a slab is 32 keys
 constexpr float R8_TAU = 8.0f;
 
@@ -58,9 +57,9 @@ struct __align__(16) Slab8 {
   int rt, q0, nq, len;        // row tile; the sequence's tokens and length
 };
 
-template <int D, int NST>
+template <int D, int NST, int W>
 struct Rows8Smem {
-  static constexpr int W = R8_WARPS, KEYS = 1 << R8_KL;
+  static constexpr int KEYS = 1 << R8_KL;
   static constexpr int PART = KEYS * D;                         // keys or values of one slab
   static constexpr int SCALES = 2 * PART, STAGE = 2 * PART + 2 * KEYS * 4;
   static constexpr int NOTE = W * NST * STAGE;                  // Slab8 [W][NST]
@@ -71,9 +70,11 @@ struct Rows8Smem {
   }
 };
 
-template <int D, int NST, int FMT>
-__global__ void __launch_bounds__(R8_WARPS * 32, 1) paged_rows8_kernel(const PagedParams p, const int keep_infos) {
-  using S = Rows8Smem<D, NST>;
+// W: warps of a CTA.  At head dim 64 the 168 registers that 12 of them leave a thread are enough (8: 48
+// sequences, window 2048, 20 rows 39.0 us, 12: 36.0; 16 sequences of 8192 keys 92, 80); at 128 they are not.
+template <int D, int NST, int FMT, int W>
+__global__ void __launch_bounds__(W * 32, 1) paged_rows8_kernel(const PagedParams p, const int keep_infos) {
+  using S = Rows8Smem<D, NST, W>;
   using C = F16Codes<FMT>;
   constexpr int KL = R8_KL, KEYS = S::KEYS, NSUB = KEYS / 16, NB = KEYS / 8;
   constexpr int NOT_SEEN = INT_MIN;
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(R8_WARPS * 32, 1) paged_rows8_kernel(const Pag
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int sms = gridDim.x;
   if (p.share.side) {
-    sms = my_sms<S::W * 32>(p, sms, reinterpret_cast<longlong2 *>(rows8_smem));
+    sms = my_sms<W * 32>(p, sms, reinterpret_cast<longlong2 *>(rows8_smem));
     if (static_cast<int>(blockIdx.x) >= sms) {
       end_after_previous(p);
       return;
@@ -94,12 +95,12 @@ __global__ void __launch_bounds__(R8_WARPS * 32, 1) paged_rows8_kernel(const Pag
     __syncthreads();
   }
   if (p.warp_plan) make_warp_plan<R8_ROWS, KL>(p, 0, rows8_smem + S::FIRST + warp * PLAN_WARP, first, info);
-  else make_plan<R8_ROWS, KL, S::W * 32>(p, 0, first, info, scan);
+  else make_plan<R8_ROWS, KL, W * 32>(p, 0, first, info, scan);
   finish_empty<D, R8_ROWS, KL>(p, info, 0, sms);
 
-  const int n_spans = p.share.side ? sms * S::W / p.hp : p.n_spans;
+  const int n_spans = p.share.side ? sms * W / p.hp : p.n_spans;
   const long long total = first[p.n_seqs], span = span_of(total, n_spans);
-  const long long worker = static_cast<long long>(blockIdx.x) * S::W + warp, span_no = worker / p.hp;
+  const long long worker = static_cast<long long>(blockIdx.x) * W + warp, span_no = worker / p.hp;
   const int sub = static_cast<int>(worker - span_no * p.hp);    // this warp's head of a group
   const long long from = min(span_no * span, total), to = min(total, from + span);
   if (from >= to) {
@@ -514,15 +515,15 @@ __global__ void __launch_bounds__(R8_WARPS * 32, 1) paged_rows8_kernel(const Pag
 
 // ---------------------------------------------------------------------- host
 
-template <int D, int NST, int FMT>
+template <int D, int NST, int FMT, int W>
 static int launch_rows8(PagedParams &p, cudaStream_t s) {
-  using S = Rows8Smem<D, NST>;
+  using S = Rows8Smem<D, NST, W>;
   constexpr int kDev = 64;
   static bool done[kDev] = {};
   static std::mutex mu;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDev) return ATTN_ERR_CUDA;
-  auto kern = paged_rows8_kernel<D, NST, FMT>;
+  auto kern = paged_rows8_kernel<D, NST, FMT, W>;
   auto join = paged_join_kernel<D, R8_ROWS, true>;
   {
     std::lock_guard<std::mutex> lock(mu);
@@ -530,32 +531,33 @@ static int launch_rows8(PagedParams &p, cudaStream_t s) {
   }
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  // as many heads side by side as divide both the heads and a CTA's warps
+  // as many heads side by side as divide the heads, up to 8
   p.hp = 1;
-  while (p.hp < S::W && p.hk % (2 * p.hp) == 0) p.hp *= 2;
-  p.n_spans = sms * S::W / p.hp;
+  while (p.hp < 8 && p.hk % (2 * p.hp) == 0) p.hp *= 2;
+  p.n_spans = sms * W / p.hp;
   p.warp_plan = p.n_seqs <= 32 && (!p.causal || static_cast<long long>(p.n_tokens) * p.G <= 64 * R8_ROWS);
+  // pieces of 16 rows: of 12 warps at head dim 64, where the workspace has room for the tiles' 512 rows an SM
+  static_assert(W * 2 * R8_ROWS <= 2 * 256, "pieces");
+  const size_t slots = static_cast<size_t>(sms) * W * 2 * R8_ROWS;
+  p.part_ml = p.part_o + slots * D;
+  p.cuts = reinterpret_cast<Cut *>(p.part_ml + slots * 2);
   const bool infos = S::bytes(p, true) <= kSmemMax;      // not above 3900 sequences
-  const int rc = launch_after(kern, dim3(sms), S::W * 32, S::bytes(p, infos), s, p, infos ? 1 : 0);
+  const int rc = launch_after(kern, dim3(sms), W * 32, S::bytes(p, infos), s, p, infos ? 1 : 0);
   if (rc != ATTN_OK || p.rec) return rc;
   // few items: each has many pieces, and its rows go to blocks of their own
   const long long items = static_cast<long long>(p.n_seqs) * p.hk;
-  return launch_after(join, dim3(sms * S::W, items * 8 < sms * S::W ? 4 : 1), 256, 0, s, p);
+  return launch_after(join, dim3(sms * W, items * 8 < sms * W ? 4 : 1), 256, 0, s, p);
 }
 
-// The workspace is that of paged_rows_launch: as many workers, of as many rows.
 int paged_rows8_launch(PagedParams &p, int d, cudaStream_t s) {
-  const int sms = device_sm_count();
-  if (sms <= 0) return ATTN_ERR_CUDA;
-  p.part_ml = p.part_o + paged_piece_floats(R8_ROWS, d);
-  p.cuts = reinterpret_cast<Cut *>(p.part_ml + static_cast<size_t>(sms) * R8_WARPS * 2 * R8_ROWS * 2);
   const bool many = p.n_seqs > 1024, e4m3 = p.format == ATTN_CODES_E4M3;
+  constexpr int I8 = ATTN_CODES_INT8, E4 = ATTN_CODES_E4M3;
   if (d == 128) {
-    if (many) return e4m3 ? launch_rows8<128, 2, ATTN_CODES_E4M3>(p, s) : launch_rows8<128, 2, ATTN_CODES_INT8>(p, s);
-    return e4m3 ? launch_rows8<128, 3, ATTN_CODES_E4M3>(p, s) : launch_rows8<128, 3, ATTN_CODES_INT8>(p, s);
+    if (many) return e4m3 ? launch_rows8<128, 2, E4, 8>(p, s) : launch_rows8<128, 2, I8, 8>(p, s);
+    return e4m3 ? launch_rows8<128, 3, E4, 8>(p, s) : launch_rows8<128, 3, I8, 8>(p, s);
   }
-  if (many) return e4m3 ? launch_rows8<64, 2, ATTN_CODES_E4M3>(p, s) : launch_rows8<64, 2, ATTN_CODES_INT8>(p, s);
-  return e4m3 ? launch_rows8<64, 4, ATTN_CODES_E4M3>(p, s) : launch_rows8<64, 4, ATTN_CODES_INT8>(p, s);
+  if (many) return e4m3 ? launch_rows8<64, 2, E4, 12>(p, s) : launch_rows8<64, 2, I8, 12>(p, s);
+  return e4m3 ? launch_rows8<64, 3, E4, 12>(p, s) : launch_rows8<64, 3, I8, 12>(p, s);
 }
 
 }  // namespace attn

@@ -151,16 +151,19 @@ PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, co
   return p;
 }
 
-// Whether no warp of the row kernels can have more than 6 slabs of 32 keys: what counts then
-// is their start, and the kernel for few rows has the longer one (12 warps, tensor maps).
-// One sequence of 4 query heads to each of 8 key/value heads of 128, it against the kernel
-// for 16 rows: 512 keys 16.9, 14.2 us; 8192 20.7, 18.0; 16384 23.9, 22.7; 32768 29.2, 28.6.
-// Four sequences: 4096 keys 24.3, 22.1; 6144 25.8, 26.0; 8192 29.8, 31.1; 32768 64.1, 75.5.
-// Of 64 columns: 4096 keys 21.9, 18.8; 8192 25.5, 24.8; 12288 29.2, 30.4; 32768 50.6, 56.1.
-bool short_call(const PagedParams &p) {
-  long long keys = static_cast<long long>(p.max_pages) << p.page_shift;
-  if (p.causal && p.window > 0) keys = std::min<long long>(keys, static_cast<long long>(p.window) + p.sinks + 32);
-  return keys * p.n_seqs * p.hk <= 6 * 32ll * 8 * device_sm_count();
+// Whether no warp of the row kernels of codes can have more than a few slabs of 32 keys: what
+// counts then is their start.  12 warps take the register file, so that a join's blocks wait
+// for its end, and the kernel for few rows has tensor maps to read besides.  4 query heads to each
+// of 8 key/value heads of 128, that kernel against the one for 16 rows.  One sequence: 512 keys
+// 16.9, 14.2 us; 8192 20.7, 18.0; 16384 23.9, 22.7; 32768 29.2, 28.6.  Four: 4096 keys 24.3,
+// 22.1; 6144 25.8, 26.0; 8192 29.8, 31.1; 32768 64.1, 75.5.  Of 64 columns, four sequences, against
+// 8 warps for 16 rows: 4096 keys 21.9, 18.6; 8192 25.5, 24.7; 12288 29.2, 30.2; 32768 50.4, 55.7;
+// and for 16 rows 12 warps against 8: 4096 28.2, 23.3; 8192 31.9, 30.7; 12288 35.5, 36.3; 32768
+// 56.8, 61.7; 28 rows, which are two passes: 4096 31.8, 30.8; 6144 35.4, 36.3; 32768 89, 99.5.
+bool short_call(const PagedParams &p, int d, int64_t rows) {
+  double keys = static_cast<double>(static_cast<int64_t>(p.max_pages) << p.page_shift);
+  if (p.causal && p.window > 0) keys = std::min(keys, static_cast<double>(p.window) + p.sinks + 32);
+  return keys * p.n_seqs * p.hk * static_cast<double>((rows + 15) / 16) <= (d == 64 ? 9 : 6) * 32.0 * 8 * device_sm_count();
 }
 
 // Items of up to 16 rows (query heads of one key/value head times tokens) go to
@@ -172,18 +175,22 @@ bool short_call(const PagedParams &p) {
 // of 1500 keys: 40, 45; 51, 46.  What the kernel chose is left in p and, the rows of a piece,
 // in `tile_rows`.
 int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_rows) {
-  if (static_cast<int64_t>(tokens) * p.G > (p.bits8 ? 32 : 16)) {
+  const int64_t rows = static_cast<int64_t>(tokens) * p.G;
+  if (rows > (p.bits8 ? 32 : 16)) {
     const int rc = paged_tiles_launch(p, d, tokens, s, tile_rows);
     if (rc != ATTN_ERR_UNSUPPORTED) return rc;
   }
   if (p.share.side == 1) p.share.side = 0;     // two passes share the SMs only where tiles are the first
-  if (p.bits8 && static_cast<int64_t>(tokens) * p.G <= 8 && !short_call(p)) {
+  *tile_rows = 16;
+  if (!p.bits8) return paged_rows_launch(p, d, s);
+  const bool brief = short_call(p, d, rows);
+  if (rows <= 8 && !brief) {
     *tile_rows = 8;
     const int rc = paged_few8_launch(p, d, s);
     if (rc != ATTN_ERR_UNSUPPORTED) return rc;
+    *tile_rows = 16;
   }
-  *tile_rows = 16;
-  return p.bits8 ? paged_rows8_launch(p, d, s) : paged_rows_launch(p, d, s);
+  return paged_rows8_launch(p, d, brief, s);
 }
 
 // The prefix's tiles are bound by their products, what follows it by the cache's

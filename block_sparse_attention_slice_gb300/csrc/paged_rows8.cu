@@ -549,13 +549,16 @@ static int launch_rows8(PagedParams &p, cudaStream_t s) {
   return launch_after(join, dim3(sms * W, items * 8 < sms * W ? 4 : 1), 256, 0, s, p);
 }
 
-int paged_rows8_launch(PagedParams &p, int d, cudaStream_t s) {
+// brief: no warp has many slabs; what counts is then that the join's blocks start beside the kernel's,
+// for which 12 warps of 168 registers leave no room.
+int paged_rows8_launch(PagedParams &p, int d, bool brief, cudaStream_t s) {
   const bool many = p.n_seqs > 1024, e4m3 = p.format == ATTN_CODES_E4M3;
   constexpr int I8 = ATTN_CODES_INT8, E4 = ATTN_CODES_E4M3;
   if (d == 128) {
     if (many) return e4m3 ? launch_rows8<128, 2, E4, 8>(p, s) : launch_rows8<128, 2, I8, 8>(p, s);
     return e4m3 ? launch_rows8<128, 3, E4, 8>(p, s) : launch_rows8<128, 3, I8, 8>(p, s);
   }
+  if (brief && !many) return e4m3 ? launch_rows8<64, 4, E4, 8>(p, s) : launch_rows8<64, 4, I8, 8>(p, s);
   if (many) return e4m3 ? launch_rows8<64, 2, E4, 12>(p, s) : launch_rows8<64, 2, I8, 12>(p, s);
   return e4m3 ? launch_rows8<64, 3, E4, 12>(p, s) : launch_rows8<64, 3, I8, 12>(p, s);
 }

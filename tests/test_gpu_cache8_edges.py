@@ -13,7 +13,7 @@ from block_sparse_attention_slice_gb300 import binding as B
 from test_gpu_cache8 import FMTS, Pages, ints, paged, prefix, tokens
 
 pytestmark = pytest.mark.gpu
-WIDE = 300000      # keys that a table row of this width could hold: a call that is not a short one
+WIDE = 400000      # keys that a table row of this width could hold: a call that is not a short one
 
 
 def widen(c):
@@ -43,6 +43,17 @@ def test_windows_of_many_sequences(page, d, window, sinks, fmt):
     lens = [(37 * i) % 150 for i in range(900)]
     c = widen(P8.make(fmt, lens, [1] * len(lens), page, 16, 8, d, seed=window + d, spread=0.5))
     out, lse = paged(c, window, sinks, q_ptr=None)
+    assert attn_last_device_error() == 0
+    P8.check(c, out, lse, P.reference(c, window, sinks))
+
+
+@pytest.mark.parametrize("lens,news,page,hq,hk,d,window,sinks", [
+    ([40, 3, 9], [5, 3, 9], 16, 4, 2, 64, 0, 0), ([300, 130, 0, 5], [7, 8, 1, 6], 32, 8, 2, 64, 20, 3), ([257, 1000], [4, 4], 64, 20, 4, 64, 0, 0),
+    ([3000, 33], [2, 2], 16, 16, 2, 64, 700, 1), ([900, 70], [3, 4], 128, 40, 8, 128, 0, 0), ([5000], [16], 256, 4, 2, 64, 0, 0), ([40] * 70, [5] * 70, 16, 8, 2, 64, 9, 1)])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_up_to_32_rows_of_wide_tables(lens, news, page, hq, hk, d, window, sinks, fmt):
+    c = widen(P8.make(fmt, lens, news, page, hq, hk, d, seed=sum(news) + d, spread=0.5))
+    out, lse = paged(c, window, sinks, max_q=min(max(news), 32 * hk // hq))
     assert attn_last_device_error() == 0
     P8.check(c, out, lse, P.reference(c, window, sinks))
 

@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(W * 32, 1) paged_few8_kernel(const __grid_cons
       for (int k = 0; k < D / 4; ++k) top = max(top, y[k] & 0x7fffu);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^(14 - exponent of the largest), as far as an f32 power of two and its inverse go
-      const int ex = min(max(141 - static_cast<int>(top >> 7), -100), 100);
+      // 2^(14 - exponent of the largest), as far as an f32 power of two and its inverse go: -114 .. 100
+      const int ex = min(141 - static_cast<int>(top >> 7), 100);
       const float f = pow2_of(ex);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(W * 32, 1) paged_few8_kernel(const __grid_cons
       // S^T = K Q^T: x[e]: key 16 j + lr; x[2 + e]: key 16 j + 8 + lr
       float x[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = 0.f;
+      for (int e = 0; e < 4; ++e) x[e] = 0.f;
 #pragma unroll
       for (int hh = 0; hh < D / 64; ++hh) {
         const uint4 u = lds16(ks + (k_at ^ (hh << 6)) + 16 * j * D), v = lds16(ks + (k_at ^ (hh << 6)) + (16 * j + 8) * D);
@@ -366,33 +366,33 @@ __global__ void __launch_bounds__(W * 32, 1) paged_few8_kernel(const __grid_cons
       const int key = key0 + 16 * j;
       if (key + 16 > all_hi || (key < all_lo && key + 16 > p.sinks)) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 2 * c + e;
-            long long row;
-            const int pos = r < rows_here ? (p.causal ? item_len - item_nq + token_of(r, row) : item_len - 1) : -1,
-                      lo = p.causal && p.window > 0 ? pos - p.window + 1 : 0;
+        for (int e = 0; e < 2; ++e) {
+          const int r = 2 * c + e;
+          long long row;
+          const int pos = r < rows_here ? (p.causal ? item_len - item_nq + token_of(r, row) : item_len - 1) : -1,
+                    lo = p.causal && p.window > 0 ? pos - p.window + 1 : 0;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int k = key + 8 * u + lr;
-              if (!(k <= pos && (k >= lo || k < p.sinks))) x[2 * u + e] = -INFINITY;
-            }
+          for (int u = 0; u < 2; ++u) {
+            const int k = key + 8 * u + lr;
+            if (!(k <= pos && (k >= lo || k < p.sinks))) x[2 * u + e] = -INFINITY;
           }
+        }
       }
       // the rows' maxima are looked at together only where one of a lane's scores calls for it
       bool high = false;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) high |= fmaxf(x[e], x[2 + e]) > m[e] + F8_TAU;
+      for (int e = 0; e < 2; ++e) high |= fmaxf(x[e], x[2 + e]) > m[e] + F8_TAU;
       if (__any_sync(0xffffffffu, high)) {
         float f[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float a = over_keys(fmaxf(x[e], x[2 + e]));
-            const bool g = a > m[e] + F8_TAU;
-            f[e] = g ? ex2_approx(m[e] - a) : 1.f;
-            if (g) m[e] = a;
-            unset |= static_cast<unsigned>(g) << (e);
-            l[e] *= f[e];
-          }
+        for (int e = 0; e < 2; ++e) {
+          const float a = over_keys(fmaxf(x[e], x[2 + e]));
+          const bool g = a > m[e] + F8_TAU;
+          f[e] = g ? ex2_approx(m[e] - a) : 1.f;
+          if (g) m[e] = a;
+          unset |= static_cast<unsigned>(g) << e;
+          l[e] *= f[e];
+        }
         rescale(f);
       }
       const float v0 = lds4(sc + KEYS * 4 + j * 64), v1 = lds4(sc + KEYS * 4 + j * 64 + 32);
@@ -418,22 +418,22 @@ __global__ void __launch_bounds__(W * 32, 1) paged_few8_kernel(const __grid_cons
         float f[2];
         bool moved = false;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float a = over_keys(w[e]);
-            const unsigned bit = 1u << (e);
-            f[e] = 1.f;
-            if (a > 32768.f || ((unset & bit) && a > 0.f && a < 1.f)) {
-              const int by = min(max(134 - static_cast<int>(__float_as_uint(a) >> 23), max(-126 - lc[e], -126)), min(126 - lc[e], 126));
-              f[e] = pow2_of(by);
-              lc[e] += by;
-              moved = true;
-            }
-            if (a > 0.f) unset &= ~bit;
+        for (int e = 0; e < 2; ++e) {
+          const float a = over_keys(w[e]);
+          const unsigned bit = 1u << e;
+          f[e] = 1.f;
+          if (a > 32768.f || ((unset & bit) && a > 0.f && a < 1.f)) {
+            const int by = min(max(134 - static_cast<int>(__float_as_uint(a) >> 23), max(-126 - lc[e], -126)), min(126 - lc[e], 126));
+            f[e] = pow2_of(by);
+            lc[e] += by;
+            moved = true;
           }
+          if (a > 0.f) unset &= ~bit;
+        }
         if (__any_sync(0xffffffffu, moved)) {
           rescale(f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] *= f[e & 1];
+          for (int e = 0; e < 4; ++e) x[e] *= f[e & 1];
         }
       }
       // O^T += V^T W^T: row lr of block mb is column (D / 8) lr + 2 mb, row lr + 8 the next one
@@ -467,52 +467,52 @@ __global__ void __launch_bounds__(W * 32, 1) paged_few8_kernel(const __grid_cons
       int np = 0, slot0 = 0;
       if (p.rec && piece0 == 0) item_pieces(from + n - tile_i, tile_n, span_no, span, from, np, slot0);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float sum = l[e];
-          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-          const int r = 2 * c + e;
-          if (r >= rows_here) continue;
-          long long row;
-          const int t = token_of(r, row);
-          if (p.rec && piece0 == 0 && lr == 0) p.rec[row] = Rec4{static_cast<int>(worker), slot0, np, r};
-          // this lane's D / 8 columns in a row; the row's power of two leaves
-          float y[D / 8];
-          const float f = pow2_of(-lc[e]);
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[e];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int r = 2 * c + e;
+        if (r >= rows_here) continue;
+        long long row;
+        const int t = token_of(r, row);
+        if (p.rec && piece0 == 0 && lr == 0) p.rec[row] = Rec4{static_cast<int>(worker), slot0, np, r};
+        // this lane's D / 8 columns in a row; the row's power of two leaves
+        float y[D / 8];
+        const float f = pow2_of(-lc[e]);
 #pragma unroll
-          for (int mb = 0; mb < D / 16; ++mb) {
-            y[2 * mb] = o[mb][e] * f;
-            y[2 * mb + 1] = o[mb][2 + e] * f;
-          }
-          if (whole && !p.rec) {
-            float fo, lse;
-            row_final(m[e], sum, fo, lse);
-            const long long at = row * D + lr * (D / 8);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) y[i] = finished(y[i], fo);
-            if (p.out_f32) {
-#pragma unroll
-              for (int i = 0; i < D / 8; i += 4)
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < D / 8; i += 8)
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at + i) =
-                    make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]), pack_bf16x2(y[i + 4], y[i + 5]),
-                               pack_bf16x2(y[i + 6], y[i + 7]));
-            }
-            if (lr == 0) p.lse[(static_cast<long long>(item_h) * p.G + item_x0 + r - t * p.G) * p.n_tokens + item_q0 + t] = lse;
-          } else {
-            // to the dense arrays, or to a piece: slot 0 the one a span begins
-            // with, slot 1 one that begins in it and goes on
-            const long long slot = worker * 2 + (n - (tile_i - piece0) == 0 ? 0 : 1), to = whole ? row : slot * F8_ROWS + r;
-            float *po = (whole ? p.dense_o : p.part_o) + to * D + lr * (D / 8);
-#pragma unroll
-            for (int i = 0; i < D / 8; i += 4) *reinterpret_cast<float4 *>(po + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-            if (lr == 0) *reinterpret_cast<float2 *>((whole ? p.dense_ml : p.part_ml) + to * 2) = make_float2(m[e], sum);
-          }
+        for (int mb = 0; mb < D / 16; ++mb) {
+          y[2 * mb] = o[mb][e] * f;
+          y[2 * mb + 1] = o[mb][2 + e] * f;
         }
+        if (whole && !p.rec) {
+          float fo, lse;
+          row_final(m[e], sum, fo, lse);
+          const long long at = row * D + lr * (D / 8);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) y[i] = finished(y[i], fo);
+          if (p.out_f32) {
+#pragma unroll
+            for (int i = 0; i < D / 8; i += 4)
+              *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < D / 8; i += 8)
+              *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at + i) =
+                  make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]), pack_bf16x2(y[i + 4], y[i + 5]),
+                             pack_bf16x2(y[i + 6], y[i + 7]));
+          }
+          if (lr == 0) p.lse[(static_cast<long long>(item_h) * p.G + item_x0 + r - t * p.G) * p.n_tokens + item_q0 + t] = lse;
+        } else {
+          // to the dense arrays, or to a piece: slot 0 the one a span begins
+          // with, slot 1 one that begins in it and goes on
+          const long long slot = worker * 2 + (n - (tile_i - piece0) == 0 ? 0 : 1), to = whole ? row : slot * F8_ROWS + r;
+          float *po = (whole ? p.dense_o : p.part_o) + to * D + lr * (D / 8);
+#pragma unroll
+          for (int i = 0; i < D / 8; i += 4) *reinterpret_cast<float4 *>(po + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          if (lr == 0) *reinterpret_cast<float2 *>((whole ? p.dense_ml : p.part_ml) + to * 2) = make_float2(m[e], sum);
+        }
+      }
     }
   }
   if (lane == 0 && !p.rec && !gave_up) leave_cut<F8_ROWS, KL>(p, in, 0, in.h * p.hp + sub, worker, span_no, span, from, to);

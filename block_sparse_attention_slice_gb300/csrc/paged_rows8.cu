@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(W * 32, 1) paged_rows8_kernel(const PagedParam
         for (int k = 0; k < D / 4; ++k) top = max(top, y[k] & 0x7fffu);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^(14 - exponent of the largest), as far as an f32 power of two and its inverse go
-        const int e = min(max(141 - static_cast<int>(top >> 7), -100), 100);
+        // 2^(14 - exponent of the largest), as far as an f32 power of two and its inverse go: -114 .. 100
+        const int e = min(141 - static_cast<int>(top >> 7), 100);
         const float f = pow2_of(e);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {

@@ -108,7 +108,7 @@ int attn_paged_workspace_bytes(int n_tokens, int hq, int d, int prefix, size_t *
  * a slot, length, q_ptr entry or needed page index out of range.  A sequence
  * with a bad slot, length or q_ptr is taken as one of length 0 or of no
  * tokens; one with a bad page gets outputs of no meaning; others are served.
- * TIMEOUT where a bounded wait of the tensor-core kernel ran out
+ * TIMEOUT where a bounded wait for a kernel's loads or products ran out
  * (attn_set_wait_limit_ns): outputs are then incomplete. */
 int attn_paged_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
                    const attn_pages_t *pages, const attn_seqs_t *seqs, float scale, int window,
@@ -279,7 +279,8 @@ int attn_prefix8_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_
  * magnitude a, M = 127 (int8) or 448 (e4m3): its scale is a / M, and x becomes
  * the code next to x M / a, the even one of two as near (a = 0: scale and codes
  * 0).  Where a value is not finite the scale is NaN and the codes are 0: the
- * head's whole row reads as NaN.  UNSUPPORTED also: scales with a stride of zero,
+ * head's whole row reads as NaN.  Where `seqs` names a row twice, its last
+ * positions may hold codes and scales of different tokens.  UNSUPPORTED also: scales with a stride of zero,
  * hk > 1024. */
 int attn_cache8_write(const attn_pages8_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr,
                       const void *k_new, const void *v_new, int n_tokens, int64_t new_token_stride,

@@ -354,3 +354,29 @@ def test_refusals():
     with pytest.raises(TypeError):
         read(n_tokens=2.5)
     assert attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("max_q,wide", [(1, False), (1, True), (4, False), (20, False)])
+@pytest.mark.parametrize("size", [2.0 ** 118, 2.0 ** -133])
+def test_queries_as_large_and_as_small_as_they_come(fmt, max_q, wide, size):
+    """Large: scores of 1e11 and more, of which the largest alone has a weight; it is rounded once, to bf16 at
+    the coarsest (2^-8).  Small: all scores are 0 to within 1e-30, every weight is 1."""
+    c = P8.make(fmt, [500, 77], [1, 1], 16, 4, 1, 64, seed=3)
+    down = torch.tensor(1e-24 if size > 1 else 1.0)
+    c["ks"], c["k64"] = c["ks"] * down.cuda(), c["k64"] * down.double().item()
+    c["q"] = (c["q"].cpu().double() * size).bfloat16()
+    c["q64"] = c["q"].double().numpy()
+    c["q"] = c["q"].cuda()
+    assert np.isfinite(c["q64"]).all() and np.any(c["q64"])
+    out, lse = paged(widen(c) if wide else c, out_dtype=torch.float32, max_q=max_q)
+    assert attn_last_device_error() == 0
+    O, L, A, _ = P.reference(c)
+    if size > 1:
+        for b, n in enumerate(c["lens"]):       # the inputs leave one key a weight
+            k = oracle.paged.cached_rows(c["k64"], c["table"][b], n)[:, 0]
+            s = np.sort(k @ c["q64"][b].T * c["scale"], axis=0)
+            assert np.all(s[-1] - s[-2] > 1e7) and np.all(s[-1] - s[-2] > 2.0 ** -12 * np.abs(s[-1]))
+    # weights, and sums of up to 500 f32 terms
+    assert np.all(np.abs(out.double().cpu().numpy() - O) <= (2.0 ** -8 + 500 * 2.0 ** -24) * A)
+    assert np.all(np.abs(lse.double().cpu().numpy() - L) <= 2.0 ** -16 * np.abs(L) + 2.0 ** -20)

@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
   __shared__ int isum[BP_T / 32];
   __shared__ unsigned long long list_k[BP_CAP];
   __shared__ int list_b[BP_CAP], list_v[BP_CAP];
-  __shared__ int listed;
+  __shared__ int listed, source[ATTN_BEAM_MAX];
+  __shared__ bool ended[ATTN_BEAM_MAX];
   after_previous();
   admit_next();
   const int g = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = p.splits * p.keep, n = p.beams * per;
@@ -391,12 +392,17 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
   for (int b = warp; b < p.beams; b += BP_T / 32) {
     const long long row = static_cast<long long>(g) * p.beams + b;
     double c = __longlong_as_double(0x7ff8000000000000ll);
+    // all that is read of a beam is asked for at once
+    const float2 y0 = lane < p.splits ? p.ms[row * p.splits + lane] : make_float2(-INFINITY, 0.f);
     const float score = p.scores[row];
-    if (!(p.done && p.done[row]) && score > -INFINITY && score < INFINITY) {
+    const bool over = p.done && p.done[row];
+    const int from = p.slots ? p.slots[row] : static_cast<int>(row);
+    if (lane == 0) ended[b] = over, source[b] = from;
+    if (!over && score > -INFINITY && score < INFINITY) {
       // the parts' sums brought to the largest maximum
       float m = -INFINITY, s = 0.f;
       for (int i0 = 0; i0 < p.splits; i0 += 32) {
-        const float2 y = i0 + lane < p.splits ? p.ms[row * p.splits + i0 + lane] : make_float2(-INFINITY, 0.f);
+        const float2 y = i0 == 0 ? y0 : i0 + lane < p.splits ? p.ms[row * p.splits + i0 + lane] : make_float2(-INFINITY, 0.f);
         float top = y.x;
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -427,12 +433,12 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
     unsigned long long k = 0;
     if (i < p.keep) {
       const float score = p.scores[row];
-      const bool ended = p.done && p.done[row] && score > -INFINITY && score < INFINITY;
-      if (ended && i == 0) {
+      const bool over = ended[b] && score > -INFINITY && score < INFINITY;
+      if (over && i == 0) {
         v = p.eos;
         k = key_of(static_cast<double>(score));
       } else {
-        v = ended ? i - 1 + (i - 1 >= p.eos) : i;
+        v = over ? i - 1 + (i - 1 >= p.eos) : i;
         if (v < p.vocab) k = key_of(-static_cast<double>(INFINITY));
       }
     }
@@ -477,8 +483,8 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
     p.out_scores[to] = static_cast<float>(value_of(k));
     p.out_parents[to] = static_cast<int32_t>(row);
     p.out_tokens[to] = v;
-    if (p.out_done) p.out_done[to] = (p.done && p.done[row]) || v == p.eos;
-    if (p.out_src) p.out_src[to] = p.slots ? p.slots[row] : static_cast<int32_t>(row);
+    if (p.out_done) p.out_done[to] = ended[b] || v == p.eos;
+    if (p.out_src) p.out_src[to] = source[b];
   };
   const int m = listed;
   if (m <= BP_CAP) {
@@ -667,10 +673,10 @@ __global__ void __launch_bounds__(RE_T, !RUNS ? 1 : MOST <= 8 ? 4 : 2) beam_reor
   }
 }
 
-// Parts of a row, a warp each: as many as fill the SMs with 24 warps
-// (32, of 64 registers a thread, were slower), of 32 BS_WORDS words at
-// least.  words: of a row, wherever it begins.
-// Not more than leave a group's choice 16384 candidates.
+// Parts of a row, a warp each: as many as fill the SMs with 24 warps (64 prompts of 8 beams
+// and 131072 tokens, the whole step: 63.6 us; 20 warps 69.3; 32, of 64 registers a thread, 72.1),
+// of 32 BS_WORDS words at least.  words: of a row, wherever it begins.  Not more than leave
+// a group's choice 16384 candidates.
 int splits_of(int groups, int beams, int vocab, int keep, int dtype, int sms, int *words) {
   const int n = dtype == ATTN_DTYPE_F32 ? 4 : 8;
   *words = (vocab + 2 * n - 2) / n;

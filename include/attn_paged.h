@@ -249,7 +249,8 @@ int attn_cache_read(const attn_pages_t *pages, const attn_seqs_t *seqs, const in
  * and one for its values, [n_pages, page_size, hk] f32, strides in elements,
  * alike for both and not negative.  A value is code * scale.
  * The table operations above serve these pages as they are: attn_cache_copy_pages
- * moves the codes in one call and the scales in another. */
+ * moves the codes in one call and the scales in another.  A code of e4m3 that is no
+ * number (the calls below write none) counts as some value up to 480 or as NaN. */
 enum { ATTN_CODES_INT8 = 0, ATTN_CODES_E4M3 = 1 };
 typedef struct {
   attn_pages_t pages;

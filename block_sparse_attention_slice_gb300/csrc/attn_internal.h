@@ -81,7 +81,7 @@ int paged_check_seqs(const attn_seqs_t *s, int page_size);
 struct PagedParams;
 size_t paged_rows_workspace(int d);
 int paged_rows_launch(PagedParams &p, int d, cudaStream_t s);
-int paged_rows8_launch(PagedParams &p, int d, bool brief, cudaStream_t s);
+int paged_rows8_launch(PagedParams &p, int d, int warps, cudaStream_t s);
 int paged_few8_launch(PagedParams &p, int d, cudaStream_t s);
 int paged_map8(CUtensorMap *m, const void *base, const PagedParams &p, int d, int keys);
 size_t paged_tiles_workspace(int d);

@@ -151,19 +151,32 @@ PagedParams params(const void *q, const int32_t *q_ptr, int n_tokens, int hq, co
   return p;
 }
 
-// Whether no warp of the row kernels of codes can have more than a few slabs of 32 keys: what
-// counts then is their start.  12 warps take the register file, so that a join's blocks wait
-// for its end, and the kernel for few rows has tensor maps to read besides.  4 query heads to each
-// of 8 key/value heads of 128, that kernel against the one for 16 rows.  One sequence: 512 keys
-// 16.9, 14.2 us; 8192 20.7, 18.0; 16384 23.9, 22.7; 32768 29.2, 28.6.  Four: 4096 keys 24.3,
-// 22.1; 6144 25.8, 26.0; 8192 29.8, 31.1; 32768 64.1, 75.5.  Of 64 columns, four sequences, against
-// 8 warps for 16 rows: 4096 keys 21.9, 18.6; 8192 25.5, 24.7; 12288 29.2, 30.2; 32768 50.4, 55.7;
-// and for 16 rows 12 warps against 8: 4096 28.2, 23.3; 8192 31.9, 30.7; 12288 35.5, 36.3; 32768
-// 56.8, 61.7; 28 rows, which are two passes: 4096 31.8, 30.8; 6144 35.4, 36.3; 32768 89, 99.5.
-bool short_call(const PagedParams &p, int d, int64_t rows) {
+// The most slabs of 32 keys that an SM of the row kernels of codes can have.  Where they are few
+// what counts is the kernels' start: a join's blocks, and the next call's, start beside a kernel
+// that leaves them registers.  12 warps leave none, 8 some at head dim 64, 4 at either; and the
+// kernel for few rows has tensor maps to read besides.
+double slabs_of(const PagedParams &p, int64_t rows) {
   double keys = static_cast<double>(static_cast<int64_t>(p.max_pages) << p.page_shift);
   if (p.causal && p.window > 0) keys = std::min(keys, static_cast<double>(p.window) + p.sinks + 32);
-  return keys * p.n_seqs * p.hk * static_cast<double>((rows + 15) / 16) <= (d == 64 ? 9 : 6) * 32.0 * 8 * device_sm_count();
+  return keys * p.n_seqs * p.hk * static_cast<double>((rows + 15) / 16) / (32.0 * device_sm_count());
+}
+
+// The kernel for few rows, from 6 (head dim 64: 9) slabs for each of 8 warps.  4 query heads to
+// each of 8 key/value heads of 128, it against 8 warps of the one for 16 rows.  One sequence: 512 keys 16.9,
+// 14.2 us; 8192 20.7, 18.0; 16384 23.9, 22.7; 32768 29.2, 28.6.  Four: 4096 keys 24.3, 22.1;
+// 6144 25.8, 26.0; 8192 29.8, 31.1; 32768 64.1, 75.5.  Of 64 columns, four sequences: 4096 keys 21.9,
+// 18.6; 8192 25.5, 24.7; 12288 29.2, 30.2; 32768 50.4, 55.7.
+bool few_slabs(double slabs, int d) { return slabs <= 8 * (d == 64 ? 9 : 6); }
+
+// Warps of the kernel for 16 rows.  8 against 4, one sequence of 128 columns: 512 keys 14.0, 11.9 us; 4096
+// 15.9, 14.1; 12288 20.6, 20.1; 16384 22.5, 24.5; four: 512 15.1, 12.7; 1024 15.4, 14.5; 2048 17.4,
+// 18.6.  Of 64 columns, one: 512 12.6, 11.0; 8192 15.4, 14.5; 32768 22.8, 25.4; four: 2048 15.6, 14.4; 4096
+// 18.5, 19.4.  12 against 8, of 64 columns, 16 rows, four sequences: 4096 28.2, 23.3; 8192 31.9, 30.7;
+// 12288 35.5, 36.3; 32768 56.8, 61.7; 28 rows, which are two passes: 4096 31.8, 30.8; 6144 35.4,
+// 36.3; 32768 89, 99.5.
+int rows8_warps(double slabs, int d) {
+  if (slabs <= 4 * (d == 64 ? 5 : 3)) return 4;
+  return d == 128 || few_slabs(slabs, d) ? 8 : 12;
 }
 
 // Items of up to 16 rows (query heads of one key/value head times tokens) go to
@@ -183,14 +196,14 @@ int paged_launch(PagedParams &p, int d, int tokens, cudaStream_t s, int *tile_ro
   if (p.share.side == 1) p.share.side = 0;     // two passes share the SMs only where tiles are the first
   *tile_rows = 16;
   if (!p.bits8) return paged_rows_launch(p, d, s);
-  const bool brief = short_call(p, d, rows);
-  if (rows <= 8 && !brief) {
+  const double slabs = slabs_of(p, rows);
+  if (rows <= 8 && !few_slabs(slabs, d)) {
     *tile_rows = 8;
     const int rc = paged_few8_launch(p, d, s);
     if (rc != ATTN_ERR_UNSUPPORTED) return rc;
     *tile_rows = 16;
   }
-  return paged_rows8_launch(p, d, brief, s);
+  return paged_rows8_launch(p, d, rows8_warps(slabs, d), s);
 }
 
 // The prefix's tiles are bound by their products, what follows it by the cache's

@@ -74,7 +74,8 @@ struct Rows8Smem {
 };
 
 // W: warps of a CTA.  At head dim 64 the 168 registers that 12 of them leave a thread are enough (8: 48
-// sequences, window 2048, 20 rows 39.0 us, 12: 36.0; 16 sequences of 8192 keys 92, 80); at 128 they are not.
+// sequences, window 2048, 20 rows 39.0 us, 12: 36.0; 16 sequences of 8192 keys 92, 80); at 128 they are not.  Short
+// calls have 4 or 8 (rows8_warps).
 template <int D, int NST, int FMT, int W>
 __global__ void __launch_bounds__(W * 32, 1) paged_rows8_kernel(const PagedParams p, const int keep_infos) {
   using S = Rows8Smem<D, NST, W>;
@@ -552,17 +553,19 @@ static int launch_rows8(PagedParams &p, cudaStream_t s) {
   return launch_after(join, dim3(sms * W, items * 8 < sms * W ? 4 : 1), 256, 0, s, p);
 }
 
-// brief: no warp has many slabs; what counts is then that the join's blocks start beside the kernel's,
-// for which 12 warps of 168 registers leave no room.
-int paged_rows8_launch(PagedParams &p, int d, bool brief, cudaStream_t s) {
+// warps: of a CTA, 4, 8 or (head dim 64) 12; beside the plan of thousands of sequences as many as the
+// largest calls have.
+int paged_rows8_launch(PagedParams &p, int d, int warps, cudaStream_t s) {
   const bool many = p.n_seqs > 1024, e4m3 = p.format == ATTN_CODES_E4M3;
   constexpr int I8 = ATTN_CODES_INT8, E4 = ATTN_CODES_E4M3;
   if (d == 128) {
     if (many) return e4m3 ? launch_rows8<128, 2, E4, 8>(p, s) : launch_rows8<128, 2, I8, 8>(p, s);
+    if (warps == 4) return e4m3 ? launch_rows8<128, 3, E4, 4>(p, s) : launch_rows8<128, 3, I8, 4>(p, s);
     return e4m3 ? launch_rows8<128, 3, E4, 8>(p, s) : launch_rows8<128, 3, I8, 8>(p, s);
   }
-  if (brief && !many) return e4m3 ? launch_rows8<64, 4, E4, 8>(p, s) : launch_rows8<64, 4, I8, 8>(p, s);
   if (many) return e4m3 ? launch_rows8<64, 2, E4, 12>(p, s) : launch_rows8<64, 2, I8, 12>(p, s);
+  if (warps == 4) return e4m3 ? launch_rows8<64, 4, E4, 4>(p, s) : launch_rows8<64, 4, I8, 4>(p, s);
+  if (warps == 8) return e4m3 ? launch_rows8<64, 4, E4, 8>(p, s) : launch_rows8<64, 4, I8, 8>(p, s);
   return e4m3 ? launch_rows8<64, 3, E4, 12>(p, s) : launch_rows8<64, 3, I8, 12>(p, s);
 }
 

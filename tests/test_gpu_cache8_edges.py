@@ -16,12 +16,12 @@ pytestmark = pytest.mark.gpu
 WIDE = 400000      # keys that a table row of this width could hold: a call that is not a short one
 
 
-def widen(c):
+def widen(c, keys=WIDE):
     """The table with more columns, which no length reaches: long sequences are possible then, and the
     kernel for them is taken."""
     for name in ("d_table", "d_ptable"):
         t = c[name]
-        c[name] = torch.cat([t, torch.full((t.shape[0], -(-WIDE // c["k"].shape[1])), 1 << 28, dtype=torch.int32, device="cuda")], 1).contiguous()
+        c[name] = torch.cat([t, torch.full((t.shape[0], -(-keys // c["k"].shape[1])), 1 << 28, dtype=torch.int32, device="cuda")], 1).contiguous()
     return c
 
 
@@ -56,6 +56,18 @@ def test_up_to_32_rows_of_wide_tables(lens, news, page, hq, hk, d, window, sinks
     out, lse = paged(c, window, sinks, max_q=min(max(news), 32 * hk // hq))
     assert attn_last_device_error() == 0
     P8.check(c, out, lse, P.reference(c, window, sinks))
+
+
+@pytest.mark.parametrize("keys", [3000, 12000, 30000])
+@pytest.mark.parametrize("news", [[1, 1, 1], [4, 3, 1], [7, 2, 5]])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_tables_between_narrow_and_wide(keys, news, d, fmt):
+    c = widen(P8.make(fmt, [2700, 333, 16], news, 16, 8, 2, d, seed=keys + d, spread=0.5), keys)
+    for window, sinks in ((0, 0), (2500, 3)):
+        out, lse = paged(c, window, sinks, max_q=max(news))
+        assert attn_last_device_error() == 0
+        P8.check(c, out, lse, P.reference(c, window, sinks))
 
 
 @pytest.mark.parametrize("news", [[2, 2, 1], [1, 0, 2], [7, 5, 1]])

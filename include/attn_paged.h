@@ -265,8 +265,9 @@ typedef struct {
  * negative, finite and, but for 0, above 1e-24; codes and scales behind a
  * sequence's end, and those that no token of the sequence sees, are never used,
  * whatever they hold; a key that some tokens of a sequence see and others do not
- * has to have a value and scale that are finite, as above.  The workspace is that
- * of the calls above. */
+ * has to have a value and scale that are finite, as above.  The outputs of a token
+ * that sees a scale that is not finite mean nothing.  The workspace is that of the
+ * calls above. */
 int attn_paged8_fwd(const void *q, const int32_t *q_ptr, int n_tokens, int max_q, int hq,
                     const attn_pages8_t *pages, const attn_seqs_t *seqs, float scale, int window,
                     int sinks, void *out, int out_dtype, float *lse, void *d_ws, size_t ws_bytes,

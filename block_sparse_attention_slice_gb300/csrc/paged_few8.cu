@@ -220,12 +220,11 @@ __global__ void __launch_bounds__(W * 32, 1) paged_few8_kernel(const __grid_cons
 
   // This lane's rows are 2 c + e, with keys lr and lr + 8 of each 16; it shares them
   // with the lanes of equal c.  As the column of an operand it stands for row lr.
-  // p = 2^(s - m), m the lazy maximum; a value's weight is p vs 2^lc, and so O holds
-  // 2^lc times its sum.  unset, bit e: no weight other than 0 has been met since m
-  // last grew, so lc may not suit what comes.
+  // p = 2^(s - m), m the lazy maximum; a value's weight is p vs 2^lc (warp8.cuh).  unset, bit
+  // e: no weight other than 0 has been met since m last grew, so lc may not suit what comes.
   uint32_t qf[D / 16][2];
   float o[D / 16][4];          // columns (D / 8) lr + 2 mb, of rows e = 0, 1, and the next one
-  float m[2], l[2], rs[2];
+  float m[2], l[2], rs[2], most[2];
   int lc[2];
   unsigned unset = 0;
   int all_lo = 0, all_hi = 0;      // keys in [all_lo, all_hi) are seen by every row
@@ -298,6 +297,7 @@ __global__ void __launch_bounds__(W * 32, 1) paged_few8_kernel(const __grid_cons
       for (int e = 0; e < 2; ++e) {
         m[e] = -INFINITY;
         l[e] = 0.f;
+        most[e] = 0.f;
         lc[e] = 0;
       }
 #pragma unroll
@@ -396,50 +396,40 @@ __global__ void __launch_bounds__(W * 32, 1) paged_few8_kernel(const __grid_cons
           if (g) m[e] = a;
           unset |= static_cast<unsigned>(g) << e;
           l[e] *= f[e];
+          most[e] *= f[e];
         }
         rescale(f);
       }
       const float v0 = lds4(sc + KEYS * 4 + j * 64), v1 = lds4(sc + KEYS * 4 + j * 64 + 32);
       float w[2];            // largest weights, of this lane's keys
       bool look = unset != 0;
-      const uint64_t nm = f2_make(m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]),
-                     cc = f2_make(pow2_of(lc[0]), pow2_of(lc[1]));
+      const uint64_t nm = f2_make(m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]);
       f2_split(f2_add(f2_make(x[0], x[1]), nm), x[0], x[1]);
       f2_split(f2_add(f2_make(x[2], x[3]), nm), x[2], x[3]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = ex2_approx(x[e]);
       l[0] += x[0] + x[2];
       l[1] += x[1] + x[3];
-      f2_split(f2_mul(f2_make(x[0], x[1]), f2_mul(f2_make(v0, v0), cc)), x[0], x[1]);
-      f2_split(f2_mul(f2_make(x[2], x[3]), f2_mul(f2_make(v1, v1), cc)), x[2], x[3]);
+      f2_split(f2_mul(f2_make(x[0], x[1]), f2_make(v0, v0)), x[0], x[1]);
+      f2_split(f2_mul(f2_make(x[2], x[3]), f2_make(v1, v1)), x[2], x[3]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         w[e] = fmaxf(fabsf(x[e]), fabsf(x[2 + e]));
-        look |= w[e] > 32768.f;
+        look |= w[e] > most_at(lc[e]);
       }
       if (__any_sync(0xffffffffu, look)) {
-        // the rows' powers of two are looked at: the largest weight to 2^7 .. 2^8
+        // the rows' powers of two are looked at
         float f[2];
-        bool moved = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float a = over_keys(w[e]);
-          const unsigned bit = 1u << e;
-          f[e] = 1.f;
-          if (a > 32768.f || ((unset & bit) && a > 0.f && a < 1.f)) {
-            const int by = min(max(134 - static_cast<int>(__float_as_uint(a) >> 23), max(-126 - lc[e], -126)), min(126 - lc[e], 126));
-            f[e] = pow2_of(by);
-            lc[e] += by;
-            moved = true;
-          }
-          if (a > 0.f) unset &= ~bit;
+          f[e] = refit(over_keys(w[e]), most[e], lc[e]);
+          if (most[e] > 0.f) unset &= ~(1u << e);
         }
-        if (__any_sync(0xffffffffu, moved)) {
-          rescale(f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] *= f[e & 1];
-        }
+        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) rescale(f);
       }
+      const uint64_t cc = f2_make(pow2_of(lc[0]), pow2_of(lc[1]));
+      f2_split(f2_mul(f2_make(x[0], x[1]), cc), x[0], x[1]);
+      f2_split(f2_mul(f2_make(x[2], x[3]), cc), x[2], x[3]);
       // O^T += V^T W^T: row lr of block mb is column (D / 8) lr + 2 mb, row lr + 8 the next one
       const uint32_t p0 = transposed(pack_f16x2(x[0], x[1])), p1 = transposed(pack_f16x2(x[2], x[3]));
       uint32_t y[4][D / 32];

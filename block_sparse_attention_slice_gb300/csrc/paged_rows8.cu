@@ -199,12 +199,10 @@ __global__ void __launch_bounds__(W * 32, 1) paged_rows8_kernel(const PagedParam
 
   uint32_t qf[D / 16][4];
   float o[D / 8][4];
-  // p = 2^(s - m), m the lazy maximum; a value's weight is p vs 2^lc, and so O holds
-  // 2^lc times its sum.  unset: no weight other than 0 has been met since m last grew,
-  // so lc may not suit what comes.
-  float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f, rs0 = 0.f, rs1 = 0.f;
+  // p = 2^(s - m), m the lazy maximum; a value's weight is p vs 2^lc (warp8.cuh), top the
+  // largest p vs that was looked at.
+  float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f, rs0 = 0.f, rs1 = 0.f, top0 = 0.f, top1 = 0.f;
   int lc0 = 0, lc1 = 0;
-  bool unset0 = true, unset1 = true;
   int pos0 = -1, pos1 = -1, lo0 = 0, lo1 = 0;      // last key a row sees, first of its window
   int all_lo = 0, all_hi = 0;                      // keys in [all_lo, all_hi) are seen by every row
   long long row0 = -1, row1 = -1;                  // (token * hq + head), -1: no row
@@ -286,8 +284,8 @@ __global__ void __launch_bounds__(W * 32, 1) paged_rows8_kernel(const PagedParam
       rs1 = load_q(row1, 1);
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.f;
+      top0 = top1 = 0.f;
       lc0 = lc1 = 0;
-      unset0 = unset1 = true;
 #pragma unroll
       for (int j = 0; j < D / 8; ++j)
 #pragma unroll
@@ -372,14 +370,13 @@ __global__ void __launch_bounds__(W * 32, 1) paged_rows8_kernel(const PagedParam
       const float f0 = g0 ? ex2_approx(m0 - a0) : 1.f, f1 = g1 ? ex2_approx(m1 - a1) : 1.f;
       if (g0) m0 = a0;
       if (g1) m1 = a1;
-      unset0 |= g0;
-      unset1 |= g1;
       l0 *= f0;
       l1 *= f1;
+      top0 *= f0;
+      top1 *= f1;
       rescale(f0, f1);
     }
     const float b0 = m0 == -INFINITY ? 0.f : -m0, b1 = m1 == -INFINITY ? 0.f : -m1;
-    const float c0 = pow2_of(lc0), c1 = pow2_of(lc1);
     float w0 = 0.f, w1 = 0.f;            // largest weights, of this lane's keys
 #pragma unroll
     for (int j = 0; j < NSUB; ++j) {
@@ -394,37 +391,26 @@ __global__ void __launch_bounds__(W * 32, 1) paged_rows8_kernel(const PagedParam
         for (int e = 0; e < 4; ++e) y[e] = ex2_approx(y[e]);
         l0 += y[0] + y[1];
         l1 += y[2] + y[3];
-        times(y[0], y[1], f2_mul(v2[b], f2_make(c0, c0)));
-        times(y[2], y[3], f2_mul(v2[b], f2_make(c1, c1)));
+        times(y[0], y[1], v2[b]);
+        times(y[2], y[3], v2[b]);
         w0 = max3f(w0, fabsf(y[0]), fabsf(y[1]));
         w1 = max3f(w1, fabsf(y[2]), fabsf(y[3]));
       }
     }
-    if (__any_sync(0xffffffffu, unset0 || unset1 || w0 > 32768.f || w1 > 32768.f)) {
-      // the rows' powers of two are looked at: the largest weight to 2^7 .. 2^8
-      auto fit = [&](float w, int &lc, bool &unset) -> float {
+    if (__any_sync(0xffffffffu, top0 < pow2_of(-lc0) || top1 < pow2_of(-lc1) || w0 > most_at(lc0) || w1 > most_at(lc1))) {
+      // the rows' powers of two are looked at
+      auto fit = [](float w, float &top, int &lc) -> float {
         w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 1));
-        w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 2));
-        float f = 1.f;
-        if (w > 32768.f || (unset && w > 0.f && w < 1.f)) {
-          const int by = min(max(134 - static_cast<int>(__float_as_uint(w) >> 23), max(-126 - lc, -126)), min(126 - lc, 126));
-          f = pow2_of(by);
-          lc += by;
-        }
-        if (w > 0.f) unset = false;
-        return f;
+        return refit(fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 2)), top, lc);
       };
-      const float f0 = fit(w0, lc0, unset0), f1 = fit(w1, lc1, unset1);
-      if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
-        rescale(f0, f1);
+      const float f0 = fit(w0, top0, lc0), f1 = fit(w1, top1, lc1);
+      if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) rescale(f0, f1);
+    }
+    const float c0 = pow2_of(lc0), c1 = pow2_of(lc1);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          x[b][0] *= f0;
-          x[b][1] *= f0;
-          x[b][2] *= f1;
-          x[b][3] *= f1;
-        }
-      }
+    for (int b = 0; b < NB; ++b) {
+      times(x[b][0], x[b][1], f2_make(c0, c0));
+      times(x[b][2], x[b][3], f2_make(c1, c1));
     }
     // O += W V: column n of block e is column (D / 8) n + e
 #pragma unroll

@@ -48,4 +48,27 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float pow2_of(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }   // -126 <= e <= 127
 
+// A row's weights w = p vs become f16 times 2^lc, -113 <= lc <= 126, and O holds 2^lc times
+// their sums.  p <= 2^8, so w is formed first, in f32, where it is finite for every vs up to 2^119; the
+// power of two comes last, once it suits: 2^lc vs alone would leave f32 where lc was raised for
+// tiny values and large ones follow.
+// The largest w that 2^lc suits: 2^(15 - lc), infinity at -113.
+__device__ __forceinline__ float most_at(int lc) { return __uint_as_float(static_cast<uint32_t>(142 - lc) << 23); }
+// Fits lc to w, the largest weight of the keys at hand, and `top`, the largest that was looked at
+// before, less what the row's maximum has grown by since: down where w is too large, up where
+// both are below 2^-lc; the larger then comes to 2^7 .. 2^8.  Rising by what O holds as well as by
+// w keeps O in range: it never comes to more than 2^23 times codes and keys.  Returns O's factor.
+__device__ __forceinline__ float refit(float w, float &top, int &lc) {
+  const float t = fmaxf(top, w);
+  float f = 1.f;
+  if (w > most_at(lc) || (t > 0.f && t < pow2_of(-lc))) {
+    int by = min(max(134 - static_cast<int>(__float_as_uint(t) >> 23), -113), 126) - lc;
+    if (top > 0.f) by = min(by, 126);        // 0: O is 0, or below 2^-24 of what comes
+    f = by < -126 ? 0.f : pow2_of(min(by, 126));
+    lc += by;
+  }
+  top = t;
+  return f;
+}
+
 }  // namespace attn

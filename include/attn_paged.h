@@ -262,8 +262,11 @@ typedef struct {
 /* attn_paged_fwd and attn_prefix_fwd over such pages.  Scores and weights take
  * the scales in 32 bits; codes enter the products as they are, so that nothing
  * is rounded that the codes had not been.  Scales are expected not to be
- * negative, finite and, but for 0, above 1e-24; codes and scales behind a
- * sequence's end, and those that no token of the sequence sees, are never used,
+ * negative, finite and, but for 0, above 1e-24, and may lie as far apart as that.
+ * What is formed in 32 bits has to be finite there: a query's products with codes,
+ * its largest magnitude times `scale` and a key's scale, and 2^8 times the sum of a
+ * sequence's values (which scales up to 1e24 keep to at any length).  Codes and
+ * scales behind a sequence's end, and those that no token of the sequence sees, are never used,
  * whatever they hold; a key that some tokens of a sequence see and others do not
  * has to have a value and scale that are finite, as above.  The outputs of a token
  * that sees a scale that is not finite mean nothing.  The workspace is that of the

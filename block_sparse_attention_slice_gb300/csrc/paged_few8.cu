@@ -84,6 +84,7 @@ struct Few8Smem {
   static constexpr int PART = KEYS * D, STAGE = 2 * PART;       // keys or values of one slab; both
   static constexpr int SCALES = W * NST * STAGE;                // [W][NST][keys', values'][KEYS]
   static constexpr int NOTE = SCALES + W * NST * 2 * KEYS * 4;  // FewSlab [W][NST]
+  static_assert(W * NST * sizeof(FewSlab) >= W * 16, "my_sms puts its sums where the notes will be");
   static constexpr int BAR = NOTE + W * NST * static_cast<int>(sizeof(FewSlab));
   static constexpr int SCAN = BAR + (W * NST * 8 + 15) / 16 * 16;
   static constexpr int FIRST = SCAN + (W + 2) / 2 * 16;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(W * 32, 1) paged_few8_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int sms = gridDim.x;
   if (p.share.side) {
-    sms = my_sms<W * 32>(p, sms, reinterpret_cast<longlong2 *>(few8_smem));
+    sms = my_sms<W * 32>(p, sms, reinterpret_cast<longlong2 *>(few8_smem + S::NOTE));      // not in the ring, which TMA writes
     if (static_cast<int>(blockIdx.x) >= sms) {
       end_after_previous(p);
       return;

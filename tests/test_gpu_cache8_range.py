@@ -8,7 +8,8 @@ import torch
 from block_sparse_attention_slice_gb300 import attn_last_device_error, attn_paged_fwd
 from oracle import codes as C
 import paged8_cases as P8
-from test_gpu_cache8 import FMTS, ints
+import paged_cases as P
+from test_gpu_cache8 import FMTS, ints, prefix
 
 pytestmark = pytest.mark.gpu
 PAGE, G = 16, 4
@@ -100,3 +101,16 @@ def test_scales_far_apart(case, kernel, d, fmt):
             bound = A * (2 * r + (2 * m + 1) * u + 2.0 ** -21 + h) + m * u * V
             assert np.all(np.abs(out[:, t, g] - O) <= bound), (t, g, np.abs((out[:, t, g] - O) / bound).max())
             assert np.all(np.abs(lse[g, :, t] - L) <= r + m * u + 2.0 ** -21 + 2 * u * abs(L))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_two_passes_that_share_the_sms(fmt):
+    """Prefixes of many rows on the tiles and long sequences of a token each behind them on the kernel for few
+    rows, side by side: the same bits every time."""
+    lens = [(2600 + 91 * i) % 3000 for i in range(24)]
+    c = P8.make(fmt, lens, [1] * 24, 64, 32, 8, 128, seed=11, plens=[3000, 900], first=[0, 16, 24], spread=0.3)
+    want = prefix(c, max_q=1)
+    assert attn_last_device_error() == 0
+    P8.check(c, *want, P.reference(c))
+    for _ in range(30):
+        assert all(torch.equal(x, y) for x, y in zip(prefix(c, max_q=1), want))

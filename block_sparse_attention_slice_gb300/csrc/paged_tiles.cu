@@ -25,7 +25,7 @@
 // the softmax of 64 columns is 0.6 (100 rows, 16384 keys, 16 heads, 4 groups: 34
 // us on all SMs).
 //
-// Pages in 8 bits: the same call over int8 takes 236 us.  A warpgroup makes bf16 operands of the codes,
+// Pages in 8 bits: the same call over int8 takes 241 us.  A warpgroup makes bf16 operands of the codes,
 // once for each 256 rows, and a warp prepares the scales; left out, the first is worth 19 us, both
 // with the softmax's extra operations 50, more than their sum (they share the issue slots).
 //
@@ -69,7 +69,7 @@ struct TileLayout {
   static constexpr int NS = B8 ? (D == 64 ? 6 - 2 * (TILES == 1) : 3) : D == 64 ? 10 : TILES == 2 ? 4 : 5;   // K/V ring slots: 64 to 160 KB
   static constexpr int HALF = 128 * 64 * 2, NHALF = D / 64, TILE = NHALF * HALF;
   // pages in 8 bits: slots of codes, and of what the softmax needs of a tile's scales
-  static constexpr int NG = !B8 ? 0 : D == 64 ? 8 : TILES == 2 ? 3 : 4, CODES = TILE / 2, NC = B8 ? 4 : 0, SCALES = 3 * 128 * 4;
+  static constexpr int NG = !B8 ? 0 : D == 64 ? 8 : TILES == 2 ? 3 : 4, CODES = TILE / 2, NC = B8 ? 4 : 0, SCALES = 2 * 128 * 4;
   static constexpr int Q_OFF = 0, KV_OFF = TILES * TILE, G_OFF = KV_OFF + NS * TILE, C_OFF = G_OFF + NG * CODES,
                        SEG_OFF = C_OFF + NC * SCALES;
   static constexpr int BAR_OFF = SEG_OFF + PT_IQ * 64;
@@ -575,13 +575,11 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
     __syncwarp();
   } else if (B8 && warp == WS) {
     // ---------------------------------------------------------------- scales
-    // Of a key's scale ks and its value's scale vs the softmax takes a = ks scale log2 e,
-    // b = log2 vs and c = 1 / vs: a score S gives y = S a + b, the logarithm of its
-    // value's weight w = p vs = 2^(y - m), and p = w c goes to the row's sum.  So a scaled
-    // softmax costs one operation a pair of scores more than a plain one, not three.  (vs
-    // = 0 counts as 2^-90, whose codes are zeros.)  A lane has four neighbouring keys,
-    // which lie in one page; its entry is read two tiles ahead, the scales one.  Keys that
-    // no row sees get 0.
+    // Of a key the softmax takes a = ks scale log2 e, with which a score S becomes s = S a, and its
+    // value's scale vs: p = 2^(s - m) goes to the row's sum, p vs to the product.  The row's
+    // maximum is that of s: that of s + log2 vs leaves no p where a small vs meets a large one.  A lane
+    // has four neighbouring keys, which lie in one page; its entry is read two tiles ahead, the
+    // scales one.  Keys that no row sees get 0.
     uint32_t tiles = 0, nseg = 0;
     bool ok = true;
     while (ok) {
@@ -613,20 +611,17 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
         for (int k = 0; k < 4; ++k) {
           const bool live = good && seen(k0 + k);
           ks[k] = live ? p.k_scales[at + k * p.scale_token] : 0.f;
-          vs[k] = live ? p.v_scales[at + k * p.scale_token] : 1.f;
+          vs[k] = live ? p.v_scales[at + k * p.scale_token] : 0.f;
         }
       };
       fetch(0, look_up(0));
       int pg = look_up(1);
       for (int j = 0; j < steps; ++j, ++tiles) {
-        float a[4], b[4], c[4];
+        float a[4], v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           a[k] = ks[k] * p.scale_log2;
-          float y;
-          asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(vs[k]));
-          b[k] = y < -90.f ? -90.f : y;
-          c[k] = ex2_approx(-b[k]);
+          v[k] = vs[k];
         }
         fetch(j + 1, pg);
         pg = look_up(j + 2);
@@ -636,12 +631,11 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
           break;
         }
         const uint32_t dst = sb + L::C_OFF + st * L::SCALES;
-        auto put = [](uint32_t at, float x, float y, float z, float u) {
-          st_shared_v4(at, make_uint4(__float_as_uint(x), __float_as_uint(y), __float_as_uint(z), __float_as_uint(u)));
+        auto put = [](uint32_t at, const float (&x)[4]) {
+          st_shared_v4(at, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])));
         };
-        put(dst + lane * 32, a[0], a[1], b[0], b[1]);
-        put(dst + lane * 32 + 16, a[2], a[3], b[2], b[3]);
-        put(dst + 1024 + lane * 16, c[0], c[1], c[2], c[3]);
+        put(dst + lane * 16, a);
+        put(dst + 512 + lane * 16, v);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::B_CF + st));
       }
@@ -756,9 +750,8 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
           break;
         }
         tc_fence_after();
-        // of this group's columns: a and b of each pair, and c
-        const uint32_t sab = sb + L::C_OFF + (step % NC8) * L::SCALES + (TILES == 1 ? grp * 512 : 0),
-                       sc = sb + L::C_OFF + (step % NC8) * L::SCALES + 1024 + (TILES == 1 ? grp * 256 : 0);
+        // of this group's columns: a and vs
+        const uint32_t sa = sb + L::C_OFF + (step % NC8) * L::SCALES + (TILES == 1 ? grp * 256 : 0), sv = sa + 512;
         if (!idle) {
           float x[NC];
           {
@@ -773,11 +766,11 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
             }
           }
           if constexpr (B8) {
-            // the logarithms of weights; their maximum is one of these rounded numbers
 #pragma unroll
-            for (int k = 0; k < NC; k += 2) {
-              const uint4 ab = ld_shared_v4(sab + k * 8);
-              f2_split(f2_fma(f2_make(x[k], x[k + 1]), f2_make_u(ab.x, ab.y), f2_make_u(ab.z, ab.w)), x[k], x[k + 1]);
+            for (int k = 0; k < NC; k += 4) {
+              const uint4 a = ld_shared_v4(sa + k * 4);
+              f2_split(f2_mul(f2_make(x[k], x[k + 1]), f2_make_u(a.x, a.y)), x[k], x[k + 1]);
+              f2_split(f2_mul(f2_make(x[k + 2], x[k + 3]), f2_make_u(a.z, a.w)), x[k + 2], x[k + 3]);
             }
           }
           if (masked) {
@@ -809,7 +802,7 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < NC / 32; ++c) {
             uint32_t pk[16];
-            uint4 c4;
+            uint4 v4;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               float a0, a1;
@@ -817,11 +810,10 @@ __global__ void __launch_bounds__(TileLayout<D, TILES, B8>::THREADS, 1)
               f2_split(B8 ? f2_add(x2, nb2) : f2_fma(x2, sc2, nb2), a0, a1);
               a0 = ex2_approx(a0);
               a1 = ex2_approx(a1);
+              l2[k & 3] = f2_add(l2[k & 3], f2_make(a0, a1));
               if constexpr (B8) {
-                if (k % 2 == 0) c4 = ld_shared_v4(sc + (c * 32 + 2 * k) * 4);
-                l2[k & 3] = f2_fma(f2_make(a0, a1), k % 2 ? f2_make_u(c4.z, c4.w) : f2_make_u(c4.x, c4.y), l2[k & 3]);
-              } else {
-                l2[k & 3] = f2_add(l2[k & 3], f2_make(a0, a1));
+                if (k % 2 == 0) v4 = ld_shared_v4(sv + (c * 32 + 2 * k) * 4);
+                f2_split(f2_mul(f2_make(a0, a1), k % 2 ? f2_make_u(v4.z, v4.w) : f2_make_u(v4.x, v4.y)), a0, a1);
               }
               pk[k] = pack_bf16x2(a0, a1);
             }

@@ -1,5 +1,5 @@
 """Attention over a cache in 8 bits where the scales of one sequence lie far apart: small ones before
-large ones, none (0) beside large ones, and scores that grow from key to key.  Each case goes to each
+large ones, none (0) beside large ones, and scores that grow from key to key.  Each case goes to every
 kernel, many times the same sequence in one call, so that an item has several slabs of one warp."""
 import numpy as np
 import pytest
@@ -16,7 +16,8 @@ PAGE, G = 16, 4
 FACTORS = (1.0, 0.75, 1.5, 0.875)        # of a token's heads: their queries
 
 # tokens of a sequence and sequences of a call, by the kernel that they go to
-KERNELS = {"up to 8 rows": (1, 900), "16 rows, 4 warps": (1, 80), "16 rows, 8 warps": (1, 250), "20 rows": (5, 500)}
+KERNELS = {"up to 8 rows": (1, 900), "16 rows, 4 warps": (1, 80), "16 rows, 8 warps": (1, 250), "20 rows": (5, 500), "a row tile": (12, 300),
+           "two row tiles": (60, 100)}
 
 
 def tiny_then_huge(n, rng):

@@ -8,7 +8,7 @@
 // scores and keeps the best of them all.
 //
 // beam_scan_kernel: a warp takes a part of a row as a stream, keeps the running maximum and
-// sum of each lane, and the best so far, one or two a lane in their order.  A word is
+// sum of each lane, and the best so far, one or two a lane in their order.  16 bytes are
 // looked into only where its largest value beats the last of them, which gets rare: 512
 // rows of 131072 bf16 take 38 us (a block a part, its threshold by an exchange and its
 // candidates ranked in shared memory, took half as long again).  The first
@@ -30,7 +30,7 @@ namespace attn {
 namespace {
 
 constexpr int BS_T = 256;            // threads of a scanning block
-constexpr int BS_WORDS = 4;          // 16-byte words that a lane of it takes at a time
+constexpr int BS_REGS = 16;          // words of 4 bytes that a lane of it takes at a time, in groups of 4
 constexpr int BP_T = 256;            // of a choosing block
 constexpr int BP_CAP = 1024;
 
@@ -129,37 +129,48 @@ struct ScanParams {
   const void *logits;
   const uint8_t *done;
   long long row_stride;      // elements
-  int vocab, splits, keep, words, rest, parts;       // a part: `words` 16-byte words, the first `rest` of a row one more; parts: of all rows
+  int vocab, splits, keep, units, rest, parts;       // a part: `units` of the row, the first `rest` of a row one more; parts: of all rows
   float2 *ms;                // [rows][splits]: maximum, sum of exp(x - maximum)
   uint32_t *keys;            // [rows][splits][keep], best first
   int *ids;                  // their tokens; -1: none
 };
 
-template <typename E>
-struct Vec;                  // a 16-byte word of logits
-template <>
-struct Vec<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ float get(const uint4 &w, int e) {
-    return __uint_as_float(e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w);
+// A lane's logits: units of UNIT bytes, N values each, in registers of V values.
+template <typename E, int UNIT>
+struct Vec {
+  static constexpr int N = UNIT / static_cast<int>(sizeof(E)), V = UNIT == 2 ? 1 : 4 / static_cast<int>(sizeof(E));
+  static constexpr int REGS = N / V, UNITS = BS_REGS / REGS;      // registers of a unit; units of a lane
+  static constexpr uint32_t NONE = sizeof(E) == 4 ? 0xff800000u : V == 2 ? 0xff80ff80u : 0xff80u;      // -inf
+  // value e of a register
+  static __device__ __forceinline__ float get(uint32_t x, int e) {
+    return __uint_as_float(sizeof(E) == 4 ? x : e ? x & 0xffff0000u : x << 16);
   }
-  static __device__ __forceinline__ uint32_t bits(const float *p) { return __float_as_uint(*p); }
-  static __device__ __forceinline__ float top(const uint4 &w) { return fmaxf(max3f(get(w, 0), get(w, 1), get(w, 2)), get(w, 3)); }
-};
-template <>
-struct Vec<uint16_t> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ float get(const uint4 &w, int e) {
-    const uint32_t y = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
-    return __uint_as_float(e & 1 ? y & 0xffff0000u : y << 16);
+  // the largest of 4 registers; a NaN is passed by
+  static __device__ __forceinline__ float top(const uint32_t *x) {
+    if constexpr (V == 1) {
+      return fmaxf(max3f(get(x[0], 0), get(x[1], 0), get(x[2], 0)), get(x[3], 0));
+    } else {
+      uint32_t a, b;
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(x[0]), "r"(x[1]));
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(x[2]), "r"(x[3]));
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+      return fmaxf(get(a, 0), get(a, 1));
+    }
   }
-  static __device__ __forceinline__ uint32_t bits(const uint16_t *p) { return *p; }
-  static __device__ __forceinline__ float top(const uint4 &w) {
-    uint32_t a, b;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w.z), "r"(w.w));
-    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
-    return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  // the unit at p, which is aligned to it
+  static __device__ __forceinline__ void load(const E *p, uint32_t *x) {
+    if constexpr (UNIT == 16) {
+      const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p));
+      x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+    } else if constexpr (UNIT == 4) {
+      x[0] = __ldcs(reinterpret_cast<const uint32_t *>(p));
+    } else {
+      x[0] = __ldcs(reinterpret_cast<const uint16_t *>(p));
+    }
+  }
+  static __device__ __forceinline__ uint32_t bits(const E *p) {
+    if constexpr (sizeof(E) == 4) return __float_as_uint(*p);
+    else return *p;
   }
 };
 
@@ -200,12 +211,16 @@ struct Best {
   }
 };
 
-// E: the logits' type; R: best a lane.  A row is taken by its 16-byte words wherever it
-// begins; of a word that the row's ends cut the values outside count as -inf and are no
-// candidates.
-template <typename E, int R>
+// E: the logits' type; R: best a lane.  A row is taken by its units of UNIT bytes wherever it
+// begins; of a unit that the row's ends cut the values outside count as -inf and are no
+// candidates.  A unit divides the distance of two rows, so that all rows are cut alike: equal rows have
+// equal sums to the last bit, whatever their addresses, and their beams stand in order.  The choice
+// for 64 prompts of 8 beams, bf16: 131072 tokens in units of 16 bytes 47.2 us, 131070 in units of 4 47.4,
+// 131071 in units of 2 56.6; 24 of 5, f32: 100004 and 100003 tokens 26.0, 25.2.
+template <typename E, int UNIT, int R>
 __global__ void __launch_bounds__(BS_T, 3) beam_scan_kernel(const ScanParams p) {
-  constexpr int N = Vec<E>::N, W = BS_WORDS;
+  using X = Vec<E, UNIT>;
+  constexpr int N = X::N, V = X::V, Q = X::REGS, W = X::UNITS, STEP = 32 * W;
   after_previous();
   admit_next();
   const int lane = threadIdx.x & 31;
@@ -214,52 +229,56 @@ __global__ void __launch_bounds__(BS_T, 3) beam_scan_kernel(const ScanParams p) 
   const int row = at / p.splits, split = at - row * p.splits;
   if (p.done && p.done[row]) return;
   const E *base = static_cast<const E *>(p.logits) + row * p.row_stride;
-  const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(E));
-  const int begin = split * p.words + min(split, p.rest), end = begin + p.words + (split < p.rest);      // words
-  // words w of them, w = at + 32 i + lane
-  auto load = [&](int from, uint4 (&x)[W]) {
-    const bool inner = from > 0 && (from + 32 * W) * N - skew <= p.vocab && from + 32 * W <= end;
+  const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & (UNIT - 1)) / sizeof(E));
+  const int begin = split * p.units + min(split, p.rest), end = begin + p.units + (split < p.rest);
+  // units u of them, u = from + 32 i + lane
+  auto load = [&](int from, uint32_t (&x)[BS_REGS]) {
+    const bool inner = from > 0 && (from + STEP) * N - skew <= p.vocab && from + STEP <= end;
     if (inner) {
-      const uint4 *src = reinterpret_cast<const uint4 *>(base - skew + static_cast<long long>(from) * N) + lane;
+      const E *src = base - skew + (static_cast<long long>(from) + lane) * N;
 #pragma unroll
-      for (int i = 0; i < W; ++i) x[i] = __ldcs(src + 32 * i);
+      for (int i = 0; i < W; ++i) X::load(src + 32 * i * N, x + Q * i);
       return;
     }
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-      const int w = from + 32 * i + lane;
-      const long long v = w < end ? static_cast<long long>(w) * N - skew : p.vocab;
+      const int u = from + 32 * i + lane;
+      const long long v = u < end ? static_cast<long long>(u) * N - skew : p.vocab;
       if (v >= 0 && v + N <= p.vocab) {
-        x[i] = __ldcs(reinterpret_cast<const uint4 *>(base + v));
+        X::load(base + v, x + Q * i);
         continue;
       }
-      uint32_t z[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const uint32_t b = v + e >= 0 && v + e < p.vocab ? Vec<E>::bits(base + v + e) : N == 4 ? 0xff800000u : 0xff80u;
-        z[e * 4 / N] |= N == 4 ? b : b << (16 * (e & 1));
+      for (int k = 0; k < Q; ++k) {
+        uint32_t z = X::NONE;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const long long y = v + k * V + e;
+          const int by = 32 / V * e;
+          if (y >= 0 && y < p.vocab) z = V == 1 ? X::bits(base + y) : (z & ~(0xffffu << by)) | X::bits(base + y) << by;
+        }
+        x[Q * i + k] = z;
       }
-      x[i] = make_uint4(z[0], z[1], z[2], z[3]);
     }
   };
-  uint4 next[W];
+  uint32_t next[BS_REGS];
   load(begin, next);
   Best<R> best;
   uint32_t last_k = 0;       // what a candidate has to beat: this key, with a lower token
   int last_i = INT_MAX;
   float m = -INFINITY, s = 0.f;
   bool first = true;
-  for (int from = begin; from < end; from += 32 * W) {
-    uint4 x[W];
+  for (int from = begin; from < end; from += STEP) {
+    uint32_t x[BS_REGS];
 #pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = next[i];
-    if (from + 32 * W < end) load(from + 32 * W, next);
+    for (int i = 0; i < BS_REGS; ++i) x[i] = next[i];
+    if (from + STEP < end) load(from + STEP, next);
     // maximum (a NaN is passed by, and spoils the sum)
-    float mw[W];
+    float mw[BS_REGS / 4];
 #pragma unroll
-    for (int i = 0; i < W; ++i) mw[i] = Vec<E>::top(x[i]);
+    for (int i = 0; i < BS_REGS / 4; ++i) mw[i] = X::top(x + 4 * i);
     const float top = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
-    static_assert(W == 4, "the maximum of a lane's words");
+    static_assert(BS_REGS == 16, "the maximum of a lane's groups");
     const uint32_t key = key_of(top);
     // tokens ascend: what is equal to the last of the best comes behind it
     uint32_t least = max(last_k, last_k + 1);
@@ -275,18 +294,18 @@ __global__ void __launch_bounds__(BS_T, 3) beam_scan_kernel(const ScanParams p) 
     }
     if (__any_sync(0xffffffffu, key >= least)) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        for (unsigned hot = __ballot_sync(0xffffffffu, key_of(mw[i]) >= least); hot; hot &= hot - 1) {
-          // the word's values to as many lanes
+      for (int g = 0; g < BS_REGS / 4; ++g) {
+        for (unsigned hot = __ballot_sync(0xffffffffu, key_of(mw[g]) >= least); hot; hot &= hot - 1) {
+          // the group's values to as many lanes
           const int src = __ffs(hot) - 1;
-          const uint32_t y0 = __shfl_sync(0xffffffffu, x[i].x, src), y1 = __shfl_sync(0xffffffffu, x[i].y, src),
-                         y2 = __shfl_sync(0xffffffffu, x[i].z, src), y3 = __shfl_sync(0xffffffffu, x[i].w, src);
-          const int part = N == 4 ? lane : lane >> 1;
-          const uint32_t bits = part & 2 ? (part & 1 ? y3 : y2) : (part & 1 ? y1 : y0);
-          const uint32_t k = key_of(__uint_as_float(N == 4 || (lane & 1) ? bits & (N == 4 ? 0xffffffffu : 0xffff0000u) : bits << 16));
-          const long long token = static_cast<long long>(from + 32 * i + src) * N - skew + lane;
+          const uint32_t y0 = __shfl_sync(0xffffffffu, x[4 * g], src), y1 = __shfl_sync(0xffffffffu, x[4 * g + 1], src),
+                         y2 = __shfl_sync(0xffffffffu, x[4 * g + 2], src), y3 = __shfl_sync(0xffffffffu, x[4 * g + 3], src);
+          const int part = lane / V;
+          const uint32_t k = key_of(X::get(part & 2 ? (part & 1 ? y3 : y2) : (part & 1 ? y1 : y0), lane % V));
+          const int unit = from + 32 * ((4 * g + part) / Q) + src;
+          const long long token = static_cast<long long>(unit) * N - skew + lane % N;
           const int id = static_cast<int>(token);
-          const bool there = lane < N && from + 32 * i + src < end && token >= 0 && token < p.vocab && k >= least;
+          const bool there = lane < 4 * V && unit < end && token >= 0 && token < p.vocab && k >= least;
           for (unsigned c = __ballot_sync(0xffffffffu, there && before(k, id, last_k, last_i)); c; c &= c - 1) {
             const int e = __ffs(c) - 1;
             const uint32_t ck = __shfl_sync(0xffffffffu, k, e);
@@ -294,9 +313,10 @@ __global__ void __launch_bounds__(BS_T, 3) beam_scan_kernel(const ScanParams p) 
             if (!before(ck, ci, last_k, last_i)) continue;       // the ones before it left no room
             best.insert(ck, ci);
             best.last(p.keep, last_k, last_i);
-            least = max(least, max(last_k, last_k + 1));
           }
         }
+        // a group's tokens stand behind those of the one before, in no order of their own
+        least = max(least, max(last_k, last_k + 1));
       }
     }
     first = false;
@@ -307,13 +327,11 @@ __global__ void __launch_bounds__(BS_T, 3) beam_scan_kernel(const ScanParams p) 
     const uint64_t nm = f2_make(-mb, -mb), c2 = f2_make(1.44269504f, 1.44269504f);
     uint64_t s2 = 0ull;
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-#pragma unroll
-      for (int e = 0; e < N; e += 2) {
-        float a, b;
-        f2_split(f2_mul(f2_add(f2_make(Vec<E>::get(x[i], e), Vec<E>::get(x[i], e + 1)), nm), c2), a, b);
-        s2 = f2_add(s2, f2_make(ex2_approx(a), ex2_approx(b)));
-      }
+    for (int e = 0; e < BS_REGS * V; e += 2) {
+      float a, b;
+      f2_split(f2_mul(f2_add(f2_make(X::get(x[e / V], e % V), X::get(x[(e + 1) / V], (e + 1) % V)), nm), c2), a, b);
+      s2 = f2_add(s2, f2_make(ex2_approx(a), ex2_approx(b)));
+    }
     float a, b;
     f2_split(s2, a, b);
     s += a + b;
@@ -676,14 +694,28 @@ __global__ void __launch_bounds__(RE_T, !RUNS ? 1 : MOST <= 8 ? 4 : 2) beam_reor
 
 // Parts of a row, a warp each: as many as fill the SMs with 24 warps (64 prompts of 8 beams
 // and 131072 tokens, the whole step: 63.6 us; 20 warps 69.3; 32, of 64 registers a thread, 72.1),
-// of 32 BS_WORDS words at least.  words: of a row, wherever it begins.  Not more than leave
-// a group's choice 16384 candidates.
-int splits_of(int groups, int beams, int vocab, int keep, int dtype, int sms, int *words) {
-  const int n = dtype == ATTN_DTYPE_F32 ? 4 : 8;
-  *words = (vocab + 2 * n - 2) / n;
-  const int most = (*words + 32 * BS_WORDS - 1) / (32 * BS_WORDS);
+// of what a warp takes at a time at least.  n: values of a unit; units: of a row, wherever it
+// begins.  Not more than leave a group's choice 16384 candidates.
+int splits_of(int groups, int beams, int vocab, int keep, int n, int per_lane, int sms, int *units) {
+  *units = (vocab + 2 * n - 2) / n;
+  const int step = 32 * per_lane / n, most = (*units + step - 1) / step;
   return std::max(1, std::min({most, sms * 24 / std::max(groups * beams, 1), 16384 / (beams * keep)}));
 }
+
+// The scans: `n` values of a unit of `unit` bytes, a lane takes `per_lane` at a time; with one best a
+// lane and with two.
+struct Scan {
+  int dtype, unit, n, per_lane;
+  void (*few)(const ScanParams), (*many)(const ScanParams);
+};
+template <typename E, int UNIT>
+constexpr Scan scan_of(int dtype) {
+  using X = Vec<E, UNIT>;
+  return Scan{dtype, UNIT, X::N, X::N * X::UNITS, beam_scan_kernel<E, UNIT, 1>, beam_scan_kernel<E, UNIT, 2>};
+}
+// by type, the widest first
+const Scan kScans[] = {scan_of<float, 16>(ATTN_DTYPE_F32), scan_of<float, 4>(ATTN_DTYPE_F32), scan_of<uint16_t, 16>(ATTN_DTYPE_BF16),
+                       scan_of<uint16_t, 4>(ATTN_DTYPE_BF16), scan_of<uint16_t, 2>(ATTN_DTYPE_BF16)};
 
 int check_beams(int groups, int beams, int vocab, int keep) {
   if (groups < 0 || beams < 1 || vocab < 1 || keep < 1) return ATTN_ERR_INVALID_ARG;
@@ -707,9 +739,9 @@ int attn_beam_workspace_bytes(int groups, int beams, int vocab, int keep, size_t
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   size_t most = 0;
-  for (int dtype : {ATTN_DTYPE_F32, ATTN_DTYPE_BF16}) {
-    int words;
-    const size_t parts = static_cast<size_t>(groups) * beams * splits_of(groups, beams, vocab, keep, dtype, sms, &words);
+  for (const Scan &x : kScans) {
+    int units;
+    const size_t parts = static_cast<size_t>(groups) * beams * splits_of(groups, beams, vocab, keep, x.n, x.per_lane, sms, &units);
     const size_t need = up256(parts * 8) + 2 * up256(parts * keep * 4);
     most = need > most ? need : most;
   }
@@ -738,18 +770,20 @@ int attn_beam_select(const void *logits, int logits_dtype, int64_t row_stride, i
   const int rows = groups * beams;
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  int words;
-  const int splits = splits_of(groups, beams, vocab, keep, logits_dtype, sms, &words);
+  // the first whose units divide the distance of two beams' rows
+  const Scan *x = kScans;
+  while (x->dtype != logits_dtype || (beams > 1 && row_stride * esize % x->unit)) ++x;
+  int units;
+  const int splits = splits_of(groups, beams, vocab, keep, x->n, x->per_lane, sms, &units);
   const size_t parts = static_cast<size_t>(rows) * splits;
   if (parts >= (size_t(1) << 30) || static_cast<int64_t>(beams) * splits * keep >= INT_MAX) return ATTN_ERR_UNSUPPORTED;
   uint8_t *ws = static_cast<uint8_t *>(d_ws);
   float2 *ms = reinterpret_cast<float2 *>(ws);
   uint32_t *keys = reinterpret_cast<uint32_t *>(ws + up256(parts * 8));
   int *ids = reinterpret_cast<int *>(ws + up256(parts * 8) + up256(parts * keep * 4));
-  const ScanParams sp{logits, done, row_stride, vocab, splits, keep, words / splits, words % splits, static_cast<int>(parts), ms, keys, ids};
+  const ScanParams sp{logits, done, row_stride, vocab, splits, keep, units / splits, units % splits, static_cast<int>(parts), ms, keys, ids};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto scan = logits_dtype == ATTN_DTYPE_F32 ? (keep <= 32 ? beam_scan_kernel<float, 1> : beam_scan_kernel<float, 2>)
-                                             : (keep <= 32 ? beam_scan_kernel<uint16_t, 1> : beam_scan_kernel<uint16_t, 2>);
+  auto scan = keep <= 32 ? x->few : x->many;
   const unsigned grid = static_cast<unsigned>((parts + BS_T / 32 - 1) / (BS_T / 32));
   if ((rc = launch_after(scan, dim3(grid), BS_T, 0, s, sp)) != ATTN_OK) return rc;
   const PickParams pp{scores, done, slots, ms, keys, ids, beams, vocab, splits, keep, eos, out_scores, out_parents, out_tokens, out_src, out_done};

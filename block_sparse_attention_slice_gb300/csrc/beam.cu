@@ -9,7 +9,7 @@
 //
 // beam_scan_kernel: a warp takes a part of a row as a stream, keeps the running maximum and
 // sum of each lane, and the best so far, one or two a lane in their order.  16 bytes are
-// looked into only where its largest value beats the last of them, which gets rare: 512
+// looked into only where their largest value beats the last of them, which gets rare: 512
 // rows of 131072 bf16 take 38 us (a block a part, its threshold by an exchange and its
 // candidates ranked in shared memory, took half as long again).  The first
 // words have a threshold of their own, the `keep`-th of the lanes' largest values.  Values are
@@ -53,32 +53,21 @@ __device__ __forceinline__ double value_of(unsigned long long k) {
 // A key, not 0, that at least min(keep, keys there are) of the block's keys reach, given
 // the largest of each thread's (0: none), of which the first `active` have some;
 // keep <= 64.  `sums` has a place a warp.
-template <int T, typename K>
-__device__ __forceinline__ K threshold(K top, int keep, int active, K *sums) {
+template <int T>
+__device__ __forceinline__ unsigned long long threshold(unsigned long long top, int keep, int active, unsigned long long *sums) {
   // groups of as many threads as leave `keep` of them, a warp at most
   int width = 32;
   while (width > 1 && active < keep * width) width >>= 1;
-  const int lane = threadIdx.x & 31;
-  if constexpr (sizeof(K) == 4) {
-    top = __reduce_max_sync(width == 32 ? 0xffffffffu : ((1u << width) - 1) << (lane & ~(width - 1)), top);
-  } else {
-    for (int o = 1; o < width; o <<= 1) {
-      const K a = __shfl_xor_sync(0xffffffffu, top, o);
-      top = a > top ? a : top;
-    }
+  for (int o = 1; o < width; o <<= 1) {
+    const unsigned long long a = __shfl_xor_sync(0xffffffffu, top, o);
+    top = a > top ? a : top;
   }
-  if (static_cast<int>(threadIdx.x & ~(width - 1)) >= active) top = ~K(0);
-  if (width < 32) {
-    if constexpr (sizeof(K) == 4) {
-      top = __reduce_min_sync(0xffffffffu, top);
-    } else {
-      for (int o = width; o < 32; o <<= 1) {
-        const K a = __shfl_xor_sync(0xffffffffu, top, o);
-        top = a < top ? a : top;
-      }
-    }
+  if (static_cast<int>(threadIdx.x & ~(width - 1)) >= active) top = ~0ull;
+  for (int o = width; o < 32; o <<= 1) {
+    const unsigned long long a = __shfl_xor_sync(0xffffffffu, top, o);
+    top = a < top ? a : top;
   }
-  if (lane == 0) sums[threadIdx.x >> 5] = top;
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = top;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < T / 32; ++w) top = sums[w] < top ? sums[w] : top;
@@ -110,7 +99,7 @@ __device__ __forceinline__ void block_best(K &k, int &i, K *ks, int *is) {
 
 // Writes the best of n listed keys: a warp takes an entry at a time and counts those that
 // stand before it, 32 together.
-template <int T, typename K, typename B, typename W>
+template <int T, typename B, typename W>
 __device__ __forceinline__ void rank_list(int n, int keep, B stands_before, W write) {
   const int lane = threadIdx.x & 31;
   for (int i = threadIdx.x >> 5; i < n; i += T / 32) {
@@ -507,7 +496,7 @@ __global__ void __launch_bounds__(BP_T) beam_pick_kernel(const PickParams p) {
   };
   const int m = listed;
   if (m <= BP_CAP) {
-    rank_list<BP_T, unsigned long long>(
+    rank_list<BP_T>(
         m, p.keep,
         [&](int x, int y) {
           return list_k[x] > list_k[y] || (list_k[x] == list_k[y] && (list_b[x] < list_b[y] || (list_b[x] == list_b[y] && list_v[x] < list_v[y])));

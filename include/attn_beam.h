@@ -4,7 +4,9 @@
  *   attn_beam_select    the best continuations of every prompt, over its beams
  *                       and the vocabulary
  *   attn_beam_reorder   states brought into the chosen order; the cache itself
- *                       is reordered by attn_cache_fork
+ *                       is reordered by attn_cache_fork, whose copies
+ *                       attn_cache_copy_pages makes (of pages in 8 bits one
+ *                       call for the codes and one for the scales)
  *
  * Conventions are those of attn_paged.h.  Row g * beams + b of an array is beam
  * b of prompt (group) g.

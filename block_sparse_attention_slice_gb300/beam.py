@@ -21,7 +21,8 @@ def attn_beam_select(logits, scores, done=None, eos: int = -1, slots=None, keep=
     g * beams + b, the token, and whether the beam has ended.  Equal ones stand in
     the order of beam, then token.  With ``slots`` (int32 [groups * beams], each
     beam's row of the page table) a fifth: slots[parents], the ``src`` of
-    ``attn_cache_fork``."""
+    ``attn_cache_fork``.  A ``stream`` other than the current one waits for what
+    the current one holds; what follows on the current one does not wait for it."""
     made = ()
     if stream is not None:
         import torch
@@ -41,8 +42,15 @@ def attn_beam_select(logits, scores, done=None, eos: int = -1, slots=None, keep=
 def attn_beam_reorder(states, parents, stream=None):
     """Row i of every tensor of ``states`` ([groups * beams, ...], each row
     contiguous) becomes what row parents[i] was, in place; parents int32
-    [groups, beams], each within its own group."""
-    (P._module or P._m()).beam_reorder(states, parents, stream and stream.cuda_stream)
+    [groups, beams], each within its own group.  A ``stream`` other than the
+    current one waits for what the current one holds, as in ``attn_beam_select``."""
+    if stream is not None:
+        import torch
+        here = torch.cuda.current_stream(parents.device)
+        if stream != here:
+            stream.wait_stream(here)
+        stream = stream.cuda_stream
+    (P._module or P._m()).beam_reorder(states, parents, stream)
 
 
 def _declare(lib):

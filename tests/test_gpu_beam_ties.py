@@ -3,6 +3,7 @@ lie in memory."""
 import pytest
 import torch
 
+from block_sparse_attention_slice_gb300 import attn_beam_select, attn_last_device_error
 from test_gpu_beam import make, run
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +47,23 @@ def test_rows_apart(V, pad, dtype):
     logits, scores = make(3, 4, V, V, dtype)
     for skip in range(pad + 1):
         run(spread(logits, pad, skip), scores, keep=min(9, 4 * V))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [50, 6001, 100003, 1 << 21])
+@pytest.mark.parametrize("sigma", [0.01, 2.5])
+def test_beams_as_near_as_their_sums_tell_apart(V, sigma, dtype):
+    """Rows of the same logits in other orders: their sums differ by rounding alone, at most 2^-19 each, and
+    scores 2^-18 apart and more decide."""
+    gen = torch.Generator().manual_seed(V)
+    row = (torch.randn(V, generator=gen) * sigma).to(dtype)
+    row = row.clamp(max=7.5)
+    row[0] = 8.0       # the best of each beam
+    beams = torch.stack([row[torch.randperm(V, generator=gen)] for _ in range(8)]).cuda()
+    order = torch.randperm(8, generator=gen)
+    scores = torch.empty(8)
+    scores[order] = -torch.arange(8).float() * 2.0 ** -18 * 1.0625
+    got = attn_beam_select(beams, scores.view(1, 8).cuda())
+    assert got[1].view(-1).tolist() == order.tolist()
+    assert torch.equal(got[2].view(-1).cpu(), (beams == 8).int().argmax(1).int().cpu()[order])
+    assert attn_last_device_error() == 0

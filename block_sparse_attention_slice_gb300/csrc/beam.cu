@@ -10,7 +10,7 @@
 // beam_scan_kernel: a warp takes a part of a row as a stream, keeps the running maximum and
 // sum of each lane, and the best so far, one or two a lane in their order.  16 bytes are
 // looked into only where their largest value beats the last of them, which gets rare: 512
-// rows of 131072 bf16 take 38 us (a block a part, its threshold by an exchange and its
+// rows of 131072 bf16 take 37 us (a block a part, its threshold by an exchange and its
 // candidates ranked in shared memory, took half as long again).  The first
 // words have a threshold of their own, the `keep`-th of the lanes' largest values.  Values are
 // compared as whole numbers in the order of the floats, -0 as 0.
@@ -354,7 +354,7 @@ struct PickParams {
   uint8_t *out_done;
 };
 
-// One block a group, 8 us behind a launch of its own whatever the sizes: dependent loads, the
+// One block a group, 10 us behind its scan for 24 and for 64 groups (9.4 alone): dependent loads, the
 // sums in 64 bits, one exchange and the ranks of what is left.  Continuations are the parts' best, and of a beam that offers
 // nothing the first `keep` by their place, at -inf (of one that has ended its eos, then
 // those), so that the choice needs no other rule.
@@ -553,7 +553,7 @@ __host__ __device__ __forceinline__ int run_pitch(int beams) { return unit_bytes
 
 // All parents' words of one column of a group, then all rows': the column is this
 // thread's alone, so the rows may change places in memory.  Rows that stay are not
-// touched.  64 groups of 8 rows of 139 KB: 14.4 us, the most part from and to L2.
+// touched.  64 groups of 8 rows of 139 KB: 15.3 us a call, the most part from and to L2.
 template <int MOST>
 __device__ __forceinline__ void move_column(uint8_t *base, long long stride, const int *par, int beams) {
   uint4 x[MOST];
@@ -574,8 +574,8 @@ __device__ __forceinline__ int whole_words(int n, int skew, int &head) {
 
 // The same for `n` bytes of rows at any address, or of more than 16 beams, through shared
 // memory: words of 16 bytes where they lie in memory, read as they are and written as two of
-// them shifted into the new row's place.  (24 groups of 5 rows of 100003 bytes: 10.7 us;
-// words of 4 bytes, whose instructions bound it, took 20, bytes four times that.)  The bytes at the
+// them shifted into the new row's place.  (24 groups of 5 rows of 100003 bytes: 8.9 us a
+// call, 12.3 alone with cold caches; words of 4 bytes, whose instructions bound it, took twice that, bytes four times as long again.)  The bytes at the
 // ends of the run are moved alone, those outside it neither read nor written.
 __device__ __forceinline__ void move_run(uint8_t *base, long long stride, int n, const int *par, const int *used, int n_used, int beams, uint8_t *buf) {
   constexpr int BATCH = 4;
@@ -633,7 +633,7 @@ __device__ __forceinline__ void move_run(uint8_t *base, long long stride, int n,
 }
 
 // RUNS: some state is loose; 64 registers then, for more blocks an SM (runs of 5 rows: 15.6, 10.7
-// us), which columns of 8 rows would pay for (15.0, 24.5).
+// us when that was chosen), which columns of 8 rows would pay for (15.0, 24.5).
 template <int MOST, bool RUNS>
 __global__ void __launch_bounds__(RE_T, !RUNS ? 1 : MOST <= 8 ? 4 : 2) beam_reorder_kernel(const __grid_constant__ ReorderParams p) {
   __shared__ int par[ATTN_BEAM_MAX], used[ATTN_BEAM_MAX], n_used;
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(RE_T, !RUNS ? 1 : MOST <= 8 ? 4 : 2) beam_reor
 }
 
 // Parts of a row, a warp each: as many as fill the SMs with 24 warps (64 prompts of 8 beams
-// and 131072 tokens, the whole step: 63.6 us; 20 warps 69.3; 32, of 64 registers a thread, 72.1),
+// and 131072 tokens, the whole step when that was chosen: 63.6 us; 20 warps 69.3; 32, of 64 registers a thread, 72.1),
 // of what a warp takes at a time at least.  n: values of a unit; units: of a row, wherever it
 // begins.  Not more than leave a group's choice 16384 candidates.
 int splits_of(int groups, int beams, int vocab, int keep, int n, int per_lane, int sms, int *units) {

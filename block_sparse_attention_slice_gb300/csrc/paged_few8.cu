@@ -25,8 +25,9 @@
 //     read): 9 % fewer instructions than copies of 16 bytes.
 //
 // 16 sequences of 8191 to 131072 tokens, e4m3, 4 heads to each of 8 of 128 columns: 1.5 GB in
-// 231 us with the join, 6.5 TB/s.  64 with a window of 4096, int8: 394 MB in 84 us; 46 % of the issue
-// slots, a sixth of the waits are for instructions (branches marked unlikely changed nothing).
+// 232 us with the join, 6.5 TB/s.  64 with a window of 4096, int8: 394 MB in 84 us; 46 % of the issue
+// slots and 43 % of the converting unit: no path is full, a sixth of the waits are for instructions (branches
+// marked unlikely changed nothing).
 //
 // Numerics.  Codes become f16 exactly.  A row of Q becomes f16 times a power of
 // two that brings its largest value to 2^14 .. 2^15: exact but for values 2^-29

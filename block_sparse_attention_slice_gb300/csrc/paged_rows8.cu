@@ -3,31 +3,19 @@
 // stream of paged_rows.cu, whose plan, rings and pieces it has, over codes of one
 // byte with a scale for each token and head.
 //
-// What bounds it.  A byte read now costs a conversion to a 16-bit operand, and
-// the integer and conversion units take 2 cycles a warp's instruction on each of
-// an SM's four schedulers (measured), as a product of 16 x 8 x 16 takes 8: at 22
-// bytes a cycle and SM, what the cache's bandwidth comes to, a code has 5.8 lane
-// operations of those units in all.  So
-//   - operands are f16, not bf16: e4m3 converts by one instruction a pair, int8 by
-//     one logical operation and one addition (bf16 would take four);
-//   - a lane reads 16 codes at once and they are its operands as they lie: the sum
-//     over d, the sum over keys and the columns of O may each be taken in any order
-//     that both operands agree on.  Of 64 columns of a key lane c of its four takes
-//     16 in a row, for four products; of 16 keys a lane has four neighbouring ones,
-//     in P as in V, and of V's columns it takes 16 (8) in a row from each of these
-//     rows, so that two rows' words make operands by one byte permutation a pair.
-//     ldmatrix has no part in it.
-// 48 sequences, window 2048, 20 rows of 64 columns to each of 8 heads, e4m3: 68 MB in two passes, 35.6
+// What bounds it is what bounds paged_few8.cu: a byte costs a conversion, of units that have few
+// operations a code to spare.  Operands are f16 for the same reason, and a lane reads 16 codes at
+// once and they are its operands as they lie: the sum over d, the sum over keys and the columns
+// of O may each be taken in any order that both operands agree on.  Of 64 columns of a key lane c
+// of its four takes 16 in a row, for four products; of 16 keys a lane has four neighbouring ones,
+// in P as in V, and of V's columns it takes 16 (8) in a row from each of these rows, so that two
+// rows' words make operands by one byte permutation a pair.  ldmatrix has no part in it.
+//
+// 48 sequences, window 2048, 20 rows of 64 columns to each of 8 heads, e4m3: 68 MB in two passes, 35.5
 // us with 10 of start and join.  Two row tiles to a pass (255 registers, 8 warps): 49 us; on 16
 // sequences of 8192 keys 75, where this takes 78.
 //
-// Numerics.  Codes become f16 exactly.  A row of Q becomes f16 times a power of
-// two that brings its largest value to 2^14 .. 2^15: exact but for values 2^-29
-// below that one, which are off by 2^-40 of it at most.  Scores are f32 and take
-// the key's scale and the row's power of two there.  The weight of a value is
-// w = p vs; it is rounded to f16 (half a step, 2^-11 relative) times a power of
-// two of its row, chosen so that the largest w lies between 1 and 2^15; weights
-// below 2^-14 are off by 2^-25 at most.  Running maximum, sums and O are f32.
+// Numerics as in paged_few8.cu.
 #include <cuda_runtime.h>
 
 #include <climits>
